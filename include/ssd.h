@@ -327,6 +327,116 @@ int ssd_diag_scan_bwd(const ssd_problem* p, const void* x, const float* dt, cons
                       const float* dhT, void* dx, float* ddt, float* dA, void* dB, void* dC, float* dD,
                       float* dh0, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- The gated delta rule ----
+ * The same operands and state as the scan, with a write strength beta per token and head:
+ * each token first erases what the decayed state answers to its key B_t, then writes x_t:
+ *
+ *     r_t = x_t - a_t h_{t-1} B_t,   h_t = a_t h_{t-1} + beta_t r_t B_t^T,   y_t = h_t C_t,
+ *     a_t = exp(dt_t A_h)
+ *
+ * (h_t = a_t h_{t-1} (I - beta_t B_t B_t^T) + beta_t x_t B_t^T).  There is no skip term.  The
+ * state stays bounded where beta |B_t|^2 is in [0, 2] and A <= 0; keys are usually brought to
+ * unit length first (ssd_bc_norm).
+ *
+ *   x, y, dt, A, B, C, h0, hT   as for ssd_scan_fwd (layouts, groups, dtypes, alignment;
+ *                               h0 NULL = 0, hT NULL = not written)
+ *   beta                        [batch, seqlen, nheads], problem dtype (aligned to one element)
+ *
+ * Evaluated in chunks of 64 tokens: `chunk` must be 64 and `flags` 0.  headdim, dstate, dtype,
+ * ngroups and grid limits as for ssd_scan_fwd; also under 2^24 (chunk, head) pairs and
+ * (batch, head, 16 headdim columns) under 2^26, else SSD_ERR_UNSUPPORTED.
+ * Precision: decay sums are float64; the state, residuals and all accumulation float32, and
+ * where they enter the bfloat16 matrix cores they do so as a sum of bfloat16 terms that
+ * keeps the float32 mantissa, so the float32 outputs (hT, and ddt, dA, dh0 of the
+ * backward) are float32-accurate in bfloat16 problems too; y is rounded once.  A NaN or
+ * infinity in an input reaches every output of its head from the start of its chunk on.
+ * `ws` must hold ssd_delta_workspace_bytes(p) bytes (0 for an invalid or empty problem).
+ * Ownership, ordering, capture, aliasing and errors as for ssd_scan_fwd. */
+size_t ssd_delta_workspace_bytes(const ssd_problem* p);
+int ssd_delta_fwd(const ssd_problem* p, const void* x, const float* dt, const float* A,
+                  const void* B, const void* C, const void* beta, const float* h0, void* y,
+                  float* hT, void* ws, size_t ws_bytes, void* stream);
+
+/* Packed variable-length sequences: layouts and cu_seqlens as for ssd_scan_fwd_varlen (beta
+ * [seqlen, nheads]), for every problem that ssd_delta_fwd supports (seqlen under 2^31).
+ * Tokens before the first sequence and behind the last are neither read nor written. */
+size_t ssd_delta_varlen_workspace_bytes(const ssd_problem* p);
+int ssd_delta_fwd_varlen(const ssd_problem* p, const int32_t* cu_seqlens, const void* x,
+                         const float* dt, const float* A, const void* B, const void* C,
+                         const void* beta, const float* h0, void* y, float* hT, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/* The rule token by token on a state the caller holds, in place, in float32 (a decode step is
+ * seqlen = 1): arguments as for ssd_step plus beta, B and C 16-byte aligned, no D.  `chunk`
+ * is ignored, flags must be 0.  batch = 0 or seqlen = 0 leaves h untouched. */
+int ssd_delta_step(const ssd_problem* p, const void* x, const float* dt, const float* A,
+                   const void* B, const void* C, const void* beta, float* h, void* y, void* stream);
+
+/* Backward pass of ssd_delta_fwd: with g_t = dL/dh_t = dy_t C_t^T + a_{t+1} g_{t+1} (I - beta_{t+1}
+ * B_{t+1} B_{t+1}^T) (and dhT after the last token), z_t = g_t B_t and r_t as above,
+ *
+ *     dx_t = beta_t z_t,  dbeta_t = z_t . r_t,  dC_t = sum over the group's heads of h_t^T dy_t
+ *     dB_t = sum over heads of beta_t (g_t^T r_t - a_t h_{t-1}^T z_t)
+ *     ddt_t = A_h <g_t (I - beta_t B_t B_t^T), a_t h_{t-1}>,  dA_h = sum_{b,t} dt_t ddt_t / A_h
+ *     dh0 = a_0 g_0 (I - beta_0 B_0 B_0^T)
+ *
+ * computed chunk-wise; nothing from a forward call is reused.  dy and dx in the problem dtype
+ * [batch, seqlen, nheads, headdim], ddt float32 [batch, seqlen, nheads], dA float32 [nheads],
+ * dB and dC [batch, seqlen, ngroups, dstate] and dbeta [batch, seqlen, nheads] in the problem
+ * dtype, dhT (NULL = 0) and dh0 (NULL = not written) float32 states.  Every output is
+ * overwritten.  With no tokens dA = 0 and dh0 = dhT.  `ws` must hold
+ * ssd_delta_bwd_workspace_bytes(p) bytes.  Support, precision, alignment and errors as for
+ * ssd_delta_fwd (dbeta aligned to one element, ddt and dA to 4 bytes, the other outputs 16). */
+size_t ssd_delta_bwd_workspace_bytes(const ssd_problem* p);
+int ssd_delta_bwd(const ssd_problem* p, const void* x, const float* dt, const float* A,
+                  const void* B, const void* C, const void* beta, const float* h0, const void* dy,
+                  const float* dhT, void* dx, float* ddt, float* dA, void* dB, void* dC, void* dbeta,
+                  float* dh0, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- The norm of B and C ----
+ * Each row v (one token's one head, dstate elements) of B and of C is normalised, scaled and
+ * turned by its token's position, in one pass over both:
+ *
+ *     v <- w o v / sqrt(s |v|^2 + eps),   s = 1 / dstate (SSD_NORM_RMS) or 1 (SSD_NORM_L2)
+ *     (v_i, v_j) <- (v_i cos f - v_j sin f, v_i sin f + v_j cos f),   f = position * inv_freq_i,
+ *
+ * for i = 0 .. pairs - 1 with j = i + pairs, or the pairs (2i, 2i + 1) where interleaved = 1;
+ * columns from 2 pairs on are not turned.  Angles are reduced in float64.
+ *
+ *   B  [batch, seqlen, bheads, dstate], C [batch, seqlen, cheads, dstate]  problem dtype; the
+ *      heads of a token contiguous, bstride / cstride elements from one token to the next (of
+ *      all batch * seqlen tokens), at least bheads * dstate / cheads * dstate and a multiple
+ *      of 16 bytes: slices of a wider projection need no copy
+ *   wB, wC     [dstate] float32, or NULL = 1
+ *   inv_freq   [pairs] float32 (NULL allowed where pairs = 0)
+ *   positions  [batch, seqlen] int32, or NULL = the token's index in its row
+ *   Bn, Cn     contiguous, like B and C
+ *
+ * dstate in {16, 32, 64, 128, 256}; pairs a multiple of 4 with 2 pairs <= dstate; eps > 0 and
+ * finite; bheads and cheads at most 65536 (one of them may be 0, its pointers NULL);
+ * batch * seqlen under 2^24.  Sums are float32; outputs are rounded once.
+ *
+ * Backward: dB and dC (contiguous, problem dtype) from dBn and dCn (contiguous), and the
+ * weights' gradients dwB, dwC [dstate] float32 (NULL = not written; they are formed for
+ * weights of 1 where wB / wC is NULL), summed over all tokens and heads in a fixed order.
+ * `ws`: ssd_bc_norm_bwd_workspace_bytes(p) bytes, needed where dwB or dwC is given.
+ * Alignment 16 bytes (weights, inv_freq and positions 4); no output may overlap an input, an
+ * output or the workspace.  Errors are reported before any HIP call. */
+typedef enum { SSD_NORM_RMS = 0, SSD_NORM_L2 = 1 } ssd_norm_mode;
+typedef struct {
+    int64_t batch, seqlen, bheads, cheads, dstate, pairs;
+    int64_t bstride, cstride;
+    float eps;
+    int32_t mode, interleaved, dtype;
+} ssd_norm;
+int ssd_bc_norm(const ssd_norm* p, const void* B, const void* C, const float* wB, const float* wC,
+                const float* inv_freq, const int32_t* positions, void* Bn, void* Cn, void* stream);
+size_t ssd_bc_norm_bwd_workspace_bytes(const ssd_norm* p);
+int ssd_bc_norm_bwd(const ssd_norm* p, const void* B, const void* C, const float* wB, const float* wC,
+                    const float* inv_freq, const int32_t* positions, const void* dBn, const void* dCn,
+                    void* dB, void* dC, float* dwB, float* dwC, void* ws, size_t ws_bytes,
+                    void* stream);
+
 /* Static text for a status code. */
 const char* ssd_status_string(int status);
 

@@ -9,6 +9,8 @@ to load, every call raises: there is no fallback path.
     y, hT = diag_scan_fwd(x, dt, A, B, C, D=None, h0=None, chunk=128)
     grads = scan_bwd(x, dt, A, B, C, dy, D=None, h0=None, dhT=None, chunk=256)
 
+The gated delta rule on the same operands and the norm of B and C are in :mod:`.delta`.
+
 Layouts: x [b,T,H,P]; dt [b,T,H] f32; A [H] (scalar decay) or [H,N] (diagonal
 decay) f32; B, C [b,T,G,N]; D [H] f32; h0 [b,H,P,N] f32.  x/B/C share one dtype,
 bfloat16 or float32; y has that dtype, hT is float32.
@@ -20,7 +22,10 @@ import os
 
 __all__ = ["scan_fwd", "diag_scan_fwd", "scan_fwd_into", "scan_bwd", "scan_bwd_into", "bwd_workspace_bytes",
            "Problem", "workspace_bytes",
-           "workspace_layout", "status_string", "version", "library_path", "SSDError"]
+           "workspace_layout", "status_string", "version", "library_path", "SSDError",
+           "delta_fwd", "delta_fwd_into", "delta_fwd_varlen", "delta_fwd_varlen_into", "delta_step",
+           "delta_step_into", "delta_bwd", "delta_bwd_into", "delta_workspace_bytes", "delta_bwd_workspace_bytes",
+           "bc_norm", "bc_norm_into", "bc_norm_bwd", "bc_norm_bwd_into", "bc_norm_bwd_workspace_bytes", "Norm"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libssd.so")
@@ -34,6 +39,9 @@ EXPORTS = ("ssd_workspace_bytes", "ssd_get_workspace_layout", "ssd_scan_fwd", "s
            "ssd_varlen_workspace_bytes", "ssd_scan_fwd_varlen",
            "ssd_step", "ssd_diag_step", "ssd_bwd_workspace_bytes", "ssd_scan_bwd",
            "ssd_diag_bwd_workspace_bytes", "ssd_diag_scan_bwd",
+           "ssd_delta_workspace_bytes", "ssd_delta_fwd", "ssd_delta_varlen_workspace_bytes", "ssd_delta_fwd_varlen",
+           "ssd_delta_step", "ssd_delta_bwd_workspace_bytes", "ssd_delta_bwd",
+           "ssd_bc_norm", "ssd_bc_norm_bwd_workspace_bytes", "ssd_bc_norm_bwd",
            "ssd_status_string", "ssd_version")
 
 
@@ -94,6 +102,7 @@ def _load():
     lib.ssd_status_string.restype = ctypes.c_char_p
     lib.ssd_version.argtypes = []
     lib.ssd_version.restype = ci
+    delta._bind(lib)
     _lib = lib
     return lib
 
@@ -417,3 +426,10 @@ def diag_scan_bwd(x, dt, A, B, C, dy, D=None, h0=None, dhT=None, chunk=128, work
     """Backward pass of the diagonal-decay forward (A [H, N]): as scan_bwd, with dA
     float32 [H, N]."""
     return _backward(True, x, dt, A, B, C, dy, D, h0, dhT, chunk, workspace)
+
+
+from . import delta  # noqa: E402
+from .delta import (DELTA_CHUNK, Norm, bc_norm, bc_norm_bwd, bc_norm_bwd_into,  # noqa: E402,F401
+                    bc_norm_bwd_workspace_bytes, bc_norm_into, delta_bwd, delta_bwd_into, delta_bwd_workspace_bytes,
+                    delta_fwd, delta_fwd_into, delta_fwd_varlen, delta_fwd_varlen_into, delta_step, delta_step_into,
+                    delta_workspace_bytes)

@@ -1,0 +1,1180 @@
+// delta.hpp -- the gated delta rule on the scan's operands (x, dt, A, B, C) with a write
+// strength beta per token and head:
+//
+//   r_t = x_t - a_t h_{t-1} B_t      what the decayed state does not yet answer to key B_t
+//   h_t = a_t h_{t-1} + beta_t r_t B_t^T,   y_t = h_t C_t,   a_t = exp(dt_t A_h)
+//
+// Chunks of L = 64 tokens.  With c the cumulative sum of dt A in the chunk, K and Q the
+// chunk's B and C rows, G_ij = exp(c_i - c_j) (i >= j), h the state entering the chunk:
+//
+//   KK = strict_tril(G o K K^T),  M = tril(G o Q K^T)
+//   S  = (I + KK diag(beta))^-1 KK                       (strictly lower, one per chunk and head)
+//   R  = X - diag(e^c) K h^T,  r = R - S (beta R),  u = beta r
+//   Y  = diag(e^c) Q h^T + M u
+//   h' = e^{c_L} h + (diag(e^{c_L - c}) u)^T K
+//
+// r follows from S without a division by beta (r = (I + KK diag(beta))^-1 R and
+// (I + KK diag(beta))^-1 = I - S diag(beta)), and the adjoint needs the same S:
+//
+//   dU = M^T dY + diag(e^{c_L - c}) K dh'^T,  z = dU - S^T (beta dU),  dX = beta z
+//   dh = e^{c_L} dh' + (diag(e^c) dY)^T Q - (diag(e^c) dX)^T K
+//   dP_ij = G_ij beta_j dY_i . r_j (i >= j),  W_ij = -beta_i G_ij beta_j z_i . r_j (i > j)
+//   dQ = diag(e^c) dY h + dP K,  dbeta_i = z_i . r_i
+//   dK = dP^T Q + (W + W^T) K + diag(e^{c_L - c} beta) r dh' - diag(e^c) dX h
+//   dlog a_t = sum_{s >= t} (dY_s . Y_s - dX_s . X_s) + <dh', h'>          (s in the chunk)
+//
+// Precision.  One bfloat16 rounding of the state in a product would cost 2e-3 of the float32
+// outputs (hT, ddt, dA, dh0), so float32 operands enter the matrix cores as a sum of three
+// bfloat16 terms (8 bits each: the whole float32 mantissa): 3 products against an operand
+// that is bfloat16 already, the 6 of order <= 2 between two split ones.  Products that only
+// reach bfloat16 outputs take fewer terms (noted where).  float32 problems run on the
+// float32 matrix cores throughout.
+//
+// Tiles.  A wave keeps the state of 16 or 32 headdim columns, h^T[n][p], in accumulators.
+// The accumulator layout (lane l: rows 4 (l / 16) + e, column l % 16) of two row tiles is a
+// matrix-core B operand whose k index runs 16 (e / 4) + 4 (l / 16) + e % 4; with the A
+// operand read in that same k order, every product of the chunk feeds the next one from
+// registers, and waves never exchange data.
+#pragma once
+
+#include <type_traits>
+
+#include "kernels.hpp"
+
+namespace ssd {
+namespace delta {
+
+constexpr int L = 64;                 // tokens per chunk
+constexpr int kTri = 10;              // 16 x 16 blocks on and below the diagonal of a 64 x 64 table
+constexpr int kTab = 2 * kTri * 256;  // floats of one (chunk, head)'s S and M tables
+constexpr int kVec = 4 * L;           // floats of its e^c, e^{c_L - c} and c (log2 units, two parts)
+constexpr int kFrag = 6;              // 16 x 32 operand fragments covering a triangular 64 x 64 table
+
+struct Args {
+    Rows rows;
+    int64_t T;   // dense: tokens per row; packed: tokens of the axis
+    int H, P, N, G, nc;
+    int ntab;    // chunks of the table axis (dense b nc, packed kcap)
+    const void* x;
+    const float* dt;
+    const float* A;
+    const void* B;
+    const void* C;
+    const void* beta;
+    const float* h0;
+    void* y;
+    float* hT;
+    float* tab;  // [ntab][H][kTab]
+    float* vec;  // [ntab][H][kVec]
+    // backward
+    const void* dy;
+    const float* dhT;
+    void* dx;
+    float* ddt;
+    float* dA;
+    void* dB;
+    void* dC;
+    void* dbeta;
+    float* dh0;
+    void* r;      // [b T][H][P] residuals
+    void* z;      // [b T][H][P]
+    void* hin;    // [ntab][H][P][N] state entering each chunk
+    short* hlo;   // bfloat16: what hin's rounding left of the float32 state (split_state)
+    void* lin;    // [ntab][H][P][N] dh' of each chunk
+    float* hend;  // [b H][P][N] state after the last chunk
+    float* dyy;   // [slices][b H][T] per-slice dY . Y
+    float* dxx;   // [slices][b H][T] per-slice dX . X
+    float* tot;   // [slices][ntab][H] per-slice <dh', h'> of each chunk
+    float* dAp;   // [ntab][H]
+    float* part;  // [nsub][2][b T][G][N] partial dK, dQ when a group's heads are shared out
+    int slices, nsub;
+    hipStream_t stream;
+};
+
+// ---------------------------------------------------------------------------
+// float32 operands as sums of matrix-core operands
+// ---------------------------------------------------------------------------
+template <typename T> struct Sp;
+template <> struct Sp<bf16> { bf16x8 t[3]; };
+template <> struct Sp<float> { f32x8 t[1]; };
+template <typename T> constexpr int kTerms = std::is_same<T, bf16>::value ? 3 : 1;
+
+__device__ __forceinline__ void split8(f32x8 v, Sp<bf16>& s) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            s.t[k][e] = (bf16)v[e];
+            v[e] -= (float)s.t[k][e];
+        }
+}
+__device__ __forceinline__ void split8(f32x8 v, Sp<float>& s) { s.t[0] = v; }
+
+// c += a b, a exact in T, b in its first NB terms
+template <int NB, typename T, typename V>
+__device__ __forceinline__ f32x4 mma_es(f32x4 c, V a, const Sp<T>& b) {
+#pragma unroll
+    for (int k = 0; k < (NB < kTerms<T> ? NB : kTerms<T>); ++k) c = mma(c, a, b.t[k]);
+    return c;
+}
+// c += a b, both split: the products whose order is under ORD
+template <int ORD, typename T>
+__device__ __forceinline__ f32x4 mma_ss(f32x4 c, const Sp<T>& a, const Sp<T>& b) {
+#pragma unroll
+    for (int i = 0; i < kTerms<T>; ++i)
+#pragma unroll
+        for (int j = 0; j < kTerms<T>; ++j)
+            if (i + j < ORD) c = mma(c, a.t[i], b.t[j]);
+    return c;
+}
+// c += a b over k = 16 in float32 (k index 4 (lane / 16) + e for both operands)
+__device__ __forceinline__ f32x4 mma16(f32x4 c, f32x4 a, f32x4 b) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+}
+
+// A float32 state as a bfloat16 (rounded to nearest) and the 16-bit rest of its bit pattern:
+// the gradient products read the first alone, the decay gradient's <dh', h'> both, exactly.
+__device__ __forceinline__ void split_state(float v, bf16& hi, short& lo) {
+    const unsigned b = __builtin_bit_cast(unsigned, v);
+    const bool fin = (b & 0x7f800000u) != 0x7f800000u;
+    const unsigned t = fin ? b + 0x8000u : b | ((b & 0xffffu) ? 0x400000u : 0u);
+    hi = __builtin_bit_cast(bf16, (unsigned short)(t >> 16));
+    lo = fin ? (short)(b - (t & 0xffff0000u)) : (short)0;
+}
+__device__ __forceinline__ float join_state(bf16 hi, short lo) {
+    return __builtin_bit_cast(float, ((unsigned)__builtin_bit_cast(unsigned short, hi) << 16) + (unsigned)(int)lo);
+}
+
+__device__ __forceinline__ f32x8 join(f32x4 a, f32x4 b) {
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+__device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// A operand of row `row`, columns k0 + 16 (e / 4) + 4 q + e % 4, of a row-major tile
+template <typename T>
+__device__ __forceinline__ typename V8<T>::type frag_k(const T* M, int ld, int row, int k0, int q) {
+    return join(ld4(M + row * ld + k0 + 4 * q), ld4(M + row * ld + k0 + 16 + 4 * q));
+}
+
+__host__ __device__ constexpr int tri(int i, int j) { return i * (i + 1) / 2 + j; }
+// fragment of row tile i, 32 columns t of a lower triangular table (t <= i / 2), and of an
+// upper triangular one (t >= i / 2)
+__host__ __device__ constexpr int frag_lo(int i, int t) { return i < 2 ? i : 2 + (i - 2) * 2 + t; }
+__host__ __device__ constexpr int frag_up(int i, int t) { return i < 2 ? i * 2 + t : 4 + (i - 2); }
+
+// The triangular table `src` (16 x 16 blocks, row-major, as k_delta_prep stores it) into LDS as
+// operand fragments: dst[term][fragment][lane][8].  UP: its transpose.
+template <typename T, int NT, bool UP>
+__device__ void stage_tri(const float* __restrict__ src, T* dst, int tid, int nthr) {
+    // 10 stored blocks and the two zero ones that complete fragments; 64 pieces of 4 each
+    for (int p = tid; p < 12 * 64; p += nthr) {
+        const int blk = p >> 6, l = p & 63, l16 = l & 15, q = l >> 4;
+        int i, j;  // block row, column
+        if (blk < kTri) {
+            i = blk < 1 ? 0 : blk < 3 ? 1 : blk < 6 ? 2 : 3;
+            j = blk - tri(i, 0);
+        } else {
+            i = blk == kTri ? 0 : 2;
+            j = i + 1;
+        }
+        f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (blk < kTri) {
+            if (UP) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = src[blk * 256 + (4 * q + e) * 16 + l16];
+            } else {
+                v = ld4(src + blk * 256 + l16 * 16 + 4 * q);
+            }
+        }
+        const int f = UP ? frag_up(j, i >> 1) : frag_lo(i, j >> 1);
+        T* d = dst + f * 512 + l * 8 + 4 * ((UP ? i : j) & 1);
+#pragma unroll
+        for (int k = 0; k < NT; ++k) {
+            typename V4<T>::type o;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                o[e] = from_f<T>(v[e]);
+                v[e] -= to_f(o[e]);
+            }
+            st4(d + k * kFrag * 512, o);
+        }
+    }
+}
+template <typename T, int NT>
+__device__ __forceinline__ Sp<T> frag_tab(const T* tab, int f, int lane) {
+    Sp<T> s;
+#pragma unroll
+    for (int k = 0; k < NT; ++k) s.t[k] = ld8(tab + (k * kFrag + f) * 512 + lane * 8);
+    return s;
+}
+
+// rows [0, n) x cols [0, w) of src (row stride ss) into dst (row stride ds), rows [n, 64) and
+// columns [w, wpad) zero; w a multiple of 8
+template <typename T>
+__device__ __forceinline__ void stage_rows(const T* __restrict__ src, int64_t ss, T* dst, int ds, int n, int w,
+                                           int wpad, int tid, int nthr, int nrows = L) {
+    const int per = wpad >> 3;
+    for (int p = tid; p < nrows * per; p += nthr) {
+        const int row = p / per, col = (p - row * per) << 3;
+        typename V8<T>::type v = zero8<T>();
+        if (row < n && col < w) v = ld8(src + row * ss + col);
+        st8(dst + row * ds + col, v);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_rows(T* __restrict__ dst, int64_t ds, const T* src, int ss, int n, int w,
+                                           int tid, int nthr) {
+    const int per = w >> 3;
+    for (int p = tid; p < n * per; p += nthr) {
+        const int row = p / per, col = (p - row * per) << 3;
+        st8(dst + row * ds + col, ld8(src + row * ss + col));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// k_delta_prep: S and M of one (chunk, head), and the chunk's decay factors.  One work-group of
+// 4 waves; K K^T and Q K^T on the matrix cores straight from global rows, S by blocked
+// forward substitution in float32 (S_ii in registers, one lane per column; below the
+// diagonal S_ij = Z - S_ii (beta Z), Z = KK_ij - sum_k KK_ik (beta S_kj), wave j taking
+// block column j).  Decay sums and their differences are float64, so a strongly decayed
+// chunk keeps the exact ratio of neighbouring tokens.
+// ---------------------------------------------------------------------------
+template <typename T, int N>
+__global__ __launch_bounds__(256) void k_delta_prep(Args a) {
+    constexpr int LD = L + 4;
+    constexpr double LOG2E = 1.4426950408889634;
+    __shared__ double cs[L];
+    __shared__ float bet[L];
+    __shared__ __attribute__((aligned(16))) float Km[L * LD];  // KK, zeros on and above the diagonal
+    __shared__ __attribute__((aligned(16))) float Sd[4 * 256];  // S_ii
+    const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
+    const int H = a.H, G = a.G;
+    const int h = (int)(blockIdx.x % (unsigned)H), kk = (int)(blockIdx.x / (unsigned)H);
+    if (kk >= a.rows.total_chunks()) return;
+    const int row = a.rows.row_of(kk), c = kk - a.rows.kbase(row);
+    const int64_t t0 = a.rows.tok0(row) + (int64_t)c * L;
+    const int n = (int)min((int64_t)L, a.rows.len(row) - (int64_t)c * L);
+    const int g = h / (H / G);
+
+    if (w == 0) {
+        const bool on = lane < n;
+        const int64_t t = t0 + (on ? lane : 0);
+        double v = on ? (double)a.dt[t * H + h] * (double)a.A[h] * LOG2E : 0.0;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const double o = __shfl_up(v, off, 64);
+            if (lane >= off) v += o;
+        }
+        cs[lane] = v;
+        bet[lane] = on ? to_f(static_cast<const T*>(a.beta)[t * H + h]) : 0.f;
+        const double last = __shfl(v, 63, 64);
+        float* vec = a.vec + ((int64_t)kk * H + h) * kVec;
+        vec[lane] = exp2f_fast((float)v);
+        vec[L + lane] = exp2f_fast((float)(last - v));
+        vec[2 * L + lane] = (float)v;
+        vec[3 * L + lane] = (float)(v - (double)(float)v);
+    }
+    // K K^T and Q K^T: wave w takes row tile w against column tiles 0 .. w
+    const T* Kg = static_cast<const T*>(a.B) + (t0 * G + g) * N;
+    const T* Qg = static_cast<const T*>(a.C) + (t0 * G + g) * N;
+    const int64_t rs = (int64_t)G * N;
+    f32x4 kt[4], qt[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) kt[j] = qt[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int ri = w * 16 + l16;
+    const int rc = ri < n ? ri : n - 1;
+#pragma unroll
+    for (int ks = 0; ks < (N + 31) / 32; ++ks) {
+        const int col = ks * 32 + 8 * q;
+        const bool in = N >= 32 || col < N;
+        const int cc = in ? col : 0;
+        const auto ka = sel8(in && ri < n, ld8(Kg + rc * rs + cc));
+        const auto qa = sel8(in && ri < n, ld8(Qg + rc * rs + cc));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j > w) break;
+            const int rj = j * 16 + l16;
+            const auto kb = sel8(in && rj < n, ld8(Kg + (rj < n ? rj : n - 1) * rs + cc));
+            kt[j] = mma(kt[j], ka, kb);
+            qt[j] = mma(qt[j], qa, kb);
+        }
+    }
+    __syncthreads();
+    float* St = a.tab + ((int64_t)kk * H + h) * kTab;
+    float* Mt = St + kTri * 256;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j > w) break;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i16 = 4 * q + r, i = w * 16 + i16, jj = j * 16 + l16;
+            const float gam = i >= jj ? exp2f_fast((float)(cs[i] - cs[jj])) : 0.f;
+            Mt[tri(w, j) * 256 + i16 * 16 + l16] = qt[j][r] * gam;
+            Km[i * LD + jj] = i > jj ? kt[j][r] * gam : 0.f;
+        }
+    }
+    __syncthreads();
+    {  // S_ww: column l16, rows in order
+        float s[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float* kr = Km + (w * 16 + i) * LD + w * 16;
+            float v = kr[l16];
+#pragma unroll
+            for (int k = 0; k < i; ++k) v -= kr[k] * (bet[w * 16 + k] * s[k]);
+            s[i] = v;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if ((i >> 2) == q) {
+                Sd[w * 256 + i * 16 + l16] = s[i];
+                St[tri(w, w) * 256 + i * 16 + l16] = s[i];
+            }
+    }
+    __syncthreads();
+    {  // block column w
+        f32x4 col[4];  // S_kw, lane: rows 4q + e, column l16
+#pragma unroll
+        for (int e = 0; e < 4; ++e) col[0][e] = Sd[w * 256 + (4 * q + e) * 16 + l16];
+#pragma unroll
+        for (int m = 1; m < 4; ++m) {  // block row w + m
+            const int i = w + m;
+            if (i > 3) break;
+            f32x4 zv = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < m; ++k) {
+                f32x4 bs;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) bs[e] = bet[(w + k) * 16 + 4 * q + e] * col[k][e];
+                zv = mma16(zv, ld4(Km + (i * 16 + l16) * LD + (w + k) * 16 + 4 * q), bs);
+            }
+            f32x4 bz;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                zv[e] = Km[(i * 16 + 4 * q + e) * LD + w * 16 + l16] - zv[e];
+                bz[e] = bet[i * 16 + 4 * q + e] * zv[e];
+            }
+            const f32x4 d = mma16(f32x4{0.f, 0.f, 0.f, 0.f}, ld4(Sd + i * 256 + l16 * 16 + 4 * q), bz);
+            col[m] = zv - d;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) St[tri(i, w) * 256 + (4 * q + e) * 16 + l16] = col[m][e];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// LDS of the chunk walks (bytes).  Where the K and Q tiles do not fit together (float32 at
+// dstate 256) they take turns in one.
+// ---------------------------------------------------------------------------
+template <typename T, int N>
+struct Cfg {
+    static constexpr int NP = N < 32 ? 32 : N;      // key columns, padded to a matrix-core k step
+    static constexpr int LDK = NP + 8;
+    static constexpr bool SHARE = sizeof(T) == 4 && N == 256;
+    static constexpr int KT = L * LDK;              // elements of one K / Q tile
+    static constexpr int NT = kTerms<T>;
+    static constexpr int ldx(int sw) { return sw + 8; }
+    static size_t walk_bytes(int sw, int mterms, int xtiles) {
+        return (size_t)((SHARE ? 1 : 2) * KT + (NT + mterms) * kFrag * 512 + xtiles * L * ldx(sw)) * sizeof(T) +
+               (size_t)(3 * L + 4 * L) * 4;
+    }
+};
+
+// ---------------------------------------------------------------------------
+// k_delta: the chunks of one (row, head) and a slice of 16 CT W headdim columns, in order
+// (W waves, each CT column tiles, no exchange between waves).  SAVE = false writes y and
+// hT.  SAVE = true is the backward's first walk: it writes the residuals r, the state
+// entering every chunk and after the last, and the per-token dY . Y (Y in float32, all
+// terms) instead.
+// ---------------------------------------------------------------------------
+template <typename T, int N, int CT, bool SAVE>
+__global__ __launch_bounds__(256) void k_delta(Args a) {
+    typedef Cfg<T, N> CF;
+    constexpr int NP = CF::NP, LDK = CF::LDK, NTL = N / 16, KS = NP / 32, NT = CF::NT;
+    constexpr int MT = SAVE ? NT : 1;  // terms of M (1: y is rounded to the problem dtype anyway)
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
+    const int H = a.H, G = a.G, P = a.P;
+    const int SW = 16 * CT * (nthr >> 6), ldx = CF::ldx(SW);
+    T* Ks = reinterpret_cast<T*>(smem);
+    T* Qs = CF::SHARE ? Ks : Ks + CF::KT;
+    T* Sf = Qs + CF::KT;
+    T* Mf = Sf + NT * kFrag * 512;
+    T* Xs = Mf + MT * kFrag * 512;
+    T* Ys = Xs + L * ldx;  // SAVE: dY rows
+    float* ecs = reinterpret_cast<float*>(Ys + (SAVE ? L * ldx : 0));
+    float* ews = ecs + L;
+    float* bts = ews + L;
+    float* dots = bts + L;  // SAVE: [wave][token]
+
+    const int nsl = P / SW, BH = a.rows.nrows * H;
+    const int sl = (int)(blockIdx.x % (unsigned)nsl);
+    int k = (int)(blockIdx.x / (unsigned)nsl);
+    const int64_t bh = k;
+    const int h = (int)(bh % H), row = (int)(bh / H), g = h / (H / G);
+    const int64_t Tn = a.rows.len(row), tok0 = a.rows.tok0(row);
+    const int nc = a.rows.nchunks(row), kb0 = a.rows.kbase(row);
+    const int p0 = sl * SW, pw = w * 16 * CT;  // first column of the slice, of this wave in it
+
+    f32x4 acc[NTL][CT];  // h^T: row n = 16 t + 4q + e, column p
+#pragma unroll
+    for (int t = 0; t < NTL; ++t)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+            acc[t][ct] = a.h0 ? ld4(a.h0 + (bh * P + p0 + pw + ct * 16 + l16) * N + t * 16 + 4 * q)
+                              : f32x4{0.f, 0.f, 0.f, 0.f};
+
+    for (int c = 0; c < nc; ++c) {
+        const int64_t t0 = tok0 + (int64_t)c * L;
+        const int n = (int)min((int64_t)L, Tn - (int64_t)c * L);
+        const int64_t e = (int64_t)(kb0 + c) * H + h;
+        const T* Kg = static_cast<const T*>(a.B) + (t0 * G + g) * N;
+        const T* Qg = static_cast<const T*>(a.C) + (t0 * G + g) * N;
+        __syncthreads();  // the previous chunk's tiles are no longer read
+        stage_rows(Qg, (int64_t)G * N, Qs, LDK, n, N, NP, tid, nthr);
+        if (!CF::SHARE) stage_rows(Kg, (int64_t)G * N, Ks, LDK, n, N, NP, tid, nthr);
+        stage_rows(static_cast<const T*>(a.x) + (t0 * H + h) * P + p0, (int64_t)H * P, Xs, ldx, n, SW, SW, tid, nthr);
+        if (SAVE)
+            stage_rows(static_cast<const T*>(a.dy) + (t0 * H + h) * P + p0, (int64_t)H * P, Ys, ldx, n, SW, SW, tid,
+                       nthr);
+        stage_tri<T, NT, false>(a.tab + e * kTab, Sf, tid, nthr);
+        stage_tri<T, MT, false>(a.tab + e * kTab + kTri * 256, Mf, tid, nthr);
+        for (int t = tid; t < L; t += nthr) {
+            ecs[t] = a.vec[e * kVec + t];
+            ews[t] = a.vec[e * kVec + L + t];
+            bts[t] = t < n ? to_f(static_cast<const T*>(a.beta)[(t0 + t) * H + h]) : 0.f;
+        }
+        __syncthreads();
+        if (SAVE) {
+            const int64_t ho = (e * P + p0 + pw) * N;
+#pragma unroll
+            for (int t = 0; t < NTL; ++t)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    const int64_t o = ho + (ct * 16 + l16) * N + t * 16 + 4 * q;
+                    if constexpr (std::is_same<T, bf16>::value) {
+                        bf16x4 hi;
+                        s16x4 lo;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            bf16 hv;
+                            short lv;
+                            split_state(acc[t][ct][i], hv, lv);
+                            hi[i] = hv;
+                            lo[i] = lv;
+                        }
+                        st4(static_cast<T*>(a.hin) + o, hi);
+                        *reinterpret_cast<s16x4*>(a.hlo + o) = lo;
+                    } else {
+                        st4(static_cast<T*>(a.hin) + o, acc[t][ct]);
+                    }
+                }
+        }
+
+        // K h^T and Q h^T (Q: two terms are enough for a bfloat16 y)
+        f32x4 v[4][CT], yq[4][CT];
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) v[it][ct] = yq[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+        auto state_products = [&](const T* tile, f32x4(&o)[4][CT], auto nb) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                Sp<T> hs[CT];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    split8(join(acc[2 * ks][ct], 2 * ks + 1 < NTL ? acc[2 * ks + 1 < NTL ? 2 * ks + 1 : 0][ct]
+                                                                  : f32x4{0.f, 0.f, 0.f, 0.f}),
+                           hs[ct]);
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const auto fr = frag_k(tile, LDK, it * 16 + l16, ks * 32, q);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) o[it][ct] = mma_es<decltype(nb)::value>(o[it][ct], fr, hs[ct]);
+                }
+            }
+        };
+        state_products(Qs, yq, std::integral_constant<int, SAVE ? 3 : 2>());
+        if (CF::SHARE) {
+            __syncthreads();
+            stage_rows(Kg, (int64_t)G * N, Ks, LDK, n, N, NP, tid, nthr);
+            __syncthreads();
+        }
+        state_products(Ks, v, std::integral_constant<int, 3>());
+
+        // R, then r = R - S (beta R)
+        Sp<T> b2[2][CT];
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = it * 16 + 4 * q + i;
+                    v[it][ct][i] = to_f(Xs[t * ldx + pw + ct * 16 + l16]) - ecs[t] * v[it][ct][i];
+                }
+        auto scaled = [&](const float* s, bool two) {  // s_t v_t as operands
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    f32x4 lo = v[2 * t][ct], hi = v[2 * t + 1][ct];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r0 = 32 * t + 4 * q + i;
+                        lo[i] *= two ? s[r0] * bts[r0] : s[r0];
+                        hi[i] *= two ? s[r0 + 16] * bts[r0 + 16] : s[r0 + 16];
+                    }
+                    split8(join(lo, hi), b2[t][ct]);
+                }
+        };
+        scaled(bts, false);
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            f32x4 d[CT];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) d[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int t = 0; t <= it / 2; ++t) {
+                const Sp<T> sf = frag_tab<T, NT>(Sf, frag_lo(it, t), lane);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) d[ct] = mma_ss<3>(d[ct], sf, b2[t][ct]);
+            }
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) v[it][ct] -= d[ct];
+        }
+        // Y = e^c Q h^T + M u
+        scaled(bts, false);
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) yq[it][ct][i] *= ecs[it * 16 + 4 * q + i];
+#pragma unroll
+            for (int t = 0; t <= it / 2; ++t) {
+                const Sp<T> mf = frag_tab<T, MT>(Mf, frag_lo(it, t), lane);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    yq[it][ct] = SAVE ? mma_ss<3>(yq[it][ct], mf, b2[t][ct])
+                                      : mma_es<2>(yq[it][ct], mf.t[0], b2[t][ct]);
+            }
+        }
+        // h' = e^{c_L} h + K^T (e^{c_L - c} u)
+        scaled(ews, true);
+        const float el = ecs[L - 1];
+#pragma unroll
+        for (int t = 0; t < NTL; ++t) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) acc[t][ct] *= el;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const auto kf = frag_rows_split(Ks, LDK, ks * 32 + 4 * q, ks * 32 + 16 + 4 * q, t * 16, lane);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) acc[t][ct] = mma_es<3>(acc[t][ct], kf, b2[ks][ct]);
+            }
+        }
+        // out through the (own columns of the) x tile: y, or r and the dY . Y sums
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = it * 16 + 4 * q + i;
+                float dot = 0.f;
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    T* o = Xs + t * ldx + pw + ct * 16 + l16;
+                    if (SAVE) {
+                        dot += to_f(Ys[t * ldx + pw + ct * 16 + l16]) * yq[it][ct][i];
+                        *o = from_f<T>(v[it][ct][i]);
+                    } else {
+                        *o = from_f<T>(yq[it][ct][i]);
+                    }
+                }
+                if (SAVE) {
+#pragma unroll
+                    for (int off = 8; off > 0; off >>= 1) dot += __shfl_xor(dot, off, 64);
+                    if (l16 == 0) dots[w * L + t] = dot;
+                }
+            }
+        __syncthreads();
+        store_rows(static_cast<T*>(SAVE ? a.r : a.y) + (t0 * H + h) * P + p0, (int64_t)H * P, Xs, ldx, n, SW, tid,
+                   nthr);
+        if (SAVE) {
+            for (int t = tid; t < n; t += nthr) {
+                float s = 0.f;
+                for (int k2 = 0; k2 < (nthr >> 6); ++k2) s += dots[k2 * L + t];
+                a.dyy[((int64_t)sl * BH + bh) * a.T + (int64_t)c * L + t] = s;
+            }
+        }
+    }
+    if (float* hT = SAVE ? a.hend : a.hT) {
+#pragma unroll
+        for (int t = 0; t < NTL; ++t)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+                st4(hT + (bh * P + p0 + pw + ct * 16 + l16) * N + t * 16 + 4 * q, acc[t][ct]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// k_delta_rev: the adjoint walk, chunks in reverse; the same slices and layout, the adjoint
+// state dh^T[n][p] in accumulators.  Writes dx, z, dh' of every chunk (problem dtype), the
+// per-token dX . X, <dh', h'> of every chunk, and dh0.
+// ---------------------------------------------------------------------------
+template <typename T, int N, int CT>
+__global__ __launch_bounds__(256) void k_delta_rev(Args a) {
+    typedef Cfg<T, N> CF;
+    constexpr int NP = CF::NP, LDK = CF::LDK, NTL = N / 16, KS = NP / 32, NT = CF::NT;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
+    const int H = a.H, G = a.G, P = a.P;
+    const int SW = 16 * CT * (nthr >> 6), ldx = CF::ldx(SW);
+    T* Ks = reinterpret_cast<T*>(smem);
+    T* Qs = CF::SHARE ? Ks : Ks + CF::KT;
+    T* Sf = Qs + CF::KT;
+    T* Mf = Sf + NT * kFrag * 512;
+    T* Xs = Mf + NT * kFrag * 512;
+    T* Ys = Xs + L * ldx;  // dY rows, then z
+    float* ecs = reinterpret_cast<float*>(Ys + L * ldx);
+    float* ews = ecs + L;
+    float* bts = ews + L;
+    float* dots = bts + L;  // [wave][token]
+
+    const int nsl = P / SW, BH = a.rows.nrows * H;
+    const int sl = (int)(blockIdx.x % (unsigned)nsl);
+    const int64_t bh = blockIdx.x / (unsigned)nsl;
+    const int h = (int)(bh % H), row = (int)(bh / H), g = h / (H / G);
+    const int64_t Tn = a.rows.len(row), tok0 = a.rows.tok0(row);
+    const int nc = a.rows.nchunks(row), kb0 = a.rows.kbase(row);
+    const int p0 = sl * SW, pw = w * 16 * CT;
+
+    f32x4 acc[NTL][CT];  // dh^T
+#pragma unroll
+    for (int t = 0; t < NTL; ++t)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+            acc[t][ct] = a.dhT ? ld4(a.dhT + (bh * P + p0 + pw + ct * 16 + l16) * N + t * 16 + 4 * q)
+                               : f32x4{0.f, 0.f, 0.f, 0.f};
+
+    for (int c = nc - 1; c >= 0; --c) {
+        const int64_t t0 = tok0 + (int64_t)c * L;
+        const int n = (int)min((int64_t)L, Tn - (int64_t)c * L);
+        const int64_t e = (int64_t)(kb0 + c) * H + h;
+        const T* Kg = static_cast<const T*>(a.B) + (t0 * G + g) * N;
+        const T* Qg = static_cast<const T*>(a.C) + (t0 * G + g) * N;
+        {  // <dh', h'> over this slice
+            const bool last = c + 1 == nc;
+            const int64_t ho = ((last ? bh : e + H) * P + p0 + pw) * N;
+            float s = 0.f;
+#pragma unroll
+            for (int t = 0; t < NTL; ++t)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    const int64_t o = ho + (ct * 16 + l16) * N + t * 16 + 4 * q;
+                    f32x4 hv;
+                    if (last) {
+                        hv = ld4(a.hend + o);
+                    } else if constexpr (std::is_same<T, bf16>::value) {
+                        const bf16x4 hi = ld4(static_cast<const T*>(a.hin) + o);
+                        const s16x4 lo = *reinterpret_cast<const s16x4*>(a.hlo + o);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) hv[i] = join_state(hi[i], lo[i]);
+                    } else {
+                        hv = ld4(static_cast<const T*>(a.hin) + o);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s += hv[i] * acc[t][ct][i];
+                }
+#pragma unroll
+            for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
+            __syncthreads();  // the sums of the chunk before are no longer read
+            if (lane == 0) dots[w] = s;
+            __syncthreads();
+            if (tid == 0) {
+                float v = 0.f;
+                for (int k2 = 0; k2 < (nthr >> 6); ++k2) v += dots[k2];
+                a.tot[(int64_t)sl * a.ntab * H + e] = v;
+            }
+        }
+        __syncthreads();
+        stage_rows(Kg, (int64_t)G * N, Ks, LDK, n, N, NP, tid, nthr);
+        if (!CF::SHARE) stage_rows(Qg, (int64_t)G * N, Qs, LDK, n, N, NP, tid, nthr);
+        stage_rows(static_cast<const T*>(a.x) + (t0 * H + h) * P + p0, (int64_t)H * P, Xs, ldx, n, SW, SW, tid, nthr);
+        stage_rows(static_cast<const T*>(a.dy) + (t0 * H + h) * P + p0, (int64_t)H * P, Ys, ldx, n, SW, SW, tid, nthr);
+        stage_tri<T, NT, true>(a.tab + e * kTab, Sf, tid, nthr);
+        stage_tri<T, NT, true>(a.tab + e * kTab + kTri * 256, Mf, tid, nthr);
+        for (int t = tid; t < L; t += nthr) {
+            ecs[t] = a.vec[e * kVec + t];
+            ews[t] = a.vec[e * kVec + L + t];
+            bts[t] = t < n ? to_f(static_cast<const T*>(a.beta)[(t0 + t) * H + h]) : 0.f;
+        }
+        __syncthreads();
+        {
+            T* lp = static_cast<T*>(a.lin) + (e * P + p0 + pw) * N;
+#pragma unroll
+            for (int t = 0; t < NTL; ++t)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    typename V4<T>::type o;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = from_f<T>(acc[t][ct][i]);
+                    st4(lp + (ct * 16 + l16) * N + t * 16 + 4 * q, o);
+                }
+        }
+        // dU = e^{c_L - c} K dh'^T + M^T dY
+        f32x4 v[4][CT];
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) v[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            Sp<T> hs[CT];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+                split8(join(acc[2 * ks][ct], 2 * ks + 1 < NTL ? acc[2 * ks + 1 < NTL ? 2 * ks + 1 : 0][ct]
+                                                              : f32x4{0.f, 0.f, 0.f, 0.f}),
+                       hs[ct]);
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const auto fr = frag_k(Ks, LDK, it * 16 + l16, ks * 32, q);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) v[it][ct] = mma_es<3>(v[it][ct], fr, hs[ct]);
+            }
+        }
+        typename V8<T>::type dyf[2][CT];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+                dyf[t][ct] = frag_rows_split(Ys, ldx, 32 * t + 4 * q, 32 * t + 16 + 4 * q, pw + ct * 16, lane);
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[it][ct][i] *= ews[it * 16 + 4 * q + i];
+#pragma unroll
+            for (int t = it / 2; t < 2; ++t) {
+                const Sp<T> mf = frag_tab<T, NT>(Mf, frag_up(it, t), lane);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                    for (int k2 = 0; k2 < NT; ++k2) v[it][ct] = mma(v[it][ct], mf.t[k2], dyf[t][ct]);
+            }
+        }
+        // z = dU - S^T (beta dU)
+        Sp<T> b2[2][CT];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                f32x4 lo = v[2 * t][ct], hi = v[2 * t + 1][ct];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    lo[i] *= bts[32 * t + 4 * q + i];
+                    hi[i] *= bts[32 * t + 16 + 4 * q + i];
+                }
+                split8(join(lo, hi), b2[t][ct]);
+            }
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            f32x4 d[CT];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) d[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int t = it / 2; t < 2; ++t) {
+                const Sp<T> sf = frag_tab<T, NT>(Sf, frag_up(it, t), lane);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) d[ct] = mma_ss<3>(d[ct], sf, b2[t][ct]);
+            }
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) v[it][ct] -= d[ct];
+        }
+        // dX = beta z, its dot with X; the tiles leave through LDS (own columns)
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = it * 16 + 4 * q + i;
+                float dot = 0.f;
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    const int o = t * ldx + pw + ct * 16 + l16;
+                    const float dxv = bts[t] * v[it][ct][i];
+                    dot += dxv * to_f(Xs[o]);
+                    Xs[o] = from_f<T>(dxv);
+                    Ys[o] = from_f<T>(v[it][ct][i]);
+                    v[it][ct][i] = dxv;
+                }
+#pragma unroll
+                for (int off = 8; off > 0; off >>= 1) dot += __shfl_xor(dot, off, 64);
+                if (l16 == 0) dots[w * L + t] = dot;
+            }
+        // dh = e^{c_L} dh' - K^T (e^c dX) + Q^T (e^c dY)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                f32x4 lo = v[2 * t][ct], hi = v[2 * t + 1][ct];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    lo[i] *= -ecs[32 * t + 4 * q + i];
+                    hi[i] *= -ecs[32 * t + 16 + 4 * q + i];
+                }
+                split8(join(lo, hi), b2[t][ct]);
+            }
+        const float el = ecs[L - 1];
+#pragma unroll
+        for (int t = 0; t < NTL; ++t) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) acc[t][ct] *= el;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const auto kf = frag_rows_split(Ks, LDK, ks * 32 + 4 * q, ks * 32 + 16 + 4 * q, t * 16, lane);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) acc[t][ct] = mma_es<3>(acc[t][ct], kf, b2[ks][ct]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                f32x8 d;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    d[i] = to_f(dyf[t][ct][i]) * ecs[32 * t + 16 * (i >> 2) + 4 * q + (i & 3)];
+                split8(d, b2[t][ct]);
+            }
+        if (CF::SHARE) {
+            __syncthreads();
+            stage_rows(Qg, (int64_t)G * N, Qs, LDK, n, N, NP, tid, nthr);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < NTL; ++t)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const auto qf = frag_rows_split(Qs, LDK, ks * 32 + 4 * q, ks * 32 + 16 + 4 * q, t * 16, lane);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) acc[t][ct] = mma_es<3>(acc[t][ct], qf, b2[ks][ct]);
+            }
+        store_rows(static_cast<T*>(a.dx) + (t0 * H + h) * P + p0, (int64_t)H * P, Xs, ldx, n, SW, tid, nthr);
+        store_rows(static_cast<T*>(a.z) + (t0 * H + h) * P + p0, (int64_t)H * P, Ys, ldx, n, SW, tid, nthr);
+        for (int t = tid; t < n; t += nthr) {
+            float s = 0.f;
+            for (int k2 = 0; k2 < (nthr >> 6); ++k2) s += dots[k2 * L + t];
+            a.dxx[((int64_t)sl * BH + bh) * a.T + (int64_t)c * L + t] = s;
+        }
+    }
+    if (a.dh0) {
+#pragma unroll
+        for (int t = 0; t < NTL; ++t)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+                st4(a.dh0 + (bh * P + p0 + pw + ct * 16 + l16) * N + t * 16 + 4 * q, acc[t][ct]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// k_delta_grad: dB and dC of one chunk, group and slab of NS key columns, summed over a share
+// of the group's heads in registers (and dbeta, by the first slab).  Wave w owns token tile
+// w as the COLUMNS of dQ^T[n][i] and dK^T[n][i], so the 64 x 64 gradient tables it needs,
+// dP^T and the two sides of W, come out of the matrix cores in the layout their products
+// read.  Everything here ends in the problem dtype: one bfloat16 term per operand, but two
+// for the tables, which the products above form in float32.
+// ---------------------------------------------------------------------------
+template <typename T, int N>
+struct GradCfg {
+    static constexpr int NS = N < 64 ? N : 64;
+    static constexpr int LDN = NS + 8;
+    static size_t bytes(int P) {
+        const int PP = P < 32 ? 32 : P;
+        return (size_t)(2 * L + 2 * PP) * LDN * sizeof(T) + (size_t)5 * L * 4;
+    }
+};
+
+template <typename T, int N>
+__global__ __launch_bounds__(256) void k_delta_grad(Args a) {
+    typedef GradCfg<T, N> CF;
+    constexpr int NS = CF::NS, LDN = CF::LDN, NTL = NS / 16, SLABS = N / NS;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
+    const int H = a.H, G = a.G, P = a.P, PP = P < 32 ? 32 : P;
+    T* Ks = reinterpret_cast<T*>(smem);
+    T* Qs = Ks + L * LDN;
+    T* Hs = Qs + L * LDN;
+    T* Ls = Hs + PP * LDN;
+    float* ecs = reinterpret_cast<float*>(Ls + PP * LDN);
+    float* ews = ecs + L;
+    float* chi = ews + L;
+    float* clo = chi + L;
+    float* bts = clo + L;
+
+    unsigned id = blockIdx.x;
+    const int slab = (int)(id % SLABS);
+    id /= SLABS;
+    const int sub = (int)(id % (unsigned)a.nsub);
+    id /= (unsigned)a.nsub;
+    const int g = (int)(id % (unsigned)G), kk = (int)(id / (unsigned)G);
+    const int row = a.rows.row_of(kk), c = kk - a.rows.kbase(row);
+    const int64_t t0 = a.rows.tok0(row) + (int64_t)c * L;
+    const int n = (int)min((int64_t)L, a.rows.len(row) - (int64_t)c * L);
+    const int Hg = H / G, per = (Hg + a.nsub - 1) / a.nsub;
+    const int hb = g * Hg + sub * per, he = min(g * Hg + Hg, hb + per);
+    const int n0 = slab * NS;
+
+    stage_rows(static_cast<const T*>(a.B) + (t0 * G + g) * N + n0, (int64_t)G * N, Ks, LDN, n, NS, NS, tid, 256);
+    stage_rows(static_cast<const T*>(a.C) + (t0 * G + g) * N + n0, (int64_t)G * N, Qs, LDN, n, NS, NS, tid, 256);
+    f32x4 dq[NTL], dk[NTL];
+#pragma unroll
+    for (int t = 0; t < NTL; ++t) dq[t] = dk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int i = w * 16 + l16;  // this lane's token column
+
+    for (int h = hb; h < he; ++h) {
+        const int64_t e = (int64_t)kk * H + h;
+        __syncthreads();
+        stage_rows(static_cast<const T*>(a.hin) + e * P * N + n0, (int64_t)N, Hs, LDN, P, NS, NS, tid, 256, PP);
+        stage_rows(static_cast<const T*>(a.lin) + e * P * N + n0, (int64_t)N, Ls, LDN, P, NS, NS, tid, 256, PP);
+        if (tid < L) {
+            ecs[tid] = a.vec[e * kVec + tid];
+            ews[tid] = a.vec[e * kVec + L + tid];
+            chi[tid] = a.vec[e * kVec + 2 * L + tid];
+            clo[tid] = a.vec[e * kVec + 3 * L + tid];
+            bts[tid] = tid < n ? to_f(static_cast<const T*>(a.beta)[(t0 + tid) * H + h]) : 0.f;
+        }
+        __syncthreads();
+        const T* Yg = static_cast<const T*>(a.dy) + (t0 * H + h) * P;
+        const T* Rg = static_cast<const T*>(a.r) + (t0 * H + h) * P;
+        const T* Zg = static_cast<const T*>(a.z) + (t0 * H + h) * P;
+        const int64_t rs = (int64_t)H * P;
+        auto rowf = [&](const T* base, int tile, int ks) {  // row fragment, zero past n and P
+            const int t = tile * 16 + l16, col = ks * 32 + 8 * q;
+            const bool in = t < n && col < P;
+            return sel8(in, ld8(base + (t < n ? t : 0) * rs + (col < P ? col : 0)));
+        };
+        // tables: pt = dP_{ij} (rows j), wt = W_{ij} (rows j) for j <= i; pc = dP_{ai},
+        // wc = W_{ai} (rows a) for a >= i
+        f32x4 pt[4], wt[4], pc[4], wc[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) pt[j] = wt[j] = pc[j] = wc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        f32x4 th[NTL], tz[NTL], tl[NTL];  // h^T dY^T, h^T z^T, dh'^T r^T
+#pragma unroll
+        for (int t = 0; t < NTL; ++t) th[t] = tz[t] = tl[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int ks = 0; ks < PP / 32; ++ks) {
+            const auto yi = rowf(Yg, w, ks), ri = rowf(Rg, w, ks), zi = rowf(Zg, w, ks);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j <= w) {
+                    const auto rj = j == w ? ri : rowf(Rg, j, ks);
+                    pt[j] = mma(pt[j], rj, yi);
+                    wt[j] = mma(wt[j], rj, zi);
+                }
+                if (j >= w) {
+                    pc[j] = mma(pc[j], j == w ? yi : rowf(Yg, j, ks), ri);
+                    wc[j] = mma(wc[j], j == w ? zi : rowf(Zg, j, ks), ri);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < NTL; ++t) {
+                const auto hf = frag_rows(Hs, LDN, ks * 32, t * 16, lane);
+                const auto lf = frag_rows(Ls, LDN, ks * 32, t * 16, lane);
+                th[t] = mma(th[t], hf, yi);
+                tz[t] = mma(tz[t], hf, zi);
+                tl[t] = mma(tl[t], lf, ri);
+            }
+        }
+        const float bi = bts[i], ci = chi[i], di = clo[i];
+        if (slab == 0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float zr = 0.f;  // z_i . r_i sits on the diagonal of this wave's own tile
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j == w) zr = wt[j][r];
+                if (4 * q + r == l16 && i < n)
+                    static_cast<T*>(a.dbeta)[(t0 + i) * H + h] = from_f<T>(zr);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int o = j * 16 + 4 * q + r;  // the other token
+                const float bo = bts[o], d = (ci - chi[o]) + (di - clo[o]);
+                const float gl = exp2f_fast(fminf(d, 0.f)), gc = exp2f_fast(fminf(-d, 0.f));
+                pt[j][r] = o <= i ? pt[j][r] * (gl * bo) : 0.f;
+                pc[j][r] = o >= i ? pc[j][r] * (gc * bi) : 0.f;
+                wt[j][r] = (o < i ? -wt[j][r] * (gl * bo * bi) : 0.f) + (o > i ? -wc[j][r] * (gc * bo * bi) : 0.f);
+            }
+        Sp<T> sp[2], sc[2], sw[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            split8(join(pt[2 * t], pt[2 * t + 1]), sp[t]);
+            split8(join(pc[2 * t], pc[2 * t + 1]), sc[t]);
+            split8(join(wt[2 * t], wt[2 * t + 1]), sw[t]);
+        }
+        const float s1 = ecs[i], s2 = ecs[i] * bi, s3 = ews[i] * bi;
+#pragma unroll
+        for (int t = 0; t < NTL; ++t) {
+            dq[t] += th[t] * s1;
+            dk[t] += tl[t] * s3 - tz[t] * s2;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const auto kf = frag_rows_split(Ks, LDN, ks * 32 + 4 * q, ks * 32 + 16 + 4 * q, t * 16, lane);
+                const auto qf = frag_rows_split(Qs, LDN, ks * 32 + 4 * q, ks * 32 + 16 + 4 * q, t * 16, lane);
+                dq[t] = mma_es<2>(dq[t], kf, sp[ks]);
+                dk[t] = mma_es<2>(dk[t], kf, sw[ks]);
+                dk[t] = mma_es<2>(dk[t], qf, sc[ks]);
+            }
+        }
+    }
+    if (i >= n) return;
+    const int64_t o = ((t0 + i) * G + g) * N + n0 + 4 * q;
+    if (a.nsub == 1) {
+#pragma unroll
+        for (int t = 0; t < NTL; ++t) {
+            typename V4<T>::type ok, oq;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                ok[r] = from_f<T>(dk[t][r]);
+                oq[r] = from_f<T>(dq[t][r]);
+            }
+            st4(static_cast<T*>(a.dB) + o + t * 16, ok);
+            st4(static_cast<T*>(a.dC) + o + t * 16, oq);
+        }
+    } else {
+        const int64_t all = (int64_t)a.rows.nrows * a.T * G * N;
+        float* pk = a.part + (int64_t)sub * 2 * all + o;
+#pragma unroll
+        for (int t = 0; t < NTL; ++t) {
+            st4(pk + t * 16, dk[t]);
+            st4(pk + all + t * 16, dq[t]);
+        }
+    }
+}
+
+// dB and dC from the shares' partial sums, in share order
+template <typename T>
+__global__ __launch_bounds__(256) void k_delta_sum(const float* __restrict__ part, T* __restrict__ dB,
+                                                   T* __restrict__ dC, int64_t all, int nsub) {
+    const int64_t v = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (v >= 2 * all) return;
+    f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < nsub; ++k) s += ld4(part + (int64_t)k * 2 * all + v);
+    typename V4<T>::type o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = from_f<T>(s[e]);
+    st4(v < all ? dB + v : dC + (v - all), o);
+}
+
+// k_delta_dt: ddt of one (chunk, head), a reverse running sum over its tokens (one per lane),
+// and the chunk's share of dA, in float64.
+template <int LANES = 64>
+__global__ __launch_bounds__(LANES) void k_delta_dt(Args a) {
+    const int lane = threadIdx.x, H = a.H, BH = a.rows.nrows * H;
+    const int h = (int)(blockIdx.x % (unsigned)H), kk = (int)(blockIdx.x / (unsigned)H);
+    const int64_t row = kk / a.nc;
+    const int64_t t = (int64_t)(kk % a.nc) * L + lane, e = (int64_t)kk * H + h, bh = row * H + h;
+    const bool on = t < a.T;
+    double v = 0.0, tot = 0.0;
+    for (int sl = 0; sl < a.slices; ++sl) {
+        const int64_t o = ((int64_t)sl * BH + bh) * a.T + (on ? t : 0);
+        if (on) v += (double)a.dyy[o] - (double)a.dxx[o];
+        tot += (double)a.tot[(int64_t)sl * a.ntab * H + e];
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const double o = __shfl_down(v, off, 64);
+        if (lane + off < 64) v += o;
+    }
+    v += tot;
+    const int64_t o = (row * a.T + (on ? t : 0)) * H + h;
+    if (on) a.ddt[o] = (float)(v * (double)a.A[h]);
+    double da = on ? v * (double)a.dt[o] : 0.0;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) da += __shfl_xor(da, off, 64);
+    if (lane == 0) a.dAp[e] = (float)da;
+}
+// dA_h over the chunks, in order
+template <int BLOCK = 64>
+__global__ __launch_bounds__(BLOCK) void k_delta_dA(const float* __restrict__ p, float* __restrict__ dA, int ntab,
+                                                    int H) {
+    const int h = blockIdx.x;
+    double s = 0.0;
+    for (int v = threadIdx.x; v < ntab; v += BLOCK) s += (double)p[(int64_t)v * H + h];
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
+    if (threadIdx.x == 0) dA[h] = (float)s;
+}
+
+// ---------------------------------------------------------------------------
+// k_delta_step: the recurrence token by token on a held state, in place, all in float32.
+// One thread owns 8 consecutive elements of a state row p; the N / 8 lanes of a row (one
+// wave) reduce h B and then h C.  The state is read and written once per call: bound by HBM.
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ __launch_bounds__(256) void k_delta_step(const T* __restrict__ x, const float* __restrict__ dt,
+                                                    const float* __restrict__ A, const T* __restrict__ Bm,
+                                                    const T* __restrict__ Cm, const T* __restrict__ beta,
+                                                    float* __restrict__ hst, T* __restrict__ y, int64_t Tn, int H,
+                                                    int P, int N, int G) {
+    constexpr int E = 8;
+    const int64_t bh = blockIdx.x;
+    const int h = (int)(bh % H), g = h / (H / G);
+    const int64_t bi = bh / H;
+    const int e0 = (blockIdx.y * 256 + threadIdx.x) * E;
+    const bool active = e0 < P * N;
+    const int ec = active ? e0 : 0, p = ec / N, n0 = ec % N, R = N / E, lane = threadIdx.x & 63;
+    float* hp = hst + bh * (int64_t)P * N + ec;
+    float hv[E];
+#pragma unroll
+    for (int k = 0; k < E; ++k) hv[k] = 0.f;
+    if (active) {
+        const f32x8 v = ld8(hp);
+#pragma unroll
+        for (int k = 0; k < E; ++k) hv[k] = v[k];
+    }
+    const double Ah = (double)A[h] * 1.4426950408889634;
+    for (int64_t t = 0; t < Tn; ++t) {
+        const int64_t row = bi * Tn + t;
+        const float d = exp2f_fast((float)((double)dt[row * H + h] * Ah));
+        const float xp = to_f(x[(row * H + h) * P + p]), bt = to_f(beta[row * H + h]);
+        float bv[E], cv[E], s = 0.f, o = 0.f;
+        const T* br = Bm + (row * G + g) * N + n0;
+        const T* cr = Cm + (row * G + g) * N + n0;
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            bv[k] = to_f(br[k]);
+            cv[k] = to_f(cr[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            hv[k] *= d;
+            s += hv[k] * bv[k];
+        }
+        for (int off = R >> 1; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
+        const float u = bt * (xp - s);
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            hv[k] += u * bv[k];
+            o += hv[k] * cv[k];
+        }
+        for (int off = R >> 1; off > 0; off >>= 1) o += __shfl_xor(o, off, 64);
+        if (active && (lane & (R - 1)) == 0) y[(row * H + h) * P + p] = from_f<T>(o);
+    }
+    if (active) {
+        f32x8 v;
+#pragma unroll
+        for (int k = 0; k < E; ++k) v[k] = hv[k];
+        st8(hp, v);
+    }
+}
+
+}  // namespace delta
+}  // namespace ssd

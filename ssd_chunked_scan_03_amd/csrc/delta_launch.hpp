@@ -1,0 +1,113 @@
+// delta_launch.hpp -- enqueue the gated delta rule's kernels on a stream.
+#pragma once
+
+#include "delta.hpp"
+
+namespace ssd {
+namespace delta {
+
+// Columns of headdim one work-group of the chunk walks takes: waves of 16 CT columns.  Two
+// column tiles per wave read each table and key fragment once for both (bfloat16, where the
+// state's accumulators leave the registers for it); as many waves as P allows, up to 4.
+struct Slice {
+    int ct, waves;
+    int cols() const { return 16 * ct * waves; }
+};
+inline Slice slice_of(bool bf16_dtype, int64_t bh, int64_t P, int64_t N) {
+    Slice s;
+    s.ct = bf16_dtype && N <= 128 && P >= 32 ? 2 : 1;
+    s.waves = (int)(P / (16 * s.ct));
+    if (s.waves > 4) s.waves = 4;
+    while (s.waves > 1 && bh * (P / s.cols()) < 256) s.waves >>= 1;
+    return s;
+}
+
+// Shares of a group's heads in the gradient kernel: enough work-groups for every CU several
+// times over, each summing as many heads in registers as that leaves.
+inline int grad_shares(int64_t chunks, int64_t H, int64_t G, int64_t N) {
+    const int64_t base = chunks * G * (N > 64 ? N / 64 : 1), hg = H / G;
+    int64_t s = (1024 + base - 1) / (base > 0 ? base : 1);
+    return (int)(s < 1 ? 1 : s > hg ? hg : s);
+}
+
+template <typename K>
+bool lds_limit(K* kernel, size_t bytes) {
+    return bytes <= 64 * 1024 || hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                     (int)bytes) == hipSuccess;
+}
+
+template <typename T, int N, int CT>
+int walk(const Args& a, int waves, int which) {
+    typedef Cfg<T, N> CF;
+    const int sw = 16 * CT * waves;
+    const unsigned grid = (unsigned)((int64_t)a.rows.nrows * a.H * (a.P / sw));
+    if (which == 0) {
+        const size_t lds = CF::walk_bytes(sw, 1, 1);
+        if (!lds_limit(k_delta<T, N, CT, false>, lds)) return 7;
+        k_delta<T, N, CT, false><<<grid, 64 * waves, lds, a.stream>>>(a);
+    } else if (which == 1) {
+        const size_t lds = CF::walk_bytes(sw, CF::NT, 2);
+        if (!lds_limit(k_delta<T, N, CT, true>, lds)) return 7;
+        k_delta<T, N, CT, true><<<grid, 64 * waves, lds, a.stream>>>(a);
+    } else {
+        const size_t lds = CF::walk_bytes(sw, CF::NT, 2);
+        if (!lds_limit(k_delta_rev<T, N, CT>, lds)) return 7;
+        k_delta_rev<T, N, CT><<<grid, 64 * waves, lds, a.stream>>>(a);
+    }
+    return hipGetLastError() == hipSuccess ? 0 : 7;
+}
+
+template <typename T, int N>
+int walk_n(const Args& a, const Slice& s, int which) {
+    if constexpr (std::is_same<T, bf16>::value && N <= 128) {
+        if (s.ct == 2) return walk<T, N, 2>(a, s.waves, which);
+    }
+    return walk<T, N, 1>(a, s.waves, which);
+}
+
+template <typename T, int N>
+int run_fwd(const Args& a) {
+    const Slice s = slice_of(std::is_same<T, bf16>::value, (int64_t)a.rows.nrows * a.H, a.P, N);
+    k_delta_prep<T, N><<<(unsigned)((int64_t)a.ntab * a.H), 256, 0, a.stream>>>(a);
+    return walk_n<T, N>(a, s, 0);
+}
+
+template <typename T, int N>
+int run_bwd(const Args& a) {
+    typedef GradCfg<T, N> GC;
+    const Slice s = slice_of(std::is_same<T, bf16>::value, (int64_t)a.rows.nrows * a.H, a.P, N);
+    k_delta_prep<T, N><<<(unsigned)((int64_t)a.ntab * a.H), 256, 0, a.stream>>>(a);
+    int st = walk_n<T, N>(a, s, 1);
+    if (!st) st = walk_n<T, N>(a, s, 2);
+    if (st) return st;
+    const size_t lds = GC::bytes(a.P);
+    if (!lds_limit(k_delta_grad<T, N>, lds)) return 7;
+    const int64_t wgs = (int64_t)a.ntab * a.G * a.nsub * (N / GC::NS);
+    k_delta_grad<T, N><<<(unsigned)wgs, 256, lds, a.stream>>>(a);
+    if (a.nsub > 1) {
+        const int64_t all = (int64_t)a.rows.nrows * a.T * a.G * N;
+        k_delta_sum<T><<<(unsigned)((2 * all / 4 + 255) / 256), 256, 0, a.stream>>>(
+            a.part, static_cast<T*>(a.dB), static_cast<T*>(a.dC), all, a.nsub);
+    }
+    k_delta_dt<64><<<(unsigned)((int64_t)a.ntab * a.H), 64, 0, a.stream>>>(a);
+    k_delta_dA<64><<<(unsigned)a.H, 64, 0, a.stream>>>(a.dAp, a.dA, a.ntab, a.H);
+    return hipGetLastError() == hipSuccess ? 0 : 7;
+}
+
+template <typename T>
+int run(const Args& a, bool bwd) {
+    switch (a.N) {
+        case 16: return bwd ? run_bwd<T, 16>(a) : run_fwd<T, 16>(a);
+        case 32: return bwd ? run_bwd<T, 32>(a) : run_fwd<T, 32>(a);
+        case 64: return bwd ? run_bwd<T, 64>(a) : run_fwd<T, 64>(a);
+        case 128: return bwd ? run_bwd<T, 128>(a) : run_fwd<T, 128>(a);
+        case 256: return bwd ? run_bwd<T, 256>(a) : run_fwd<T, 256>(a);
+        default: return 3;
+    }
+}
+
+int run_bf16(const Args& a, bool bwd);
+int run_f32(const Args& a, bool bwd);
+
+}  // namespace delta
+}  // namespace ssd

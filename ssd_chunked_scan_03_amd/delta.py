@@ -1,0 +1,310 @@
+"""The gated delta rule on the scan's operands, and the norm of B and C that prepares them.
+
+    y, hT = delta_fwd(x, dt, A, B, C, beta, h0=None)
+    y, hT = delta_fwd_varlen(x, dt, A, B, C, beta, cu_seqlens, h0=None)
+    y = delta_step(x, dt, A, B, C, beta, h)                     # h updated in place
+    grads = delta_bwd(x, dt, A, B, C, beta, dy, h0=None, dhT=None)
+    Bn, Cn = bc_norm(B, C, wB=None, wC=None, mode="rms", inv_freq=None, positions=None)
+    grads = bc_norm_bwd(B, C, dBn, dCn, wB=None, wC=None, ...)
+
+Layouts as for the scan, with beta [b,T,H] (the write strength) in x's dtype:
+r_t = x_t - a_t h_{t-1} B_t, h_t = a_t h_{t-1} + beta_t r_t B_t^T, y_t = h_t C_t,
+a_t = exp(dt_t A_h).  Keys are meant to have about unit length; ``norm`` (a dict of
+:func:`bc_norm`'s keyword arguments) passes B and C through bc_norm first.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import (SSDError, _check_args, _dtype_code, _load, _ptr, Problem, make_problem)
+
+DELTA_CHUNK = 64
+NORM_MODES = {"rms": 0, "l2": 1}
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("bheads", ctypes.c_int64),
+                ("cheads", ctypes.c_int64), ("dstate", ctypes.c_int64), ("pairs", ctypes.c_int64),
+                ("bstride", ctypes.c_int64), ("cstride", ctypes.c_int64), ("eps", ctypes.c_float),
+                ("mode", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+def _bind(lib):
+    """Argument types of this module's entry points."""
+    P, Q = ctypes.POINTER(Problem), ctypes.POINTER(Norm)
+    vp, sz, ci = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+    for name, res, args in (
+            ("ssd_delta_workspace_bytes", sz, [P]), ("ssd_delta_varlen_workspace_bytes", sz, [P]),
+            ("ssd_delta_bwd_workspace_bytes", sz, [P]), ("ssd_bc_norm_bwd_workspace_bytes", sz, [Q]),
+            ("ssd_delta_fwd", ci, [P] + [vp] * 10 + [sz, vp]),
+            ("ssd_delta_fwd_varlen", ci, [P] + [vp] * 11 + [sz, vp]),
+            ("ssd_delta_step", ci, [P] + [vp] * 9),
+            ("ssd_delta_bwd", ci, [P] + [vp] * 17 + [sz, vp]),
+            ("ssd_bc_norm", ci, [Q] + [vp] * 9),
+            ("ssd_bc_norm_bwd", ci, [Q] + [vp] * 13 + [sz, vp])):
+        f = getattr(lib, name)
+        f.restype, f.argtypes = res, args
+
+
+def _call(name, head, tensors, ws=False, stream=None):
+    """Enqueue one entry point on `stream` (default: the current stream of the tensors' device).
+    The first of `tensors` names the device; `ws` is the workspace (False: the entry point
+    takes none)."""
+    import torch
+    dev = next(t for t in tensors if t is not None).device
+    args = [ctypes.byref(head), *map(_ptr, tensors)]
+    if ws is not False:
+        args += [_ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()]
+    if dev.index is not None and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            s = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+            st = getattr(_load(), name)(*args, ctypes.c_void_p(int(s)))
+    else:
+        s = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+        st = getattr(_load(), name)(*args, ctypes.c_void_p(int(s)))
+    if st:
+        raise SSDError(st, name)
+
+
+def delta_workspace_bytes(prob: Problem, varlen: bool = False) -> int:
+    lib = _load()
+    f = lib.ssd_delta_varlen_workspace_bytes if varlen else lib.ssd_delta_workspace_bytes
+    return int(f(ctypes.byref(prob)))
+
+
+def delta_bwd_workspace_bytes(prob: Problem) -> int:
+    return int(_load().ssd_delta_bwd_workspace_bytes(ctypes.byref(prob)))
+
+
+def _workspace(ws, need, device):
+    import torch
+    if ws is not None and ws.device != device:
+        raise ValueError(f"workspace is on {ws.device}, the other tensors on {device}")
+    if ws is None or ws.numel() * ws.element_size() < need:
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    return ws
+
+
+def delta_fwd_into(prob: Problem, x, dt, A, B, C, beta, h0, y, hT, ws, stream=None) -> None:
+    """Enqueue one forward into caller-provided outputs and workspace (no allocation)."""
+    _call("ssd_delta_fwd", prob, (x, dt, A, B, C, beta, h0, y, hT), ws, stream)
+
+
+def delta_fwd_varlen_into(prob: Problem, cu_seqlens, x, dt, A, B, C, beta, h0, y, hT, ws, stream=None) -> None:
+    """Enqueue one packed forward (prob.batch sequences on one axis of prob.seqlen tokens)
+    into caller-provided outputs and workspace (no allocation)."""
+    _call("ssd_delta_fwd_varlen", prob, (cu_seqlens, x, dt, A, B, C, beta, h0, y, hT), ws, stream)
+
+
+def delta_step_into(prob: Problem, x, dt, A, B, C, beta, h, y, stream=None) -> None:
+    """Enqueue the rule over prob.seqlen tokens: h is updated in place, y receives the
+    outputs (no allocation)."""
+    _call("ssd_delta_step", prob, (x, dt, A, B, C, beta, h, y), stream=stream)
+
+
+def delta_bwd_into(prob: Problem, x, dt, A, B, C, beta, h0, dy, dhT, dx, ddt, dA, dB, dC, dbeta, dh0, ws,
+                   stream=None) -> None:
+    """Enqueue one backward pass into caller-provided gradients and workspace (no allocation)."""
+    _call("ssd_delta_bwd", prob, (x, dt, A, B, C, beta, h0, dy, dhT, dx, ddt, dA, dB, dC, dbeta, dh0), ws, stream)
+
+
+def _normed(B, C, norm):
+    return (B, C) if norm is None else bc_norm(B, C, **norm)
+
+
+def _shapes4(x, B):
+    if x.dim() != 4 or B.dim() != 4:
+        raise ValueError("x must be [b, T, H, P] and B [b, T, G, N]")
+    return (*x.shape, B.shape[2], B.shape[3])
+
+
+def delta_fwd(x, dt, A, B, C, beta, h0=None, chunk=DELTA_CHUNK, return_final_state=True, workspace=None, norm=None):
+    """Gated delta rule forward: x [b, T, H, P], dt [b, T, H] f32, A [H] f32, B/C [b, T, G, N],
+    beta [b, T, H] in x's dtype, h0 [b, H, P, N] f32 or None.  Returns (y, hT)."""
+    import torch
+    b, T, H, P, G, N = _shapes4(x, B)
+    B, C = _normed(B, C, norm)
+    _check_args({"x": (x, (b, T, H, P)), "dt": (dt, (b, T, H)), "A": (A, (H,)), "B": (B, (b, T, G, N)),
+                 "C": (C, (b, T, G, N)), "beta": (beta, (b, T, H)), "h0": (h0, (b, H, P, N))},
+                floats=("dt", "A", "h0"), same_dtype=("x", "B", "C", "beta"))
+    prob = make_problem(b, T, H, P, N, G, chunk, _dtype_code(x))
+    y = torch.empty_like(x)
+    hT = torch.empty((b, H, P, N), dtype=torch.float32, device=x.device) if return_final_state else None
+    ws = _workspace(workspace, delta_workspace_bytes(prob), x.device)
+    delta_fwd_into(prob, x, dt, A, B, C, beta, h0, y, hT, ws)
+    return y, hT
+
+
+def delta_fwd_varlen(x, dt, A, B, C, beta, cu_seqlens, h0=None, chunk=DELTA_CHUNK, return_final_state=True,
+                     workspace=None, norm=None):
+    """Gated delta rule forward over packed sequences: x [T, H, P], dt [T, H], B/C [T, G, N],
+    beta [T, H]; sequence s on tokens [cu_seqlens[s], cu_seqlens[s+1]) (int32 GPU tensor);
+    h0 / hT [nseq, H, P, N].  Rows of y outside every sequence are not written.  Returns
+    (y, hT)."""
+    import torch
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise TypeError("cu_seqlens must be a 1-D int32 tensor of nseq + 1 offsets")
+    if x.dim() != 3 or B.dim() != 3:
+        raise ValueError("x must be [T, H, P] and B [T, G, N]")
+    T, H, P = x.shape
+    G, N = B.shape[1], B.shape[2]
+    nseq = cu_seqlens.numel() - 1
+    if norm is not None:
+        if norm.get("inv_freq") is not None and norm.get("positions") is None:
+            raise ValueError("packed sequences need norm's positions: every sequence counts its own")
+        pos = norm.get("positions")
+        Bn, Cn = bc_norm(B[None], C[None], **dict(norm, positions=None if pos is None else pos.reshape(1, -1)))
+        B, C = Bn[0], Cn[0]
+    _check_args({"x": (x, (T, H, P)), "dt": (dt, (T, H)), "A": (A, (H,)), "B": (B, (T, G, N)), "C": (C, (T, G, N)),
+                 "beta": (beta, (T, H)), "h0": (h0, (nseq, H, P, N)), "cu_seqlens": (cu_seqlens, (nseq + 1,))},
+                floats=("dt", "A", "h0"), same_dtype=("x", "B", "C", "beta"))
+    prob = make_problem(nseq, T, H, P, N, G, chunk, _dtype_code(x))
+    y = torch.empty_like(x)
+    hT = torch.empty((nseq, H, P, N), dtype=torch.float32, device=x.device) if return_final_state else None
+    ws = _workspace(workspace, delta_workspace_bytes(prob, True), x.device)
+    delta_fwd_varlen_into(prob, cu_seqlens, x, dt, A, B, C, beta, h0, y, hT, ws)
+    return y, hT
+
+
+def delta_step(x, dt, A, B, C, beta, h, norm=None):
+    """Decode: run the rule over x's tokens on state h [b, H, P, N] f32 (updated in place).
+    x [b, T, H, P], dt [b, T, H] f32, A [H] f32, B/C [b, T, G, N], beta [b, T, H].  Returns y."""
+    import torch
+    b, T, H, P, G, N = _shapes4(x, B)
+    if h is None:
+        raise ValueError("h (the state, updated in place) is required")
+    B, C = _normed(B, C, norm)
+    _check_args({"x": (x, (b, T, H, P)), "dt": (dt, (b, T, H)), "A": (A, (H,)), "B": (B, (b, T, G, N)),
+                 "C": (C, (b, T, G, N)), "beta": (beta, (b, T, H)), "h": (h, (b, H, P, N))},
+                floats=("dt", "A", "h"), same_dtype=("x", "B", "C", "beta"))
+    prob = make_problem(b, T, H, P, N, G, DELTA_CHUNK, _dtype_code(x))
+    y = torch.empty_like(x)
+    delta_step_into(prob, x, dt, A, B, C, beta, h, y)
+    return y
+
+
+def delta_bwd(x, dt, A, B, C, beta, dy, h0=None, dhT=None, chunk=DELTA_CHUNK, workspace=None, norm=None):
+    """Backward pass of delta_fwd: gradients of a loss with respect to every input, given dy
+    (like x) and dhT ([b, H, P, N] float32, None = 0).  Returns a dict with dx, dB, dC, dbeta
+    (their inputs' dtype), ddt, dA and dh0 (float32).  With ``norm``, dB and dC are the
+    gradients of the tensors before bc_norm, and dwB / dwC are added for its weights."""
+    import torch
+    b, T, H, P, G, N = _shapes4(x, B)
+    B0, C0 = B, C
+    B, C = _normed(B, C, norm)
+    _check_args({"x": (x, (b, T, H, P)), "dt": (dt, (b, T, H)), "A": (A, (H,)), "B": (B, (b, T, G, N)),
+                 "C": (C, (b, T, G, N)), "beta": (beta, (b, T, H)), "dy": (dy, (b, T, H, P)),
+                 "h0": (h0, (b, H, P, N)), "dhT": (dhT, (b, H, P, N))},
+                floats=("dt", "A", "h0", "dhT"), same_dtype=("x", "B", "C", "beta", "dy"))
+    prob = make_problem(b, T, H, P, N, G, chunk, _dtype_code(x))
+    out = dict(dx=torch.empty_like(x), ddt=torch.empty_like(dt), dA=torch.empty_like(A), dB=torch.empty_like(B),
+               dC=torch.empty_like(C), dbeta=torch.empty_like(beta),
+               dh0=torch.empty((b, H, P, N), dtype=torch.float32, device=x.device))
+    ws = _workspace(workspace, delta_bwd_workspace_bytes(prob), x.device)
+    delta_bwd_into(prob, x, dt, A, B, C, beta, h0, dy, dhT, out["dx"], out["ddt"], out["dA"], out["dB"], out["dC"],
+                   out["dbeta"], out["dh0"], ws)
+    if norm is not None:
+        out.update(bc_norm_bwd(B0, C0, out["dB"], out["dC"], **norm))
+    return out
+
+
+# ---- the norm of B and C ----
+def _token_stride(name, t):
+    """Elements between tokens of a [b, T, heads, N] tensor whose heads are contiguous; views
+    into a wider projection are accepted as they are."""
+    b, T, heads, N = t.shape
+    if t.numel() == 0:
+        return heads * N
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.stride(3) != 1 or (heads > 1 and t.stride(2) != N):
+        raise ValueError(f"{name}'s heads must be contiguous")
+    if T > 1:
+        step = t.stride(1)
+        if b > 1 and t.stride(0) != T * step:
+            raise ValueError(f"{name}'s tokens must be evenly spaced over the batch")
+    else:
+        step = t.stride(0) if b > 1 else heads * N
+    if step < heads * N:
+        raise ValueError(f"{name}'s tokens must not overlap")
+    return step
+
+
+def _norm_problem(B, C, wB, wC, mode, eps, inv_freq, positions, interleaved):
+    import torch
+    if B.dim() != 4 or C.dim() != 4:
+        raise ValueError("B and C must be [b, T, heads, N]")
+    b, T, GB, N = B.shape
+    GC = C.shape[2]
+    if mode not in NORM_MODES:
+        raise ValueError(f"mode must be one of {sorted(NORM_MODES)}, got {mode!r}")
+    if C.shape != (b, T, GC, N):
+        raise ValueError(f"C must have shape {(b, T, GC, N)}, got {tuple(C.shape)}")
+    F = 0 if inv_freq is None else inv_freq.numel()
+    _dtype_code(B)
+    if C.dtype != B.dtype:
+        raise TypeError("B, C must share one dtype")
+    for name, t, shape, dtype in (("wB", wB, (N,), torch.float32), ("wC", wC, (N,), torch.float32),
+                                  ("inv_freq", inv_freq, (F,), torch.float32),
+                                  ("positions", positions, (b, T), torch.int32)):
+        if t is None:
+            continue
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.device != B.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor on {B.device}")
+    if C.device != B.device or not B.is_cuda:
+        raise ValueError("B and C must be GPU tensors on one device")
+    return Norm(b, T, GB, GC, N, F, _token_stride("B", B), _token_stride("C", C), float(eps), NORM_MODES[mode],
+                int(bool(interleaved)), _dtype_code(B))
+
+
+def bc_norm_into(prob: Norm, B, C, wB, wC, inv_freq, positions, Bn, Cn, stream=None) -> None:
+    """Enqueue one norm into caller-provided outputs (no allocation)."""
+    _call("ssd_bc_norm", prob, (B, C, wB, wC, inv_freq, positions, Bn, Cn), stream=stream)
+
+
+def bc_norm(B, C, wB=None, wC=None, mode="rms", eps=1e-6, inv_freq=None, positions=None, interleaved=False):
+    """Normalise every head's row of B [b, T, GB, N] and C [b, T, GC, N] (rms or l2), scale by
+    the weights wB / wC ([N] f32) and turn it by its position: pairs (i, i + F), or
+    (2i, 2i + 1) where interleaved, by positions [b, T] (int32; default: the token's index)
+    times inv_freq [F] (f32, F a multiple of 4, 2F <= N; None: no rotation).  B and C may be
+    views into a wider projection.  Returns (Bn, Cn), contiguous."""
+    import torch
+    prob = _norm_problem(B, C, wB, wC, mode, eps, inv_freq, positions, interleaved)
+    Bn, Cn = torch.empty(B.shape, dtype=B.dtype, device=B.device), torch.empty(C.shape, dtype=C.dtype, device=C.device)
+    bc_norm_into(prob, B, C, wB, wC, inv_freq, positions, Bn, Cn)
+    return Bn, Cn
+
+
+def bc_norm_bwd_workspace_bytes(prob: Norm) -> int:
+    return int(_load().ssd_bc_norm_bwd_workspace_bytes(ctypes.byref(prob)))
+
+
+def bc_norm_bwd_into(prob: Norm, B, C, wB, wC, inv_freq, positions, dBn, dCn, dB, dC, dwB, dwC, ws,
+                     stream=None) -> None:
+    """Enqueue one backward into caller-provided gradients and workspace (no allocation)."""
+    _call("ssd_bc_norm_bwd", prob, (B, C, wB, wC, inv_freq, positions, dBn, dCn, dB, dC, dwB, dwC), ws, stream)
+
+
+def bc_norm_bwd(B, C, dBn, dCn, wB=None, wC=None, mode="rms", eps=1e-6, inv_freq=None, positions=None,
+                interleaved=False, workspace=None):
+    """Backward of bc_norm, given dBn and dCn (contiguous, like Bn and Cn).  Returns a dict with
+    dB and dC (contiguous) and, for the weights that were given, dwB and dwC (float32 [N])."""
+    import torch
+    prob = _norm_problem(B, C, wB, wC, mode, eps, inv_freq, positions, interleaved)
+    for name, t, like in (("dBn", dBn, B), ("dCn", dCn, C)):
+        if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {like.dtype} tensor of shape {tuple(like.shape)} on {like.device}")
+    out = dict(dB=torch.empty_like(dBn), dC=torch.empty_like(dCn))
+    for name, w in (("dwB", wB), ("dwC", wC)):
+        if w is not None:
+            out[name] = torch.empty_like(w)
+    ws = None
+    if wB is not None or wC is not None:
+        ws = _workspace(workspace, bc_norm_bwd_workspace_bytes(prob), B.device)
+    bc_norm_bwd_into(prob, B, C, wB, wC, inv_freq, positions, dBn, dCn, out["dB"], out["dC"], out.get("dwB"),
+                     out.get("dwC"), ws)
+    return out
