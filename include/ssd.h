@@ -343,8 +343,9 @@ int ssd_diag_scan_bwd(const ssd_problem* p, const void* x, const float* dt, cons
  *   beta                        [batch, seqlen, nheads], problem dtype (aligned to one element)
  *
  * Evaluated in chunks of 64 tokens: `chunk` must be 64 and `flags` 0.  headdim, dstate, dtype,
- * ngroups and grid limits as for ssd_scan_fwd; also under 2^24 (chunk, head) pairs and
- * (batch, head, 16 headdim columns) under 2^26, else SSD_ERR_UNSUPPORTED.
+ * ngroups and grid limits as for ssd_scan_fwd; also under 2^24 (chunk, head) pairs,
+ * (batch, head, 16 headdim columns) under 2^26 and 64 tokens' x under 2 GiB, else
+ * SSD_ERR_UNSUPPORTED.
  * Precision: decay sums are float64; the state, residuals and all accumulation float32, and
  * where they enter the bfloat16 matrix cores they do so as a sum of bfloat16 terms that
  * keeps the float32 mantissa, so the float32 outputs (hT, and ddt, dA, dh0 of the

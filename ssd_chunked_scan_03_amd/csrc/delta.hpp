@@ -47,7 +47,10 @@ namespace delta {
 constexpr int L = 64;                 // tokens per chunk
 constexpr int kTri = 10;              // 16 x 16 blocks on and below the diagonal of a 64 x 64 table
 constexpr int kTab = 2 * kTri * 256;  // floats of one (chunk, head)'s S and M tables
-constexpr int kVec = 4 * L;           // floats of its e^c, e^{c_L - c} and c (log2 units, two parts)
+constexpr int kVec = 5 * L;           // floats of its e^c, e^{c_L - c}, beta and c (log2 units, two parts)
+// Forward tables of one (chunk, head) as operand fragments (bfloat16, dstate 64 and up): S in
+// three terms, then M, [term][fragment][lane][8].
+constexpr int kFragTab = (3 + 1) * 6 * 512;  // bfloat16 elements
 constexpr int kFrag = 6;              // 16 x 32 operand fragments covering a triangular 64 x 64 table
 
 struct Args {
@@ -238,18 +241,19 @@ __device__ __forceinline__ void store_rows(T* __restrict__ dst, int64_t ds, cons
 // ---------------------------------------------------------------------------
 // k_delta_prep: S and M of one (chunk, head), and the chunk's decay factors.  One work-group of
 // 4 waves; K K^T and Q K^T on the matrix cores straight from global rows, S by blocked
-// forward substitution in float32 (S_ii in registers, one lane per column; below the
-// diagonal S_ij = Z - S_ii (beta Z), Z = KK_ij - sum_k KK_ik (beta S_kj), wave j taking
-// block column j).  Decay sums and their differences are float64, so a strongly decayed
-// chunk keeps the exact ratio of neighbouring tokens.
+// forward substitution in float32: the four S_ii side by side in one wave (a lane per
+// column), then S_ij = Z - S_ii (beta Z), Z = KK_ij - sum_k KK_ik (beta S_kj), wave j taking
+// block column j.  (The product form (I - X)(I + X^2)(I + X^4)... of the inverse needs no
+// substitution but loses four digits where keys repeat.)  Decay sums are float64 and leave
+// in two float32 parts, so a strongly decayed chunk keeps the exact ratio of neighbouring
+// tokens.  FRAG: the tables leave as the operand fragments that k_delta_dma reads.
 // ---------------------------------------------------------------------------
-template <typename T, int N>
+template <typename T, int N, bool FRAG>
 __global__ __launch_bounds__(256) void k_delta_prep(Args a) {
     constexpr int LD = L + 4;
     constexpr double LOG2E = 1.4426950408889634;
-    __shared__ double cs[L];
-    __shared__ float bet[L];
-    __shared__ __attribute__((aligned(16))) float Km[L * LD];  // KK, zeros on and above the diagonal
+    __shared__ float bet[L], chi[L], clo[L];
+    __shared__ __attribute__((aligned(16))) float Km[L * LD];  // KK, zeros on and above the diagonal; then S
     __shared__ __attribute__((aligned(16))) float Sd[4 * 256];  // S_ii
     const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
     const int H = a.H, G = a.G;
@@ -269,16 +273,20 @@ __global__ __launch_bounds__(256) void k_delta_prep(Args a) {
             const double o = __shfl_up(v, off, 64);
             if (lane >= off) v += o;
         }
-        cs[lane] = v;
-        bet[lane] = on ? to_f(static_cast<const T*>(a.beta)[t * H + h]) : 0.f;
+        const float hi = (float)v, lo = (float)(v - (double)hi);
+        const float b = on ? to_f(static_cast<const T*>(a.beta)[t * H + h]) : 0.f;
         const double last = __shfl(v, 63, 64);
         float* vec = a.vec + ((int64_t)kk * H + h) * kVec;
-        vec[lane] = exp2f_fast((float)v);
+        vec[lane] = exp2f_fast(hi);
         vec[L + lane] = exp2f_fast((float)(last - v));
-        vec[2 * L + lane] = (float)v;
-        vec[3 * L + lane] = (float)(v - (double)(float)v);
+        vec[2 * L + lane] = b;
+        vec[3 * L + lane] = hi;
+        vec[4 * L + lane] = lo;
+        bet[lane] = b;
+        chi[lane] = hi;
+        clo[lane] = lo;
     }
-    // K K^T and Q K^T: wave w takes row tile w against column tiles 0 .. w
+    // K K^T (rows i) and K Q^T or Q K^T: wave w takes row tile w against column tiles 0 .. w
     const T* Kg = static_cast<const T*>(a.B) + (t0 * G + g) * N;
     const T* Qg = static_cast<const T*>(a.C) + (t0 * G + g) * N;
     const int64_t rs = (int64_t)G * N;
@@ -300,68 +308,116 @@ __global__ __launch_bounds__(256) void k_delta_prep(Args a) {
             const int rj = j * 16 + l16;
             const auto kb = sel8(in && rj < n, ld8(Kg + (rj < n ? rj : n - 1) * rs + cc));
             kt[j] = mma(kt[j], ka, kb);
-            qt[j] = mma(qt[j], qa, kb);
+            qt[j] = FRAG ? mma(qt[j], kb, qa) : mma(qt[j], qa, kb);
         }
     }
     __syncthreads();
-    float* St = a.tab + ((int64_t)kk * H + h) * kTab;
-    float* Mt = St + kTri * 256;
+    const int64_t e0 = (int64_t)kk * H + h;
+    float* St = a.tab + e0 * kTab;
+    T* Sg = reinterpret_cast<T*>(a.tab) + e0 * kFragTab;
+    T* Mg = Sg + 3 * kFrag * 512;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (j > w) break;
+        typename V4<T>::type mo;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int i16 = 4 * q + r, i = w * 16 + i16, jj = j * 16 + l16;
-            const float gam = i >= jj ? exp2f_fast((float)(cs[i] - cs[jj])) : 0.f;
-            Mt[tri(w, j) * 256 + i16 * 16 + l16] = qt[j][r] * gam;
+            const float gam = i >= jj ? exp2f_fast((chi[i] - chi[jj]) + (clo[i] - clo[jj])) : 0.f;
             Km[i * LD + jj] = i > jj ? kt[j][r] * gam : 0.f;
+            if (FRAG) {  // this lane: row i2, column j2
+                const int i2 = w * 16 + l16, j2 = j * 16 + i16;
+                const float g2 = i2 >= j2 ? exp2f_fast((chi[i2] - chi[j2]) + (clo[i2] - clo[j2])) : 0.f;
+                mo[r] = from_f<T>(qt[j][r] * g2);
+            } else {
+                St[(kTri + tri(w, j)) * 256 + i16 * 16 + l16] = qt[j][r] * gam;
+            }
         }
+        if (FRAG) st4(Mg + frag_lo(w, j >> 1) * 512 + lane * 8 + 4 * (j & 1), mo);
+    }
+    if (FRAG && (w == 0 || w == 2)) {  // the fragments' halves above the diagonal
+        typename V4<T>::type z;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] = from_f<T>(0.f);
+        const int o = frag_lo(w, w >> 1) * 512 + lane * 8 + 4;
+        st4(Mg + o, z);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) st4(Sg + k * kFrag * 512 + o, z);
     }
     __syncthreads();
-    {  // S_ww: column l16, rows in order
-        float s[16];
+    if (w == 0) {  // S_qq: lane group q, column l16, rows in order
+        float s[16], bs[16];
+        const float* kd = Km + q * 16 * LD + q * 16;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float* kr = Km + (w * 16 + i) * LD + w * 16;
-            float v = kr[l16];
+            float v = kd[i * LD + l16];
 #pragma unroll
-            for (int k = 0; k < i; ++k) v -= kr[k] * (bet[w * 16 + k] * s[k]);
-            s[i] = v;
-        }
+            for (int k4 = 0; k4 < i; k4 += 4) {
+                const f32x4 kr = ld4(kd + i * LD + k4);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if ((i >> 2) == q) {
-                Sd[w * 256 + i * 16 + l16] = s[i];
-                St[tri(w, w) * 256 + i * 16 + l16] = s[i];
+                for (int k = k4; k < k4 + 4 && k < i; ++k) v -= kr[k - k4] * bs[k];
             }
+            s[i] = v;
+            bs[i] = bet[q * 16 + i] * v;
+            Sd[q * 256 + i * 16 + l16] = v;
+        }
     }
     __syncthreads();
-    {  // block column w
-        f32x4 col[4];  // S_kw, lane: rows 4q + e, column l16
+    f32x4 col[4];  // S_kw of block column w, lane: rows 4q + e, column l16
 #pragma unroll
-        for (int e = 0; e < 4; ++e) col[0][e] = Sd[w * 256 + (4 * q + e) * 16 + l16];
+    for (int e = 0; e < 4; ++e) col[0][e] = Sd[w * 256 + (4 * q + e) * 16 + l16];
 #pragma unroll
-        for (int m = 1; m < 4; ++m) {  // block row w + m
-            const int i = w + m;
-            if (i > 3) break;
-            f32x4 zv = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int m = 1; m < 4; ++m) {  // block row w + m
+        const int i = w + m;
+        if (i > 3) break;
+        f32x4 zv = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < m; ++k) {
-                f32x4 bs;
+        for (int k = 0; k < m; ++k) {
+            f32x4 bs;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) bs[e] = bet[(w + k) * 16 + 4 * q + e] * col[k][e];
-                zv = mma16(zv, ld4(Km + (i * 16 + l16) * LD + (w + k) * 16 + 4 * q), bs);
+            for (int e = 0; e < 4; ++e) bs[e] = bet[(w + k) * 16 + 4 * q + e] * col[k][e];
+            zv = mma16(zv, ld4(Km + (i * 16 + l16) * LD + (w + k) * 16 + 4 * q), bs);
+        }
+        f32x4 bz;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            zv[e] = Km[(i * 16 + 4 * q + e) * LD + w * 16 + l16] - zv[e];
+            bz[e] = bet[i * 16 + 4 * q + e] * zv[e];
+        }
+        const f32x4 d = mma16(f32x4{0.f, 0.f, 0.f, 0.f}, ld4(Sd + i * 256 + l16 * 16 + 4 * q), bz);
+        col[m] = zv - d;
+    }
+    if (!FRAG) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            if (w + m > 3) break;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) St[tri(w + m, w) * 256 + (4 * q + e) * 16 + l16] = col[m][e];
+        }
+        return;
+    }
+    __syncthreads();  // KK is no longer read
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        if (w + m > 3) break;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) Km[((w + m) * 16 + 4 * q + e) * LD + w * 16 + l16] = col[m][e];
+    }
+    __syncthreads();
+    for (int p = tid; p < kTri * 64; p += 256) {
+        const int blk = p >> 6;
+        const int i = blk < 1 ? 0 : blk < 3 ? 1 : blk < 6 ? 2 : 3, j = blk - tri(i, 0);
+        f32x4 v = ld4(Km + (i * 16 + l16) * LD + j * 16 + 4 * q);
+        T* d = Sg + frag_lo(i, j >> 1) * 512 + lane * 8 + 4 * (j & 1);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            typename V4<T>::type o;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                o[x] = from_f<T>(v[x]);
+                v[x] -= to_f(o[x]);
             }
-            f32x4 bz;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                zv[e] = Km[(i * 16 + 4 * q + e) * LD + w * 16 + l16] - zv[e];
-                bz[e] = bet[i * 16 + 4 * q + e] * zv[e];
-            }
-            const f32x4 d = mma16(f32x4{0.f, 0.f, 0.f, 0.f}, ld4(Sd + i * 256 + l16 * 16 + 4 * q), bz);
-            col[m] = zv - d;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) St[tri(i, w) * 256 + (4 * q + e) * 16 + l16] = col[m][e];
+            st4(d + k * kFrag * 512, o);
         }
     }
 }
@@ -618,6 +674,266 @@ __global__ __launch_bounds__(256) void k_delta(Args a) {
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
                 st4(hT + (bh * P + p0 + pw + ct * 16 + l16) * N + t * 16 + 4 * q, acc[t][ct]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// k_delta_dma: the forward walk for bfloat16 at dstate 64 and up, every tile fetched straight into
+// LDS while the chunk before computes.  K has two buffers (it is read first and last in a
+// chunk); Q is refilled once Q h^T is done, the tables once M u is done; x goes to registers
+// a chunk ahead, and y leaves from them.  LDS tiles are unpadded (the transfer writes 16
+// bytes per lane in order); a row's 16-byte pieces are exchanged by the row's low bits, so
+// that the 16 rows of a fragment lie in different banks.  Every buffer is an array of its own
+// and the two K buffers are named at compile time (chunks in pairs), so the compiler knows
+// which reads a transfer in flight does not concern and does not wait for it there.
+// ---------------------------------------------------------------------------
+template <int N>
+struct Dma {
+    static constexpr int PIECES = N / 8;                              // 16-byte pieces of a row
+    static constexpr int SWZ = PIECES < 16 ? PIECES - 1 : 15;
+    static constexpr int TILE = L * N;                                // elements
+};
+typedef __attribute__((address_space(3))) void lds_void;
+
+// Every wave's LDS reads are done, or (LOADS) its transfers have landed; transfers that no
+// wave reads yet stay in flight (a __syncthreads would wait for them all).
+__device__ __forceinline__ void wave_meet(bool loads) {
+    if (loads) __builtin_amdgcn_s_waitcnt(0xF70);  // vmcnt(0)
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// one wave's share of a 64 x N tile (row stride rs bytes, rows past the resource zero)
+template <int N>
+__device__ __forceinline__ void dma_tile(brsrc r, bf16* dst, int rs, int w, int nw, int lane) {
+    constexpr int RPI = 512 / N, PC = Dma<N>::PIECES;
+    for (int m = w; m < L / RPI; m += nw) {
+        const int row = m * RPI + lane / PC, j = (lane % PC) ^ (row & Dma<N>::SWZ);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + m * 512), 16, row * rs + j * 16, 0, 0, 0);
+    }
+}
+// `n16` KiB-sized runs of contiguous bytes
+__device__ __forceinline__ void dma_run(brsrc r, char* dst, int runs, int w, int nw, int lane) {
+    for (int m = w; m < runs; m += nw)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + m * 1024), 16, m * 1024 + lane * 16, 0, 0, 0);
+}
+
+template <int N, int CT>
+__global__ __launch_bounds__(256, 2) void k_delta_dma(Args a) {
+    constexpr int NTL = N / 16, KS = N / 32, TILE = Dma<N>::TILE, SWZ = Dma<N>::SWZ;
+    __shared__ __attribute__((aligned(16))) bf16 K0[TILE];
+    __shared__ __attribute__((aligned(16))) bf16 K1[TILE];
+    __shared__ __attribute__((aligned(16))) bf16 Qs[TILE];
+    __shared__ __attribute__((aligned(16))) bf16 Sf[kFragTab];  // S in three terms, then M
+    __shared__ __attribute__((aligned(16))) float V0[4 * L];
+    __shared__ __attribute__((aligned(16))) float V1[4 * L];
+    const bf16* Mf = Sf + 3 * kFrag * 512;
+    const int tid = threadIdx.x, nw = blockDim.x >> 6, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
+    const int H = a.H, G = a.G, P = a.P;
+    const int SW = 16 * CT * nw;
+    const int nsl = P / SW, BH = a.rows.nrows * H;
+    const int sl = (int)(blockIdx.x % (unsigned)nsl);
+    int bh = (int)(blockIdx.x / (unsigned)nsl);
+    const int h = bh % H, row = bh / H, g = h / (H / G);
+    const int64_t Tn = a.rows.len(row), tok0 = a.rows.tok0(row);
+    const int nc = a.rows.nchunks(row), kb0 = a.rows.kbase(row);
+    const int p0 = sl * SW + w * 16 * CT;  // this wave's first column
+
+    f32x4 acc[NTL][CT];
+#pragma unroll
+    for (int t = 0; t < NTL; ++t)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+            acc[t][ct] = a.h0 ? ld4(a.h0 + ((int64_t)bh * P + p0 + ct * 16 + l16) * N + t * 16 + 4 * q)
+                              : f32x4{0.f, 0.f, 0.f, 0.f};
+
+    const int rsk = G * N * 2, rsx = H * P * 2;
+    auto rows_left = [&](int c) { return (int)min((int64_t)L, Tn - (int64_t)c * L); };
+    auto key_rsrc = [&](const void* base, int c) {
+        return make_rsrc(static_cast<const bf16*>(base) + ((tok0 + (int64_t)c * L) * G + g) * N,
+                         (uint32_t)((rows_left(c) - 1) * rsk + N * 2));
+    };
+    auto x_rsrc = [&](const void* base, int c) {
+        return make_rsrc(static_cast<const bf16*>(base) + ((tok0 + (int64_t)c * L) * H + h) * P,
+                         (uint32_t)((rows_left(c) - 1) * rsx + P * 2));
+    };
+    auto item = [&](int c) { return (int64_t)(kb0 + c) * H + h; };
+    auto fetch_k = [&](int c, bf16* kd, float* vd) {
+        dma_tile<N>(key_rsrc(a.B, c), kd, rsk, w, nw, lane);
+        if (w == 0 && lane < 48) dma_run(make_rsrc(a.vec + item(c) * kVec, 3 * L * 4), (char*)vd, 1, 0, 1, lane);
+    };
+    auto fetch_q = [&](int c) { dma_tile<N>(key_rsrc(a.C, c), Qs, rsk, w, nw, lane); };
+    auto fetch_tab = [&](int c) {
+        dma_run(make_rsrc(reinterpret_cast<const bf16*>(a.tab) + item(c) * kFragTab, kFragTab * 2),
+                reinterpret_cast<char*>(Sf), kFragTab / 512, w, nw, lane);
+    };
+    const int xo = 4 * q * rsx + (p0 + l16) * 2;  // bytes of (token 4q, column l16)
+    unsigned short xr[4][CT][4];
+    auto fetch_x = [&](int c) {
+        const brsrc r = x_rsrc(a.x, c);
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    xr[it][ct][i] = __builtin_amdgcn_raw_buffer_load_b16(r, xo + ct * 32, (it * 16 + i) * rsx, 0);
+    };
+
+    // lane offsets (elements) of the fragment reads; further fragments differ by an exchange of
+    // piece bits and by whole row tiles
+    const int ka = l16 * N + (((q >> 1) ^ (l16 & SWZ)) << 3) + 4 * (q & 1);
+    const int tr = 4 * q + (l16 >> 2);
+    const int kt = tr * N + ((((l16 & 3) >> 1) ^ (tr & SWZ)) << 3) + 4 * (l16 & 1);
+
+    if (nc > 0) {
+        fetch_k(0, K0, V0);
+        fetch_q(0);
+        fetch_tab(0);
+        fetch_x(0);
+    }
+    auto chunk = [&](int c, const bf16* Ks, const float* ecs, bf16* Kn, float* Vn) {
+        wave_meet(true);  // the chunk's tiles have landed
+        const bool more = c + 1 < nc;
+        if (more) fetch_k(c + 1, Kn, Vn);
+        const float* ews = ecs + L;
+        const float* bts = ews + L;
+
+        // K h^T in three terms, Q h^T in two (enough for a bfloat16 y)
+        f32x4 v[4][CT], yq[4][CT];
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) v[it][ct] = yq[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            Sp<bf16> hs[CT];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) split8(join(acc[2 * ks][ct], acc[2 * ks + 1][ct]), hs[ct]);
+            bf16x8 kf[4], qf[4];
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const int o1 = (ka ^ (ks << 5)) + it * 16 * N, o2 = (ka ^ ((ks << 5) | 16)) + it * 16 * N;
+                kf[it] = join(ld4(Ks + o1), ld4(Ks + o2));
+                qf[it] = join(ld4(Qs + o1), ld4(Qs + o2));
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (int it = 0; it < 4; ++it)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+                        v[it][ct] = mma(v[it][ct], kf[it], hs[ct].t[k]);
+                        if (k < 2) yq[it][ct] = mma(yq[it][ct], qf[it], hs[ct].t[k]);
+                    }
+        }
+        wave_meet(false);  // every wave is done with Q
+        if (more) fetch_q(c + 1);
+
+        // R, then r = R - S (beta R)
+        Sp<bf16> b2[2][CT];
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float ec = ecs[it * 16 + 4 * q + i];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    v[it][ct][i] = to_f(__builtin_bit_cast(bf16, xr[it][ct][i])) - ec * v[it][ct][i];
+                    yq[it][ct][i] *= ec;
+                }
+            }
+        if (more) fetch_x(c + 1);
+        auto scaled = [&](const float* s1, const float* s2) {  // s1_t s2_t v_t as operands
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                f32x4 sa = ld4(s1 + 32 * t + 4 * q), sb = ld4(s1 + 32 * t + 16 + 4 * q);
+                if (s2) {
+                    sa *= ld4(s2 + 32 * t + 4 * q);
+                    sb *= ld4(s2 + 32 * t + 16 + 4 * q);
+                }
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) split8(join(v[2 * t][ct] * sa, v[2 * t + 1][ct] * sb), b2[t][ct]);
+            }
+        };
+        scaled(bts, nullptr);
+        f32x4 d[4][CT];
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) d[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int k = 0; k < 3; ++k)  // term of S
+#pragma unroll
+                for (int it = 2 * t; it < 4; ++it) {
+                    const bf16x8 sf = ld8(Sf + (k * kFrag + frag_lo(it, t)) * 512 + lane * 8);
+#pragma unroll
+                    for (int m = 0; m < 3 - k; ++m)
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) d[it][ct] = mma(d[it][ct], sf, b2[t][ct].t[m]);
+                }
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) v[it][ct] -= d[it][ct];
+        // Y = e^c Q h^T + M u
+        scaled(bts, nullptr);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int it = 2 * t; it < 4; ++it) {
+                const bf16x8 mf = ld8(Mf + frag_lo(it, t) * 512 + lane * 8);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) yq[it][ct] = mma(yq[it][ct], mf, b2[t][ct].t[k]);
+            }
+        wave_meet(false);  // every wave is done with the tables
+        if (more) fetch_tab(c + 1);
+        {
+            const brsrc ry = x_rsrc(a.y, c);
+#pragma unroll
+            for (int it = 0; it < 4; ++it)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+                        __builtin_amdgcn_raw_buffer_store_b16(
+                            __builtin_bit_cast(unsigned short, (bf16)yq[it][ct][i]), ry, xo + ct * 32,
+                            (it * 16 + i) * rsx, 0);
+        }
+        // h' = e^{c_L} h + K^T (e^{c_L - c} u)
+        scaled(ews, bts);
+        const float el = ecs[L - 1];
+#pragma unroll
+        for (int t = 0; t < NTL; ++t) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) acc[t][ct] *= el;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const bf16* kp = Ks + (kt ^ (t << 4)) + ks * 32 * N;
+                const bf16x8 kf = __builtin_bit_cast(
+                    bf16x8, __builtin_shufflevector(ds_tr16(kp), ds_tr16(kp + 16 * N), 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) acc[t][ct] = mma(acc[t][ct], kf, b2[ks][ct].t[k]);
+            }
+        }
+    };
+    for (int c = 0; c < nc; c += 2) {
+        chunk(c, K0, V0, K1, V1);
+        if (c + 1 < nc) chunk(c + 1, K1, V1, K0, V0);
+    }
+    if (a.hT) {
+#pragma unroll
+        for (int t = 0; t < NTL; ++t)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+                st4(a.hT + ((int64_t)bh * P + p0 + ct * 16 + l16) * N + t * 16 + 4 * q, acc[t][ct]);
     }
 }
 
@@ -944,8 +1260,8 @@ __global__ __launch_bounds__(256) void k_delta_grad(Args a) {
         if (tid < L) {
             ecs[tid] = a.vec[e * kVec + tid];
             ews[tid] = a.vec[e * kVec + L + tid];
-            chi[tid] = a.vec[e * kVec + 2 * L + tid];
-            clo[tid] = a.vec[e * kVec + 3 * L + tid];
+            chi[tid] = a.vec[e * kVec + 3 * L + tid];
+            clo[tid] = a.vec[e * kVec + 4 * L + tid];
             bts[tid] = tid < n ? to_f(static_cast<const T*>(a.beta)[(t0 + tid) * H + h]) : 0.f;
         }
         __syncthreads();

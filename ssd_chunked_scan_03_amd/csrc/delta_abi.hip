@@ -26,6 +26,8 @@ int check_delta(const ssd_problem* p, bool packed) {
     const int64_t tabs = packed ? nc + b : b * nc;
     // one work-group per (chunk, head), and per (row, head, 16 columns)
     if (!grid_ok(tabs * H, 256) || !grid_ok(b * H * (p->headdim / 16), 64)) return SSD_ERR_UNSUPPORTED;
+    // a chunk's rows lie within 2 GiB
+    if (H * p->headdim * (int64_t)esize(p->dtype) * p->chunk > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;
     if (packed && T > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;  // int32 offsets
     return SSD_OK;
 }
@@ -50,7 +52,8 @@ Layout layout_of(const ssd_problem* p, bool packed, bool bwd) {
         at = off;
         off += align_up(bytes);
     };
-    take(o.tab, (size_t)(o.ntab * H) * kTab * 4);
+    const size_t frag = ssd::delta::dma_walk(p->dtype == SSD_BF16, N) && !bwd ? ssd::delta::kFragTab * 2 : 0;
+    take(o.tab, (size_t)(o.ntab * H) * (frag ? frag : kTab * 4));
     take(o.vec, (size_t)(o.ntab * H) * kVec * 4);
     if (packed) {
         take(o.ts, (size_t)(b + 1) * 4);

@@ -65,18 +65,37 @@ int walk_n(const Args& a, const Slice& s, int which) {
     return walk<T, N, 1>(a, s.waves, which);
 }
 
+// Whether the forward runs k_delta_dma (tables as fragments).
+inline bool dma_walk(bool bf16_dtype, int64_t N) { return bf16_dtype && N >= 64; }
+
+template <int N, int CT>
+int walk_dma(const Args& a, int waves) {
+    const unsigned grid = (unsigned)((int64_t)a.rows.nrows * a.H * (a.P / (16 * CT * waves)));
+    k_delta_dma<N, CT><<<grid, 64 * waves, 0, a.stream>>>(a);
+    return hipGetLastError() == hipSuccess ? 0 : 7;
+}
+
 template <typename T, int N>
 int run_fwd(const Args& a) {
-    const Slice s = slice_of(std::is_same<T, bf16>::value, (int64_t)a.rows.nrows * a.H, a.P, N);
-    k_delta_prep<T, N><<<(unsigned)((int64_t)a.ntab * a.H), 256, 0, a.stream>>>(a);
-    return walk_n<T, N>(a, s, 0);
+    const unsigned tabs = (unsigned)((int64_t)a.ntab * a.H);
+    if constexpr (std::is_same<T, bf16>::value && N >= 64) {
+        k_delta_prep<T, N, true><<<tabs, 256, 0, a.stream>>>(a);
+        if constexpr (N <= 128) {
+            if (a.P == 128) return walk_dma<N, 2>(a, 4);
+        }
+        return walk_dma<N, 1>(a, a.P >= 64 ? 4 : a.P / 16);
+    } else {
+        const Slice s = slice_of(std::is_same<T, bf16>::value, (int64_t)a.rows.nrows * a.H, a.P, N);
+        k_delta_prep<T, N, false><<<tabs, 256, 0, a.stream>>>(a);
+        return walk_n<T, N>(a, s, 0);
+    }
 }
 
 template <typename T, int N>
 int run_bwd(const Args& a) {
     typedef GradCfg<T, N> GC;
     const Slice s = slice_of(std::is_same<T, bf16>::value, (int64_t)a.rows.nrows * a.H, a.P, N);
-    k_delta_prep<T, N><<<(unsigned)((int64_t)a.ntab * a.H), 256, 0, a.stream>>>(a);
+    k_delta_prep<T, N, false><<<(unsigned)((int64_t)a.ntab * a.H), 256, 0, a.stream>>>(a);
     int st = walk_n<T, N>(a, s, 1);
     if (!st) st = walk_n<T, N>(a, s, 2);
     if (st) return st;
