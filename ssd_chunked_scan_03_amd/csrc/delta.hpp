@@ -48,9 +48,11 @@ constexpr int L = 64;                 // tokens per chunk
 constexpr int kTri = 10;              // 16 x 16 blocks on and below the diagonal of a 64 x 64 table
 constexpr int kTab = 2 * kTri * 256;  // floats of one (chunk, head)'s S and M tables
 constexpr int kVec = 5 * L;           // floats of its e^c, e^{c_L - c}, beta and c (log2 units, two parts)
-// Forward tables of one (chunk, head) as operand fragments (bfloat16, dstate 64 and up): S in
-// three terms, then M, [term][fragment][lane][8].
-constexpr int kFragTab = (3 + 1) * 6 * 512;  // bfloat16 elements
+// Forward tables of one (chunk, head) as operand fragments (bfloat16, dstate 64 and up): -S
+// diag(beta) in three terms, then M diag(beta), [term][fragment][lane][8]; the 10 blocks on and
+// below the diagonal fill 5 fragments (frag_at), and beta is folded into their columns and
+// into the e^{c_L - c} of vec, so that the walk never reads it.
+constexpr int kFragTab = (3 + 1) * 5 * 512;  // bfloat16 elements
 constexpr int kFrag = 6;              // 16 x 32 operand fragments covering a triangular 64 x 64 table
 
 struct Args {
@@ -95,22 +97,36 @@ struct Args {
 };
 
 // ---------------------------------------------------------------------------
-// float32 operands as sums of matrix-core operands
+// float32 operands as sums of matrix-core operands: pairs are converted together (one
+// instruction each way), 5.5 operations an element for three terms
 // ---------------------------------------------------------------------------
 template <typename T> struct Sp;
 template <> struct Sp<bf16> { bf16x8 t[3]; };
 template <> struct Sp<float> { f32x8 t[1]; };
 template <typename T> constexpr int kTerms = std::is_same<T, bf16>::value ? 3 : 1;
 
+template <int NB = 3>
 __device__ __forceinline__ void split8(f32x8 v, Sp<bf16>& s) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    u32x4v o[3];
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
+    for (int e = 0; e < 8; e += 2) {
+        float a = v[e], b = v[e + 1];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            s.t[k][e] = (bf16)v[e];
-            v[e] -= (float)s.t[k][e];
+        for (int k = 0; k < NB; ++k) {
+            const unsigned u = __builtin_bit_cast(unsigned, __builtin_convertvector(f32x2{a, b}, bf16x2));
+            o[k][e >> 1] = u;
+            if (k + 1 < NB) {
+                a -= __builtin_bit_cast(float, u << 16);
+                b -= __builtin_bit_cast(float, u & 0xffff0000u);
+            }
         }
+    }
+#pragma unroll
+    for (int k = 0; k < NB; ++k) s.t[k] = __builtin_bit_cast(bf16x8, o[k]);
 }
+template <int NB = 3>
 __device__ __forceinline__ void split8(f32x8 v, Sp<float>& s) { s.t[0] = v; }
 
 // c += a b, a exact in T, b in its first NB terms
@@ -168,6 +184,18 @@ __host__ __device__ constexpr int tri(int i, int j) { return i * (i + 1) / 2 + j
 // upper triangular one (t >= i / 2)
 __host__ __device__ constexpr int frag_lo(int i, int t) { return i < 2 ? i : 2 + (i - 2) * 2 + t; }
 __host__ __device__ constexpr int frag_up(int i, int t) { return i < 2 ? i * 2 + t : 4 + (i - 2); }
+
+// element offset, in a table of 5 fragments, of block (i, j)'s four elements of lane 0
+__host__ __device__ constexpr int frag_at(int i, int j) {
+    return i == 0 ? 0 : i == 2 && j == 2 ? 4 : (i < 3 ? i : 3 + (j >> 1)) * 512 + 4 * (j & 1);
+}
+// the 16 x 32 fragment of row tile i, columns 32 t on
+__device__ __forceinline__ bf16x8 frag_tab5(const bf16* tab, int i, int t, int lane) {
+    const bf16x4 z = bf16x4{(bf16)0.f, (bf16)0.f, (bf16)0.f, (bf16)0.f};
+    if (i == 0) return join(ld4(tab + lane * 8), z);
+    if (i == 2 && t == 1) return join(ld4(tab + lane * 8 + 4), z);
+    return ld8(tab + frag_at(i, 2 * t) + lane * 8);
+}
 
 // The triangular table `src` (16 x 16 blocks, row-major, as k_delta_prep stores it) into LDS as
 // operand fragments: dst[term][fragment][lane][8].  UP: its transpose.
@@ -239,186 +267,209 @@ __device__ __forceinline__ void store_rows(T* __restrict__ dst, int64_t ds, cons
 }
 
 // ---------------------------------------------------------------------------
-// k_delta_prep: S and M of one (chunk, head), and the chunk's decay factors.  One work-group of
-// 4 waves; K K^T and Q K^T on the matrix cores straight from global rows, S by blocked
-// forward substitution in float32: the four S_ii side by side in one wave (a lane per
-// column), then S_ij = Z - S_ii (beta Z), Z = KK_ij - sum_k KK_ik (beta S_kj), wave j taking
-// block column j.  (The product form (I - X)(I + X^2)(I + X^4)... of the inverse needs no
-// substitution but loses four digits where keys repeat.)  Decay sums are float64 and leave
-// in two float32 parts, so a strongly decayed chunk keeps the exact ratio of neighbouring
-// tokens.  FRAG: the tables leave as the operand fragments that k_delta_dma reads.
+// k_delta_prep: S and M of a (chunk, head), and the chunk's decay factors; one wave per item,
+// no barriers.  A wave takes one (chunk, group) and `heads` of its heads: K K^T and Q K^T once,
+// on the matrix cores straight from global rows, kept in accumulators in the orientations
+// the steps below read; then per head the decays and S by blocked substitution in float32:
+// the four diagonal blocks S_ii side by side (16 lanes each, a lane per column, rows in
+// order through LDS), and below the diagonal, transposed so that every product's result is
+// the next one's operand and leaves in the order the walks load,
+//   Z^T = KK_ij^T - sum_{j < k <= i} KK_kj^T (beta_k S_ik^T),   S_ij^T = Z^T - S_jj^T (beta_j Z^T).
+// (The product form (I - X)(I + X^2)(I + X^4)... of the inverse needs no substitution but loses
+// four digits where keys repeat.)  Decay sums are float64 and kept in two float32 parts, so
+// a strongly decayed chunk keeps the exact ratio of neighbouring tokens.
+// FRAG: the tables leave as the operand fragments that k_delta_dma reads.
 // ---------------------------------------------------------------------------
+struct PrepLds {
+    float chi[L], clo[L], bet[L];
+    float d[4][16][20];  // the diagonal blocks of KK, then of S
+};
+
 template <typename T, int N, bool FRAG>
-__global__ __launch_bounds__(256) void k_delta_prep(Args a) {
-    constexpr int LD = L + 4;
+__global__ __launch_bounds__(256, 2) void k_delta_prep(Args a, int heads) {
     constexpr double LOG2E = 1.4426950408889634;
-    __shared__ float bet[L], chi[L], clo[L];
-    __shared__ __attribute__((aligned(16))) float Km[L * LD];  // KK, zeros on and above the diagonal; then S
-    __shared__ __attribute__((aligned(16))) float Sd[4 * 256];  // S_ii
-    const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
-    const int H = a.H, G = a.G;
-    const int h = (int)(blockIdx.x % (unsigned)H), kk = (int)(blockIdx.x / (unsigned)H);
+    __shared__ __attribute__((aligned(16))) PrepLds lds[4];
+    const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
+    PrepLds& m = lds[w];
+    const int H = a.H, G = a.G, Hg = H / G, nhb = (Hg + heads - 1) / heads;
+    const int64_t id = (int64_t)blockIdx.x * 4 + w;
+    const int hb = (int)(id % nhb), g = (int)(id / nhb % G);
+    const int64_t kk = id / nhb / G;
     if (kk >= a.rows.total_chunks()) return;
-    const int row = a.rows.row_of(kk), c = kk - a.rows.kbase(row);
+    const int row = a.rows.row_of((int)kk), c = (int)kk - a.rows.kbase(row);
     const int64_t t0 = a.rows.tok0(row) + (int64_t)c * L;
     const int n = (int)min((int64_t)L, a.rows.len(row) - (int64_t)c * L);
-    const int g = h / (H / G);
 
-    if (w == 0) {
-        const bool on = lane < n;
-        const int64_t t = t0 + (on ? lane : 0);
-        double v = on ? (double)a.dt[t * H + h] * (double)a.A[h] * LOG2E : 0.0;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const double o = __shfl_up(v, off, 64);
-            if (lane >= off) v += o;
-        }
-        const float hi = (float)v, lo = (float)(v - (double)hi);
-        const float b = on ? to_f(static_cast<const T*>(a.beta)[t * H + h]) : 0.f;
-        const double last = __shfl(v, 63, 64);
-        float* vec = a.vec + ((int64_t)kk * H + h) * kVec;
-        vec[lane] = exp2f_fast(hi);
-        vec[L + lane] = exp2f_fast((float)(last - v));
-        vec[2 * L + lane] = b;
-        vec[3 * L + lane] = hi;
-        vec[4 * L + lane] = lo;
-        bet[lane] = b;
-        chi[lane] = hi;
-        clo[lane] = lo;
-    }
-    // K K^T (rows i) and K Q^T or Q K^T: wave w takes row tile w against column tiles 0 .. w
+    // off-diagonal pairs (i, j), i > j, in order (1,0) (2,0) (2,1) (3,0) (3,1) (3,2)
     const T* Kg = static_cast<const T*>(a.B) + (t0 * G + g) * N;
     const T* Qg = static_cast<const T*>(a.C) + (t0 * G + g) * N;
     const int64_t rs = (int64_t)G * N;
-    f32x4 kt[4], qt[4];
+    f32x4 k1[6], k2[6], kd[4], qk[kTri];  // [i][j] (rows i), [j][i], [i][i], [j][i] of Q K^T
 #pragma unroll
-    for (int j = 0; j < 4; ++j) kt[j] = qt[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int ri = w * 16 + l16;
-    const int rc = ri < n ? ri : n - 1;
+    for (int v = 0; v < 6; ++v) k1[v] = k2[v] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int v = 0; v < 4; ++v) kd[v] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int v = 0; v < kTri; ++v) qk[v] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int ks = 0; ks < (N + 31) / 32; ++ks) {
         const int col = ks * 32 + 8 * q;
         const bool in = N >= 32 || col < N;
         const int cc = in ? col : 0;
-        const auto ka = sel8(in && ri < n, ld8(Kg + rc * rs + cc));
-        const auto qa = sel8(in && ri < n, ld8(Qg + rc * rs + cc));
+        typename V8<T>::type kf[4], qf[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j > w) break;
-            const int rj = j * 16 + l16;
-            const auto kb = sel8(in && rj < n, ld8(Kg + (rj < n ? rj : n - 1) * rs + cc));
-            kt[j] = mma(kt[j], ka, kb);
-            qt[j] = FRAG ? mma(qt[j], kb, qa) : mma(qt[j], qa, kb);
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 16 + l16, rc = r < n ? r : n - 1;
+            kf[i] = sel8(in && r < n, ld8(Kg + rc * rs + cc));
+            qf[i] = sel8(in && r < n, ld8(Qg + rc * rs + cc));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            kd[i] = mma(kd[i], kf[i], kf[i]);
+#pragma unroll
+            for (int j = 0; j <= i; ++j) {
+                qk[tri(i, j)] = mma(qk[tri(i, j)], kf[j], qf[i]);
+                if (j < i) {
+                    k1[tri(i - 1, j)] = mma(k1[tri(i - 1, j)], kf[i], kf[j]);
+                    k2[tri(i - 1, j)] = mma(k2[tri(i - 1, j)], kf[j], kf[i]);
+                }
+            }
         }
     }
-    __syncthreads();
-    const int64_t e0 = (int64_t)kk * H + h;
-    float* St = a.tab + e0 * kTab;
-    T* Sg = reinterpret_cast<T*>(a.tab) + e0 * kFragTab;
-    T* Mg = Sg + 3 * kFrag * 512;
+    const int h0 = g * Hg + hb * heads, h1 = min(g * Hg + Hg, h0 + heads);
+    for (int h = h0; h < h1; ++h) {
+        const int64_t e0 = kk * H + h;
+        {
+            const bool on = lane < n;
+            const int64_t t = t0 + (on ? lane : 0);
+            double v = on ? (double)a.dt[t * H + h] * (double)a.A[h] * LOG2E : 0.0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (j > w) break;
-        typename V4<T>::type mo;
+            for (int off = 1; off < 64; off <<= 1) {
+                const double o = __shfl_up(v, off, 64);
+                if (lane >= off) v += o;
+            }
+            const float hi = (float)v, lo = (float)(v - (double)hi);
+            const float b = on ? to_f(static_cast<const T*>(a.beta)[t * H + h]) : 0.f;
+            const float ew = exp2f_fast((float)(__shfl(v, 63, 64) - v));
+            float* vec = a.vec + e0 * kVec;
+            vec[lane] = exp2f_fast(hi);
+            vec[L + lane] = FRAG ? ew * b : ew;
+            if (!FRAG) {
+                vec[2 * L + lane] = b;
+                vec[3 * L + lane] = hi;
+                vec[4 * L + lane] = lo;
+            }
+            m.bet[lane] = b;
+            m.chi[lane] = hi;
+            m.clo[lane] = lo;
+        }
+        __builtin_amdgcn_wave_barrier();
+        f32x4 ch[4], cl[4], bt[4];  // of this lane's rows 4q + e
+        float sh[4], sl[4];         // of this lane's column l16
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i16 = 4 * q + r, i = w * 16 + i16, jj = j * 16 + l16;
-            const float gam = i >= jj ? exp2f_fast((chi[i] - chi[jj]) + (clo[i] - clo[jj])) : 0.f;
-            Km[i * LD + jj] = i > jj ? kt[j][r] * gam : 0.f;
-            if (FRAG) {  // this lane: row i2, column j2
-                const int i2 = w * 16 + l16, j2 = j * 16 + i16;
-                const float g2 = i2 >= j2 ? exp2f_fast((chi[i2] - chi[j2]) + (clo[i2] - clo[j2])) : 0.f;
-                mo[r] = from_f<T>(qt[j][r] * g2);
+        for (int i = 0; i < 4; ++i) {
+            ch[i] = ld4(m.chi + i * 16 + 4 * q);
+            cl[i] = ld4(m.clo + i * 16 + 4 * q);
+            bt[i] = ld4(m.bet + i * 16 + 4 * q);
+            sh[i] = m.chi[i * 16 + l16];
+            sl[i] = m.clo[i * 16 + l16];
+        }
+        float* St = a.tab + e0 * kTab;
+        T* Sg = reinterpret_cast<T*>(a.tab) + e0 * kFragTab;
+        T* Mg = Sg + 3 * 5 * 512;
+        auto put = [&](int i, int j, f32x4 v) {  // S_ij, this lane: row l16, columns 4q + e
+            if (FRAG) {
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    typename V4<T>::type o;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (k == 0) v[e] *= -bt[j][e];
+                        o[e] = from_f<T>(v[e]);
+                        v[e] -= to_f(o[e]);
+                    }
+                    st4(Sg + k * 5 * 512 + frag_at(i, j) + lane * 8, o);
+                }
             } else {
-                St[(kTri + tri(w, j)) * 256 + i16 * 16 + l16] = qt[j][r] * gam;
+                st4(St + tri(i, j) * 256 + l16 * 16 + 4 * q, v);
+            }
+        };
+        // M, and the diagonal blocks of KK
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int j = 0; j <= i; ++j) {
+                f32x4 v;
+                typename V4<T>::type o;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float gam = exp2f_fast((sh[i] - ch[j][e]) + (sl[i] - cl[j][e]));
+                    v[e] = i > j || l16 >= 4 * q + e ? qk[tri(i, j)][e] * gam : 0.f;
+                    o[e] = from_f<T>(v[e] * bt[j][e]);
+                }
+                if (FRAG) st4(Mg + frag_at(i, j) + lane * 8, o);
+                else st4(St + (kTri + tri(i, j)) * 256 + l16 * 16 + 4 * q, v);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float gam = exp2f_fast((ch[i][e] - sh[i]) + (cl[i][e] - sl[i]));
+                m.d[i][4 * q + e][l16] = 4 * q + e > l16 ? kd[i][e] * gam : 0.f;
             }
         }
-        if (FRAG) st4(Mg + frag_lo(w, j >> 1) * 512 + lane * 8 + 4 * (j & 1), mo);
-    }
-    if (FRAG && (w == 0 || w == 2)) {  // the fragments' halves above the diagonal
-        typename V4<T>::type z;
+        __builtin_amdgcn_wave_barrier();
+        {  // S_qq: column l16, rows in order
+            float s[16], bs[16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] = from_f<T>(0.f);
-        const int o = frag_lo(w, w >> 1) * 512 + lane * 8 + 4;
-        st4(Mg + o, z);
+            for (int i = 0; i < 16; ++i) {
+                float v = m.d[q][i][l16];
 #pragma unroll
-        for (int k = 0; k < 3; ++k) st4(Sg + k * kFrag * 512 + o, z);
-    }
-    __syncthreads();
-    if (w == 0) {  // S_qq: lane group q, column l16, rows in order
-        float s[16], bs[16];
-        const float* kd = Km + q * 16 * LD + q * 16;
+                for (int k4 = 0; k4 < i; k4 += 4) {
+                    const f32x4 kr = ld4(&m.d[q][i][k4]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float v = kd[i * LD + l16];
-#pragma unroll
-            for (int k4 = 0; k4 < i; k4 += 4) {
-                const f32x4 kr = ld4(kd + i * LD + k4);
-#pragma unroll
-                for (int k = k4; k < k4 + 4 && k < i; ++k) v -= kr[k - k4] * bs[k];
+                    for (int k = k4; k < k4 + 4 && k < i; ++k) v -= kr[k - k4] * bs[k];
+                }
+                s[i] = v;
+                bs[i] = m.bet[q * 16 + i] * v;
             }
-            s[i] = v;
-            bs[i] = bet[q * 16 + i] * v;
-            Sd[q * 256 + i * 16 + l16] = v;
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m.d[q][i][l16] = s[i];
         }
-    }
-    __syncthreads();
-    f32x4 col[4];  // S_kw of block column w, lane: rows 4q + e, column l16
+        __builtin_amdgcn_wave_barrier();
+        f32x4 sd[4];  // S_jj^T as an A operand: S_jj[4q + e][l16]
 #pragma unroll
-    for (int e = 0; e < 4; ++e) col[0][e] = Sd[w * 256 + (4 * q + e) * 16 + l16];
+        for (int j = 0; j < 3; ++j)
 #pragma unroll
-    for (int m = 1; m < 4; ++m) {  // block row w + m
-        const int i = w + m;
-        if (i > 3) break;
-        f32x4 zv = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int e = 0; e < 4; ++e) sd[j][e] = m.d[j][4 * q + e][l16];
+        f32x4 b1[6];  // KK_kj^T as A operands
 #pragma unroll
-        for (int k = 0; k < m; ++k) {
-            f32x4 bs;
+        for (int k = 1; k < 4; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) bs[e] = bet[(w + k) * 16 + 4 * q + e] * col[k][e];
-            zv = mma16(zv, ld4(Km + (i * 16 + l16) * LD + (w + k) * 16 + 4 * q), bs);
-        }
-        f32x4 bz;
+            for (int j = 0; j < k; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            zv[e] = Km[(i * 16 + 4 * q + e) * LD + w * 16 + l16] - zv[e];
-            bz[e] = bet[i * 16 + 4 * q + e] * zv[e];
-        }
-        const f32x4 d = mma16(f32x4{0.f, 0.f, 0.f, 0.f}, ld4(Sd + i * 256 + l16 * 16 + 4 * q), bz);
-        col[m] = zv - d;
-    }
-    if (!FRAG) {
+                for (int e = 0; e < 4; ++e)
+                    b1[tri(k - 1, j)][e] =
+                        k1[tri(k - 1, j)][e] * exp2f_fast((ch[k][e] - sh[j]) + (cl[k][e] - sl[j]));
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            if (w + m > 3) break;
+        for (int i = 0; i < 4; ++i) {
+            f32x4 st[4];  // beta_k S_ik^T
+            f32x4 v = ld4(&m.d[i][l16][4 * q]);
+            put(i, i, v);
+            st[i] = v * bt[i];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) St[tri(w + m, w) * 256 + (4 * q + e) * 16 + l16] = col[m][e];
-        }
-        return;
-    }
-    __syncthreads();  // KK is no longer read
+            for (int j = i - 1; j >= 0; --j) {
+                f32x4 zn = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        if (w + m > 3) break;
+                for (int k = j + 1; k <= i; ++k) zn = mma16(zn, b1[tri(k - 1, j)], st[k]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) Km[((w + m) * 16 + 4 * q + e) * LD + w * 16 + l16] = col[m][e];
-    }
-    __syncthreads();
-    for (int p = tid; p < kTri * 64; p += 256) {
-        const int blk = p >> 6;
-        const int i = blk < 1 ? 0 : blk < 3 ? 1 : blk < 6 ? 2 : 3, j = blk - tri(i, 0);
-        f32x4 v = ld4(Km + (i * 16 + l16) * LD + j * 16 + 4 * q);
-        T* d = Sg + frag_lo(i, j >> 1) * 512 + lane * 8 + 4 * (j & 1);
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            typename V4<T>::type o;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                o[x] = from_f<T>(v[x]);
-                v[x] -= to_f(o[x]);
+                for (int e = 0; e < 4; ++e)
+                    v[e] = k2[tri(i - 1, j)][e] * exp2f_fast((sh[i] - ch[j][e]) + (sl[i] - cl[j][e])) - zn[e];
+                v -= mma16(f32x4{0.f, 0.f, 0.f, 0.f}, sd[j], v * bt[j]);
+                put(i, j, v);
+                st[j] = v * bt[j];
             }
-            st4(d + k * kFrag * 512, o);
         }
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
@@ -679,9 +730,10 @@ __global__ __launch_bounds__(256) void k_delta(Args a) {
 
 // ---------------------------------------------------------------------------
 // k_delta_dma: the forward walk for bfloat16 at dstate 64 and up, every tile fetched straight into
-// LDS while the chunk before computes.  K has two buffers (it is read first and last in a
-// chunk); Q is refilled once Q h^T is done, the tables once M u is done; x goes to registers
-// a chunk ahead, and y leaves from them.  LDS tiles are unpadded (the transfer writes 16
+// LDS while the chunk before computes.  Q is refilled once Q h^T is done, the tables once M u
+// is done; K, read first and last in a chunk, has two buffers (KB = 2), or one (KB = 1) where
+// a third work-group per CU covers the wait; x goes to registers a chunk ahead, and y leaves
+// from them.  LDS tiles are unpadded (the transfer writes 16
 // bytes per lane in order); a row's 16-byte pieces are exchanged by the row's low bits, so
 // that the 16 rows of a fragment lie in different banks.  Every buffer is an array of its own
 // and the two K buffers are named at compile time (chunks in pairs), so the compiler knows
@@ -719,33 +771,34 @@ __device__ __forceinline__ void dma_run(brsrc r, char* dst, int runs, int w, int
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + m * 1024), 16, m * 1024 + lane * 16, 0, 0, 0);
 }
 
-template <int N, int CT>
-__global__ __launch_bounds__(256, 2) void k_delta_dma(Args a) {
+template <int N, int CT, int KB, int OCC>
+__global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
     constexpr int NTL = N / 16, KS = N / 32, TILE = Dma<N>::TILE, SWZ = Dma<N>::SWZ;
     __shared__ __attribute__((aligned(16))) bf16 K0[TILE];
-    __shared__ __attribute__((aligned(16))) bf16 K1[TILE];
+    __shared__ __attribute__((aligned(16))) bf16 K1[KB == 2 ? TILE : 8];
     __shared__ __attribute__((aligned(16))) bf16 Qs[TILE];
     __shared__ __attribute__((aligned(16))) bf16 Sf[kFragTab];  // S in three terms, then M
-    __shared__ __attribute__((aligned(16))) float V0[4 * L];
-    __shared__ __attribute__((aligned(16))) float V1[4 * L];
-    const bf16* Mf = Sf + 3 * kFrag * 512;
+    __shared__ __attribute__((aligned(16))) float Vs[2 * L];    // e^c, beta e^{c_L - c}
+    const bf16* Mf = Sf + 3 * 5 * 512;
     const int tid = threadIdx.x, nw = blockDim.x >> 6, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
     const int H = a.H, G = a.G, P = a.P;
-    const int SW = 16 * CT * nw;
-    const int nsl = P / SW, BH = a.rows.nrows * H;
-    const int sl = (int)(blockIdx.x % (unsigned)nsl);
-    int bh = (int)(blockIdx.x / (unsigned)nsl);
+    const int SW = 16 * CT * nw, nsl = P / SW;
+    const int sl = (int)(blockIdx.x % (unsigned)nsl), bh = (int)(blockIdx.x / (unsigned)nsl);
     const int h = bh % H, row = bh / H, g = h / (H / G);
     const int64_t Tn = a.rows.len(row), tok0 = a.rows.tok0(row);
     const int nc = a.rows.nchunks(row), kb0 = a.rows.kbase(row);
     const int p0 = sl * SW + w * 16 * CT;  // this wave's first column
 
+    // h^T: row 4q + e of tile t is n = 32 (t / 2) + 8q + 4 (t % 2) + e, so that a pair of tiles is
+    // the operand whose other side reads 8 consecutive columns of K or Q
     f32x4 acc[NTL][CT];
+    const int64_t ho = ((int64_t)bh * P + p0 + l16) * N + 8 * q;
+    auto hn = [&](int t, int ct) { return ho + ct * 16 * N + (t >> 1) * 32 + (t & 1) * 4; };
 #pragma unroll
     for (int t = 0; t < NTL; ++t)
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
-            acc[t][ct] = a.h0 ? ld4(a.h0 + ((int64_t)bh * P + p0 + ct * 16 + l16) * N + t * 16 + 4 * q)
+            acc[t][ct] = a.h0 ? ld4(a.h0 + hn(t, ct))
                               : f32x4{0.f, 0.f, 0.f, 0.f};
 
     const int rsk = G * N * 2, rsx = H * P * 2;
@@ -759,14 +812,13 @@ __global__ __launch_bounds__(256, 2) void k_delta_dma(Args a) {
                          (uint32_t)((rows_left(c) - 1) * rsx + P * 2));
     };
     auto item = [&](int c) { return (int64_t)(kb0 + c) * H + h; };
-    auto fetch_k = [&](int c, bf16* kd, float* vd) {
-        dma_tile<N>(key_rsrc(a.B, c), kd, rsk, w, nw, lane);
-        if (w == 0 && lane < 48) dma_run(make_rsrc(a.vec + item(c) * kVec, 3 * L * 4), (char*)vd, 1, 0, 1, lane);
-    };
+    auto fetch_k = [&](int c, bf16* kd) { dma_tile<N>(key_rsrc(a.B, c), kd, rsk, w, nw, lane); };
     auto fetch_q = [&](int c) { dma_tile<N>(key_rsrc(a.C, c), Qs, rsk, w, nw, lane); };
     auto fetch_tab = [&](int c) {
         dma_run(make_rsrc(reinterpret_cast<const bf16*>(a.tab) + item(c) * kFragTab, kFragTab * 2),
                 reinterpret_cast<char*>(Sf), kFragTab / 512, w, nw, lane);
+        if (w == 0 && lane < 32)
+            dma_run(make_rsrc(a.vec + item(c) * kVec, 2 * L * 4), reinterpret_cast<char*>(Vs), 1, 0, 1, lane);
     };
     const int xo = 4 * q * rsx + (p0 + l16) * 2;  // bytes of (token 4q, column l16)
     unsigned short xr[4][CT][4];
@@ -783,22 +835,20 @@ __global__ __launch_bounds__(256, 2) void k_delta_dma(Args a) {
 
     // lane offsets (elements) of the fragment reads; further fragments differ by an exchange of
     // piece bits and by whole row tiles
-    const int ka = l16 * N + (((q >> 1) ^ (l16 & SWZ)) << 3) + 4 * (q & 1);
+    const int ka = l16 * N + ((q ^ (l16 & SWZ)) << 3);
     const int tr = 4 * q + (l16 >> 2);
-    const int kt = tr * N + ((((l16 & 3) >> 1) ^ (tr & SWZ)) << 3) + 4 * (l16 & 1);
+    const int kt = tr * N + (((l16 & 3) ^ (tr & SWZ)) << 3);
 
     if (nc > 0) {
-        fetch_k(0, K0, V0);
+        fetch_k(0, K0);
         fetch_q(0);
         fetch_tab(0);
         fetch_x(0);
     }
-    auto chunk = [&](int c, const bf16* Ks, const float* ecs, bf16* Kn, float* Vn) {
+    auto chunk = [&](int c, const bf16* Ks, bf16* Kn) {
         wave_meet(true);  // the chunk's tiles have landed
         const bool more = c + 1 < nc;
-        if (more) fetch_k(c + 1, Kn, Vn);
-        const float* ews = ecs + L;
-        const float* bts = ews + L;
+        if (KB == 2 && more) fetch_k(c + 1, Kn);
 
         // K h^T in three terms, Q h^T in two (enough for a bfloat16 y)
         f32x4 v[4][CT], yq[4][CT];
@@ -814,9 +864,8 @@ __global__ __launch_bounds__(256, 2) void k_delta_dma(Args a) {
             bf16x8 kf[4], qf[4];
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
-                const int o1 = (ka ^ (ks << 5)) + it * 16 * N, o2 = (ka ^ ((ks << 5) | 16)) + it * 16 * N;
-                kf[it] = join(ld4(Ks + o1), ld4(Ks + o2));
-                qf[it] = join(ld4(Qs + o1), ld4(Qs + o2));
+                kf[it] = ld8(Ks + (ka ^ (ks << 5)) + it * 16 * N);
+                qf[it] = ld8(Qs + (ka ^ (ks << 5)) + it * 16 * N);
             }
 #pragma unroll
             for (int k = 0; k < 3; ++k)
@@ -831,66 +880,59 @@ __global__ __launch_bounds__(256, 2) void k_delta_dma(Args a) {
         wave_meet(false);  // every wave is done with Q
         if (more) fetch_q(c + 1);
 
-        // R, then r = R - S (beta R)
+        // R, then r = R - S beta R
         Sp<bf16> b2[2][CT];
 #pragma unroll
-        for (int it = 0; it < 4; ++it)
+        for (int it = 0; it < 4; ++it) {
+            const f32x4 ec = ld4(Vs + it * 16 + 4 * q);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float ec = ecs[it * 16 + 4 * q + i];
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-                    v[it][ct][i] = to_f(__builtin_bit_cast(bf16, xr[it][ct][i])) - ec * v[it][ct][i];
-                    yq[it][ct][i] *= ec;
+                    v[it][ct][i] = to_f(__builtin_bit_cast(bf16, xr[it][ct][i])) - ec[i] * v[it][ct][i];
+                    yq[it][ct][i] *= ec[i];
                 }
-            }
+        }
         if (more) fetch_x(c + 1);
-        auto scaled = [&](const float* s1, const float* s2) {  // s1_t s2_t v_t as operands
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                f32x4 sa = ld4(s1 + 32 * t + 4 * q), sb = ld4(s1 + 32 * t + 16 + 4 * q);
-                if (s2) {
-                    sa *= ld4(s2 + 32 * t + 4 * q);
-                    sb *= ld4(s2 + 32 * t + 16 + 4 * q);
-                }
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) split8(join(v[2 * t][ct] * sa, v[2 * t + 1][ct] * sb), b2[t][ct]);
-            }
-        };
-        scaled(bts, nullptr);
-        f32x4 d[4][CT];
-#pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) d[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int ct = 0; ct < CT; ++ct) split8(join(v[2 * t][ct], v[2 * t + 1][ct]), b2[t][ct]);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int k = 0; k < 3; ++k)  // term of S
 #pragma unroll
                 for (int it = 2 * t; it < 4; ++it) {
-                    const bf16x8 sf = ld8(Sf + (k * kFrag + frag_lo(it, t)) * 512 + lane * 8);
+                    const bf16x8 sf = frag_tab5(Sf + k * 5 * 512, it, t, lane);
 #pragma unroll
                     for (int m = 0; m < 3 - k; ++m)
 #pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) d[it][ct] = mma(d[it][ct], sf, b2[t][ct].t[m]);
+                        for (int ct = 0; ct < CT; ++ct) v[it][ct] = mma(v[it][ct], sf, b2[t][ct].t[m]);
                 }
+        // Y = e^c Q h^T + M beta r
 #pragma unroll
-        for (int it = 0; it < 4; ++it)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) v[it][ct] -= d[it][ct];
-        // Y = e^c Q h^T + M u
-        scaled(bts, nullptr);
+            for (int ct = 0; ct < CT; ++ct) split8<2>(join(v[2 * t][ct], v[2 * t + 1][ct]), b2[t][ct]);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int it = 2 * t; it < 4; ++it) {
-                const bf16x8 mf = ld8(Mf + frag_lo(it, t) * 512 + lane * 8);
+                const bf16x8 mf = frag_tab5(Mf, it, t, lane);
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) yq[it][ct] = mma(yq[it][ct], mf, b2[t][ct].t[k]);
             }
+        // e^{c_L - c} u as operands
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const f32x4 sa = ld4(Vs + L + 32 * t + 4 * q), sb = ld4(Vs + L + 32 * t + 16 + 4 * q);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) split8(join(v[2 * t][ct] * sa, v[2 * t + 1][ct] * sb), b2[t][ct]);
+        }
+        const float el = Vs[L - 1];
         wave_meet(false);  // every wave is done with the tables
         if (more) fetch_tab(c + 1);
         {
@@ -906,15 +948,13 @@ __global__ __launch_bounds__(256, 2) void k_delta_dma(Args a) {
                             (it * 16 + i) * rsx, 0);
         }
         // h' = e^{c_L} h + K^T (e^{c_L - c} u)
-        scaled(ews, bts);
-        const float el = ecs[L - 1];
 #pragma unroll
         for (int t = 0; t < NTL; ++t) {
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) acc[t][ct] *= el;
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                const bf16* kp = Ks + (kt ^ (t << 4)) + ks * 32 * N;
+                const bf16* kp = Ks + (kt ^ ((t >> 1) << 5)) + 4 * (t & 1) + ks * 32 * N;
                 const bf16x8 kf = __builtin_bit_cast(
                     bf16x8, __builtin_shufflevector(ds_tr16(kp), ds_tr16(kp + 16 * N), 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
@@ -923,17 +963,25 @@ __global__ __launch_bounds__(256, 2) void k_delta_dma(Args a) {
                     for (int ct = 0; ct < CT; ++ct) acc[t][ct] = mma(acc[t][ct], kf, b2[ks][ct].t[k]);
             }
         }
+        if (KB == 1 && more) {
+            wave_meet(false);  // every wave is done with K
+            fetch_k(c + 1, K0);
+        }
     };
-    for (int c = 0; c < nc; c += 2) {
-        chunk(c, K0, V0, K1, V1);
-        if (c + 1 < nc) chunk(c + 1, K1, V1, K0, V0);
+    if (KB == 2) {
+        for (int c = 0; c < nc; c += 2) {
+            chunk(c, K0, K1);
+            if (c + 1 < nc) chunk(c + 1, K1, K0);
+        }
+    } else {
+        for (int c = 0; c < nc; ++c) chunk(c, K0, K0);
     }
     if (a.hT) {
 #pragma unroll
         for (int t = 0; t < NTL; ++t)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
-                st4(a.hT + ((int64_t)bh * P + p0 + ct * 16 + l16) * N + t * 16 + 4 * q, acc[t][ct]);
+                st4(a.hT + hn(t, ct), acc[t][ct]);
     }
 }
 

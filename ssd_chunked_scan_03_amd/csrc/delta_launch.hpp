@@ -68,25 +68,43 @@ int walk_n(const Args& a, const Slice& s, int which) {
 // Whether the forward runs k_delta_dma (tables as fragments).
 inline bool dma_walk(bool bf16_dtype, int64_t N) { return bf16_dtype && N >= 64; }
 
-template <int N, int CT>
+// Heads of a group that one wave of the preparation takes, sharing their K K^T and Q K^T: up
+// to 4 while that leaves 8 waves per SIMD.
+inline int prep_heads(int64_t ntab, int64_t H, int64_t G) {
+    int s = 4;
+    while (s > 1 && (s > H / G || ntab * G * ((H / G + s - 1) / s) < 8192)) s >>= 1;
+    return s;
+}
+template <typename T, int N, bool FRAG>
+void prep(const Args& a) {
+    const int heads = prep_heads(a.ntab, a.H, a.G);
+    const int64_t waves = (int64_t)a.ntab * a.G * ((a.H / a.G + heads - 1) / heads);
+    k_delta_prep<T, N, FRAG><<<(unsigned)((waves + 3) / 4), 256, 0, a.stream>>>(a, heads);
+}
+
+template <int N, int CT, int KB, int OCC>
 int walk_dma(const Args& a, int waves) {
     const unsigned grid = (unsigned)((int64_t)a.rows.nrows * a.H * (a.P / (16 * CT * waves)));
-    k_delta_dma<N, CT><<<grid, 64 * waves, 0, a.stream>>>(a);
+    k_delta_dma<N, CT, KB, OCC><<<grid, 64 * waves, 0, a.stream>>>(a);
     return hipGetLastError() == hipSuccess ? 0 : 7;
 }
 
 template <typename T, int N>
 int run_fwd(const Args& a) {
-    const unsigned tabs = (unsigned)((int64_t)a.ntab * a.H);
     if constexpr (std::is_same<T, bf16>::value && N >= 64) {
-        k_delta_prep<T, N, true><<<tabs, 256, 0, a.stream>>>(a);
+        prep<T, N, true>(a);
+        const int waves = a.P >= 64 ? 4 : a.P / 16;
         if constexpr (N <= 128) {
-            if (a.P == 128) return walk_dma<N, 2>(a, 4);
+            if (a.P == 128) return walk_dma<N, 2, 2, 2>(a, 4);
+            // more chains than two work-groups per CU hold: three, with one K buffer
+            if ((int64_t)a.rows.nrows * a.H > 512) return walk_dma<N, 1, 1, 3>(a, waves);
+            return walk_dma<N, 1, 2, 2>(a, waves);
+        } else {
+            return walk_dma<N, 1, 2, 1>(a, waves);
         }
-        return walk_dma<N, 1>(a, a.P >= 64 ? 4 : a.P / 16);
     } else {
         const Slice s = slice_of(std::is_same<T, bf16>::value, (int64_t)a.rows.nrows * a.H, a.P, N);
-        k_delta_prep<T, N, false><<<tabs, 256, 0, a.stream>>>(a);
+        prep<T, N, false>(a);
         return walk_n<T, N>(a, s, 0);
     }
 }
@@ -95,7 +113,7 @@ template <typename T, int N>
 int run_bwd(const Args& a) {
     typedef GradCfg<T, N> GC;
     const Slice s = slice_of(std::is_same<T, bf16>::value, (int64_t)a.rows.nrows * a.H, a.P, N);
-    k_delta_prep<T, N, false><<<(unsigned)((int64_t)a.ntab * a.H), 256, 0, a.stream>>>(a);
+    prep<T, N, false>(a);
     int st = walk_n<T, N>(a, s, 1);
     if (!st) st = walk_n<T, N>(a, s, 2);
     if (st) return st;
