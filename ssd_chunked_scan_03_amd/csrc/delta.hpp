@@ -53,6 +53,9 @@ constexpr int kVec = 5 * L;           // floats of its e^c, e^{c_L - c}, beta an
 // below the diagonal fill 5 fragments (frag_at), and beta is folded into their columns and
 // into the e^{c_L - c} of vec, so that the walk never reads it.
 constexpr int kFragTab = (3 + 1) * 5 * 512;  // bfloat16 elements
+// The backward's: -S and M, three terms each, nothing folded.
+constexpr int kFragTab2 = (3 + 3) * 5 * 512;
+enum Tab { kPlain, kFold, kBoth };  // tables as float32 blocks, the forward's, the backward's fragments
 constexpr int kFrag = 6;              // 16 x 32 operand fragments covering a triangular 64 x 64 table
 
 struct Args {
@@ -81,8 +84,10 @@ struct Args {
     void* dC;
     void* dbeta;
     float* dh0;
-    void* r;      // [b T][H][P] residuals
-    void* z;      // [b T][H][P]
+    void* r;      // [b T][H][P] residuals; bfloat16: and what their rounding left, rounded
+    void* rlo;
+    void* z;      // [b T][H][P], the same
+    void* zlo;
     void* hin;    // [ntab][H][P][N] state entering each chunk
     short* hlo;   // bfloat16: what hin's rounding left of the float32 state (split_state)
     void* lin;    // [ntab][H][P][N] dh' of each chunk
@@ -278,15 +283,17 @@ __device__ __forceinline__ void store_rows(T* __restrict__ dst, int64_t ds, cons
 // (The product form (I - X)(I + X^2)(I + X^4)... of the inverse needs no substitution but loses
 // four digits where keys repeat.)  Decay sums are float64 and kept in two float32 parts, so
 // a strongly decayed chunk keeps the exact ratio of neighbouring tokens.
-// FRAG: the tables leave as the operand fragments that k_delta_dma reads.
+// TAB: float32 blocks, or the operand fragments that the forward's or the backward's
+// k_delta_dma walks read.
 // ---------------------------------------------------------------------------
 struct PrepLds {
     float chi[L], clo[L], bet[L];
     float d[4][16][20];  // the diagonal blocks of KK, then of S
 };
 
-template <typename T, int N, bool FRAG>
+template <typename T, int N, Tab TAB>
 __global__ __launch_bounds__(256, 2) void k_delta_prep(Args a, int heads) {
+    constexpr bool FRAG = TAB != kPlain, FOLD = TAB == kFold;
     constexpr double LOG2E = 1.4426950408889634;
     __shared__ __attribute__((aligned(16))) PrepLds lds[4];
     const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
@@ -353,8 +360,8 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(Args a, int heads) {
             const float ew = exp2f_fast((float)(__shfl(v, 63, 64) - v));
             float* vec = a.vec + e0 * kVec;
             vec[lane] = exp2f_fast(hi);
-            vec[L + lane] = FRAG ? ew * b : ew;
-            if (!FRAG) {
+            vec[L + lane] = FOLD ? ew * b : ew;
+            if (!FOLD) {
                 vec[2 * L + lane] = b;
                 vec[3 * L + lane] = hi;
                 vec[4 * L + lane] = lo;
@@ -375,24 +382,25 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(Args a, int heads) {
             sl[i] = m.clo[i * 16 + l16];
         }
         float* St = a.tab + e0 * kTab;
-        T* Sg = reinterpret_cast<T*>(a.tab) + e0 * kFragTab;
+        T* Sg = reinterpret_cast<T*>(a.tab) + e0 * (FOLD ? kFragTab : kFragTab2);
         T* Mg = Sg + 3 * 5 * 512;
-        auto put = [&](int i, int j, f32x4 v) {  // S_ij, this lane: row l16, columns 4q + e
-            if (FRAG) {
+        // a block's elements (this lane: row l16, columns 4q + e) in `terms` terms
+        auto frags = [&](T* dst, int i, int j, f32x4 v, int terms) {
 #pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    typename V4<T>::type o;
+            for (int k = 0; k < 3; ++k) {
+                if (k >= terms) break;
+                typename V4<T>::type o;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (k == 0) v[e] *= -bt[j][e];
-                        o[e] = from_f<T>(v[e]);
-                        v[e] -= to_f(o[e]);
-                    }
-                    st4(Sg + k * 5 * 512 + frag_at(i, j) + lane * 8, o);
+                for (int e = 0; e < 4; ++e) {
+                    o[e] = from_f<T>(v[e]);
+                    v[e] -= to_f(o[e]);
                 }
-            } else {
-                st4(St + tri(i, j) * 256 + l16 * 16 + 4 * q, v);
+                st4(dst + k * 5 * 512 + frag_at(i, j) + lane * 8, o);
             }
+        };
+        auto put = [&](int i, int j, f32x4 v) {  // S_ij
+            if (FRAG) frags(Sg, i, j, FOLD ? v * -bt[j] : -v, 3);
+            else st4(St + tri(i, j) * 256 + l16 * 16 + 4 * q, v);
         };
         // M, and the diagonal blocks of KK
 #pragma unroll
@@ -400,14 +408,12 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(Args a, int heads) {
 #pragma unroll
             for (int j = 0; j <= i; ++j) {
                 f32x4 v;
-                typename V4<T>::type o;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float gam = exp2f_fast((sh[i] - ch[j][e]) + (sl[i] - cl[j][e]));
                     v[e] = i > j || l16 >= 4 * q + e ? qk[tri(i, j)][e] * gam : 0.f;
-                    o[e] = from_f<T>(v[e] * bt[j][e]);
                 }
-                if (FRAG) st4(Mg + frag_at(i, j) + lane * 8, o);
+                if (FRAG) frags(Mg, i, j, FOLD ? v * bt[j] : v, FOLD ? 1 : 3);
                 else st4(St + (kTri + tri(i, j)) * 256 + l16 * 16 + 4 * q, v);
             }
 #pragma unroll
@@ -696,8 +702,10 @@ __global__ __launch_bounds__(256) void k_delta(Args a) {
                 for (int ct = 0; ct < CT; ++ct) {
                     T* o = Xs + t * ldx + pw + ct * 16 + l16;
                     if (SAVE) {
-                        dot += to_f(Ys[t * ldx + pw + ct * 16 + l16]) * yq[it][ct][i];
+                        T* o2 = Ys + t * ldx + pw + ct * 16 + l16;
+                        dot += to_f(*o2) * yq[it][ct][i];
                         *o = from_f<T>(v[it][ct][i]);
+                        *o2 = from_f<T>(v[it][ct][i] - to_f(*o));
                     } else {
                         *o = from_f<T>(yq[it][ct][i]);
                     }
@@ -712,6 +720,8 @@ __global__ __launch_bounds__(256) void k_delta(Args a) {
         store_rows(static_cast<T*>(SAVE ? a.r : a.y) + (t0 * H + h) * P + p0, (int64_t)H * P, Xs, ldx, n, SW, tid,
                    nthr);
         if (SAVE) {
+            if (NT > 1)
+                store_rows(static_cast<T*>(a.rlo) + (t0 * H + h) * P + p0, (int64_t)H * P, Ys, ldx, n, SW, tid, nthr);
             for (int t = tid; t < n; t += nthr) {
                 float s = 0.f;
                 for (int k2 = 0; k2 < (nthr >> 6); ++k2) s += dots[k2 * L + t];
@@ -771,18 +781,20 @@ __device__ __forceinline__ void dma_run(brsrc r, char* dst, int runs, int w, int
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + m * 1024), 16, m * 1024 + lane * 16, 0, 0, 0);
 }
 
-template <int N, int CT, int KB, int OCC>
+template <int N, int CT, int KB, int OCC, bool SAVE>
 __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
+    constexpr int TABN = SAVE ? kFragTab2 : kFragTab, NV = SAVE ? 3 : 2, QT = SAVE ? 3 : 2;
     constexpr int NTL = N / 16, KS = N / 32, TILE = Dma<N>::TILE, SWZ = Dma<N>::SWZ;
     __shared__ __attribute__((aligned(16))) bf16 K0[TILE];
     __shared__ __attribute__((aligned(16))) bf16 K1[KB == 2 ? TILE : 8];
     __shared__ __attribute__((aligned(16))) bf16 Qs[TILE];
-    __shared__ __attribute__((aligned(16))) bf16 Sf[kFragTab];  // S in three terms, then M
-    __shared__ __attribute__((aligned(16))) float Vs[2 * L];    // e^c, beta e^{c_L - c}
+    __shared__ __attribute__((aligned(16))) bf16 Sf[TABN];    // -S in three terms, then M
+    __shared__ __attribute__((aligned(16))) float Vs[NV * L];  // e^c, e^{c_L - c} (times beta), SAVE: beta
+    __shared__ float dots[SAVE ? 4 * L : 1];                   // SAVE: [wave][token] dY . Y
     const bf16* Mf = Sf + 3 * 5 * 512;
     const int tid = threadIdx.x, nw = blockDim.x >> 6, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
     const int H = a.H, G = a.G, P = a.P;
-    const int SW = 16 * CT * nw, nsl = P / SW;
+    const int SW = 16 * CT * nw, nsl = P / SW, BH = a.rows.nrows * H;
     const int sl = (int)(blockIdx.x % (unsigned)nsl), bh = (int)(blockIdx.x / (unsigned)nsl);
     const int h = bh % H, row = bh / H, g = h / (H / G);
     const int64_t Tn = a.rows.len(row), tok0 = a.rows.tok0(row);
@@ -815,22 +827,34 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
     auto fetch_k = [&](int c, bf16* kd) { dma_tile<N>(key_rsrc(a.B, c), kd, rsk, w, nw, lane); };
     auto fetch_q = [&](int c) { dma_tile<N>(key_rsrc(a.C, c), Qs, rsk, w, nw, lane); };
     auto fetch_tab = [&](int c) {
-        dma_run(make_rsrc(reinterpret_cast<const bf16*>(a.tab) + item(c) * kFragTab, kFragTab * 2),
-                reinterpret_cast<char*>(Sf), kFragTab / 512, w, nw, lane);
-        if (w == 0 && lane < 32)
-            dma_run(make_rsrc(a.vec + item(c) * kVec, 2 * L * 4), reinterpret_cast<char*>(Vs), 1, 0, 1, lane);
+        dma_run(make_rsrc(reinterpret_cast<const bf16*>(a.tab) + item(c) * TABN, TABN * 2),
+                reinterpret_cast<char*>(Sf), TABN / 512, w, nw, lane);
+        if (w == 0 && lane < NV * 16)
+            dma_run(make_rsrc(a.vec + item(c) * kVec, NV * L * 4), reinterpret_cast<char*>(Vs), 1, 0, 1, lane);
     };
     const int xo = 4 * q * rsx + (p0 + l16) * 2;  // bytes of (token 4q, column l16)
-    unsigned short xr[4][CT][4];
-    auto fetch_x = [&](int c) {
-        const brsrc r = x_rsrc(a.x, c);
+    unsigned short xr[4][CT][4], yr[4][CT][4];  // x and (SAVE) dy of the chunk
+    auto fetch_rows = [&](const void* base, int c, unsigned short(&o)[4][CT][4]) {
+        const brsrc r = x_rsrc(base, c);
 #pragma unroll
         for (int it = 0; it < 4; ++it)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct)
-                    xr[it][ct][i] = __builtin_amdgcn_raw_buffer_load_b16(r, xo + ct * 32, (it * 16 + i) * rsx, 0);
+                    o[it][ct][i] = __builtin_amdgcn_raw_buffer_load_b16(r, xo + ct * 32, (it * 16 + i) * rsx, 0);
+    };
+    auto fetch_x = [&](int c) { fetch_rows(a.x, c, xr); };
+    auto store_rows16 = [&](void* base, int c, const f32x4(&o)[4][CT]) {
+        const brsrc r = x_rsrc(base, c);
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (bf16)o[it][ct][i]), r,
+                                                          xo + ct * 32, (it * 16 + i) * rsx, 0);
     };
 
     // lane offsets (elements) of the fragment reads; further fragments differ by an exchange of
@@ -844,11 +868,32 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
         fetch_q(0);
         fetch_tab(0);
         fetch_x(0);
+        if (SAVE) fetch_rows(a.dy, 0, yr);
     }
     auto chunk = [&](int c, const bf16* Ks, bf16* Kn) {
         wave_meet(true);  // the chunk's tiles have landed
         const bool more = c + 1 < nc;
         if (KB == 2 && more) fetch_k(c + 1, Kn);
+        if (SAVE) {  // the state entering the chunk
+            const int64_t so = item(c) * P * N - (int64_t)bh * P * N;
+#pragma unroll
+            for (int t = 0; t < NTL; ++t)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    bf16x4 hi;
+                    s16x4 lo;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        bf16 hv;
+                        short lv;
+                        split_state(acc[t][ct][i], hv, lv);
+                        hi[i] = hv;
+                        lo[i] = lv;
+                    }
+                    st4(static_cast<bf16*>(a.hin) + so + hn(t, ct), hi);
+                    *reinterpret_cast<s16x4*>(a.hlo + so + hn(t, ct)) = lo;
+                }
+        }
 
         // K h^T in three terms, Q h^T in two (enough for a bfloat16 y)
         f32x4 v[4][CT], yq[4][CT];
@@ -874,7 +919,7 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) {
                         v[it][ct] = mma(v[it][ct], kf[it], hs[ct].t[k]);
-                        if (k < 2) yq[it][ct] = mma(yq[it][ct], qf[it], hs[ct].t[k]);
+                        if (k < QT) yq[it][ct] = mma(yq[it][ct], qf[it], hs[ct].t[k]);
                     }
         }
         wave_meet(false);  // every wave is done with Q
@@ -894,10 +939,26 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
                 }
         }
         if (more) fetch_x(c + 1);
+        auto operands = [&](const float* s1, const float* s2, auto nb) {  // s1_t s2_t v_t
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 2; ++t) {
+                f32x4 sa = f32x4{1.f, 1.f, 1.f, 1.f}, sb = sa;
+                if (s1) {
+                    sa = ld4(s1 + 32 * t + 4 * q);
+                    sb = ld4(s1 + 32 * t + 16 + 4 * q);
+                }
+                if (s2) {
+                    sa *= ld4(s2 + 32 * t + 4 * q);
+                    sb *= ld4(s2 + 32 * t + 16 + 4 * q);
+                }
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) split8(join(v[2 * t][ct], v[2 * t + 1][ct]), b2[t][ct]);
+                for (int ct = 0; ct < CT; ++ct)
+                    split8<decltype(nb)::value>(s1 ? join(v[2 * t][ct] * sa, v[2 * t + 1][ct] * sb)
+                                                   : join(v[2 * t][ct], v[2 * t + 1][ct]),
+                                                b2[t][ct]);
+            }
+        };
+        operands(SAVE ? Vs + 2 * L : nullptr, nullptr, std::integral_constant<int, 3>());
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -911,41 +972,48 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
                         for (int ct = 0; ct < CT; ++ct) v[it][ct] = mma(v[it][ct], sf, b2[t][ct].t[m]);
                 }
         // Y = e^c Q h^T + M beta r
+        operands(SAVE ? Vs + 2 * L : nullptr, nullptr, std::integral_constant<int, SAVE ? 3 : 2>());
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) split8<2>(join(v[2 * t][ct], v[2 * t + 1][ct]), b2[t][ct]);
+            for (int k = 0; k < (SAVE ? 3 : 1); ++k)  // term of M
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+                for (int it = 2 * t; it < 4; ++it) {
+                    const bf16x8 mf = frag_tab5(Mf + k * 5 * 512, it, t, lane);
 #pragma unroll
-            for (int it = 2 * t; it < 4; ++it) {
-                const bf16x8 mf = frag_tab5(Mf, it, t, lane);
+                    for (int m = 0; m < (SAVE ? 3 - k : 2); ++m)
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) yq[it][ct] = mma(yq[it][ct], mf, b2[t][ct].t[k]);
-            }
-        // e^{c_L - c} u as operands
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const f32x4 sa = ld4(Vs + L + 32 * t + 4 * q), sb = ld4(Vs + L + 32 * t + 16 + 4 * q);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) split8(join(v[2 * t][ct] * sa, v[2 * t + 1][ct] * sb), b2[t][ct]);
-        }
+                        for (int ct = 0; ct < CT; ++ct) yq[it][ct] = mma(yq[it][ct], mf, b2[t][ct].t[m]);
+                }
+        operands(Vs + L, SAVE ? Vs + 2 * L : nullptr, std::integral_constant<int, 3>());  // e^{c_L - c} u
         const float el = Vs[L - 1];
         wave_meet(false);  // every wave is done with the tables
         if (more) fetch_tab(c + 1);
-        {
-            const brsrc ry = x_rsrc(a.y, c);
+        if (SAVE) {
 #pragma unroll
             for (int it = 0; it < 4; ++it)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i) {
+                    float dot = 0.f;
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct)
-                        __builtin_amdgcn_raw_buffer_store_b16(
-                            __builtin_bit_cast(unsigned short, (bf16)yq[it][ct][i]), ry, xo + ct * 32,
-                            (it * 16 + i) * rsx, 0);
+                        dot += to_f(__builtin_bit_cast(bf16, yr[it][ct][i])) * yq[it][ct][i];
+#pragma unroll
+                    for (int off = 8; off > 0; off >>= 1) dot += __shfl_xor(dot, off, 64);
+                    if (l16 == 0) dots[w * L + it * 16 + 4 * q + i] = dot;
+                }
+            if (more) fetch_rows(a.dy, c + 1, yr);
+            store_rows16(a.r, c, v);
+            f32x4 rest[4][CT];
+#pragma unroll
+            for (int it = 0; it < 4; ++it)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) rest[it][ct][i] = v[it][ct][i] - (float)(bf16)v[it][ct][i];
+            store_rows16(a.rlo, c, rest);
+        } else {
+            store_rows16(a.y, c, yq);
         }
         // h' = e^{c_L} h + K^T (e^{c_L - c} u)
 #pragma unroll
@@ -967,6 +1035,14 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
             wave_meet(false);  // every wave is done with K
             fetch_k(c + 1, K0);
         }
+        if (SAVE) {
+            wave_meet(false);
+            for (int t = tid; t < rows_left(c); t += blockDim.x) {
+                float s = 0.f;
+                for (int k = 0; k < nw; ++k) s += dots[k * L + t];
+                a.dyy[((int64_t)sl * BH + bh) * a.T + (int64_t)c * L + t] = s;
+            }
+        }
     };
     if (KB == 2) {
         for (int c = 0; c < nc; c += 2) {
@@ -976,12 +1052,297 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
     } else {
         for (int c = 0; c < nc; ++c) chunk(c, K0, K0);
     }
-    if (a.hT) {
+    if (float* hT = SAVE ? a.hend : a.hT) {
 #pragma unroll
         for (int t = 0; t < NTL; ++t)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
-                st4(a.hT + hn(t, ct), acc[t][ct]);
+                st4(hT + hn(t, ct), acc[t][ct]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// k_delta_adj: the adjoint walk in the same form (chunks in reverse, dh^T in accumulators): dy
+// needs no tile, its registers are the operand; the tables' transposes are read from the
+// same fragments by transposing loads.  Outputs as k_delta_rev.
+// ---------------------------------------------------------------------------
+template <int N, int CT, int OCC>
+__global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
+    constexpr int NTL = N / 16, KS = N / 32, TILE = Dma<N>::TILE, SWZ = Dma<N>::SWZ, TABN = kFragTab2;
+    __shared__ __attribute__((aligned(16))) bf16 K0[TILE];
+    __shared__ __attribute__((aligned(16))) bf16 Qs[TILE];
+    __shared__ __attribute__((aligned(16))) bf16 Sf[TABN];
+    __shared__ __attribute__((aligned(16))) float Vs[3 * L];
+    __shared__ float dots[4 * L], tots[4];
+    const bf16* Mf = Sf + 3 * 5 * 512;
+    const int tid = threadIdx.x, nw = blockDim.x >> 6, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
+    const int H = a.H, G = a.G, P = a.P;
+    const int SW = 16 * CT * nw, nsl = P / SW, BH = a.rows.nrows * H;
+    const int sl = (int)(blockIdx.x % (unsigned)nsl), bh = (int)(blockIdx.x / (unsigned)nsl);
+    const int h = bh % H, row = bh / H, g = h / (H / G);
+    const int64_t Tn = a.rows.len(row), tok0 = a.rows.tok0(row);
+    const int nc = a.rows.nchunks(row), kb0 = a.rows.kbase(row);
+    const int p0 = sl * SW + w * 16 * CT;
+
+    f32x4 acc[NTL][CT];
+    const int64_t ho = ((int64_t)bh * P + p0 + l16) * N + 8 * q;
+    auto hn = [&](int t, int ct) { return ho + ct * 16 * N + (t >> 1) * 32 + (t & 1) * 4; };
+#pragma unroll
+    for (int t = 0; t < NTL; ++t)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+            acc[t][ct] = a.dhT ? ld4(a.dhT + hn(t, ct)) : f32x4{0.f, 0.f, 0.f, 0.f};
+
+    const int rsk = G * N * 2, rsx = H * P * 2;
+    auto rows_left = [&](int c) { return (int)min((int64_t)L, Tn - (int64_t)c * L); };
+    auto key_rsrc = [&](const void* base, int c) {
+        return make_rsrc(static_cast<const bf16*>(base) + ((tok0 + (int64_t)c * L) * G + g) * N,
+                         (uint32_t)((rows_left(c) - 1) * rsk + N * 2));
+    };
+    auto x_rsrc = [&](const void* base, int c) {
+        return make_rsrc(static_cast<const bf16*>(base) + ((tok0 + (int64_t)c * L) * H + h) * P,
+                         (uint32_t)((rows_left(c) - 1) * rsx + P * 2));
+    };
+    auto item = [&](int c) { return (int64_t)(kb0 + c) * H + h; };
+    auto fetch_k = [&](int c) { dma_tile<N>(key_rsrc(a.B, c), K0, rsk, w, nw, lane); };
+    auto fetch_q = [&](int c) { dma_tile<N>(key_rsrc(a.C, c), Qs, rsk, w, nw, lane); };
+    auto fetch_tab = [&](int c) {
+        dma_run(make_rsrc(reinterpret_cast<const bf16*>(a.tab) + item(c) * TABN, TABN * 2),
+                reinterpret_cast<char*>(Sf), TABN / 512, w, nw, lane);
+        if (w == 0 && lane < 48)
+            dma_run(make_rsrc(a.vec + item(c) * kVec, 3 * L * 4), reinterpret_cast<char*>(Vs), 1, 0, 1, lane);
+    };
+    const int xo = 4 * q * rsx + (p0 + l16) * 2;
+    unsigned short xr[4][CT][4], yr[4][CT][4];
+    auto fetch_rows = [&](const void* base, int c, unsigned short(&o)[4][CT][4]) {
+        const brsrc r = x_rsrc(base, c);
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    o[it][ct][i] = __builtin_amdgcn_raw_buffer_load_b16(r, xo + ct * 32, (it * 16 + i) * rsx, 0);
+    };
+    auto store_rows16 = [&](void* base, int c, const f32x4(&o)[4][CT]) {
+        const brsrc r = x_rsrc(base, c);
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (bf16)o[it][ct][i]), r,
+                                                          xo + ct * 32, (it * 16 + i) * rsx, 0);
+    };
+    const int ka = l16 * N + ((q ^ (l16 & SWZ)) << 3);
+    const int tr = 4 * q + (l16 >> 2);
+    const int kt = tr * N + (((l16 & 3) ^ (tr & SWZ)) << 3);
+    const int ft = (tr + 16 * (l16 & 3)) * 8;  // four columns of a block's row, in a table's fragment
+    // rows [16 j, 16 j + 16) of the table's transpose, columns 32 t on (t >= j / 2)
+    auto frag_up5 = [&](const bf16* tab, int j, int t) {
+        const s16x4 z = s16x4{0, 0, 0, 0};
+        const s16x4 lo = 2 * t >= j ? ds_tr16(tab + frag_at(2 * t, j) + ft) : z;
+        const s16x4 hi = ds_tr16(tab + frag_at(2 * t + 1, j) + ft);
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+
+    if (nc > 0) {
+        fetch_k(nc - 1);
+        fetch_q(nc - 1);
+        fetch_tab(nc - 1);
+        fetch_rows(a.x, nc - 1, xr);
+        fetch_rows(a.dy, nc - 1, yr);
+    }
+    for (int c = nc - 1; c >= 0; --c) {
+        const bool more = c > 0;
+        wave_meet(true);  // the chunk's tiles have landed
+        {  // <dh', h'> over this wave's columns, and dh' for the gradients of B
+            const bool last = c + 1 == nc;
+            const int64_t so = (last ? 0 : item(c + 1) * P * N - (int64_t)bh * P * N), lo = (item(c) - bh) * P * N;
+            float s = 0.f;
+#pragma unroll
+            for (int t = 0; t < NTL; ++t)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    f32x4 hv;
+                    if (last) {
+                        hv = ld4(a.hend + hn(t, ct));
+                    } else {
+                        const bf16x4 hi = ld4(static_cast<const bf16*>(a.hin) + so + hn(t, ct));
+                        const s16x4 hl = *reinterpret_cast<const s16x4*>(a.hlo + so + hn(t, ct));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) hv[i] = join_state(hi[i], hl[i]);
+                    }
+                    bf16x4 o;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        s += hv[i] * acc[t][ct][i];
+                        o[i] = (bf16)acc[t][ct][i];
+                    }
+                    st4(static_cast<bf16*>(a.lin) + lo + hn(t, ct), o);
+                }
+#pragma unroll
+            for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
+            if (lane == 0) tots[w] = s;
+        }
+        // dU = e^{c_L - c} K dh'^T + M^T dY
+        f32x4 v[4][CT];
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) v[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            Sp<bf16> hs[CT];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) split8(join(acc[2 * ks][ct], acc[2 * ks + 1][ct]), hs[ct]);
+            bf16x8 kf[4];
+#pragma unroll
+            for (int it = 0; it < 4; ++it) kf[it] = ld8(K0 + (ka ^ (ks << 5)) + it * 16 * N);
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (int it = 0; it < 4; ++it)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) v[it][ct] = mma(v[it][ct], kf[it], hs[ct].t[k]);
+        }
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const f32x4 ew = ld4(Vs + L + it * 16 + 4 * q);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) v[it][ct] *= ew;
+        }
+        bf16x8 dyf[2][CT];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    dyf[t][ct][i] = __builtin_bit_cast(bf16, yr[2 * t + (i >> 2)][ct][i & 3]);
+        if (more) fetch_rows(a.dy, c - 1, yr);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (int it = 0; it <= 2 * t + 1; ++it) {
+                    const bf16x8 mf = frag_up5(Mf + k * 5 * 512, it, t);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) v[it][ct] = mma(v[it][ct], mf, dyf[t][ct]);
+                }
+        // z = dU - S^T (beta dU)
+        Sp<bf16> b2[2][CT];
+        auto operands = [&](const float* s1, float sign) {  // sign s1_t v_t
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const f32x4 sa = ld4(s1 + 32 * t + 4 * q) * sign, sb = ld4(s1 + 32 * t + 16 + 4 * q) * sign;
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) split8(join(v[2 * t][ct] * sa, v[2 * t + 1][ct] * sb), b2[t][ct]);
+            }
+        };
+        operands(Vs + 2 * L, 1.f);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (int it = 0; it <= 2 * t + 1; ++it) {
+                    const bf16x8 sf = frag_up5(Sf + k * 5 * 512, it, t);
+#pragma unroll
+                    for (int m = 0; m < 3 - k; ++m)
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) v[it][ct] = mma(v[it][ct], sf, b2[t][ct].t[m]);
+                }
+        // z leaves in two terms, dX = beta z, its dot with X
+        store_rows16(a.z, c, v);
+        {
+            f32x4 rest[4][CT];
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const f32x4 bt = ld4(Vs + 2 * L + it * 16 + 4 * q);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) rest[it][ct][i] = v[it][ct][i] - (float)(bf16)v[it][ct][i];
+                    v[it][ct] *= bt;
+                }
+            }
+            store_rows16(a.zlo, c, rest);
+        }
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float dot = 0.f;
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    dot += to_f(__builtin_bit_cast(bf16, xr[it][ct][i])) * v[it][ct][i];
+#pragma unroll
+                for (int off = 8; off > 0; off >>= 1) dot += __shfl_xor(dot, off, 64);
+                if (l16 == 0) dots[w * L + it * 16 + 4 * q + i] = dot;
+            }
+        if (more) fetch_rows(a.x, c - 1, xr);
+        store_rows16(a.dx, c, v);
+        // dh = e^{c_L} dh' - K^T (e^c dX) + Q^T (e^c dY)
+        operands(Vs, -1.f);
+        const float el = Vs[L - 1];
+        Sp<bf16> d2[2][CT];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const f32x4 sa = ld4(Vs + 32 * t + 4 * q), sb = ld4(Vs + 32 * t + 16 + 4 * q);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                f32x8 d;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i] = to_f(dyf[t][ct][i]) * (i < 4 ? sa[i & 3] : sb[i & 3]);
+                split8(d, d2[t][ct]);
+            }
+        }
+        wave_meet(false);  // every wave is done with the tables; the sums are in place
+        if (more) fetch_tab(c - 1);
+        for (int t = tid; t < rows_left(c); t += blockDim.x) {
+            float s = 0.f;
+            for (int k = 0; k < nw; ++k) s += dots[k * L + t];
+            a.dxx[((int64_t)sl * BH + bh) * a.T + (int64_t)c * L + t] = s;
+        }
+        if (tid == 0) {
+            float s = 0.f;
+            for (int k = 0; k < nw; ++k) s += tots[k];
+            a.tot[(int64_t)sl * a.ntab * H + item(c)] = s;
+        }
+#pragma unroll
+        for (int t = 0; t < NTL; ++t) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) acc[t][ct] *= el;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const int o = (kt ^ ((t >> 1) << 5)) + 4 * (t & 1) + ks * 32 * N;
+                const bf16x8 kf = __builtin_bit_cast(
+                    bf16x8, __builtin_shufflevector(ds_tr16(K0 + o), ds_tr16(K0 + o + 16 * N), 0, 1, 2, 3, 4, 5, 6, 7));
+                const bf16x8 qf = __builtin_bit_cast(
+                    bf16x8, __builtin_shufflevector(ds_tr16(Qs + o), ds_tr16(Qs + o + 16 * N), 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+                        acc[t][ct] = mma(acc[t][ct], kf, b2[ks][ct].t[k]);
+                        acc[t][ct] = mma(acc[t][ct], qf, d2[ks][ct].t[k]);
+                    }
+            }
+        }
+        if (more) {
+            wave_meet(false);  // every wave is done with K and Q
+            fetch_k(c - 1);
+            fetch_q(c - 1);
+        }
+    }
+    if (a.dh0) {
+#pragma unroll
+        for (int t = 0; t < NTL; ++t)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) st4(a.dh0 + hn(t, ct), acc[t][ct]);
     }
 }
 
@@ -1174,6 +1535,9 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a) {
                     dot += dxv * to_f(Xs[o]);
                     Xs[o] = from_f<T>(dxv);
                     Ys[o] = from_f<T>(v[it][ct][i]);
+                    if (NT > 1 && t < n)
+                        static_cast<T*>(a.zlo)[((t0 + t) * H + h) * P + p0 + pw + ct * 16 + l16] =
+                            from_f<T>(v[it][ct][i] - to_f(Ys[o]));
                     v[it][ct][i] = dxv;
                 }
 #pragma unroll
@@ -1250,8 +1614,8 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a) {
 // of the group's heads in registers (and dbeta, by the first slab).  Wave w owns token tile
 // w as the COLUMNS of dQ^T[n][i] and dK^T[n][i], so the 64 x 64 gradient tables it needs,
 // dP^T and the two sides of W, come out of the matrix cores in the layout their products
-// read.  Everything here ends in the problem dtype: one bfloat16 term per operand, but two
-// for the tables, which the products above form in float32.
+// read.  Everything here ends in the problem dtype: the states enter with one bfloat16
+// term, r, z and the tables with two, so that every product has one rounded factor at most.
 // ---------------------------------------------------------------------------
 template <typename T, int N>
 struct GradCfg {
@@ -1313,15 +1677,16 @@ __global__ __launch_bounds__(256) void k_delta_grad(Args a) {
             bts[tid] = tid < n ? to_f(static_cast<const T*>(a.beta)[(t0 + tid) * H + h]) : 0.f;
         }
         __syncthreads();
-        const T* Yg = static_cast<const T*>(a.dy) + (t0 * H + h) * P;
-        const T* Rg = static_cast<const T*>(a.r) + (t0 * H + h) * P;
-        const T* Zg = static_cast<const T*>(a.z) + (t0 * H + h) * P;
-        const int64_t rs = (int64_t)H * P;
-        auto rowf = [&](const T* base, int tile, int ks) {  // row fragment, zero past n and P
+        const int64_t r0 = (t0 * H + h) * P, rs = (int64_t)H * P;
+        auto rowf = [&](const void* base, int tile, int ks) {  // row fragment, zero past n and P
             const int t = tile * 16 + l16, col = ks * 32 + 8 * q;
             const bool in = t < n && col < P;
-            return sel8(in, ld8(base + (t < n ? t : 0) * rs + (col < P ? col : 0)));
+            return sel8(in, ld8(static_cast<const T*>(base) + r0 + (t < n ? t : 0) * rs + (col < P ? col : 0)));
         };
+        // r and z in two terms (the gradients of B would lose half of their rounding's room to
+        // one): the product with a tensor that has one term, and of the two
+        constexpr bool TWO = kTerms<T> > 1;
+        typedef typename V8<T>::type F8;
         // tables: pt = dP_{ij} (rows j), wt = W_{ij} (rows j) for j <= i; pc = dP_{ai},
         // wc = W_{ai} (rows a) for a >= i
         f32x4 pt[4], wt[4], pc[4], wc[4];
@@ -1331,17 +1696,34 @@ __global__ __launch_bounds__(256) void k_delta_grad(Args a) {
 #pragma unroll
         for (int t = 0; t < NTL; ++t) th[t] = tz[t] = tl[t] = f32x4{0.f, 0.f, 0.f, 0.f};
         for (int ks = 0; ks < PP / 32; ++ks) {
-            const auto yi = rowf(Yg, w, ks), ri = rowf(Rg, w, ks), zi = rowf(Zg, w, ks);
+            const F8 yi = rowf(a.dy, w, ks), ri = rowf(a.r, w, ks), zi = rowf(a.z, w, ks);
+            F8 rl = ri, zl = zi;
+            if (TWO) {
+                rl = rowf(a.rlo, w, ks);
+                zl = rowf(a.zlo, w, ks);
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (j <= w) {
-                    const auto rj = j == w ? ri : rowf(Rg, j, ks);
+                    const F8 rj = j == w ? ri : rowf(a.r, j, ks);
                     pt[j] = mma(pt[j], rj, yi);
                     wt[j] = mma(wt[j], rj, zi);
+                    if (TWO) {
+                        const F8 rk = j == w ? rl : rowf(a.rlo, j, ks);
+                        pt[j] = mma(pt[j], rk, yi);
+                        wt[j] = mma(wt[j], rk, zi);
+                        wt[j] = mma(wt[j], rj, zl);
+                    }
                 }
                 if (j >= w) {
-                    pc[j] = mma(pc[j], j == w ? yi : rowf(Yg, j, ks), ri);
-                    wc[j] = mma(wc[j], j == w ? zi : rowf(Zg, j, ks), ri);
+                    const F8 yj = j == w ? yi : rowf(a.dy, j, ks), zj = j == w ? zi : rowf(a.z, j, ks);
+                    pc[j] = mma(pc[j], yj, ri);
+                    wc[j] = mma(wc[j], zj, ri);
+                    if (TWO) {
+                        pc[j] = mma(pc[j], yj, rl);
+                        wc[j] = mma(wc[j], zj, rl);
+                        wc[j] = mma(wc[j], j == w ? zl : rowf(a.zlo, j, ks), ri);
+                    }
                 }
             }
 #pragma unroll
@@ -1351,6 +1733,10 @@ __global__ __launch_bounds__(256) void k_delta_grad(Args a) {
                 th[t] = mma(th[t], hf, yi);
                 tz[t] = mma(tz[t], hf, zi);
                 tl[t] = mma(tl[t], lf, ri);
+                if (TWO) {
+                    tz[t] = mma(tz[t], hf, zl);
+                    tl[t] = mma(tl[t], lf, rl);
+                }
             }
         }
         const float bi = bts[i], ci = chi[i], di = clo[i];

@@ -36,7 +36,7 @@ int check_delta(const ssd_problem* p, bool packed) {
 // backward also the residuals, the adjoint's z, the entering states and adjoints of every
 // chunk, the last state and the partial sums.
 struct Layout {
-    size_t tab, vec, ts, kb, r, z, hin, hlo, lin, hend, dyy, dxx, tot, dAp, part, total;
+    size_t tab, vec, ts, kb, r, rlo, z, zlo, hin, hlo, lin, hend, dyy, dxx, tot, dAp, part, total;
     int64_t ntab, slices, nsub;
 };
 
@@ -52,7 +52,8 @@ Layout layout_of(const ssd_problem* p, bool packed, bool bwd) {
         at = off;
         off += align_up(bytes);
     };
-    const size_t frag = ssd::delta::dma_walk(p->dtype == SSD_BF16, N) && !bwd ? ssd::delta::kFragTab * 2 : 0;
+    const size_t frag = !ssd::delta::dma_walk(p->dtype == SSD_BF16, N) ? 0
+                        : bwd ? ssd::delta::kFragTab2 * 2 : ssd::delta::kFragTab * 2;
     take(o.tab, (size_t)(o.ntab * H) * (frag ? frag : kTab * 4));
     take(o.vec, (size_t)(o.ntab * H) * kVec * 4);
     if (packed) {
@@ -60,11 +61,14 @@ Layout layout_of(const ssd_problem* p, bool packed, bool bwd) {
         take(o.kb, (size_t)(b + 1) * 4);
     }
     if (bwd) {
-        const ssd::delta::Slice s = ssd::delta::slice_of(p->dtype == SSD_BF16, b * H, P, N);
-        o.slices = P / s.cols();
+        o.slices = ssd::delta::bwd_slices(p->dtype == SSD_BF16, b * H, P, N);
         o.nsub = ssd::delta::grad_shares(o.ntab, H, G, N);
         take(o.r, (size_t)(b * T * H * P) * es);
         take(o.z, (size_t)(b * T * H * P) * es);
+        if (es == 2) {
+            take(o.rlo, (size_t)(b * T * H * P) * es);
+            take(o.zlo, (size_t)(b * T * H * P) * es);
+        }
         take(o.hin, (size_t)(o.ntab * H * P * N) * es);
         if (es == 2) take(o.hlo, (size_t)(o.ntab * H * P * N) * 2);
         take(o.lin, (size_t)(o.ntab * H * P * N) * es);
@@ -208,7 +212,9 @@ int delta_bwd(const ssd_problem* p, const void* x, const float* dt, const float*
     a.x = x; a.dt = dt; a.A = A; a.B = B; a.C = C; a.beta = beta; a.h0 = h0; a.dy = dy; a.dhT = dhT;
     a.dx = dx; a.ddt = ddt; a.dA = dA; a.dB = dB; a.dC = dC; a.dbeta = dbeta; a.dh0 = dh0;
     a.r = w + o.r;
+    a.rlo = w + o.rlo;
     a.z = w + o.z;
+    a.zlo = w + o.zlo;
     a.hin = w + o.hin;
     a.lin = w + o.lin;
     a.hlo = reinterpret_cast<short*>(w + o.hlo);

@@ -30,6 +30,13 @@ inline int grad_shares(int64_t chunks, int64_t H, int64_t G, int64_t N) {
     return (int)(s < 1 ? 1 : s > hg ? hg : s);
 }
 
+inline bool dma_walk(bool bf16_dtype, int64_t N);
+inline int adj_waves(int64_t P);
+// Slices of headdim that the backward's walks write partial sums for.
+inline int64_t bwd_slices(bool bf16_dtype, int64_t bh, int64_t P, int64_t N) {
+    return P / (dma_walk(bf16_dtype, N) ? 16 * adj_waves(P) : slice_of(bf16_dtype, bh, P, N).cols());
+}
+
 template <typename K>
 bool lds_limit(K* kernel, size_t bytes) {
     return bytes <= 64 * 1024 || hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
@@ -75,24 +82,36 @@ inline int prep_heads(int64_t ntab, int64_t H, int64_t G) {
     while (s > 1 && (s > H / G || ntab * G * ((H / G + s - 1) / s) < 8192)) s >>= 1;
     return s;
 }
-template <typename T, int N, bool FRAG>
+template <typename T, int N, Tab TAB>
 void prep(const Args& a) {
     const int heads = prep_heads(a.ntab, a.H, a.G);
     const int64_t waves = (int64_t)a.ntab * a.G * ((a.H / a.G + heads - 1) / heads);
-    k_delta_prep<T, N, FRAG><<<(unsigned)((waves + 3) / 4), 256, 0, a.stream>>>(a, heads);
+    k_delta_prep<T, N, TAB><<<(unsigned)((waves + 3) / 4), 256, 0, a.stream>>>(a, heads);
 }
 
-template <int N, int CT, int KB, int OCC>
+template <int N, int CT, int KB, int OCC, bool SAVE = false>
 int walk_dma(const Args& a, int waves) {
     const unsigned grid = (unsigned)((int64_t)a.rows.nrows * a.H * (a.P / (16 * CT * waves)));
-    k_delta_dma<N, CT, KB, OCC><<<grid, 64 * waves, 0, a.stream>>>(a);
+    k_delta_dma<N, CT, KB, OCC, SAVE><<<grid, 64 * waves, 0, a.stream>>>(a);
+    return hipGetLastError() == hipSuccess ? 0 : 7;
+}
+// The backward's two walks: four waves of one column tile.
+inline int adj_waves(int64_t P) { return P >= 64 ? 4 : (int)(P / 16); }
+template <int N>
+int walks_bwd(const Args& a) {
+    const int waves = adj_waves(a.P);
+    const unsigned grid = (unsigned)((int64_t)a.rows.nrows * a.H * (a.P / (16 * waves)));
+    constexpr int OCC = N == 256 ? 1 : 2;
+    const int st = walk_dma<N, 1, 1, OCC, true>(a, waves);
+    if (st) return st;
+    k_delta_adj<N, 1, OCC><<<grid, 64 * waves, 0, a.stream>>>(a);
     return hipGetLastError() == hipSuccess ? 0 : 7;
 }
 
 template <typename T, int N>
 int run_fwd(const Args& a) {
     if constexpr (std::is_same<T, bf16>::value && N >= 64) {
-        prep<T, N, true>(a);
+        prep<T, N, kFold>(a);
         const int waves = a.P >= 64 ? 4 : a.P / 16;
         if constexpr (N <= 128) {
             if (a.P == 128) return walk_dma<N, 2, 2, 2>(a, 4);
@@ -104,7 +123,7 @@ int run_fwd(const Args& a) {
         }
     } else {
         const Slice s = slice_of(std::is_same<T, bf16>::value, (int64_t)a.rows.nrows * a.H, a.P, N);
-        prep<T, N, false>(a);
+        prep<T, N, kPlain>(a);
         return walk_n<T, N>(a, s, 0);
     }
 }
@@ -112,10 +131,16 @@ int run_fwd(const Args& a) {
 template <typename T, int N>
 int run_bwd(const Args& a) {
     typedef GradCfg<T, N> GC;
-    const Slice s = slice_of(std::is_same<T, bf16>::value, (int64_t)a.rows.nrows * a.H, a.P, N);
-    prep<T, N, false>(a);
-    int st = walk_n<T, N>(a, s, 1);
-    if (!st) st = walk_n<T, N>(a, s, 2);
+    int st;
+    if constexpr (std::is_same<T, bf16>::value && N >= 64) {
+        prep<T, N, kBoth>(a);
+        st = walks_bwd<N>(a);
+    } else {
+        const Slice s = slice_of(std::is_same<T, bf16>::value, (int64_t)a.rows.nrows * a.H, a.P, N);
+        prep<T, N, kPlain>(a);
+        st = walk_n<T, N>(a, s, 1);
+        if (!st) st = walk_n<T, N>(a, s, 2);
+    }
     if (st) return st;
     const size_t lds = GC::bytes(a.P);
     if (!lds_limit(k_delta_grad<T, N>, lds)) return 7;
