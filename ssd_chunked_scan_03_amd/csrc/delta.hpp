@@ -1069,8 +1069,11 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
 template <int N, int CT, int OCC>
 __global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
     constexpr int NTL = N / 16, KS = N / 32, TILE = Dma<N>::TILE, SWZ = Dma<N>::SWZ, TABN = kFragTab2;
+    constexpr bool TWO = N <= 128;  // two buffers for K and Q
     __shared__ __attribute__((aligned(16))) bf16 K0[TILE];
-    __shared__ __attribute__((aligned(16))) bf16 Qs[TILE];
+    __shared__ __attribute__((aligned(16))) bf16 Q0[TILE];
+    __shared__ __attribute__((aligned(16))) bf16 K1[TWO ? TILE : 8];
+    __shared__ __attribute__((aligned(16))) bf16 Q1[TWO ? TILE : 8];
     __shared__ __attribute__((aligned(16))) bf16 Sf[TABN];
     __shared__ __attribute__((aligned(16))) float Vs[3 * L];
     __shared__ float dots[4 * L], tots[4];
@@ -1104,8 +1107,10 @@ __global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
                          (uint32_t)((rows_left(c) - 1) * rsx + P * 2));
     };
     auto item = [&](int c) { return (int64_t)(kb0 + c) * H + h; };
-    auto fetch_k = [&](int c) { dma_tile<N>(key_rsrc(a.B, c), K0, rsk, w, nw, lane); };
-    auto fetch_q = [&](int c) { dma_tile<N>(key_rsrc(a.C, c), Qs, rsk, w, nw, lane); };
+    auto fetch_kq = [&](int c, bf16* kd, bf16* qd) {
+        dma_tile<N>(key_rsrc(a.B, c), kd, rsk, w, nw, lane);
+        dma_tile<N>(key_rsrc(a.C, c), qd, rsk, w, nw, lane);
+    };
     auto fetch_tab = [&](int c) {
         dma_run(make_rsrc(reinterpret_cast<const bf16*>(a.tab) + item(c) * TABN, TABN * 2),
                 reinterpret_cast<char*>(Sf), TABN / 512, w, nw, lane);
@@ -1148,43 +1153,27 @@ __global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
     };
 
     if (nc > 0) {
-        fetch_k(nc - 1);
-        fetch_q(nc - 1);
+        fetch_kq(nc - 1, K0, Q0);
         fetch_tab(nc - 1);
         fetch_rows(a.x, nc - 1, xr);
         fetch_rows(a.dy, nc - 1, yr);
     }
-    for (int c = nc - 1; c >= 0; --c) {
-        const bool more = c > 0;
+    auto chunk = [&](int c, const bf16* Ks, const bf16* Qs, bf16* Kn, bf16* Qn) {
+        const bool more = c > 0, last = c + 1 == nc;
         wave_meet(true);  // the chunk's tiles have landed
-        {  // <dh', h'> over this wave's columns, and dh' for the gradients of B
-            const bool last = c + 1 == nc;
-            const int64_t so = (last ? 0 : item(c + 1) * P * N - (int64_t)bh * P * N), lo = (item(c) - bh) * P * N;
-            float s = 0.f;
+        if (TWO && more) fetch_kq(c - 1, Kn, Qn);
+        // h' (the state entering the next chunk), consumed once the first products are under way
+        bf16x4 hi[NTL][CT];
+        s16x4 hl[NTL][CT];
+        if (!last) {
+            const int64_t so = (item(c + 1) - bh) * P * N;
 #pragma unroll
             for (int t = 0; t < NTL; ++t)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-                    f32x4 hv;
-                    if (last) {
-                        hv = ld4(a.hend + hn(t, ct));
-                    } else {
-                        const bf16x4 hi = ld4(static_cast<const bf16*>(a.hin) + so + hn(t, ct));
-                        const s16x4 hl = *reinterpret_cast<const s16x4*>(a.hlo + so + hn(t, ct));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) hv[i] = join_state(hi[i], hl[i]);
-                    }
-                    bf16x4 o;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        s += hv[i] * acc[t][ct][i];
-                        o[i] = (bf16)acc[t][ct][i];
-                    }
-                    st4(static_cast<bf16*>(a.lin) + lo + hn(t, ct), o);
+                    hi[t][ct] = ld4(static_cast<const bf16*>(a.hin) + so + hn(t, ct));
+                    hl[t][ct] = *reinterpret_cast<const s16x4*>(a.hlo + so + hn(t, ct));
                 }
-#pragma unroll
-            for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
-            if (lane == 0) tots[w] = s;
         }
         // dU = e^{c_L - c} K dh'^T + M^T dY
         f32x4 v[4][CT];
@@ -1199,7 +1188,7 @@ __global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
             for (int ct = 0; ct < CT; ++ct) split8(join(acc[2 * ks][ct], acc[2 * ks + 1][ct]), hs[ct]);
             bf16x8 kf[4];
 #pragma unroll
-            for (int it = 0; it < 4; ++it) kf[it] = ld8(K0 + (ka ^ (ks << 5)) + it * 16 * N);
+            for (int it = 0; it < 4; ++it) kf[it] = ld8(Ks + (ka ^ (ks << 5)) + it * 16 * N);
 #pragma unroll
             for (int k = 0; k < 3; ++k)
 #pragma unroll
@@ -1232,6 +1221,32 @@ __global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) v[it][ct] = mma(v[it][ct], mf, dyf[t][ct]);
                 }
+        {  // <dh', h'> over this wave's columns, and dh' for the gradients of B
+            const int64_t lo = (item(c) - bh) * P * N;
+            float s = 0.f;
+#pragma unroll
+            for (int t = 0; t < NTL; ++t)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    f32x4 hv;
+                    if (last) {
+                        hv = ld4(a.hend + hn(t, ct));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) hv[i] = join_state(hi[t][ct][i], hl[t][ct][i]);
+                    }
+                    bf16x4 o;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        s += hv[i] * acc[t][ct][i];
+                        o[i] = (bf16)acc[t][ct][i];
+                    }
+                    st4(static_cast<bf16*>(a.lin) + lo + hn(t, ct), o);
+                }
+#pragma unroll
+            for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
+            if (lane == 0) tots[w] = s;
+        }
         // z = dU - S^T (beta dU)
         Sp<bf16> b2[2][CT];
         auto operands = [&](const float* s1, float sign) {  // sign s1_t v_t
@@ -1320,7 +1335,7 @@ __global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
             for (int ks = 0; ks < 2; ++ks) {
                 const int o = (kt ^ ((t >> 1) << 5)) + 4 * (t & 1) + ks * 32 * N;
                 const bf16x8 kf = __builtin_bit_cast(
-                    bf16x8, __builtin_shufflevector(ds_tr16(K0 + o), ds_tr16(K0 + o + 16 * N), 0, 1, 2, 3, 4, 5, 6, 7));
+                    bf16x8, __builtin_shufflevector(ds_tr16(Ks + o), ds_tr16(Ks + o + 16 * N), 0, 1, 2, 3, 4, 5, 6, 7));
                 const bf16x8 qf = __builtin_bit_cast(
                     bf16x8, __builtin_shufflevector(ds_tr16(Qs + o), ds_tr16(Qs + o + 16 * N), 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
@@ -1332,10 +1347,18 @@ __global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
                     }
             }
         }
-        if (more) {
+        if (!TWO && more) {
             wave_meet(false);  // every wave is done with K and Q
-            fetch_k(c - 1);
-            fetch_q(c - 1);
+            fetch_kq(c - 1, Kn, Qn);
+        }
+    };
+    for (int c = nc - 1; c >= 0; c -= 2) {
+        if (TWO) {
+            chunk(c, K0, Q0, K1, Q1);
+            if (c > 0) chunk(c - 1, K1, Q1, K0, Q0);
+        } else {
+            chunk(c, K0, Q0, K0, Q0);
+            if (c > 0) chunk(c - 1, K0, Q0, K0, Q0);
         }
     }
     if (a.dh0) {
@@ -1628,7 +1651,7 @@ struct GradCfg {
 };
 
 template <typename T, int N>
-__global__ __launch_bounds__(256) void k_delta_grad(Args a) {
+__global__ __launch_bounds__(256, 2) void k_delta_grad(Args a) {
     typedef GradCfg<T, N> CF;
     constexpr int NS = CF::NS, LDN = CF::LDN, NTL = NS / 16, SLABS = N / NS;
     extern __shared__ __attribute__((aligned(16))) char smem[];

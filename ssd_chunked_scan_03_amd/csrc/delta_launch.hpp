@@ -102,7 +102,7 @@ int walks_bwd(const Args& a) {
     const int waves = adj_waves(a.P);
     const unsigned grid = (unsigned)((int64_t)a.rows.nrows * a.H * (a.P / (16 * waves)));
     constexpr int OCC = N == 256 ? 1 : 2;
-    const int st = walk_dma<N, 1, 1, OCC, true>(a, waves);
+    const int st = walk_dma<N, 1, 2, OCC, true>(a, waves);
     if (st) return st;
     k_delta_adj<N, 1, OCC><<<grid, 64 * waves, 0, a.stream>>>(a);
     return hipGetLastError() == hipSuccess ? 0 : 7;
