@@ -110,17 +110,22 @@ template <> struct Sp<bf16> { bf16x8 t[3]; };
 template <> struct Sp<float> { f32x8 t[1]; };
 template <typename T> constexpr int kTerms = std::is_same<T, bf16>::value ? 3 : 1;
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+// two bfloat16, rounded to nearest, in one instruction
+__device__ __forceinline__ unsigned cvt2(float a, float b) {
+    return __builtin_bit_cast(unsigned, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
 template <int NB = 3>
 __device__ __forceinline__ void split8(f32x8 v, Sp<bf16>& s) {
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     u32x4v o[3];
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
         float a = v[e], b = v[e + 1];
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const unsigned u = __builtin_bit_cast(unsigned, __builtin_convertvector(f32x2{a, b}, bf16x2));
+            const unsigned u = cvt2(a, b);
             o[k][e >> 1] = u;
             if (k + 1 < NB) {
                 a -= __builtin_bit_cast(float, u << 16);
@@ -158,17 +163,37 @@ __device__ __forceinline__ f32x4 mma16(f32x4 c, f32x4 a, f32x4 b) {
     return c;
 }
 
-// A float32 state as a bfloat16 (rounded to nearest) and the 16-bit rest of its bit pattern:
-// the gradient products read the first alone, the decay gradient's <dh', h'> both, exactly.
-__device__ __forceinline__ void split_state(float v, bf16& hi, short& lo) {
-    const unsigned b = __builtin_bit_cast(unsigned, v);
-    const bool fin = (b & 0x7f800000u) != 0x7f800000u;
-    const unsigned t = fin ? b + 0x8000u : b | ((b & 0xffffu) ? 0x400000u : 0u);
-    hi = __builtin_bit_cast(bf16, (unsigned short)(t >> 16));
-    lo = fin ? (short)(b - (t & 0xffff0000u)) : (short)0;
+// A float32 state as a bfloat16 (rounded to nearest) and 16 bits of what that left of its bit
+// pattern, halved to fit: the gradient products read the first alone, the decay gradient's
+// <dh', h'> both, good to 2^-23.
+__device__ __forceinline__ void split_state(f32x8 v, bf16x8& hi, s16x8& lo) {
+    u32x4v h, l;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        const unsigned u = cvt2(v[e], v[e + 1]);
+        const int a = __builtin_bit_cast(int, (float)v[e]) - (int)(u << 16);
+        const int b = __builtin_bit_cast(int, (float)v[e + 1]) - (int)(u & 0xffff0000u);
+        h[e >> 1] = u;
+        l[e >> 1] = ((unsigned)(a >> 1) & 0xffffu) | ((unsigned)(b >> 1) << 16);
+    }
+    hi = __builtin_bit_cast(bf16x8, h);
+    lo = __builtin_bit_cast(s16x8, l);
 }
 __device__ __forceinline__ float join_state(bf16 hi, short lo) {
-    return __builtin_bit_cast(float, ((unsigned)__builtin_bit_cast(unsigned short, hi) << 16) + (unsigned)(int)lo);
+    return __builtin_bit_cast(float, ((unsigned)__builtin_bit_cast(unsigned short, hi) << 16) + ((unsigned)(int)lo << 1));
+}
+
+// Sum over the 16 lanes of a row, in every lane: lane rotations in the ALU (a shuffle is an LDS
+// round trip, and a walk's 64 of them in a row cost more than its products).
+__device__ __forceinline__ float row_sum16(float v) {
+    auto turn = [](float x, auto by) {
+        const int i = __builtin_bit_cast(int, x);
+        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, 0x120 + decltype(by)::value, 0xf, 0xf, false));
+    };
+    v += turn(v, std::integral_constant<int, 8>());
+    v += turn(v, std::integral_constant<int, 4>());
+    v += turn(v, std::integral_constant<int, 2>());
+    return v + turn(v, std::integral_constant<int, 1>());
 }
 
 __device__ __forceinline__ f32x8 join(f32x4 a, f32x4 b) {
@@ -570,18 +595,11 @@ __global__ __launch_bounds__(256) void k_delta(Args a) {
                 for (int ct = 0; ct < CT; ++ct) {
                     const int64_t o = ho + (ct * 16 + l16) * N + t * 16 + 4 * q;
                     if constexpr (std::is_same<T, bf16>::value) {
-                        bf16x4 hi;
-                        s16x4 lo;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            bf16 hv;
-                            short lv;
-                            split_state(acc[t][ct][i], hv, lv);
-                            hi[i] = hv;
-                            lo[i] = lv;
-                        }
-                        st4(static_cast<T*>(a.hin) + o, hi);
-                        *reinterpret_cast<s16x4*>(a.hlo + o) = lo;
+                        bf16x8 hi;
+                        s16x8 lo;
+                        split_state(join(acc[t][ct], acc[t][ct]), hi, lo);
+                        st4(static_cast<T*>(a.hin) + o, __builtin_shufflevector(hi, hi, 0, 1, 2, 3));
+                        *reinterpret_cast<s16x4*>(a.hlo + o) = __builtin_shufflevector(lo, lo, 0, 1, 2, 3);
                     } else {
                         st4(static_cast<T*>(a.hin) + o, acc[t][ct]);
                     }
@@ -711,8 +729,7 @@ __global__ __launch_bounds__(256) void k_delta(Args a) {
                     }
                 }
                 if (SAVE) {
-#pragma unroll
-                    for (int off = 8; off > 0; off >>= 1) dot += __shfl_xor(dot, off, 64);
+                    dot = row_sum16(dot);
                     if (l16 == 0) dots[w * L + t] = dot;
                 }
             }
@@ -877,21 +894,14 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
         if (SAVE) {  // the state entering the chunk
             const int64_t so = item(c) * P * N - (int64_t)bh * P * N;
 #pragma unroll
-            for (int t = 0; t < NTL; ++t)
+            for (int t = 0; t < NTL; t += 2)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-                    bf16x4 hi;
-                    s16x4 lo;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        bf16 hv;
-                        short lv;
-                        split_state(acc[t][ct][i], hv, lv);
-                        hi[i] = hv;
-                        lo[i] = lv;
-                    }
-                    st4(static_cast<bf16*>(a.hin) + so + hn(t, ct), hi);
-                    *reinterpret_cast<s16x4*>(a.hlo + so + hn(t, ct)) = lo;
+                    bf16x8 hi;
+                    s16x8 lo;
+                    split_state(join(acc[t][ct], acc[t + 1][ct]), hi, lo);
+                    st8(static_cast<bf16*>(a.hin) + so + hn(t, ct), hi);
+                    *reinterpret_cast<s16x8*>(a.hlo + so + hn(t, ct)) = lo;
                 }
         }
 
@@ -998,8 +1008,7 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct)
                         dot += to_f(__builtin_bit_cast(bf16, yr[it][ct][i])) * yq[it][ct][i];
-#pragma unroll
-                    for (int off = 8; off > 0; off >>= 1) dot += __shfl_xor(dot, off, 64);
+                    dot = row_sum16(dot);
                     if (l16 == 0) dots[w * L + it * 16 + 4 * q + i] = dot;
                 }
             if (more) fetch_rows(a.dy, c + 1, yr);
@@ -1163,16 +1172,16 @@ __global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
         wave_meet(true);  // the chunk's tiles have landed
         if (TWO && more) fetch_kq(c - 1, Kn, Qn);
         // h' (the state entering the next chunk), consumed once the first products are under way
-        bf16x4 hi[NTL][CT];
-        s16x4 hl[NTL][CT];
+        bf16x8 hi[KS][CT];
+        s16x8 hl[KS][CT];
         if (!last) {
             const int64_t so = (item(c + 1) - bh) * P * N;
 #pragma unroll
-            for (int t = 0; t < NTL; ++t)
+            for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-                    hi[t][ct] = ld4(static_cast<const bf16*>(a.hin) + so + hn(t, ct));
-                    hl[t][ct] = *reinterpret_cast<const s16x4*>(a.hlo + so + hn(t, ct));
+                    hi[ks][ct] = ld8(static_cast<const bf16*>(a.hin) + so + hn(2 * ks, ct));
+                    hl[ks][ct] = *reinterpret_cast<const s16x8*>(a.hlo + so + hn(2 * ks, ct));
                 }
         }
         // dU = e^{c_L - c} K dh'^T + M^T dY
@@ -1225,23 +1234,22 @@ __global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
             const int64_t lo = (item(c) - bh) * P * N;
             float s = 0.f;
 #pragma unroll
-            for (int t = 0; t < NTL; ++t)
+            for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-                    f32x4 hv;
+                    f32x8 hv;
                     if (last) {
-                        hv = ld4(a.hend + hn(t, ct));
+                        hv = ld8(a.hend + hn(2 * ks, ct));
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) hv[i] = join_state(hi[t][ct][i], hl[t][ct][i]);
+                        for (int i = 0; i < 8; ++i) hv[i] = join_state(hi[ks][ct][i], hl[ks][ct][i]);
                     }
-                    bf16x4 o;
+                    const f32x8 av = join(acc[2 * ks][ct], acc[2 * ks + 1][ct]);
+                    Sp<bf16> o;
+                    split8<1>(av, o);
+                    st8(static_cast<bf16*>(a.lin) + lo + hn(2 * ks, ct), o.t[0]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        s += hv[i] * acc[t][ct][i];
-                        o[i] = (bf16)acc[t][ct][i];
-                    }
-                    st4(static_cast<bf16*>(a.lin) + lo + hn(t, ct), o);
+                    for (int i = 0; i < 8; ++i) s += hv[i] * av[i];
                 }
 #pragma unroll
             for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
@@ -1294,8 +1302,7 @@ __global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct)
                     dot += to_f(__builtin_bit_cast(bf16, xr[it][ct][i])) * v[it][ct][i];
-#pragma unroll
-                for (int off = 8; off > 0; off >>= 1) dot += __shfl_xor(dot, off, 64);
+                dot = row_sum16(dot);
                 if (l16 == 0) dots[w * L + it * 16 + 4 * q + i] = dot;
             }
         if (more) fetch_rows(a.x, c - 1, xr);
@@ -1563,8 +1570,7 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a) {
                             from_f<T>(v[it][ct][i] - to_f(Ys[o]));
                     v[it][ct][i] = dxv;
                 }
-#pragma unroll
-                for (int off = 8; off > 0; off >>= 1) dot += __shfl_xor(dot, off, 64);
+                dot = row_sum16(dot);
                 if (l16 == 0) dots[w * L + t] = dot;
             }
         // dh = e^{c_L} dh' - K^T (e^c dX) + Q^T (e^c dY)
