@@ -196,6 +196,43 @@ __device__ __forceinline__ float row_sum16(float v) {
     return v + turn(v, std::integral_constant<int, 1>());
 }
 
+// The 4 x 4 transpose of 16-bit elements among 4 neighbouring lanes (lane b, element i <-> lane i,
+// element b): accumulator columns (4 tokens of one headdim column per lane) <-> rows (4
+// columns of one token per lane), so that x, y and their gradients move 8 bytes a lane.  One
+// exchange of halves with lane b ^ 1 (`sel`, quad_sel), one of words with lane b ^ 2.
+typedef unsigned u32x2v __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ unsigned quad_sel(int lane) { return lane & 1 ? 0x03020706u : 0x05040100u; }
+__device__ __forceinline__ u32x2v quad_t(u32x2v v, unsigned sel, bool upper) {
+    auto turn = [](unsigned x, auto by) {
+        return (unsigned)__builtin_amdgcn_update_dpp((int)x, (int)x, decltype(by)::value, 0xf, 0xf, false);
+    };
+    const unsigned a = __builtin_amdgcn_perm(turn(v[0], std::integral_constant<int, 0xB1>()), v[0], sel);
+    const unsigned b = __builtin_amdgcn_perm(turn(v[1], std::integral_constant<int, 0xB1>()), v[1], sel);
+    const unsigned a2 = turn(a, std::integral_constant<int, 0x4E>()), b2 = turn(b, std::integral_constant<int, 0x4E>());
+    return upper ? u32x2v{b2, b} : u32x2v{a, a2};
+}
+// One wave's 64 tokens x 16 headdim columns of a [token][H P] tensor (resource at the chunk's
+// first token, rows past its end read as zero and drop stores), in accumulator order: two
+// words of two tokens each per 16-token tile.  xo: byte offset of this lane's token and columns.
+__device__ __forceinline__ int rows16_off(int lane, int rsx, int p0) {
+    return (4 * (lane >> 4) + (lane & 3)) * rsx + (p0 + (lane & 12)) * 2;
+}
+__device__ __forceinline__ u32x2v load_rows16(brsrc r, int xo, int it, int rsx) {
+    return __builtin_bit_cast(u32x2v, __builtin_amdgcn_raw_buffer_load_b64(r, xo, it * 16 * rsx, 0));
+}
+__device__ __forceinline__ void store_rows16(brsrc r, f32x4 v, int xo, int it, int rsx, unsigned sel, bool upper) {
+    __builtin_amdgcn_raw_buffer_store_b64(
+        __builtin_bit_cast(u32x2, quad_t(u32x2v{cvt2(v[0], v[1]), cvt2(v[2], v[3])}, sel, upper)), r, xo, it * 16 * rsx, 0);
+}
+__device__ __forceinline__ f32x4 floats(u32x2v v) {
+    return f32x4{__builtin_bit_cast(float, v[0] << 16), __builtin_bit_cast(float, v[0] & 0xffff0000u),
+                 __builtin_bit_cast(float, v[1] << 16), __builtin_bit_cast(float, v[1] & 0xffff0000u)};
+}
+// what rounding to bfloat16 leaves of v
+__device__ __forceinline__ f32x4 rest16(f32x4 v) {
+    return v - floats(u32x2v{cvt2(v[0], v[1]), cvt2(v[2], v[3])});
+}
+
 __device__ __forceinline__ f32x8 join(f32x4 a, f32x4 b) {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
@@ -849,29 +886,23 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
         if (w == 0 && lane < NV * 16)
             dma_run(make_rsrc(a.vec + item(c) * kVec, NV * L * 4), reinterpret_cast<char*>(Vs), 1, 0, 1, lane);
     };
-    const int xo = 4 * q * rsx + (p0 + l16) * 2;  // bytes of (token 4q, column l16)
-    unsigned short xr[4][CT][4], yr[4][CT][4];  // x and (SAVE) dy of the chunk
-    auto fetch_rows = [&](const void* base, int c, unsigned short(&o)[4][CT][4]) {
+    const int xo = rows16_off(lane, rsx, p0);
+    const unsigned sel = quad_sel(lane);
+    const bool upper = (lane & 2) != 0;
+    u32x2v xr[4][CT], yr[4][CT];  // x and (SAVE) dy of the chunk, as loaded
+    auto fetch_rows = [&](const void* base, int c, u32x2v(&o)[4][CT]) {
         const brsrc r = x_rsrc(base, c);
 #pragma unroll
         for (int it = 0; it < 4; ++it)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-                    o[it][ct][i] = __builtin_amdgcn_raw_buffer_load_b16(r, xo + ct * 32, (it * 16 + i) * rsx, 0);
+            for (int ct = 0; ct < CT; ++ct) o[it][ct] = load_rows16(r, xo + ct * 32, it, rsx);
     };
-    auto fetch_x = [&](int c) { fetch_rows(a.x, c, xr); };
-    auto store_rows16 = [&](void* base, int c, const f32x4(&o)[4][CT]) {
+    auto store_rows = [&](void* base, int c, const f32x4(&o)[4][CT]) {
         const brsrc r = x_rsrc(base, c);
 #pragma unroll
         for (int it = 0; it < 4; ++it)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-                    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (bf16)o[it][ct][i]), r,
-                                                          xo + ct * 32, (it * 16 + i) * rsx, 0);
+            for (int ct = 0; ct < CT; ++ct) store_rows16(r, o[it][ct], xo + ct * 32, it, rsx, sel, upper);
     };
 
     // lane offsets (elements) of the fragment reads; further fragments differ by an exchange of
@@ -884,7 +915,7 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
         fetch_k(0, K0);
         fetch_q(0);
         fetch_tab(0);
-        fetch_x(0);
+        fetch_rows(a.x, 0, xr);
         if (SAVE) fetch_rows(a.dy, 0, yr);
     }
     auto chunk = [&](int c, const bf16* Ks, bf16* Kn) {
@@ -941,14 +972,12 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
         for (int it = 0; it < 4; ++it) {
             const f32x4 ec = ld4(Vs + it * 16 + 4 * q);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    v[it][ct][i] = to_f(__builtin_bit_cast(bf16, xr[it][ct][i])) - ec[i] * v[it][ct][i];
-                    yq[it][ct][i] *= ec[i];
-                }
+            for (int ct = 0; ct < CT; ++ct) {
+                v[it][ct] = floats(quad_t(xr[it][ct], sel, upper)) - ec * v[it][ct];
+                yq[it][ct] *= ec;
+            }
         }
-        if (more) fetch_x(c + 1);
+        if (more) fetch_rows(a.x, c + 1, xr);
         auto operands = [&](const float* s1, const float* s2, auto nb) {  // s1_t s2_t v_t
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -1001,28 +1030,26 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
         if (more) fetch_tab(c + 1);
         if (SAVE) {
 #pragma unroll
-            for (int it = 0; it < 4; ++it)
+            for (int it = 0; it < 4; ++it) {
+                f32x4 dot = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) dot += floats(quad_t(yr[it][ct], sel, upper)) * yq[it][ct];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float dot = 0.f;
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct)
-                        dot += to_f(__builtin_bit_cast(bf16, yr[it][ct][i])) * yq[it][ct][i];
-                    dot = row_sum16(dot);
-                    if (l16 == 0) dots[w * L + it * 16 + 4 * q + i] = dot;
+                    const float d = row_sum16(dot[i]);
+                    if (l16 == 0) dots[w * L + it * 16 + 4 * q + i] = d;
                 }
+            }
             if (more) fetch_rows(a.dy, c + 1, yr);
-            store_rows16(a.r, c, v);
+            store_rows(a.r, c, v);
             f32x4 rest[4][CT];
 #pragma unroll
             for (int it = 0; it < 4; ++it)
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) rest[it][ct][i] = v[it][ct][i] - (float)(bf16)v[it][ct][i];
-            store_rows16(a.rlo, c, rest);
+                for (int ct = 0; ct < CT; ++ct) rest[it][ct] = rest16(v[it][ct]);
+            store_rows(a.rlo, c, rest);
         } else {
-            store_rows16(a.y, c, yq);
+            store_rows(a.y, c, yq);
         }
         // h' = e^{c_L} h + K^T (e^{c_L - c} u)
 #pragma unroll
@@ -1126,28 +1153,23 @@ __global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
         if (w == 0 && lane < 48)
             dma_run(make_rsrc(a.vec + item(c) * kVec, 3 * L * 4), reinterpret_cast<char*>(Vs), 1, 0, 1, lane);
     };
-    const int xo = 4 * q * rsx + (p0 + l16) * 2;
-    unsigned short xr[4][CT][4], yr[4][CT][4];
-    auto fetch_rows = [&](const void* base, int c, unsigned short(&o)[4][CT][4]) {
+    const int xo = rows16_off(lane, rsx, p0);
+    const unsigned sel = quad_sel(lane);
+    const bool upper = (lane & 2) != 0;
+    u32x2v xr[4][CT], yr[4][CT];
+    auto fetch_rows = [&](const void* base, int c, u32x2v(&o)[4][CT]) {
         const brsrc r = x_rsrc(base, c);
 #pragma unroll
         for (int it = 0; it < 4; ++it)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-                    o[it][ct][i] = __builtin_amdgcn_raw_buffer_load_b16(r, xo + ct * 32, (it * 16 + i) * rsx, 0);
+            for (int ct = 0; ct < CT; ++ct) o[it][ct] = load_rows16(r, xo + ct * 32, it, rsx);
     };
-    auto store_rows16 = [&](void* base, int c, const f32x4(&o)[4][CT]) {
+    auto store_rows = [&](void* base, int c, const f32x4(&o)[4][CT]) {
         const brsrc r = x_rsrc(base, c);
 #pragma unroll
         for (int it = 0; it < 4; ++it)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-                    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (bf16)o[it][ct][i]), r,
-                                                          xo + ct * 32, (it * 16 + i) * rsx, 0);
+            for (int ct = 0; ct < CT; ++ct) store_rows16(r, o[it][ct], xo + ct * 32, it, rsx, sel, upper);
     };
     const int ka = l16 * N + ((q ^ (l16 & SWZ)) << 3);
     const int tr = 4 * q + (l16 >> 2);
@@ -1174,8 +1196,8 @@ __global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
         // h' (the state entering the next chunk), consumed once the first products are under way
         bf16x8 hi[KS][CT];
         s16x8 hl[KS][CT];
-        if (!last) {
-            const int64_t so = (item(c + 1) - bh) * P * N;
+        {  // (the last chunk's is hend; its loads here are of some other chunk's, unused)
+            const int64_t so = (item(last ? c : c + 1) - bh) * P * N;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -1216,9 +1238,10 @@ __global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    dyf[t][ct][i] = __builtin_bit_cast(bf16, yr[2 * t + (i >> 2)][ct][i & 3]);
+            {
+                const u32x2v lo = quad_t(yr[2 * t][ct], sel, upper), hi2 = quad_t(yr[2 * t + 1][ct], sel, upper);
+                dyf[t][ct] = __builtin_bit_cast(bf16x8, u32x4v{lo[0], lo[1], hi2[0], hi2[1]});
+            }
         if (more) fetch_rows(a.dy, c - 1, yr);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -1279,34 +1302,29 @@ __global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
                         for (int ct = 0; ct < CT; ++ct) v[it][ct] = mma(v[it][ct], sf, b2[t][ct].t[m]);
                 }
         // z leaves in two terms, dX = beta z, its dot with X
-        store_rows16(a.z, c, v);
+        store_rows(a.z, c, v);
         {
             f32x4 rest[4][CT];
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
                 const f32x4 bt = ld4(Vs + 2 * L + it * 16 + 4 * q);
+                f32x4 dot = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) rest[it][ct][i] = v[it][ct][i] - (float)(bf16)v[it][ct][i];
+                    rest[it][ct] = rest16(v[it][ct]);
                     v[it][ct] *= bt;
+                    dot += floats(quad_t(xr[it][ct], sel, upper)) * v[it][ct];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float d = row_sum16(dot[i]);
+                    if (l16 == 0) dots[w * L + it * 16 + 4 * q + i] = d;
                 }
             }
-            store_rows16(a.zlo, c, rest);
+            store_rows(a.zlo, c, rest);
         }
-#pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float dot = 0.f;
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-                    dot += to_f(__builtin_bit_cast(bf16, xr[it][ct][i])) * v[it][ct][i];
-                dot = row_sum16(dot);
-                if (l16 == 0) dots[w * L + it * 16 + 4 * q + i] = dot;
-            }
         if (more) fetch_rows(a.x, c - 1, xr);
-        store_rows16(a.dx, c, v);
+        store_rows(a.dx, c, v);
         // dh = e^{c_L} dh' - K^T (e^c dX) + Q^T (e^c dY)
         operands(Vs, -1.f);
         const float el = Vs[L - 1];
