@@ -183,17 +183,41 @@ __device__ __forceinline__ float join_state(bf16 hi, short lo) {
     return __builtin_bit_cast(float, ((unsigned)__builtin_bit_cast(unsigned short, hi) << 16) + ((unsigned)(int)lo << 1));
 }
 
-// Sum over the 16 lanes of a row, in every lane: lane rotations in the ALU (a shuffle is an LDS
-// round trip, and a walk's 64 of them in a row cost more than its products).
+// Lane exchanges inside a row of 16 in the ALU (a shuffle is an LDS round trip, and a walk's 64
+// of them in a row cost more than its products).
+template <int CTRL> __device__ __forceinline__ unsigned lane_turn(unsigned v) {
+    return (unsigned)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);
+}
+template <int CTRL> __device__ __forceinline__ float lane_turn(float v) {
+    return __builtin_bit_cast(float, lane_turn<CTRL>(__builtin_bit_cast(unsigned, v)));
+}
+// Sum over the 16 lanes of a row, in every lane (rotations by 8, 4, 2, 1).
 __device__ __forceinline__ float row_sum16(float v) {
-    auto turn = [](float x, auto by) {
-        const int i = __builtin_bit_cast(int, x);
-        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, 0x120 + decltype(by)::value, 0xf, 0xf, false));
-    };
-    v += turn(v, std::integral_constant<int, 8>());
-    v += turn(v, std::integral_constant<int, 4>());
-    v += turn(v, std::integral_constant<int, 2>());
-    return v + turn(v, std::integral_constant<int, 1>());
+    v += lane_turn<0x128>(v);
+    v += lane_turn<0x124>(v);
+    v += lane_turn<0x122>(v);
+    return v + lane_turn<0x121>(v);
+}
+// 16 such sums at once: lane k of the row gets that of v[k].  Each step hands half of the values
+// to the lane across (mirrors of 16, 8, 4 and 2 lanes) and adds the half it receives.
+__device__ __forceinline__ float row_sums16(float (&v)[16], int l16) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float keep = l16 & 8 ? v[k + 8] : v[k], send = l16 & 8 ? v[k] : v[k + 8];
+        v[k] = keep + lane_turn<0x140>(send);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float keep = l16 & 4 ? v[k + 4] : v[k], send = l16 & 4 ? v[k] : v[k + 4];
+        v[k] = keep + lane_turn<0x141>(send);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float keep = l16 & 2 ? v[k + 2] : v[k], send = l16 & 2 ? v[k] : v[k + 2];
+        v[k] = keep + lane_turn<0x1B>(send);
+    }
+    const float keep = l16 & 1 ? v[1] : v[0], send = l16 & 1 ? v[0] : v[1];
+    return keep + lane_turn<0xB1>(send);
 }
 
 // The 4 x 4 transpose of 16-bit elements among 4 neighbouring lanes (lane b, element i <-> lane i,
@@ -203,12 +227,9 @@ __device__ __forceinline__ float row_sum16(float v) {
 typedef unsigned u32x2v __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ unsigned quad_sel(int lane) { return lane & 1 ? 0x03020706u : 0x05040100u; }
 __device__ __forceinline__ u32x2v quad_t(u32x2v v, unsigned sel, bool upper) {
-    auto turn = [](unsigned x, auto by) {
-        return (unsigned)__builtin_amdgcn_update_dpp((int)x, (int)x, decltype(by)::value, 0xf, 0xf, false);
-    };
-    const unsigned a = __builtin_amdgcn_perm(turn(v[0], std::integral_constant<int, 0xB1>()), v[0], sel);
-    const unsigned b = __builtin_amdgcn_perm(turn(v[1], std::integral_constant<int, 0xB1>()), v[1], sel);
-    const unsigned a2 = turn(a, std::integral_constant<int, 0x4E>()), b2 = turn(b, std::integral_constant<int, 0x4E>());
+    const unsigned a = __builtin_amdgcn_perm(lane_turn<0xB1>((unsigned)v[0]), v[0], sel);
+    const unsigned b = __builtin_amdgcn_perm(lane_turn<0xB1>((unsigned)v[1]), v[1], sel);
+    const unsigned a2 = lane_turn<0x4E>(a), b2 = lane_turn<0x4E>(b);
     return upper ? u32x2v{b2, b} : u32x2v{a, a2};
 }
 // One wave's 64 tokens x 16 headdim columns of a [token][H P] tensor (resource at the chunk's
@@ -910,6 +931,11 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
     const int ka = l16 * N + ((q ^ (l16 & SWZ)) << 3);
     const int tr = 4 * q + (l16 >> 2);
     const int kt = tr * N + (((l16 & 3) ^ (tr & SWZ)) << 3);
+    // rows n of tile t (see acc), tokens as the accumulators hold them
+    auto frag_t = [&](const bf16* tile, int t) {
+        const bf16* p = tile + (kt ^ ((t >> 1) << 5)) + 4 * (t & 1);
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(ds_tr16(p), ds_tr16(p + 16 * N), 0, 1, 2, 3, 4, 5, 6, 7));
+    };
 
     if (nc > 0) {
         fetch_k(0, K0);
@@ -1001,45 +1027,48 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int k = 0; k < 3; ++k)  // term of S
+            for (int k = 0; k < 3; ++k) {  // term of S
+                bf16x8 sf[4];
 #pragma unroll
-                for (int it = 2 * t; it < 4; ++it) {
-                    const bf16x8 sf = frag_tab5(Sf + k * 5 * 512, it, t, lane);
+                for (int it = 2 * t; it < 4; ++it) sf[it] = frag_tab5(Sf + k * 5 * 512, it, t, lane);
 #pragma unroll
-                    for (int m = 0; m < 3 - k; ++m)
+                for (int m = 0; m < 3 - k; ++m)
 #pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) v[it][ct] = mma(v[it][ct], sf, b2[t][ct].t[m]);
-                }
+                    for (int it = 2 * t; it < 4; ++it)
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) v[it][ct] = mma(v[it][ct], sf[it], b2[t][ct].t[m]);
+            }
         // Y = e^c Q h^T + M beta r
         operands(SAVE ? Vs + 2 * L : nullptr, nullptr, std::integral_constant<int, SAVE ? 3 : 2>());
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int k = 0; k < (SAVE ? 3 : 1); ++k)  // term of M
+            for (int k = 0; k < (SAVE ? 3 : 1); ++k) {  // term of M
+                bf16x8 mf[4];
 #pragma unroll
-                for (int it = 2 * t; it < 4; ++it) {
-                    const bf16x8 mf = frag_tab5(Mf + k * 5 * 512, it, t, lane);
+                for (int it = 2 * t; it < 4; ++it) mf[it] = frag_tab5(Mf + k * 5 * 512, it, t, lane);
 #pragma unroll
-                    for (int m = 0; m < (SAVE ? 3 - k : 2); ++m)
+                for (int m = 0; m < (SAVE ? 3 - k : 2); ++m)
 #pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) yq[it][ct] = mma(yq[it][ct], mf, b2[t][ct].t[m]);
-                }
+                    for (int it = 2 * t; it < 4; ++it)
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) yq[it][ct] = mma(yq[it][ct], mf[it], b2[t][ct].t[m]);
+            }
         operands(Vs + L, SAVE ? Vs + 2 * L : nullptr, std::integral_constant<int, 3>());  // e^{c_L - c} u
         const float el = Vs[L - 1];
         wave_meet(false);  // every wave is done with the tables
         if (more) fetch_tab(c + 1);
         if (SAVE) {
+            float dot[16];
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
-                f32x4 dot = f32x4{0.f, 0.f, 0.f, 0.f};
+                f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) dot += floats(quad_t(yr[it][ct], sel, upper)) * yq[it][ct];
+                for (int ct = 0; ct < CT; ++ct) d += floats(quad_t(yr[it][ct], sel, upper)) * yq[it][ct];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float d = row_sum16(dot[i]);
-                    if (l16 == 0) dots[w * L + it * 16 + 4 * q + i] = d;
-                }
+                for (int i = 0; i < 4; ++i) dot[it * 4 + i] = d[i];
             }
+            dots[w * L + (l16 >> 2) * 16 + 4 * q + (l16 & 3)] = row_sums16(dot, l16);
             if (more) fetch_rows(a.dy, c + 1, yr);
             store_rows(a.r, c, v);
             f32x4 rest[4][CT];
@@ -1051,21 +1080,28 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
         } else {
             store_rows(a.y, c, yq);
         }
-        // h' = e^{c_L} h + K^T (e^{c_L - c} u)
+        // h' = e^{c_L} h + K^T (e^{c_L - c} u), four row tiles side by side: a product on an
+        // accumulator waits for the one before it
 #pragma unroll
-        for (int t = 0; t < NTL; ++t) {
+        for (int t4 = 0; t4 < NTL; t4 += 4) {
+            bf16x8 kf[4][2];
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) acc[t][ct] *= el;
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                const bf16* kp = Ks + (kt ^ ((t >> 1) << 5)) + 4 * (t & 1) + ks * 32 * N;
-                const bf16x8 kf = __builtin_bit_cast(
-                    bf16x8, __builtin_shufflevector(ds_tr16(kp), ds_tr16(kp + 16 * N), 0, 1, 2, 3, 4, 5, 6, 7));
+                for (int ks = 0; ks < 2; ++ks) kf[t][ks] = frag_t(Ks + ks * 32 * N, t4 + t);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) acc[t4 + t][ct] *= el;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
                 for (int k = 0; k < 3; ++k)
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) acc[t][ct] = mma(acc[t][ct], kf, b2[ks][ct].t[k]);
-            }
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct)
+                            acc[t4 + t][ct] = mma(acc[t4 + t][ct], kf[t][ks], b2[ks][ct].t[k]);
         }
         if (KB == 1 && more) {
             wave_meet(false);  // every wave is done with K
@@ -1174,6 +1210,11 @@ __global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
     const int ka = l16 * N + ((q ^ (l16 & SWZ)) << 3);
     const int tr = 4 * q + (l16 >> 2);
     const int kt = tr * N + (((l16 & 3) ^ (tr & SWZ)) << 3);
+    // rows n of tile t (see acc), tokens as the accumulators hold them
+    auto frag_t = [&](const bf16* tile, int t) {
+        const bf16* p = tile + (kt ^ ((t >> 1) << 5)) + 4 * (t & 1);
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(ds_tr16(p), ds_tr16(p + 16 * N), 0, 1, 2, 3, 4, 5, 6, 7));
+    };
     const int ft = (tr + 16 * (l16 & 3)) * 8;  // four columns of a block's row, in a table's fragment
     // rows [16 j, 16 j + 16) of the table's transpose, columns 32 t on (t >= j / 2)
     auto frag_up5 = [&](const bf16* tab, int j, int t) {
@@ -1246,13 +1287,15 @@ __global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int k = 0; k < 3; ++k)
+            for (int k = 0; k < 3; ++k) {
+                bf16x8 mf[4];
 #pragma unroll
-                for (int it = 0; it <= 2 * t + 1; ++it) {
-                    const bf16x8 mf = frag_up5(Mf + k * 5 * 512, it, t);
+                for (int it = 0; it <= 2 * t + 1; ++it) mf[it] = frag_up5(Mf + k * 5 * 512, it, t);
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) v[it][ct] = mma(v[it][ct], mf, dyf[t][ct]);
-                }
+                for (int it = 0; it <= 2 * t + 1; ++it)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) v[it][ct] = mma(v[it][ct], mf[it], dyf[t][ct]);
+            }
         {  // <dh', h'> over this wave's columns, and dh' for the gradients of B
             const int64_t lo = (item(c) - bh) * P * N;
             float s = 0.f;
@@ -1292,35 +1335,36 @@ __global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int k = 0; k < 3; ++k)
+            for (int k = 0; k < 3; ++k) {
+                bf16x8 sf[4];
 #pragma unroll
-                for (int it = 0; it <= 2 * t + 1; ++it) {
-                    const bf16x8 sf = frag_up5(Sf + k * 5 * 512, it, t);
+                for (int it = 0; it <= 2 * t + 1; ++it) sf[it] = frag_up5(Sf + k * 5 * 512, it, t);
 #pragma unroll
-                    for (int m = 0; m < 3 - k; ++m)
+                for (int m = 0; m < 3 - k; ++m)
 #pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) v[it][ct] = mma(v[it][ct], sf, b2[t][ct].t[m]);
-                }
+                    for (int it = 0; it <= 2 * t + 1; ++it)
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) v[it][ct] = mma(v[it][ct], sf[it], b2[t][ct].t[m]);
+            }
         // z leaves in two terms, dX = beta z, its dot with X
         store_rows(a.z, c, v);
         {
             f32x4 rest[4][CT];
+            float dot[16];
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
                 const f32x4 bt = ld4(Vs + 2 * L + it * 16 + 4 * q);
-                f32x4 dot = f32x4{0.f, 0.f, 0.f, 0.f};
+                f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
                     rest[it][ct] = rest16(v[it][ct]);
                     v[it][ct] *= bt;
-                    dot += floats(quad_t(xr[it][ct], sel, upper)) * v[it][ct];
+                    d += floats(quad_t(xr[it][ct], sel, upper)) * v[it][ct];
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float d = row_sum16(dot[i]);
-                    if (l16 == 0) dots[w * L + it * 16 + 4 * q + i] = d;
-                }
+                for (int i = 0; i < 4; ++i) dot[it * 4 + i] = d[i];
             }
+            dots[w * L + (l16 >> 2) * 16 + 4 * q + (l16 & 3)] = row_sums16(dot, l16);
             store_rows(a.zlo, c, rest);
         }
         if (more) fetch_rows(a.x, c - 1, xr);
@@ -1353,25 +1397,36 @@ __global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
             a.tot[(int64_t)sl * a.ntab * H + item(c)] = s;
         }
 #pragma unroll
-        for (int t = 0; t < NTL; ++t) {
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) acc[t][ct] *= el;
+        for (int t4 = 0; t4 < NTL; t4 += 4)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                const int o = (kt ^ ((t >> 1) << 5)) + 4 * (t & 1) + ks * 32 * N;
-                const bf16x8 kf = __builtin_bit_cast(
-                    bf16x8, __builtin_shufflevector(ds_tr16(Ks + o), ds_tr16(Ks + o + 16 * N), 0, 1, 2, 3, 4, 5, 6, 7));
-                const bf16x8 qf = __builtin_bit_cast(
-                    bf16x8, __builtin_shufflevector(ds_tr16(Qs + o), ds_tr16(Qs + o + 16 * N), 0, 1, 2, 3, 4, 5, 6, 7));
+                bf16x8 kf[4], qf[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    kf[t] = frag_t(Ks + ks * 32 * N, t4 + t);
+                    qf[t] = frag_t(Qs + ks * 32 * N, t4 + t);
+                }
+                if (ks == 0) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) acc[t4 + t][ct] *= el;
+                }
 #pragma unroll
                 for (int k = 0; k < 3; ++k)
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) {
-                        acc[t][ct] = mma(acc[t][ct], kf, b2[ks][ct].t[k]);
-                        acc[t][ct] = mma(acc[t][ct], qf, d2[ks][ct].t[k]);
-                    }
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct)
+                            acc[t4 + t][ct] = mma(acc[t4 + t][ct], kf[t], b2[ks][ct].t[k]);
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct)
+                            acc[t4 + t][ct] = mma(acc[t4 + t][ct], qf[t], d2[ks][ct].t[k]);
             }
-        }
         if (!TWO && more) {
             wave_meet(false);  // every wave is done with K and Q
             fetch_kq(c - 1, Kn, Qn);
