@@ -138,6 +138,18 @@ __device__ __forceinline__ void split8(f32x8 v, Sp<bf16>& s) {
 }
 template <int NB = 3>
 __device__ __forceinline__ void split8(f32x8 v, Sp<float>& s) { s.t[0] = v; }
+template <int NB>
+__device__ __forceinline__ void split4(f32x4 v, bf16x4 (&o)[NB]) {
+    float a[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+        const u32x2 u = u32x2{cvt2(a[0], a[1]), cvt2(a[2], a[3])};
+        o[k] = __builtin_bit_cast(bf16x4, u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            a[e] -= __builtin_bit_cast(float, e & 1 ? u[e >> 1] & 0xffff0000u : u[e >> 1] << 16);
+    }
+}
 
 // c += a b, a exact in T, b in its first NB terms
 template <int NB, typename T, typename V>
@@ -183,8 +195,7 @@ __device__ __forceinline__ float join_state(bf16 hi, short lo) {
     return __builtin_bit_cast(float, ((unsigned)__builtin_bit_cast(unsigned short, hi) << 16) + ((unsigned)(int)lo << 1));
 }
 
-// Lane exchanges inside a row of 16 in the ALU (a shuffle is an LDS round trip, and a walk's 64
-// of them in a row cost more than its products).
+// Lane exchanges inside a row of 16 in the ALU (a shuffle is an LDS round trip).
 template <int CTRL> __device__ __forceinline__ unsigned lane_turn(unsigned v) {
     return (unsigned)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);
 }
@@ -198,28 +209,6 @@ __device__ __forceinline__ float row_sum16(float v) {
     v += lane_turn<0x122>(v);
     return v + lane_turn<0x121>(v);
 }
-// 16 such sums at once: lane k of the row gets that of v[k].  Each step hands half of the values
-// to the lane across (mirrors of 16, 8, 4 and 2 lanes) and adds the half it receives.
-__device__ __forceinline__ float row_sums16(float (&v)[16], int l16) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const float keep = l16 & 8 ? v[k + 8] : v[k], send = l16 & 8 ? v[k] : v[k + 8];
-        v[k] = keep + lane_turn<0x140>(send);
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float keep = l16 & 4 ? v[k + 4] : v[k], send = l16 & 4 ? v[k] : v[k + 4];
-        v[k] = keep + lane_turn<0x141>(send);
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const float keep = l16 & 2 ? v[k + 2] : v[k], send = l16 & 2 ? v[k] : v[k + 2];
-        v[k] = keep + lane_turn<0x1B>(send);
-    }
-    const float keep = l16 & 1 ? v[1] : v[0], send = l16 & 1 ? v[0] : v[1];
-    return keep + lane_turn<0xB1>(send);
-}
-
 // The 4 x 4 transpose of 16-bit elements among 4 neighbouring lanes (lane b, element i <-> lane i,
 // element b): accumulator columns (4 tokens of one headdim column per lane) <-> rows (4
 // columns of one token per lane), so that x, y and their gradients move 8 bytes a lane.  One
@@ -856,20 +845,18 @@ __device__ __forceinline__ void dma_run(brsrc r, char* dst, int runs, int w, int
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + m * 1024), 16, m * 1024 + lane * 16, 0, 0, 0);
 }
 
-template <int N, int CT, int KB, int OCC, bool SAVE>
+template <int N, int CT, int KB, int OCC>
 __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
-    constexpr int TABN = SAVE ? kFragTab2 : kFragTab, NV = SAVE ? 3 : 2, QT = SAVE ? 3 : 2;
     constexpr int NTL = N / 16, KS = N / 32, TILE = Dma<N>::TILE, SWZ = Dma<N>::SWZ;
     __shared__ __attribute__((aligned(16))) bf16 K0[TILE];
     __shared__ __attribute__((aligned(16))) bf16 K1[KB == 2 ? TILE : 8];
     __shared__ __attribute__((aligned(16))) bf16 Qs[TILE];
-    __shared__ __attribute__((aligned(16))) bf16 Sf[TABN];    // -S in three terms, then M
-    __shared__ __attribute__((aligned(16))) float Vs[NV * L];  // e^c, e^{c_L - c} (times beta), SAVE: beta
-    __shared__ float dots[SAVE ? 4 * L : 1];                   // SAVE: [wave][token] dY . Y
+    __shared__ __attribute__((aligned(16))) bf16 Sf[kFragTab];  // -S beta in three terms, then M beta
+    __shared__ __attribute__((aligned(16))) float Vs[2 * L];    // e^c, beta e^{c_L - c}
     const bf16* Mf = Sf + 3 * 5 * 512;
     const int tid = threadIdx.x, nw = blockDim.x >> 6, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
     const int H = a.H, G = a.G, P = a.P;
-    const int SW = 16 * CT * nw, nsl = P / SW, BH = a.rows.nrows * H;
+    const int SW = 16 * CT * nw, nsl = P / SW;
     const int sl = (int)(blockIdx.x % (unsigned)nsl), bh = (int)(blockIdx.x / (unsigned)nsl);
     const int h = bh % H, row = bh / H, g = h / (H / G);
     const int64_t Tn = a.rows.len(row), tok0 = a.rows.tok0(row);
@@ -902,28 +889,21 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
     auto fetch_k = [&](int c, bf16* kd) { dma_tile<N>(key_rsrc(a.B, c), kd, rsk, w, nw, lane); };
     auto fetch_q = [&](int c) { dma_tile<N>(key_rsrc(a.C, c), Qs, rsk, w, nw, lane); };
     auto fetch_tab = [&](int c) {
-        dma_run(make_rsrc(reinterpret_cast<const bf16*>(a.tab) + item(c) * TABN, TABN * 2),
-                reinterpret_cast<char*>(Sf), TABN / 512, w, nw, lane);
-        if (w == 0 && lane < NV * 16)
-            dma_run(make_rsrc(a.vec + item(c) * kVec, NV * L * 4), reinterpret_cast<char*>(Vs), 1, 0, 1, lane);
+        dma_run(make_rsrc(reinterpret_cast<const bf16*>(a.tab) + item(c) * kFragTab, kFragTab * 2),
+                reinterpret_cast<char*>(Sf), kFragTab / 512, w, nw, lane);
+        if (w == 0 && lane < 32)
+            dma_run(make_rsrc(a.vec + item(c) * kVec, 2 * L * 4), reinterpret_cast<char*>(Vs), 1, 0, 1, lane);
     };
     const int xo = rows16_off(lane, rsx, p0);
     const unsigned sel = quad_sel(lane);
     const bool upper = (lane & 2) != 0;
-    u32x2v xr[4][CT], yr[4][CT];  // x and (SAVE) dy of the chunk, as loaded
-    auto fetch_rows = [&](const void* base, int c, u32x2v(&o)[4][CT]) {
-        const brsrc r = x_rsrc(base, c);
+    u32x2v xr[4][CT];  // x of the chunk, as loaded
+    auto fetch_x = [&](int c) {
+        const brsrc r = x_rsrc(a.x, c);
 #pragma unroll
         for (int it = 0; it < 4; ++it)
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) o[it][ct] = load_rows16(r, xo + ct * 32, it, rsx);
-    };
-    auto store_rows = [&](void* base, int c, const f32x4(&o)[4][CT]) {
-        const brsrc r = x_rsrc(base, c);
-#pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) store_rows16(r, o[it][ct], xo + ct * 32, it, rsx, sel, upper);
+            for (int ct = 0; ct < CT; ++ct) xr[it][ct] = load_rows16(r, xo + ct * 32, it, rsx);
     };
 
     // lane offsets (elements) of the fragment reads; further fragments differ by an exchange of
@@ -941,26 +921,12 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
         fetch_k(0, K0);
         fetch_q(0);
         fetch_tab(0);
-        fetch_rows(a.x, 0, xr);
-        if (SAVE) fetch_rows(a.dy, 0, yr);
+        fetch_x(0);
     }
     auto chunk = [&](int c, const bf16* Ks, bf16* Kn) {
         wave_meet(true);  // the chunk's tiles have landed
         const bool more = c + 1 < nc;
         if (KB == 2 && more) fetch_k(c + 1, Kn);
-        if (SAVE) {  // the state entering the chunk
-            const int64_t so = item(c) * P * N - (int64_t)bh * P * N;
-#pragma unroll
-            for (int t = 0; t < NTL; t += 2)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    bf16x8 hi;
-                    s16x8 lo;
-                    split_state(join(acc[t][ct], acc[t + 1][ct]), hi, lo);
-                    st8(static_cast<bf16*>(a.hin) + so + hn(t, ct), hi);
-                    *reinterpret_cast<s16x8*>(a.hlo + so + hn(t, ct)) = lo;
-                }
-        }
 
         // K h^T in three terms, Q h^T in two (enough for a bfloat16 y)
         f32x4 v[4][CT], yq[4][CT];
@@ -986,7 +952,7 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) {
                         v[it][ct] = mma(v[it][ct], kf[it], hs[ct].t[k]);
-                        if (k < QT) yq[it][ct] = mma(yq[it][ct], qf[it], hs[ct].t[k]);
+                        if (k < 2) yq[it][ct] = mma(yq[it][ct], qf[it], hs[ct].t[k]);
                     }
         }
         wave_meet(false);  // every wave is done with Q
@@ -1003,27 +969,11 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
                 yq[it][ct] *= ec;
             }
         }
-        if (more) fetch_rows(a.x, c + 1, xr);
-        auto operands = [&](const float* s1, const float* s2, auto nb) {  // s1_t s2_t v_t
+        if (more) fetch_x(c + 1);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                f32x4 sa = f32x4{1.f, 1.f, 1.f, 1.f}, sb = sa;
-                if (s1) {
-                    sa = ld4(s1 + 32 * t + 4 * q);
-                    sb = ld4(s1 + 32 * t + 16 + 4 * q);
-                }
-                if (s2) {
-                    sa *= ld4(s2 + 32 * t + 4 * q);
-                    sb *= ld4(s2 + 32 * t + 16 + 4 * q);
-                }
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-                    split8<decltype(nb)::value>(s1 ? join(v[2 * t][ct] * sa, v[2 * t + 1][ct] * sb)
-                                                   : join(v[2 * t][ct], v[2 * t + 1][ct]),
-                                                b2[t][ct]);
-            }
-        };
-        operands(SAVE ? Vs + 2 * L : nullptr, nullptr, std::integral_constant<int, 3>());
+            for (int ct = 0; ct < CT; ++ct) split8(join(v[2 * t][ct], v[2 * t + 1][ct]), b2[t][ct]);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -1039,46 +989,36 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
                         for (int ct = 0; ct < CT; ++ct) v[it][ct] = mma(v[it][ct], sf[it], b2[t][ct].t[m]);
             }
         // Y = e^c Q h^T + M beta r
-        operands(SAVE ? Vs + 2 * L : nullptr, nullptr, std::integral_constant<int, SAVE ? 3 : 2>());
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 2; ++t) {
 #pragma unroll
-            for (int k = 0; k < (SAVE ? 3 : 1); ++k) {  // term of M
-                bf16x8 mf[4];
+            for (int ct = 0; ct < CT; ++ct) split8<2>(join(v[2 * t][ct], v[2 * t + 1][ct]), b2[t][ct]);
+            bf16x8 mf[4];
 #pragma unroll
-                for (int it = 2 * t; it < 4; ++it) mf[it] = frag_tab5(Mf + k * 5 * 512, it, t, lane);
+            for (int it = 2 * t; it < 4; ++it) mf[it] = frag_tab5(Mf, it, t, lane);
 #pragma unroll
-                for (int m = 0; m < (SAVE ? 3 - k : 2); ++m)
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int it = 2 * t; it < 4; ++it)
+                for (int it = 2 * t; it < 4; ++it)
 #pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) yq[it][ct] = mma(yq[it][ct], mf[it], b2[t][ct].t[m]);
-            }
-        operands(Vs + L, SAVE ? Vs + 2 * L : nullptr, std::integral_constant<int, 3>());  // e^{c_L - c} u
+                    for (int ct = 0; ct < CT; ++ct) yq[it][ct] = mma(yq[it][ct], mf[it], b2[t][ct].t[k]);
+        }
+        // e^{c_L - c} u as operands
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const f32x4 sa = ld4(Vs + L + 32 * t + 4 * q), sb = ld4(Vs + L + 32 * t + 16 + 4 * q);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) split8(join(v[2 * t][ct] * sa, v[2 * t + 1][ct] * sb), b2[t][ct]);
+        }
         const float el = Vs[L - 1];
         wave_meet(false);  // every wave is done with the tables
         if (more) fetch_tab(c + 1);
-        if (SAVE) {
-            float dot[16];
-#pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) d += floats(quad_t(yr[it][ct], sel, upper)) * yq[it][ct];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dot[it * 4 + i] = d[i];
-            }
-            dots[w * L + (l16 >> 2) * 16 + 4 * q + (l16 & 3)] = row_sums16(dot, l16);
-            if (more) fetch_rows(a.dy, c + 1, yr);
-            store_rows(a.r, c, v);
-            f32x4 rest[4][CT];
+        {
+            const brsrc ry = x_rsrc(a.y, c);
 #pragma unroll
             for (int it = 0; it < 4; ++it)
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) rest[it][ct] = rest16(v[it][ct]);
-            store_rows(a.rlo, c, rest);
-        } else {
-            store_rows(a.y, c, yq);
+                for (int ct = 0; ct < CT; ++ct) store_rows16(ry, yq[it][ct], xo + ct * 32, it, rsx, sel, upper);
         }
         // h' = e^{c_L} h + K^T (e^{c_L - c} u), four row tiles side by side: a product on an
         // accumulator waits for the one before it
@@ -1107,14 +1047,6 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
             wave_meet(false);  // every wave is done with K
             fetch_k(c + 1, K0);
         }
-        if (SAVE) {
-            wave_meet(false);
-            for (int t = tid; t < rows_left(c); t += blockDim.x) {
-                float s = 0.f;
-                for (int k = 0; k < nw; ++k) s += dots[k * L + t];
-                a.dyy[((int64_t)sl * BH + bh) * a.T + (int64_t)c * L + t] = s;
-            }
-        }
     };
     if (KB == 2) {
         for (int c = 0; c < nc; c += 2) {
@@ -1124,328 +1056,556 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
     } else {
         for (int c = 0; c < nc; ++c) chunk(c, K0, K0);
     }
-    if (float* hT = SAVE ? a.hend : a.hT) {
+    if (a.hT) {
 #pragma unroll
         for (int t = 0; t < NTL; ++t)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
-                st4(hT + hn(t, ct), acc[t][ct]);
+                st4(a.hT + hn(t, ct), acc[t][ct]);
     }
 }
 
 // ---------------------------------------------------------------------------
-// k_delta_adj: the adjoint walk in the same form (chunks in reverse, dh^T in accumulators): dy
-// needs no tile, its registers are the operand; the tables' transposes are read from the
-// same fragments by transposing loads.  Outputs as k_delta_rev.
+// k_delta_team: the same walk by a team of 4 waves per 16 CT columns, for few chains (a chain's
+// time is then one wave's, and 4 waves share it) and for the backward's first walk (SAVE).
+// Wave w takes token tile w of every product over tokens and NTL / 4 of the state's tiles; the
+// state, R, r and the weighted u pass between the waves as split operands in LDS (written
+// once, read by the waves that need them): three exchanges per chunk.
+// SAVE = true writes the residuals r, the state entering every chunk and after the last, and
+// the per-token dY . Y (Y in float32, all terms) instead of y and hT.
 // ---------------------------------------------------------------------------
-template <int N, int CT, int OCC>
-__global__ __launch_bounds__(256, OCC) void k_delta_adj(Args a) {
-    constexpr int NTL = N / 16, KS = N / 32, TILE = Dma<N>::TILE, SWZ = Dma<N>::SWZ, TABN = kFragTab2;
-    constexpr bool TWO = N <= 128;  // two buffers for K and Q
-    __shared__ __attribute__((aligned(16))) bf16 K0[TILE];
-    __shared__ __attribute__((aligned(16))) bf16 Q0[TILE];
-    __shared__ __attribute__((aligned(16))) bf16 K1[TWO ? TILE : 8];
-    __shared__ __attribute__((aligned(16))) bf16 Q1[TWO ? TILE : 8];
-    __shared__ __attribute__((aligned(16))) bf16 Sf[TABN];
-    __shared__ __attribute__((aligned(16))) float Vs[3 * L];
-    __shared__ float dots[4 * L], tots[4];
-    const bf16* Mf = Sf + 3 * 5 * 512;
-    const int tid = threadIdx.x, nw = blockDim.x >> 6, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
-    const int H = a.H, G = a.G, P = a.P;
-    const int SW = 16 * CT * nw, nsl = P / SW, BH = a.rows.nrows * H;
-    const int sl = (int)(blockIdx.x % (unsigned)nsl), bh = (int)(blockIdx.x / (unsigned)nsl);
-    const int h = bh % H, row = bh / H, g = h / (H / G);
-    const int64_t Tn = a.rows.len(row), tok0 = a.rows.tok0(row);
-    const int nc = a.rows.nchunks(row), kb0 = a.rows.kbase(row);
-    const int p0 = sl * SW + w * 16 * CT;
-
-    f32x4 acc[NTL][CT];
-    const int64_t ho = ((int64_t)bh * P + p0 + l16) * N + 8 * q;
-    auto hn = [&](int t, int ct) { return ho + ct * 16 * N + (t >> 1) * 32 + (t & 1) * 4; };
-#pragma unroll
-    for (int t = 0; t < NTL; ++t)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-            acc[t][ct] = a.dhT ? ld4(a.dhT + hn(t, ct)) : f32x4{0.f, 0.f, 0.f, 0.f};
-
-    const int rsk = G * N * 2, rsx = H * P * 2;
-    auto rows_left = [&](int c) { return (int)min((int64_t)L, Tn - (int64_t)c * L); };
-    auto key_rsrc = [&](const void* base, int c) {
+// what the two team walks share: the chunk addresses of one (row, head) and the lane's offsets
+template <int N, int CT>
+struct Team {
+    static constexpr int OT = N / 64;  // state tiles per wave: OT w .. OT w + OT - 1
+    int lane, w, l16, q, H, G, P, h, row, g, nc, kb0, sl, bh, p0, rsk, rsx, xo;
+    int64_t Tn, tok0, ho;
+    unsigned sel;
+    bool upper;
+    int ka, kt;
+    const Args& a;
+    __device__ __forceinline__ Team(const Args& a_) : a(a_) {
+        constexpr int SWZ = Dma<N>::SWZ;
+        lane = threadIdx.x & 63; w = wave_id(); l16 = lane & 15; q = lane >> 4;
+        H = a.H; G = a.G; P = a.P;
+        const int nsl = P / (16 * CT);
+        sl = (int)(blockIdx.x % (unsigned)nsl); bh = (int)(blockIdx.x / (unsigned)nsl);
+        h = bh % H; row = bh / H; g = h / (H / G);
+        Tn = a.rows.len(row); tok0 = a.rows.tok0(row); nc = a.rows.nchunks(row); kb0 = a.rows.kbase(row);
+        p0 = sl * 16 * CT;
+        rsk = G * N * 2; rsx = H * P * 2;
+        xo = rows16_off(lane, rsx, p0);
+        sel = quad_sel(lane); upper = (lane & 2) != 0;
+        ho = ((int64_t)bh * P + p0 + l16) * N + 8 * q;
+        ka = l16 * N + ((q ^ (l16 & SWZ)) << 3);
+        const int tr = 4 * q + (l16 >> 2);
+        kt = tr * N + (((l16 & 3) ^ (tr & SWZ)) << 3);
+    }
+    __device__ __forceinline__ int64_t hn(int t, int ct) const { return ho + ct * 16 * N + (t >> 1) * 32 + (t & 1) * 4; }
+    __device__ __forceinline__ int rows_left(int c) const { return (int)min((int64_t)L, Tn - (int64_t)c * L); }
+    __device__ __forceinline__ int64_t item(int c) const { return (int64_t)(kb0 + c) * H + h; }
+    __device__ __forceinline__ brsrc key_rsrc(const void* base, int c) const {
         return make_rsrc(static_cast<const bf16*>(base) + ((tok0 + (int64_t)c * L) * G + g) * N,
                          (uint32_t)((rows_left(c) - 1) * rsk + N * 2));
-    };
-    auto x_rsrc = [&](const void* base, int c) {
+    }
+    __device__ __forceinline__ brsrc x_rsrc(const void* base, int c) const {
         return make_rsrc(static_cast<const bf16*>(base) + ((tok0 + (int64_t)c * L) * H + h) * P,
                          (uint32_t)((rows_left(c) - 1) * rsx + P * 2));
-    };
-    auto item = [&](int c) { return (int64_t)(kb0 + c) * H + h; };
-    auto fetch_kq = [&](int c, bf16* kd, bf16* qd) {
-        dma_tile<N>(key_rsrc(a.B, c), kd, rsk, w, nw, lane);
-        dma_tile<N>(key_rsrc(a.C, c), qd, rsk, w, nw, lane);
-    };
-    auto fetch_tab = [&](int c) {
-        dma_run(make_rsrc(reinterpret_cast<const bf16*>(a.tab) + item(c) * TABN, TABN * 2),
-                reinterpret_cast<char*>(Sf), TABN / 512, w, nw, lane);
-        if (w == 0 && lane < 48)
-            dma_run(make_rsrc(a.vec + item(c) * kVec, 3 * L * 4), reinterpret_cast<char*>(Vs), 1, 0, 1, lane);
-    };
-    const int xo = rows16_off(lane, rsx, p0);
-    const unsigned sel = quad_sel(lane);
-    const bool upper = (lane & 2) != 0;
-    u32x2v xr[4][CT], yr[4][CT];
-    auto fetch_rows = [&](const void* base, int c, u32x2v(&o)[4][CT]) {
+    }
+    __device__ __forceinline__ void fetch_tile(const void* base, int c, bf16* dst) const {
+        constexpr int RPI = 512 / N, PC = Dma<N>::PIECES;
+        const brsrc r = key_rsrc(base, c);
+#pragma unroll
+        for (int k = 0; k < L / RPI / 4; ++k) {
+            const int m = w + 4 * k, rw = m * RPI + lane / PC, j = (lane % PC) ^ (rw & Dma<N>::SWZ);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + m * 512), 16, rw * rsk + j * 16, 0, 0, 0);
+        }
+    }
+    template <int ELEMS, int NV>
+    __device__ __forceinline__ void fetch_tab(int c, bf16* dst, float* vec) const {
+        const brsrc r = make_rsrc(reinterpret_cast<const bf16*>(a.tab) + item(c) * ELEMS, ELEMS * 2);
+#pragma unroll
+        for (int k = 0; k < ELEMS / 512; k += 4)
+            if (k + w < ELEMS / 512)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + (k + w) * 512), 16, (k + w) * 1024 + lane * 16, 0,
+                                                         0, 0);
+        if (w == 0 && lane < NV * 16)
+            dma_run(make_rsrc(a.vec + item(c) * kVec, NV * L * 4), reinterpret_cast<char*>(vec), 1, 0, 1, lane);
+    }
+    // a chunk's 64 x 16 CT tile of x or dy: dst[ct][token][16]
+    __device__ __forceinline__ void fetch_x(const void* base, int c, bf16* dst) const {
         const brsrc r = x_rsrc(base, c);
-#pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) o[it][ct] = load_rows16(r, xo + ct * 32, it, rsx);
-    };
-    auto store_rows = [&](void* base, int c, const f32x4(&o)[4][CT]) {
-        const brsrc r = x_rsrc(base, c);
-#pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) store_rows16(r, o[it][ct], xo + ct * 32, it, rsx, sel, upper);
-    };
-    const int ka = l16 * N + ((q ^ (l16 & SWZ)) << 3);
-    const int tr = 4 * q + (l16 >> 2);
-    const int kt = tr * N + (((l16 & 3) ^ (tr & SWZ)) << 3);
-    // rows n of tile t (see acc), tokens as the accumulators hold them
-    auto frag_t = [&](const bf16* tile, int t) {
+        if (w < 2 * CT)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + w * 512), 16,
+                                                     ((w & 1) * 32 + (lane >> 1)) * rsx +
+                                                         (p0 + (w >> 1) * 16 + 8 * (lane & 1)) * 2,
+                                                     0, 0, 0);
+    }
+    // token tile `it` of it, in accumulator order (4 tokens of one column)
+    __device__ __forceinline__ s16x4 x_tile(const bf16* src, int it, int ct) const {
+        return ds_tr16(src + ct * 1024 + (it * 16 + 4 * q + (l16 >> 2)) * 16 + 4 * (l16 & 3));
+    }
+    // fragments: token tile `it`, key columns 32 ks on; state tile t, 32 tokens from tile row `p`
+    __device__ __forceinline__ bf16x8 frag_rows16(const bf16* tile, int it, int ks) const {
+        return ld8(tile + (ka ^ (ks << 5)) + it * 16 * N);
+    }
+    __device__ __forceinline__ bf16x8 frag_t(const bf16* tile, int t) const {
         const bf16* p = tile + (kt ^ ((t >> 1) << 5)) + 4 * (t & 1);
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(ds_tr16(p), ds_tr16(p + 16 * N), 0, 1, 2, 3, 4, 5, 6, 7));
-    };
-    const int ft = (tr + 16 * (l16 & 3)) * 8;  // four columns of a block's row, in a table's fragment
-    // rows [16 j, 16 j + 16) of the table's transpose, columns 32 t on (t >= j / 2)
-    auto frag_up5 = [&](const bf16* tab, int j, int t) {
-        const s16x4 z = s16x4{0, 0, 0, 0};
-        const s16x4 lo = 2 * t >= j ? ds_tr16(tab + frag_at(2 * t, j) + ft) : z;
-        const s16x4 hi = ds_tr16(tab + frag_at(2 * t + 1, j) + ft);
-        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-    };
-
-    if (nc > 0) {
-        fetch_kq(nc - 1, K0, Q0);
-        fetch_tab(nc - 1);
-        fetch_rows(a.x, nc - 1, xr);
-        fetch_rows(a.dy, nc - 1, yr);
     }
-    auto chunk = [&](int c, const bf16* Ks, const bf16* Qs, bf16* Kn, bf16* Qn) {
-        const bool more = c > 0, last = c + 1 == nc;
-        wave_meet(true);  // the chunk's tiles have landed
-        if (TWO && more) fetch_kq(c - 1, Kn, Qn);
-        // h' (the state entering the next chunk), consumed once the first products are under way
-        bf16x8 hi[KS][CT];
-        s16x8 hl[KS][CT];
-        {  // (the last chunk's is hend; its loads here are of some other chunk's, unused)
-            const int64_t so = (item(last ? c : c + 1) - bh) * P * N;
+    // this wave's state tiles to LDS operands dst[ks][term][ct][lane][8]
+    __device__ __forceinline__ void put_state(bf16* dst, const f32x4 (&acc)[OT][CT]) const {
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
+        for (int o = 0; o < OT; o += 2)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                Sp<bf16> sp;
+                const int t = OT * w + o;
+                split8(join(acc[o][ct], acc[o + 1 < OT ? o + 1 : o][ct]), sp);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    bf16* d = dst + (((t >> 1) * 3 + k) * CT + ct) * 512 + lane * 8;
+                    if (OT > 1) st8(d, sp.t[k]);
+                    else st4(d + 4 * (t & 1), __builtin_shufflevector(sp.t[k], sp.t[k], 0, 1, 2, 3));
+                }
+            }
+    }
+    // token tile w's values to LDS operands dst[t][term][ct][lane][8] of TS terms
+    template <int TS>
+    __device__ __forceinline__ void put_rows(bf16* dst, const f32x4 (&v)[CT]) const {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            bf16x4 o[TS];
+            split4<TS>(v[ct], o);
+#pragma unroll
+            for (int k = 0; k < TS; ++k) st4(dst + (((w >> 1) * TS + k) * CT + ct) * 512 + lane * 8 + 4 * (w & 1), o[k]);
+        }
+    }
+    template <int TS>
+    __device__ __forceinline__ bf16x8 get(const bf16* src, int t, int k, int ct) const {
+        return ld8(src + ((t * TS + k) * CT + ct) * 512 + lane * 8);
+    }
+};
+__device__ __forceinline__ f32x4 floats(s16x4 v) { return floats(__builtin_bit_cast(u32x2v, v)); }
+
+template <int N, int CT, int KB, bool SAVE>
+__global__ __launch_bounds__(256) void k_delta_team(Args a) {
+    constexpr int KS = N / 32, TILE = Dma<N>::TILE, OT = Team<N, CT>::OT;
+    constexpr int TABN = SAVE ? kFragTab2 : kFragTab, NV = SAVE ? 3 : 2, QT = SAVE ? 3 : 2, MT = SAVE ? 3 : 1, UT = SAVE ? 3 : 2;
+    __shared__ __attribute__((aligned(16))) bf16 K0[TILE];
+    __shared__ __attribute__((aligned(16))) bf16 K1[KB == 2 ? TILE : 8];
+    __shared__ __attribute__((aligned(16))) bf16 Qs[TILE];
+    __shared__ __attribute__((aligned(16))) bf16 Sf[TABN];
+    __shared__ __attribute__((aligned(16))) float Vs[NV * L];
+    __shared__ __attribute__((aligned(16))) bf16 Hf[KS * 3 * CT * 512];
+    __shared__ __attribute__((aligned(16))) bf16 Rf[2 * 3 * CT * 512];
+    __shared__ __attribute__((aligned(16))) bf16 Uf[2 * UT * CT * 512];
+    __shared__ __attribute__((aligned(16))) bf16 Wf[2 * 3 * CT * 512];
+    __shared__ __attribute__((aligned(16))) bf16 Xs[CT * 1024];
+    __shared__ __attribute__((aligned(16))) bf16 Ys[SAVE ? CT * 1024 : 8];
+    const bf16* Mf = Sf + 3 * 5 * 512;
+    const Team<N, CT> tm(a);
+    const int lane = tm.lane, w = tm.w, l16 = tm.l16, q = tm.q, nc = tm.nc, t0w = OT * w;
+
+    f32x4 acc[OT][CT];
+#pragma unroll
+    for (int o = 0; o < OT; ++o)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+            acc[o][ct] = a.h0 ? ld4(a.h0 + tm.hn(t0w + o, ct)) : f32x4{0.f, 0.f, 0.f, 0.f};
+    auto store_rows = [&](void* base, int c, const f32x4(&v)[CT]) {
+        const brsrc r = tm.x_rsrc(base, c);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) store_rows16(r, v[ct], tm.xo + ct * 32, w, tm.rsx, tm.sel, tm.upper);
+    };
+    if (nc > 0) {
+        tm.fetch_tile(a.B, 0, K0);
+        tm.fetch_tile(a.C, 0, Qs);
+        tm.template fetch_tab<TABN, NV>(0, Sf, Vs);
+        tm.fetch_x(a.x, 0, Xs);
+        if (SAVE) tm.fetch_x(a.dy, 0, Ys);
+        tm.put_state(Hf, acc);
+    }
+    auto chunk = [&](int c, const bf16* Ks, bf16* Kn) {
+        const bool more = c + 1 < nc;
+        wave_meet(true);  // the chunk's tiles have landed, the state's operands are in place
+        if (KB == 2 && more) tm.fetch_tile(a.B, c + 1, Kn);
+        if (SAVE) {
+            const int64_t so = (tm.item(c) - tm.bh) * a.P * N;
+#pragma unroll
+            for (int o = 0; o < OT; o += 2)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-                    hi[ks][ct] = ld8(static_cast<const bf16*>(a.hin) + so + hn(2 * ks, ct));
-                    hl[ks][ct] = *reinterpret_cast<const s16x8*>(a.hlo + so + hn(2 * ks, ct));
+                    bf16x8 hi;
+                    s16x8 lo;
+                    split_state(join(acc[o][ct], acc[o + 1 < OT ? o + 1 : o][ct]), hi, lo);
+                    bf16* hp = static_cast<bf16*>(a.hin) + so + tm.hn(t0w + o, ct);
+                    short* lp = a.hlo + so + tm.hn(t0w + o, ct);
+                    if (OT > 1) {
+                        st8(hp, hi);
+                        *reinterpret_cast<s16x8*>(lp) = lo;
+                    } else {
+                        st4(hp, __builtin_shufflevector(hi, hi, 0, 1, 2, 3));
+                        *reinterpret_cast<s16x4*>(lp) = __builtin_shufflevector(lo, lo, 0, 1, 2, 3);
+                    }
                 }
         }
-        // dU = e^{c_L - c} K dh'^T + M^T dY
-        f32x4 v[4][CT];
+        // K h^T and Q h^T of token tile w, two accumulators each
+        f32x4 v[CT], yq[CT], v2[CT], y2[CT];
 #pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) v[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int ct = 0; ct < CT; ++ct) v[ct] = yq[ct] = v2[ct] = y2[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            Sp<bf16> hs[CT];
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) split8(join(acc[2 * ks][ct], acc[2 * ks + 1][ct]), hs[ct]);
-            bf16x8 kf[4];
-#pragma unroll
-            for (int it = 0; it < 4; ++it) kf[it] = ld8(Ks + (ka ^ (ks << 5)) + it * 16 * N);
+            const bf16x8 kf = tm.frag_rows16(Ks, w, ks), qf = tm.frag_rows16(Qs, w, ks);
 #pragma unroll
             for (int k = 0; k < 3; ++k)
 #pragma unroll
-                for (int it = 0; it < 4; ++it)
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) v[it][ct] = mma(v[it][ct], kf[it], hs[ct].t[k]);
-        }
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-            const f32x4 ew = ld4(Vs + L + it * 16 + 4 * q);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) v[it][ct] *= ew;
-        }
-        bf16x8 dyf[2][CT];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-            {
-                const u32x2v lo = quad_t(yr[2 * t][ct], sel, upper), hi2 = quad_t(yr[2 * t + 1][ct], sel, upper);
-                dyf[t][ct] = __builtin_bit_cast(bf16x8, u32x4v{lo[0], lo[1], hi2[0], hi2[1]});
-            }
-        if (more) fetch_rows(a.dy, c - 1, yr);
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                bf16x8 mf[4];
-#pragma unroll
-                for (int it = 0; it <= 2 * t + 1; ++it) mf[it] = frag_up5(Mf + k * 5 * 512, it, t);
-#pragma unroll
-                for (int it = 0; it <= 2 * t + 1; ++it)
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) v[it][ct] = mma(v[it][ct], mf[it], dyf[t][ct]);
-            }
-        {  // <dh', h'> over this wave's columns, and dh' for the gradients of B
-            const int64_t lo = (item(c) - bh) * P * N;
-            float s = 0.f;
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-                    f32x8 hv;
-                    if (last) {
-                        hv = ld8(a.hend + hn(2 * ks, ct));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) hv[i] = join_state(hi[ks][ct][i], hl[ks][ct][i]);
-                    }
-                    const f32x8 av = join(acc[2 * ks][ct], acc[2 * ks + 1][ct]);
-                    Sp<bf16> o;
-                    split8<1>(av, o);
-                    st8(static_cast<bf16*>(a.lin) + lo + hn(2 * ks, ct), o.t[0]);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) s += hv[i] * av[i];
+                    const bf16x8 hf = tm.template get<3>(Hf, ks, k, ct);
+                    f32x4 &vv = ks & 1 ? v2[ct] : v[ct], &yy = ks & 1 ? y2[ct] : yq[ct];
+                    vv = mma(vv, kf, hf);
+                    if (k < QT) yy = mma(yy, qf, hf);
                 }
-#pragma unroll
-            for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
-            if (lane == 0) tots[w] = s;
         }
-        // z = dU - S^T (beta dU)
-        Sp<bf16> b2[2][CT];
-        auto operands = [&](const float* s1, float sign) {  // sign s1_t v_t
+        const f32x4 ec = ld4(Vs + w * 16 + 4 * q);
+        f32x4 bt = f32x4{1.f, 1.f, 1.f, 1.f};
+        if (SAVE) bt = ld4(Vs + 2 * L + w * 16 + 4 * q);
+        f32x4 rb[CT];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            v[ct] = floats(tm.x_tile(Xs, w, ct)) - ec * (v[ct] + v2[ct]);
+            yq[ct] = ec * (yq[ct] + y2[ct]);
+            rb[ct] = v[ct] * bt;
+        }
+        tm.template put_rows<3>(Rf, rb);
+        wave_meet(false);  // R is in place; every wave is done with Q
+        if (more) {
+            tm.fetch_tile(a.C, c + 1, Qs);
+            tm.fetch_x(a.x, c + 1, Xs);
+        }
+        // r = R - S beta R, over the tiles up to w
+        auto table = [&](f32x4(&o)[CT], const bf16* tab, const bf16* src, auto terms, auto order, auto st) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const f32x4 sa = ld4(s1 + 32 * t + 4 * q) * sign, sb = ld4(s1 + 32 * t + 16 + 4 * q) * sign;
+                if (t > (w >> 1)) break;
+                const int lo = w == 2 && t == 1 ? 4 : w == 0 ? 0 : (w < 3 ? w : 3 + t) * 512;
+                const int hi = w < 3 && t == (w >> 1) && !(w & 1) ? lo : lo + 4;  // (no such block: zero)
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) split8(join(v[2 * t][ct] * sa, v[2 * t + 1][ct] * sb), b2[t][ct]);
+                for (int k = 0; k < decltype(terms)::value; ++k) {
+                    const bf16* tk = tab + k * 5 * 512 + lane * 8;
+                    u32x2 h2 = __builtin_bit_cast(u32x2, ld4(tk + hi));
+                    if (hi == lo) h2 = u32x2{0, 0};
+                    const bf16x8 f = join(ld4(tk + lo), __builtin_bit_cast(bf16x4, h2));
+#pragma unroll
+                    for (int m = 0; m < decltype(order)::value - k; ++m)
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct)
+                            o[ct] = mma(o[ct], f, tm.template get<decltype(st)::value>(src, t, m, ct));
+                }
             }
         };
-        operands(Vs + 2 * L, 1.f);
+        typedef std::integral_constant<int, 3> three;
+        table(v, Sf, Rf, three(), three(), three());
+        const f32x4 ew = ld4(Vs + L + w * 16 + 4 * q) * bt;
+        f32x4 uw[CT];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int ct = 0; ct < CT; ++ct) {
+            rb[ct] = v[ct] * bt;
+            uw[ct] = v[ct] * ew;
+        }
+        tm.template put_rows<UT>(Uf, rb);
+        tm.template put_rows<3>(Wf, uw);
+        const float el = Vs[L - 1];
+        wave_meet(false);  // r and the weighted u are in place
+        // Y = e^c Q h^T + M beta r
+        table(yq, Mf, Uf, std::integral_constant<int, MT>(), std::integral_constant<int, UT>(), std::integral_constant<int, UT>());
+        f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f};  // SAVE: dY . Y
+        if (SAVE) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) d += floats(tm.x_tile(Ys, w, ct)) * yq[ct];
+        }
+        wave_meet(false);  // every wave is done with the tables
+        if (more) {
+            tm.template fetch_tab<TABN, NV>(c + 1, Sf, Vs);
+            if (SAVE) tm.fetch_x(a.dy, c + 1, Ys);
+        }
+        // h' = e^{c_L} h + K^T (e^{c_L - c} u) of this wave's tiles
+#pragma unroll
+        for (int o = 0; o < OT; ++o)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) acc[o][ct] *= el;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            bf16x8 kf[OT];
+#pragma unroll
+            for (int o = 0; o < OT; ++o) kf[o] = tm.frag_t(Ks + ks * 32 * N, t0w + o);
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    const bf16x8 wf = tm.template get<3>(Wf, ks, k, ct);
+#pragma unroll
+                    for (int o = 0; o < OT; ++o) acc[o][ct] = mma(acc[o][ct], kf[o], wf);
+                }
+        }
+        if (more) tm.put_state(Hf, acc);
+        if (SAVE) {
+            f32x4 rest[CT];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) rest[ct] = rest16(v[ct]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i] = row_sum16(d[i]);
+            const int t = w * 16 + 4 * q + (l16 & 3);
+            const float dt = l16 & 2 ? (l16 & 1 ? d[3] : d[2]) : (l16 & 1 ? d[1] : d[0]);
+            if (l16 < 4 && t < tm.rows_left(c))
+                a.dyy[((int64_t)tm.sl * a.rows.nrows * a.H + tm.bh) * a.T + (int64_t)c * L + t] = dt;
+            store_rows(a.r, c, v);
+            store_rows(a.rlo, c, rest);
+        } else {
+            store_rows(a.y, c, yq);
+        }
+        if (KB == 1 && more) {
+            wave_meet(false);  // every wave is done with K
+            tm.fetch_tile(a.B, c + 1, Kn);
+        }
+    };
+    for (int c = 0; c < nc; c += 2) {
+        chunk(c, K0, KB == 2 ? K1 : K0);
+        if (c + 1 < nc) chunk(c + 1, KB == 2 ? K1 : K0, K0);
+    }
+    if (float* hT = SAVE ? a.hend : a.hT) {
+#pragma unroll
+        for (int o = 0; o < OT; ++o)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) st4(hT + tm.hn(t0w + o, ct), acc[o][ct]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// k_delta_adj: the adjoint walk by the same teams (chunks in reverse, dh^T in accumulators); the
+// tables' transposes are read from the same fragments by transposing loads.  Outputs as
+// k_delta_rev.
+// ---------------------------------------------------------------------------
+template <int N, int CT, int KB>
+__global__ __launch_bounds__(256) void k_delta_adj(Args a) {
+    constexpr int KS = N / 32, TILE = Dma<N>::TILE, OT = Team<N, CT>::OT, TABN = kFragTab2;
+    __shared__ __attribute__((aligned(16))) bf16 K0[TILE];
+    __shared__ __attribute__((aligned(16))) bf16 K1[KB == 2 ? TILE : 8];
+    __shared__ __attribute__((aligned(16))) bf16 Qs[TILE];
+    __shared__ __attribute__((aligned(16))) bf16 Sf[TABN];
+    __shared__ __attribute__((aligned(16))) float Vs[3 * L];
+    __shared__ __attribute__((aligned(16))) bf16 Hf[KS * 3 * CT * 512];
+    __shared__ __attribute__((aligned(16))) bf16 Rf[2 * 3 * CT * 512];
+    __shared__ __attribute__((aligned(16))) bf16 Wf[2 * 3 * CT * 512];  // -e^c dX
+    __shared__ __attribute__((aligned(16))) bf16 Yf[2 * 3 * CT * 512];  // e^c dY
+    __shared__ __attribute__((aligned(16))) bf16 Xs[CT * 1024];
+    __shared__ __attribute__((aligned(16))) bf16 Ys[CT * 1024];
+    __shared__ float tots[4];
+    const bf16* Mf = Sf + 3 * 5 * 512;
+    const Team<N, CT> tm(a);
+    const int lane = tm.lane, w = tm.w, l16 = tm.l16, q = tm.q, nc = tm.nc, t0w = OT * w;
+    const int64_t BH = (int64_t)a.rows.nrows * a.H;
+
+    f32x4 acc[OT][CT];
+#pragma unroll
+    for (int o = 0; o < OT; ++o)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+            acc[o][ct] = a.dhT ? ld4(a.dhT + tm.hn(t0w + o, ct)) : f32x4{0.f, 0.f, 0.f, 0.f};
+    auto store_rows = [&](void* base, int c, const f32x4(&v)[CT]) {
+        const brsrc r = tm.x_rsrc(base, c);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) store_rows16(r, v[ct], tm.xo + ct * 32, w, tm.rsx, tm.sel, tm.upper);
+    };
+    const int ft = (4 * q + (l16 >> 2) + 16 * (l16 & 3)) * 8;  // four columns of a block's row, in a fragment
+    // rows of tile w of the table's transpose, columns 32 t on (t >= w / 2)
+    auto frag_up = [&](const bf16* tab, int t) {
+        const s16x4 z = s16x4{0, 0, 0, 0};
+        auto at = [&](int i) { return i == 2 && w == 2 ? 4 : i == 0 ? 0 : (i < 3 ? i : 3 + (w >> 1)) * 512 + 4 * (w & 1); };
+        const s16x4 lo = 2 * t >= w ? ds_tr16(tab + at(2 * t) + ft) : z;
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, ds_tr16(tab + at(2 * t + 1) + ft), 0, 1, 2, 3, 4,
+                                                                  5, 6, 7));
+    };
+    if (nc > 0) {
+        tm.fetch_tile(a.B, nc - 1, K0);
+        tm.template fetch_tab<TABN, 3>(nc - 1, Sf, Vs);
+        tm.fetch_x(a.x, nc - 1, Xs);
+        tm.fetch_x(a.dy, nc - 1, Ys);
+        tm.put_state(Hf, acc);
+    }
+    auto chunk = [&](int c, const bf16* Ks, bf16* Kn) {
+        const bool more = c > 0, last = c + 1 == nc;
+        wave_meet(true);  // the chunk's tiles have landed, the adjoint's operands are in place
+        tm.fetch_tile(a.C, c, Qs);  // read last in the chunk
+        if (KB == 2 && more) tm.fetch_tile(a.B, c - 1, Kn);
+        // h' (the state entering the next chunk), consumed once the first products are under way
+        // (the last chunk's is hend; its loads here are unused)
+        constexpr int OP = (OT + 1) / 2;
+        bf16x8 hi[OP][CT];
+        s16x8 hl[OP][CT];
+        {
+            const int64_t so = (tm.item(last ? c : c + 1) - tm.bh) * a.P * N;
+#pragma unroll
+            for (int o = 0; o < OP; ++o)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    const bf16* hp = static_cast<const bf16*>(a.hin) + so + tm.hn(t0w + 2 * o, ct);
+                    const short* lp = a.hlo + so + tm.hn(t0w + 2 * o, ct);
+                    if (OT > 1) {
+                        hi[o][ct] = ld8(hp);
+                        hl[o][ct] = *reinterpret_cast<const s16x8*>(lp);
+                    } else {
+                        hi[o][ct] = join(ld4(hp), ld4(hp));
+                        const s16x4 l4 = *reinterpret_cast<const s16x4*>(lp);
+                        hl[o][ct] = __builtin_shufflevector(l4, l4, 0, 1, 2, 3, 4, 5, 6, 7);
+                    }
+                }
+        }
+        // dU = e^{c_L - c} K dh'^T + M^T dY of token tile w
+        f32x4 v[CT], v2[CT];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) v[ct] = v2[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            const bf16x8 kf = tm.frag_rows16(Ks, w, ks);
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    f32x4& vv = ks & 1 ? v2[ct] : v[ct];
+                    vv = mma(vv, kf, tm.template get<3>(Hf, ks, k, ct));
+                }
+        }
+        const f32x4 ec = ld4(Vs + w * 16 + 4 * q), ew = ld4(Vs + L + w * 16 + 4 * q),
+                    bt = ld4(Vs + 2 * L + w * 16 + 4 * q);
+        f32x4 rb[CT], yw[CT];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            v[ct] = ew * (v[ct] + v2[ct]);
+            yw[ct] = ec * floats(tm.x_tile(Ys, w, ct));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (t < (w >> 1)) continue;
+                const bf16x8 dyf = __builtin_bit_cast(
+                    bf16x8, __builtin_shufflevector(tm.x_tile(Ys, 2 * t, ct), tm.x_tile(Ys, 2 * t + 1, ct), 0, 1, 2, 3, 4,
+                                                    5, 6, 7));
+#pragma unroll
+                for (int k = 0; k < 3; ++k) v[ct] = mma(v[ct], frag_up(Mf + k * 5 * 512, t), dyf);
+            }
+            rb[ct] = v[ct] * bt;
+        }
+        tm.template put_rows<3>(Rf, rb);
+        tm.template put_rows<3>(Yf, yw);
+        wave_meet(false);  // beta dU is in place; every wave is done with dY
+        if (more) tm.fetch_x(a.dy, c - 1, Ys);
+        {  // <dh', h'> over this wave's tiles, and dh' for the gradients of B
+            const int64_t lo = (tm.item(c) - tm.bh) * a.P * N;
+            float s = 0.f;
+#pragma unroll
+            for (int o = 0; o < OP; ++o)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    const f32x8 av = join(acc[2 * o][ct], acc[2 * o + 1 < OT ? 2 * o + 1 : 2 * o][ct]);
+                    f32x8 hv;
+                    if (last) {
+                        const float* hp = a.hend + tm.hn(t0w + 2 * o, ct);
+                        hv = join(ld4(hp), ld4(OT > 1 ? hp + 4 : hp));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) hv[i] = join_state(hi[o][ct][i], hl[o][ct][i]);
+                    }
+                    Sp<bf16> ov;
+                    split8<1>(av, ov);
+                    bf16* lp = static_cast<bf16*>(a.lin) + lo + tm.hn(t0w + 2 * o, ct);
+                    if (OT > 1) st8(lp, ov.t[0]);
+                    else st4(lp, __builtin_shufflevector(ov.t[0], ov.t[0], 0, 1, 2, 3));
+#pragma unroll
+                    for (int i = 0; i < (OT > 1 ? 8 : 4); ++i) s += hv[i] * av[i];
+                }
+            s = row_sum16(s);
+            s += __shfl_xor(s, 16, 64);
+            s += __shfl_xor(s, 32, 64);
+            if (lane == 0) tots[w] = s;
+        }
+        // z = dU - S^T (beta dU), over the tiles from w on
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if (t < (w >> 1)) continue;
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
-                bf16x8 sf[4];
-#pragma unroll
-                for (int it = 0; it <= 2 * t + 1; ++it) sf[it] = frag_up5(Sf + k * 5 * 512, it, t);
+                const bf16x8 f = frag_up(Sf + k * 5 * 512, t);
 #pragma unroll
                 for (int m = 0; m < 3 - k; ++m)
 #pragma unroll
-                    for (int it = 0; it <= 2 * t + 1; ++it)
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) v[it][ct] = mma(v[it][ct], sf[it], b2[t][ct].t[m]);
+                    for (int ct = 0; ct < CT; ++ct) v[ct] = mma(v[ct], f, tm.template get<3>(Rf, t, m, ct));
             }
-        // z leaves in two terms, dX = beta z, its dot with X
-        store_rows(a.z, c, v);
-        {
-            f32x4 rest[4][CT];
-            float dot[16];
+        }
+        f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f}, rest[CT], dx[CT], wv[CT];
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                const f32x4 bt = ld4(Vs + 2 * L + it * 16 + 4 * q);
-                f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int ct = 0; ct < CT; ++ct) {
+            rest[ct] = rest16(v[ct]);
+            dx[ct] = v[ct] * bt;
+            wv[ct] = dx[ct] * -ec;
+            d += floats(tm.x_tile(Xs, w, ct)) * dx[ct];
+        }
+        tm.template put_rows<3>(Wf, wv);
+        const float el = Vs[L - 1];
+        wave_meet(true);  // dX is in place, Q has landed; every wave is done with the tables
+        if (more) {
+            tm.template fetch_tab<TABN, 3>(c - 1, Sf, Vs);
+            tm.fetch_x(a.x, c - 1, Xs);
+        }
+        store_rows(a.z, c, v);
+        store_rows(a.zlo, c, rest);
+        store_rows(a.dx, c, dx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = row_sum16(d[i]);
+        {
+            const int t = w * 16 + 4 * q + (l16 & 3);
+            const float dt = l16 & 2 ? (l16 & 1 ? d[3] : d[2]) : (l16 & 1 ? d[1] : d[0]);
+            if (l16 < 4 && t < tm.rows_left(c)) a.dxx[((int64_t)tm.sl * BH + tm.bh) * a.T + (int64_t)c * L + t] = dt;
+            if (threadIdx.x == 0)
+                a.tot[(int64_t)tm.sl * a.ntab * a.H + tm.item(c)] = (tots[0] + tots[1]) + (tots[2] + tots[3]);
+        }
+        // dh = e^{c_L} dh' - K^T (e^c dX) + Q^T (e^c dY) of this wave's tiles
+#pragma unroll
+        for (int o = 0; o < OT; ++o)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) acc[o][ct] *= el;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            bf16x8 kf[OT], qf[OT];
+#pragma unroll
+            for (int o = 0; o < OT; ++o) {
+                kf[o] = tm.frag_t(Ks + ks * 32 * N, t0w + o);
+                qf[o] = tm.frag_t(Qs + ks * 32 * N, t0w + o);
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-                    rest[it][ct] = rest16(v[it][ct]);
-                    v[it][ct] *= bt;
-                    d += floats(quad_t(xr[it][ct], sel, upper)) * v[it][ct];
+                    const bf16x8 wf = tm.template get<3>(Wf, ks, k, ct), yf = tm.template get<3>(Yf, ks, k, ct);
+#pragma unroll
+                    for (int o = 0; o < OT; ++o) acc[o][ct] = mma(acc[o][ct], kf[o], wf);
+#pragma unroll
+                    for (int o = 0; o < OT; ++o) acc[o][ct] = mma(acc[o][ct], qf[o], yf);
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dot[it * 4 + i] = d[i];
-            }
-            dots[w * L + (l16 >> 2) * 16 + 4 * q + (l16 & 3)] = row_sums16(dot, l16);
-            store_rows(a.zlo, c, rest);
         }
-        if (more) fetch_rows(a.x, c - 1, xr);
-        store_rows(a.dx, c, v);
-        // dh = e^{c_L} dh' - K^T (e^c dX) + Q^T (e^c dY)
-        operands(Vs, -1.f);
-        const float el = Vs[L - 1];
-        Sp<bf16> d2[2][CT];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const f32x4 sa = ld4(Vs + 32 * t + 4 * q), sb = ld4(Vs + 32 * t + 16 + 4 * q);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                f32x8 d;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) d[i] = to_f(dyf[t][ct][i]) * (i < 4 ? sa[i & 3] : sb[i & 3]);
-                split8(d, d2[t][ct]);
-            }
-        }
-        wave_meet(false);  // every wave is done with the tables; the sums are in place
-        if (more) fetch_tab(c - 1);
-        for (int t = tid; t < rows_left(c); t += blockDim.x) {
-            float s = 0.f;
-            for (int k = 0; k < nw; ++k) s += dots[k * L + t];
-            a.dxx[((int64_t)sl * BH + bh) * a.T + (int64_t)c * L + t] = s;
-        }
-        if (tid == 0) {
-            float s = 0.f;
-            for (int k = 0; k < nw; ++k) s += tots[k];
-            a.tot[(int64_t)sl * a.ntab * H + item(c)] = s;
-        }
-#pragma unroll
-        for (int t4 = 0; t4 < NTL; t4 += 4)
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                bf16x8 kf[4], qf[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    kf[t] = frag_t(Ks + ks * 32 * N, t4 + t);
-                    qf[t] = frag_t(Qs + ks * 32 * N, t4 + t);
-                }
-                if (ks == 0) {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) acc[t4 + t][ct] *= el;
-                }
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct)
-                            acc[t4 + t][ct] = mma(acc[t4 + t][ct], kf[t], b2[ks][ct].t[k]);
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct)
-                            acc[t4 + t][ct] = mma(acc[t4 + t][ct], qf[t], d2[ks][ct].t[k]);
-            }
-        if (!TWO && more) {
-            wave_meet(false);  // every wave is done with K and Q
-            fetch_kq(c - 1, Kn, Qn);
+        if (more) tm.put_state(Hf, acc);
+        if (KB == 1 && more) {
+            wave_meet(false);  // every wave is done with K
+            tm.fetch_tile(a.B, c - 1, Kn);
         }
     };
     for (int c = nc - 1; c >= 0; c -= 2) {
-        if (TWO) {
-            chunk(c, K0, Q0, K1, Q1);
-            if (c > 0) chunk(c - 1, K1, Q1, K0, Q0);
-        } else {
-            chunk(c, K0, Q0, K0, Q0);
-            if (c > 0) chunk(c - 1, K0, Q0, K0, Q0);
-        }
+        chunk(c, K0, KB == 2 ? K1 : K0);
+        if (c > 0) chunk(c - 1, KB == 2 ? K1 : K0, K0);
     }
     if (a.dh0) {
 #pragma unroll
-        for (int t = 0; t < NTL; ++t)
+        for (int o = 0; o < OT; ++o)
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) st4(a.dh0 + hn(t, ct), acc[t][ct]);
+            for (int ct = 0; ct < CT; ++ct) st4(a.dh0 + tm.hn(t0w + o, ct), acc[o][ct]);
     }
 }
 

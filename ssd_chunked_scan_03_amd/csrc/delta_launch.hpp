@@ -31,10 +31,10 @@ inline int grad_shares(int64_t chunks, int64_t H, int64_t G, int64_t N) {
 }
 
 inline bool dma_walk(bool bf16_dtype, int64_t N);
-inline int adj_waves(int64_t P);
+inline int team_tiles(int64_t bh, int64_t P, int64_t N);
 // Slices of headdim that the backward's walks write partial sums for.
 inline int64_t bwd_slices(bool bf16_dtype, int64_t bh, int64_t P, int64_t N) {
-    return P / (dma_walk(bf16_dtype, N) ? 16 * adj_waves(P) : slice_of(bf16_dtype, bh, P, N).cols());
+    return P / (dma_walk(bf16_dtype, N) ? 16 * team_tiles(bh, P, N) : slice_of(bf16_dtype, bh, P, N).cols());
 }
 
 template <typename K>
@@ -89,34 +89,50 @@ void prep(const Args& a) {
     k_delta_prep<T, N, TAB><<<(unsigned)((waves + 3) / 4), 256, 0, a.stream>>>(a, heads);
 }
 
-template <int N, int CT, int KB, int OCC, bool SAVE = false>
+template <int N, int CT, int KB, int OCC>
 int walk_dma(const Args& a, int waves) {
     const unsigned grid = (unsigned)((int64_t)a.rows.nrows * a.H * (a.P / (16 * CT * waves)));
-    k_delta_dma<N, CT, KB, OCC, SAVE><<<grid, 64 * waves, 0, a.stream>>>(a);
+    k_delta_dma<N, CT, KB, OCC><<<grid, 64 * waves, 0, a.stream>>>(a);
     return hipGetLastError() == hipSuccess ? 0 : 7;
 }
-// The backward's two walks: four waves of one column tile.
-inline int adj_waves(int64_t P) { return P >= 64 ? 4 : (int)(P / 16); }
-template <int N>
+// Column tiles per team: one, or two where that still gives every CU a team (the key and table
+// fragments are then read once for both; at dstate 256 the state's operands leave no room).
+inline int team_tiles(int64_t bh, int64_t P, int64_t N) { return N <= 128 && P >= 32 && bh * P > 256 * 16 ? 2 : 1; }
+template <int N, int CT, bool SAVE>
+int walk_team(const Args& a) {
+    const unsigned grid = (unsigned)((int64_t)a.rows.nrows * a.H * (a.P / (16 * CT)));
+    // (at dstate 256 the backward's tables leave room for one K buffer only)
+    k_delta_team<N, CT, N == 256 && SAVE ? 1 : 2, SAVE><<<grid, 256, 0, a.stream>>>(a);
+    return hipGetLastError() == hipSuccess ? 0 : 7;
+}
+template <int N, int CT>
 int walks_bwd(const Args& a) {
-    const int waves = adj_waves(a.P);
-    const unsigned grid = (unsigned)((int64_t)a.rows.nrows * a.H * (a.P / (16 * waves)));
-    constexpr int OCC = N == 256 ? 1 : 2;
-    const int st = walk_dma<N, 1, 2, OCC, true>(a, waves);
+    const int st = walk_team<N, CT, true>(a);
     if (st) return st;
-    k_delta_adj<N, 1, OCC><<<grid, 64 * waves, 0, a.stream>>>(a);
+    const unsigned grid = (unsigned)((int64_t)a.rows.nrows * a.H * (a.P / (16 * CT)));
+    k_delta_adj<N, CT, N == 256 ? 1 : 2><<<grid, 256, 0, a.stream>>>(a);
     return hipGetLastError() == hipSuccess ? 0 : 7;
 }
+// Few chains: a team of four waves per 16 columns, while that leaves two work-groups per CU
+// or less of the other kind (a wave per 16 or 32 columns).
+inline bool team_walk(int64_t bh, int64_t P) { return bh * P < 512 * 64; }
 
 template <typename T, int N>
 int run_fwd(const Args& a) {
     if constexpr (std::is_same<T, bf16>::value && N >= 64) {
         prep<T, N, kFold>(a);
+        const int64_t bh = (int64_t)a.rows.nrows * a.H;
+        if (team_walk(bh, a.P)) {
+            if constexpr (N <= 128) {
+                if (team_tiles(bh, a.P, N) == 2) return walk_team<N, 2, false>(a);
+            }
+            return walk_team<N, 1, false>(a);
+        }
         const int waves = a.P >= 64 ? 4 : a.P / 16;
         if constexpr (N <= 128) {
             if (a.P == 128) return walk_dma<N, 2, 2, 2>(a, 4);
             // more chains than two work-groups per CU hold: three, with one K buffer
-            if ((int64_t)a.rows.nrows * a.H > 512) return walk_dma<N, 1, 1, 3>(a, waves);
+            if (bh > 512) return walk_dma<N, 1, 1, 3>(a, waves);
             return walk_dma<N, 1, 2, 2>(a, waves);
         } else {
             return walk_dma<N, 1, 2, 1>(a, waves);
@@ -134,7 +150,11 @@ int run_bwd(const Args& a) {
     int st;
     if constexpr (std::is_same<T, bf16>::value && N >= 64) {
         prep<T, N, kBoth>(a);
-        st = walks_bwd<N>(a);
+        if constexpr (N <= 128) {
+            st = team_tiles((int64_t)a.rows.nrows * a.H, a.P, N) == 2 ? walks_bwd<N, 2>(a) : walks_bwd<N, 1>(a);
+        } else {
+            st = walks_bwd<N, 1>(a);
+        }
     } else {
         const Slice s = slice_of(std::is_same<T, bf16>::value, (int64_t)a.rows.nrows * a.H, a.P, N);
         prep<T, N, kPlain>(a);
