@@ -55,6 +55,9 @@ constexpr int kVec = 5 * L;           // floats of its e^c, e^{c_L - c}, beta an
 constexpr int kFragTab = (3 + 1) * 5 * 512;  // bfloat16 elements
 // The backward's: -S and M, three terms each, nothing folded.
 constexpr int kFragTab2 = (3 + 3) * 5 * 512;
+// Behind either, the decay factors of the walk (float32): e^c, e^{c_L - c} (times beta where
+// folded), and for the backward beta.
+constexpr int kFragVec = 512;  // bfloat16 elements (1 KiB, one transfer)
 enum Tab { kPlain, kFold, kBoth };  // tables as float32 blocks, the forward's, the backward's fragments
 constexpr int kFrag = 6;              // 16 x 32 operand fragments covering a triangular 64 x 64 table
 
@@ -418,6 +421,9 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(Args a, int heads) {
     const int h0 = g * Hg + hb * heads, h1 = min(g * Hg + Hg, h0 + heads);
     for (int h = h0; h < h1; ++h) {
         const int64_t e0 = kk * H + h;
+        float* St = a.tab + e0 * kTab;
+        T* Sg = reinterpret_cast<T*>(a.tab) + e0 * ((FOLD ? kFragTab : kFragTab2) + kFragVec);
+        T* Mg = Sg + 3 * 5 * 512;
         {
             const bool on = lane < n;
             const int64_t t = t0 + (on ? lane : 0);
@@ -430,10 +436,17 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(Args a, int heads) {
             const float hi = (float)v, lo = (float)(v - (double)hi);
             const float b = on ? to_f(static_cast<const T*>(a.beta)[t * H + h]) : 0.f;
             const float ew = exp2f_fast((float)(__shfl(v, 63, 64) - v));
-            float* vec = a.vec + e0 * kVec;
-            vec[lane] = exp2f_fast(hi);
-            vec[L + lane] = FOLD ? ew * b : ew;
+            const float ec = exp2f_fast(hi);
+            if (FRAG) {
+                float* fv = reinterpret_cast<float*>(Sg + (FOLD ? kFragTab : kFragTab2));
+                fv[lane] = ec;
+                fv[L + lane] = FOLD ? ew * b : ew;
+                if (!FOLD) fv[2 * L + lane] = b;
+            }
             if (!FOLD) {
+                float* vec = a.vec + e0 * kVec;
+                vec[lane] = ec;
+                vec[L + lane] = ew;
                 vec[2 * L + lane] = b;
                 vec[3 * L + lane] = hi;
                 vec[4 * L + lane] = lo;
@@ -453,9 +466,6 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(Args a, int heads) {
             sh[i] = m.chi[i * 16 + l16];
             sl[i] = m.clo[i * 16 + l16];
         }
-        float* St = a.tab + e0 * kTab;
-        T* Sg = reinterpret_cast<T*>(a.tab) + e0 * (FOLD ? kFragTab : kFragTab2);
-        T* Mg = Sg + 3 * 5 * 512;
         // a block's elements (this lane: row l16, columns 4q + e) in `terms` terms
         auto frags = [&](T* dst, int i, int j, f32x4 v, int terms) {
 #pragma unroll
@@ -889,10 +899,10 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
     auto fetch_k = [&](int c, bf16* kd) { dma_tile<N>(key_rsrc(a.B, c), kd, rsk, w, nw, lane); };
     auto fetch_q = [&](int c) { dma_tile<N>(key_rsrc(a.C, c), Qs, rsk, w, nw, lane); };
     auto fetch_tab = [&](int c) {
-        dma_run(make_rsrc(reinterpret_cast<const bf16*>(a.tab) + item(c) * kFragTab, kFragTab * 2),
-                reinterpret_cast<char*>(Sf), kFragTab / 512, w, nw, lane);
+        const bf16* src = reinterpret_cast<const bf16*>(a.tab) + item(c) * (kFragTab + kFragVec);
+        dma_run(make_rsrc(src, kFragTab * 2), reinterpret_cast<char*>(Sf), kFragTab / 512, w, nw, lane);
         if (w == 0 && lane < 32)
-            dma_run(make_rsrc(a.vec + item(c) * kVec, 2 * L * 4), reinterpret_cast<char*>(Vs), 1, 0, 1, lane);
+            dma_run(make_rsrc(src + kFragTab, 2 * L * 4), reinterpret_cast<char*>(Vs), 1, 0, 1, lane);
     };
     const int xo = rows16_off(lane, rsx, p0);
     const unsigned sel = quad_sel(lane);
@@ -1121,16 +1131,21 @@ struct Team {
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + m * 512), 16, rw * rsk + j * 16, 0, 0, 0);
         }
     }
-    template <int ELEMS, int NV>
-    __device__ __forceinline__ void fetch_tab(int c, bf16* dst, float* vec) const {
+    // One transfer of no consequence (dst is written before it is read).  The compiler waits for
+    // every transfer in flight before it reads an LDS array that none ever goes to; an array
+    // that one goes to is waited for on its own account only.
+    __device__ __forceinline__ void mark(bf16* dst) const {
+        if (w == 0) dma_run(make_rsrc(a.tab, 1024), reinterpret_cast<char*>(dst), 1, 0, 1, lane);
+    }
+    // a chunk's table and factors, ELEMS bfloat16 elements in all
+    template <int ELEMS>
+    __device__ __forceinline__ void fetch_tab(int c, bf16* dst) const {
         const brsrc r = make_rsrc(reinterpret_cast<const bf16*>(a.tab) + item(c) * ELEMS, ELEMS * 2);
 #pragma unroll
         for (int k = 0; k < ELEMS / 512; k += 4)
             if (k + w < ELEMS / 512)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + (k + w) * 512), 16, (k + w) * 1024 + lane * 16, 0,
                                                          0, 0);
-        if (w == 0 && lane < NV * 16)
-            dma_run(make_rsrc(a.vec + item(c) * kVec, NV * L * 4), reinterpret_cast<char*>(vec), 1, 0, 1, lane);
     }
     // a chunk's 64 x 16 CT tile of x or dy: dst[ct][token][16]
     __device__ __forceinline__ void fetch_x(const void* base, int c, bf16* dst) const {
@@ -1191,19 +1206,18 @@ __device__ __forceinline__ f32x4 floats(s16x4 v) { return floats(__builtin_bit_c
 template <int N, int CT, int KB, bool SAVE>
 __global__ __launch_bounds__(256) void k_delta_team(Args a) {
     constexpr int KS = N / 32, TILE = Dma<N>::TILE, OT = Team<N, CT>::OT;
-    constexpr int TABN = SAVE ? kFragTab2 : kFragTab, NV = SAVE ? 3 : 2, QT = SAVE ? 3 : 2, MT = SAVE ? 3 : 1, UT = SAVE ? 3 : 2;
+    constexpr int TABN = (SAVE ? kFragTab2 : kFragTab) + kFragVec, QT = SAVE ? 3 : 2, MT = SAVE ? 3 : 1, UT = SAVE ? 3 : 2;
     __shared__ __attribute__((aligned(16))) bf16 K0[TILE];
     __shared__ __attribute__((aligned(16))) bf16 K1[KB == 2 ? TILE : 8];
     __shared__ __attribute__((aligned(16))) bf16 Qs[TILE];
     __shared__ __attribute__((aligned(16))) bf16 Sf[TABN];
-    __shared__ __attribute__((aligned(16))) float Vs[NV * L];
-    __shared__ __attribute__((aligned(16))) bf16 Hf[KS * 3 * CT * 512];
-    __shared__ __attribute__((aligned(16))) bf16 Rf[2 * 3 * CT * 512];
-    __shared__ __attribute__((aligned(16))) bf16 Uf[2 * UT * CT * 512];
-    __shared__ __attribute__((aligned(16))) bf16 Wf[2 * 3 * CT * 512];
     __shared__ __attribute__((aligned(16))) bf16 Xs[CT * 1024];
     __shared__ __attribute__((aligned(16))) bf16 Ys[SAVE ? CT * 1024 : 8];
+    constexpr int HF = KS * 3 * CT * 512, RF = 2 * 3 * CT * 512, UF = 2 * UT * CT * 512;
+    __shared__ __attribute__((aligned(16))) bf16 Ex[HF + 2 * RF + UF];  // operands passed between the waves
     const bf16* Mf = Sf + 3 * 5 * 512;
+    const float* Vs = reinterpret_cast<const float*>(Sf + TABN - kFragVec);
+    bf16 *Hf = Ex, *Rf = Hf + HF, *Wf = Rf + RF, *Uf = Wf + RF;
     const Team<N, CT> tm(a);
     const int lane = tm.lane, w = tm.w, l16 = tm.l16, q = tm.q, nc = tm.nc, t0w = OT * w;
 
@@ -1221,9 +1235,10 @@ __global__ __launch_bounds__(256) void k_delta_team(Args a) {
     if (nc > 0) {
         tm.fetch_tile(a.B, 0, K0);
         tm.fetch_tile(a.C, 0, Qs);
-        tm.template fetch_tab<TABN, NV>(0, Sf, Vs);
+        tm.template fetch_tab<TABN>(0, Sf);
         tm.fetch_x(a.x, 0, Xs);
         if (SAVE) tm.fetch_x(a.dy, 0, Ys);
+        tm.mark(Rf);
         tm.put_state(Hf, acc);
     }
     auto chunk = [&](int c, const bf16* Ks, bf16* Kn) {
@@ -1326,7 +1341,7 @@ __global__ __launch_bounds__(256) void k_delta_team(Args a) {
         }
         wave_meet(false);  // every wave is done with the tables
         if (more) {
-            tm.template fetch_tab<TABN, NV>(c + 1, Sf, Vs);
+            tm.template fetch_tab<TABN>(c + 1, Sf);
             if (SAVE) tm.fetch_x(a.dy, c + 1, Ys);
         }
         // h' = e^{c_L} h + K^T (e^{c_L - c} u) of this wave's tiles
@@ -1388,20 +1403,19 @@ __global__ __launch_bounds__(256) void k_delta_team(Args a) {
 // ---------------------------------------------------------------------------
 template <int N, int CT, int KB>
 __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
-    constexpr int KS = N / 32, TILE = Dma<N>::TILE, OT = Team<N, CT>::OT, TABN = kFragTab2;
+    constexpr int KS = N / 32, TILE = Dma<N>::TILE, OT = Team<N, CT>::OT, TABN = kFragTab2 + kFragVec;
     __shared__ __attribute__((aligned(16))) bf16 K0[TILE];
     __shared__ __attribute__((aligned(16))) bf16 K1[KB == 2 ? TILE : 8];
     __shared__ __attribute__((aligned(16))) bf16 Qs[TILE];
     __shared__ __attribute__((aligned(16))) bf16 Sf[TABN];
-    __shared__ __attribute__((aligned(16))) float Vs[3 * L];
-    __shared__ __attribute__((aligned(16))) bf16 Hf[KS * 3 * CT * 512];
-    __shared__ __attribute__((aligned(16))) bf16 Rf[2 * 3 * CT * 512];
-    __shared__ __attribute__((aligned(16))) bf16 Wf[2 * 3 * CT * 512];  // -e^c dX
-    __shared__ __attribute__((aligned(16))) bf16 Yf[2 * 3 * CT * 512];  // e^c dY
     __shared__ __attribute__((aligned(16))) bf16 Xs[CT * 1024];
     __shared__ __attribute__((aligned(16))) bf16 Ys[CT * 1024];
-    __shared__ float tots[4];
+    constexpr int HF = KS * 3 * CT * 512, RF = 2 * 3 * CT * 512;
+    __shared__ __attribute__((aligned(16))) bf16 Ex[HF + 3 * RF + 8];  // operands passed between the waves
     const bf16* Mf = Sf + 3 * 5 * 512;
+    const float* Vs = reinterpret_cast<const float*>(Sf + TABN - kFragVec);
+    bf16 *Hf = Ex, *Rf = Hf + HF, *Wf = Rf + RF, *Yf = Wf + RF;  // Wf: -e^c dX, Yf: e^c dY
+    float* tots = reinterpret_cast<float*>(Yf + RF);
     const Team<N, CT> tm(a);
     const int lane = tm.lane, w = tm.w, l16 = tm.l16, q = tm.q, nc = tm.nc, t0w = OT * w;
     const int64_t BH = (int64_t)a.rows.nrows * a.H;
@@ -1428,9 +1442,10 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
     };
     if (nc > 0) {
         tm.fetch_tile(a.B, nc - 1, K0);
-        tm.template fetch_tab<TABN, 3>(nc - 1, Sf, Vs);
+        tm.template fetch_tab<TABN>(nc - 1, Sf);
         tm.fetch_x(a.x, nc - 1, Xs);
         tm.fetch_x(a.dy, nc - 1, Ys);
+        tm.mark(Rf);
         tm.put_state(Hf, acc);
     }
     auto chunk = [&](int c, const bf16* Ks, bf16* Kn) {
@@ -1552,7 +1567,7 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
         const float el = Vs[L - 1];
         wave_meet(true);  // dX is in place, Q has landed; every wave is done with the tables
         if (more) {
-            tm.template fetch_tab<TABN, 3>(c - 1, Sf, Vs);
+            tm.template fetch_tab<TABN>(c - 1, Sf);
             tm.fetch_x(a.x, c - 1, Xs);
         }
         store_rows(a.z, c, v);

@@ -52,10 +52,10 @@ Layout layout_of(const ssd_problem* p, bool packed, bool bwd) {
         at = off;
         off += align_up(bytes);
     };
-    const size_t frag = !ssd::delta::dma_walk(p->dtype == SSD_BF16, N) ? 0
-                        : bwd ? ssd::delta::kFragTab2 * 2 : ssd::delta::kFragTab * 2;
-    take(o.tab, (size_t)(o.ntab * H) * (frag ? frag : kTab * 4));
-    take(o.vec, (size_t)(o.ntab * H) * kVec * 4);
+    const bool frag = ssd::delta::dma_walk(p->dtype == SSD_BF16, N);
+    take(o.tab, (size_t)(o.ntab * H) * (!frag ? kTab * 4
+                                        : ((bwd ? ssd::delta::kFragTab2 : ssd::delta::kFragTab) + ssd::delta::kFragVec) * 2));
+    if (bwd || !frag) take(o.vec, (size_t)(o.ntab * H) * kVec * 4);
     if (packed) {
         take(o.ts, (size_t)(b + 1) * 4);
         take(o.kb, (size_t)(b + 1) * 4);
