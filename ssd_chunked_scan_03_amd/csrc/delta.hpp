@@ -224,18 +224,37 @@ __device__ __forceinline__ u32x2v quad_t(u32x2v v, unsigned sel, bool upper) {
     const unsigned a2 = lane_turn<0x4E>(a), b2 = lane_turn<0x4E>(b);
     return upper ? u32x2v{b2, b} : u32x2v{a, a2};
 }
-// One wave's 64 tokens x 16 headdim columns of a [token][H P] tensor (resource at the chunk's
-// first token, rows past its end read as zero and drop stores), in accumulator order: two
-// words of two tokens each per 16-token tile.  xo: byte offset of this lane's token and columns.
-__device__ __forceinline__ int rows16_off(int lane, int rsx, int p0) {
-    return (4 * (lane >> 4) + (lane & 3)) * rsx + (p0 + (lane & 12)) * 2;
+// A wave's 16 CT headdim columns: lane l16 of column tile ct holds column 4 CT (l16 / 4) + 4 ct +
+// l16 % 4 of them, so that after the transpose a lane has 4 CT neighbours of one token.
+template <int CT>
+__device__ __forceinline__ constexpr int tile_col(int l16, int ct) { return 4 * CT * (l16 >> 2) + 4 * ct + (l16 & 3); }
+// Those columns of token tile `it` in a [token][H P] tensor (resource at the chunk's first token,
+// rows past its end read as zero and drop stores).  xo: byte offset of this lane's token and
+// columns.
+template <int CT>
+__device__ __forceinline__ int rows_off(int lane, int rsx, int p0) {
+    return (4 * (lane >> 4) + (lane & 3)) * rsx + (p0 + 4 * CT * ((lane & 15) >> 2)) * 2;
 }
-__device__ __forceinline__ u32x2v load_rows16(brsrc r, int xo, int it, int rsx) {
-    return __builtin_bit_cast(u32x2v, __builtin_amdgcn_raw_buffer_load_b64(r, xo, it * 16 * rsx, 0));
+template <int CT>
+__device__ __forceinline__ void load_tile(brsrc r, u32x2v (&o)[CT], int xo, int it, int rsx) {
+    if constexpr (CT == 2) {
+        const u32x4v v = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(r, xo, it * 16 * rsx, 0));
+        o[0] = u32x2v{v[0], v[1]};
+        o[1] = u32x2v{v[2], v[3]};
+    } else {
+        o[0] = __builtin_bit_cast(u32x2v, __builtin_amdgcn_raw_buffer_load_b64(r, xo, it * 16 * rsx, 0));
+    }
 }
-__device__ __forceinline__ void store_rows16(brsrc r, f32x4 v, int xo, int it, int rsx, unsigned sel, bool upper) {
-    __builtin_amdgcn_raw_buffer_store_b64(
-        __builtin_bit_cast(u32x2, quad_t(u32x2v{cvt2(v[0], v[1]), cvt2(v[2], v[3])}, sel, upper)), r, xo, it * 16 * rsx, 0);
+template <int CT>
+__device__ __forceinline__ void store_tile(brsrc r, const f32x4 (&v)[CT], int xo, int it, int rsx, unsigned sel, bool upper) {
+    u32x2v w[CT];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+        w[ct] = quad_t(u32x2v{cvt2(v[ct][0], v[ct][1]), cvt2(v[ct][2], v[ct][3])}, sel, upper);
+    if constexpr (CT == 2)
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4v{w[0][0], w[0][1], w[1][0], w[1][1]}, r, xo, it * 16 * rsx, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, w[0]), r, xo, it * 16 * rsx, 0);
 }
 __device__ __forceinline__ f32x4 floats(u32x2v v) {
     return f32x4{__builtin_bit_cast(float, v[0] << 16), __builtin_bit_cast(float, v[0] & 0xffff0000u),
@@ -876,8 +895,8 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
     // h^T: row 4q + e of tile t is n = 32 (t / 2) + 8q + 4 (t % 2) + e, so that a pair of tiles is
     // the operand whose other side reads 8 consecutive columns of K or Q
     f32x4 acc[NTL][CT];
-    const int64_t ho = ((int64_t)bh * P + p0 + l16) * N + 8 * q;
-    auto hn = [&](int t, int ct) { return ho + ct * 16 * N + (t >> 1) * 32 + (t & 1) * 4; };
+    const int64_t ho = ((int64_t)bh * P + p0 + tile_col<CT>(l16, 0)) * N + 8 * q;
+    auto hn = [&](int t, int ct) { return ho + ct * 4 * N + (t >> 1) * 32 + (t & 1) * 4; };
 #pragma unroll
     for (int t = 0; t < NTL; ++t)
 #pragma unroll
@@ -904,16 +923,14 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
         if (w == 0 && lane < 32)
             dma_run(make_rsrc(src + kFragTab, 2 * L * 4), reinterpret_cast<char*>(Vs), 1, 0, 1, lane);
     };
-    const int xo = rows16_off(lane, rsx, p0);
+    const int xo = rows_off<CT>(lane, rsx, p0);
     const unsigned sel = quad_sel(lane);
     const bool upper = (lane & 2) != 0;
     u32x2v xr[4][CT];  // x of the chunk, as loaded
     auto fetch_x = [&](int c) {
         const brsrc r = x_rsrc(a.x, c);
 #pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) xr[it][ct] = load_rows16(r, xo + ct * 32, it, rsx);
+        for (int it = 0; it < 4; ++it) load_tile<CT>(r, xr[it], xo, it, rsx);
     };
 
     // lane offsets (elements) of the fragment reads; further fragments differ by an exchange of
@@ -1026,9 +1043,7 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
         {
             const brsrc ry = x_rsrc(a.y, c);
 #pragma unroll
-            for (int it = 0; it < 4; ++it)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) store_rows16(ry, yq[it][ct], xo + ct * 32, it, rsx, sel, upper);
+            for (int it = 0; it < 4; ++it) store_tile<CT>(ry, yq[it], xo, it, rsx, sel, upper);
         }
         // h' = e^{c_L} h + K^T (e^{c_L - c} u), four row tiles side by side: a product on an
         // accumulator waits for the one before it
@@ -1104,14 +1119,14 @@ struct Team {
         Tn = a.rows.len(row); tok0 = a.rows.tok0(row); nc = a.rows.nchunks(row); kb0 = a.rows.kbase(row);
         p0 = sl * 16 * CT;
         rsk = G * N * 2; rsx = H * P * 2;
-        xo = rows16_off(lane, rsx, p0);
+        xo = rows_off<CT>(lane, rsx, p0);
         sel = quad_sel(lane); upper = (lane & 2) != 0;
-        ho = ((int64_t)bh * P + p0 + l16) * N + 8 * q;
+        ho = ((int64_t)bh * P + p0 + tile_col<CT>(l16, 0)) * N + 8 * q;
         ka = l16 * N + ((q ^ (l16 & SWZ)) << 3);
         const int tr = 4 * q + (l16 >> 2);
         kt = tr * N + (((l16 & 3) ^ (tr & SWZ)) << 3);
     }
-    __device__ __forceinline__ int64_t hn(int t, int ct) const { return ho + ct * 16 * N + (t >> 1) * 32 + (t & 1) * 4; }
+    __device__ __forceinline__ int64_t hn(int t, int ct) const { return ho + ct * 4 * N + (t >> 1) * 32 + (t & 1) * 4; }
     __device__ __forceinline__ int rows_left(int c) const { return (int)min((int64_t)L, Tn - (int64_t)c * L); }
     __device__ __forceinline__ int64_t item(int c) const { return (int64_t)(kb0 + c) * H + h; }
     __device__ __forceinline__ brsrc key_rsrc(const void* base, int c) const {
@@ -1147,18 +1162,21 @@ struct Team {
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + (k + w) * 512), 16, (k + w) * 1024 + lane * 16, 0,
                                                          0, 0);
     }
-    // a chunk's 64 x 16 CT tile of x or dy: dst[ct][token][16]
+    // a chunk's 64 x 16 CT tile of x or dy: dst[token][16 CT]
     __device__ __forceinline__ void fetch_x(const void* base, int c, bf16* dst) const {
         const brsrc r = x_rsrc(base, c);
         if (w < 2 * CT)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + w * 512), 16,
-                                                     ((w & 1) * 32 + (lane >> 1)) * rsx +
-                                                         (p0 + (w >> 1) * 16 + 8 * (lane & 1)) * 2,
+                                                     (w * 32 / CT + lane / (2 * CT)) * rsx + (p0 + 8 * (lane % (2 * CT))) * 2,
                                                      0, 0, 0);
     }
     // token tile `it` of it, in accumulator order (4 tokens of one column)
     __device__ __forceinline__ s16x4 x_tile(const bf16* src, int it, int ct) const {
-        return ds_tr16(src + ct * 1024 + (it * 16 + 4 * q + (l16 >> 2)) * 16 + 4 * (l16 & 3));
+        return ds_tr16(src + (it * 16 + 4 * q + (l16 >> 2)) * 16 * CT + 4 * CT * (l16 & 3) + 4 * ct);
+    }
+    // token tile w of a [token][H P] tensor
+    __device__ __forceinline__ void store_rows(void* base, int c, const f32x4 (&v)[CT]) const {
+        store_tile<CT>(x_rsrc(base, c), v, xo, w, rsx, sel, upper);
     }
     // fragments: token tile `it`, key columns 32 ks on; state tile t, 32 tokens from tile row `p`
     __device__ __forceinline__ bf16x8 frag_rows16(const bf16* tile, int it, int ks) const {
@@ -1227,11 +1245,6 @@ __global__ __launch_bounds__(256) void k_delta_team(Args a) {
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
             acc[o][ct] = a.h0 ? ld4(a.h0 + tm.hn(t0w + o, ct)) : f32x4{0.f, 0.f, 0.f, 0.f};
-    auto store_rows = [&](void* base, int c, const f32x4(&v)[CT]) {
-        const brsrc r = tm.x_rsrc(base, c);
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) store_rows16(r, v[ct], tm.xo + ct * 32, w, tm.rsx, tm.sel, tm.upper);
-    };
     if (nc > 0) {
         tm.fetch_tile(a.B, 0, K0);
         tm.fetch_tile(a.C, 0, Qs);
@@ -1374,10 +1387,10 @@ __global__ __launch_bounds__(256) void k_delta_team(Args a) {
             const float dt = l16 & 2 ? (l16 & 1 ? d[3] : d[2]) : (l16 & 1 ? d[1] : d[0]);
             if (l16 < 4 && t < tm.rows_left(c))
                 a.dyy[((int64_t)tm.sl * a.rows.nrows * a.H + tm.bh) * a.T + (int64_t)c * L + t] = dt;
-            store_rows(a.r, c, v);
-            store_rows(a.rlo, c, rest);
+            tm.store_rows(a.r, c, v);
+            tm.store_rows(a.rlo, c, rest);
         } else {
-            store_rows(a.y, c, yq);
+            tm.store_rows(a.y, c, yq);
         }
         if (KB == 1 && more) {
             wave_meet(false);  // every wave is done with K
@@ -1426,11 +1439,6 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
             acc[o][ct] = a.dhT ? ld4(a.dhT + tm.hn(t0w + o, ct)) : f32x4{0.f, 0.f, 0.f, 0.f};
-    auto store_rows = [&](void* base, int c, const f32x4(&v)[CT]) {
-        const brsrc r = tm.x_rsrc(base, c);
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) store_rows16(r, v[ct], tm.xo + ct * 32, w, tm.rsx, tm.sel, tm.upper);
-    };
     const int ft = (4 * q + (l16 >> 2) + 16 * (l16 & 3)) * 8;  // four columns of a block's row, in a fragment
     // rows of tile w of the table's transpose, columns 32 t on (t >= w / 2)
     auto frag_up = [&](const bf16* tab, int t) {
@@ -1440,6 +1448,30 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, ds_tr16(tab + at(2 * t + 1) + ft), 0, 1, 2, 3, 4,
                                                                   5, 6, 7));
     };
+    // dh' of a chunk, in accumulators: stored for the gradients of B, and <dh', h'> over this
+    // wave's tiles (summed over the waves after the next barrier)
+    constexpr int OP = (OT + 1) / 2;
+    auto leave = [&](int c, auto h8) {
+        const int64_t lo = (tm.item(c) - tm.bh) * a.P * N;
+        float s = 0.f;
+#pragma unroll
+        for (int o = 0; o < OP; ++o)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                const f32x8 av = join(acc[2 * o][ct], acc[2 * o + 1 < OT ? 2 * o + 1 : 2 * o][ct]), hv = h8(o, ct);
+                Sp<bf16> ov;
+                split8<1>(av, ov);
+                bf16* lp = static_cast<bf16*>(a.lin) + lo + tm.hn(t0w + 2 * o, ct);
+                if (OT > 1) st8(lp, ov.t[0]);
+                else st4(lp, __builtin_shufflevector(ov.t[0], ov.t[0], 0, 1, 2, 3));
+#pragma unroll
+                for (int i = 0; i < (OT > 1 ? 8 : 4); ++i) s += hv[i] * av[i];
+            }
+        s = row_sum16(s);
+        s += __shfl_xor(s, 16, 64);
+        s += __shfl_xor(s, 32, 64);
+        if (lane == 0) tots[w] = s;
+    };
     if (nc > 0) {
         tm.fetch_tile(a.B, nc - 1, K0);
         tm.template fetch_tab<TABN>(nc - 1, Sf);
@@ -1447,19 +1479,23 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
         tm.fetch_x(a.dy, nc - 1, Ys);
         tm.mark(Rf);
         tm.put_state(Hf, acc);
+        leave(nc - 1, [&](int o, int ct) {
+            const float* hp = a.hend + tm.hn(t0w + 2 * o, ct);
+            return join(ld4(hp), ld4(OT > 1 ? hp + 4 : hp));
+        });
     }
     auto chunk = [&](int c, const bf16* Ks, bf16* Kn) {
-        const bool more = c > 0, last = c + 1 == nc;
+        const bool more = c > 0;
         wave_meet(true);  // the chunk's tiles have landed, the adjoint's operands are in place
         tm.fetch_tile(a.C, c, Qs);  // read last in the chunk
         if (KB == 2 && more) tm.fetch_tile(a.B, c - 1, Kn);
-        // h' (the state entering the next chunk), consumed once the first products are under way
-        // (the last chunk's is hend; its loads here are unused)
-        constexpr int OP = (OT + 1) / 2;
+        if (threadIdx.x == 0)
+            a.tot[(int64_t)tm.sl * a.ntab * a.H + tm.item(c)] = (tots[0] + tots[1]) + (tots[2] + tots[3]);
+        // the state entering this chunk, for the chunk before: consumed at the end
         bf16x8 hi[OP][CT];
         s16x8 hl[OP][CT];
         {
-            const int64_t so = (tm.item(last ? c : c + 1) - tm.bh) * a.P * N;
+            const int64_t so = (tm.item(c) - tm.bh) * a.P * N;
 #pragma unroll
             for (int o = 0; o < OP; ++o)
 #pragma unroll
@@ -1513,35 +1549,6 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
         tm.template put_rows<3>(Yf, yw);
         wave_meet(false);  // beta dU is in place; every wave is done with dY
         if (more) tm.fetch_x(a.dy, c - 1, Ys);
-        {  // <dh', h'> over this wave's tiles, and dh' for the gradients of B
-            const int64_t lo = (tm.item(c) - tm.bh) * a.P * N;
-            float s = 0.f;
-#pragma unroll
-            for (int o = 0; o < OP; ++o)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    const f32x8 av = join(acc[2 * o][ct], acc[2 * o + 1 < OT ? 2 * o + 1 : 2 * o][ct]);
-                    f32x8 hv;
-                    if (last) {
-                        const float* hp = a.hend + tm.hn(t0w + 2 * o, ct);
-                        hv = join(ld4(hp), ld4(OT > 1 ? hp + 4 : hp));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) hv[i] = join_state(hi[o][ct][i], hl[o][ct][i]);
-                    }
-                    Sp<bf16> ov;
-                    split8<1>(av, ov);
-                    bf16* lp = static_cast<bf16*>(a.lin) + lo + tm.hn(t0w + 2 * o, ct);
-                    if (OT > 1) st8(lp, ov.t[0]);
-                    else st4(lp, __builtin_shufflevector(ov.t[0], ov.t[0], 0, 1, 2, 3));
-#pragma unroll
-                    for (int i = 0; i < (OT > 1 ? 8 : 4); ++i) s += hv[i] * av[i];
-                }
-            s = row_sum16(s);
-            s += __shfl_xor(s, 16, 64);
-            s += __shfl_xor(s, 32, 64);
-            if (lane == 0) tots[w] = s;
-        }
         // z = dU - S^T (beta dU), over the tiles from w on
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -1570,17 +1577,15 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
             tm.template fetch_tab<TABN>(c - 1, Sf);
             tm.fetch_x(a.x, c - 1, Xs);
         }
-        store_rows(a.z, c, v);
-        store_rows(a.zlo, c, rest);
-        store_rows(a.dx, c, dx);
+        tm.store_rows(a.z, c, v);
+        tm.store_rows(a.zlo, c, rest);
+        tm.store_rows(a.dx, c, dx);
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[i] = row_sum16(d[i]);
         {
             const int t = w * 16 + 4 * q + (l16 & 3);
             const float dt = l16 & 2 ? (l16 & 1 ? d[3] : d[2]) : (l16 & 1 ? d[1] : d[0]);
             if (l16 < 4 && t < tm.rows_left(c)) a.dxx[((int64_t)tm.sl * BH + tm.bh) * a.T + (int64_t)c * L + t] = dt;
-            if (threadIdx.x == 0)
-                a.tot[(int64_t)tm.sl * a.ntab * a.H + tm.item(c)] = (tots[0] + tots[1]) + (tots[2] + tots[3]);
         }
         // dh = e^{c_L} dh' - K^T (e^c dX) + Q^T (e^c dY) of this wave's tiles
 #pragma unroll
@@ -1606,7 +1611,15 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
                     for (int o = 0; o < OT; ++o) acc[o][ct] = mma(acc[o][ct], qf[o], yf);
                 }
         }
-        if (more) tm.put_state(Hf, acc);
+        if (more) {
+            tm.put_state(Hf, acc);
+            leave(c - 1, [&](int o, int ct) {
+                f32x8 hv;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) hv[i] = join_state(hi[o][ct][i], hl[o][ct][i]);
+                return hv;
+            });
+        }
         if (KB == 1 && more) {
             wave_meet(false);  // every wave is done with K
             tm.fetch_tile(a.B, c - 1, Kn);
