@@ -237,18 +237,26 @@ __global__ __launch_bounds__(256) void k_bc_norm_bwd(Args a) {
     }
 }
 
-// dwB and dwC from the work-groups' sums, in a fixed order, in float64
+// dwB and dwC from the work-groups' sums, in a fixed order, in float64: 4 columns per
+// work-group, 64 runs of every 64th row (with 32 columns of 8 runs, few work-groups of long
+// dependent sums, it took 40 us at 1024 rows of 256)
 template <int BLOCK = 256>
 __global__ __launch_bounds__(BLOCK) void k_bc_norm_dw(const float* __restrict__ part, float* __restrict__ dwB,
                                                       float* __restrict__ dwC, int N, int groups) {
+    constexpr int RUNS = BLOCK / 4;
     __shared__ double red[BLOCK];
-    const int k = blockIdx.x * 32 + (threadIdx.x & 31), j = threadIdx.x >> 5;
+    const int k = blockIdx.x * 4 + (threadIdx.x & 3), j = threadIdx.x >> 2;
     double s = 0.0;
-    for (int gr = j; gr < groups; gr += BLOCK / 32) s += (double)part[(int64_t)gr * 2 * N + k];
+#pragma unroll 4
+    for (int gr = j; gr < groups; gr += RUNS) s += (double)part[(int64_t)gr * 2 * N + k];
     red[threadIdx.x] = s;
     __syncthreads();
+    for (int half = RUNS / 2; half > 0; half >>= 1) {
+        if (j < half) red[threadIdx.x] += red[threadIdx.x + 4 * half];
+        __syncthreads();
+    }
     if (j == 0) {
-        for (int m = 1; m < BLOCK / 32; ++m) s += red[m * 32 + threadIdx.x];
+        s = red[threadIdx.x];
         if (k < N) {
             if (dwB) dwB[k] = (float)s;
         } else if (dwC) {
@@ -269,7 +277,7 @@ int launch(const Args& a, bool bwd) {
     } else {
         const size_t red = a.part ? (size_t)2 * 256 * VPL * 4 : 0;
         k_bc_norm_bwd<T, VPL><<<(unsigned)a.groups, 256, ang > red ? ang : red, a.stream>>>(a);
-        if (a.part) k_bc_norm_dw<256><<<(unsigned)(2 * a.N / 32), 256, 0, a.stream>>>(a.part, a.dwB, a.dwC, a.N, a.groups);
+        if (a.part) k_bc_norm_dw<256><<<(unsigned)(2 * a.N / 4), 256, 0, a.stream>>>(a.part, a.dwB, a.dwC, a.N, a.groups);
     }
     return hipGetLastError() == hipSuccess ? 0 : 7;
 }

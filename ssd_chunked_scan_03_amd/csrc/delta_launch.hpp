@@ -113,16 +113,18 @@ int walks_bwd(const Args& a) {
     k_delta_adj<N, CT, N == 256 ? 1 : 2><<<grid, 256, 0, a.stream>>>(a);
     return hipGetLastError() == hipSuccess ? 0 : 7;
 }
-// Few chains: a team of four waves per 16 columns, while that leaves two work-groups per CU
-// or less of the other kind (a wave per 16 or 32 columns).
-inline bool team_walk(int64_t bh, int64_t P) { return bh * P < 512 * 64; }
+// Teams while each has a CU of its own, else a wave per 16 or 32 columns.  Forward of 2048 tokens
+// at headdim 64, dstate 128 (us, team / wave): 32 heads 80 / 131, 128 heads 140 / 152, 192 heads
+// 253 / 170; dstate 256: 64 heads 121 / 200, 96 heads 217 / 213; 2.7B layer shape (640 chains)
+// 1210 / 680 for the walk alone.
+inline bool team_walk(int64_t bh, int64_t P, int64_t N) { return bh * P <= 256 * 16 * (N <= 128 && P >= 32 ? 2 : 1); }
 
 template <typename T, int N>
 int run_fwd(const Args& a) {
     if constexpr (std::is_same<T, bf16>::value && N >= 64) {
         prep<T, N, kFold>(a);
         const int64_t bh = (int64_t)a.rows.nrows * a.H;
-        if (team_walk(bh, a.P)) {
+        if (team_walk(bh, a.P, N)) {
             if constexpr (N <= 128) {
                 if (team_tiles(bh, a.P, N) == 2) return walk_team<N, 2, false>(a);
             }
