@@ -15,8 +15,9 @@ a_t = exp(dt_t A_h).  Keys are meant to have about unit length; ``norm`` (a dict
 from __future__ import annotations
 
 import ctypes
+import functools
 
-from . import (SSDError, _check_args, _dtype_code, _load, _ptr, Problem, make_problem)
+from . import SSD_BF16, SSD_F32, Problem, SSDError, _check_args, _load, make_problem
 
 DELTA_CHUNK = 64
 NORM_MODES = {"rms": 0, "l2": 1}
@@ -46,24 +47,74 @@ def _bind(lib):
         f.restype, f.argtypes = res, args
 
 
-def _call(name, head, tensors, ws=False, stream=None):
-    """Enqueue one entry point on `stream` (default: the current stream of the tensors' device).
-    The first of `tensors` names the device; `ws` is the workspace (False: the entry point
-    takes none)."""
+_calls = {}  # bound entry points
+
+
+def _raw_stream(index):
+    """The current stream of device `index` as an integer (hipStream_t)."""
     import torch
-    dev = next(t for t in tensors if t is not None).device
-    args = [ctypes.byref(head), *map(_ptr, tensors)]
+    f = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return f(index) if f is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _call(name, head, tensors, ws=False, stream=None):
+    """Enqueue one entry point on `stream` (default: the current stream of the tensors' device,
+    which the call makes the current device meanwhile).  The first of `tensors` names the
+    device; `ws` is the workspace (False: the entry point takes none)."""
+    import torch
+    fn = _calls.get(name)
+    if fn is None:
+        fn = _calls[name] = getattr(_load(), name)
+    for t in tensors:
+        if t is not None:
+            index = t.get_device()
+            break
+    args = [None if t is None else t.data_ptr() for t in tensors]
     if ws is not False:
-        args += [_ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()]
-    if dev.index is not None and dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            s = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
-            st = getattr(_load(), name)(*args, ctypes.c_void_p(int(s)))
+        args += (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+    if index < 0 or index == torch.cuda.current_device():
+        st = fn(head, *args, (_raw_stream(index) if index >= 0 else 0) if stream is None else int(stream))
     else:
-        s = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
-        st = getattr(_load(), name)(*args, ctypes.c_void_p(int(s)))
+        with torch.cuda.device(index):
+            st = fn(head, *args, _raw_stream(index) if stream is None else int(stream))
     if st:
         raise SSDError(st, name)
+
+
+@functools.lru_cache(maxsize=256)
+def _plan(kind, b, T, H, P, N, G, chunk, code):
+    """The problem of these sizes and its workspace bytes (a descriptor: it holds no data)."""
+    prob = make_problem(b, T, H, P, N, G, chunk, code)
+    return prob, (0 if kind == "step" else delta_bwd_workspace_bytes(prob) if kind == "bwd"
+                  else delta_workspace_bytes(prob, kind == "varlen"))
+
+
+def _check(x, tensors):
+    """_check_args for (name, tensor or None, shape, dtype) entries against x's device; the
+    message is formed only where something is wrong."""
+    dev = x.get_device()
+    ok = dev >= 0 and x.dtype in _codes()
+    for _, t, shape, dtype in tensors:
+        if t is not None and (t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous()):
+            ok = False
+    if not ok:
+        import torch
+        _check_args({n: (t, shape) for n, t, shape, _ in tensors},
+                    floats=[n for n, _, _, d in tensors if d == torch.float32 and n not in _PROBLEM_DTYPE],
+                    same_dtype=[n for n, t, _, _ in tensors if n in _PROBLEM_DTYPE])
+        for n, t, _, dtype in tensors:
+            if t is not None and t.dtype != dtype:
+                raise TypeError(f"{n} must be {dtype}, got {t.dtype}")
+    return _codes()[x.dtype]
+
+
+_PROBLEM_DTYPE = ("x", "B", "C", "beta", "dy")
+
+
+@functools.lru_cache(maxsize=1)
+def _codes():
+    import torch
+    return {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
 
 
 def delta_workspace_bytes(prob: Problem, varlen: bool = False) -> int:
@@ -124,14 +175,14 @@ def delta_fwd(x, dt, A, B, C, beta, h0=None, chunk=DELTA_CHUNK, return_final_sta
     import torch
     b, T, H, P, G, N = _shapes4(x, B)
     B, C = _normed(B, C, norm)
-    _check_args({"x": (x, (b, T, H, P)), "dt": (dt, (b, T, H)), "A": (A, (H,)), "B": (B, (b, T, G, N)),
-                 "C": (C, (b, T, G, N)), "beta": (beta, (b, T, H)), "h0": (h0, (b, H, P, N))},
-                floats=("dt", "A", "h0"), same_dtype=("x", "B", "C", "beta"))
-    prob = make_problem(b, T, H, P, N, G, chunk, _dtype_code(x))
+    f32, td = torch.float32, x.dtype
+    code = _check(x, (("x", x, (b, T, H, P), td), ("dt", dt, (b, T, H), f32), ("A", A, (H,), f32),
+                      ("B", B, (b, T, G, N), td), ("C", C, (b, T, G, N), td), ("beta", beta, (b, T, H), td),
+                      ("h0", h0, (b, H, P, N), f32)))
+    prob, need = _plan("fwd", b, T, H, P, N, G, chunk, code)
     y = torch.empty_like(x)
-    hT = torch.empty((b, H, P, N), dtype=torch.float32, device=x.device) if return_final_state else None
-    ws = _workspace(workspace, delta_workspace_bytes(prob), x.device)
-    delta_fwd_into(prob, x, dt, A, B, C, beta, h0, y, hT, ws)
+    hT = torch.empty((b, H, P, N), dtype=f32, device=x.device) if return_final_state else None
+    delta_fwd_into(prob, x, dt, A, B, C, beta, h0, y, hT, _workspace(workspace, need, x.device))
     return y, hT
 
 
@@ -155,14 +206,14 @@ def delta_fwd_varlen(x, dt, A, B, C, beta, cu_seqlens, h0=None, chunk=DELTA_CHUN
         pos = norm.get("positions")
         Bn, Cn = bc_norm(B[None], C[None], **dict(norm, positions=None if pos is None else pos.reshape(1, -1)))
         B, C = Bn[0], Cn[0]
-    _check_args({"x": (x, (T, H, P)), "dt": (dt, (T, H)), "A": (A, (H,)), "B": (B, (T, G, N)), "C": (C, (T, G, N)),
-                 "beta": (beta, (T, H)), "h0": (h0, (nseq, H, P, N)), "cu_seqlens": (cu_seqlens, (nseq + 1,))},
-                floats=("dt", "A", "h0"), same_dtype=("x", "B", "C", "beta"))
-    prob = make_problem(nseq, T, H, P, N, G, chunk, _dtype_code(x))
+    f32, td = torch.float32, x.dtype
+    code = _check(x, (("x", x, (T, H, P), td), ("dt", dt, (T, H), f32), ("A", A, (H,), f32), ("B", B, (T, G, N), td),
+                      ("C", C, (T, G, N), td), ("beta", beta, (T, H), td), ("h0", h0, (nseq, H, P, N), f32),
+                      ("cu_seqlens", cu_seqlens, (nseq + 1,), torch.int32)))
+    prob, need = _plan("varlen", nseq, T, H, P, N, G, chunk, code)
     y = torch.empty_like(x)
-    hT = torch.empty((nseq, H, P, N), dtype=torch.float32, device=x.device) if return_final_state else None
-    ws = _workspace(workspace, delta_workspace_bytes(prob, True), x.device)
-    delta_fwd_varlen_into(prob, cu_seqlens, x, dt, A, B, C, beta, h0, y, hT, ws)
+    hT = torch.empty((nseq, H, P, N), dtype=f32, device=x.device) if return_final_state else None
+    delta_fwd_varlen_into(prob, cu_seqlens, x, dt, A, B, C, beta, h0, y, hT, _workspace(workspace, need, x.device))
     return y, hT
 
 
@@ -174,10 +225,11 @@ def delta_step(x, dt, A, B, C, beta, h, norm=None):
     if h is None:
         raise ValueError("h (the state, updated in place) is required")
     B, C = _normed(B, C, norm)
-    _check_args({"x": (x, (b, T, H, P)), "dt": (dt, (b, T, H)), "A": (A, (H,)), "B": (B, (b, T, G, N)),
-                 "C": (C, (b, T, G, N)), "beta": (beta, (b, T, H)), "h": (h, (b, H, P, N))},
-                floats=("dt", "A", "h"), same_dtype=("x", "B", "C", "beta"))
-    prob = make_problem(b, T, H, P, N, G, DELTA_CHUNK, _dtype_code(x))
+    f32, td = torch.float32, x.dtype
+    code = _check(x, (("x", x, (b, T, H, P), td), ("dt", dt, (b, T, H), f32), ("A", A, (H,), f32),
+                      ("B", B, (b, T, G, N), td), ("C", C, (b, T, G, N), td), ("beta", beta, (b, T, H), td),
+                      ("h", h, (b, H, P, N), f32)))
+    prob, _ = _plan("step", b, T, H, P, N, G, DELTA_CHUNK, code)
     y = torch.empty_like(x)
     delta_step_into(prob, x, dt, A, B, C, beta, h, y)
     return y
@@ -192,17 +244,16 @@ def delta_bwd(x, dt, A, B, C, beta, dy, h0=None, dhT=None, chunk=DELTA_CHUNK, wo
     b, T, H, P, G, N = _shapes4(x, B)
     B0, C0 = B, C
     B, C = _normed(B, C, norm)
-    _check_args({"x": (x, (b, T, H, P)), "dt": (dt, (b, T, H)), "A": (A, (H,)), "B": (B, (b, T, G, N)),
-                 "C": (C, (b, T, G, N)), "beta": (beta, (b, T, H)), "dy": (dy, (b, T, H, P)),
-                 "h0": (h0, (b, H, P, N)), "dhT": (dhT, (b, H, P, N))},
-                floats=("dt", "A", "h0", "dhT"), same_dtype=("x", "B", "C", "beta", "dy"))
-    prob = make_problem(b, T, H, P, N, G, chunk, _dtype_code(x))
-    out = dict(dx=torch.empty_like(x), ddt=torch.empty_like(dt), dA=torch.empty_like(A), dB=torch.empty_like(B),
-               dC=torch.empty_like(C), dbeta=torch.empty_like(beta),
-               dh0=torch.empty((b, H, P, N), dtype=torch.float32, device=x.device))
-    ws = _workspace(workspace, delta_bwd_workspace_bytes(prob), x.device)
+    f32, td = torch.float32, x.dtype
+    code = _check(x, (("x", x, (b, T, H, P), td), ("dt", dt, (b, T, H), f32), ("A", A, (H,), f32),
+                      ("B", B, (b, T, G, N), td), ("C", C, (b, T, G, N), td), ("beta", beta, (b, T, H), td),
+                      ("dy", dy, (b, T, H, P), td), ("h0", h0, (b, H, P, N), f32), ("dhT", dhT, (b, H, P, N), f32)))
+    prob, need = _plan("bwd", b, T, H, P, N, G, chunk, code)
+    e = torch.empty_like
+    out = dict(dx=e(x), ddt=e(dt), dA=e(A), dB=e(B), dC=e(C), dbeta=e(beta),
+               dh0=torch.empty((b, H, P, N), dtype=f32, device=x.device))
     delta_bwd_into(prob, x, dt, A, B, C, beta, h0, dy, dhT, out["dx"], out["ddt"], out["dA"], out["dB"], out["dC"],
-                   out["dbeta"], out["dh0"], ws)
+                   out["dbeta"], out["dh0"], _workspace(workspace, need, x.device))
     if norm is not None:
         out.update(bc_norm_bwd(B0, C0, out["dB"], out["dC"], **norm))
     return out
@@ -230,6 +281,13 @@ def _token_stride(name, t):
     return step
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_plan(*sizes):
+    """The descriptor of these sizes and its backward's workspace bytes."""
+    prob = Norm(*sizes)
+    return prob, bc_norm_bwd_workspace_bytes(prob)
+
+
 def _norm_problem(B, C, wB, wC, mode, eps, inv_freq, positions, interleaved):
     import torch
     if B.dim() != 4 or C.dim() != 4:
@@ -241,24 +299,27 @@ def _norm_problem(B, C, wB, wC, mode, eps, inv_freq, positions, interleaved):
     if C.shape != (b, T, GC, N):
         raise ValueError(f"C must have shape {(b, T, GC, N)}, got {tuple(C.shape)}")
     F = 0 if inv_freq is None else inv_freq.numel()
-    _dtype_code(B)
+    code = _codes().get(B.dtype)
+    if code is None:
+        raise TypeError(f"B and C must be bfloat16 or float32, got {B.dtype}")
     if C.dtype != B.dtype:
         raise TypeError("B, C must share one dtype")
+    dev = B.get_device()
     for name, t, shape, dtype in (("wB", wB, (N,), torch.float32), ("wC", wC, (N,), torch.float32),
                                   ("inv_freq", inv_freq, (F,), torch.float32),
                                   ("positions", positions, (b, T), torch.int32)):
         if t is None:
             continue
-        if tuple(t.shape) != shape:
+        if t.shape != shape:
             raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
         if t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.device != B.device or not t.is_contiguous():
+        if t.get_device() != dev or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous tensor on {B.device}")
-    if C.device != B.device or not B.is_cuda:
+    if dev < 0 or C.get_device() != dev:
         raise ValueError("B and C must be GPU tensors on one device")
-    return Norm(b, T, GB, GC, N, F, _token_stride("B", B), _token_stride("C", C), float(eps), NORM_MODES[mode],
-                int(bool(interleaved)), _dtype_code(B))
+    return _norm_plan(b, T, GB, GC, N, F, _token_stride("B", B), _token_stride("C", C), float(eps), NORM_MODES[mode],
+                      int(bool(interleaved)), code)
 
 
 def bc_norm_into(prob: Norm, B, C, wB, wC, inv_freq, positions, Bn, Cn, stream=None) -> None:
@@ -273,7 +334,7 @@ def bc_norm(B, C, wB=None, wC=None, mode="rms", eps=1e-6, inv_freq=None, positio
     times inv_freq [F] (f32, F a multiple of 4, 2F <= N; None: no rotation).  B and C may be
     views into a wider projection.  Returns (Bn, Cn), contiguous."""
     import torch
-    prob = _norm_problem(B, C, wB, wC, mode, eps, inv_freq, positions, interleaved)
+    prob, _ = _norm_problem(B, C, wB, wC, mode, eps, inv_freq, positions, interleaved)
     Bn, Cn = torch.empty(B.shape, dtype=B.dtype, device=B.device), torch.empty(C.shape, dtype=C.dtype, device=C.device)
     bc_norm_into(prob, B, C, wB, wC, inv_freq, positions, Bn, Cn)
     return Bn, Cn
@@ -294,9 +355,9 @@ def bc_norm_bwd(B, C, dBn, dCn, wB=None, wC=None, mode="rms", eps=1e-6, inv_freq
     """Backward of bc_norm, given dBn and dCn (contiguous, like Bn and Cn).  Returns a dict with
     dB and dC (contiguous) and, for the weights that were given, dwB and dwC (float32 [N])."""
     import torch
-    prob = _norm_problem(B, C, wB, wC, mode, eps, inv_freq, positions, interleaved)
+    prob, need = _norm_problem(B, C, wB, wC, mode, eps, inv_freq, positions, interleaved)
     for name, t, like in (("dBn", dBn, B), ("dCn", dCn, C)):
-        if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device or not t.is_contiguous():
+        if t.shape != like.shape or t.dtype != like.dtype or t.get_device() != like.get_device() or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {like.dtype} tensor of shape {tuple(like.shape)} on {like.device}")
     out = dict(dB=torch.empty_like(dBn), dC=torch.empty_like(dCn))
     for name, w in (("dwB", wB), ("dwC", wC)):
@@ -304,7 +365,7 @@ def bc_norm_bwd(B, C, dBn, dCn, wB=None, wC=None, mode="rms", eps=1e-6, inv_freq
             out[name] = torch.empty_like(w)
     ws = None
     if wB is not None or wC is not None:
-        ws = _workspace(workspace, bc_norm_bwd_workspace_bytes(prob), B.device)
+        ws = _workspace(workspace, need, B.device)
     bc_norm_bwd_into(prob, B, C, wB, wC, inv_freq, positions, dBn, dCn, out["dB"], out["dC"], out.get("dwB"),
                      out.get("dwC"), ws)
     return out
