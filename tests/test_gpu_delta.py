@@ -78,6 +78,24 @@ FORWARD = [
     (1, 190, 3, 16, 32, 1, "f32"),
     (1, 333, 2, 32, 128, 1, "f32"),
     (2, 150, 140, 64, 64, 2, "bf16"),  # enough chains for the widest slices
+    # two column tiles a team
+    (1, 130, 80, 64, 128, 8, "bf16"),
+    (1, 70, 40, 128, 64, 2, "bf16"),
+    # a wave per 16 or 32 columns: headdim 128, few and many chains, narrow heads, dstate 256
+    (1, 130, 80, 128, 128, 4, "bf16"),
+    (1, 70, 160, 128, 64, 160, "bf16"),
+    (1, 130, 160, 64, 128, 8, "bf16"),
+    (2, 70, 150, 32, 64, 2, "bf16"),
+    (1, 70, 260, 16, 128, 4, "bf16"),
+    (2, 70, 264, 64, 128, 8, "bf16"),
+    (2, 200, 264, 32, 64, 3, "bf16"),
+    (1, 130, 80, 64, 256, 8, "bf16"),
+    (1, 70, 40, 128, 256, 5, "bf16"),
+    (2, 70, 260, 16, 256, 1, "bf16"),
+    # float32 and dstate 16, 32 with full work-groups
+    (2, 70, 132, 64, 32, 2, "f32"),
+    (1, 130, 260, 64, 128, 4, "f32"),
+    (2, 70, 132, 64, 32, 2, "bf16"),
 ]
 
 
@@ -255,6 +273,13 @@ BACKWARD = [
     (1, 65, 2, 128, 256, 2, "f32"),
     (1, 90, 3, 16, 16, 1, "f32"),
     (1, 1100, 2, 16, 32, 1, "f32"),   # a long sum into dA
+    # two column tiles a team; dstate 256 with more teams than CUs; full work-groups
+    (1, 130, 80, 64, 128, 8, "bf16"),
+    (1, 70, 40, 128, 64, 2, "bf16"),
+    (2, 70, 40, 128, 128, 1, "bf16"),
+    (1, 70, 80, 64, 256, 8, "bf16"),
+    (2, 70, 132, 64, 32, 2, "f32"),
+    (2, 70, 132, 64, 32, 2, "bf16"),
 ]
 
 
