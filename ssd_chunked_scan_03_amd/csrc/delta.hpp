@@ -1091,19 +1091,31 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
 }
 
 // ---------------------------------------------------------------------------
-// k_delta_team: the same walk by a team of 4 waves per 16 CT columns, for few chains (a chain's
-// time is then one wave's, and 4 waves share it) and for the backward's first walk (SAVE).
-// Wave w takes token tile w of every product over tokens and NTL / 4 of the state's tiles; the
-// state, R, r and the weighted u pass between the waves as split operands in LDS (written
-// once, read by the waves that need them): three exchanges per chunk.
+// k_delta_team: the same walk by a team of 8 waves per 16 CT columns, for few chains and for the
+// backward's first walk (SAVE).  Four waves own a quarter of the state each and carry what the
+// next chunk waits for: K h^T in partial sums (their own state is the operand, straight from the
+// accumulators), R, r and the state's update.  The other four, one beside each on its SIMD, do
+// the rest meanwhile: every transfer into LDS, Q h^T, Y and its store.  Four exchanges per chunk.
 // SAVE = true writes the residuals r, the state entering every chunk and after the last, and
 // the per-token dY . Y (Y in float32, all terms) instead of y and hT.
 // ---------------------------------------------------------------------------
+// Blocks k, k + 8, k + 16, ... run on one XCD: within a row, each XCD takes a contiguous range
+// of its (head, slice) items, so that the slices of a head and the heads of a group read their
+// tables and keys through one L2.  (Rows are not gathered: their lengths may differ.)
+struct Item {
+    int bh, sl;
+};
+__device__ __forceinline__ Item xcd_item(unsigned k, int H, int nsl) {
+    const unsigned n = (unsigned)H * nsl, row = k / n, j = k % n, x = j & 7, r = n & 7;
+    const unsigned it = x * (n >> 3) + (x < r ? x : r) + (j >> 3);
+    return Item{(int)(row * H + it / nsl), (int)(it % nsl)};
+}
+
 // what the two team walks share: the chunk addresses of one (row, head) and the lane's offsets
 template <int N, int CT>
 struct Team {
     static constexpr int OT = N / 64;  // state tiles per wave: OT w .. OT w + OT - 1
-    int lane, w, l16, q, H, G, P, h, row, g, nc, kb0, sl, bh, p0, rsk, rsx, xo;
+    int lane, w, l16, q, H, G, P, h, row, g, nc, kb0, sl, bh, p0, rsk, rsx, xo;  // w: wave of four
     int64_t Tn, tok0, ho;
     unsigned sel;
     bool upper;
@@ -1111,10 +1123,11 @@ struct Team {
     const Args& a;
     __device__ __forceinline__ Team(const Args& a_) : a(a_) {
         constexpr int SWZ = Dma<N>::SWZ;
-        lane = threadIdx.x & 63; w = wave_id(); l16 = lane & 15; q = lane >> 4;
+        lane = threadIdx.x & 63; w = wave_id() & 3; l16 = lane & 15; q = lane >> 4;
         H = a.H; G = a.G; P = a.P;
         const int nsl = P / (16 * CT);
-        sl = (int)(blockIdx.x % (unsigned)nsl); bh = (int)(blockIdx.x / (unsigned)nsl);
+        const Item it = xcd_item(blockIdx.x, H, nsl);
+        sl = it.sl; bh = it.bh;
         h = bh % H; row = bh / H; g = h / (H / G);
         Tn = a.rows.len(row); tok0 = a.rows.tok0(row); nc = a.rows.nchunks(row); kb0 = a.rows.kbase(row);
         p0 = sl * 16 * CT;
@@ -1152,13 +1165,13 @@ struct Team {
     __device__ __forceinline__ void mark(bf16* dst) const {
         if (w == 0) dma_run(make_rsrc(a.tab, 1024), reinterpret_cast<char*>(dst), 1, 0, 1, lane);
     }
-    // a chunk's table and factors, ELEMS bfloat16 elements in all
-    template <int ELEMS>
+    // a chunk's table and factors, RUNS KiB in all
+    template <int RUNS>
     __device__ __forceinline__ void fetch_tab(int c, bf16* dst) const {
-        const brsrc r = make_rsrc(reinterpret_cast<const bf16*>(a.tab) + item(c) * ELEMS, ELEMS * 2);
+        const brsrc r = make_rsrc(reinterpret_cast<const bf16*>(a.tab) + item(c) * RUNS * 512, RUNS * 1024);
 #pragma unroll
-        for (int k = 0; k < ELEMS / 512; k += 4)
-            if (k + w < ELEMS / 512)
+        for (int k = 0; k < RUNS; k += 4)
+            if (k + w < RUNS)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + (k + w) * 512), 16, (k + w) * 1024 + lane * 16, 0,
                                                          0, 0);
     }
@@ -1186,22 +1199,66 @@ struct Team {
         const bf16* p = tile + (kt ^ ((t >> 1) << 5)) + 4 * (t & 1);
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(ds_tr16(p), ds_tr16(p + 16 * N), 0, 1, 2, 3, 4, 5, 6, 7));
     }
-    // this wave's state tiles to LDS operands dst[ks][term][ct][lane][8]
-    __device__ __forceinline__ void put_state(bf16* dst, const f32x4 (&acc)[OT][CT]) const {
+    // this wave's state tiles as operands, in pairs of tiles (dstate 64: one tile and zeros)
+    static constexpr int OP = (OT + 1) / 2;
+    __device__ __forceinline__ void split(const f32x4 (&acc)[OT][CT], Sp<bf16> (&sp)[OP][CT]) const {
+        const f32x4 z = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int o = 0; o < OT; o += 2)
+        for (int o = 0; o < OP; ++o)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                Sp<bf16> sp;
-                const int t = OT * w + o;
-                split8(join(acc[o][ct], acc[o + 1 < OT ? o + 1 : o][ct]), sp);
-#pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    bf16* d = dst + (((t >> 1) * 3 + k) * CT + ct) * 512 + lane * 8;
-                    if (OT > 1) st8(d, sp.t[k]);
-                    else st4(d + 4 * (t & 1), __builtin_shufflevector(sp.t[k], sp.t[k], 0, 1, 2, 3));
-                }
+                if (OT > 1) split8(join(acc[2 * o][ct], acc[2 * o + 1 < OT ? 2 * o + 1 : 0][ct]), sp[o][ct]);
+                else split8(w & 1 ? join(z, acc[0][ct]) : join(acc[0][ct], z), sp[o][ct]);
             }
+    }
+    __device__ __forceinline__ int ks_of(int o) const { return OT > 1 ? OT / 2 * w + o : w >> 1; }
+    // the first TS terms to LDS: dst[ks][term][ct][lane][8]
+    template <int TS>
+    __device__ __forceinline__ void put_state(bf16* dst, const Sp<bf16> (&sp)[OP][CT]) const {
+#pragma unroll
+        for (int o = 0; o < OP; ++o)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int k = 0; k < TS; ++k) {
+                    bf16* d = dst + ((ks_of(o) * TS + k) * CT + ct) * 512 + lane * 8;
+                    const bf16x8 v = sp[o][ct].t[k];
+                    if (OT > 1) st8(d, v);
+                    else st4(d + 4 * (w & 1), w & 1 ? __builtin_shufflevector(v, v, 4, 5, 6, 7)
+                                                    : __builtin_shufflevector(v, v, 0, 1, 2, 3));
+                }
+    }
+    // the product of a key tile with the state, this wave's part of its sum for all 4 token
+    // tiles, to dst[wave][tile][ct][lane]; `sum` adds tile w up over the waves
+    __device__ __forceinline__ void part_sums(const bf16* tile, const Sp<bf16> (&sp)[OP][CT], float* dst) const {
+        f32x4 pv[4][CT];
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) pv[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+        bf16x8 kf[OP][4];
+#pragma unroll
+        for (int o = 0; o < OP; ++o)
+#pragma unroll
+            for (int it = 0; it < 4; ++it) kf[o][it] = frag_rows16(tile, it, ks_of(o));
+#pragma unroll
+        for (int o = 0; o < OP; ++o)
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (int it = 0; it < 4; ++it)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) pv[it][ct] = mma(pv[it][ct], kf[o][it], sp[o][ct].t[k]);
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) st4(dst + ((w * 4 + it) * CT + ct) * 256 + lane * 4, pv[it][ct]);
+    }
+    __device__ __forceinline__ f32x4 sum(const float* src, int ct) const {
+        f32x4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = ld4(src + ((k * 4 + w) * CT + ct) * 256 + lane * 4);
+        return (v[0] + v[1]) + (v[2] + v[3]);
     }
     // token tile w's values to LDS operands dst[t][term][ct][lane][8] of TS terms
     template <int TS>
@@ -1218,194 +1275,259 @@ struct Team {
     __device__ __forceinline__ bf16x8 get(const bf16* src, int t, int k, int ct) const {
         return ld8(src + ((t * TS + k) * CT + ct) * 512 + lane * 8);
     }
+    // tile row w of a table of TERMS terms, columns 32 t on (t <= w / 2)
+    template <int TERMS>
+    __device__ __forceinline__ void table_row(const bf16* tab, bf16x8 (&f)[2][TERMS]) const {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if (t > (w >> 1)) break;
+            const int lo = w == 2 && t == 1 ? 4 : w == 0 ? 0 : (w < 3 ? w : 3 + t) * 512;
+            const int hi = w < 3 && t == (w >> 1) && !(w & 1) ? lo : lo + 4;  // (no such block: zero)
+#pragma unroll
+            for (int k = 0; k < TERMS; ++k) {
+                const bf16* tk = tab + k * 5 * 512 + lane * 8;
+                u32x2 h2 = __builtin_bit_cast(u32x2, ld4(tk + hi));
+                if (hi == lo) h2 = u32x2{0, 0};
+                f[t][k] = join(ld4(tk + lo), __builtin_bit_cast(bf16x4, h2));
+            }
+        }
+    }
+    // o += that row times token operands src in LDS (ST terms), products of order below ST
+    template <int TERMS, int ST>
+    __device__ __forceinline__ void times_rows(f32x4 (&o)[CT], const bf16x8 (&f)[2][TERMS], const bf16* src) const {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if (t > (w >> 1)) break;
+            f32x4 p[CT];  // the second half of the products, beside the first
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) p[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < TERMS; ++k)
+#pragma unroll
+                for (int m = 0; m < ST - k; ++m)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+                        f32x4& v = (k + m) & 1 ? p[ct] : o[ct];
+                        v = mma(v, f[t][k], get<ST>(src, t, m, ct));
+                    }
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) o[ct] += p[ct];
+        }
+    }
 };
 __device__ __forceinline__ f32x4 floats(s16x4 v) { return floats(__builtin_bit_cast(u32x2v, v)); }
 
 template <int N, int CT, int KB, bool SAVE>
-__global__ __launch_bounds__(256) void k_delta_team(Args a) {
-    constexpr int KS = N / 32, TILE = Dma<N>::TILE, OT = Team<N, CT>::OT;
-    constexpr int TABN = (SAVE ? kFragTab2 : kFragTab) + kFragVec, QT = SAVE ? 3 : 2, MT = SAVE ? 3 : 1, UT = SAVE ? 3 : 2;
+__global__ __launch_bounds__(512) void k_delta_team(Args a) {
+    typedef Team<N, CT> TM;
+    constexpr int KS = N / 32, TILE = Dma<N>::TILE, OT = TM::OT, OP = TM::OP;
+    constexpr int QT = SAVE ? 3 : 2, MT = SAVE ? 3 : 1, UT = SAVE ? 3 : 2;  // terms of h, M and u in Y
+    constexpr int RUNS = (SAVE ? kFragTab2 : kFragTab) / 512 + 1;
     __shared__ __attribute__((aligned(16))) bf16 K0[TILE];
     __shared__ __attribute__((aligned(16))) bf16 K1[KB == 2 ? TILE : 8];
     __shared__ __attribute__((aligned(16))) bf16 Qs[TILE];
-    __shared__ __attribute__((aligned(16))) bf16 Sf[TABN];
+    __shared__ __attribute__((aligned(16))) bf16 Sf[RUNS * 512];
     __shared__ __attribute__((aligned(16))) bf16 Xs[CT * 1024];
     __shared__ __attribute__((aligned(16))) bf16 Ys[SAVE ? CT * 1024 : 8];
-    constexpr int HF = KS * 3 * CT * 512, RF = 2 * 3 * CT * 512, UF = 2 * UT * CT * 512;
-    __shared__ __attribute__((aligned(16))) bf16 Ex[HF + 2 * RF + UF];  // operands passed between the waves
-    const bf16* Mf = Sf + 3 * 5 * 512;
-    const float* Vs = reinterpret_cast<const float*>(Sf + TABN - kFragVec);
-    bf16 *Hf = Ex, *Rf = Hf + HF, *Wf = Rf + RF, *Uf = Wf + RF;
-    const Team<N, CT> tm(a);
+    // passed between the waves: partial sums, then (once they are read) the weighted u and u;
+    // the state's operands for Q h^T; R
+    constexpr int PF = 16 * CT * 512, HF = KS * QT * CT * 512, RF = 2 * 3 * CT * 512;
+    __shared__ __attribute__((aligned(16))) bf16 Ex[PF + HF + RF];
+    bf16 *Wf = Ex, *Uf = Wf + RF, *Hf = Ex + PF, *Rf = Hf + HF;
+    float* Pf = reinterpret_cast<float*>(Ex);
+    const bf16* Mf = Sf + 15 * 512;
+    const float* Vs = reinterpret_cast<const float*>(Sf + (RUNS - 1) * 512);
+    const TM tm(a);
     const int lane = tm.lane, w = tm.w, l16 = tm.l16, q = tm.q, nc = tm.nc, t0w = OT * w;
-
-    f32x4 acc[OT][CT];
-#pragma unroll
-    for (int o = 0; o < OT; ++o)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-            acc[o][ct] = a.h0 ? ld4(a.h0 + tm.hn(t0w + o, ct)) : f32x4{0.f, 0.f, 0.f, 0.f};
-    if (nc > 0) {
+    if (nc > 0 && wave_id() >= 4) {
+        auto bring = [&](int c) {
+            tm.template fetch_tab<RUNS>(c, Sf);
+            tm.fetch_x(a.x, c, Xs);
+            if (SAVE) tm.fetch_x(a.dy, c, Ys);
+        };
         tm.fetch_tile(a.B, 0, K0);
         tm.fetch_tile(a.C, 0, Qs);
-        tm.template fetch_tab<TABN>(0, Sf);
-        tm.fetch_x(a.x, 0, Xs);
-        if (SAVE) tm.fetch_x(a.dy, 0, Ys);
+        bring(0);
         tm.mark(Rf);
-        tm.put_state(Hf, acc);
-    }
-    auto chunk = [&](int c, const bf16* Ks, bf16* Kn) {
-        const bool more = c + 1 < nc;
-        wave_meet(true);  // the chunk's tiles have landed, the state's operands are in place
-        if (KB == 2 && more) tm.fetch_tile(a.B, c + 1, Kn);
-        if (SAVE) {
-            const int64_t so = (tm.item(c) - tm.bh) * a.P * N;
+        f32x4 yq[CT], d;
+        // what a chunk leaves to memory, sent on its way at the start of the next
+        auto leave = [&](int c) {
+            if (SAVE) {
+                f32x4 e;
 #pragma unroll
-            for (int o = 0; o < OT; o += 2)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    bf16x8 hi;
-                    s16x8 lo;
-                    split_state(join(acc[o][ct], acc[o + 1 < OT ? o + 1 : o][ct]), hi, lo);
-                    bf16* hp = static_cast<bf16*>(a.hin) + so + tm.hn(t0w + o, ct);
-                    short* lp = a.hlo + so + tm.hn(t0w + o, ct);
-                    if (OT > 1) {
-                        st8(hp, hi);
-                        *reinterpret_cast<s16x8*>(lp) = lo;
-                    } else {
-                        st4(hp, __builtin_shufflevector(hi, hi, 0, 1, 2, 3));
-                        *reinterpret_cast<s16x4*>(lp) = __builtin_shufflevector(lo, lo, 0, 1, 2, 3);
-                    }
-                }
-        }
-        // K h^T and Q h^T of token tile w, two accumulators each
-        f32x4 v[CT], yq[CT], v2[CT], y2[CT];
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) v[ct] = yq[ct] = v2[ct] = y2[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            const bf16x8 kf = tm.frag_rows16(Ks, w, ks), qf = tm.frag_rows16(Qs, w, ks);
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    const bf16x8 hf = tm.template get<3>(Hf, ks, k, ct);
-                    f32x4 &vv = ks & 1 ? v2[ct] : v[ct], &yy = ks & 1 ? y2[ct] : yq[ct];
-                    vv = mma(vv, kf, hf);
-                    if (k < QT) yy = mma(yy, qf, hf);
-                }
-        }
-        const f32x4 ec = ld4(Vs + w * 16 + 4 * q);
-        f32x4 bt = f32x4{1.f, 1.f, 1.f, 1.f};
-        if (SAVE) bt = ld4(Vs + 2 * L + w * 16 + 4 * q);
-        f32x4 rb[CT];
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            v[ct] = floats(tm.x_tile(Xs, w, ct)) - ec * (v[ct] + v2[ct]);
-            yq[ct] = ec * (yq[ct] + y2[ct]);
-            rb[ct] = v[ct] * bt;
-        }
-        tm.template put_rows<3>(Rf, rb);
-        wave_meet(false);  // R is in place; every wave is done with Q
-        if (more) {
-            tm.fetch_tile(a.C, c + 1, Qs);
-            tm.fetch_x(a.x, c + 1, Xs);
-        }
-        // r = R - S beta R, over the tiles up to w
-        auto table = [&](f32x4(&o)[CT], const bf16* tab, const bf16* src, auto terms, auto order, auto st) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (t > (w >> 1)) break;
-                const int lo = w == 2 && t == 1 ? 4 : w == 0 ? 0 : (w < 3 ? w : 3 + t) * 512;
-                const int hi = w < 3 && t == (w >> 1) && !(w & 1) ? lo : lo + 4;  // (no such block: zero)
-#pragma unroll
-                for (int k = 0; k < decltype(terms)::value; ++k) {
-                    const bf16* tk = tab + k * 5 * 512 + lane * 8;
-                    u32x2 h2 = __builtin_bit_cast(u32x2, ld4(tk + hi));
-                    if (hi == lo) h2 = u32x2{0, 0};
-                    const bf16x8 f = join(ld4(tk + lo), __builtin_bit_cast(bf16x4, h2));
-#pragma unroll
-                    for (int m = 0; m < decltype(order)::value - k; ++m)
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct)
-                            o[ct] = mma(o[ct], f, tm.template get<decltype(st)::value>(src, t, m, ct));
-                }
+                for (int i = 0; i < 4; ++i) e[i] = row_sum16(d[i]);
+                const int t = w * 16 + 4 * q + (l16 & 3);
+                const float dt = l16 & 2 ? (l16 & 1 ? e[3] : e[2]) : (l16 & 1 ? e[1] : e[0]);
+                if (l16 < 4 && t < tm.rows_left(c))
+                    a.dyy[((int64_t)tm.sl * a.rows.nrows * a.H + tm.bh) * a.T + (int64_t)c * L + t] = dt;
+            } else {
+                tm.store_rows(a.y, c, yq);
             }
         };
-        typedef std::integral_constant<int, 3> three;
-        table(v, Sf, Rf, three(), three(), three());
-        const f32x4 ew = ld4(Vs + L + w * 16 + 4 * q) * bt;
-        f32x4 uw[CT];
+        auto chunk = [&](int c, bf16* Kn) {
+            const bool more = c + 1 < nc;
+            wave_meet(true);  // the chunk's tiles have landed, the state's operands are in place
+            if (c > 0) leave(c - 1);
+            if (KB == 2 && more) tm.fetch_tile(a.B, c + 1, Kn);
+            const f32x4 ec = ld4(Vs + w * 16 + 4 * q);
+            // Q h^T of token tile w, two accumulators
+            f32x4 y2[CT];
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            rb[ct] = v[ct] * bt;
-            uw[ct] = v[ct] * ew;
-        }
-        tm.template put_rows<UT>(Uf, rb);
-        tm.template put_rows<3>(Wf, uw);
-        const float el = Vs[L - 1];
-        wave_meet(false);  // r and the weighted u are in place
-        // Y = e^c Q h^T + M beta r
-        table(yq, Mf, Uf, std::integral_constant<int, MT>(), std::integral_constant<int, UT>(), std::integral_constant<int, UT>());
-        f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f};  // SAVE: dY . Y
-        if (SAVE) {
+            for (int ct = 0; ct < CT; ++ct) yq[ct] = y2[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+            auto qh = [&](int from, int to) {
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) d += floats(tm.x_tile(Ys, w, ct)) * yq[ct];
-        }
-        wave_meet(false);  // every wave is done with the tables
-        if (more) {
-            tm.template fetch_tab<TABN>(c + 1, Sf);
-            if (SAVE) tm.fetch_x(a.dy, c + 1, Ys);
-        }
-        // h' = e^{c_L} h + K^T (e^{c_L - c} u) of this wave's tiles
+                for (int ks = from; ks < to; ++ks) {
+                    const bf16x8 qf = tm.frag_rows16(Qs, w, ks);
 #pragma unroll
-        for (int o = 0; o < OT; ++o)
+                    for (int k = 0; k < QT; ++k)
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) acc[o][ct] *= el;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            bf16x8 kf[OT];
-#pragma unroll
-            for (int o = 0; o < OT; ++o) kf[o] = tm.frag_t(Ks + ks * 32 * N, t0w + o);
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    const bf16x8 wf = tm.template get<3>(Wf, ks, k, ct);
-#pragma unroll
-                    for (int o = 0; o < OT; ++o) acc[o][ct] = mma(acc[o][ct], kf[o], wf);
+                        for (int ct = 0; ct < CT; ++ct) {
+                            f32x4& yy = ks & 1 ? y2[ct] : yq[ct];
+                            yy = mma(yy, qf, tm.template get<QT>(Hf, ks, k, ct));
+                        }
                 }
-        }
-        if (more) tm.put_state(Hf, acc);
-        if (SAVE) {
-            f32x4 rest[CT];
+            };
+            bf16x8 mf[2][MT];
+            tm.template table_row<MT>(Mf, mf);
+            f32x4 dy[CT];
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) rest[ct] = rest16(v[ct]);
+            for (int ct = 0; ct < CT; ++ct)
+                if (SAVE) dy[ct] = floats(tm.x_tile(Ys, w, ct));
+            qh(0, KS - KS / 4);
+            wave_meet(false);  // the partial sums are in place, the tables, X and dY in registers
+            if (more) bring(c + 1);
+            qh(KS - KS / 4, KS);
+            wave_meet(false);  // R is in place, K^T in registers, Q is free
+            if (more) {
+                tm.fetch_tile(a.C, c + 1, Qs);
+                if (KB == 1) tm.fetch_tile(a.B, c + 1, Kn);
+            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) d[i] = row_sum16(d[i]);
-            const int t = w * 16 + 4 * q + (l16 & 3);
-            const float dt = l16 & 2 ? (l16 & 1 ? d[3] : d[2]) : (l16 & 1 ? d[1] : d[0]);
-            if (l16 < 4 && t < tm.rows_left(c))
-                a.dyy[((int64_t)tm.sl * a.rows.nrows * a.H + tm.bh) * a.T + (int64_t)c * L + t] = dt;
-            tm.store_rows(a.r, c, v);
-            tm.store_rows(a.rlo, c, rest);
-        } else {
-            tm.store_rows(a.y, c, yq);
+            for (int ct = 0; ct < CT; ++ct) yq[ct] = ec * (yq[ct] + y2[ct]);
+            wave_meet(false);  // u is in place
+            // Y = e^c Q h^T + M beta r
+            tm.template times_rows<MT, UT>(yq, mf, Uf);
+            d = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (SAVE) {
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) d += dy[ct] * yq[ct];
+            }
+        };
+        for (int c = 0; c < nc; c += 2) {
+            chunk(c, KB == 2 ? K1 : K0);
+            if (c + 1 < nc) chunk(c + 1, K0);
         }
-        if (KB == 1 && more) {
-            wave_meet(false);  // every wave is done with K
-            tm.fetch_tile(a.B, c + 1, Kn);
-        }
-    };
-    for (int c = 0; c < nc; c += 2) {
-        chunk(c, K0, KB == 2 ? K1 : K0);
-        if (c + 1 < nc) chunk(c + 1, KB == 2 ? K1 : K0, K0);
-    }
-    if (float* hT = SAVE ? a.hend : a.hT) {
+        leave(nc - 1);
+    } else if (wave_id() < 4) {
+        f32x4 acc[OT][CT];
 #pragma unroll
         for (int o = 0; o < OT; ++o)
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) st4(hT + tm.hn(t0w + o, ct), acc[o][ct]);
+            for (int ct = 0; ct < CT; ++ct)
+                acc[o][ct] = a.h0 ? ld4(a.h0 + tm.hn(t0w + o, ct)) : f32x4{0.f, 0.f, 0.f, 0.f};
+        Sp<bf16> sp[OP][CT];
+        tm.split(acc, sp);
+        if (nc > 0) tm.template put_state<QT>(Hf, sp);
+        __builtin_amdgcn_s_setprio(2);  // before the wave that shares the SIMD
+        auto chunk = [&](int c, const bf16* Ks) {
+            wave_meet(false);  // the chunk's tiles have landed
+            tm.part_sums(Ks, sp, Pf);
+            if (SAVE) {
+                const int64_t so = (tm.item(c) - tm.bh) * a.P * N;
+#pragma unroll
+                for (int o = 0; o < OT; o += 2)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+                        bf16x8 hi;
+                        s16x8 lo;
+                        split_state(join(acc[o][ct], acc[o + 1 < OT ? o + 1 : o][ct]), hi, lo);
+                        bf16* hp = static_cast<bf16*>(a.hin) + so + tm.hn(t0w + o, ct);
+                        short* lp = a.hlo + so + tm.hn(t0w + o, ct);
+                        if (OT > 1) {
+                            st8(hp, hi);
+                            *reinterpret_cast<s16x8*>(lp) = lo;
+                        } else {
+                            st4(hp, __builtin_shufflevector(hi, hi, 0, 1, 2, 3));
+                            *reinterpret_cast<s16x4*>(lp) = __builtin_shufflevector(lo, lo, 0, 1, 2, 3);
+                        }
+                    }
+            }
+            const f32x4 ec = ld4(Vs + w * 16 + 4 * q), ew0 = ld4(Vs + L + w * 16 + 4 * q);
+            f32x4 bt = f32x4{1.f, 1.f, 1.f, 1.f};
+            if (SAVE) bt = ld4(Vs + 2 * L + w * 16 + 4 * q);
+            const float el = Vs[L - 1];
+            f32x4 v[CT], rb[CT], uw[CT];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) v[ct] = floats(tm.x_tile(Xs, w, ct));
+            bf16x8 sf[2][3];
+            tm.template table_row<3>(Sf, sf);
+            wave_meet(false);  // the partial sums are in place
+            // R = X - e^c K h^T of token tile w
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                v[ct] -= ec * tm.sum(Pf, ct);
+                rb[ct] = v[ct] * bt;
+            }
+            tm.template put_rows<3>(Rf, rb);
+            bf16x8 kf[2][OT];
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int o = 0; o < OT; ++o) kf[ks][o] = tm.frag_t(Ks + ks * 32 * N, t0w + o);
+            wave_meet(false);  // R is in place
+            // r = R - S beta R, over the tiles up to w
+            tm.template times_rows<3, 3>(v, sf, Rf);
+            const f32x4 ew = ew0 * bt;
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                rb[ct] = v[ct] * bt;
+                uw[ct] = v[ct] * ew;
+            }
+            tm.template put_rows<3>(Wf, uw);
+            tm.template put_rows<UT>(Uf, rb);
+#pragma unroll
+            for (int o = 0; o < OT; ++o)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) acc[o][ct] *= el;
+            wave_meet(false);  // the weighted u is in place
+            // h' = e^{c_L} h + K^T (e^{c_L - c} u) of this wave's tiles
+            bf16x8 wf[2][3][CT];
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) wf[ks][k][ct] = tm.template get<3>(Wf, ks, k, ct);
+#pragma unroll
+            for (int p = 0; p < OP; ++p)  // (a pair of tiles is split while the next is multiplied)
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+#pragma unroll
+                        for (int o = 2 * p; o < 2 * p + (OT > 1 ? 2 : 1); ++o)
+#pragma unroll
+                            for (int ct = 0; ct < CT; ++ct) acc[o][ct] = mma(acc[o][ct], kf[ks][o], wf[ks][k][ct]);
+            tm.split(acc, sp);
+            if (c + 1 < nc) tm.template put_state<QT>(Hf, sp);
+            if (SAVE) {
+                f32x4 rest[CT];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) rest[ct] = rest16(v[ct]);
+                tm.store_rows(a.r, c, v);
+                tm.store_rows(a.rlo, c, rest);
+            }
+        };
+        for (int c = 0; c < nc; c += 2) {
+            chunk(c, K0);
+            if (c + 1 < nc) chunk(c + 1, KB == 2 ? K1 : K0);
+        }
+        if (float* hT = SAVE ? a.hend : a.hT) {
+#pragma unroll
+            for (int o = 0; o < OT; ++o)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) st4(hT + tm.hn(t0w + o, ct), acc[o][ct]);
+        }
     }
 }
 
@@ -1474,11 +1596,13 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
     };
     if (nc > 0) {
         tm.fetch_tile(a.B, nc - 1, K0);
-        tm.template fetch_tab<TABN>(nc - 1, Sf);
+        tm.template fetch_tab<TABN / 512>(nc - 1, Sf);
         tm.fetch_x(a.x, nc - 1, Xs);
         tm.fetch_x(a.dy, nc - 1, Ys);
         tm.mark(Rf);
-        tm.put_state(Hf, acc);
+        Sp<bf16> sp[OP][CT];
+        tm.split(acc, sp);
+        tm.template put_state<3>(Hf, sp);
         leave(nc - 1, [&](int o, int ct) {
             const float* hp = a.hend + tm.hn(t0w + 2 * o, ct);
             return join(ld4(hp), ld4(OT > 1 ? hp + 4 : hp));
@@ -1574,7 +1698,7 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
         const float el = Vs[L - 1];
         wave_meet(true);  // dX is in place, Q has landed; every wave is done with the tables
         if (more) {
-            tm.template fetch_tab<TABN>(c - 1, Sf);
+            tm.template fetch_tab<TABN / 512>(c - 1, Sf);
             tm.fetch_x(a.x, c - 1, Xs);
         }
         tm.store_rows(a.z, c, v);
@@ -1612,7 +1736,9 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
                 }
         }
         if (more) {
-            tm.put_state(Hf, acc);
+            Sp<bf16> sp[OP][CT];
+            tm.split(acc, sp);
+            tm.template put_state<3>(Hf, sp);
             leave(c - 1, [&](int o, int ct) {
                 f32x8 hv;
 #pragma unroll

@@ -102,7 +102,7 @@ template <int N, int CT, bool SAVE>
 int walk_team(const Args& a) {
     const unsigned grid = (unsigned)((int64_t)a.rows.nrows * a.H * (a.P / (16 * CT)));
     // (at dstate 256 the backward's tables leave room for one K buffer only)
-    k_delta_team<N, CT, N == 256 && SAVE ? 1 : 2, SAVE><<<grid, 256, 0, a.stream>>>(a);
+    k_delta_team<N, CT, N == 256 && SAVE ? 1 : 2, SAVE><<<grid, 512, 0, a.stream>>>(a);
     return hipGetLastError() == hipSuccess ? 0 : 7;
 }
 template <int N, int CT>
