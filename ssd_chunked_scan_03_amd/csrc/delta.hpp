@@ -296,13 +296,33 @@ __device__ __forceinline__ bf16x8 frag_tab5(const bf16* tab, int i, int t, int l
     return ld8(tab + frag_at(i, 2 * t) + lane * 8);
 }
 
-// The triangular table `src` (16 x 16 blocks, row-major, as k_delta_prep stores it) into LDS as
-// operand fragments: dst[term][fragment][lane][8].  UP: its transpose.
+// The triangular table `src` (16 x 16 blocks, row-major, as k_delta_prep stores it) by way of 256
+// threads' registers into LDS as operand fragments: dst[term][fragment][lane][8].  UP: its
+// transpose.  Thread t holds lane t % 64's 4 elements of blocks t / 64, + 4 and + 8 (10 stored
+// blocks and the two zero ones that complete fragments).
+template <bool UP>
+__device__ __forceinline__ void get_tri(const float* __restrict__ src, f32x4 (&v)[3]) {
+    const int l = threadIdx.x & 63, l16 = l & 15, q = l >> 4;
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+        const int blk = wave_id() + 4 * u;
+        v[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (blk < kTri) {
+            if (UP) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[u][e] = src[blk * 256 + (4 * q + e) * 16 + l16];
+            } else {
+                v[u] = ld4(src + blk * 256 + l16 * 16 + 4 * q);
+            }
+        }
+    }
+}
 template <typename T, int NT, bool UP>
-__device__ void stage_tri(const float* __restrict__ src, T* dst, int tid, int nthr) {
-    // 10 stored blocks and the two zero ones that complete fragments; 64 pieces of 4 each
-    for (int p = tid; p < 12 * 64; p += nthr) {
-        const int blk = p >> 6, l = p & 63, l16 = l & 15, q = l >> 4;
+__device__ __forceinline__ void put_tri(const f32x4 (&s)[3], T* dst) {
+    const int l = threadIdx.x & 63;
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+        const int blk = wave_id() + 4 * u;
         int i, j;  // block row, column
         if (blk < kTri) {
             i = blk < 1 ? 0 : blk < 3 ? 1 : blk < 6 ? 2 : 3;
@@ -311,15 +331,7 @@ __device__ void stage_tri(const float* __restrict__ src, T* dst, int tid, int nt
             i = blk == kTri ? 0 : 2;
             j = i + 1;
         }
-        f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (blk < kTri) {
-            if (UP) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = src[blk * 256 + (4 * q + e) * 16 + l16];
-            } else {
-                v = ld4(src + blk * 256 + l16 * 16 + 4 * q);
-            }
-        }
+        f32x4 v = s[u];
         const int f = UP ? frag_up(j, i >> 1) : frag_lo(i, j >> 1);
         T* d = dst + f * 512 + l * 8 + 4 * ((UP ? i : j) & 1);
 #pragma unroll
@@ -340,6 +352,15 @@ __device__ __forceinline__ Sp<T> frag_tab(const T* tab, int f, int lane) {
 #pragma unroll
     for (int k = 0; k < NT; ++k) s.t[k] = ld8(tab + (k * kFrag + f) * 512 + lane * 8);
     return s;
+}
+
+// Every wave's LDS reads are done, or (LOADS) its transfers have landed; transfers that no
+// wave reads yet stay in flight (a __syncthreads would wait for them all).
+__device__ __forceinline__ void wave_meet(bool loads) {
+    if (loads) __builtin_amdgcn_s_waitcnt(0xF70);  // vmcnt(0)
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // rows [0, n) x cols [0, w) of src (row stride ss) into dst (row stride ds), rows [n, 64) and
@@ -598,22 +619,84 @@ struct Cfg {
     }
 };
 
+// A chunk's inputs on their way from memory to LDS, in 256 threads' registers: K and Q (dstate
+// 256 in float32, where one buffer holds both in turn: the one that is read first, Q in the
+// forward walk, K in the adjoint one), x, dY, the tables of S and M and the factors.
+template <typename T, int N, int CT, int MT, bool UP>
+struct Staged {
+    typedef Cfg<T, N> CF;
+    typedef typename V8<T>::type V;
+    static constexpr int NK = CF::NP / 32, NX = 2 * CT;  // 8-element pieces per thread
+    static constexpr bool K = UP || !CF::SHARE, Q = !UP || !CF::SHARE;
+    V k[K ? NK : 1], q[Q ? NK : 1], x[NX], y[NX];
+    f32x4 s[3], m[3];
+    float f[3];
+    template <int C>
+    static __device__ __forceinline__ void get(const T* src, int64_t ss, int n, int w, int wpad, V (&v)[C]) {
+        const int per = wpad >> 3;
+#pragma unroll
+        for (int u = 0; u < C; ++u) {
+            const int p = (int)threadIdx.x + u * 256, row = p / per, col = (p - row * per) << 3;
+            v[u] = zero8<T>();
+            if (row < n && col < w) v[u] = ld8(src + row * ss + col);
+        }
+    }
+    template <int C>
+    static __device__ __forceinline__ void set(T* dst, int ds, int wpad, const V (&v)[C]) {
+        const int per = wpad >> 3;
+#pragma unroll
+        for (int u = 0; u < C; ++u) {
+            const int p = (int)threadIdx.x + u * 256, row = p / per, col = (p - row * per) << 3;
+            if (row < L) st8(dst + row * ds + col, v[u]);
+        }
+    }
+    __device__ __forceinline__ void load(const Args& a, int row, int h, int c, int p0, int SW, bool dy) {
+        const int H = a.H, G = a.G, P = a.P, g = h / (H / G), t = threadIdx.x;
+        const int64_t t0 = a.rows.tok0(row) + (int64_t)c * L, e = (int64_t)(a.rows.kbase(row) + c) * H + h;
+        const int n = (int)min((int64_t)L, a.rows.len(row) - (int64_t)c * L);
+        if (K) get(static_cast<const T*>(a.B) + (t0 * G + g) * N, (int64_t)G * N, n, N, CF::NP, k);
+        if (Q) get(static_cast<const T*>(a.C) + (t0 * G + g) * N, (int64_t)G * N, n, N, CF::NP, q);
+        get(static_cast<const T*>(a.x) + (t0 * H + h) * P + p0, (int64_t)H * P, n, SW, SW, x);
+        if (dy) get(static_cast<const T*>(a.dy) + (t0 * H + h) * P + p0, (int64_t)H * P, n, SW, SW, y);
+        get_tri<UP>(a.tab + e * kTab, s);
+        get_tri<UP>(a.tab + e * kTab + kTri * 256, m);
+        if (t < L) {
+            f[0] = a.vec[e * kVec + t];
+            f[1] = a.vec[e * kVec + L + t];
+            f[2] = t < n ? to_f(static_cast<const T*>(a.beta)[(t0 + t) * H + h]) : 0.f;
+        }
+    }
+    __device__ __forceinline__ void put(T* Ks, T* Qs, T* Xs, T* Ys, T* Sf, T* Mf, float* factors, int SW, bool dy) const {
+        const int t = threadIdx.x;
+        if (K) set(Ks, CF::LDK, CF::NP, k);
+        if (Q) set(Qs, CF::LDK, CF::NP, q);
+        set(Xs, CF::ldx(SW), SW, x);
+        if (dy) set(Ys, CF::ldx(SW), SW, y);
+        put_tri<T, CF::NT, UP>(s, Sf);
+        put_tri<T, MT, UP>(m, Mf);
+        if (t < L)
+#pragma unroll
+            for (int i = 0; i < 3; ++i) factors[i * L + t] = f[i];
+    }
+};
+
 // ---------------------------------------------------------------------------
 // k_delta: the chunks of one (row, head) and a slice of 16 CT W headdim columns, in order
-// (W waves, each CT column tiles, no exchange between waves).  SAVE = false writes y and
+// (W waves, each CT column tiles, no exchange between waves).  All 256 threads stage; a
+// chunk's inputs are asked for while the chunk before is computed and wait in registers.  SAVE = false writes y and
 // hT.  SAVE = true is the backward's first walk: it writes the residuals r, the state
 // entering every chunk and after the last, and the per-token dY . Y (Y in float32, all
 // terms) instead.
 // ---------------------------------------------------------------------------
 template <typename T, int N, int CT, bool SAVE>
-__global__ __launch_bounds__(256) void k_delta(Args a) {
+__global__ __launch_bounds__(256) void k_delta(Args a, int waves) {
     typedef Cfg<T, N> CF;
     constexpr int NP = CF::NP, LDK = CF::LDK, NTL = N / 16, KS = NP / 32, NT = CF::NT;
     constexpr int MT = SAVE ? NT : 1;  // terms of M (1: y is rounded to the problem dtype anyway)
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
     const int H = a.H, G = a.G, P = a.P;
-    const int SW = 16 * CT * (nthr >> 6), ldx = CF::ldx(SW);
+    const int SW = 16 * CT * waves, ldx = CF::ldx(SW);
     T* Ks = reinterpret_cast<T*>(smem);
     T* Qs = CF::SHARE ? Ks : Ks + CF::KT;
     T* Sf = Qs + CF::KT;
@@ -633,37 +716,27 @@ __global__ __launch_bounds__(256) void k_delta(Args a) {
     const int64_t Tn = a.rows.len(row), tok0 = a.rows.tok0(row);
     const int nc = a.rows.nchunks(row), kb0 = a.rows.kbase(row);
     const int p0 = sl * SW, pw = w * 16 * CT;  // first column of the slice, of this wave in it
+    const bool on = w < waves;                 // the others stage only
 
     f32x4 acc[NTL][CT];  // h^T: row n = 16 t + 4q + e, column p
 #pragma unroll
     for (int t = 0; t < NTL; ++t)
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
-            acc[t][ct] = a.h0 ? ld4(a.h0 + (bh * P + p0 + pw + ct * 16 + l16) * N + t * 16 + 4 * q)
+            acc[t][ct] = a.h0 && on ? ld4(a.h0 + (bh * P + p0 + pw + ct * 16 + l16) * N + t * 16 + 4 * q)
                               : f32x4{0.f, 0.f, 0.f, 0.f};
 
+    Staged<T, N, CT, MT, false> in;
+    if (nc > 0) in.load(a, row, h, 0, p0, SW, SAVE);
     for (int c = 0; c < nc; ++c) {
         const int64_t t0 = tok0 + (int64_t)c * L;
         const int n = (int)min((int64_t)L, Tn - (int64_t)c * L);
         const int64_t e = (int64_t)(kb0 + c) * H + h;
-        const T* Kg = static_cast<const T*>(a.B) + (t0 * G + g) * N;
-        const T* Qg = static_cast<const T*>(a.C) + (t0 * G + g) * N;
-        __syncthreads();  // the previous chunk's tiles are no longer read
-        stage_rows(Qg, (int64_t)G * N, Qs, LDK, n, N, NP, tid, nthr);
-        if (!CF::SHARE) stage_rows(Kg, (int64_t)G * N, Ks, LDK, n, N, NP, tid, nthr);
-        stage_rows(static_cast<const T*>(a.x) + (t0 * H + h) * P + p0, (int64_t)H * P, Xs, ldx, n, SW, SW, tid, nthr);
-        if (SAVE)
-            stage_rows(static_cast<const T*>(a.dy) + (t0 * H + h) * P + p0, (int64_t)H * P, Ys, ldx, n, SW, SW, tid,
-                       nthr);
-        stage_tri<T, NT, false>(a.tab + e * kTab, Sf, tid, nthr);
-        stage_tri<T, MT, false>(a.tab + e * kTab + kTri * 256, Mf, tid, nthr);
-        for (int t = tid; t < L; t += nthr) {
-            ecs[t] = a.vec[e * kVec + t];
-            ews[t] = a.vec[e * kVec + L + t];
-            bts[t] = t < n ? to_f(static_cast<const T*>(a.beta)[(t0 + t) * H + h]) : 0.f;
-        }
-        __syncthreads();
-        if (SAVE) {
+        wave_meet(false);  // the previous chunk's tiles are no longer read
+        in.put(Ks, Qs, Xs, Ys, Sf, Mf, ecs, SW, SAVE);
+        wave_meet(false);
+        if (c + 1 < nc) in.load(a, row, h, c + 1, p0, SW, SAVE);
+        if (SAVE && on) {
             const int64_t ho = (e * P + p0 + pw) * N;
 #pragma unroll
             for (int t = 0; t < NTL; ++t)
@@ -705,12 +778,13 @@ __global__ __launch_bounds__(256) void k_delta(Args a) {
                 }
             }
         };
-        state_products(Qs, yq, std::integral_constant<int, SAVE ? 3 : 2>());
+        if (on) state_products(Qs, yq, std::integral_constant<int, SAVE ? 3 : 2>());
         if (CF::SHARE) {
-            __syncthreads();
-            stage_rows(Kg, (int64_t)G * N, Ks, LDK, n, N, NP, tid, nthr);
-            __syncthreads();
+            wave_meet(false);
+            stage_rows(static_cast<const T*>(a.B) + (t0 * G + g) * N, (int64_t)G * N, Ks, LDK, n, N, NP, tid, 256);
+            wave_meet(false);
         }
+        if (on) {
         state_products(Ks, v, std::integral_constant<int, 3>());
 
         // R, then r = R - S (beta R)
@@ -809,20 +883,22 @@ __global__ __launch_bounds__(256) void k_delta(Args a) {
                     if (l16 == 0) dots[w * L + t] = dot;
                 }
             }
-        __syncthreads();
+        }
+        wave_meet(false);
         store_rows(static_cast<T*>(SAVE ? a.r : a.y) + (t0 * H + h) * P + p0, (int64_t)H * P, Xs, ldx, n, SW, tid,
-                   nthr);
+                   256);
         if (SAVE) {
             if (NT > 1)
-                store_rows(static_cast<T*>(a.rlo) + (t0 * H + h) * P + p0, (int64_t)H * P, Ys, ldx, n, SW, tid, nthr);
-            for (int t = tid; t < n; t += nthr) {
+                store_rows(static_cast<T*>(a.rlo) + (t0 * H + h) * P + p0, (int64_t)H * P, Ys, ldx, n, SW, tid, 256);
+            for (int t = tid; t < n; t += 256) {
                 float s = 0.f;
-                for (int k2 = 0; k2 < (nthr >> 6); ++k2) s += dots[k2 * L + t];
+                for (int k2 = 0; k2 < waves; ++k2) s += dots[k2 * L + t];
                 a.dyy[((int64_t)sl * BH + bh) * a.T + (int64_t)c * L + t] = s;
             }
         }
     }
-    if (float* hT = SAVE ? a.hend : a.hT) {
+    float* hT = SAVE ? a.hend : a.hT;
+    if (hT && on) {
 #pragma unroll
         for (int t = 0; t < NTL; ++t)
 #pragma unroll
@@ -849,15 +925,6 @@ struct Dma {
     static constexpr int TILE = L * N;                                // elements
 };
 typedef __attribute__((address_space(3))) void lds_void;
-
-// Every wave's LDS reads are done, or (LOADS) its transfers have landed; transfers that no
-// wave reads yet stay in flight (a __syncthreads would wait for them all).
-__device__ __forceinline__ void wave_meet(bool loads) {
-    if (loads) __builtin_amdgcn_s_waitcnt(0xF70);  // vmcnt(0)
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
 
 // one wave's share of a 64 x N tile (row stride rs bytes, rows past the resource zero)
 template <int N>
@@ -1428,7 +1495,6 @@ __global__ __launch_bounds__(512) void k_delta_team(Args a) {
         Sp<bf16> sp[OP][CT];
         tm.split(acc, sp);
         if (nc > 0) tm.template put_state<QT>(Hf, sp);
-        __builtin_amdgcn_s_setprio(2);  // before the wave that shares the SIMD
         auto chunk = [&](int c, const bf16* Ks) {
             wave_meet(false);  // the chunk's tiles have landed
             tm.part_sums(Ks, sp, Pf);
@@ -1769,13 +1835,13 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
 // per-token dX . X, <dh', h'> of every chunk, and dh0.
 // ---------------------------------------------------------------------------
 template <typename T, int N, int CT>
-__global__ __launch_bounds__(256) void k_delta_rev(Args a) {
+__global__ __launch_bounds__(256) void k_delta_rev(Args a, int waves) {
     typedef Cfg<T, N> CF;
     constexpr int NP = CF::NP, LDK = CF::LDK, NTL = N / 16, KS = NP / 32, NT = CF::NT;
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
     const int H = a.H, G = a.G, P = a.P;
-    const int SW = 16 * CT * (nthr >> 6), ldx = CF::ldx(SW);
+    const int SW = 16 * CT * waves, ldx = CF::ldx(SW);
     T* Ks = reinterpret_cast<T*>(smem);
     T* Qs = CF::SHARE ? Ks : Ks + CF::KT;
     T* Sf = Qs + CF::KT;
@@ -1786,6 +1852,7 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a) {
     float* ews = ecs + L;
     float* bts = ews + L;
     float* dots = bts + L;  // [wave][token]
+    __shared__ float tots[4];
 
     const int nsl = P / SW, BH = a.rows.nrows * H;
     const int sl = (int)(blockIdx.x % (unsigned)nsl);
@@ -1794,69 +1861,76 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a) {
     const int64_t Tn = a.rows.len(row), tok0 = a.rows.tok0(row);
     const int nc = a.rows.nchunks(row), kb0 = a.rows.kbase(row);
     const int p0 = sl * SW, pw = w * 16 * CT;
+    const bool on = w < waves;  // the others stage only
 
     f32x4 acc[NTL][CT];  // dh^T
 #pragma unroll
     for (int t = 0; t < NTL; ++t)
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
-            acc[t][ct] = a.dhT ? ld4(a.dhT + (bh * P + p0 + pw + ct * 16 + l16) * N + t * 16 + 4 * q)
+            acc[t][ct] = a.dhT && on ? ld4(a.dhT + (bh * P + p0 + pw + ct * 16 + l16) * N + t * 16 + 4 * q)
                                : f32x4{0.f, 0.f, 0.f, 0.f};
 
+    // the state after a chunk, for <dh', h'>: asked for with the chunk's inputs (dstate 256 leaves
+    // no registers to wait in)
+    constexpr bool AHEAD = N <= 128;
+    typename V4<T>::type hi[NTL][CT];
+    s16x4 lo[NTL][CT];
+    auto load_h = [&](int c) {
+        const int64_t ho = (((int64_t)(kb0 + c + 1) * H + h) * P + p0 + pw) * N;
+#pragma unroll
+        for (int t = 0; t < NTL; ++t)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                const int64_t o = ho + (ct * 16 + l16) * N + t * 16 + 4 * q;
+                hi[t][ct] = ld4(static_cast<const T*>(a.hin) + o);
+                if (NT > 1) lo[t][ct] = *reinterpret_cast<const s16x4*>(a.hlo + o);
+            }
+    };
+    Staged<T, N, CT, NT, true> in;
+    if (nc > 0) in.load(a, row, h, nc - 1, p0, SW, true);
     for (int c = nc - 1; c >= 0; --c) {
         const int64_t t0 = tok0 + (int64_t)c * L;
         const int n = (int)min((int64_t)L, Tn - (int64_t)c * L);
         const int64_t e = (int64_t)(kb0 + c) * H + h;
-        const T* Kg = static_cast<const T*>(a.B) + (t0 * G + g) * N;
-        const T* Qg = static_cast<const T*>(a.C) + (t0 * G + g) * N;
-        {  // <dh', h'> over this slice
-            const bool last = c + 1 == nc;
-            const int64_t ho = ((last ? bh : e + H) * P + p0 + pw) * N;
-            float s = 0.f;
+        float s = 0.f;  // <dh', h'> over this wave's columns
+        if (on) {
+            if (!AHEAD && c + 1 < nc) load_h(c);
 #pragma unroll
             for (int t = 0; t < NTL; ++t)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-                    const int64_t o = ho + (ct * 16 + l16) * N + t * 16 + 4 * q;
                     f32x4 hv;
-                    if (last) {
-                        hv = ld4(a.hend + o);
+                    if (c + 1 == nc) {
+                        hv = ld4(a.hend + (bh * P + p0 + pw + ct * 16 + l16) * N + t * 16 + 4 * q);
                     } else if constexpr (std::is_same<T, bf16>::value) {
-                        const bf16x4 hi = ld4(static_cast<const T*>(a.hin) + o);
-                        const s16x4 lo = *reinterpret_cast<const s16x4*>(a.hlo + o);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) hv[i] = join_state(hi[i], lo[i]);
+                        for (int i = 0; i < 4; ++i) hv[i] = join_state(hi[t][ct][i], lo[t][ct][i]);
                     } else {
-                        hv = ld4(static_cast<const T*>(a.hin) + o);
+                        hv = hi[t][ct];
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s += hv[i] * acc[t][ct][i];
                 }
-#pragma unroll
-            for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
-            __syncthreads();  // the sums of the chunk before are no longer read
-            if (lane == 0) dots[w] = s;
-            __syncthreads();
-            if (tid == 0) {
-                float v = 0.f;
-                for (int k2 = 0; k2 < (nthr >> 6); ++k2) v += dots[k2];
-                a.tot[(int64_t)sl * a.ntab * H + e] = v;
-            }
+            s = row_sum16(s);
+            s += __shfl_xor(s, 16, 64);
+            s += __shfl_xor(s, 32, 64);
         }
-        __syncthreads();
-        stage_rows(Kg, (int64_t)G * N, Ks, LDK, n, N, NP, tid, nthr);
-        if (!CF::SHARE) stage_rows(Qg, (int64_t)G * N, Qs, LDK, n, N, NP, tid, nthr);
-        stage_rows(static_cast<const T*>(a.x) + (t0 * H + h) * P + p0, (int64_t)H * P, Xs, ldx, n, SW, SW, tid, nthr);
-        stage_rows(static_cast<const T*>(a.dy) + (t0 * H + h) * P + p0, (int64_t)H * P, Ys, ldx, n, SW, SW, tid, nthr);
-        stage_tri<T, NT, true>(a.tab + e * kTab, Sf, tid, nthr);
-        stage_tri<T, NT, true>(a.tab + e * kTab + kTri * 256, Mf, tid, nthr);
-        for (int t = tid; t < L; t += nthr) {
-            ecs[t] = a.vec[e * kVec + t];
-            ews[t] = a.vec[e * kVec + L + t];
-            bts[t] = t < n ? to_f(static_cast<const T*>(a.beta)[(t0 + t) * H + h]) : 0.f;
+        wave_meet(false);  // the previous chunk's tiles are no longer read
+        if (on && lane == 0) tots[w] = s;
+        in.put(Ks, Qs, Xs, Ys, Sf, Mf, ecs, SW, true);
+        wave_meet(false);
+        if (c > 0) {
+            in.load(a, row, h, c - 1, p0, SW, true);
+            if (AHEAD && on) load_h(c - 1);
         }
-        __syncthreads();
-        {
+        if (tid == 0) {
+            float v = 0.f;
+            for (int k2 = 0; k2 < waves; ++k2) v += tots[k2];
+            a.tot[(int64_t)sl * a.ntab * H + e] = v;
+        }
+        Sp<T> b2[2][CT];
+        if (on) {
             T* lp = static_cast<T*>(a.lin) + (e * P + p0 + pw) * N;
 #pragma unroll
             for (int t = 0; t < NTL; ++t)
@@ -1867,7 +1941,6 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a) {
                     for (int i = 0; i < 4; ++i) o[i] = from_f<T>(acc[t][ct][i]);
                     st4(lp + (ct * 16 + l16) * N + t * 16 + 4 * q, o);
                 }
-        }
         // dU = e^{c_L - c} K dh'^T + M^T dY
         f32x4 v[4][CT];
 #pragma unroll
@@ -1911,7 +1984,6 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a) {
             }
         }
         // z = dU - S^T (beta dU)
-        Sp<T> b2[2][CT];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -1995,11 +2067,13 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a) {
                     d[i] = to_f(dyf[t][ct][i]) * ecs[32 * t + 16 * (i >> 2) + 4 * q + (i & 3)];
                 split8(d, b2[t][ct]);
             }
-        if (CF::SHARE) {
-            __syncthreads();
-            stage_rows(Qg, (int64_t)G * N, Qs, LDK, n, N, NP, tid, nthr);
         }
-        __syncthreads();
+        if (CF::SHARE) {
+            wave_meet(false);
+            stage_rows(static_cast<const T*>(a.C) + (t0 * G + g) * N, (int64_t)G * N, Qs, LDK, n, N, NP, tid, 256);
+        }
+        wave_meet(false);
+        if (on) {
 #pragma unroll
         for (int t = 0; t < NTL; ++t)
 #pragma unroll
@@ -2008,15 +2082,16 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a) {
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) acc[t][ct] = mma_es<3>(acc[t][ct], qf, b2[ks][ct]);
             }
-        store_rows(static_cast<T*>(a.dx) + (t0 * H + h) * P + p0, (int64_t)H * P, Xs, ldx, n, SW, tid, nthr);
-        store_rows(static_cast<T*>(a.z) + (t0 * H + h) * P + p0, (int64_t)H * P, Ys, ldx, n, SW, tid, nthr);
-        for (int t = tid; t < n; t += nthr) {
+        }
+        store_rows(static_cast<T*>(a.dx) + (t0 * H + h) * P + p0, (int64_t)H * P, Xs, ldx, n, SW, tid, 256);
+        store_rows(static_cast<T*>(a.z) + (t0 * H + h) * P + p0, (int64_t)H * P, Ys, ldx, n, SW, tid, 256);
+        for (int t = tid; t < n; t += 256) {
             float s = 0.f;
-            for (int k2 = 0; k2 < (nthr >> 6); ++k2) s += dots[k2 * L + t];
+            for (int k2 = 0; k2 < waves; ++k2) s += dots[k2 * L + t];
             a.dxx[((int64_t)sl * BH + bh) * a.T + (int64_t)c * L + t] = s;
         }
     }
-    if (a.dh0) {
+    if (a.dh0 && on) {
 #pragma unroll
         for (int t = 0; t < NTL; ++t)
 #pragma unroll

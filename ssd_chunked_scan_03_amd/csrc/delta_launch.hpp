@@ -51,15 +51,15 @@ int walk(const Args& a, int waves, int which) {
     if (which == 0) {
         const size_t lds = CF::walk_bytes(sw, 1, 1);
         if (!lds_limit(k_delta<T, N, CT, false>, lds)) return 7;
-        k_delta<T, N, CT, false><<<grid, 64 * waves, lds, a.stream>>>(a);
+        k_delta<T, N, CT, false><<<grid, 256, lds, a.stream>>>(a, waves);
     } else if (which == 1) {
         const size_t lds = CF::walk_bytes(sw, CF::NT, 2);
         if (!lds_limit(k_delta<T, N, CT, true>, lds)) return 7;
-        k_delta<T, N, CT, true><<<grid, 64 * waves, lds, a.stream>>>(a);
+        k_delta<T, N, CT, true><<<grid, 256, lds, a.stream>>>(a, waves);
     } else {
         const size_t lds = CF::walk_bytes(sw, CF::NT, 2);
         if (!lds_limit(k_delta_rev<T, N, CT>, lds)) return 7;
-        k_delta_rev<T, N, CT><<<grid, 64 * waves, lds, a.stream>>>(a);
+        k_delta_rev<T, N, CT><<<grid, 256, lds, a.stream>>>(a, waves);
     }
     return hipGetLastError() == hipSuccess ? 0 : 7;
 }
