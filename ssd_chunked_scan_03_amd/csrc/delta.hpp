@@ -2108,28 +2108,38 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a, int waves) {
 // read.  Everything here ends in the problem dtype: the states enter with one bfloat16
 // term, r, z and the tables with two, so that every product has one rounded factor at most.
 // ---------------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ typename V8<T>::type bld8(brsrc r, int vo, int so) {
+    const u32x4v a = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(r, vo, so, 0));
+    if constexpr (sizeof(T) == 2) {
+        return __builtin_bit_cast(bf16x8, a);
+    } else {
+        const u32x4v b = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(r, vo + 16, so, 0));
+        return join(__builtin_bit_cast(f32x4, a), __builtin_bit_cast(f32x4, b));
+    }
+}
+
 template <typename T, int N>
 struct GradCfg {
     static constexpr int NS = N < 64 ? N : 64;
-    static constexpr int LDN = NS + 8;
-    static size_t bytes(int P) {
-        const int PP = P < 32 ? 32 : P;
-        return (size_t)(2 * L + 2 * PP) * LDN * sizeof(T) + (size_t)5 * L * 4;
-    }
+    static constexpr int LDN = NS + 8, LDP = 32 + 8;
+    static constexpr int TILES = kTerms<T> > 1 ? 5 : 3;  // dY, r, z, and (bfloat16) the terms that r and z leave
+    static constexpr size_t BYTES = (size_t)((2 * L + 2 * 32) * LDN + TILES * L * LDP) * sizeof(T) + (size_t)5 * L * 4;
 };
 
 template <typename T, int N>
-__global__ __launch_bounds__(256, 2) void k_delta_grad(Args a) {
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_grad(Args a) {
     typedef GradCfg<T, N> CF;
-    constexpr int NS = CF::NS, LDN = CF::LDN, NTL = NS / 16, SLABS = N / NS;
+    constexpr int NS = CF::NS, LDN = CF::LDN, LDP = CF::LDP, NTL = NS / 16, SLABS = N / NS, TILES = CF::TILES;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
-    const int H = a.H, G = a.G, P = a.P, PP = P < 32 ? 32 : P;
+    const int H = a.H, G = a.G, P = a.P, KP = (P + 31) / 32;
     T* Ks = reinterpret_cast<T*>(smem);
     T* Qs = Ks + L * LDN;
     T* Hs = Qs + L * LDN;
-    T* Ls = Hs + PP * LDN;
-    float* ecs = reinterpret_cast<float*>(Ls + PP * LDN);
+    T* Ls = Hs + 32 * LDN;
+    T* Ts = Ls + 32 * LDN;
+    float* ecs = reinterpret_cast<float*>(Ts + TILES * L * LDP);
     float* ews = ecs + L;
     float* chi = ews + L;
     float* clo = chi + L;
@@ -2148,6 +2158,49 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(Args a) {
     const int hb = g * Hg + sub * per, he = min(g * Hg + Hg, hb + per);
     const int n0 = slab * NS;
 
+    // 32 headdim columns of a head at a time, asked for a step ahead
+    typedef typename V8<T>::type F8;
+    auto rows = [&](const void* p) {
+        return make_rsrc(static_cast<const T*>(p) + t0 * H * P, (uint32_t)((int64_t)n * H * P * sizeof(T)));
+    };
+    auto states = [&](const void* p) {
+        return make_rsrc(static_cast<const T*>(p) + (int64_t)kk * H * P * N, (uint32_t)((int64_t)H * P * N * sizeof(T)));
+    };
+    const brsrc src[5] = {rows(a.dy), rows(a.r), rows(a.z), rows(TILES > 3 ? a.rlo : a.r), rows(TILES > 3 ? a.zlo : a.z)};
+    const brsrc hsrc = states(a.hin), lsrc = states(a.lin);
+    F8 tv[TILES], hv, lv;
+    float fv[5];
+    const int tr = tid >> 2, tc = (tid & 3) << 3, hr = tid / (NS / 8), hc = (tid % (NS / 8)) << 3;
+    constexpr int NONE = 0x7fff0000;  // beyond every resource: reads as zero
+    const int to = tc < P ? (tr * H * P + tc) * (int)sizeof(T) : NONE;
+    const int ho = hr < 32 && hr < P ? (hr * N + n0 + hc) * (int)sizeof(T) : NONE;
+    auto load = [&](int h, int ks) {
+        const int64_t e = (int64_t)kk * H + h;
+        const int ts = (h * P + ks * 32) * (int)sizeof(T), hs = (h * P + ks * 32) * N * (int)sizeof(T);
+#pragma unroll
+        for (int k = 0; k < TILES; ++k) tv[k] = bld8<T>(src[k], to, ts);
+        hv = bld8<T>(hsrc, ho, hs);
+        lv = bld8<T>(lsrc, ho, hs);
+        if (ks == 0 && tid < L) {
+            fv[0] = a.vec[e * kVec + tid];
+            fv[1] = a.vec[e * kVec + L + tid];
+            fv[2] = a.vec[e * kVec + 3 * L + tid];
+            fv[3] = a.vec[e * kVec + 4 * L + tid];
+            fv[4] = tid < n ? to_f(static_cast<const T*>(a.beta)[(t0 + tid) * H + h]) : 0.f;
+        }
+    };
+    auto put = [&](int ks) {
+#pragma unroll
+        for (int k = 0; k < TILES; ++k) st8(Ts + (k * L + tr) * LDP + tc, tv[k]);
+        if (hr < 32) {
+            st8(Hs + hr * LDN + hc, hv);
+            st8(Ls + hr * LDN + hc, lv);
+        }
+        if (ks == 0 && tid < L)
+#pragma unroll
+            for (int k = 0; k < 5; ++k) ecs[k * L + tid] = fv[k];
+    };
+    if (hb < he) load(hb, 0);
     stage_rows(static_cast<const T*>(a.B) + (t0 * G + g) * N + n0, (int64_t)G * N, Ks, LDN, n, NS, NS, tid, 256);
     stage_rows(static_cast<const T*>(a.C) + (t0 * G + g) * N + n0, (int64_t)G * N, Qs, LDN, n, NS, NS, tid, 256);
     f32x4 dq[NTL], dk[NTL];
@@ -2156,71 +2209,64 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(Args a) {
     const int i = w * 16 + l16;  // this lane's token column
 
     for (int h = hb; h < he; ++h) {
-        const int64_t e = (int64_t)kk * H + h;
-        __syncthreads();
-        stage_rows(static_cast<const T*>(a.hin) + e * P * N + n0, (int64_t)N, Hs, LDN, P, NS, NS, tid, 256, PP);
-        stage_rows(static_cast<const T*>(a.lin) + e * P * N + n0, (int64_t)N, Ls, LDN, P, NS, NS, tid, 256, PP);
-        if (tid < L) {
-            ecs[tid] = a.vec[e * kVec + tid];
-            ews[tid] = a.vec[e * kVec + L + tid];
-            chi[tid] = a.vec[e * kVec + 3 * L + tid];
-            clo[tid] = a.vec[e * kVec + 4 * L + tid];
-            bts[tid] = tid < n ? to_f(static_cast<const T*>(a.beta)[(t0 + tid) * H + h]) : 0.f;
-        }
-        __syncthreads();
-        const int64_t r0 = (t0 * H + h) * P, rs = (int64_t)H * P;
-        auto rowf = [&](const void* base, int tile, int ks) {  // row fragment, zero past n and P
-            const int t = tile * 16 + l16, col = ks * 32 + 8 * q;
-            const bool in = t < n && col < P;
-            return sel8(in, ld8(static_cast<const T*>(base) + r0 + (t < n ? t : 0) * rs + (col < P ? col : 0)));
-        };
         // r and z in two terms (the gradients of B would lose half of their rounding's room to
         // one): the product with a tensor that has one term, and of the two
         constexpr bool TWO = kTerms<T> > 1;
-        typedef typename V8<T>::type F8;
-        // tables: pt = dP_{ij} (rows j), wt = W_{ij} (rows j) for j <= i; pc = dP_{ai},
-        // wc = W_{ai} (rows a) for a >= i
-        f32x4 pt[4], wt[4], pc[4], wc[4];
+        // tables, rows j: pa = dP_{ij}, wa = W_{ij} in the tiles j <= i (i is this wave's), and in
+        // those beyond dP_{ji}, W_{ji}; pd, wd the latter in the diagonal tile
+        f32x4 pa[4], wa[4], pd = f32x4{0.f, 0.f, 0.f, 0.f}, wd = pd;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) pt[j] = wt[j] = pc[j] = wc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < 4; ++j) pa[j] = wa[j] = f32x4{0.f, 0.f, 0.f, 0.f};
         f32x4 th[NTL], tz[NTL], tl[NTL];  // h^T dY^T, h^T z^T, dh'^T r^T
 #pragma unroll
         for (int t = 0; t < NTL; ++t) th[t] = tz[t] = tl[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (int ks = 0; ks < PP / 32; ++ks) {
-            const F8 yi = rowf(a.dy, w, ks), ri = rowf(a.r, w, ks), zi = rowf(a.z, w, ks);
+        for (int ks = 0; ks < KP; ++ks) {
+            wave_meet(false);  // the step before is done with its tiles
+            put(ks);
+            wave_meet(false);
+            if (ks + 1 < KP) load(h, ks + 1);
+            else if (h + 1 < he) load(h + 1, 0);
+            auto rowf = [&](int k, int tile) { return ld8(Ts + (k * L + tile * 16 + l16) * LDP + 8 * q); };
+            const F8 yi = rowf(0, w), ri = rowf(1, w), zi = rowf(2, w);
             F8 rl = ri, zl = zi;
             if (TWO) {
-                rl = rowf(a.rlo, w, ks);
-                zl = rowf(a.zlo, w, ks);
+                rl = rowf(3, w);
+                zl = rowf(4, w);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (j <= w) {
-                    const F8 rj = j == w ? ri : rowf(a.r, j, ks);
-                    pt[j] = mma(pt[j], rj, yi);
-                    wt[j] = mma(wt[j], rj, zi);
+                    const F8 rj = rowf(1, j);
+                    pa[j] = mma(pa[j], rj, yi);
+                    wa[j] = mma(wa[j], rj, zi);
                     if (TWO) {
-                        const F8 rk = j == w ? rl : rowf(a.rlo, j, ks);
-                        pt[j] = mma(pt[j], rk, yi);
-                        wt[j] = mma(wt[j], rk, zi);
-                        wt[j] = mma(wt[j], rj, zl);
+                        const F8 rk = rowf(3, j);
+                        pa[j] = mma(pa[j], rk, yi);
+                        wa[j] = mma(wa[j], rk, zi);
+                        wa[j] = mma(wa[j], rj, zl);
                     }
-                }
-                if (j >= w) {
-                    const F8 yj = j == w ? yi : rowf(a.dy, j, ks), zj = j == w ? zi : rowf(a.z, j, ks);
-                    pc[j] = mma(pc[j], yj, ri);
-                    wc[j] = mma(wc[j], zj, ri);
+                } else {
+                    const F8 yj = rowf(0, j), zj = rowf(2, j);
+                    pa[j] = mma(pa[j], yj, ri);
+                    wa[j] = mma(wa[j], zj, ri);
                     if (TWO) {
-                        pc[j] = mma(pc[j], yj, rl);
-                        wc[j] = mma(wc[j], zj, rl);
-                        wc[j] = mma(wc[j], j == w ? zl : rowf(a.zlo, j, ks), ri);
+                        pa[j] = mma(pa[j], yj, rl);
+                        wa[j] = mma(wa[j], zj, rl);
+                        wa[j] = mma(wa[j], rowf(4, j), ri);
                     }
                 }
             }
+            pd = mma(pd, yi, ri);
+            wd = mma(wd, zi, ri);
+            if (TWO) {
+                pd = mma(pd, yi, rl);
+                wd = mma(wd, zi, rl);
+                wd = mma(wd, zl, ri);
+            }
 #pragma unroll
             for (int t = 0; t < NTL; ++t) {
-                const auto hf = frag_rows(Hs, LDN, ks * 32, t * 16, lane);
-                const auto lf = frag_rows(Ls, LDN, ks * 32, t * 16, lane);
+                const auto hf = frag_rows(Hs, LDN, 0, t * 16, lane);
+                const auto lf = frag_rows(Ls, LDN, 0, t * 16, lane);
                 th[t] = mma(th[t], hf, yi);
                 tz[t] = mma(tz[t], hf, zi);
                 tl[t] = mma(tl[t], lf, ri);
@@ -2231,49 +2277,53 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(Args a) {
             }
         }
         const float bi = bts[i], ci = chi[i], di = clo[i];
-        if (slab == 0) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float zr = 0.f;  // z_i . r_i sits on the diagonal of this wave's own tile
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j == w) zr = wt[j][r];
-                if (4 * q + r == l16 && i < n)
-                    static_cast<T*>(a.dbeta)[(t0 + i) * H + h] = from_f<T>(zr);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int o = j * 16 + 4 * q + r;  // the other token
-                const float bo = bts[o], d = (ci - chi[o]) + (di - clo[o]);
-                const float gl = exp2f_fast(fminf(d, 0.f)), gc = exp2f_fast(fminf(-d, 0.f));
-                pt[j][r] = o <= i ? pt[j][r] * (gl * bo) : 0.f;
-                pc[j][r] = o >= i ? pc[j][r] * (gc * bi) : 0.f;
-                wt[j][r] = (o < i ? -wt[j][r] * (gl * bo * bi) : 0.f) + (o > i ? -wc[j][r] * (gc * bo * bi) : 0.f);
-            }
-        Sp<T> sp[2], sc[2], sw[2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            split8(join(pt[2 * t], pt[2 * t + 1]), sp[t]);
-            split8(join(pc[2 * t], pc[2 * t + 1]), sc[t]);
-            split8(join(wt[2 * t], wt[2 * t + 1]), sw[t]);
-        }
         const float s1 = ecs[i], s2 = ecs[i] * bi, s3 = ews[i] * bi;
 #pragma unroll
         for (int t = 0; t < NTL; ++t) {
             dq[t] += th[t] * s1;
             dk[t] += tl[t] * s3 - tz[t] * s2;
+        }
+        Sp<T> sp[2], sc[2], sw[2];  // dP below, dP above, W, with their decays
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            f32x4 pl[2], pu[2], wt[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int j = 2 * t + u;
+                const f32x4 bo = ld4(bts + j * 16 + 4 * q), co = ld4(chi + j * 16 + 4 * q), lo = ld4(clo + j * 16 + 4 * q);
+                if (j == w && slab == 0) {  // z_i . r_i sits on the diagonal of this wave's own tile
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (4 * q + r == l16 && i < n)
+                            static_cast<T*>(a.dbeta)[(t0 + i) * H + h] = from_f<T>(wa[j][r]);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int o = j * 16 + 4 * q + r;  // the other token
+                    const float d = (ci - co[r]) + (di - lo[r]);
+                    const float e = exp2f_fast(fminf(o <= i ? d : -d, 0.f));
+                    const bool up = j == w && o >= i;
+                    pl[u][r] = o <= i ? pa[j][r] * (e * bo[r]) : 0.f;
+                    pu[u][r] = o >= i ? (up ? pd[r] : pa[j][r]) * (e * bi) : 0.f;
+                    wt[u][r] = o != i ? -(up ? wd[r] : wa[j][r]) * (e * bo[r] * bi) : 0.f;
+                }
+            }
+            split8(join(pl[0], pl[1]), sp[t]);
+            split8(join(pu[0], pu[1]), sc[t]);
+            split8(join(wt[0], wt[1]), sw[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < NTL; ++t)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 const auto kf = frag_rows_split(Ks, LDN, ks * 32 + 4 * q, ks * 32 + 16 + 4 * q, t * 16, lane);
-                const auto qf = frag_rows_split(Qs, LDN, ks * 32 + 4 * q, ks * 32 + 16 + 4 * q, t * 16, lane);
-                dq[t] = mma_es<2>(dq[t], kf, sp[ks]);
                 dk[t] = mma_es<2>(dk[t], kf, sw[ks]);
-                dk[t] = mma_es<2>(dk[t], qf, sc[ks]);
+                if (2 * ks <= w) dq[t] = mma_es<2>(dq[t], kf, sp[ks]);
+                if (2 * ks + 1 >= w) {
+                    const auto qf = frag_rows_split(Qs, LDN, ks * 32 + 4 * q, ks * 32 + 16 + 4 * q, t * 16, lane);
+                    dk[t] = mma_es<2>(dk[t], qf, sc[ks]);
+                }
             }
-        }
     }
     if (i >= n) return;
     const int64_t o = ((t0 + i) * G + g) * N + n0 + 4 * q;

@@ -164,7 +164,7 @@ int run_bwd(const Args& a) {
         if (!st) st = walk_n<T, N>(a, s, 2);
     }
     if (st) return st;
-    const size_t lds = GC::bytes(a.P);
+    const size_t lds = GC::BYTES;
     if (!lds_limit(k_delta_grad<T, N>, lds)) return 7;
     const int64_t wgs = (int64_t)a.ntab * a.G * a.nsub * (N / GC::NS);
     k_delta_grad<T, N><<<(unsigned)wgs, 256, lds, a.stream>>>(a);
