@@ -304,22 +304,24 @@ def _norm_problem(B, C, wB, wC, mode, eps, inv_freq, positions, interleaved):
         raise TypeError(f"B and C must be bfloat16 or float32, got {B.dtype}")
     if C.dtype != B.dtype:
         raise TypeError("B, C must share one dtype")
-    dev = B.get_device()
-    for name, t, shape, dtype in (("wB", wB, (N,), torch.float32), ("wC", wC, (N,), torch.float32),
-                                  ("inv_freq", inv_freq, (F,), torch.float32),
-                                  ("positions", positions, (b, T), torch.int32)):
-        if t is None:
-            continue
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.get_device() != dev or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous tensor on {B.device}")
+    dev, f32 = B.get_device(), torch.float32
+    for t, shape, dtype in ((wB, (N,), f32), (wC, (N,), f32), (inv_freq, (F,), f32), (positions, (b, T), torch.int32)):
+        if t is not None and (t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous()):
+            name = "wB" if t is wB else "wC" if t is wC else "inv_freq" if t is inv_freq else "positions"
+            _norm_refuse(t, name, shape, dtype, B)
     if dev < 0 or C.get_device() != dev:
         raise ValueError("B and C must be GPU tensors on one device")
-    return _norm_plan(b, T, GB, GC, N, F, _token_stride("B", B), _token_stride("C", C), float(eps), NORM_MODES[mode],
-                      int(bool(interleaved)), code)
+    sB = GB * N if B.is_contiguous() else _token_stride("B", B)
+    sC = GC * N if C.is_contiguous() else _token_stride("C", C)
+    return _norm_plan(b, T, GB, GC, N, F, sB, sC, float(eps), NORM_MODES[mode], int(bool(interleaved)), code)
+
+
+def _norm_refuse(t, name, shape, dtype, B):
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be a contiguous tensor on {B.device}")
 
 
 def bc_norm_into(prob: Norm, B, C, wB, wC, inv_freq, positions, Bn, Cn, stream=None) -> None:
@@ -335,7 +337,8 @@ def bc_norm(B, C, wB=None, wC=None, mode="rms", eps=1e-6, inv_freq=None, positio
     views into a wider projection.  Returns (Bn, Cn), contiguous."""
     import torch
     prob, _ = _norm_problem(B, C, wB, wC, mode, eps, inv_freq, positions, interleaved)
-    Bn, Cn = torch.empty(B.shape, dtype=B.dtype, device=B.device), torch.empty(C.shape, dtype=C.dtype, device=C.device)
+    whole = torch.contiguous_format
+    Bn, Cn = torch.empty_like(B, memory_format=whole), torch.empty_like(C, memory_format=whole)
     bc_norm_into(prob, B, C, wB, wC, inv_freq, positions, Bn, Cn)
     return Bn, Cn
 
