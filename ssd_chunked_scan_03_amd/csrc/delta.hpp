@@ -101,6 +101,7 @@ struct Args {
     float* dAp;   // [ntab][H]
     float* part;  // [nsub][2][b T][G][N] partial dK, dQ when a group's heads are shared out
     int slices, nsub;
+    int* order;   // packed: [nrows] the rows in the order that the walks start them
     hipStream_t stream;
 };
 
@@ -386,6 +387,50 @@ __device__ __forceinline__ void store_rows(T* __restrict__ dst, int64_t ds, cons
     }
 }
 
+// Blocks k, k + 8, k + 16, ... run on one XCD: block k of n takes the item that gives each XCD a
+// contiguous range of them, so that neighbours share what they read through one L2.
+__device__ __forceinline__ unsigned xcd_range(unsigned k, unsigned n) {
+    const unsigned x = k & 7, r = n & 7;
+    return x * (n >> 3) + (x < r ? x : r) + (k >> 3);
+}
+// The (head, slice) items of the walks, in ranges within each row: the slices of a head share
+// its tables, the heads of a group its keys.  Packed rows run in `order`, longest first: a
+// long row that starts last would be walked alone.
+struct Item {
+    int bh, sl;
+};
+__device__ __forceinline__ Item xcd_item(unsigned k, int H, int nsl, const int* order) {
+    const unsigned n = (unsigned)H * nsl, it = xcd_range(k % n, n);
+    const int r = (int)(k / n), row = order ? order[r] : r;
+    return Item{row * H + (int)(it / nsl), (int)(it % nsl)};
+}
+// That order, by one wave: rows by the power of two below their chunks, descending (one pass
+// for the powers there are, one for each; past 1024 rows, where no row is much of the whole, as
+// they come).
+__device__ __forceinline__ void order_rows(const Rows& rows, int* order, int lane) {
+    const int n = rows.nrows;
+    if (n > 1024) {
+        for (int r = lane; r < n; r += 64) order[r] = r;
+        return;
+    }
+    auto key = [&](int r) { return 32 - __clz(rows.nchunks(r)); };
+    unsigned there = 0;
+    for (int r = lane; r < n; r += 64) there |= 1u << key(r);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) there |= (unsigned)__shfl_xor((int)there, off, 64);
+    int at = 0;
+    for (int k = 31; k >= 0; --k) {
+        if (!(there >> k & 1)) continue;
+        for (int r0 = 0; r0 < n; r0 += 64) {
+            const int r = r0 + lane;
+            const bool mine = r < n && key(r) == k;
+            const uint64_t m = __ballot(mine);
+            if (mine) order[at + __popcll(m & ((1ull << lane) - 1))] = r;
+            at += __popcll(m);
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // k_delta_prep: S and M of a (chunk, head), and the chunk's decay factors; one wave per item,
 // no barriers.  A wave takes one (chunk, group) and `heads` of its heads: K K^T and Q K^T once,
@@ -414,6 +459,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(Args a, int heads) {
     const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
     PrepLds& m = lds[w];
     const int H = a.H, G = a.G, Hg = H / G, nhb = (Hg + heads - 1) / heads;
+    if (a.order && blockIdx.x == 0 && w == 0) order_rows(a.rows, a.order, lane);
     const int64_t id = (int64_t)blockIdx.x * 4 + w;
     const int hb = (int)(id % nhb), g = (int)(id / nhb % G);
     const int64_t kk = id / nhb / G;
@@ -709,9 +755,9 @@ __global__ __launch_bounds__(256) void k_delta(Args a, int waves) {
     float* dots = bts + L;  // SAVE: [wave][token]
 
     const int nsl = P / SW, BH = a.rows.nrows * H;
-    const int sl = (int)(blockIdx.x % (unsigned)nsl);
-    int k = (int)(blockIdx.x / (unsigned)nsl);
-    const int64_t bh = k;
+    const Item it0 = xcd_item(blockIdx.x, H, nsl, a.order);
+    const int sl = it0.sl;
+    const int64_t bh = it0.bh;
     const int h = (int)(bh % H), row = (int)(bh / H), g = h / (H / G);
     const int64_t Tn = a.rows.len(row), tok0 = a.rows.tok0(row);
     const int nc = a.rows.nchunks(row), kb0 = a.rows.kbase(row);
@@ -953,7 +999,8 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
     const int tid = threadIdx.x, nw = blockDim.x >> 6, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
     const int H = a.H, G = a.G, P = a.P;
     const int SW = 16 * CT * nw, nsl = P / SW;
-    const int sl = (int)(blockIdx.x % (unsigned)nsl), bh = (int)(blockIdx.x / (unsigned)nsl);
+    const Item it0 = xcd_item(blockIdx.x, H, nsl, a.order);
+    const int sl = it0.sl, bh = it0.bh;
     const int h = bh % H, row = bh / H, g = h / (H / G);
     const int64_t Tn = a.rows.len(row), tok0 = a.rows.tok0(row);
     const int nc = a.rows.nchunks(row), kb0 = a.rows.kbase(row);
@@ -1166,18 +1213,6 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
 // SAVE = true writes the residuals r, the state entering every chunk and after the last, and
 // the per-token dY . Y (Y in float32, all terms) instead of y and hT.
 // ---------------------------------------------------------------------------
-// Blocks k, k + 8, k + 16, ... run on one XCD: within a row, each XCD takes a contiguous range
-// of its (head, slice) items, so that the slices of a head and the heads of a group read their
-// tables and keys through one L2.  (Rows are not gathered: their lengths may differ.)
-struct Item {
-    int bh, sl;
-};
-__device__ __forceinline__ Item xcd_item(unsigned k, int H, int nsl) {
-    const unsigned n = (unsigned)H * nsl, row = k / n, j = k % n, x = j & 7, r = n & 7;
-    const unsigned it = x * (n >> 3) + (x < r ? x : r) + (j >> 3);
-    return Item{(int)(row * H + it / nsl), (int)(it % nsl)};
-}
-
 // what the two team walks share: the chunk addresses of one (row, head) and the lane's offsets
 template <int N, int CT>
 struct Team {
@@ -1193,7 +1228,7 @@ struct Team {
         lane = threadIdx.x & 63; w = wave_id() & 3; l16 = lane & 15; q = lane >> 4;
         H = a.H; G = a.G; P = a.P;
         const int nsl = P / (16 * CT);
-        const Item it = xcd_item(blockIdx.x, H, nsl);
+        const Item it = xcd_item(blockIdx.x, H, nsl, a.order);
         sl = it.sl; bh = it.bh;
         h = bh % H; row = bh / H; g = h / (H / G);
         Tn = a.rows.len(row); tok0 = a.rows.tok0(row); nc = a.rows.nchunks(row); kb0 = a.rows.kbase(row);
@@ -2145,7 +2180,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_grad(Args
     float* clo = chi + L;
     float* bts = clo + L;
 
-    unsigned id = blockIdx.x;
+    unsigned id = xcd_range(blockIdx.x, gridDim.x);
     const int slab = (int)(id % SLABS);
     id /= SLABS;
     const int sub = (int)(id % (unsigned)a.nsub);

@@ -36,7 +36,7 @@ int check_delta(const ssd_problem* p, bool packed) {
 // backward also the residuals, the adjoint's z, the entering states and adjoints of every
 // chunk, the last state and the partial sums.
 struct Layout {
-    size_t tab, vec, ts, kb, r, rlo, z, zlo, hin, hlo, lin, hend, dyy, dxx, tot, dAp, part, total;
+    size_t tab, vec, ts, kb, order, r, rlo, z, zlo, hin, hlo, lin, hend, dyy, dxx, tot, dAp, part, total;
     int64_t ntab, slices, nsub;
 };
 
@@ -59,6 +59,7 @@ Layout layout_of(const ssd_problem* p, bool packed, bool bwd) {
     if (packed) {
         take(o.ts, (size_t)(b + 1) * 4);
         take(o.kb, (size_t)(b + 1) * 4);
+        take(o.order, (size_t)b * 4);
     }
     if (bwd) {
         o.slices = ssd::delta::bwd_slices(p->dtype == SSD_BF16, b * H, P, N);
@@ -96,6 +97,7 @@ ssd::delta::Args args_of(const ssd_problem* p, const Layout& o, void* ws, void* 
     a.ntab = (int)o.ntab;
     a.rows.ts = packed ? reinterpret_cast<int*>(w + o.ts) : nullptr;
     a.rows.kb = packed ? reinterpret_cast<int*>(w + o.kb) : nullptr;
+    a.order = packed ? reinterpret_cast<int*>(w + o.order) : nullptr;
     a.rows.T = a.T;
     a.rows.nc = a.nc;
     a.rows.nrows = (int)p->batch;

@@ -132,7 +132,6 @@ int run_fwd(const Args& a) {
         }
         const int waves = a.P >= 64 ? 4 : a.P / 16;
         if constexpr (N <= 128) {
-            if (a.P == 128) return walk_dma<N, 2, 2, 2>(a, 4);
             // more chains than two work-groups per CU hold: three, with one K buffer
             if (bh > 512) return walk_dma<N, 1, 1, 3>(a, waves);
             return walk_dma<N, 1, 2, 2>(a, waves);
