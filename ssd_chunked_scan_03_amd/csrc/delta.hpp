@@ -957,12 +957,15 @@ __global__ __launch_bounds__(256) void k_delta(Args a, int waves) {
 // k_delta_dma: the forward walk for bfloat16 at dstate 64 and up, every tile fetched straight into
 // LDS while the chunk before computes.  Q is refilled once Q h^T is done, the tables once M u
 // is done; K, read first and last in a chunk, has two buffers (KB = 2), or one (KB = 1) where
-// a third work-group per CU covers the wait; x goes to registers a chunk ahead, and y leaves
-// from them.  LDS tiles are unpadded (the transfer writes 16
-// bytes per lane in order); a row's 16-byte pieces are exchanged by the row's low bits, so
-// that the 16 rows of a fragment lie in different banks.  Every buffer is an array of its own
+// three work-groups per CU cover the wait; x goes to registers a chunk ahead, and y leaves
+// from them.  LDS tiles are unpadded (the transfer writes 16 bytes per lane in order); a row's
+// 16-byte pieces are exchanged by the row's low bits, so that the 16 rows of a fragment lie in
+// different banks.  Every buffer is an array of its own
 // and the two K buffers are named at compile time (chunks in pairs), so the compiler knows
 // which reads a transfer in flight does not concern and does not wait for it there.
+// Bound by issue: at 8 rows of 4096 tokens, 80 heads of 64, dstate 128, one group: 0.61 ms, of
+// whose cycles matrix instructions take 47% and the splitting into terms most of the other 53%;
+// x and y alone would take 0.13 ms.
 // ---------------------------------------------------------------------------
 template <int N>
 struct Dma {
@@ -987,9 +990,9 @@ __device__ __forceinline__ void dma_run(brsrc r, char* dst, int runs, int w, int
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + m * 1024), 16, m * 1024 + lane * 16, 0, 0, 0);
 }
 
-template <int N, int CT, int KB, int OCC>
+template <int N, int KB, int OCC>
 __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
-    constexpr int NTL = N / 16, KS = N / 32, TILE = Dma<N>::TILE, SWZ = Dma<N>::SWZ;
+    constexpr int CT = 1, NTL = N / 16, KS = N / 32, TILE = Dma<N>::TILE, SWZ = Dma<N>::SWZ;
     __shared__ __attribute__((aligned(16))) bf16 K0[TILE];
     __shared__ __attribute__((aligned(16))) bf16 K1[KB == 2 ? TILE : 8];
     __shared__ __attribute__((aligned(16))) bf16 Qs[TILE];

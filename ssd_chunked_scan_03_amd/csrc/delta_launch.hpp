@@ -72,7 +72,7 @@ int walk_n(const Args& a, const Slice& s, int which) {
     return walk<T, N, 1>(a, s.waves, which);
 }
 
-// Whether the forward runs k_delta_dma (tables as fragments).
+// Whether the walks run on tables stored as fragments (k_delta_dma, k_delta_team, k_delta_adj).
 inline bool dma_walk(bool bf16_dtype, int64_t N) { return bf16_dtype && N >= 64; }
 
 // Heads of a group that one wave of the preparation takes, sharing their K K^T and Q K^T: up
@@ -89,10 +89,10 @@ void prep(const Args& a) {
     k_delta_prep<T, N, TAB><<<(unsigned)((waves + 3) / 4), 256, 0, a.stream>>>(a, heads);
 }
 
-template <int N, int CT, int KB, int OCC>
+template <int N, int KB, int OCC>
 int walk_dma(const Args& a, int waves) {
-    const unsigned grid = (unsigned)((int64_t)a.rows.nrows * a.H * (a.P / (16 * CT * waves)));
-    k_delta_dma<N, CT, KB, OCC><<<grid, 64 * waves, 0, a.stream>>>(a);
+    const unsigned grid = (unsigned)((int64_t)a.rows.nrows * a.H * (a.P / (16 * waves)));
+    k_delta_dma<N, KB, OCC><<<grid, 64 * waves, 0, a.stream>>>(a);
     return hipGetLastError() == hipSuccess ? 0 : 7;
 }
 // Column tiles per team: one, or two where that still gives every CU a team (the key and table
@@ -113,11 +113,16 @@ int walks_bwd(const Args& a) {
     k_delta_adj<N, CT, N == 256 ? 1 : 2><<<grid, 256, 0, a.stream>>>(a);
     return hipGetLastError() == hipSuccess ? 0 : 7;
 }
-// Teams while each has a CU of its own, else a wave per 16 or 32 columns.  Forward of 2048 tokens
-// at headdim 64, dstate 128 (us, team / wave): 32 heads 80 / 131, 128 heads 140 / 152, 192 heads
-// 253 / 170; dstate 256: 64 heads 121 / 200, 96 heads 217 / 213; 2.7B layer shape (640 chains)
-// 1210 / 680 for the walk alone.
-inline bool team_walk(int64_t bh, int64_t P, int64_t N) { return bh * P <= 256 * 16 * (N <= 128 && P >= 32 ? 2 : 1); }
+// Teams while each has a CU of its own, and at any number of chains where a head is too narrow for
+// a work-group of four waves to share its tables; else a wave per 16 columns.  Forward of 2048
+// tokens, whole call (us, team / wave): headdim 64, dstate 128: 32 heads 67 / 127, 128 heads
+// 121 / 153, 192 heads 213 / 172, 768 heads 657 / 493; headdim 64, dstate 256: 64 heads 114 / 201,
+// 96 heads 202 / 216, 192 heads 313 / 254; headdim 32, dstate 128: 256 heads 154 / 182, 768 heads
+// 418 / 406; headdim 32, dstate 256: 256 heads 259 / 271, 768 heads 670 / 719; headdim 16, 768
+// heads: dstate 128 342 / 347, dstate 256 440 / 800.
+inline bool team_walk(int64_t bh, int64_t P, int64_t N) {
+    return P < (N <= 128 ? 32 : 64) || bh * P <= 256 * 16 * (N <= 128 ? 2 : 1);
+}
 
 template <typename T, int N>
 int run_fwd(const Args& a) {
@@ -130,14 +135,11 @@ int run_fwd(const Args& a) {
             }
             return walk_team<N, 1, false>(a);
         }
-        const int waves = a.P >= 64 ? 4 : a.P / 16;
-        if constexpr (N <= 128) {
-            // more chains than two work-groups per CU hold: three, with one K buffer
-            if (bh > 512) return walk_dma<N, 1, 1, 3>(a, waves);
-            return walk_dma<N, 1, 2, 2>(a, waves);
-        } else {
-            return walk_dma<N, 1, 2, 1>(a, waves);
-        }
+        const int waves = a.P >= 64 ? 4 : 2;
+        // Up to dstate 128 one K buffer, and three work-groups per CU cover its wait.  2048 tokens,
+        // headdim 64, dstate 128, whole call (us, that / two buffers and two work-groups): 192 heads
+        // 165 / 173, 768 heads 480 / 495.  At dstate 256 only one fits, and two buffers with it.
+        return walk_dma<N, N <= 128 ? 1 : 2, N <= 128 ? 3 : 1>(a, waves);
     } else {
         const Slice s = slice_of(std::is_same<T, bf16>::value, (int64_t)a.rows.nrows * a.H, a.P, N);
         prep<T, N, kPlain>(a);
