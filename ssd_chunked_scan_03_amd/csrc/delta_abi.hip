@@ -17,6 +17,8 @@ constexpr int64_t kMaxThreads = 0xffffffffLL;  // threads of one launch
 
 bool grid_ok(int64_t groups, int64_t threads) { return groups <= 0x7fffffffLL && groups * threads <= kMaxThreads; }
 
+constexpr int64_t kReach = 0x7fff0000;  // bytes that a kernel addresses from one base
+
 int check_delta(const ssd_problem* p, bool packed) {
     const int st = check_problem(p);
     if (st) return st;
@@ -25,9 +27,9 @@ int check_delta(const ssd_problem* p, bool packed) {
     const int64_t nc = (T + p->chunk - 1) / p->chunk;
     const int64_t tabs = packed ? nc + b : b * nc;
     // one work-group per (chunk, head), and per (row, head, 16 columns)
-    if (!grid_ok(tabs * H, 256) || !grid_ok(b * H * (p->headdim / 16), 64)) return SSD_ERR_UNSUPPORTED;
-    // a chunk's rows lie within 2 GiB
-    if (H * p->headdim * (int64_t)esize(p->dtype) * p->chunk > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;
+    if (!grid_ok(tabs * H, 256) || !grid_ok(b * H * (p->headdim / 16), 512)) return SSD_ERR_UNSUPPORTED;
+    // a chunk's rows lie within 2 GiB (B's and C's do: check_problem bounds the groups)
+    if (H * p->headdim * (int64_t)esize(p->dtype) * p->chunk > kReach) return SSD_ERR_UNSUPPORTED;
     if (packed && T > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;  // int32 offsets
     return SSD_OK;
 }
@@ -172,6 +174,8 @@ int check_delta_bwd(const ssd_problem* p) {
     const int64_t nsub = ssd::delta::grad_shares(b * nc, H, G, N);
     if (!grid_ok(b * nc * G * nsub * (N > 64 ? N / 64 : 1), 256) || !grid_ok(2 * b * T * G * N / 4 / 256 + 1, 256))
         return SSD_ERR_UNSUPPORTED;
+    // the states of a chunk's heads lie within 2 GiB
+    if (H * p->headdim * N * (int64_t)esize(p->dtype) > kReach) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
 

@@ -233,3 +233,18 @@ def test_reference_gradients_against_differences():
         v = torch.randn(d[k].shape, generator=g, dtype=torch.float64)
         diff = (loss(dict(d, **{k: d[k] + 1e-5 * v})) - loss(dict(d, **{k: d[k] - 1e-5 * v}))) / 2e-5
         assert abs((want[n] * v).sum().item() - diff) < 1e-6 * max(1.0, abs(diff)), n
+
+
+def test_sizes_past_the_kernels_reach_are_refused():
+    """A chunk's rows of x, or (backward) the states of its heads, past 2 GiB; more threads than a
+    launch takes.  Slightly smaller problems are taken."""
+    lib = ssd._load()
+    fwd, bwd = lib.ssd_delta_workspace_bytes, lib.ssd_delta_bwd_workspace_bytes
+    size = lambda f, **kw: f(ctypes.byref(prob(b=1, T=64, **kw)))  # noqa: E731
+    over = 1 << 19
+    assert size(fwd, H=over, G=1) == 0 and size(fwd, H=over - 512, G=1) > 0
+    states = dict(P=32, N=128, G=1)
+    assert size(bwd, H=1 << 18, **states) == 0 and size(bwd, H=(1 << 18) - 64, **states) > 0
+    assert size(fwd, H=1 << 18, **states) > 0
+    assert fwd(ctypes.byref(prob(b=65535, T=1, H=64, P=128, G=1))) == 0
+    assert fwd(ctypes.byref(prob(b=16383, T=1, H=64, P=128, G=1))) > 0
