@@ -49,10 +49,11 @@ constexpr int kTri = 10;              // 16 x 16 blocks on and below the diagona
 constexpr int kTab = 2 * kTri * 256;  // floats of one (chunk, head)'s S and M tables
 constexpr int kVec = 5 * L;           // floats of its e^c, e^{c_L - c}, beta and c (log2 units, two parts)
 // Forward tables of one (chunk, head) as operand fragments (bfloat16, dstate 64 and up): -S
-// diag(beta) in three terms, then M diag(beta), [term][fragment][lane][8]; the 10 blocks on and
+// diag(beta) in three terms, then M diag(beta) in two (one would cost y as much as its own
+// rounding wherever M u cancels), [term][fragment][lane][8]; the 10 blocks on and
 // below the diagonal fill 5 fragments (frag_at), and beta is folded into their columns and
 // into the e^{c_L - c} of vec, so that the walk never reads it.
-constexpr int kFragTab = (3 + 1) * 5 * 512;  // bfloat16 elements
+constexpr int kFragTab = (3 + 2) * 5 * 512;  // bfloat16 elements
 // The backward's: -S and M, three terms each, nothing folded.
 constexpr int kFragTab2 = (3 + 3) * 5 * 512;
 // Behind either, the decay factors of the walk (float32): e^c, e^{c_L - c} (times beta where
@@ -581,7 +582,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(Args a, int heads) {
                     const float gam = exp2f_fast((sh[i] - ch[j][e]) + (sl[i] - cl[j][e]));
                     v[e] = i > j || l16 >= 4 * q + e ? qk[tri(i, j)][e] * gam : 0.f;
                 }
-                if (FRAG) frags(Mg, i, j, FOLD ? v * bt[j] : v, FOLD ? 1 : 3);
+                if (FRAG) frags(Mg, i, j, FOLD ? v * bt[j] : v, FOLD ? 2 : 3);
                 else st4(St + (kTri + tri(i, j)) * 256 + l16 * 16 + 4 * q, v);
             }
 #pragma unroll
@@ -738,7 +739,7 @@ template <typename T, int N, int CT, bool SAVE>
 __global__ __launch_bounds__(256) void k_delta(Args a, int waves) {
     typedef Cfg<T, N> CF;
     constexpr int NP = CF::NP, LDK = CF::LDK, NTL = N / 16, KS = NP / 32, NT = CF::NT;
-    constexpr int MT = SAVE ? NT : 1;  // terms of M (1: y is rounded to the problem dtype anyway)
+    constexpr int MT = SAVE || NT == 1 ? NT : 2;  // terms of M (y is rounded to the problem dtype)
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
     const int H = a.H, G = a.G, P = a.P;
@@ -887,8 +888,7 @@ __global__ __launch_bounds__(256) void k_delta(Args a, int waves) {
                 const Sp<T> mf = frag_tab<T, MT>(Mf, frag_lo(it, t), lane);
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct)
-                    yq[it][ct] = SAVE ? mma_ss<3>(yq[it][ct], mf, b2[t][ct])
-                                      : mma_es<2>(yq[it][ct], mf.t[0], b2[t][ct]);
+                    yq[it][ct] = mma_ss<SAVE ? 3 : 2>(yq[it][ct], mf, b2[t][ct]);
             }
         }
         // h' = e^{c_L} h + K^T (e^{c_L - c} u)
@@ -996,7 +996,7 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
     __shared__ __attribute__((aligned(16))) bf16 K0[TILE];
     __shared__ __attribute__((aligned(16))) bf16 K1[KB == 2 ? TILE : 8];
     __shared__ __attribute__((aligned(16))) bf16 Qs[TILE];
-    __shared__ __attribute__((aligned(16))) bf16 Sf[kFragTab];  // -S beta in three terms, then M beta
+    __shared__ __attribute__((aligned(16))) bf16 Sf[kFragTab];  // -S beta in three terms, then M beta in two
     __shared__ __attribute__((aligned(16))) float Vs[2 * L];    // e^c, beta e^{c_L - c}
     const bf16* Mf = Sf + 3 * 5 * 512;
     const int tid = threadIdx.x, nw = blockDim.x >> 6, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
@@ -1137,15 +1137,18 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) split8<2>(join(v[2 * t][ct], v[2 * t + 1][ct]), b2[t][ct]);
-            bf16x8 mf[4];
 #pragma unroll
-            for (int it = 2 * t; it < 4; ++it) mf[it] = frag_tab5(Mf, it, t, lane);
+            for (int k = 0; k < 2; ++k) {  // term of M
+                bf16x8 mf[4];
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+                for (int it = 2 * t; it < 4; ++it) mf[it] = frag_tab5(Mf + k * 5 * 512, it, t, lane);
 #pragma unroll
-                for (int it = 2 * t; it < 4; ++it)
+                for (int m = 0; m < 2 - k; ++m)
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) yq[it][ct] = mma(yq[it][ct], mf[it], b2[t][ct].t[k]);
+                    for (int it = 2 * t; it < 4; ++it)
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) yq[it][ct] = mma(yq[it][ct], mf[it], b2[t][ct].t[m]);
+            }
         }
         // e^{c_L - c} u as operands
 #pragma unroll
@@ -1426,13 +1429,12 @@ template <int N, int CT, int KB, bool SAVE>
 __global__ __launch_bounds__(512) void k_delta_team(Args a) {
     typedef Team<N, CT> TM;
     constexpr int KS = N / 32, TILE = Dma<N>::TILE, OT = TM::OT, OP = TM::OP;
-    constexpr int QT = SAVE ? 3 : 2, MT = SAVE ? 3 : 1, UT = SAVE ? 3 : 2;  // terms of h, M and u in Y
+    constexpr int QT = SAVE ? 3 : 2, MT = QT, UT = QT;  // terms of h, M and u in Y
     constexpr int RUNS = (SAVE ? kFragTab2 : kFragTab) / 512 + 1;
     __shared__ __attribute__((aligned(16))) bf16 K0[TILE];
     __shared__ __attribute__((aligned(16))) bf16 K1[KB == 2 ? TILE : 8];
     __shared__ __attribute__((aligned(16))) bf16 Qs[TILE];
     __shared__ __attribute__((aligned(16))) bf16 Sf[RUNS * 512];
-    __shared__ __attribute__((aligned(16))) bf16 Xs[CT * 1024];
     __shared__ __attribute__((aligned(16))) bf16 Ys[SAVE ? CT * 1024 : 8];
     // passed between the waves: partial sums, then (once they are read) the weighted u and u;
     // the state's operands for Q h^T; R
@@ -1447,7 +1449,6 @@ __global__ __launch_bounds__(512) void k_delta_team(Args a) {
     if (nc > 0 && wave_id() >= 4) {
         auto bring = [&](int c) {
             tm.template fetch_tab<RUNS>(c, Sf);
-            tm.fetch_x(a.x, c, Xs);
             if (SAVE) tm.fetch_x(a.dy, c, Ys);
         };
         tm.fetch_tile(a.B, 0, K0);
@@ -1499,7 +1500,7 @@ __global__ __launch_bounds__(512) void k_delta_team(Args a) {
             for (int ct = 0; ct < CT; ++ct)
                 if (SAVE) dy[ct] = floats(tm.x_tile(Ys, w, ct));
             qh(0, KS - KS / 4);
-            wave_meet(false);  // the partial sums are in place, the tables, X and dY in registers
+            wave_meet(false);  // the partial sums are in place, the tables and dY in registers
             if (more) bring(c + 1);
             qh(KS - KS / 4, KS);
             wave_meet(false);  // R is in place, K^T in registers, Q is free
@@ -1533,6 +1534,8 @@ __global__ __launch_bounds__(512) void k_delta_team(Args a) {
         Sp<bf16> sp[OP][CT];
         tm.split(acc, sp);
         if (nc > 0) tm.template put_state<QT>(Hf, sp);
+        u32x2v xr[CT];  // x of the chunk's token tile w, as loaded
+        if (nc > 0) load_tile<CT>(tm.x_rsrc(a.x, 0), xr, tm.xo, w, tm.rsx);
         auto chunk = [&](int c, const bf16* Ks) {
             wave_meet(false);  // the chunk's tiles have landed
             tm.part_sums(Ks, sp, Pf);
@@ -1562,7 +1565,9 @@ __global__ __launch_bounds__(512) void k_delta_team(Args a) {
             const float el = Vs[L - 1];
             f32x4 v[CT], rb[CT], uw[CT];
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) v[ct] = floats(tm.x_tile(Xs, w, ct));
+            for (int ct = 0; ct < CT; ++ct) v[ct] = floats(quad_t(xr[ct], tm.sel, tm.upper));
+            // (no branch: the loads in flight can then be counted)
+            load_tile<CT>(tm.x_rsrc(a.x, min(c + 1, nc - 1)), xr, tm.xo, w, tm.rsx);
             bf16x8 sf[2][3];
             tm.template table_row<3>(Sf, sf);
             wave_meet(false);  // the partial sums are in place

@@ -49,7 +49,7 @@ int walk(const Args& a, int waves, int which) {
     const int sw = 16 * CT * waves;
     const unsigned grid = (unsigned)((int64_t)a.rows.nrows * a.H * (a.P / sw));
     if (which == 0) {
-        const size_t lds = CF::walk_bytes(sw, 1, 1);
+        const size_t lds = CF::walk_bytes(sw, CF::NT > 1 ? 2 : 1, 1);
         if (!lds_limit(k_delta<T, N, CT, false>, lds)) return 7;
         k_delta<T, N, CT, false><<<grid, 256, lds, a.stream>>>(a, waves);
     } else if (which == 1) {
@@ -136,10 +136,8 @@ int run_fwd(const Args& a) {
             return walk_team<N, 1, false>(a);
         }
         const int waves = a.P >= 64 ? 4 : 2;
-        // Up to dstate 128 one K buffer, and three work-groups per CU cover its wait.  2048 tokens,
-        // headdim 64, dstate 128, whole call (us, that / two buffers and two work-groups): 192 heads
-        // 165 / 173, 768 heads 480 / 495.  At dstate 256 only one fits, and two buffers with it.
-        return walk_dma<N, N <= 128 ? 1 : 2, N <= 128 ? 3 : 1>(a, waves);
+        // As many work-groups per CU as LDS takes, three with one K buffer, two or one with two.
+        return walk_dma<N, N <= 64 ? 1 : 2, N <= 64 ? 3 : N <= 128 ? 2 : 1>(a, waves);
     } else {
         const Slice s = slice_of(std::is_same<T, bf16>::value, (int64_t)a.rows.nrows * a.H, a.P, N);
         prep<T, N, kPlain>(a);

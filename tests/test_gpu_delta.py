@@ -123,6 +123,24 @@ def test_forward_edges(kw, dtype):
     check_forward(d, dtype, (kw, dtype), terms)
 
 
+@pytest.mark.parametrize("case", [(2, 130, 4, 64, 128, 2), (1, 130, 160, 64, 128, 8), (1, 130, 2, 64, 256, 1),
+                                  (1, 130, 80, 64, 256, 1), (1, 130, 2, 32, 32, 1), (1, 130, 160, 64, 64, 8)],
+                         ids=lambda c: "b{}T{}H{}P{}N{}G{}".format(*c))
+@pytest.mark.parametrize("key", ["unit", "same"])
+def test_y_is_good_to_its_own_rounding(case, key):
+    """The bfloat16 y against the exact one: its own rounding's mean square, and beside it only what
+    products in two terms leave, 3 2^-17 of each term.  Those roundings are independent and each y
+    has N terms a state column and more, so their squares add to (3 2^-17 w)^2 / N at most in the
+    mean, w the sum of absolute terms."""
+    b, T, H, P, N, G = case
+    d = ref.make(b, T, H, P, N, G, 31, "bf16", key=key, dt_hi=0.02)
+    y, _ = forward(d)
+    yr, _, w = ref.walk(d, weights=True)
+    own = (yr.to(torch.bfloat16).double() - yr).square().sum()
+    rest = (3 * 2.0 ** -17 * w).square().sum() / N
+    assert (y.double().cpu() - yr).square().sum() < 1.02 * (own + rest), (case, key)
+
+
 def test_strong_gates_keep_the_ratio_of_neighbours():
     """One token with a decay of e^-3000 in the middle of a chunk of weak ones: the decay sums
     behind it are thousands, their differences 1e-3."""
