@@ -343,13 +343,14 @@ int ssd_diag_scan_bwd(const ssd_problem* p, const void* x, const float* dt, cons
  *   beta                        [batch, seqlen, nheads], problem dtype (aligned to one element)
  *
  * Evaluated in chunks of 64 tokens: `chunk` must be 64 and `flags` 0.  headdim, dstate, dtype,
- * ngroups and grid limits as for ssd_scan_fwd; also under 2^24 (chunk, head) pairs,
- * (batch, head, 16 headdim columns) under 2^26 and 64 tokens' x under 2 GiB, else
- * SSD_ERR_UNSUPPORTED.
+ * ngroups and grid limits as for ssd_scan_fwd; also under 2^24 (chunk, head) pairs, at most
+ * 2^23 - 1 (batch, head, 16 headdim columns), 64 tokens' x under 2 GiB and, for the backward, one chunk's
+ * states of all heads in the problem dtype under 2 GiB, else SSD_ERR_UNSUPPORTED.
  * Precision: decay sums are float64; the state, residuals and all accumulation float32, and
  * where they enter the bfloat16 matrix cores they do so as a sum of bfloat16 terms that
  * keeps the float32 mantissa, so the float32 outputs (hT, and ddt, dA, dh0 of the
- * backward) are float32-accurate in bfloat16 problems too; y is rounded once.  A NaN or
+ * backward) are float32-accurate in bfloat16 problems too; a bfloat16 y comes from two terms, whose
+ * rounding stays far below its own.  A NaN or
  * infinity in an input reaches every output of its head from the start of its chunk on.
  * `ws` must hold ssd_delta_workspace_bytes(p) bytes (0 for an invalid or empty problem).
  * Ownership, ordering, capture, aliasing and errors as for ssd_scan_fwd. */

@@ -445,7 +445,10 @@ __device__ __forceinline__ void order_rows(const Rows& rows, int* order, int lan
 // four digits where keys repeat.)  Decay sums are float64 and kept in two float32 parts, so
 // a strongly decayed chunk keeps the exact ratio of neighbouring tokens.
 // TAB: float32 blocks, or the operand fragments that the forward's or the backward's
-// k_delta_dma walks read.
+// fragment walks read.
+// Bound by the tables' way to memory: 26 KB per (chunk, head) forward (bfloat16, dstate 64 and
+// up), 31 KB backward; 40960 of them (8 rows of 4096 tokens, 80 heads) in 284 us, 3.8 TB/s.
+// Small problems wait for the substitution's chain instead (16 us).
 // ---------------------------------------------------------------------------
 struct PrepLds {
     float chi[L], clo[L], bet[L];
@@ -963,9 +966,9 @@ __global__ __launch_bounds__(256) void k_delta(Args a, int waves) {
 // different banks.  Every buffer is an array of its own
 // and the two K buffers are named at compile time (chunks in pairs), so the compiler knows
 // which reads a transfer in flight does not concern and does not wait for it there.
-// Bound by issue: at 8 rows of 4096 tokens, 80 heads of 64, dstate 128, one group: 0.61 ms, of
-// whose cycles matrix instructions take 47% and the splitting into terms most of the other 53%;
-// x and y alone would take 0.13 ms.
+// Bound by issue and the tables: 8 rows of 4096 tokens, 80 heads of 64, dstate 128, one group, take
+// 0.66 to 0.75 ms (the clock gives way); matrix instructions are half of the issued cycles, the
+// splitting into terms most of the rest; x and y alone would take 0.13 ms, with the tables 0.34.
 // ---------------------------------------------------------------------------
 template <int N>
 struct Dma {
@@ -1216,6 +1219,11 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
 // next chunk waits for: K h^T in partial sums (their own state is the operand, straight from the
 // accumulators), R, r and the state's update.  The other four, one beside each on its SIMD, do
 // the rest meanwhile: every transfer into LDS, Q h^T, Y and its store.  Four exchanges per chunk.
+// Bound by a chunk's latency: one row of 65536 tokens, 32 heads of 64, dstate 256 (128 teams), 2.4 ms,
+// 2.3 us a chunk; without its transfers 1.9.  LDS moves 390 KB a chunk, 1.3 us at 128 bytes a
+// cycle.  (Four waves doing all of it in turn: 2.8 ms.  Keys and tables straight to the
+// registers of the one wave that reads them: 3.1 ms, their scattered rows choke the
+// address unit.  Lines touched two chunks ahead: 2.7 ms, of the same cause.)
 // SAVE = true writes the residuals r, the state entering every chunk and after the last, and
 // the per-token dY . Y (Y in float32, all terms) instead of y and hT.
 // ---------------------------------------------------------------------------
@@ -1643,7 +1651,8 @@ __global__ __launch_bounds__(512) void k_delta_team(Args a) {
 // ---------------------------------------------------------------------------
 // k_delta_adj: the adjoint walk by the same teams (chunks in reverse, dh^T in accumulators); the
 // tables' transposes are read from the same fragments by transposing loads.  Outputs as
-// k_delta_rev.
+// k_delta_rev.  Four waves, which share every product.  Bound by a chunk's latency: 2 rows of 2048
+// tokens, 48 heads of 64, dstate 128, in 178 us, 5.5 us a chunk (the first walk: 130 us).
 // ---------------------------------------------------------------------------
 template <int N, int CT, int KB>
 __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
@@ -2148,7 +2157,9 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a, int waves) {
 // of the group's heads in registers (and dbeta, by the first slab).  Wave w owns token tile
 // w as the COLUMNS of dQ^T[n][i] and dK^T[n][i], so the 64 x 64 gradient tables it needs,
 // dP^T and the two sides of W, come out of the matrix cores in the layout their products
-// read.  Everything here ends in the problem dtype: the states enter with one bfloat16
+// read.  Rows pass through LDS 32 headdim columns at a time, asked for a step ahead.  2 rows of
+// 2048 tokens, 48 heads of 64, dstate 128, one group: 107 us for 0.33 GB (0.07 ms at copy rate;
+// every wave fetching its own fragments took 171).  Everything here ends in the problem dtype: the states enter with one bfloat16
 // term, r, z and the tables with two, so that every product has one rounded factor at most.
 // ---------------------------------------------------------------------------
 template <typename T>
@@ -2451,6 +2462,8 @@ __global__ __launch_bounds__(BLOCK) void k_delta_dA(const float* __restrict__ p,
 // k_delta_step: the recurrence token by token on a held state, in place, all in float32.
 // One thread owns 8 consecutive elements of a state row p; the N / 8 lanes of a row (one
 // wave) reduce h B and then h C.  The state is read and written once per call: bound by HBM.
+// 64 rows, 80 heads of 64, dstate 128: 66 us for 0.34 GB, 5.1 TB/s, what a copy reaches.  One row of 32
+// heads of 128: 4 us, behind 10 us of the host's.
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ __launch_bounds__(256) void k_delta_step(const T* __restrict__ x, const float* __restrict__ dt,

@@ -96,7 +96,7 @@ int walk_dma(const Args& a, int waves) {
     return hipGetLastError() == hipSuccess ? 0 : 7;
 }
 // Column tiles per team: one, or two where that still gives every CU a team (the key and table
-// fragments are then read once for both; at dstate 256 the state's operands leave no room).
+// fragments are then read once for both; at dstate 256 LDS leaves no room).
 inline int team_tiles(int64_t bh, int64_t P, int64_t N) { return N <= 128 && P >= 32 && bh * P > 256 * 16 ? 2 : 1; }
 template <int N, int CT, bool SAVE>
 int walk_team(const Args& a) {
@@ -115,11 +115,11 @@ int walks_bwd(const Args& a) {
 }
 // Teams while each has a CU of its own, and at any number of chains where a head is too narrow for
 // a work-group of four waves to share its tables; else a wave per 16 columns.  Forward of 2048
-// tokens, whole call (us, team / wave): headdim 64, dstate 128: 32 heads 67 / 127, 128 heads
-// 121 / 153, 192 heads 213 / 172, 768 heads 657 / 493; headdim 64, dstate 256: 64 heads 114 / 201,
-// 96 heads 202 / 216, 192 heads 313 / 254; headdim 32, dstate 128: 256 heads 154 / 182, 768 heads
-// 418 / 406; headdim 32, dstate 256: 256 heads 259 / 271, 768 heads 670 / 719; headdim 16, 768
-// heads: dstate 128 342 / 347, dstate 256 440 / 800.
+// tokens, whole call (us, team / wave; M then in one term): headdim 64, dstate 128: 32 heads
+// 67 / 127, 128 heads 121 / 153, 192 heads 213 / 172, 768 heads 657 / 493; headdim 64, dstate 256:
+// 64 heads 114 / 201, 96 heads 202 / 216, 192 heads 313 / 254; headdim 32, dstate 128: 256 heads
+// 154 / 182, 768 heads 418 / 406; headdim 32, dstate 256: 256 heads 259 / 271, 768 heads 670 / 719;
+// headdim 16, 768 heads: dstate 128 342 / 347, dstate 256 440 / 800.
 inline bool team_walk(int64_t bh, int64_t P, int64_t N) {
     return P < (N <= 128 ? 32 : 64) || bh * P <= 256 * 16 * (N <= 128 ? 2 : 1);
 }
@@ -136,7 +136,9 @@ int run_fwd(const Args& a) {
             return walk_team<N, 1, false>(a);
         }
         const int waves = a.P >= 64 ? 4 : 2;
-        // As many work-groups per CU as LDS takes, three with one K buffer, two or one with two.
+        // As many work-groups per CU as LDS takes: three with one K buffer to dstate 64; two, with
+        // two K buffers, at 128 (three, with the second term of M from memory: 24 ragged prompts 278
+        // us against 260, the 2.7B layer shape 879 against 885); one at 256.
         return walk_dma<N, N <= 64 ? 1 : 2, N <= 64 ? 3 : N <= 128 ? 2 : 1>(a, waves);
     } else {
         const Slice s = slice_of(std::is_same<T, bf16>::value, (int64_t)a.rows.nrows * a.H, a.P, N);
