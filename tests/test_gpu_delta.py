@@ -174,6 +174,8 @@ def test_empty_sequence_and_batch():
     ([0, 1, 63, 0, 64, 65, 130, 0], (4, 64, 128, 1), "bf16"),
     ([3, 200, 1, 1, 1, 77], (2, 32, 32, 2), "f32"),
     ([0, 0, 0], (2, 16, 16, 1), "bf16"),
+    ([0, 1, 63, 0, 64, 65, 130, 0], (40, 128, 128, 4), "bf16"),  # a wave per 16 columns
+    ([70, 0, 129], (40, 64, 256, 2), "bf16"),
 ])
 def test_packed_sequences(lengths, shape, dtype):
     """Each sequence is its own walk; tokens outside every sequence keep y as it was, and
@@ -203,6 +205,29 @@ def test_packed_sequences(lengths, shape, dtype):
         yr, hr, w = ref.walk(dict(one, A=d["A"], h0=h0[s:s + 1]), weights=True)
         check_y(y[lo:lo + n][None], yr, w, dtype, (lengths, s))
         assert ref.rel(hT[s:s + 1], hr) < F32, (lengths, s)
+
+
+@pytest.mark.parametrize("rows", [200, 1100])
+def test_many_packed_sequences(rows):
+    """More rows than one wave's lanes, put in order by length, and more than are put in order: each
+    against the dense call on its own tokens."""
+    g = torch.Generator().manual_seed(41)
+    lens = torch.randint(0, 40, (rows,), generator=g)
+    lens[rows // 2], lens[rows - 1] = 700, 130
+    cu = torch.cat([torch.zeros(1, dtype=torch.long), lens.cumsum(0)])
+    T = int(cu[-1])
+    d = up(ref.make(1, T, 2, 32, 64, 1, 42, "bf16"))
+    h0 = 0.1 * torch.randn(rows, 2, 32, 64, generator=g).cuda()
+    t = {k: d[k][0].contiguous() for k in ("x", "dt", "B", "C", "beta")}
+    y, hT = ssd.delta_fwd_varlen(t["x"], t["dt"], d["A"], t["B"], t["C"], t["beta"], cu.int().cuda(), h0)
+    for r in [0, 1, 63, 64, rows // 2, rows - 2, rows - 1]:
+        lo, hi = int(cu[r]), int(cu[r + 1])
+        cut = {k: d[k][:, lo:hi].contiguous() for k in t}
+        y1, h1 = ssd.delta_fwd(cut["x"], cut["dt"], d["A"], cut["B"], cut["C"], cut["beta"], h0[r:r + 1])
+        # (the few rows of the dense call may run in teams: sums in another order, y a rounding apart)
+        assert ref.rel(hT[r:r + 1], h1.cpu().double()) < F32, r
+        if hi > lo:
+            assert ref.rel(y[None, lo:hi], y1.cpu().double()) < B16, r
 
 
 def test_packed_offsets_outside_the_axis_stay_in_bounds():
