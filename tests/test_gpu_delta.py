@@ -419,6 +419,31 @@ def test_graph_replays_match_eager():
         torch.cuda.synchronize()
 
 
+def test_packed_graph_follows_new_offsets():
+    """A captured packed call reads its offsets when it is replayed: other lengths in the same tensor
+    give what the eager call gives on them."""
+    d = up(ref.make(1, 400, 40, 128, 128, 4, 25, "bf16"))
+    t = [d[k][0].contiguous() for k in ("x", "dt")] + [d["A"]] + [d[k][0].contiguous() for k in ("B", "C", "beta")]
+    offsets = [[0, 10, 300, 300, 400], [0, 200, 210, 390, 400], [0, 0, 0, 0, 400]]
+    cu = torch.tensor(offsets[0], dtype=torch.int32, device="cuda")
+    out = {}
+
+    def run():
+        out["y"], out["hT"] = ssd.delta_fwd_varlen(*t, cu)
+
+    run()
+    torch.cuda.synchronize()
+    graph = _capture(run)
+    for r in range(4):
+        cu.copy_(torch.tensor(offsets[r % 3], dtype=torch.int32))
+        want = ssd.delta_fwd_varlen(*t, cu)
+        for v in out.values():
+            v.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out["y"], want[0]) and torch.equal(out["hT"], want[1]), r
+
+
 def test_on_a_side_stream():
     d = up(ref.make(2, 150, 4, 64, 64, 2, 24, "bf16"))
     args = [d[k] for k in ("x", "dt", "A", "B", "C", "beta", "h0")]
