@@ -556,23 +556,29 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(Args a, int heads) {
             sh[i] = m.chi[i * 16 + l16];
             sl[i] = m.clo[i * 16 + l16];
         }
-        // a block's elements (this lane: row l16, columns 4q + e) in `terms` terms
-        auto frags = [&](T* dst, int i, int j, f32x4 v, int terms) {
+        // fragment f of a table from its two blocks' elements (this lane: row l16, columns 4q + e), in
+        // TERMS terms: whole 16-byte pieces, since half-written lines cost the tables' way to memory
+        // twice.  `first` and `prev` hold a block for its partner (frag_at).
+        f32x4 first = f32x4{0.f, 0.f, 0.f, 0.f}, prev = first;
+        auto frags = [&](T* dst, int f, f32x4 lo, f32x4 hi, auto terms) {
+            Sp<T> sp;
+            if constexpr (FRAG) {
+                split8<decltype(terms)::value>(join(lo, hi), sp);
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                if (k >= terms) break;
-                typename V4<T>::type o;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    o[e] = from_f<T>(v[e]);
-                    v[e] -= to_f(o[e]);
-                }
-                st4(dst + k * 5 * 512 + frag_at(i, j) + lane * 8, o);
+                for (int k = 0; k < decltype(terms)::value; ++k) st8(dst + (k * 5 + f) * 512 + lane * 8, sp.t[k]);
             }
         };
-        auto put = [&](int i, int j, f32x4 v) {  // S_ij
-            if (FRAG) frags(Sg, i, j, FOLD ? v * -bt[j] : -v, 3);
-            else st4(St + tri(i, j) * 256 + l16 * 16 + 4 * q, v);
+        auto put = [&](int i, int j, f32x4 v) {  // S_ij, j downward
+            if (FRAG) {
+                v = FOLD ? v * -bt[j] : -v;
+                const std::integral_constant<int, 3> three;
+                if (i == 0) first = v;
+                else if (i == 2 && j == 2) frags(Sg, 0, first, v, three);
+                else if (j & 1) prev = v;
+                else frags(Sg, i < 3 ? i : 3 + (j >> 1), v, prev, three);
+            } else {
+                st4(St + tri(i, j) * 256 + l16 * 16 + 4 * q, v);
+            }
         };
         // M, and the diagonal blocks of KK
 #pragma unroll
@@ -585,8 +591,16 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(Args a, int heads) {
                     const float gam = exp2f_fast((sh[i] - ch[j][e]) + (sl[i] - cl[j][e]));
                     v[e] = i > j || l16 >= 4 * q + e ? qk[tri(i, j)][e] * gam : 0.f;
                 }
-                if (FRAG) frags(Mg, i, j, FOLD ? v * bt[j] : v, FOLD ? 2 : 3);
-                else st4(St + (kTri + tri(i, j)) * 256 + l16 * 16 + 4 * q, v);
+                if (FRAG) {
+                    if (FOLD) v *= bt[j];
+                    const std::integral_constant<int, FOLD ? 2 : 3> terms;
+                    if (i == 0) first = v;
+                    else if (i == 2 && j == 2) frags(Mg, 0, first, v, terms);
+                    else if (!(j & 1)) prev = v;
+                    else frags(Mg, i < 3 ? i : 3 + (j >> 1), prev, v, terms);
+                } else {
+                    st4(St + (kTri + tri(i, j)) * 256 + l16 * 16 + 4 * q, v);
+                }
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
