@@ -447,7 +447,7 @@ __device__ __forceinline__ void order_rows(const Rows& rows, int* order, int lan
 // TAB: float32 blocks, or the operand fragments that the forward's or the backward's
 // fragment walks read.
 // Bound by the tables' way to memory: 26 KB per (chunk, head) forward (bfloat16, dstate 64 and
-// up), 31 KB backward; 40960 of them (8 rows of 4096 tokens, 80 heads) in 284 us, 3.8 TB/s.
+// up), 31 KB backward; 40960 of them (8 rows of 4096 tokens, 80 heads) in 264 us, 4.1 TB/s.
 // Small problems wait for the substitution's chain instead (16 us).
 // ---------------------------------------------------------------------------
 struct PrepLds {
@@ -557,15 +557,17 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(Args a, int heads) {
             sl[i] = m.clo[i * 16 + l16];
         }
         // fragment f of a table from its two blocks' elements (this lane: row l16, columns 4q + e), in
-        // TERMS terms: whole 16-byte pieces, since half-written lines cost the tables' way to memory
-        // twice.  `first` and `prev` hold a block for its partner (frag_at).
+        // TERMS terms: whole 16-byte pieces (halves apart cost 1% of the layer forward).  `first`
+        // and `prev` hold a block for its partner (frag_at).
         f32x4 first = f32x4{0.f, 0.f, 0.f, 0.f}, prev = first;
         auto frags = [&](T* dst, int f, f32x4 lo, f32x4 hi, auto terms) {
             Sp<T> sp;
             if constexpr (FRAG) {
                 split8<decltype(terms)::value>(join(lo, hi), sp);
 #pragma unroll
-                for (int k = 0; k < decltype(terms)::value; ++k) st8(dst + (k * 5 + f) * 512 + lane * 8, sp.t[k]);
+                for (int k = 0; k < decltype(terms)::value; ++k)  // (past the caches: 2% of the layer forward)
+                    __builtin_nontemporal_store(__builtin_bit_cast(u32x4v, sp.t[k]),
+                                                reinterpret_cast<u32x4v*>(dst + (k * 5 + f) * 512 + lane * 8));
             }
         };
         auto put = [&](int i, int j, f32x4 v) {  // S_ij, j downward
