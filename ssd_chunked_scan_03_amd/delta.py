@@ -57,23 +57,25 @@ def _raw_stream(index):
     return f(index) if f is not None else torch.cuda.current_stream(index).cuda_stream
 
 
-def _call(name, head, tensors, ws=False, stream=None):
+def _call(name, head, tensors, ws=False, stream=None, index=None):
     """Enqueue one entry point on `stream` (default: the current stream of the tensors' device,
-    which the call makes the current device meanwhile).  The first of `tensors` names the
-    device; `ws` is the workspace (False: the entry point takes none)."""
+    which the call makes the current device meanwhile).  All of `tensors` and the workspace `ws`
+    (False: the entry point takes none) lie on that one GPU, `index` where the caller has checked
+    them: a kernel would read a host address."""
     import torch
     fn = _calls.get(name)
     if fn is None:
         fn = _calls[name] = getattr(_load(), name)
-    for t in tensors:
-        if t is not None:
-            index = t.get_device()
-            break
+    if index is None:
+        on = {t.get_device() for t in (*tensors, None if ws is False else ws) if t is not None}
+        index = on.pop() if len(on) == 1 else -1
+        if index < 0:
+            raise ValueError(f"{name} needs GPU tensors, all on one device")
     args = [None if t is None else t.data_ptr() for t in tensors]
     if ws is not False:
         args += (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
-    if index < 0 or index == torch.cuda.current_device():
-        st = fn(head, *args, (_raw_stream(index) if index >= 0 else 0) if stream is None else int(stream))
+    if index == torch.cuda.current_device():
+        st = fn(head, *args, _raw_stream(index) if stream is None else int(stream))
     else:
         with torch.cuda.device(index):
             st = fn(head, *args, _raw_stream(index) if stream is None else int(stream))
@@ -182,7 +184,8 @@ def delta_fwd(x, dt, A, B, C, beta, h0=None, chunk=DELTA_CHUNK, return_final_sta
     prob, need = _plan("fwd", b, T, H, P, N, G, chunk, code)
     y = torch.empty_like(x)
     hT = torch.empty((b, H, P, N), dtype=f32, device=x.device) if return_final_state else None
-    delta_fwd_into(prob, x, dt, A, B, C, beta, h0, y, hT, _workspace(workspace, need, x.device))
+    _call("ssd_delta_fwd", prob, (x, dt, A, B, C, beta, h0, y, hT), _workspace(workspace, need, x.device),
+          index=x.get_device())
     return y, hT
 
 
@@ -213,7 +216,8 @@ def delta_fwd_varlen(x, dt, A, B, C, beta, cu_seqlens, h0=None, chunk=DELTA_CHUN
     prob, need = _plan("varlen", nseq, T, H, P, N, G, chunk, code)
     y = torch.empty_like(x)
     hT = torch.empty((nseq, H, P, N), dtype=f32, device=x.device) if return_final_state else None
-    delta_fwd_varlen_into(prob, cu_seqlens, x, dt, A, B, C, beta, h0, y, hT, _workspace(workspace, need, x.device))
+    _call("ssd_delta_fwd_varlen", prob, (cu_seqlens, x, dt, A, B, C, beta, h0, y, hT),
+          _workspace(workspace, need, x.device), index=x.get_device())
     return y, hT
 
 
@@ -231,7 +235,7 @@ def delta_step(x, dt, A, B, C, beta, h, norm=None):
                       ("h", h, (b, H, P, N), f32)))
     prob, _ = _plan("step", b, T, H, P, N, G, DELTA_CHUNK, code)
     y = torch.empty_like(x)
-    delta_step_into(prob, x, dt, A, B, C, beta, h, y)
+    _call("ssd_delta_step", prob, (x, dt, A, B, C, beta, h, y), index=x.get_device())
     return y
 
 
@@ -252,8 +256,8 @@ def delta_bwd(x, dt, A, B, C, beta, dy, h0=None, dhT=None, chunk=DELTA_CHUNK, wo
     e = torch.empty_like
     out = dict(dx=e(x), ddt=e(dt), dA=e(A), dB=e(B), dC=e(C), dbeta=e(beta),
                dh0=torch.empty((b, H, P, N), dtype=f32, device=x.device))
-    delta_bwd_into(prob, x, dt, A, B, C, beta, h0, dy, dhT, out["dx"], out["ddt"], out["dA"], out["dB"], out["dC"],
-                   out["dbeta"], out["dh0"], _workspace(workspace, need, x.device))
+    _call("ssd_delta_bwd", prob, (x, dt, A, B, C, beta, h0, dy, dhT, *out.values()),
+          _workspace(workspace, need, x.device), index=x.get_device())
     if norm is not None:
         out.update(bc_norm_bwd(B0, C0, out["dB"], out["dC"], **norm))
     return out
@@ -339,7 +343,7 @@ def bc_norm(B, C, wB=None, wC=None, mode="rms", eps=1e-6, inv_freq=None, positio
     prob, _ = _norm_problem(B, C, wB, wC, mode, eps, inv_freq, positions, interleaved)
     whole = torch.contiguous_format
     Bn, Cn = torch.empty_like(B, memory_format=whole), torch.empty_like(C, memory_format=whole)
-    bc_norm_into(prob, B, C, wB, wC, inv_freq, positions, Bn, Cn)
+    _call("ssd_bc_norm", prob, (B, C, wB, wC, inv_freq, positions, Bn, Cn), index=B.get_device())
     return Bn, Cn
 
 
@@ -369,6 +373,6 @@ def bc_norm_bwd(B, C, dBn, dCn, wB=None, wC=None, mode="rms", eps=1e-6, inv_freq
     ws = None
     if wB is not None or wC is not None:
         ws = _workspace(workspace, need, B.device)
-    bc_norm_bwd_into(prob, B, C, wB, wC, inv_freq, positions, dBn, dCn, out["dB"], out["dC"], out.get("dwB"),
-                     out.get("dwC"), ws)
+    _call("ssd_bc_norm_bwd", prob, (B, C, wB, wC, inv_freq, positions, dBn, dCn, out["dB"], out["dC"], out.get("dwB"),
+                                    out.get("dwC")), ws, index=B.get_device())
     return out
