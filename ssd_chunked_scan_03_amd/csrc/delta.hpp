@@ -2371,7 +2371,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_grad(Args
                 for (int r = 0; r < 4; ++r) {
                     const int o = j * 16 + 4 * q + r;  // the other token
                     const float d = (ci - co[r]) + (di - lo[r]);
-                    const float e = exp2f_fast(fminf(o <= i ? d : -d, 0.f));
+                    const float e = exp2f_fast(o <= i ? d : -d);  // (above 1 where dt A > 0)
                     const bool up = j == w && o >= i;
                     pl[u][r] = o <= i ? pa[j][r] * (e * bo[r]) : 0.f;
                     pu[u][r] = o >= i ? (up ? pd[r] : pa[j][r]) * (e * bi) : 0.f;
