@@ -96,9 +96,7 @@ int scan(const ssd_problem* p, int diag, const void* x, const float* dt, const f
         if (!hT) return SSD_OK;
         if (overlap({hT, state_bytes}, {h0, state_bytes})) return SSD_ERR_ALIAS;
         if (check_only) return SSD_OK;
-        const int64_t n = b * H * P * N;
-        k_copy_state<<<(unsigned)((n + 255) / 256), 256, 0, (hipStream_t)stream>>>(h0, hT, n);
-        return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+        return copy_state(h0, hT, b * H * P * N, stream);
     }
     if (!x || !dt || !B || !C || !y) return SSD_ERR_NULL;
     if (!aligned(x, 16) || !aligned(B, 16) || !aligned(C, 16) || !aligned(y, 16) || !aligned(dt, 4))
@@ -248,9 +246,7 @@ int scan_varlen(const ssd_problem* p, const int* cu, const void* x, const float*
         // every sequence is empty: hT = h0 (or 0)
         if (!hT) return SSD_OK;
         if (overlap({hT, state_bytes}, {h0, state_bytes})) return SSD_ERR_ALIAS;
-        const int64_t n = nseq * H * P * N;
-        k_copy_state<<<(unsigned)((n + 255) / 256), 256, 0, (hipStream_t)stream>>>(h0, hT, n);
-        return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+        return copy_state(h0, hT, nseq * H * P * N, stream);
     }
     if (!cu || !x || !dt || !B || !C || !y) return SSD_ERR_NULL;
     if (!aligned(cu, 4) || !aligned(x, 16) || !aligned(B, 16) || !aligned(C, 16) || !aligned(y, 16) ||
@@ -452,10 +448,7 @@ int scan_bwd(const ssd_problem* p, int diag, const void* x, const float* dt, con
         }
         k_zero<<<(unsigned)((a_bytes / 4 + 255) / 256), 256, 0, s>>>(dA, (int64_t)(a_bytes / 4));
         if (dD) k_zero<<<(unsigned)((H + 255) / 256), 256, 0, s>>>(dD, H);
-        if (dh0 && b > 0) {
-            const int64_t n = b * H * P * N;
-            k_copy_state<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(dhT, dh0, n);
-        }
+        if (dh0 && b > 0) return copy_state(dhT, dh0, b * H * P * N, stream);
         return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
     }
     if (!x || !dt || !B || !C || !dy || !dx || !ddt || !dB || !dC) return SSD_ERR_NULL;

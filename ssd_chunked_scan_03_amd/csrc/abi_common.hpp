@@ -13,8 +13,15 @@ namespace {
 // hT = h0 (or 0) for an empty sequence: a fill kernel, not a memset, so that the
 // call stays safe under stream capture.
 __global__ void k_copy_state(const float* __restrict__ h0, float* __restrict__ hT, int64_t n) {
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i < n) hT[i] = h0 ? h0[i] : 0.f;
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) hT[i] = h0 ? h0[i] : 0.f;
+}
+// (The states may hold more elements than the 2^32 - 1 threads of a launch, past which a launch
+// covers their remainder and reports nothing.)
+int copy_state(const float* src, float* dst, int64_t n, void* stream) {
+    const int64_t blocks = (n + 255) / 256, most = 1 << 20;
+    k_copy_state<<<(unsigned)(blocks < most ? blocks : most), 256, 0, (hipStream_t)stream>>>(src, dst, n);
+    return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 
 // dst[0 .. n) = 0: the empty-problem values of the backward's parameter gradients

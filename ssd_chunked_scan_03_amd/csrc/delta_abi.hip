@@ -121,11 +121,6 @@ bool any_overlap(const Range* outs, int no, const Range* ins, int ni) {
     return false;
 }
 
-int copy_state(const float* src, float* dst, int64_t n, void* stream) {
-    k_copy_state<<<(unsigned)((n + 255) / 256), 256, 0, (hipStream_t)stream>>>(src, dst, n);
-    return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
-}
-
 int delta_fwd(const ssd_problem* p, const int32_t* cu, bool packed, const void* x, const float* dt, const float* A,
               const void* B, const void* C, const void* beta, const float* h0, void* y, float* hT, void* ws,
               size_t ws_bytes, void* stream) {

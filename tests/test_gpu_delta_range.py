@@ -26,3 +26,31 @@ def test_growing_states(case):
     d["A"] = d["A"].abs()
     check_forward(d, dtype, case)
     check_backward(d, ref.make_grads(b, T, H, P, N, 51, dtype), dtype, case)
+
+
+def test_empty_sequences_of_many_states():
+    """No tokens and states of more elements than one launch has threads (2^32): hT = h0, or 0; dh0 =
+    dhT, dA = 0; of the rule and of the scan."""
+    b, H, P, N = 10, 16384, 128, 256
+    f32 = dict(dtype=torch.float32, device="cuda")
+    x, dt = torch.zeros(b, 0, H, P, dtype=torch.bfloat16, device="cuda"), torch.zeros(b, 0, H, **f32)
+    B, beta = torch.zeros(b, 0, 1, N, dtype=torch.bfloat16, device="cuda"), torch.zeros(b, 0, H, dtype=torch.bfloat16, device="cuda")
+    A, dA = torch.zeros(H, **f32), torch.empty(H, **f32)
+    prob = ssd.make_problem(b, 0, H, P, N, 1, 64, ssd.SSD_BF16)
+    src, dst = torch.full((b, H, P, N), 3.0, **f32), torch.empty(b, H, P, N, **f32)
+    cu = torch.zeros(b + 1, dtype=torch.int32, device="cuda")
+    calls = [
+        ("forward", 3.0, lambda: ssd.delta_fwd_into(prob, x, dt, A, B, B, beta, src, x, dst, None)),
+        ("forward, no h0", 0.0, lambda: ssd.delta_fwd_into(prob, x, dt, A, B, B, beta, None, x, dst, None)),
+        ("packed", 3.0, lambda: ssd.delta_fwd_varlen_into(prob, cu, x[0], dt[0], A, B[0], B[0], beta[0], src, x[0], dst, None)),
+        ("backward", 3.0, lambda: ssd.delta_bwd_into(prob, x, dt, A, B, B, beta, None, x, src, x, dt, dA, B, B, beta, dst, None)),
+        ("scan", 3.0, lambda: ssd.scan_fwd_into(prob, False, x, dt, A, B, B, None, src, x, dst, None)),
+        ("scan backward", 3.0, lambda: ssd.scan_bwd_into(prob, x, dt, A, B, B, None, None, x, src, x, dt, dA, B, B, None, dst, None)),
+    ]
+    for name, want, call in calls:
+        print(f"[empty] {name}", flush=True)
+        dst.fill_(float("nan"))
+        dA.fill_(float("nan"))
+        call()
+        assert all(bool((dst[i] == want).all()) for i in range(b)), name
+        assert "backward" not in name or bool((dA == 0).all()), name
