@@ -416,7 +416,8 @@ int ssd_delta_bwd(const ssd_problem* p, const void* x, const float* dt, const fl
  *
  * dstate in {16, 32, 64, 128, 256}; pairs a multiple of 4 with 2 pairs <= dstate; eps > 0 and
  * finite; bheads and cheads at most 65536 (one of them may be 0, its pointers NULL);
- * batch * seqlen under 2^24.  Sums are float32; outputs are rounded once.
+ * batch * seqlen under 2^24.  Sums are float32 (rows whose squares leave it are scaled first);
+ * outputs are rounded once.
  *
  * Backward: dB and dC (contiguous, problem dtype) from dBn and dCn (contiguous), and the
  * weights' gradients dwB, dwC [dstate] float32 (NULL = not written; they are formed for

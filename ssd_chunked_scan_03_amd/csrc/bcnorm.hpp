@@ -124,6 +124,31 @@ __device__ __forceinline__ float row_sum(float s, int R) {
     return s;
 }
 
+// 1 / sqrt(scale |v|^2 + eps) of a row, v left as it is and k = 1; a row whose squares' sum leaves
+// float32 (values of 10^18 and more) is scaled by k = 2^-70 first, far past eps.
+template <int VPL>
+__device__ __forceinline__ float row_root(float (&v)[VPL], int R, float scale, float eps, float& k) {
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < VPL; ++e) s += v[e] * v[e];
+    s = row_sum<VPL>(s, R);
+    float r = 1.f / sqrtf(s * scale + eps);
+    const bool over = s > 3.4028235e38f;
+    k = 1.f;
+    if (__any(over)) {
+        k = over ? 0x1p-70f : 1.f;
+        s = 0.f;
+#pragma unroll
+        for (int e = 0; e < VPL; ++e) {
+            v[e] *= k;
+            s += v[e] * v[e];
+        }
+        s = row_sum<VPL>(s, R);
+        if (over) r = 1.f / sqrtf(s * scale);
+    }
+    return r;
+}
+
 template <typename T, int VPL>
 __global__ __launch_bounds__(256) void k_bc_norm(Args a) {
     extern __shared__ float cs[];
@@ -150,12 +175,9 @@ __global__ __launch_bounds__(256) void k_bc_norm(Args a) {
         const bool isB = hd < a.GB;
         const T* src = isB ? static_cast<const T*>(a.B) + t * a.sB + hd * a.N
                            : static_cast<const T*>(a.C) + t * a.sC + (hd - a.GB) * a.N;
-        float v[VPL];
+        float v[VPL], k;
         load_row<T, VPL>(src + n0, v);
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < VPL; ++e) s += v[e] * v[e];
-        const float r = 1.f / sqrtf(row_sum<VPL>(s, R) * scale + a.eps);
+        const float r = row_root<VPL>(v, R, scale, a.eps, k);
 #pragma unroll
         for (int e = 0; e < VPL; ++e) v[e] = v[e] * r * (isB ? wb[e] : wc[e]);
         if (a.F) turn<VPL>(v, cs + tk * 2 * a.F, a.F, n0, a.interleaved, 1.f);
@@ -198,11 +220,8 @@ __global__ __launch_bounds__(256) void k_bc_norm_bwd(Args a) {
             load_row<T, VPL>(src + n0, x);
             load_row<T, VPL>(static_cast<const T*>(isB ? a.dBn : a.dCn) + o + n0, g);
             if (a.F) turn<VPL>(g, cs + tk * 2 * a.F, a.F, n0, a.interleaved, -1.f);
-            float s = 0.f;
-#pragma unroll
-            for (int e = 0; e < VPL; ++e) s += x[e] * x[e];
-            const float r = 1.f / sqrtf(row_sum<VPL>(s, R) * scale + a.eps);
-            float d = 0.f;
+            float d = 0.f, k;
+            const float r = row_root<VPL>(x, R, scale, a.eps, k);
 #pragma unroll
             for (int e = 0; e < VPL; ++e) {
                 const float xr = x[e] * r;
@@ -216,7 +235,7 @@ __global__ __launch_bounds__(256) void k_bc_norm_bwd(Args a) {
             }
             d = row_sum<VPL>(d, R) * scale;
 #pragma unroll
-            for (int e = 0; e < VPL; ++e) g[e] = r * (g[e] - x[e] * d);
+            for (int e = 0; e < VPL; ++e) g[e] = r * k * (g[e] - x[e] * d);
             if (on) store_row<T, VPL>(static_cast<T*>(isB ? a.dB : a.dC) + o + n0, g);
         }
     }
