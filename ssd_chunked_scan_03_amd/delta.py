@@ -173,7 +173,9 @@ def _shapes4(x, B):
 
 def delta_fwd(x, dt, A, B, C, beta, h0=None, chunk=DELTA_CHUNK, return_final_state=True, workspace=None, norm=None):
     """Gated delta rule forward: x [b, T, H, P], dt [b, T, H] f32, A [H] f32, B/C [b, T, G, N],
-    beta [b, T, H] in x's dtype, h0 [b, H, P, N] f32 or None.  Returns (y, hT)."""
+    beta [b, T, H] in x's dtype, h0 [b, H, P, N] f32 or None.  A ``norm`` that turns counts the
+    tokens from 0: where h0 is the state behind earlier tokens, give it their positions.
+    Returns (y, hT)."""
     import torch
     b, T, H, P, G, N = _shapes4(x, B)
     B, C = _normed(B, C, norm)
@@ -223,11 +225,16 @@ def delta_fwd_varlen(x, dt, A, B, C, beta, cu_seqlens, h0=None, chunk=DELTA_CHUN
 
 def delta_step(x, dt, A, B, C, beta, h, norm=None):
     """Decode: run the rule over x's tokens on state h [b, H, P, N] f32 (updated in place).
-    x [b, T, H, P], dt [b, T, H] f32, A [H] f32, B/C [b, T, G, N], beta [b, T, H].  Returns y."""
+    x [b, T, H, P], dt [b, T, H] f32, A [H] f32, B/C [b, T, G, N], beta [b, T, H].  Returns y.
+    A ``norm`` that turns (inv_freq) needs the tokens' positions behind what h has seen: without
+    them the call's tokens count from 0, which only the first tokens of an empty state do, so a
+    single token is refused."""
     import torch
     b, T, H, P, G, N = _shapes4(x, B)
     if h is None:
         raise ValueError("h (the state, updated in place) is required")
+    if T == 1 and norm is not None and norm.get("inv_freq") is not None and norm.get("positions") is None:
+        raise ValueError("a decode step needs norm's positions: its token is not the sequence's first")
     B, C = _normed(B, C, norm)
     f32, td = torch.float32, x.dtype
     code = _check(x, (("x", x, (b, T, H, P), td), ("dt", dt, (b, T, H), f32), ("A", A, (H,), f32),

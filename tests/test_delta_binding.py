@@ -39,3 +39,18 @@ def test_enqueueing_calls_refuse_host_tensors():
         with pytest.raises(ValueError, match="GPU tensors"):
             f()
         print(name, "refused")
+
+
+def test_a_turned_decode_step_needs_its_position():
+    """Without positions a one-token call would be turned as the sequence's first token, wherever
+    it stands."""
+    t = tensors()
+    one = lambda v: v[:, :1].contiguous()  # noqa: E731
+    freq = torch.ones(4)
+    step = lambda norm: ssd.delta_step(one(t["x"]), one(t["dt"]), t["A"], one(t["B"]), one(t["C"]), one(t["beta"]),  # noqa: E731
+                                       t["h0"], norm=norm)
+    with pytest.raises(ValueError, match="positions"):
+        step(dict(inv_freq=freq))
+    for norm in (None, dict(mode="l2"), dict(inv_freq=freq, positions=torch.tensor([[7]], dtype=torch.int32))):
+        with pytest.raises(ValueError, match="GPU tensor"):  # (goes on to the next check)
+            step(norm)
