@@ -350,8 +350,12 @@ int ssd_diag_scan_bwd(const ssd_problem* p, const void* x, const float* dt, cons
  * where they enter the bfloat16 matrix cores they do so as a sum of bfloat16 terms that
  * keeps the float32 mantissa, so the float32 outputs (hT, and ddt, dA, dh0 of the
  * backward) are float32-accurate in bfloat16 problems too; a bfloat16 y comes from two terms, whose
- * rounding stays far below its own.  A NaN or
- * infinity in an input reaches every output of its head from the start of its chunk on.
+ * rounding stays far below its own.
+ * A NaN in an input is in everything that depends on it by the formulas, and in its chunk of 64
+ * tokens it may also be in earlier tokens of the same outputs; an infinity, likewise, as NaN or
+ * infinity.  It goes nowhere else: from x into its head's headdim column, from dt and beta into its
+ * head, from B into its group's heads, from C into their y of its chunk; in the backward into the
+ * gradients of its group's heads.
  * `ws` must hold ssd_delta_workspace_bytes(p) bytes (0 for an invalid or empty problem).
  * Ownership, ordering, capture, aliasing and errors as for ssd_scan_fwd. */
 size_t ssd_delta_workspace_bytes(const ssd_problem* p);

@@ -6,7 +6,7 @@ import torch
 
 import delta_ref as ref
 import ssd_chunked_scan_03_amd as ssd
-from test_gpu_delta import F32, backward, check_backward, check_forward, up
+from test_gpu_delta import check_backward, check_forward, forward
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +54,36 @@ def test_empty_sequences_of_many_states():
         call()
         assert all(bool((dst[i] == want).all()) for i in range(b)), name
         assert "backward" not in name or bool((dA == 0).all()), name
+
+
+@pytest.mark.parametrize("case", [(1, 200, 4, 32, 64, 2, "bf16"), (1, 200, 160, 64, 128, 8, "bf16"),
+                                  (1, 200, 4, 32, 32, 2, "f32")], ids=lambda c: NAME.format(*c))
+@pytest.mark.parametrize("which", ["x", "dt", "beta", "B", "C"])
+def test_a_nan_stays_where_the_formulas_take_it(case, which):
+    """From its token on it is in everything that depends on it; in its chunk it may also be in
+    earlier tokens of the same outputs; other chunks before, heads, groups and (x) headdim columns
+    are what they are without it, bit for bit."""
+    b, T, H, P, N, G, dtype = case
+    d = ref.make(b, T, H, P, N, G, 54, dtype)
+    t, h, p = 104, 1, 5  # the second chunk's token 40
+    y0, h0 = (v.cpu() for v in forward(d))
+    heads = slice(h, h + 1) if which in ("x", "dt", "beta") else slice(0, H // G)  # head 1 is of group 0
+    cols = slice(p, p + 1) if which == "x" else slice(0, P)
+    at = dict(x=(0, t, h, p), dt=(0, t, h), beta=(0, t, h), B=(0, t, 0, 3), C=(0, t, 0, 3))[which]
+    d[which] = d[which].clone()
+    d[which][at] = float("nan")
+    y, hT = (v.cpu() for v in forward(d))
+    reached = torch.zeros(y.shape, dtype=torch.bool)
+    reached[:, 64:, heads, cols] = True
+    assert torch.equal(y[~reached], y0[~reached])
+    state = torch.zeros(hT.shape, dtype=torch.bool)
+    if which == "C":  # only that token's answer
+        assert torch.isnan(y[:, t, heads]).all()
+        reached[:] = False
+        reached[:, 64:128, heads] = True
+        assert torch.equal(y[~reached], y0[~reached])
+    else:
+        assert torch.isnan(y[:, t:, heads, cols]).all()
+        state[:, heads, cols] = True
+        assert torch.isnan(hT[state]).all()
+    assert torch.equal(hT[~state], h0[~state])
