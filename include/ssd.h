@@ -350,7 +350,8 @@ int ssd_diag_scan_bwd(const ssd_problem* p, const void* x, const float* dt, cons
  * where they enter the bfloat16 matrix cores they do so as a sum of bfloat16 terms that
  * keeps the float32 mantissa, so the float32 outputs (hT, and ddt, dA, dh0 of the
  * backward) are float32-accurate in bfloat16 problems too; a bfloat16 y comes from two terms, whose
- * rounding stays far below its own.
+ * rounding stays far below its own.  ddt and dA are summed from terms that each carry their decay,
+ * so they keep that accuracy, relative to those terms, where little of a state outlives a token.
  * A NaN in an input is in everything that depends on it by the formulas, and in its chunk of 64
  * tokens it may also be in earlier tokens of the same outputs; an infinity, likewise, as NaN or
  * infinity.  It goes nowhere else: from x into its head's headdim column, from dt and beta into its

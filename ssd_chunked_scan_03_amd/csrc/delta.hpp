@@ -21,7 +21,15 @@
 //   dP_ij = G_ij beta_j dY_i . r_j (i >= j),  W_ij = -beta_i G_ij beta_j z_i . r_j (i > j)
 //   dQ = diag(e^c) dY h + dP K,  dbeta_i = z_i . r_i
 //   dK = dP^T Q + (W + W^T) K + diag(e^{c_L - c} beta) r dh' - diag(e^c) dX h
-//   dlog a_t = sum_{s >= t} (dY_s . Y_s - dX_s . X_s) + <dh', h'>          (s in the chunk)
+//   dlog a_t = sum_{i >= t > j} E_ij + sum_{i >= t} F_i + sum_{j < t} D_j + e^{c_L} <dh', h>,
+//     E_ij = dP_ij (Q_i . K_j) + W_ij (K_i . K_j),   F_i = e^{c_i} (dY_i . h Q_i - dX_i . h K_i),
+//     D_j = e^{c_L - c_j} u_j . dh' K_j
+//
+// The last sums over everything whose decay holds a_t: pairs of tokens on either side, the
+// entering state with a later token, an earlier token with the leaving state, and one state
+// with the other.  (It is also sum_{s >= t} (dY_s . Y_s - dX_s . X_s) + <dh', h'>, whose terms
+// are of order one however little of a state outlives a token: their difference loses the
+// gradient of a strong decay.)
 //
 // Precision.  One bfloat16 rounding of the state in a product would cost 2e-3 of the float32
 // outputs (hT, ddt, dA, dh0), so float32 operands enter the matrix cores as a sum of three
@@ -88,20 +96,23 @@ struct Args {
     void* dC;
     void* dbeta;
     float* dh0;
-    void* r;      // [b T][H][P] residuals; bfloat16: and what their rounding left, rounded
+    void* r;      // [b T][H][P] residuals; bfloat16: in three terms
     void* rlo;
+    void* rll;
     void* z;      // [b T][H][P], the same
     void* zlo;
+    void* zll;
+    float* kh;    // [ntab][H] e^c K h^T, 64 P values as the walks hold them (kh_at)
     void* hin;    // [ntab][H][P][N] state entering each chunk
     short* hlo;   // bfloat16: what hin's rounding left of the float32 state (split_state)
     void* lin;    // [ntab][H][P][N] dh' of each chunk
-    float* hend;  // [b H][P][N] state after the last chunk
-    float* dyy;   // [slices][b H][T] per-slice dY . Y
-    float* dxx;   // [slices][b H][T] per-slice dX . X
-    float* tot;   // [slices][ntab][H] per-slice <dh', h'> of each chunk
-    float* dAp;   // [ntab][H]
+    float* fq;    // [slices][b H][T] per-slice e^c dY . h Q
+    float* fk;    // [slices][b H][T] per-slice e^c dX . h K
+    float* dj;    // [slices][b H][T] per-slice D
+    float* tot;   // [tots][ntab][H] per-wave e^{c_L} <dh', h> of each chunk
+    double* dAp;  // [ntab][H]
     float* part;  // [nsub][2][b T][G][N] partial dK, dQ when a group's heads are shared out
-    int slices, nsub;
+    int slices, tots, nsub;
     int* order;   // packed: [nrows] the rows in the order that the walks start them
     hipStream_t stream;
 };
@@ -207,6 +218,8 @@ template <int CTRL> __device__ __forceinline__ unsigned lane_turn(unsigned v) {
 template <int CTRL> __device__ __forceinline__ float lane_turn(float v) {
     return __builtin_bit_cast(float, lane_turn<CTRL>(__builtin_bit_cast(unsigned, v)));
 }
+// The value N lanes before, in its row of 16 (zero past the row's start).
+template <int N> __device__ __forceinline__ float row_shift(float v) { return lane_turn<0x110 + N>(v); }
 // Sum over the 16 lanes of a row, in every lane (rotations by 8, 4, 2, 1).
 __device__ __forceinline__ float row_sum16(float v) {
     v += lane_turn<0x128>(v);
@@ -265,6 +278,13 @@ __device__ __forceinline__ f32x4 floats(u32x2v v) {
 // what rounding to bfloat16 leaves of v
 __device__ __forceinline__ f32x4 rest16(f32x4 v) {
     return v - floats(u32x2v{cvt2(v[0], v[1]), cvt2(v[2], v[3])});
+}
+
+// Where a wave's lane finds its four tokens of token tile `it`, column tile ct, of a chunk's e^c K
+// h^T: `tiles` = the wave's group of 16 CT columns, of P / (16 CT).
+template <int CT>
+__device__ __forceinline__ int64_t kh_at(int64_t item, int P, int tiles, int it, int ct, int lane) {
+    return item * L * P + (int64_t)((tiles * 4 + it) * CT + ct) * 256 + lane * 4;
 }
 
 __device__ __forceinline__ f32x8 join(f32x4 a, f32x4 b) {
@@ -681,13 +701,14 @@ struct Cfg {
     static constexpr int ldx(int sw) { return sw + 8; }
     static size_t walk_bytes(int sw, int mterms, int xtiles) {
         return (size_t)((SHARE ? 1 : 2) * KT + (NT + mterms) * kFrag * 512 + xtiles * L * ldx(sw)) * sizeof(T) +
-               (size_t)(3 * L + 4 * L) * 4;
+               (size_t)(3 * L + 8 * L) * 4;
     }
 };
 
 // A chunk's inputs on their way from memory to LDS, in 256 threads' registers: K and Q (dstate
 // 256 in float32, where one buffer holds both in turn: the one that is read first, Q in the
-// forward walk, K in the adjoint one), x, dY, the tables of S and M and the factors.
+// forward walk, K in the adjoint one), x (the adjoint walk: r), dY, the tables of S and M (MT = 0:
+// not M) and the factors.
 template <typename T, int N, int CT, int MT, bool UP>
 struct Staged {
     typedef Cfg<T, N> CF;
@@ -695,7 +716,7 @@ struct Staged {
     static constexpr int NK = CF::NP / 32, NX = 2 * CT;  // 8-element pieces per thread
     static constexpr bool K = UP || !CF::SHARE, Q = !UP || !CF::SHARE;
     V k[K ? NK : 1], q[Q ? NK : 1], x[NX], y[NX];
-    f32x4 s[3], m[3];
+    f32x4 s[3], m[MT ? 3 : 1];
     float f[3];
     template <int C>
     static __device__ __forceinline__ void get(const T* src, int64_t ss, int n, int w, int wpad, V (&v)[C]) {
@@ -722,10 +743,10 @@ struct Staged {
         const int n = (int)min((int64_t)L, a.rows.len(row) - (int64_t)c * L);
         if (K) get(static_cast<const T*>(a.B) + (t0 * G + g) * N, (int64_t)G * N, n, N, CF::NP, k);
         if (Q) get(static_cast<const T*>(a.C) + (t0 * G + g) * N, (int64_t)G * N, n, N, CF::NP, q);
-        get(static_cast<const T*>(a.x) + (t0 * H + h) * P + p0, (int64_t)H * P, n, SW, SW, x);
+        get(static_cast<const T*>(UP ? a.r : a.x) + (t0 * H + h) * P + p0, (int64_t)H * P, n, SW, SW, x);
         if (dy) get(static_cast<const T*>(a.dy) + (t0 * H + h) * P + p0, (int64_t)H * P, n, SW, SW, y);
         get_tri<UP>(a.tab + e * kTab, s);
-        get_tri<UP>(a.tab + e * kTab + kTri * 256, m);
+        if constexpr (MT > 0) get_tri<UP>(a.tab + e * kTab + kTri * 256, m);
         if (t < L) {
             f[0] = a.vec[e * kVec + t];
             f[1] = a.vec[e * kVec + L + t];
@@ -739,7 +760,7 @@ struct Staged {
         set(Xs, CF::ldx(SW), SW, x);
         if (dy) set(Ys, CF::ldx(SW), SW, y);
         put_tri<T, CF::NT, UP>(s, Sf);
-        put_tri<T, MT, UP>(m, Mf);
+        if constexpr (MT > 0) put_tri<T, MT, UP>(m, Mf);
         if (t < L)
 #pragma unroll
             for (int i = 0; i < 3; ++i) factors[i * L + t] = f[i];
@@ -751,14 +772,13 @@ struct Staged {
 // (W waves, each CT column tiles, no exchange between waves).  All 256 threads stage; a
 // chunk's inputs are asked for while the chunk before is computed and wait in registers.  SAVE = false writes y and
 // hT.  SAVE = true is the backward's first walk: it writes the residuals r, the state
-// entering every chunk and after the last, and the per-token dY . Y (Y in float32, all
-// terms) instead.
+// entering every chunk, e^c K h^T and the per-token e^c dY . h Q (all terms) instead.
 // ---------------------------------------------------------------------------
 template <typename T, int N, int CT, bool SAVE>
 __global__ __launch_bounds__(256) void k_delta(Args a, int waves) {
     typedef Cfg<T, N> CF;
     constexpr int NP = CF::NP, LDK = CF::LDK, NTL = N / 16, KS = NP / 32, NT = CF::NT;
-    constexpr int MT = SAVE || NT == 1 ? NT : 2;  // terms of M (y is rounded to the problem dtype)
+    constexpr int MT = SAVE ? 0 : NT == 1 ? 1 : 2;  // terms of M (y is rounded to the problem dtype)
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
     const int H = a.H, G = a.G, P = a.P;
@@ -862,8 +882,21 @@ __global__ __launch_bounds__(256) void k_delta(Args a, int waves) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int t = it * 16 + 4 * q + i;
-                    v[it][ct][i] = to_f(Xs[t * ldx + pw + ct * 16 + l16]) - ecs[t] * v[it][ct][i];
+                    v[it][ct][i] *= ecs[t];
                 }
+        if (SAVE) {
+#pragma unroll
+            for (int it = 0; it < 4; ++it)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) st4(a.kh + kh_at<CT>(e, P, (p0 + pw) / (16 * CT), it, ct, lane), v[it][ct]);
+        }
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[it][ct][i] = to_f(Xs[(it * 16 + 4 * q + i) * ldx + pw + ct * 16 + l16]) - v[it][ct][i];
         auto scaled = [&](const float* s, bool two) {  // s_t v_t as operands
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -895,19 +928,20 @@ __global__ __launch_bounds__(256) void k_delta(Args a, int waves) {
             for (int ct = 0; ct < CT; ++ct) v[it][ct] -= d[ct];
         }
         // Y = e^c Q h^T + M u
-        scaled(bts, false);
+        if (!SAVE) scaled(bts, false);
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) yq[it][ct][i] *= ecs[it * 16 + 4 * q + i];
+            if constexpr (!SAVE) {
 #pragma unroll
-            for (int t = 0; t <= it / 2; ++t) {
-                const Sp<T> mf = frag_tab<T, MT>(Mf, frag_lo(it, t), lane);
+                for (int t = 0; t <= it / 2; ++t) {
+                    const Sp<T> mf = frag_tab<T, MT>(Mf, frag_lo(it, t), lane);
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-                    yq[it][ct] = mma_ss<SAVE ? 3 : 2>(yq[it][ct], mf, b2[t][ct]);
+                    for (int ct = 0; ct < CT; ++ct) yq[it][ct] = mma_ss<2>(yq[it][ct], mf, b2[t][ct]);
+                }
             }
         }
         // h' = e^{c_L} h + K^T (e^{c_L - c} u)
@@ -924,7 +958,7 @@ __global__ __launch_bounds__(256) void k_delta(Args a, int waves) {
                 for (int ct = 0; ct < CT; ++ct) acc[t][ct] = mma_es<3>(acc[t][ct], kf, b2[ks][ct]);
             }
         }
-        // out through the (own columns of the) x tile: y, or r and the dY . Y sums
+        // out through the (own columns of the) x tile: y, or r and the sums with dY
 #pragma unroll
         for (int it = 0; it < 4; ++it)
 #pragma unroll
@@ -938,7 +972,11 @@ __global__ __launch_bounds__(256) void k_delta(Args a, int waves) {
                         T* o2 = Ys + t * ldx + pw + ct * 16 + l16;
                         dot += to_f(*o2) * yq[it][ct][i];
                         *o = from_f<T>(v[it][ct][i]);
-                        *o2 = from_f<T>(v[it][ct][i] - to_f(*o));
+                        const float rest = v[it][ct][i] - to_f(*o);
+                        *o2 = from_f<T>(rest);
+                        if (NT > 1 && t < n)
+                            static_cast<T*>(a.rll)[((t0 + t) * H + h) * P + p0 + pw + ct * 16 + l16] =
+                                from_f<T>(rest - to_f(*o2));
                     } else {
                         *o = from_f<T>(yq[it][ct][i]);
                     }
@@ -958,17 +996,16 @@ __global__ __launch_bounds__(256) void k_delta(Args a, int waves) {
             for (int t = tid; t < n; t += 256) {
                 float s = 0.f;
                 for (int k2 = 0; k2 < waves; ++k2) s += dots[k2 * L + t];
-                a.dyy[((int64_t)sl * BH + bh) * a.T + (int64_t)c * L + t] = s;
+                a.fq[((int64_t)sl * BH + bh) * a.T + (int64_t)c * L + t] = s;
             }
         }
     }
-    float* hT = SAVE ? a.hend : a.hT;
-    if (hT && on) {
+    if (!SAVE && a.hT && on) {
 #pragma unroll
         for (int t = 0; t < NTL; ++t)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
-                st4(hT + (bh * P + p0 + pw + ct * 16 + l16) * N + t * 16 + 4 * q, acc[t][ct]);
+                st4(a.hT + (bh * P + p0 + pw + ct * 16 + l16) * N + t * 16 + 4 * q, acc[t][ct]);
     }
 }
 
@@ -1240,8 +1277,8 @@ __global__ __launch_bounds__(256, OCC) void k_delta_dma(Args a) {
 // cycle.  (Four waves doing all of it in turn: 2.8 ms.  Keys and tables straight to the
 // registers of the one wave that reads them: 3.1 ms, their scattered rows choke the
 // address unit.  Lines touched two chunks ahead: 2.7 ms, of the same cause.)
-// SAVE = true writes the residuals r, the state entering every chunk and after the last, and
-// the per-token dY . Y (Y in float32, all terms) instead of y and hT.
+// SAVE = true writes the residuals r, the state entering every chunk, e^c K h^T and the per-token
+// e^c dY . h Q (all terms) instead of y and hT; it reads no M.
 // ---------------------------------------------------------------------------
 // what the two team walks share: the chunk addresses of one (row, head) and the lane's offsets
 template <int N, int CT>
@@ -1297,10 +1334,10 @@ struct Team {
     __device__ __forceinline__ void mark(bf16* dst) const {
         if (w == 0) dma_run(make_rsrc(a.tab, 1024), reinterpret_cast<char*>(dst), 1, 0, 1, lane);
     }
-    // a chunk's table and factors, RUNS KiB in all
-    template <int RUNS>
+    // RUNS KiB of a chunk's tables and factors, which are ALL KiB, from the FROM-th on
+    template <int ALL, int FROM, int RUNS>
     __device__ __forceinline__ void fetch_tab(int c, bf16* dst) const {
-        const brsrc r = make_rsrc(reinterpret_cast<const bf16*>(a.tab) + item(c) * RUNS * 512, RUNS * 1024);
+        const brsrc r = make_rsrc(reinterpret_cast<const bf16*>(a.tab) + (item(c) * ALL + FROM) * 512, RUNS * 1024);
 #pragma unroll
         for (int k = 0; k < RUNS; k += 4)
             if (k + w < RUNS)
@@ -1322,6 +1359,18 @@ struct Team {
     // token tile w of a [token][H P] tensor
     __device__ __forceinline__ void store_rows(void* base, int c, const f32x4 (&v)[CT]) const {
         store_tile<CT>(x_rsrc(base, c), v, xo, w, rsx, sel, upper);
+    }
+    // the same in three terms
+    __device__ __forceinline__ void store_rows3(void* hi, void* lo, void* ll, int c, const f32x4 (&v)[CT]) const {
+        f32x4 r1[CT], r2[CT];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            r1[ct] = rest16(v[ct]);
+            r2[ct] = rest16(r1[ct]);
+        }
+        store_rows(hi, c, v);
+        store_rows(lo, c, r1);
+        store_rows(ll, c, r2);
     }
     // fragments: token tile `it`, key columns 32 ks on; state tile t, 32 tokens from tile row `p`
     __device__ __forceinline__ bf16x8 frag_rows16(const bf16* tile, int it, int ks) const {
@@ -1453,8 +1502,8 @@ template <int N, int CT, int KB, bool SAVE>
 __global__ __launch_bounds__(512) void k_delta_team(Args a) {
     typedef Team<N, CT> TM;
     constexpr int KS = N / 32, TILE = Dma<N>::TILE, OT = TM::OT, OP = TM::OP;
-    constexpr int QT = SAVE ? 3 : 2, MT = QT, UT = QT;  // terms of h, M and u in Y
-    constexpr int RUNS = (SAVE ? kFragTab2 : kFragTab) / 512 + 1;
+    constexpr int QT = SAVE ? 3 : 2, MT = 2, UT = 2;  // terms of h, M and u in Y
+    constexpr int ALL = (SAVE ? kFragTab2 : kFragTab) / 512 + 1, RUNS = SAVE ? 16 : ALL;  // (SAVE: S and the factors)
     __shared__ __attribute__((aligned(16))) bf16 K0[TILE];
     __shared__ __attribute__((aligned(16))) bf16 K1[KB == 2 ? TILE : 8];
     __shared__ __attribute__((aligned(16))) bf16 Qs[TILE];
@@ -1472,8 +1521,11 @@ __global__ __launch_bounds__(512) void k_delta_team(Args a) {
     const int lane = tm.lane, w = tm.w, l16 = tm.l16, q = tm.q, nc = tm.nc, t0w = OT * w;
     if (nc > 0 && wave_id() >= 4) {
         auto bring = [&](int c) {
-            tm.template fetch_tab<RUNS>(c, Sf);
-            if (SAVE) tm.fetch_x(a.dy, c, Ys);
+            tm.template fetch_tab<ALL, 0, SAVE ? 15 : ALL>(c, Sf);
+            if (SAVE) {
+                tm.template fetch_tab<ALL, ALL - 1, 1>(c, Sf + 15 * 512);
+                tm.fetch_x(a.dy, c, Ys);
+            }
         };
         tm.fetch_tile(a.B, 0, K0);
         tm.fetch_tile(a.C, 0, Qs);
@@ -1489,7 +1541,7 @@ __global__ __launch_bounds__(512) void k_delta_team(Args a) {
                 const int t = w * 16 + 4 * q + (l16 & 3);
                 const float dt = l16 & 2 ? (l16 & 1 ? e[3] : e[2]) : (l16 & 1 ? e[1] : e[0]);
                 if (l16 < 4 && t < tm.rows_left(c))
-                    a.dyy[((int64_t)tm.sl * a.rows.nrows * a.H + tm.bh) * a.T + (int64_t)c * L + t] = dt;
+                    a.fq[((int64_t)tm.sl * a.rows.nrows * a.H + tm.bh) * a.T + (int64_t)c * L + t] = dt;
             } else {
                 tm.store_rows(a.y, c, yq);
             }
@@ -1518,7 +1570,7 @@ __global__ __launch_bounds__(512) void k_delta_team(Args a) {
                 }
             };
             bf16x8 mf[2][MT];
-            tm.template table_row<MT>(Mf, mf);
+            if (!SAVE) tm.template table_row<MT>(Mf, mf);
             f32x4 dy[CT];
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
@@ -1534,14 +1586,14 @@ __global__ __launch_bounds__(512) void k_delta_team(Args a) {
             }
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) yq[ct] = ec * (yq[ct] + y2[ct]);
-            wave_meet(false);  // u is in place
-            // Y = e^c Q h^T + M beta r
-            tm.template times_rows<MT, UT>(yq, mf, Uf);
             d = f32x4{0.f, 0.f, 0.f, 0.f};
             if (SAVE) {
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) d += dy[ct] * yq[ct];
             }
+            wave_meet(false);  // u is in place
+            // Y = e^c Q h^T + M beta r
+            if (!SAVE) tm.template times_rows<MT, UT>(yq, mf, Uf);
         };
         for (int c = 0; c < nc; c += 2) {
             chunk(c, KB == 2 ? K1 : K0);
@@ -1598,7 +1650,9 @@ __global__ __launch_bounds__(512) void k_delta_team(Args a) {
             // R = X - e^c K h^T of token tile w
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                v[ct] -= ec * tm.sum(Pf, ct);
+                const f32x4 kh = ec * tm.sum(Pf, ct);
+                if (SAVE) st4(a.kh + kh_at<CT>(tm.item(c), a.P, tm.sl, w, ct, lane), kh);
+                v[ct] -= kh;
                 rb[ct] = v[ct] * bt;
             }
             tm.template put_rows<3>(Rf, rb);
@@ -1617,7 +1671,7 @@ __global__ __launch_bounds__(512) void k_delta_team(Args a) {
                 uw[ct] = v[ct] * ew;
             }
             tm.template put_rows<3>(Wf, uw);
-            tm.template put_rows<UT>(Uf, rb);
+            if (!SAVE) tm.template put_rows<UT>(Uf, rb);
 #pragma unroll
             for (int o = 0; o < OT; ++o)
 #pragma unroll
@@ -1644,22 +1698,18 @@ __global__ __launch_bounds__(512) void k_delta_team(Args a) {
             tm.split(acc, sp);
             if (c + 1 < nc) tm.template put_state<QT>(Hf, sp);
             if (SAVE) {
-                f32x4 rest[CT];
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) rest[ct] = rest16(v[ct]);
-                tm.store_rows(a.r, c, v);
-                tm.store_rows(a.rlo, c, rest);
+                tm.store_rows3(a.r, a.rlo, a.rll, c, v);
             }
         };
         for (int c = 0; c < nc; c += 2) {
             chunk(c, K0);
             if (c + 1 < nc) chunk(c + 1, KB == 2 ? K1 : K0);
         }
-        if (float* hT = SAVE ? a.hend : a.hT) {
+        if (!SAVE && a.hT) {
 #pragma unroll
             for (int o = 0; o < OT; ++o)
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) st4(hT + tm.hn(t0w + o, ct), acc[o][ct]);
+                for (int ct = 0; ct < CT; ++ct) st4(a.hT + tm.hn(t0w + o, ct), acc[o][ct]);
         }
     }
 }
@@ -1668,7 +1718,7 @@ __global__ __launch_bounds__(512) void k_delta_team(Args a) {
 // k_delta_adj: the adjoint walk by the same teams (chunks in reverse, dh^T in accumulators); the
 // tables' transposes are read from the same fragments by transposing loads.  Outputs as
 // k_delta_rev.  Four waves, which share every product.  Bound by a chunk's latency: 2 rows of 2048
-// tokens, 48 heads of 64, dstate 128, in 178 us, 5.5 us a chunk (the first walk: 130 us).
+// tokens, 48 heads of 64, dstate 128, in 188 us, 5.9 us a chunk (the first walk: 129 us).
 // ---------------------------------------------------------------------------
 template <int N, int CT, int KB>
 __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
@@ -1677,14 +1727,12 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
     __shared__ __attribute__((aligned(16))) bf16 K1[KB == 2 ? TILE : 8];
     __shared__ __attribute__((aligned(16))) bf16 Qs[TILE];
     __shared__ __attribute__((aligned(16))) bf16 Sf[TABN];
-    __shared__ __attribute__((aligned(16))) bf16 Xs[CT * 1024];
     __shared__ __attribute__((aligned(16))) bf16 Ys[CT * 1024];
     constexpr int HF = KS * 3 * CT * 512, RF = 2 * 3 * CT * 512;
-    __shared__ __attribute__((aligned(16))) bf16 Ex[HF + 3 * RF + 8];  // operands passed between the waves
+    __shared__ __attribute__((aligned(16))) bf16 Ex[HF + 3 * RF];  // operands passed between the waves
     const bf16* Mf = Sf + 3 * 5 * 512;
     const float* Vs = reinterpret_cast<const float*>(Sf + TABN - kFragVec);
     bf16 *Hf = Ex, *Rf = Hf + HF, *Wf = Rf + RF, *Yf = Wf + RF;  // Wf: -e^c dX, Yf: e^c dY
-    float* tots = reinterpret_cast<float*>(Yf + RF);
     const Team<N, CT> tm(a);
     const int lane = tm.lane, w = tm.w, l16 = tm.l16, q = tm.q, nc = tm.nc, t0w = OT * w;
     const int64_t BH = (int64_t)a.rows.nrows * a.H;
@@ -1704,52 +1752,38 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, ds_tr16(tab + at(2 * t + 1) + ft), 0, 1, 2, 3, 4,
                                                                   5, 6, 7));
     };
-    // dh' of a chunk, in accumulators: stored for the gradients of B, and <dh', h'> over this
-    // wave's tiles (summed over the waves after the next barrier)
+    // dh' of a chunk, in accumulators: stored for the gradients of B
     constexpr int OP = (OT + 1) / 2;
-    auto leave = [&](int c, auto h8) {
+    auto leave = [&](int c) {
         const int64_t lo = (tm.item(c) - tm.bh) * a.P * N;
-        float s = 0.f;
 #pragma unroll
         for (int o = 0; o < OP; ++o)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                const f32x8 av = join(acc[2 * o][ct], acc[2 * o + 1 < OT ? 2 * o + 1 : 2 * o][ct]), hv = h8(o, ct);
                 Sp<bf16> ov;
-                split8<1>(av, ov);
+                split8<1>(join(acc[2 * o][ct], acc[2 * o + 1 < OT ? 2 * o + 1 : 2 * o][ct]), ov);
                 bf16* lp = static_cast<bf16*>(a.lin) + lo + tm.hn(t0w + 2 * o, ct);
                 if (OT > 1) st8(lp, ov.t[0]);
                 else st4(lp, __builtin_shufflevector(ov.t[0], ov.t[0], 0, 1, 2, 3));
-#pragma unroll
-                for (int i = 0; i < (OT > 1 ? 8 : 4); ++i) s += hv[i] * av[i];
             }
-        s = row_sum16(s);
-        s += __shfl_xor(s, 16, 64);
-        s += __shfl_xor(s, 32, 64);
-        if (lane == 0) tots[w] = s;
     };
     if (nc > 0) {
         tm.fetch_tile(a.B, nc - 1, K0);
-        tm.template fetch_tab<TABN / 512>(nc - 1, Sf);
-        tm.fetch_x(a.x, nc - 1, Xs);
+        tm.template fetch_tab<TABN / 512, 0, TABN / 512>(nc - 1, Sf);
         tm.fetch_x(a.dy, nc - 1, Ys);
         tm.mark(Rf);
         Sp<bf16> sp[OP][CT];
         tm.split(acc, sp);
         tm.template put_state<3>(Hf, sp);
-        leave(nc - 1, [&](int o, int ct) {
-            const float* hp = a.hend + tm.hn(t0w + 2 * o, ct);
-            return join(ld4(hp), ld4(OT > 1 ? hp + 4 : hp));
-        });
+        leave(nc - 1);
     }
     auto chunk = [&](int c, const bf16* Ks, bf16* Kn) {
         const bool more = c > 0;
         wave_meet(true);  // the chunk's tiles have landed, the adjoint's operands are in place
         tm.fetch_tile(a.C, c, Qs);  // read last in the chunk
         if (KB == 2 && more) tm.fetch_tile(a.B, c - 1, Kn);
-        if (threadIdx.x == 0)
-            a.tot[(int64_t)tm.sl * a.ntab * a.H + tm.item(c)] = (tots[0] + tots[1]) + (tots[2] + tots[3]);
-        // the state entering this chunk, for the chunk before: consumed at the end
+        // the state entering this chunk, e^c K h^T and r of token tile w, for the decays' gradients: consumed
+        // at the end
         bf16x8 hi[OP][CT];
         s16x8 hl[OP][CT];
         {
@@ -1770,6 +1804,13 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
                     }
                 }
         }
+        f32x4 kh[CT];
+        u32x2v rt[3][CT];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) kh[ct] = ld4(a.kh + kh_at<CT>(tm.item(c), a.P, tm.sl, w, ct, lane));
+        load_tile<CT>(tm.x_rsrc(a.r, c), rt[0], tm.xo, w, tm.rsx);
+        load_tile<CT>(tm.x_rsrc(a.rlo, c), rt[1], tm.xo, w, tm.rsx);
+        load_tile<CT>(tm.x_rsrc(a.rll, c), rt[2], tm.xo, w, tm.rsx);
         // dU = e^{c_L - c} K dh'^T + M^T dY of token tile w
         f32x4 v[CT], v2[CT];
 #pragma unroll
@@ -1787,10 +1828,10 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
         }
         const f32x4 ec = ld4(Vs + w * 16 + 4 * q), ew = ld4(Vs + L + w * 16 + 4 * q),
                     bt = ld4(Vs + 2 * L + w * 16 + 4 * q);
-        f32x4 rb[CT], yw[CT];
+        f32x4 rb[CT], yw[CT], kd[CT];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-            v[ct] = ew * (v[ct] + v2[ct]);
+            kd[ct] = v[ct] = ew * (v[ct] + v2[ct]);
             yw[ct] = ec * floats(tm.x_tile(Ys, w, ct));
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -1820,30 +1861,56 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
                     for (int ct = 0; ct < CT; ++ct) v[ct] = mma(v[ct], f, tm.template get<3>(Rf, t, m, ct));
             }
         }
-        f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f}, rest[CT], dx[CT], wv[CT];
+        f32x4 dx[CT], wv[CT];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-            rest[ct] = rest16(v[ct]);
             dx[ct] = v[ct] * bt;
             wv[ct] = dx[ct] * -ec;
-            d += floats(tm.x_tile(Xs, w, ct)) * dx[ct];
         }
         tm.template put_rows<3>(Wf, wv);
         const float el = Vs[L - 1];
         wave_meet(true);  // dX is in place, Q has landed; every wave is done with the tables
         if (more) {
-            tm.template fetch_tab<TABN / 512>(c - 1, Sf);
-            tm.fetch_x(a.x, c - 1, Xs);
+            tm.template fetch_tab<TABN / 512, 0, TABN / 512>(c - 1, Sf);
         }
-        tm.store_rows(a.z, c, v);
-        tm.store_rows(a.zlo, c, rest);
+        tm.store_rows3(a.z, a.zlo, a.zll, c, v);
         tm.store_rows(a.dx, c, dx);
+        {  // of the decays' gradients: e^c dX . h K and u . e^{c_L - c} dh' K of the tile's tokens
+            f32x4 f = f32x4{0.f, 0.f, 0.f, 0.f}, g = f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = row_sum16(d[i]);
-        {
+            for (int ct = 0; ct < CT; ++ct) {
+                f32x4 r = floats(quad_t(rt[2][ct], tm.sel, tm.upper));
+                r += floats(quad_t(rt[1][ct], tm.sel, tm.upper));
+                r += floats(quad_t(rt[0][ct], tm.sel, tm.upper));
+                f += kh[ct] * dx[ct];
+                g += r * bt * kd[ct];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[i] = row_sum16(f[i]);
+                g[i] = row_sum16(g[i]);
+            }
             const int t = w * 16 + 4 * q + (l16 & 3);
-            const float dt = l16 & 2 ? (l16 & 1 ? d[3] : d[2]) : (l16 & 1 ? d[1] : d[0]);
-            if (l16 < 4 && t < tm.rows_left(c)) a.dxx[((int64_t)tm.sl * BH + tm.bh) * a.T + (int64_t)c * L + t] = dt;
+            const bool o1 = l16 & 1, o2 = l16 & 2;
+            const int64_t at = ((int64_t)tm.sl * BH + tm.bh) * a.T + (int64_t)c * L + t;
+            if (l16 < 4 && t < tm.rows_left(c)) {
+                a.fk[at] = o2 ? (o1 ? f[3] : f[2]) : (o1 ? f[1] : f[0]);
+                a.dj[at] = o2 ? (o1 ? g[3] : g[2]) : (o1 ? g[1] : g[0]);
+            }
+            // and e^{c_L} <dh', h> over this wave's tiles
+            float s = 0.f;
+#pragma unroll
+            for (int o = 0; o < OP; ++o)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    const f32x8 av = join(acc[2 * o][ct], acc[2 * o + 1 < OT ? 2 * o + 1 : 2 * o][ct]);
+#pragma unroll
+                    for (int i = 0; i < (OT > 1 ? 8 : 4); ++i) s += join_state(hi[o][ct][i], hl[o][ct][i]) * av[i];
+                }
+            s = row_sum16(s);
+            s += __shfl_xor(s, 16, 64);
+            s += __shfl_xor(s, 32, 64);
+            if (lane == 0) a.tot[(int64_t)(tm.sl * 4 + w) * a.ntab * a.H + tm.item(c)] = s * el;
         }
         // dh = e^{c_L} dh' - K^T (e^c dX) + Q^T (e^c dY) of this wave's tiles
 #pragma unroll
@@ -1873,12 +1940,7 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
             Sp<bf16> sp[OP][CT];
             tm.split(acc, sp);
             tm.template put_state<3>(Hf, sp);
-            leave(c - 1, [&](int o, int ct) {
-                f32x8 hv;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) hv[i] = join_state(hi[o][ct][i], hl[o][ct][i]);
-                return hv;
-            });
+            leave(c - 1);
         }
         if (KB == 1 && more) {
             wave_meet(false);  // every wave is done with K
@@ -1899,8 +1961,8 @@ __global__ __launch_bounds__(256) void k_delta_adj(Args a) {
 
 // ---------------------------------------------------------------------------
 // k_delta_rev: the adjoint walk, chunks in reverse; the same slices and layout, the adjoint
-// state dh^T[n][p] in accumulators.  Writes dx, z, dh' of every chunk (problem dtype), the
-// per-token dX . X, <dh', h'> of every chunk, and dh0.
+// state dh^T[n][p] in accumulators.  Writes dx, z, dh' of every chunk (problem dtype), for the
+// decays' gradients the per-token e^c dX . h K and D and e^{c_L} <dh', h> of every chunk, and dh0.
 // ---------------------------------------------------------------------------
 template <typename T, int N, int CT>
 __global__ __launch_bounds__(256) void k_delta_rev(Args a, int waves) {
@@ -1919,8 +1981,8 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a, int waves) {
     float* ecs = reinterpret_cast<float*>(Ys + L * ldx);
     float* ews = ecs + L;
     float* bts = ews + L;
-    float* dots = bts + L;  // [wave][token]
-    __shared__ float tots[4];
+    float* dots = bts + L;       // [wave][token]
+    float* dots2 = dots + 4 * L;
 
     const int nsl = P / SW, BH = a.rows.nrows * H;
     const int sl = (int)(blockIdx.x % (unsigned)nsl);
@@ -1939,13 +2001,13 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a, int waves) {
             acc[t][ct] = a.dhT && on ? ld4(a.dhT + (bh * P + p0 + pw + ct * 16 + l16) * N + t * 16 + 4 * q)
                                : f32x4{0.f, 0.f, 0.f, 0.f};
 
-    // the state after a chunk, for <dh', h'>: asked for with the chunk's inputs (dstate 256 leaves
+    // the state entering a chunk, for <dh', h>: asked for with the chunk's inputs (dstate 256 leaves
     // no registers to wait in)
     constexpr bool AHEAD = N <= 128;
     typename V4<T>::type hi[NTL][CT];
     s16x4 lo[NTL][CT];
     auto load_h = [&](int c) {
-        const int64_t ho = (((int64_t)(kb0 + c + 1) * H + h) * P + p0 + pw) * N;
+        const int64_t ho = (((int64_t)(kb0 + c) * H + h) * P + p0 + pw) * N;
 #pragma unroll
         for (int t = 0; t < NTL; ++t)
 #pragma unroll
@@ -1956,46 +2018,37 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a, int waves) {
             }
     };
     Staged<T, N, CT, NT, true> in;
-    if (nc > 0) in.load(a, row, h, nc - 1, p0, SW, true);
+    if (nc > 0) {
+        in.load(a, row, h, nc - 1, p0, SW, true);
+        if (AHEAD && on) load_h(nc - 1);
+    }
     for (int c = nc - 1; c >= 0; --c) {
         const int64_t t0 = tok0 + (int64_t)c * L;
         const int n = (int)min((int64_t)L, Tn - (int64_t)c * L);
         const int64_t e = (int64_t)(kb0 + c) * H + h;
-        float s = 0.f;  // <dh', h'> over this wave's columns
+        float s = 0.f;  // <dh', h> over this wave's columns
         if (on) {
-            if (!AHEAD && c + 1 < nc) load_h(c);
+            if (!AHEAD) load_h(c);
 #pragma unroll
             for (int t = 0; t < NTL; ++t)
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    f32x4 hv;
-                    if (c + 1 == nc) {
-                        hv = ld4(a.hend + (bh * P + p0 + pw + ct * 16 + l16) * N + t * 16 + 4 * q);
-                    } else if constexpr (std::is_same<T, bf16>::value) {
+                for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) hv[i] = join_state(hi[t][ct][i], lo[t][ct][i]);
-                    } else {
-                        hv = hi[t][ct];
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (std::is_same<T, bf16>::value) s += join_state(hi[t][ct][i], lo[t][ct][i]) * acc[t][ct][i];
+                        else s += hi[t][ct][i] * acc[t][ct][i];
                     }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s += hv[i] * acc[t][ct][i];
-                }
             s = row_sum16(s);
             s += __shfl_xor(s, 16, 64);
             s += __shfl_xor(s, 32, 64);
         }
         wave_meet(false);  // the previous chunk's tiles are no longer read
-        if (on && lane == 0) tots[w] = s;
         in.put(Ks, Qs, Xs, Ys, Sf, Mf, ecs, SW, true);
         wave_meet(false);
+        if (on && lane == 0) a.tot[(int64_t)(sl * waves + w) * a.ntab * H + e] = s * ecs[L - 1];
         if (c > 0) {
             in.load(a, row, h, c - 1, p0, SW, true);
             if (AHEAD && on) load_h(c - 1);
-        }
-        if (tid == 0) {
-            float v = 0.f;
-            for (int k2 = 0; k2 < waves; ++k2) v += tots[k2];
-            a.tot[(int64_t)sl * a.ntab * H + e] = v;
         }
         Sp<T> b2[2][CT];
         if (on) {
@@ -2039,9 +2092,22 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a, int waves) {
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
+            for (int i = 0; i < 4; ++i) {
+                const int t = it * 16 + 4 * q + i;
+                float dot = 0.f;  // D = u . e^{c_L - c} dh' K
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[it][ct][i] *= ews[it * 16 + 4 * q + i];
+                for (int ct = 0; ct < CT; ++ct) {
+                    v[it][ct][i] *= ews[t];
+                    float r = to_f(Xs[t * ldx + pw + ct * 16 + l16]);
+                    if (NT > 1 && t < n) {
+                        const int64_t o = ((t0 + t) * H + h) * P + p0 + pw + ct * 16 + l16;
+                        r += to_f(static_cast<const T*>(a.rlo)[o]) + to_f(static_cast<const T*>(a.rll)[o]);
+                    }
+                    dot += r * bts[t] * v[it][ct][i];
+                }
+                dot = row_sum16(dot);
+                if (l16 == 0) dots2[w * L + t] = dot;
+            }
 #pragma unroll
             for (int t = it / 2; t < 2; ++t) {
                 const Sp<T> mf = frag_tab<T, NT>(Mf, frag_up(it, t), lane);
@@ -2078,7 +2144,12 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a, int waves) {
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) v[it][ct] -= d[ct];
         }
-        // dX = beta z, its dot with X; the tiles leave through LDS (own columns)
+        // dX = beta z, its dot with e^c h K; the tiles leave through LDS (own columns)
+        f32x4 kh[4][CT];
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) kh[it][ct] = ld4(a.kh + kh_at<CT>(e, P, (p0 + pw) / (16 * CT), it, ct, lane));
 #pragma unroll
         for (int it = 0; it < 4; ++it)
 #pragma unroll
@@ -2089,12 +2160,16 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a, int waves) {
                 for (int ct = 0; ct < CT; ++ct) {
                     const int o = t * ldx + pw + ct * 16 + l16;
                     const float dxv = bts[t] * v[it][ct][i];
-                    dot += dxv * to_f(Xs[o]);
+                    dot += dxv * kh[it][ct][i];
                     Xs[o] = from_f<T>(dxv);
                     Ys[o] = from_f<T>(v[it][ct][i]);
-                    if (NT > 1 && t < n)
-                        static_cast<T*>(a.zlo)[((t0 + t) * H + h) * P + p0 + pw + ct * 16 + l16] =
-                            from_f<T>(v[it][ct][i] - to_f(Ys[o]));
+                    if (NT > 1 && t < n) {
+                        const int64_t zo = ((t0 + t) * H + h) * P + p0 + pw + ct * 16 + l16;
+                        const float rest = v[it][ct][i] - to_f(Ys[o]);
+                        const T z1 = from_f<T>(rest);
+                        static_cast<T*>(a.zlo)[zo] = z1;
+                        static_cast<T*>(a.zll)[zo] = from_f<T>(rest - to_f(z1));
+                    }
                     v[it][ct][i] = dxv;
                 }
                 dot = row_sum16(dot);
@@ -2154,9 +2229,14 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a, int waves) {
         store_rows(static_cast<T*>(a.dx) + (t0 * H + h) * P + p0, (int64_t)H * P, Xs, ldx, n, SW, tid, 256);
         store_rows(static_cast<T*>(a.z) + (t0 * H + h) * P + p0, (int64_t)H * P, Ys, ldx, n, SW, tid, 256);
         for (int t = tid; t < n; t += 256) {
-            float s = 0.f;
-            for (int k2 = 0; k2 < waves; ++k2) s += dots[k2 * L + t];
-            a.dxx[((int64_t)sl * BH + bh) * a.T + (int64_t)c * L + t] = s;
+            float f = 0.f, g = 0.f;
+            for (int k2 = 0; k2 < waves; ++k2) {
+                f += dots[k2 * L + t];
+                g += dots2[k2 * L + t];
+            }
+            const int64_t at = ((int64_t)sl * BH + bh) * a.T + (int64_t)c * L + t;
+            a.fk[at] = f;
+            a.dj[at] = g;
         }
     }
     if (a.dh0 && on) {
@@ -2434,41 +2514,261 @@ __global__ __launch_bounds__(256) void k_delta_sum(const float* __restrict__ par
     st4(v < all ? dB + v : dC + (v - all), o);
 }
 
-// k_delta_dt: ddt of one (chunk, head), a reverse running sum over its tokens (one per lane),
-// and the chunk's share of dA, in float64.
-template <int LANES = 64>
-__global__ __launch_bounds__(LANES) void k_delta_dt(Args a) {
-    const int lane = threadIdx.x, H = a.H, BH = a.rows.nrows * H;
-    const int h = (int)(blockIdx.x % (unsigned)H), kk = (int)(blockIdx.x / (unsigned)H);
-    const int64_t row = kk / a.nc;
-    const int64_t t = (int64_t)(kk % a.nc) * L + lane, e = (int64_t)kk * H + h, bh = row * H + h;
-    const bool on = t < a.T;
-    double v = 0.0, tot = 0.0;
-    for (int sl = 0; sl < a.slices; ++sl) {
-        const int64_t o = ((int64_t)sl * BH + bh) * a.T + (on ? t : 0);
-        if (on) v += (double)a.dyy[o] - (double)a.dxx[o];
-        tot += (double)a.tot[(int64_t)sl * a.ntab * H + e];
+// ---------------------------------------------------------------------------
+// k_delta_ddt: ddt of a chunk, and its share of dA, for `heads` heads of a group.  Wave w forms
+// E_ij of its token tile (i, columns) with the tiles j <= w: Q K^T and K K^T once for all heads,
+// dY r^T and z r^T per head, r and z in all their terms (two would leave ddt ten times its error).
+// The sum over the pairs around each token t is taken as it stands, never as a difference of
+// longer sums: pairs of a later tile's i by their j, summed over the earlier tokens at the end; the
+// tile's own by a product with ones below the diagonal (j < t) and a mask (i >= t).  The rest are
+// sums along the chunk, one token per lane, in float64.
+// Rows are fetched straight into LDS, W headdim columns (8 elements at a time exchanged by the
+// row's low bits), a head's while the sums of the one before are formed.  Bound by the latency of
+// these steps, two work-groups a CU: 2 rows of 2048 tokens, 48 heads of 64, dstate 128: 65 us, 35 for
+// its 0.18 GB at the copy rate.
+// ---------------------------------------------------------------------------
+// a 64 x W tile of rows `stride` bytes apart: instruction `m` of TileW<T, W>::RUNS
+template <typename T, int W>
+struct TileW {
+    static constexpr int ELEMS = L * W, RUNS = ELEMS * (int)sizeof(T) / 1024, BLOCKS = W / 8;
+    static __device__ __forceinline__ void fetch(brsrc r, T* dst, int stride, int so, int m, int lane) {
+        const int o = (m * 1024 + lane * 16) / (int)sizeof(T), row = o / W, col = o % W;
+        const int src = ((col >> 3) ^ (row & (BLOCKS - 1))) * 8 + (col & 7);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + m * (1024 / (int)sizeof(T))), 16,
+                                                 row * stride + src * (int)sizeof(T), so, 0, 0);
     }
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const double o = __shfl_down(v, off, 64);
-        if (lane + off < 64) v += o;
+    // operand of rows `row`, columns 32 k + 8 q on (past W: zero)
+    static __device__ __forceinline__ typename V8<T>::type frag(const T* tile, int row, int k, int q) {
+        const int b = 4 * k + q;
+        return sel8(W >= 32 || b < BLOCKS, ld8(tile + row * W + (((b & (BLOCKS - 1)) ^ (row & (BLOCKS - 1))) << 3)));
     }
-    v += tot;
-    const int64_t o = (row * a.T + (on ? t : 0)) * H + h;
-    if (on) a.ddt[o] = (float)(v * (double)a.A[h]);
-    double da = on ? v * (double)a.dt[o] : 0.0;
+};
+template <typename T, int W>
+struct DdtCfg {
+    static constexpr int TILES = 1 + 2 * kTerms<T>;  // dY, r, z
+    static constexpr int KEYS = 4 * L * 64;          // elements of two K and Q tiles (bfloat16; float32: one of each)
+    static constexpr int ROWS = TILES * TileW<T, W>::ELEMS;
+    static constexpr int ELEMS = ROWS > KEYS / (int)(sizeof(T) / 2) ? ROWS : KEYS / (int)(sizeof(T) / 2);
+};
+
+template <typename T, int W>
+__global__ __launch_bounds__(256, 2) void k_delta_ddt(Args a, int heads) {
+    constexpr int NT = kTerms<T>;
+    typedef TileW<T, W> TW;
+    typedef typename V8<T>::type F8;
+    __shared__ __attribute__((aligned(16))) T buf[DdtCfg<T, W>::ELEMS];
+    __shared__ __attribute__((aligned(16))) float pairs[2][4][L];
+    const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
+    const int H = a.H, G = a.G, P = a.P, N = a.N, Hg = H / G, nhb = (Hg + heads - 1) / heads;
+    unsigned id = xcd_range(blockIdx.x, gridDim.x);
+    const int hb = (int)(id % (unsigned)nhb);
+    id /= (unsigned)nhb;
+    const int g = (int)(id % (unsigned)G), kk = (int)(id / (unsigned)G);
+    const int row = kk / a.nc, c = kk - row * a.nc, BH = a.rows.nrows * H;
+    const int64_t t0 = (int64_t)row * a.T + (int64_t)c * L;
+    const int n = (int)min((int64_t)L, a.T - (int64_t)c * L);
+    const int i = w * 16 + l16;
+    constexpr int ES = (int)sizeof(T);
+
+    // (rows past the end read as zero)
+    const int rsx = H * P * ES, rsk = G * N * ES;
+    auto keys = [&](const void* p) {
+        return make_rsrc(static_cast<const T*>(p) + (t0 * G + g) * N, (uint32_t)((n - 1) * rsk + N * ES));
+    };
+    f32x4 qk[4], kd[4];  // Q_i . K_j, K_i . K_j: rows j, column i
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) da += __shfl_xor(da, off, 64);
-    if (lane == 0) a.dAp[e] = (float)da;
+    for (int j = 0; j < 4; ++j) qk[j] = kd[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    {
+        const brsrc kr = keys(a.B), qr = keys(a.C);
+        // PAIRS K and Q tiles of KW columns from column k0 on
+        auto products = [&](int k0, auto kw, auto np) {
+            constexpr int KW = decltype(kw)::value, NP = decltype(np)::value;
+            typedef TileW<T, KW> TK;
+            wave_meet(false);  // the tiles before are no longer read
+            for (int m = w; m < NP * 2 * TK::RUNS; m += 4) {
+                const int tile = m / TK::RUNS;
+                TK::fetch(tile & 1 ? qr : kr, buf + tile * TK::ELEMS, rsk, (k0 + (tile >> 1) * KW) * ES, m % TK::RUNS, lane);
+            }
+            wave_meet(true);
+#pragma unroll
+            for (int u = 0; u < NP; ++u)
+#pragma unroll
+                for (int k = 0; k < (KW + 31) / 32; ++k) {
+                    const T *kt = buf + 2 * u * TK::ELEMS, *qt = kt + TK::ELEMS;
+                    const F8 qi = TK::frag(qt, i, k, q), ki = TK::frag(kt, i, k, q);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j <= w) {
+                            const F8 kj = TK::frag(kt, j * 16 + l16, k, q);
+                            qk[j] = mma(qk[j], kj, qi);
+                            kd[j] = mma(kd[j], kj, ki);
+                        }
+                }
+        };
+        const std::integral_constant<int, 1> one;
+        const std::integral_constant<int, 64> k64;
+        if (N == 16) products(0, std::integral_constant<int, 16>(), one);
+        else if (N == 32) products(0, std::integral_constant<int, 32>(), one);
+        else if (NT == 1 || N == 64)
+            for (int k0 = 0; k0 < N; k0 += 64) products(k0, k64, one);
+        else if constexpr (NT > 1)
+            for (int k0 = 0; k0 < N; k0 += 128) products(k0, k64, std::integral_constant<int, 2>());
+    }
+    auto fetch = [&](int h, int k0) {
+        for (int m = w; m < DdtCfg<T, W>::TILES * TW::RUNS; m += 4) {
+            const int tile = m / TW::RUNS;
+            const void* p = tile == 0 ? a.dy : tile == 1 ? a.r : tile == 2 ? a.z : tile == 3 ? a.rlo
+                            : tile == 4 ? a.zlo : tile == 5 ? a.rll : a.zll;
+            const brsrc r = make_rsrc(static_cast<const T*>(p) + t0 * H * P, (uint32_t)(n * rsx));
+            TW::fetch(r, buf + tile * TW::ELEMS, rsx, (h * P + k0) * ES, m % TW::RUNS, lane);
+        }
+    };
+
+    const int h0 = g * Hg + hb * heads, h1 = min(g * Hg + Hg, h0 + heads);
+    wave_meet(false);  // the key tiles are no longer read
+    fetch(h0, 0);
+    for (int h = h0; h < h1; ++h) {
+        const int64_t e = (int64_t)kk * H + h;
+        const float* vec = a.vec + e * kVec;
+        f32x4 pa[4], wa[4];  // dY_i . r_j, z_i . r_j
+#pragma unroll
+        for (int j = 0; j < 4; ++j) pa[j] = wa[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        // (asked for before the next tiles are: loads return in order)
+        const float bi = vec[2 * L + i], ci = vec[3 * L + i], di = vec[4 * L + i];
+        f32x4 bo[4], co[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j <= w) {
+                const float* vj = vec + j * 16 + 4 * q;
+                bo[j] = ld4(vj + 2 * L);
+                co[j] = ld4(vj + 3 * L);
+                lo[j] = ld4(vj + 4 * L);
+            }
+        // one wave finishes the head; its sums along the chunk, while the tiles come
+        const bool last = w == ((h - h0) & 3), on = lane < n;
+        const int64_t to = (t0 + (on ? lane : 0)) * H + h;
+        double v = 0.0, dtv = 0.0;
+        if (last) {
+            const int64_t at = ((int64_t)row * H + h) * a.T + (int64_t)c * L + lane;
+            double f = 0.0, d = 0.0;
+            if (lane < a.tots) v = (double)a.tot[(int64_t)lane * a.ntab * H + e];
+            dtv = (double)a.dt[to];
+            for (int s0 = 0; s0 < a.slices; s0 += 4) {  // (a load that waits for the one before costs 1 us)
+                float x[4], y[4], z[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int64_t o = (int64_t)min(s0 + k, a.slices - 1) * BH * a.T + (on ? at : at - lane);
+                    x[k] = a.fq[o];
+                    y[k] = a.fk[o];
+                    z[k] = a.dj[o];
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (on && s0 + k < a.slices) {
+                        f += (double)x[k] - (double)y[k];
+                        d += (double)z[k];
+                    }
+            }
+#pragma unroll
+            for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+            d = __shfl_up(d, 1, 64);
+            if (lane == 0) d = 0.0;
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                const double o = __shfl_down(f, off, 64), p = __shfl_up(d, off, 64);
+                if (lane + off < 64) f += o;
+                if (lane >= off) d += p;
+            }
+            v += f + d;
+        }
+        for (int k0 = 0; k0 < P; k0 += W) {
+            wave_meet(true);  // the tiles have landed
+            auto tile = [&](int k) { return buf + k * TW::ELEMS; };  // dY, r, z, then the further terms of r and z
+#pragma unroll
+            for (int k = 0; k < (W + 31) / 32; ++k) {
+                const F8 yi = TW::frag(tile(0), i, k, q);
+                F8 zi[NT];
+#pragma unroll
+                for (int m = 0; m < NT; ++m) zi[m] = TW::frag(tile(2 + 2 * m), i, k, q);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j <= w)
+#pragma unroll
+                        for (int m = 0; m < NT; ++m) {
+                            const F8 rj = TW::frag(tile(1 + 2 * m), j * 16 + l16, k, q);
+                            pa[j] = mma(pa[j], rj, yi);
+#pragma unroll
+                            for (int o = 0; o < NT - m; ++o) wa[j] = mma(wa[j], rj, zi[o]);
+                        }
+            }
+            wave_meet(false);  // and are no longer read
+            if (k0 + W < P) fetch(h, k0 + W);
+            else if (h + 1 < h1) fetch(h + 1, 0);
+        }
+        float(*pr)[L] = pairs[(h - h0) & 1];
+        // of four rows' sums, that of this lane's row
+        auto own_row = [&](f32x4 v) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = row_sum16(v[r]);
+            return l16 & 2 ? (l16 & 1 ? v[3] : v[2]) : (l16 & 1 ? v[1] : v[0]);
+        };
+        f32x4 es = f32x4{0.f, 0.f, 0.f, 0.f}, ed = es;  // E of the tiles before w, added up; of the diagonal tile
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j <= w) {
+                f32x4 ev;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float gam = exp2f_fast((ci - co[j][r]) + (di - lo[j][r]));
+                    ev[r] = j < w || 4 * q + r < l16 ? gam * bo[j][r] * (pa[j][r] * qk[j][r] - bi * wa[j][r] * kd[j][r]) : 0.f;
+                }
+                if (j == w) {
+                    ed = ev;
+                } else {
+                    es += ev;
+                    const float s = own_row(ev);
+                    if (l16 < 4) pr[w][j * 16 + 4 * q + l16] = s;
+                }
+            }
+        const f32x4 one = f32x4{1.f, 1.f, 1.f, 1.f};
+        f32x4 below, m;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) below[r] = 4 * q + r < l16 ? 1.f : 0.f;
+        m = mma16(mma16(f32x4{0.f, 0.f, 0.f, 0.f}, one, es), below, ed);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m[r] = l16 >= 4 * q + r ? m[r] : 0.f;
+        const float s = own_row(m);
+        if (l16 < 4) pr[w][w * 16 + 4 * q + l16] = s;
+        wave_meet(false);
+        if (!last) continue;
+        // the pairs by j: within its tile over the tokens before this one, and the tiles before
+        // (sums of 16 in float32)
+        const float c1 = lane < 16 ? pr[1][lane] : 0.f, c2 = lane < 32 ? pr[2][lane] : 0.f, c3 = lane < 48 ? pr[3][lane] : 0.f;
+        float x = c1 + c2 + c3;
+        const float s2 = row_sum16(c2), s3 = row_sum16(c3);
+        x = row_shift<1>(x);
+        x += row_shift<1>(x);
+        x += row_shift<2>(x);
+        x += row_shift<4>(x);
+        x += row_shift<8>(x);
+        const float s20 = __shfl(s2, 0, 64), s30 = __shfl(s3, 0, 64), s31 = __shfl(s3, 16, 64);
+        v += (double)pr[lane >> 4][lane] + (double)x;
+        if ((lane >> 4) == 1) v += (double)s20 + (double)s30;
+        if ((lane >> 4) == 2) v += (double)s30 + (double)s31;
+        if (on) a.ddt[to] = (float)(v * (double)a.A[h]);
+        double da = on ? v * dtv : 0.0;
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) da += __shfl_xor(da, off, 64);
+        if (lane == 0) a.dAp[e] = da;
+    }
 }
 // dA_h over the chunks, in order
 template <int BLOCK = 64>
-__global__ __launch_bounds__(BLOCK) void k_delta_dA(const float* __restrict__ p, float* __restrict__ dA, int ntab,
+__global__ __launch_bounds__(BLOCK) void k_delta_dA(const double* __restrict__ p, float* __restrict__ dA, int ntab,
                                                     int H) {
     const int h = blockIdx.x;
     double s = 0.0;
-    for (int v = threadIdx.x; v < ntab; v += BLOCK) s += (double)p[(int64_t)v * H + h];
+    for (int v = threadIdx.x; v < ntab; v += BLOCK) s += p[(int64_t)v * H + h];
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
     if (threadIdx.x == 0) dA[h] = (float)s;

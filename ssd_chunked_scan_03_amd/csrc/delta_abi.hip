@@ -35,11 +35,11 @@ int check_delta(const ssd_problem* p, bool packed) {
 }
 
 // Workspace: S, M and the decay factors of every (chunk, head); the packed row map; for the
-// backward also the residuals, the adjoint's z, the entering states and adjoints of every
-// chunk, the last state and the partial sums.
+// backward also the residuals, the adjoint's z, e^c K h^T, the entering states and adjoints of
+// every chunk and the partial sums.
 struct Layout {
-    size_t tab, vec, ts, kb, order, r, rlo, z, zlo, hin, hlo, lin, hend, dyy, dxx, tot, dAp, part, total;
-    int64_t ntab, slices, nsub;
+    size_t tab, vec, ts, kb, order, r, rlo, rll, z, zlo, zll, kh, hin, hlo, lin, fq, fk, dj, tot, dAp, part, total;
+    int64_t ntab, slices, tots, nsub;
 };
 
 Layout layout_of(const ssd_problem* p, bool packed, bool bwd) {
@@ -65,21 +65,19 @@ Layout layout_of(const ssd_problem* p, bool packed, bool bwd) {
     }
     if (bwd) {
         o.slices = ssd::delta::bwd_slices(p->dtype == SSD_BF16, b * H, P, N);
+        o.tots = ssd::delta::bwd_tots(p->dtype == SSD_BF16, b * H, P, N);
         o.nsub = ssd::delta::grad_shares(o.ntab, H, G, N);
         take(o.r, (size_t)(b * T * H * P) * es);
         take(o.z, (size_t)(b * T * H * P) * es);
-        if (es == 2) {
-            take(o.rlo, (size_t)(b * T * H * P) * es);
-            take(o.zlo, (size_t)(b * T * H * P) * es);
-        }
+        if (es == 2)
+            for (size_t* at : {&o.rlo, &o.zlo, &o.rll, &o.zll}) take(*at, (size_t)(b * T * H * P) * es);
+        take(o.kh, (size_t)(o.ntab * H * ssd::delta::L * P) * 4);
         take(o.hin, (size_t)(o.ntab * H * P * N) * es);
         if (es == 2) take(o.hlo, (size_t)(o.ntab * H * P * N) * 2);
         take(o.lin, (size_t)(o.ntab * H * P * N) * es);
-        take(o.hend, (size_t)(b * H * P * N) * 4);
-        take(o.dyy, (size_t)(o.slices * b * H * T) * 4);
-        take(o.dxx, (size_t)(o.slices * b * H * T) * 4);
-        take(o.tot, (size_t)(o.slices * o.ntab * H) * 4);
-        take(o.dAp, (size_t)(o.ntab * H) * 4);
+        for (size_t* at : {&o.fq, &o.fk, &o.dj}) take(*at, (size_t)(o.slices * b * H * T) * 4);
+        take(o.tot, (size_t)(o.tots * o.ntab * H) * 4);
+        take(o.dAp, (size_t)(o.ntab * H) * 8);
         if (o.nsub > 1) take(o.part, (size_t)(o.nsub * 2 * b * T * G * N) * 4);
     }
     o.total = (b == 0 || T == 0) ? 0 : off;
@@ -214,18 +212,22 @@ int delta_bwd(const ssd_problem* p, const void* x, const float* dt, const float*
     a.dx = dx; a.ddt = ddt; a.dA = dA; a.dB = dB; a.dC = dC; a.dbeta = dbeta; a.dh0 = dh0;
     a.r = w + o.r;
     a.rlo = w + o.rlo;
+    a.rll = w + o.rll;
     a.z = w + o.z;
     a.zlo = w + o.zlo;
+    a.zll = w + o.zll;
+    a.kh = reinterpret_cast<float*>(w + o.kh);
     a.hin = w + o.hin;
     a.lin = w + o.lin;
     a.hlo = reinterpret_cast<short*>(w + o.hlo);
-    a.hend = reinterpret_cast<float*>(w + o.hend);
-    a.dyy = reinterpret_cast<float*>(w + o.dyy);
-    a.dxx = reinterpret_cast<float*>(w + o.dxx);
+    a.fq = reinterpret_cast<float*>(w + o.fq);
+    a.fk = reinterpret_cast<float*>(w + o.fk);
+    a.dj = reinterpret_cast<float*>(w + o.dj);
     a.tot = reinterpret_cast<float*>(w + o.tot);
-    a.dAp = reinterpret_cast<float*>(w + o.dAp);
+    a.dAp = reinterpret_cast<double*>(w + o.dAp);
     a.part = o.nsub > 1 ? reinterpret_cast<float*>(w + o.part) : nullptr;
     a.slices = (int)o.slices;
+    a.tots = (int)o.tots;
     a.nsub = (int)o.nsub;
     return p->dtype == SSD_BF16 ? ssd::delta::run_bf16(a, true) : ssd::delta::run_f32(a, true);
 }

@@ -5,8 +5,9 @@ import pytest
 import torch
 
 import delta_ref as ref
+from delta_decay_ref import decay_gradients
 import ssd_chunked_scan_03_amd as ssd
-from test_gpu_delta import check_backward, check_forward, forward
+from test_gpu_delta import F32, backward, check_backward, check_forward, forward
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +88,55 @@ def test_a_nan_stays_where_the_formulas_take_it(case, which):
         state[:, heads, cols] = True
         assert torch.isnan(hT[state]).all()
     assert torch.equal(hT[~state], h0[~state])
+
+
+def strong(case, seed, lo, hi, A):
+    b, T, H, P, N, G, dtype = case
+    d, gr = ref.make(b, T, H, P, N, G, seed, dtype), ref.make_grads(b, T, H, P, N, seed, dtype)
+    g = torch.Generator().manual_seed(seed)
+    d["dt"] = lo + (hi - lo) * torch.rand(b, T, H, generator=g)
+    if A is not None:
+        d["A"] = torch.full((H,), A)
+    return d, gr
+
+
+def check_decay_gradients(d, gr, where):
+    """Every token's ddt to F32 of its own absolute terms, every head's dA to F32 of theirs: each
+    term is a product of float32 values (in bfloat16 problems sums of three terms) with its decay,
+    whose exponent of up to 2^7 is good to 2^-18.  What is left of a state under float32's smallest
+    number is nothing."""
+    print(f"[delta decay gradients] {where}", flush=True)
+    out = backward(d, gr)
+    ddt, dA, s = decay_gradients(d, gr)
+    lim = F32 * s * d["A"].abs().double() + 1e-30
+    worst = ((out["ddt"].double().cpu() - ddt).abs() / lim).max().item()
+    limA = F32 * (s * d["dt"].double()).sum((0, 1)) + 1e-30
+    worstA = ((out["dA"].double().cpu() - dA).abs() / limA).max().item()
+    assert worst <= 1.0 and worstA <= 1.0, (where, worst, worstA)
+
+
+@pytest.mark.parametrize("span", [(0.0, 0.1, None), (0.5, 1.0, -8.0), (1.0, 4.0, -8.0), (0.0, 30.0, None)],
+                         ids=lambda s: "dt{}to{}A{}".format(*s))
+@pytest.mark.parametrize("case", SHAPES, ids=lambda c: NAME.format(*c))
+def test_gradients_of_strong_decays(case, span):
+    """Little of a state outlives a token (e^-8 to e^-32 of it, or nothing), and the gradient of its
+    decay is as small: it has to come from terms that carry that factor."""
+    check_decay_gradients(*strong(case, 52, *span), (case, span))
+
+
+@pytest.mark.parametrize("at", [0, 20, 63, 64])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradients_around_a_gate(at, dtype):
+    """One token that forgets everything among weak ones: no term reaches across it, and its own
+    dt of 3000 / |A| multiplies into dA whatever it is given."""
+    case = (1, 128, 2, 32, 64, 1, dtype)
+    d, gr = strong(case, 53, 0.0, 1e-3, None)
+    d["dt"][:, at] = 3000.0 / d["A"].abs()
+    check_decay_gradients(d, gr, (case, at))
+
+
+@pytest.mark.parametrize("case", [(16, 380, 65, 16, 16, 1, "bf16"), (8, 390, 65, 16, 32, 1, "f32"), (96, 20, 32, 128, 16, 1, "bf16"),
+                                  (24, 130, 48, 64, 16, 2, "bf16")], ids=lambda c: NAME.format(*c))
+def test_gradients_of_strong_decays_of_many_heads(case):
+    """Enough heads and chunks that a work-group takes several heads (the last one of a group alone)."""
+    check_decay_gradients(*strong(case, 55, 0.0, 1.0, None), case)
