@@ -21,7 +21,6 @@
 namespace ssd {
 namespace bcnorm {
 
-constexpr int kMaxF = 128;      // pairs per row at dstate 256
 constexpr int kDwGroups = 1024;  // most work-groups of the backward (rows of its partial sums)
 
 struct Args {
@@ -118,7 +117,6 @@ __device__ __forceinline__ void turn(float (&v)[VPL], const float* cs, int F, in
     }
 }
 
-template <int VPL>
 __device__ __forceinline__ float row_sum(float s, int R) {
     for (int off = R >> 1; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
     return s;
@@ -131,7 +129,7 @@ __device__ __forceinline__ float row_root(float (&v)[VPL], int R, float scale, f
     float s = 0.f;
 #pragma unroll
     for (int e = 0; e < VPL; ++e) s += v[e] * v[e];
-    s = row_sum<VPL>(s, R);
+    s = row_sum(s, R);
     float r = 1.f / sqrtf(s * scale + eps);
     const bool over = s > 3.4028235e38f;
     k = 1.f;
@@ -143,7 +141,7 @@ __device__ __forceinline__ float row_root(float (&v)[VPL], int R, float scale, f
             v[e] *= k;
             s += v[e] * v[e];
         }
-        s = row_sum<VPL>(s, R);
+        s = row_sum(s, R);
         if (over) r = 1.f / sqrtf(s * scale);
     }
     return r;
@@ -233,7 +231,7 @@ __global__ __launch_bounds__(256) void k_bc_norm_bwd(Args a) {
                 x[e] = xr;
                 d += xr * g[e];
             }
-            d = row_sum<VPL>(d, R) * scale;
+            d = row_sum(d, R) * scale;
 #pragma unroll
             for (int e = 0; e < VPL; ++e) g[e] = r * k * (g[e] - x[e] * d);
             if (on) store_row<T, VPL>(static_cast<T*>(isB ? a.dB : a.dC) + o + n0, g);

@@ -557,9 +557,11 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(Args a, int heads) {
                 float* vec = a.vec + e0 * kVec;
                 vec[lane] = ec;
                 vec[L + lane] = ew;
-                vec[2 * L + lane] = b;
-                vec[3 * L + lane] = hi;
-                vec[4 * L + lane] = lo;
+                if (a.ddt) {  // (the backward's)
+                    vec[2 * L + lane] = b;
+                    vec[3 * L + lane] = hi;
+                    vec[4 * L + lane] = lo;
+                }
             }
             m.bet[lane] = b;
             m.chi[lane] = hi;
