@@ -6,27 +6,24 @@
 namespace ssd {
 namespace delta {
 
-// Columns of headdim one work-group of the chunk walks takes: waves of 16 CT columns.  Two
-// column tiles per wave read each table and key fragment once for both (bfloat16, where the
-// state's accumulators leave the registers for it); as many waves as P allows, up to 4.
-struct Slice {
-    int ct, waves;
-    int cols() const { return 16 * ct * waves; }
-};
-inline Slice slice_of(bool bf16_dtype, int64_t bh, int64_t P, int64_t N) {
-    Slice s;
-    s.ct = bf16_dtype && N <= 128 && P >= 32 ? 2 : 1;
-    s.waves = (int)(P / (16 * s.ct));
-    if (s.waves > 4) s.waves = 4;
-    while (s.waves > 1 && bh * (P / s.cols()) < 256) s.waves >>= 1;
-    return s;
+// Waves of a work-group of k_delta and k_delta_rev, 16 columns of headdim each: as many as P allows, up
+// to 4, and fewer while that leaves CUs without a work-group (float32, dstate 64, 512 tokens, 8 heads of
+// 64: forward 78 us with one wave, 81 with four; backward 199, 211).
+inline int walk_waves(int64_t bh, int64_t P) {
+    int w = (int)(P / 16);
+    if (w > 4) w = 4;
+    while (w > 1 && bh * (P / (16 * w)) < 256) w >>= 1;
+    return w;
 }
 
-// Shares of a group's heads in the gradient kernel: enough work-groups for every CU several
-// times over, each summing as many heads in registers as that leaves.
+// Shares of a group's heads in the gradient kernel: enough work-groups for every CU twice over, each
+// summing as many heads in registers as that leaves.  Backward with 256 / 512 / 1024 / 2048 work-groups
+// at least (us): 2 rows of 2048 tokens, 48 heads of 64, dstate 128: 556 / 509 / 520 / 535; one row of 4096,
+// 128 heads: 1237 / 1111 / 1122 / 1135; one row of 2048, 32 heads of 128, dstate 256, 2 groups: 490 / 438 / 448
+// / 467.
 inline int grad_shares(int64_t chunks, int64_t H, int64_t G, int64_t N) {
     const int64_t base = chunks * G * (N > 64 ? N / 64 : 1), hg = H / G;
-    int64_t s = (1024 + base - 1) / (base > 0 ? base : 1);
+    int64_t s = (512 + base - 1) / (base > 0 ? base : 1);
     return (int)(s < 1 ? 1 : s > hg ? hg : s);
 }
 
@@ -43,10 +40,10 @@ inline bool dma_walk(bool bf16_dtype, int64_t N);
 inline int team_tiles(int64_t bh, int64_t P, int64_t N);
 // Slices of headdim that the backward's walks write partial sums for, per token and (waves) per state.
 inline int64_t bwd_slices(bool bf16_dtype, int64_t bh, int64_t P, int64_t N) {
-    return P / (dma_walk(bf16_dtype, N) ? 16 * team_tiles(bh, P, N) : slice_of(bf16_dtype, bh, P, N).cols());
+    return P / (16 * (dma_walk(bf16_dtype, N) ? team_tiles(bh, P, N) : walk_waves(bh, P)));
 }
 inline int64_t bwd_tots(bool bf16_dtype, int64_t bh, int64_t P, int64_t N) {
-    return bwd_slices(bf16_dtype, bh, P, N) * (dma_walk(bf16_dtype, N) ? 4 : slice_of(bf16_dtype, bh, P, N).waves);
+    return dma_walk(bf16_dtype, N) ? 4 * bwd_slices(bf16_dtype, bh, P, N) : P / 16;
 }
 
 template <typename K>
@@ -55,43 +52,37 @@ bool lds_limit(K* kernel, size_t bytes) {
                                                      (int)bytes) == hipSuccess;
 }
 
-template <typename T, int N, int CT>
-int walk(const Args& a, int waves, int which) {
+template <typename T, int N>
+int walk(const Args& a, int which) {
     typedef Cfg<T, N> CF;
-    const int sw = 16 * CT * waves;
+    const int waves = walk_waves((int64_t)a.rows.nrows * a.H, a.P), sw = 16 * waves;
     const unsigned grid = (unsigned)((int64_t)a.rows.nrows * a.H * (a.P / sw));
     if (which == 0) {
         const size_t lds = CF::walk_bytes(sw, CF::NT > 1 ? 2 : 1, 1);
-        if (!lds_limit(k_delta<T, N, CT, false>, lds)) return 7;
-        k_delta<T, N, CT, false><<<grid, 256, lds, a.stream>>>(a, waves);
+        if (!lds_limit(k_delta<T, N, false>, lds)) return 7;
+        k_delta<T, N, false><<<grid, 256, lds, a.stream>>>(a, waves);
     } else if (which == 1) {
         const size_t lds = CF::walk_bytes(sw, 0, 2);
-        if (!lds_limit(k_delta<T, N, CT, true>, lds)) return 7;
-        k_delta<T, N, CT, true><<<grid, 256, lds, a.stream>>>(a, waves);
+        if (!lds_limit(k_delta<T, N, true>, lds)) return 7;
+        k_delta<T, N, true><<<grid, 256, lds, a.stream>>>(a, waves);
     } else {
         const size_t lds = CF::walk_bytes(sw, CF::NT, 2);
-        if (!lds_limit(k_delta_rev<T, N, CT>, lds)) return 7;
-        k_delta_rev<T, N, CT><<<grid, 256, lds, a.stream>>>(a, waves);
+        if (!lds_limit(k_delta_rev<T, N>, lds)) return 7;
+        k_delta_rev<T, N><<<grid, 256, lds, a.stream>>>(a, waves);
     }
     return hipGetLastError() == hipSuccess ? 0 : 7;
-}
-
-template <typename T, int N>
-int walk_n(const Args& a, const Slice& s, int which) {
-    if constexpr (std::is_same<T, bf16>::value && N <= 128) {
-        if (s.ct == 2) return walk<T, N, 2>(a, s.waves, which);
-    }
-    return walk<T, N, 1>(a, s.waves, which);
 }
 
 // Whether the walks run on tables stored as fragments (k_delta_dma, k_delta_team, k_delta_adj).
 inline bool dma_walk(bool bf16_dtype, int64_t N) { return bf16_dtype && N >= 64; }
 
-// Heads of a group that one wave of the preparation takes, sharing their K K^T and Q K^T: up
-// to 4 while that leaves 8 waves per SIMD.
+// Heads of a group that one wave of the preparation takes, sharing their K K^T and Q K^T: up to 4
+// while that leaves four waves per SIMD.  Forward with 1 / 2 / 4 (us), 80 heads of 64, dstate 128: 8 rows of
+// 4096 tokens (10240 waves with 4) 974 / 900 / 878, of 1024 (5120 with 2) 293 / 269 / 276; one row of 2048 tokens, 32
+// heads (1024 with 1) 77 / 84 / 93.
 inline int prep_heads(int64_t ntab, int64_t H, int64_t G) {
     int s = 4;
-    while (s > 1 && (s > H / G || ntab * G * ((H / G + s - 1) / s) < 8192)) s >>= 1;
+    while (s > 1 && (s > H / G || ntab * G * ((H / G + s - 1) / s) < 4096)) s >>= 1;
     return s;
 }
 template <typename T, int N, Tab TAB>
@@ -108,7 +99,9 @@ int walk_dma(const Args& a, int waves) {
     return hipGetLastError() == hipSuccess ? 0 : 7;
 }
 // Column tiles per team: one, or two where that still gives every CU a team (the key and table
-// fragments are then read once for both; at dstate 256 LDS leaves no room).
+// fragments are then read once for both; at dstate 256 LDS leaves no room).  2048 tokens, one / two tiles
+// (us), headdim 64, dstate 128: 64 heads forward 89 / 107, backward 367 / 435; 96 heads 151 / 118, 623 / 519;
+// headdim 32: 128 heads 98 / 120, 429 / 491; 192 heads 165 / 135, 719 / 606.
 inline int team_tiles(int64_t bh, int64_t P, int64_t N) { return N <= 128 && P >= 32 && bh * P > 256 * 16 ? 2 : 1; }
 template <int N, int CT, bool SAVE>
 int walk_team(const Args& a) {
@@ -125,15 +118,15 @@ int walks_bwd(const Args& a) {
     k_delta_adj<N, CT, N == 256 ? 1 : 2><<<grid, 256, 0, a.stream>>>(a);
     return hipGetLastError() == hipSuccess ? 0 : 7;
 }
-// Teams while each has a CU of its own, and at any number of chains where a head is too narrow for
-// a work-group of four waves to share its tables; else a wave per 16 columns.  Forward of 2048
-// tokens, whole call (us, team / wave; M then in one term): headdim 64, dstate 128: 32 heads
-// 67 / 127, 128 heads 121 / 153, 192 heads 213 / 172, 768 heads 657 / 493; headdim 64, dstate 256:
-// 64 heads 114 / 201, 96 heads 202 / 216, 192 heads 313 / 254; headdim 32, dstate 128: 256 heads
-// 154 / 182, 768 heads 418 / 406; headdim 32, dstate 256: 256 heads 259 / 271, 768 heads 670 / 719;
-// headdim 16, 768 heads: dstate 128 342 / 347, dstate 256 440 / 800.
+// Teams while there are at most two column tiles a CU, and at any number of chains where a head is too
+// narrow for a work-group of four waves to share its tables; else a wave per 16 columns.  Forward of
+// 2048 tokens, whole call (us, team / wave): headdim 64, dstate 128: 32 heads 78 / 137, 128 heads 125 / 157, 192
+// heads 214 / 177, 768 heads 653 / 515; dstate 256: 64 heads 116 / 205, 128 heads 219 / 228, 192 heads 319 / 256;
+// headdim 128, dstate 128: 64 heads 105 / 145, 96 heads 191 / 157; headdim 32, dstate 128: 256 heads 158 / 188,
+// 768 heads 425 / 430, 1536 heads 805 / 774; dstate 256: 256 heads 258 / 279, 1536 heads 1274 / 1376; headdim 16:
+// 1536 heads, dstate 128 631 / 712, dstate 256 795 / 1582.
 inline bool team_walk(int64_t bh, int64_t P, int64_t N) {
-    return P < (N <= 128 ? 32 : 64) || bh * P <= 256 * 16 * (N <= 128 ? 2 : 1);
+    return P < (N <= 128 ? 32 : 64) || bh * P <= 2 * 256 * 16;
 }
 
 template <typename T, int N>
@@ -153,9 +146,8 @@ int run_fwd(const Args& a) {
         // us against 260, the 2.7B layer shape 879 against 885); one at 256.
         return walk_dma<N, N <= 64 ? 1 : 2, N <= 64 ? 3 : N <= 128 ? 2 : 1>(a, waves);
     } else {
-        const Slice s = slice_of(std::is_same<T, bf16>::value, (int64_t)a.rows.nrows * a.H, a.P, N);
         prep<T, N, kPlain>(a);
-        return walk_n<T, N>(a, s, 0);
+        return walk<T, N>(a, 0);
     }
 }
 
@@ -180,10 +172,9 @@ int run_bwd(const Args& a) {
             st = walks_bwd<N, 1>(a);
         }
     } else {
-        const Slice s = slice_of(std::is_same<T, bf16>::value, (int64_t)a.rows.nrows * a.H, a.P, N);
         prep<T, N, kPlain>(a);
-        st = walk_n<T, N>(a, s, 1);
-        if (!st) st = walk_n<T, N>(a, s, 2);
+        st = walk<T, N>(a, 1);
+        if (!st) st = walk<T, N>(a, 2);
     }
     if (st) return st;
     const size_t lds = GC::BYTES;

@@ -7,6 +7,7 @@ import torch
 import delta_ref as ref
 from delta_decay_ref import decay_gradients
 import ssd_chunked_scan_03_amd as ssd
+import test_gpu_delta as base
 from test_gpu_delta import F32, backward, check_backward, check_forward, forward
 
 pytestmark = pytest.mark.gpu
@@ -140,3 +141,25 @@ def test_gradients_around_a_gate(at, dtype):
 def test_gradients_of_strong_decays_of_many_heads(case):
     """Enough heads and chunks that a work-group takes several heads (the last one of a group alone)."""
     check_decay_gradients(*strong(case, 55, 0.0, 1.0, None), case)
+
+
+@pytest.mark.parametrize("case", [(1, 130, 160, 64, 256, 8, "bf16"), (1, 70, 80, 128, 256, 5, "bf16")], ids=lambda c: NAME.format(*c))
+def test_dstate_256_with_many_chains(case):
+    """A wave per 16 columns at the widest state."""
+    b, T, H, P, N, G, dtype = case
+    check_forward(ref.make(b, T, H, P, N, G, 57, dtype), dtype, case)
+
+
+def test_packed_dstate_256_with_many_chains():
+    base.test_packed_sequences([70, 0, 129], (64, 64, 256, 2), "bf16")
+
+
+@pytest.mark.parametrize("case", [(64, 9, 129, 16, 64, 1, "bf16"), (128, 9, 131, 16, 16, 1, "bf16"), (64, 9, 129, 16, 16, 1, "f32"),
+                                  (128, 5, 131, 16, 64, 1, "bf16")], ids=lambda c: NAME.format(*c))
+def test_tables_of_several_heads_a_wave(case):
+    """Enough heads and chunks that a wave of the preparation takes two or four heads, the last one of
+    a group fewer."""
+    b, T, H, P, N, G, dtype = case
+    d = ref.make(b, T, H, P, N, G, 58, dtype)
+    check_forward(d, dtype, case)
+    check_backward(d, ref.make_grads(b, T, H, P, N, 58, dtype), dtype, case)
