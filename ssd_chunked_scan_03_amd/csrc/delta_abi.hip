@@ -305,9 +305,11 @@ ssd::bcnorm::Args norm_args(const ssd_norm* p, void* stream) {
     a.eps = p->eps;
     a.l2 = p->mode == SSD_NORM_L2;
     a.interleaved = p->interleaved;
-    // tokens per work-group: one while that already fills the GPU with work-groups or less;
-    // from 4096 tokens four, so that a token's angles and a work-group's start cost less
-    a.tok = a.tokens >= 4096 ? 4 : 1;
+    // tokens per work-group: one while that already fills the GPU with work-groups or less; from 2048
+    // tokens four, so that a token's angles and a work-group's start cost less (one / four, us, 16 + 16
+    // heads of 128: 512 tokens 8.6 / 13.9, 2048 tokens 21.9 / 17.8, backward 27.8 / 26.6, 32768 tokens 253 / 149,
+    // 208 / 199; 1 + 1 heads: 512 tokens 7.1 / 5.3, 2048 tokens 18.3 / 7.2, 21.4 / 12.7)
+    a.tok = a.tokens >= 2048 ? 4 : 1;
     a.groups = (int)((a.tokens + a.tok - 1) / a.tok);
     if (a.groups > ssd::bcnorm::kDwGroups) a.groups = ssd::bcnorm::kDwGroups;
     a.stream = (hipStream_t)stream;
