@@ -12,8 +12,8 @@
 // other half one shuffle away.  A work-group takes TOK tokens, so each token's cosines and
 // sines (the angle and its reduction in float64: a float32 product is off by 0.06 radian at
 // position 10^6) are formed once for all of its heads.  Bound by HBM: every element is read
-// and written once.  8 rows of 4096 tokens, 16 heads each of 128, bfloat16: 127 us for 0.54 GB, 4.2
-// TB/s; backward 173 us for 0.81 GB, 4.65 TB/s (a large copy reaches 5.1).
+// and written once.  8 rows of 4096 tokens, 16 heads each of 128, bfloat16: 130 us for 0.54 GB, 4.1
+// TB/s; backward 176 us for 0.81 GB, 4.6 TB/s (a large copy reaches 5.1).
 #pragma once
 
 #include "device.hpp"

@@ -467,7 +467,8 @@ __device__ __forceinline__ void order_rows(const Rows& rows, int* order, int lan
 // TAB: float32 blocks, or the operand fragments that the forward's or the backward's
 // fragment walks read.
 // Bound by the tables' way to memory: 26 KB per (chunk, head) forward (bfloat16, dstate 64 and
-// up), 31 KB backward; 40960 of them (8 rows of 4096 tokens, 80 heads) in 264 us, 4.1 TB/s.
+// up), 31 KB backward; 40960 of them (8 rows of 4096 tokens, 80 heads) in 216 to 279 us (the clock
+// gives way), 4.9 to 3.8 TB/s.
 // Small problems wait for the substitution's chain instead (16 us).
 // ---------------------------------------------------------------------------
 struct PrepLds {
@@ -1024,8 +1025,9 @@ __global__ __launch_bounds__(256) void k_delta(Args a, int waves) {
 // and the two K buffers are named at compile time (chunks in pairs), so the compiler knows
 // which reads a transfer in flight does not concern and does not wait for it there.
 // Bound by issue and the tables: 8 rows of 4096 tokens, 80 heads of 64, dstate 128, one group, take
-// 0.66 to 0.75 ms (the clock gives way); matrix instructions are half of the issued cycles, the
-// splitting into terms most of the rest; x and y alone would take 0.13 ms, with the tables 0.34.
+// 0.64 to 0.79 ms (the clock gives way); the matrix cores are busy for 46% of the cycles, and other
+// vector instructions, most of them the splitting into terms, issue in 41%; x and y alone would take
+// 0.13 ms, with the tables 0.34.
 // ---------------------------------------------------------------------------
 template <int N>
 struct Dma {
@@ -2259,7 +2261,7 @@ __global__ __launch_bounds__(256) void k_delta_rev(Args a, int waves) {
 // w as the COLUMNS of dQ^T[n][i] and dK^T[n][i], so the 64 x 64 gradient tables it needs,
 // dP^T and the two sides of W, come out of the matrix cores in the layout their products
 // read.  Rows pass through LDS 32 headdim columns at a time, asked for a step ahead.  2 rows of
-// 2048 tokens, 48 heads of 64, dstate 128, one group: 107 us for 0.33 GB (0.07 ms at copy rate;
+// 2048 tokens, 48 heads of 64, dstate 128, one group: 106 us for 0.26 GB (0.05 ms at copy rate;
 // every wave fetching its own fragments took 171).  Everything here ends in the problem dtype: the states enter with one bfloat16
 // term, r, z and the tables with two, so that every product has one rounded factor at most.
 // ---------------------------------------------------------------------------
@@ -2783,7 +2785,8 @@ __global__ __launch_bounds__(BLOCK) void k_delta_dA(const double* __restrict__ p
 // k_delta_step: the recurrence token by token on a held state, in place, all in float32.
 // One thread owns 8 consecutive elements of a state row p; the N / 8 lanes of a row (one
 // wave) reduce h B and then h C.  The state is read and written once per call: bound by HBM.
-// 64 rows, 80 heads of 64, dstate 128: 66 us for 0.34 GB, 5.1 TB/s, what a copy reaches.  One row of 32
+// 64 rows, 80 heads of 64, dstate 128: 66 us for 0.34 GB, 5.1 TB/s, what a copy reaches (51 us where the
+// state is still in the last-level cache from the call before).  One row of 32
 // heads of 128: 4 us, behind 10 us of the host's.
 // ---------------------------------------------------------------------------
 template <typename T>
