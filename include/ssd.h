@@ -445,6 +445,106 @@ int ssd_bc_norm_bwd(const ssd_norm* p, const void* B, const void* C, const float
                     void* dB, void* dC, float* dwB, float* dwC, void* ws, size_t ws_bytes,
                     void* stream);
 
+/* ---- States of many sequences in a pool ----
+ * A server holds the states of its sequences in the slots of a pool: float32, the headdim x dstate
+ * states of one slot's heads contiguous, slot_stride elements from one slot to the next (one layer's
+ * slots of a pool of several layers need no copy).  Row i of a call works on the state of slot
+ * slots[i] (device int32).  A row whose slot lies outside [0, slots) is idle: its outputs are zero
+ * and it touches no state, so a padded batch needs no other form.
+ *
+ *   x  [batch, seqlen, nheads, headdim], B, C [batch, seqlen, ngroups, dstate]  problem dtype; a
+ *      token's heads contiguous, xstride / bstride / cstride elements from one token to the next (of
+ *      all batch * seqlen tokens), at least the token's elements and a multiple of 16 bytes: slices
+ *      of a wider projection need no copy
+ *   dt [batch, seqlen, nheads] float32, A [nheads] float32, contiguous
+ *   D  [nheads] float32 (the scan's skip term) or NULL = 0
+ *   beta [batch, seqlen, nheads] problem dtype: the gated delta rule; NULL: the scan's recurrence.
+ *      The delta rule has no skip term: D is NULL with it.
+ *   y  [batch, seqlen, nheads, headdim] contiguous, problem dtype
+ *
+ * headdim in {16, 32, 64, 128}, dstate in {16, 32, 64, 128, 256}, both dtypes, flags 0; batch * nheads
+ * under 2^24, strides to 2^32, batch * seqlen times any of them under 2^40.  Alignment: x, B, C, y and
+ * pool 16 bytes, the slot stride a multiple of 4 elements, the rest one element.  No workspace.
+ * Sums, decays and states are float32 (each decay's exponent float64); y is rounded once.
+ * Outputs (y, the pool where it is written) overlap no input and each other nowhere.
+ * Ownership, ordering, capture and errors as for ssd_scan_fwd.
+ *
+ * Which slots a call names is read on the device alone.  No slot may be written by one row and
+ * read or written by another row of the same call: its state, and what that row reads, would be
+ * either's (nothing outside the pool is ever accessed).  Several rows may read one slot that none
+ * writes. */
+typedef struct {
+    int64_t batch, seqlen, nheads, headdim, dstate, ngroups;
+    int64_t xstride, bstride, cstride; /* elements between tokens */
+    int64_t slots, slot_stride;        /* of the pool; the stride in elements */
+    int32_t dtype, flags;
+} ssd_pool_problem;
+
+/* The recurrence token by token (ssd_step, ssd_delta_step) on the states of slots[i], left in
+ * out_slots[i] (NULL = slots: in place).  With out_slots a row reads a state that others share and
+ * writes one of its own, which makes a fork cost nothing; a row whose out slot lies outside the
+ * pool computes y and leaves no state.  seqlen = 0 copies the states (nothing where out_slots is NULL). */
+int ssd_pool_step(const ssd_pool_problem* p, const void* x, const float* dt, const float* A, const void* B,
+                  const void* C, const float* D, const void* beta, float* pool, const int32_t* slots,
+                  const int32_t* out_slots, void* y, void* stream);
+
+/* A tree of drafted tokens over the held states: node k of row i follows node parents[i][k], one of
+ * 0 .. k - 1, or the held state (-1).  Every node's y is that of its path from the held state, which is
+ * left as it is:
+ *
+ *     h_k = a_k h_parent + x_k B_k^T                                  y_k = h_k C_k + D_h x_k
+ *     h_k = a_k h_parent + beta_k (x_k - a_k h_parent B_k) B_k^T      y_k = h_k C_k       (delta rule)
+ *
+ * computed without a state per node: with E_k and W_kj the decays from the held state and from node
+ * j to node k along the path, y_k = E_k h C_k + sum_j W_kj (C_k . B_j) u_j over the node and its
+ * ancestors j, where u = x, or for the delta rule u_k = beta_k (x_k - E_k h B_k - sum_j W_kj (B_k . B_j) u_j)
+ * over the ancestors.  Decay sums are formed along each path; where float32 factors enter the bfloat16
+ * matrix cores they do so in two terms.
+ *
+ * A node whose parent lies outside [-1, k - 1] is absent, and so is every node below it: its y is zero
+ * and none of its values (which may be anything) reaches another node.  Rows of fewer nodes are padded
+ * with such nodes (-2).  A NaN or infinity in a node's x, dt, B or beta makes the y of that node and
+ * those below it NaN or infinite where the formulas need it, in no other branch; for the delta rule one in dt, B or beta
+ * reaches every column of the heads that read it.
+ *
+ * seqlen (the nodes) at most SSD_TREE_NODES. */
+#define SSD_TREE_NODES 256
+int ssd_tree_step(const ssd_pool_problem* p, const void* x, const float* dt, const float* A, const void* B,
+                  const void* C, const float* D, const void* beta, const int32_t* parents, const float* pool,
+                  const int32_t* slots, void* y, void* stream);
+
+/* Accept a path of such a tree: the state of slots[i] becomes, in out_slots[i] (NULL = slots), the state
+ * behind node last[i] (int32 [batch]).  last = -1 accepts none (the state goes to the out slot as it is);
+ * any other value that names no present node leaves the row idle.  C and D play no part (cstride is not read).  In float32, like
+ * ssd_pool_step over the path's tokens. */
+int ssd_tree_commit(const ssd_pool_problem* p, const void* x, const float* dt, const float* A, const void* B,
+                    const void* beta, const int32_t* parents, const int32_t* last, float* pool,
+                    const int32_t* slots, const int32_t* out_slots, void* stream);
+
+/* The pool's pages: a table (device int32 [rows]) names the slot of every row, entries outside
+ * [0, slots) mean none.  A pool holds the same slots in every layer: element (layer, slot, i) lies at
+ * layer * layer_stride + slot * slot_stride + i, i under slot_elems (a multiple of 4, as the strides are;
+ * slots and layers do not overlap).  pool is 16-byte aligned; slots at most 16384, layers at most 65536, rows at most 65536. */
+typedef struct {
+    int64_t rows, layers, slots, slot_elems, layer_stride, slot_stride;
+} ssd_pages;
+
+/* Fork, free and begin: row r goes on from the state of row sources[r] of the old table (sources[r] in
+ * [0, rows)), or is freed (-1, any other value, or the source has no slot; new entry -1), or begins from a zero
+ * state (-2).  Of the rows that go on from one slot, the one that had it keeps it, else the lowest row takes
+ * it over; every other row, and every row that begins, gets a slot that no row goes on from, the lowest
+ * such slot to the lowest row, with the state copied or zeroed in all layers.  Slots that no row ends in keep
+ * their contents.  Two rows of the old table may share a slot; rows of the new one never do.  new_table
+ * overlaps neither input; rows at most slots, so that there is always a slot. */
+int ssd_pool_fork(const ssd_pages* p, float* pool, const int32_t* table, const int32_t* sources,
+                  int32_t* new_table, void* stream);
+
+/* Compact: with n slots named by the table, every one of them at n or above moves into one below n that
+ * is not named (the lowest to the lowest).  new_table names the slots after the moves (none: -1), count[0] = n; the
+ * slots from n on keep their contents. */
+int ssd_pool_compact(const ssd_pages* p, float* pool, const int32_t* table, int32_t* new_table,
+                     int32_t* count, void* stream);
+
 /* Static text for a status code. */
 const char* ssd_status_string(int status);
 

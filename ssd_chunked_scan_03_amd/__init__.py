@@ -9,7 +9,8 @@ to load, every call raises: there is no fallback path.
     y, hT = diag_scan_fwd(x, dt, A, B, C, D=None, h0=None, chunk=128)
     grads = scan_bwd(x, dt, A, B, C, dy, D=None, h0=None, dhT=None, chunk=256)
 
-The gated delta rule on the same operands and the norm of B and C are in :mod:`.delta`.
+The gated delta rule on the same operands and the norm of B and C are in :mod:`.delta`;
+states in a pool (decode through slots, trees of drafted tokens, fork, compaction) in :mod:`.pool`.
 
 Layouts: x [b,T,H,P]; dt [b,T,H] f32; A [H] (scalar decay) or [H,N] (diagonal
 decay) f32; B, C [b,T,G,N]; D [H] f32; h0 [b,H,P,N] f32.  x/B/C share one dtype,
@@ -25,7 +26,9 @@ __all__ = ["scan_fwd", "diag_scan_fwd", "scan_fwd_into", "scan_bwd", "scan_bwd_i
            "workspace_layout", "status_string", "version", "library_path", "SSDError",
            "delta_fwd", "delta_fwd_into", "delta_fwd_varlen", "delta_fwd_varlen_into", "delta_step",
            "delta_step_into", "delta_bwd", "delta_bwd_into", "delta_workspace_bytes", "delta_bwd_workspace_bytes",
-           "bc_norm", "bc_norm_into", "bc_norm_bwd", "bc_norm_bwd_into", "bc_norm_bwd_workspace_bytes", "Norm"]
+           "bc_norm", "bc_norm_into", "bc_norm_bwd", "bc_norm_bwd_into", "bc_norm_bwd_workspace_bytes", "Norm",
+           "pool_step", "pool_step_into", "tree_step", "tree_step_into", "tree_commit", "tree_commit_into",
+           "pool_fork", "pool_fork_into", "pool_compact", "pool_compact_into", "PoolProblem", "Pages", "TREE_NODES"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libssd.so")
@@ -42,6 +45,7 @@ EXPORTS = ("ssd_workspace_bytes", "ssd_get_workspace_layout", "ssd_scan_fwd", "s
            "ssd_delta_workspace_bytes", "ssd_delta_fwd", "ssd_delta_varlen_workspace_bytes", "ssd_delta_fwd_varlen",
            "ssd_delta_step", "ssd_delta_bwd_workspace_bytes", "ssd_delta_bwd",
            "ssd_bc_norm", "ssd_bc_norm_bwd_workspace_bytes", "ssd_bc_norm_bwd",
+           "ssd_pool_step", "ssd_tree_step", "ssd_tree_commit", "ssd_pool_fork", "ssd_pool_compact",
            "ssd_status_string", "ssd_version")
 
 
@@ -103,6 +107,7 @@ def _load():
     lib.ssd_version.argtypes = []
     lib.ssd_version.restype = ci
     delta._bind(lib)
+    pool._bind(lib)
     _lib = lib
     return lib
 
@@ -433,3 +438,6 @@ from .delta import (DELTA_CHUNK, Norm, bc_norm, bc_norm_bwd, bc_norm_bwd_into,  
                     bc_norm_bwd_workspace_bytes, bc_norm_into, delta_bwd, delta_bwd_into, delta_bwd_workspace_bytes,
                     delta_fwd, delta_fwd_into, delta_fwd_varlen, delta_fwd_varlen_into, delta_step, delta_step_into,
                     delta_workspace_bytes)
+from . import pool  # noqa: E402
+from .pool import (TREE_NODES, Pages, PoolProblem, pool_compact, pool_compact_into, pool_fork,  # noqa: E402,F401
+                   pool_fork_into, pool_step, pool_step_into, tree_commit, tree_commit_into, tree_step, tree_step_into)
