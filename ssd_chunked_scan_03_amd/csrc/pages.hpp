@@ -57,21 +57,27 @@ __device__ __forceinline__ int nth_bit(const unsigned long long* words, const in
     return lo * 64 + __ffsll((long long)v) - 1;
 }
 
-// elements [at, at + kPiece) of a slot in one layer from slot `from` (negative: zeros) to slot `to`
+// Elements [at, at + kPiece) of a slot in one layer from slot `from` (negative: zeros) to slot `to`.  Two
+// loads in flight per thread, and stores that leave no copy in the caches (copies of 0.28 GB of states,
+// a slot 2.6 MB in a layer: two 122 us, two without the hint 130, four 123, eight 155, one 155; read and written bytes at 5
+// TB/s, as a large copy).
 __device__ __forceinline__ void copy_piece(const PageArgs& a, int from, int to, int64_t layer, int64_t at) {
+    constexpr int UN = 2;
     const float* src = a.pool + layer * a.ls + (int64_t)(from < 0 ? 0 : from) * a.ss;
     float* dst = a.pool + layer * a.ls + (int64_t)to * a.ss;
-    f32x4 v[8];
+    for (int k0 = 0; k0 < kPiece; k0 += UN * 1024) {
+        f32x4 v[UN];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const int64_t e = at + (k * 256 + threadIdx.x) * 4;
-        v[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (from >= 0 && e < a.elems) v[k] = ld4(src + e);
-    }
+        for (int k = 0; k < UN; ++k) {
+            const int64_t e = at + k0 + (k * 256 + threadIdx.x) * 4;
+            v[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (from >= 0 && e < a.elems) v[k] = ld4(src + e);
+        }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const int64_t e = at + (k * 256 + threadIdx.x) * 4;
-        if (e < a.elems) st4(dst + e, v[k]);
+        for (int k = 0; k < UN; ++k) {
+            const int64_t e = at + k0 + (k * 256 + threadIdx.x) * 4;
+            if (e < a.elems) __builtin_nontemporal_store(v[k], reinterpret_cast<f32x4*>(dst + e));
+        }
     }
 }
 
@@ -187,11 +193,13 @@ inline size_t compact_lds(int64_t S) {
     const size_t words = (size_t)(S + 63) / 64;
     return words * 16 + 2 * (words + 1) * 4;
 }
-// work-groups: one per piece of the most moves that there can be, up to those that fit the GPU at once
+// Work-groups: one per piece of the most moves that there can be, up to four per CU or as many as LDS
+// lets in (the copies above with 256 / 512 / 1024 / 2048 work-groups: 166 / 122 / 122 / 132 us; pieces of 8 / 16 / 32 / 64 KB:
+// 122 / 125 / 122 / 128 us, and 152 / 123 / 113 / 114 us for a compaction of 0.27 GB in slots of 1.6 MB).
 inline unsigned page_grid(const PageArgs& a, int64_t moves, size_t lds) {
-    int64_t most = 256 * (160 * 1024 / (int64_t)(lds > 20 * 1024 ? lds : 20 * 1024));
+    int64_t most = 256 * (160 * 1024 / (int64_t)(lds > 40 * 1024 ? lds : 40 * 1024));
     const int64_t pieces = (a.elems + kPiece - 1) / kPiece;
-    const int64_t each = a.layers * pieces < most ? a.layers * pieces : most;  // (no product past 64 bits)
+    const int64_t each = pieces < most / (a.layers > 0 ? a.layers : 1) + 1 ? a.layers * pieces : most;
     const int64_t items = moves * each;
     if (items < most) most = items;
     return (unsigned)(most < 1 ? 1 : most);
