@@ -47,12 +47,6 @@ def _bind(lib):
 
 
 @functools.lru_cache(maxsize=256)
-def _problem(*sizes):
-    """The descriptor of these sizes (it holds no data)."""
-    return PoolProblem(*sizes, 0)
-
-
-@functools.lru_cache(maxsize=256)
 def _pages(*sizes):
     return Pages(*sizes)
 
@@ -82,40 +76,84 @@ def _slot_stride(pool):
     return pool.stride(0) if S > 1 else H * P * N
 
 
-def _rows(x, B, C, pool, slots, tensors, nodes=None):
-    """Checks a call's tensors and returns its descriptor.  tensors: (name, tensor or None, shape, dtype)."""
+# Sizes, strides, type and device of a call's x, B, C and pool (no data) -> its descriptor, the device and what
+# its other tensors have to be, so that these are worked out once for each.
+_seen = {}
+_OTHERS = {"step": ("dt", "A", "D", "beta", "slots", "out_slots"), "tree": ("dt", "A", "D", "beta", "parents", "slots"),
+           "commit": ("dt", "A", "beta", "parents", "last", "slots", "out_slots")}
+
+
+def _rows(kind, x, B, C, pool, others):
+    """Checks a call's tensors (others: in _OTHERS' order) and returns its descriptor and device."""
+    if others[-1 if kind == "tree" else -2] is None:
+        raise ValueError("slots is required")
+    look = (kind, x.shape, x.stride(), x.dtype, x.get_device(), B.shape, B.stride(), pool.shape, pool.stride(),
+            None if C is None else C.stride())
+    found = _seen.get(look)
+    if found is None:
+        found = _work_out(kind, x, B, C, pool)
+        if len(_seen) >= 1024:
+            _seen.clear()
+        _seen[look] = found
+    prob, dev, want = found
+    td, ok = x.dtype, B.dtype == x.dtype and B.get_device() == dev and pool.get_device() == dev
+    if C is not None:
+        ok = ok and C.dtype == td and C.get_device() == dev and C.shape == B.shape
+    for t, (shape, dtype) in zip(others, want):
+        if t is not None and (t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous()):
+            ok = False
+    if not ok or pool.dtype != want[0][1]:  # (dt's type: float32)
+        _work_out(kind, x, B, C, pool)
+        _refuse(x, [(n, t, *w) for n, t, w in zip(_OTHERS[kind], others, want)])
+    if kind != "commit" and others[2] is not None and others[3] is not None:
+        raise ValueError("the gated delta rule (beta) has no skip term D")
+    return prob, dev
+
+
+def _work_out(kind, x, B, C, pool):
     import torch
     if x.dim() != 4 or B.dim() != 4 or pool.dim() != 4:
         raise ValueError("x must be [b, T, H, P], B [b, T, G, N] and pool [S, H, P, N]")
-    if slots is None:
-        raise ValueError("slots is required")
     b, T, H, P = x.shape
     G, N = B.shape[2:]
-    td = x.dtype
+    td, f32, i32 = x.dtype, torch.float32, torch.int32
     code = _codes().get(td)
     if code is None:
         raise TypeError(f"x/B/C must be bfloat16 or float32, got {td}")
     dev = x.get_device()
     if pool.shape[1:] != (H, P, N):
         raise ValueError(f"pool must have shape [S, {H}, {P}, {N}], got {tuple(pool.shape)}")
-    if pool.dtype != torch.float32:
+    if pool.dtype != f32:
         raise TypeError(f"pool must be float32, got {pool.dtype}")
     for name, t in (("B", B), ("C", C)):
-        if t is not None and (t.shape != (b, T, G, N) or t.dtype != td):
-            if t.shape != (b, T, G, N):
-                raise ValueError(f"{name} must have shape {(b, T, G, N)}, got {tuple(t.shape)}")
+        if t is not None and t.shape != (b, T, G, N):
+            raise ValueError(f"{name} must have shape {(b, T, G, N)}, got {tuple(t.shape)}")
+        if t is not None and t.dtype != td:
             raise TypeError("x, B, C must share one dtype")
     if dev < 0 or pool.get_device() != dev or B.get_device() != dev or (C is not None and C.get_device() != dev):
         raise ValueError("x, B, C and pool must be GPU tensors on one device")
-    for name, t, shape, dtype in tensors:
-        if t is not None and (t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous()):
-            _refuse(x, tensors)
-    if nodes is not None and T > TREE_NODES:
+    if kind != "step" and T > TREE_NODES:
         raise ValueError(f"a tree has at most {TREE_NODES} nodes, got {T}")
-    xs = H * P if x.is_contiguous() else _token_stride("x", x)
-    bs = G * N if B.is_contiguous() else _token_stride("B", B)
-    cs = 0 if C is None else G * N if C.is_contiguous() else _token_stride("C", C)
-    return _problem(b, T, H, P, N, G, xs, bs, cs, pool.shape[0], _slot_stride(pool), code)
+    xs, bs = _step("x", x, T, H, P), _step("B", B, T, G, N)
+    cs = 0 if C is None else _step("C", C, T, G, N)
+    prob = PoolProblem(b, T, H, P, N, G, xs, bs, cs, pool.shape[0], _slot_stride(pool), code, 0)
+    shapes = {"dt": ((b, T, H), f32), "A": ((H,), f32), "D": ((H,), f32), "beta": ((b, T, H), td),
+              "parents": ((b, T), i32), "last": ((b,), i32), "slots": ((b,), i32), "out_slots": ((b,), i32)}
+    return prob, dev, tuple(shapes[n] for n in _OTHERS[kind])
+
+
+def _step(name, t, T, heads, n):
+    """Elements from one token to the next."""
+    s = t.stride()
+    step = s[1]
+    if T > 1 and s[3] == 1 and s[2] == n and s[0] == T * step and step >= heads * n:
+        return step
+    return heads * n if t.is_contiguous() else _token_stride(name, t)
+
+
+def _like(x):
+    import torch
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 def pool_step_into(prob: PoolProblem, x, dt, A, B, C, D, beta, pool, slots, out_slots, y, stream=None) -> None:
@@ -128,16 +166,9 @@ def pool_step(x, dt, A, B, C, pool, slots, D=None, beta=None, out_slots=None):
     """Decode: run the recurrence over x's tokens [b, T, H, P] on the states pool[slots[i]], left in
     pool[out_slots[i]] (None: in place; an out slot outside the pool leaves none).  dt [b, T, H] f32, A and D
     [H] f32, B/C [b, T, G, N], beta [b, T, H] in x's dtype (the gated delta rule, no D) or None.  Returns y."""
-    import torch
-    f32, i32 = torch.float32, torch.int32
-    b, T, H, P = x.shape if x.dim() == 4 else (0, 0, 0, 0)
-    prob = _rows(x, B, C, pool, slots, (
-        ("dt", dt, (b, T, H), f32), ("A", A, (H,), f32), ("D", D, (H,), f32), ("beta", beta, (b, T, H), x.dtype),
-        ("slots", slots, (b,), i32), ("out_slots", out_slots, (b,), i32)))
-    if beta is not None and D is not None:
-        raise ValueError("the gated delta rule (beta) has no skip term D")
-    y = torch.empty((b, T, H, P), dtype=x.dtype, device=x.device)
-    _call("ssd_pool_step", prob, (x, dt, A, B, C, D, beta, pool, slots, out_slots, y), index=x.get_device())
+    prob, dev = _rows("step", x, B, C, pool, (dt, A, D, beta, slots, out_slots))
+    y = _like(x)
+    _call("ssd_pool_step", prob, (x, dt, A, B, C, D, beta, pool, slots, out_slots, y), index=dev)
     return y
 
 
@@ -151,16 +182,9 @@ def tree_step(x, dt, A, B, C, parents, pool, slots, D=None, beta=None):
     beta [b, K, H] or None; parents [b, K] int32, each a node before it or -1 (the held state pool[slots[i]]).  A
     node with any other parent, or below such a node, is absent: pad rows of fewer nodes with -2.  K is
     at most 256.  Returns y [b, K, H, P] (zero for absent nodes); the pool is left as it is."""
-    import torch
-    f32, i32 = torch.float32, torch.int32
-    b, K, H, P = x.shape if x.dim() == 4 else (0, 0, 0, 0)
-    prob = _rows(x, B, C, pool, slots, (
-        ("dt", dt, (b, K, H), f32), ("A", A, (H,), f32), ("D", D, (H,), f32), ("beta", beta, (b, K, H), x.dtype),
-        ("parents", parents, (b, K), i32), ("slots", slots, (b,), i32)), nodes=K)
-    if beta is not None and D is not None:
-        raise ValueError("the gated delta rule (beta) has no skip term D")
-    y = torch.empty((b, K, H, P), dtype=x.dtype, device=x.device)
-    _call("ssd_tree_step", prob, (x, dt, A, B, C, D, beta, parents, pool, slots, y), index=x.get_device())
+    prob, dev = _rows("tree", x, B, C, pool, (dt, A, D, beta, parents, slots))
+    y = _like(x)
+    _call("ssd_tree_step", prob, (x, dt, A, B, C, D, beta, parents, pool, slots, y), index=dev)
     return y
 
 
@@ -172,14 +196,8 @@ def tree_commit_into(prob: PoolProblem, x, dt, A, B, beta, parents, last, pool, 
 def tree_commit(x, dt, A, B, parents, last, pool, slots, beta=None, out_slots=None):
     """Accept a path of tree_step's tree (same arguments): the state behind node last[i] (int32 [b]; -1: the
     held state itself) goes to pool[out_slots[i]] (None: in place).  Returns the pool."""
-    import torch
-    f32, i32 = torch.float32, torch.int32
-    b, K, H, P = x.shape if x.dim() == 4 else (0, 0, 0, 0)
-    prob = _rows(x, B, None, pool, slots, (
-        ("dt", dt, (b, K, H), f32), ("A", A, (H,), f32), ("beta", beta, (b, K, H), x.dtype),
-        ("parents", parents, (b, K), i32), ("last", last, (b,), i32), ("slots", slots, (b,), i32),
-        ("out_slots", out_slots, (b,), i32)), nodes=K)
-    _call("ssd_tree_commit", prob, (x, dt, A, B, beta, parents, last, pool, slots, out_slots), index=x.get_device())
+    prob, dev = _rows("commit", x, B, None, pool, (dt, A, beta, parents, last, slots, out_slots))
+    _call("ssd_tree_commit", prob, (x, dt, A, B, beta, parents, last, pool, slots, out_slots), index=dev)
     return pool
 
 
