@@ -463,7 +463,7 @@ int ssd_bc_norm_bwd(const ssd_norm* p, const void* B, const void* C, const float
  *   y  [batch, seqlen, nheads, headdim] contiguous, problem dtype
  *
  * headdim in {16, 32, 64, 128}, dstate in {16, 32, 64, 128, 256}, both dtypes, flags 0; batch * nheads
- * under 2^24, strides to 2^32, batch * seqlen times any of them under 2^40.  Alignment: x, B, C, y and
+ * under 2^24, nheads * headdim at most 2^24, strides to 2^32, batch * seqlen times any of them under 2^40.  Alignment: x, B, C, y and
  * pool 16 bytes, the slot stride a multiple of 4 elements, the rest one element.  No workspace.
  * Sums, decays and states are float32 (each decay's exponent float64); y is rounded once.
  * Outputs (y, the pool where it is written) overlap no input and each other nowhere.

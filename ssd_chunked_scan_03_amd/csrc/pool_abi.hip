@@ -56,7 +56,7 @@ int check(const ssd_pool_problem* p, Kind kind) {
     if (!pn_supported(p->headdim, p->dstate) || p->flags != 0) return SSD_ERR_UNSUPPORTED;
     if (kind != kStep && p->seqlen > SSD_TREE_NODES) return SSD_ERR_UNSUPPORTED;
     const int64_t H = p->nheads, top = (int64_t)1 << 24;
-    if (H >= top || p->batch >= top || p->batch * H >= top) return SSD_ERR_UNSUPPORTED;
+    if (H >= top || p->batch >= top || p->batch * H >= top || H * p->headdim > top) return SSD_ERR_UNSUPPORTED;
     const int64_t state = H * p->headdim * p->dstate;
     if (p->slots > 0x7fffffffLL || state > kFar || p->slot_stride > kFar) return SSD_ERR_UNSUPPORTED;
     if (p->slots > 1 && p->slot_stride < state) return SSD_ERR_SHAPE;
