@@ -91,27 +91,24 @@ __device__ __forceinline__ f32x4 times_inv(const float* tab, int lane, f32x4 v) 
 
 constexpr int kTableBytes = 4096;  // of a node tile's M (or T) against a panel
 
-// Up to 64 nodes: NK tiles of 16.  C's and B's rows are kept in LDS as operand fragments, C for the
-// products with the state and B where the delta rule needs it too; B C^T and B B^T are kept (GST) or, where B is there anyway,
-// formed again for every head.
+// Up to 64 nodes: NK tiles of 16.  C's rows are kept in LDS as operand fragments for the products with the
+// state, and B's where the delta rule needs them too; the scan has B's rows there only until B C^T is formed (in M's place).
 template <typename T, int N, bool DELTA, int NK>
 struct TreeCfg {
     static constexpr int KS = N < 32 ? 1 : N / 32;
     static constexpr int ROWS = NK * KS * 512 * (int)sizeof(T);  // bytes of C's or B's fragments
     static constexpr bool LCB = ROWS * (DELTA ? 2 : 1) <= 65536;
-    static constexpr bool GST = !(DELTA && LCB);
-    static constexpr int TAB = NK == 1 ? 2048 : NK == 2 ? 4096 : 12288, G = GST ? NK * (NK + 1) / 2 * 1024 : 0;
-    static constexpr int M = 0;                                    // [tile] M as fragments
-    static constexpr int TT = M + TAB;                             // [tile] T
-    static constexpr int INV = TT + (DELTA ? TAB : 0);             // [tile] the diagonal tiles' inverses
-    static constexpr int GC = INV + (DELTA ? NK * 1024 : 0);       // [tile pair] B C^T
-    static constexpr int GB = GC + G;                              // [tile pair] B B^T
-    static constexpr int CF = GB + (DELTA ? G : 0);                // C's rows
-    static constexpr int BF = CF + (LCB ? ROWS : 0);               // B's rows
-    static constexpr int MASK = BF + (LCB && DELTA ? ROWS : 0);    // [node] the node and those above it
-    static constexpr int BADB = MASK + 512;                        // [tile] nodes whose row of B is not finite
-    static constexpr int C = BADB + 64;                            // [head][node] binary orders of decay from the held state
-    static constexpr int HEAD = 64 * (8 + 4 + (DELTA ? 4 : 0));    // C, then E (-1 absent, -2 not computable), then beta
+    static constexpr int TAB = NK == 1 ? 2048 : NK == 2 ? 4096 : NK == 3 ? 8192 : 12288;
+    static constexpr int M = 0;                                                   // [tile] M as fragments
+    static constexpr int TT = M + TAB;                                            // [tile] T
+    static constexpr int INV = TT + (DELTA ? TAB : 0);                            // [tile] the diagonal tiles' inverses
+    static constexpr int GC = DELTA ? INV + NK * 1024 : TAB > ROWS ? TAB : ROWS;  // [tile pair] the scan's B C^T
+    static constexpr int CF = GC + (DELTA ? 0 : NK * (NK + 1) / 2 * 1024);        // C's rows
+    static constexpr int BF = DELTA ? CF + (LCB ? ROWS : 0) : 0;                  // B's rows
+    static constexpr int MASK = DELTA ? BF + (LCB ? ROWS : 0) : CF + ROWS;        // [node] the node and those above it
+    static constexpr int BADB = MASK + 512;                                       // [tile] nodes whose row of B is not finite
+    static constexpr int C = BADB + 64;  // [head][node] binary orders of decay from the held state
+    static constexpr int HEAD = 64 * (8 + 4 + (DELTA ? 4 : 0));  // C, then E (-1 absent, -2 not computable), then beta
     static constexpr int total(int hb) { return C + hb * HEAD; }
     // tile kt's table: two KiB for each pair of tiles up to its own
     static __device__ int at(int kt) { return kt < 2 ? kt * 2048 : (kt - 1) * kTableBytes; }
@@ -244,15 +241,15 @@ __device__ __forceinline__ double orders(float dt, double A) {
 
 typedef unsigned long long u64;
 
-// Which (row, group, heads, columns) a work-group takes.  Blocks k, k + 8, ... run on one XCD: each takes a
+// Which (row, group, heads, columns) a work-group takes; cols: its waves that have columns.  Blocks k, k + 8, ... run on one XCD: each takes a
 // contiguous range, so that a row's B, C and dt stay in its L2.
 struct Place {
     int64_t bi;
     int g, h0, nh, p0;
-    __device__ Place(const Args& a, int hb, int waves, int w) {
-        const int hg = a.H / a.G, slabs = a.P / (16 * waves), chunks = (hg + hb - 1) / hb, nb = gridDim.x;
+    __device__ Place(const Args& a, int hb, int cols, int w) {
+        const int hg = a.H / a.G, slabs = a.P / (16 * cols), chunks = (hg + hb - 1) / hb, nb = gridDim.x;
         int64_t id = nb % 8 == 0 ? (int64_t)(blockIdx.x % 8) * (nb / 8) + blockIdx.x / 8 : blockIdx.x;
-        p0 = ((int)(id % slabs) * waves + w) * 16;
+        p0 = ((int)(id % slabs) * cols + w) * 16;
         id /= slabs;
         const int chunk = (int)(id % chunks);
         id /= chunks;
@@ -291,10 +288,10 @@ __device__ __forceinline__ f32x4 clean_x(f32x4 v, const float* decay4, unsigned&
 }
 
 // ---------------------------------------------------------------------------
-// k_tree: trees of up to 16 NK nodes.  A work-group takes hb heads of a group one after another: paths, B C^T and
-// C's rows are formed or fetched once for them.  Per head: tables (a node tile a wave), a barrier, then each
-// wave's columns tile by tile from LDS alone, while the next head's state and x are on their way: no load is waited for behind
-// a store of y.
+// k_tree: trees of up to 16 NK nodes.  A work-group takes hb heads of a group one after another: paths, the
+// products of B with C and itself, and the rows of C and B are formed or fetched once for them.  Wave w forms the tables of node
+// tile w (w < NK) and has 16 columns (w < cols).  Per head: tables, a barrier, then each wave's columns tile by tile
+// from LDS alone, while the next head's state and x are on their way: no load is waited for behind a store of y.
 // ---------------------------------------------------------------------------
 template <typename T, int N, bool DELTA, int NK>
 __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
@@ -302,16 +299,15 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
     typedef TreeCfg<T, N, DELTA, NK> CF;
     constexpr int KS = CF::KS;
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    const int waves = blockDim.x >> 6, K = (int)a.T, P = a.P, H = a.H;
-    const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
-    const Place at(a, hb, waves, w);
+    const int waves = blockDim.x >> 6, K = (int)a.T, P = a.P, H = a.H, cols = P < 64 ? P / 16 : 4;
+    const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
+    const Place at(a, hb, cols, w);
     const int64_t row0 = at.bi * K, ys = (int64_t)H * P;
     const unsigned sel = delta::quad_sel(lane);
-    const bool upper = (lane & 2) != 0;
+    const bool upper = (lane & 2) != 0, mine = w < cols, tiled = w < NK;
     T* mtab = reinterpret_cast<T*>(smem + CF::M);
     T* ttab = reinterpret_cast<T*>(smem + CF::TT);
     float* gc = reinterpret_cast<float*>(smem + CF::GC);
-    float* gb = reinterpret_cast<float*>(smem + CF::GB);
     T* crow = reinterpret_cast<T*>(smem + CF::CF);
     T* brow = reinterpret_cast<T*>(smem + CF::BF);
     u64* mask = reinterpret_cast<u64*>(smem + CF::MASK);
@@ -325,9 +321,10 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
     const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
     const int slot = a.slots[at.bi];
     if (slot < 0 || slot >= a.S) {
-        for (int hh = 0; hh < at.nh; ++hh)
-            for (int k0 = 0; k0 < K; k0 += 16)
-                store_y(static_cast<T*>(a.y) + (row0 * H + at.h0 + hh) * P + at.p0, ys, k0, K, lane, sel, upper, zero4);
+        if (mine)
+            for (int hh = 0; hh < at.nh; ++hh)
+                for (int k0 = 0; k0 < K; k0 += 16)
+                    store_y(static_cast<T*>(a.y) + (row0 * H + at.h0 + hh) * P + at.p0, ys, k0, K, lane, sel, upper, zero4);
         return;
     }
     const bool has = N >= 32 || q < 2;  // (dstate 16 fills half a fragment)
@@ -360,49 +357,56 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
         dtv[i] = a.dt[k];
         btv[i] = DELTA ? to_f(beta[k]) : 0.f;
     }
-    if (w >= NK) fetch(at.h0);
-    for (int kt = w; kt < NK; kt += waves) {
+    f32x4 gcr[NK], gbr[NK];  // the delta rule's B C^T and B B^T of this wave's node tile
+#pragma unroll
+    for (int jt = 0; jt < NK; ++jt) gcr[jt] = gbr[jt] = zero4;
+    {
         F8 cf[KS], bf[KS];
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            cf[ks] = frag(Cm, a.cs, 16 * kt + l16, ks);
-            bf[ks] = frag(Bm, a.bs, 16 * kt + l16, ks);
-        }
-        if (NK == 1) fetch(at.h0);  // (behind what the products wait for)
-        if (CF::LCB) {
+        if (tiled) {
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                st8(crow + ((kt * KS + ks) * 64 + lane) * 8, cf[ks]);
-                if (DELTA) st8(brow + ((kt * KS + ks) * 64 + lane) * 8, bf[ks]);
+                cf[ks] = frag(Cm, a.cs, 16 * w + l16, ks);
+                bf[ks] = frag(Bm, a.bs, 16 * w + l16, ks);
             }
         }
-        for (int jt = CF::GST ? 0 : kt; jt <= kt; ++jt) {
-            f32x4 c = zero4, b = zero4;
+        if (mine) fetch(at.h0);  // (behind what the products wait for)
+        if (tiled) {
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                const F8 bj = jt == kt ? bf[ks] : frag(Bm, a.bs, 16 * jt + l16, ks);
-                if (CF::GST) c = mma(c, bj, cf[ks]);
-                if (DELTA) b = mma(b, bj, bf[ks]);
+                if (CF::LCB) st8(crow + ((w * KS + ks) * 64 + lane) * 8, cf[ks]);
+                if (CF::LCB || !DELTA) st8(brow + ((w * KS + ks) * 64 + lane) * 8, bf[ks]);
             }
-            const int tile = (kt * (kt + 1) / 2 + jt) * 256 + lane * 4;
-            if (CF::GST) {
-                settle(c);
-                st4(gc + tile, c);
-            }
-            if (DELTA) {
-                settle(b);
-                if (CF::GST) st4(gb + tile, b);
-                if (jt == kt) {
-                    // |B_k|^2 on the diagonal tells whether the row is finite
-                    const float d = l16 & 2 ? (l16 & 1 ? b[3] : b[2]) : (l16 & 1 ? b[1] : b[0]);
-                    u64 who = __ballot(q == l16 >> 2 && odd_bits(d));
-                    who |= who >> 32;
-                    if (lane == 0) badb[kt] = ((who | who >> 16) & 0xffff) << (16 * kt);
+        }
+        __syncthreads();
+        if (tiled) {
+#pragma unroll
+            for (int jt = 0; jt < NK; ++jt)
+                if (jt <= w) {
+                    f32x4 c = zero4, b = zero4;
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        const F8 bj = CF::LCB || !DELTA ? kept(brow, jt, ks) : frag(Bm, a.bs, 16 * jt + l16, ks);
+                        c = mma(c, bj, cf[ks]);
+                        if (DELTA) b = mma(b, bj, bf[ks]);
+                    }
+                    settle(c);
+                    if (DELTA) {
+                        settle(b);
+                        gcr[jt] = c;
+                        gbr[jt] = b;
+                        if (jt == w) {
+                            // |B_k|^2 on the diagonal tells whether the row is finite
+                            const float d = l16 & 2 ? (l16 & 1 ? b[3] : b[2]) : (l16 & 1 ? b[1] : b[0]);
+                            u64 who = __ballot(q == l16 >> 2 && odd_bits(d));
+                            who |= who >> 32;
+                            if (lane == 0) badb[w] = ((who | who >> 16) & 0xffff) << (16 * w);
+                        }
+                    } else {
+                        st4(gc + (w * (w + 1) / 2 + jt) * 256 + lane * 4, c);
+                    }
                 }
-            }
         }
     }
-    if (NK > 1 && w < NK) fetch(at.h0);
     // the paths, by doubling: pr[r] is the node 2^r above
     bool there = lane < K && par >= -1 && par < lane;
     u64 mk = 1ull << lane;
@@ -452,51 +456,45 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
     const float nan = __builtin_nanf("");
     for (int hh = 0; hh < at.nh; ++hh) {
         const int h = at.h0 + hh;
-        // ---- M and T of this wave's node tiles ----
-        for (int kt = w; kt < NK; kt += waves) {
-            T* mt = mtab + CF::at(kt) / (int)sizeof(T);
-            T* tt = ttab + CF::at(kt) / (int)sizeof(T);
-            const int k = 16 * kt + l16;
+        // ---- M and T of this wave's node tile ----
+        if (tiled) {
+            T* mt = mtab + CF::at(w) / (int)sizeof(T);
+            T* tt = ttab + CF::at(w) / (int)sizeof(T);
+            const int k = 16 * w + l16;
             const u64 on = decay[hh * 64 + k] < 0.f ? 0 : mask[k];
             const double ck = cs[hh * 64 + k];
             const float bk = DELTA ? betas[hh * 64 + k] : 0.f;
             f32x4 diag = zero4;
-            for (int jt = 0; jt < ((kt + 2) & ~1); ++jt) {
-                f32x4 m = zero4, t = zero4;
-                if (jt <= kt) {
-                    f32x4 c = zero4, b = zero4;
-                    if (CF::GST) {
-                        const int tile = (kt * (kt + 1) / 2 + jt) * 256 + lane * 4;
-                        c = ld4(gc + tile);
-                        if (DELTA) b = ld4(gb + tile);
-                    } else {
 #pragma unroll
-                        for (int ks = 0; ks < KS; ++ks) {
-                            const F8 bj = kept(brow, jt, ks);
-                            c = mma(c, bj, kept(crow, kt, ks));
-                            b = mma(b, bj, kept(brow, kt, ks));
+            for (int jt = 0; jt < ((NK + 1) & ~1); ++jt)
+                if (jt < ((w + 2) & ~1)) {
+                    f32x4 m = zero4, t = zero4;
+                    if (jt < NK && jt <= w) {
+                        f32x4 c;
+                        if (DELTA) c = gcr[jt < NK ? jt : 0];
+                        else c = ld4(gc + (w * (w + 1) / 2 + jt) * 256 + lane * 4);
+                        weigh<DELTA>((unsigned)(on >> (16 * jt + 4 * q)) & 15u, ck, cs + hh * 64 + 16 * jt + 4 * q, bk,
+                                     k - 16 * jt - 4 * q, c, gbr[jt < NK ? jt : 0], m, t);
+                    }
+                    put(mt, jt >> 1, jt & 1, lane, m);
+                    if (DELTA) {
+                        if (jt == w) {
+                            diag = t;
+                            t = zero4;
                         }
-                        settle(c);
-                        settle(b);
+                        put(tt, jt >> 1, jt & 1, lane, t);
                     }
-                    weigh<DELTA>((unsigned)(on >> (16 * jt + 4 * q)) & 15u, ck, cs + hh * 64 + 16 * jt + 4 * q, bk,
-                                 k - 16 * jt - 4 * q, c, b, m, t);
                 }
-                put(mt, jt >> 1, jt & 1, lane, m);
-                if (DELTA) {
-                    if (jt == kt) {
-                        diag = t;
-                        t = zero4;
-                    }
-                    put(tt, jt >> 1, jt & 1, lane, t);
-                }
-            }
             if (DELTA) {
-                T* inv = reinterpret_cast<T*>(smem + CF::INV + kt * 1024);
+                T* inv = reinterpret_cast<T*>(smem + CF::INV + w * 1024);
                 put_inv(inv, lane, inverse16(diag, reinterpret_cast<float*>(inv), lane));
             }
         }
         __syncthreads();
+        if (!mine) {
+            if (hh + 1 < at.nh) __syncthreads();
+            continue;
+        }
         // ---- this head's operands; then the next head's are asked for ----
         f32x4 xr[NK];
         u64 badx = 0;
@@ -523,7 +521,7 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
         for (int kt = 0; kt <= NK; ++kt) u[kt] = zero4;
 #pragma unroll
         for (int f = 0; f < (NK + 1) / 2; ++f) {
-            if (!DELTA) xf[f] = pair8(y, xr[2 * f], NK > 1 ? xr[(2 * f + 1) % NK] : zero4);
+            if (!DELTA) xf[f] = pair8(y, xr[2 * f], 2 * f + 1 < NK ? xr[(2 * f + 1) % NK] : zero4);
             if (DELTA) split(join(zero4, zero4), uf[f]);
         }
 #pragma unroll
@@ -861,7 +859,8 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
     }
 }
 
-// Heads of a group that a work-group takes one after another.
+// Heads of a group that a work-group takes one after another: the fewest rounds of work-groups (as many at once as LDS lets
+// in, up to three a CU), each of which costs its heads and two more for what they share.
 inline int tree_heads(const Args& a, int slabs, int lds0, int lds_head) {
     const int hg = a.H / a.G;
     int best = 1;
@@ -876,9 +875,10 @@ inline int tree_heads(const Args& a, int slabs, int lds0, int lds_head) {
 }
 
 template <typename T, int N, bool DELTA, int NK>
-int launch_tree(const Args& a, int waves) {
+int launch_tree(const Args& a) {
     typedef TreeCfg<T, N, DELTA, NK> CF;
-    const int slabs = a.P / (16 * waves), hg = a.H / a.G, hb = tree_heads(a, slabs, CF::C, CF::HEAD);
+    const int cols = a.P < 64 ? a.P / 16 : 4, waves = cols > NK ? cols : NK;
+    const int slabs = a.P / (16 * cols), hg = a.H / a.G, hb = tree_heads(a, slabs, CF::C, CF::HEAD);
     const size_t lds = CF::total(hb);
     if (!delta::lds_limit(k_tree<T, N, DELTA, NK>, lds)) return 7;
     k_tree<T, N, DELTA, NK><<<(unsigned)(a.b * a.G * ((hg + hb - 1) / hb) * slabs), 64 * waves, lds, a.stream>>>(a, hb);
@@ -886,10 +886,11 @@ int launch_tree(const Args& a, int waves) {
 }
 template <typename T, int N, bool DELTA>
 int run_tree_n(const Args& a) {
+    if (a.T <= 16) return launch_tree<T, N, DELTA, 1>(a);
+    if (a.T <= 32) return launch_tree<T, N, DELTA, 2>(a);
+    if (a.T <= 48) return launch_tree<T, N, DELTA, 3>(a);
+    if (a.T <= kPanel) return launch_tree<T, N, DELTA, 4>(a);
     const int waves = a.P < 64 ? a.P / 16 : 4;
-    if (a.T <= 16) return launch_tree<T, N, DELTA, 1>(a, waves);
-    if (a.T <= 32) return launch_tree<T, N, DELTA, 2>(a, waves);
-    if (a.T <= kPanel) return launch_tree<T, N, DELTA, 4>(a, waves);
     const size_t lds = (size_t)LongLds((int)a.T, waves, DELTA).total;
     if (!delta::lds_limit(k_tree_long<T, N, DELTA>, lds)) return 7;
     k_tree_long<T, N, DELTA><<<(unsigned)(a.b * a.H * (a.P / (16 * waves))), 64 * waves, lds, a.stream>>>(a);
