@@ -247,16 +247,16 @@ struct Place {
     int64_t bi;
     int g, h0, nh, p0;
     __device__ Place(const Args& a, int hb, int cols, int w) {
-        const int hg = a.H / a.G, slabs = a.P / (16 * cols), chunks = (hg + hb - 1) / hb, nb = gridDim.x;
-        int64_t id = nb % 8 == 0 ? (int64_t)(blockIdx.x % 8) * (nb / 8) + blockIdx.x / 8 : blockIdx.x;
+        const unsigned hg = a.H / a.G, slabs = a.P / (16 * cols), chunks = (hg + hb - 1) / hb, nb = gridDim.x;
+        unsigned id = nb % 8 == 0 ? blockIdx.x % 8 * (nb / 8) + blockIdx.x / 8 : blockIdx.x;
         p0 = ((int)(id % slabs) * cols + w) * 16;
         id /= slabs;
-        const int chunk = (int)(id % chunks);
+        const unsigned chunk = id % chunks;
         id /= chunks;
         g = (int)(id % a.G);
         bi = id / a.G;
-        h0 = g * hg + chunk * hb;
-        nh = hg - chunk * hb < hb ? hg - chunk * hb : hb;
+        h0 = (int)(g * hg + chunk * hb);
+        nh = (int)(hg - chunk * hb < (unsigned)hb ? hg - chunk * hb : hb);
     }
 };
 
@@ -320,13 +320,6 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
     const T* beta = static_cast<const T*>(a.beta);
     const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
     const int slot = a.slots[at.bi];
-    if (slot < 0 || slot >= a.S) {
-        if (mine)
-            for (int hh = 0; hh < at.nh; ++hh)
-                for (int k0 = 0; k0 < K; k0 += 16)
-                    store_y(static_cast<T*>(a.y) + (row0 * H + at.h0 + hh) * P + at.p0, ys, k0, K, lane, sel, upper, zero4);
-        return;
-    }
     const bool has = N >= 32 || q < 2;  // (dstate 16 fills half a fragment)
     const int n0 = 8 * (N >= 32 ? q : q & 1);
     // the state's rows as operands: lane (q, l16) holds row p0 + l16, elements 32 ks + 8 q .. + 7; and x
@@ -357,55 +350,61 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
         dtv[i] = a.dt[k];
         btv[i] = DELTA ? to_f(beta[k]) : 0.f;
     }
+    F8 cf[KS], bf[KS];  // the rows of this wave's node tile
+    if (tiled) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            cf[ks] = frag(Cm, a.cs, 16 * w + l16, ks);
+            bf[ks] = frag(Bm, a.bs, 16 * w + l16, ks);
+        }
+    }
+    // (all of the above is on its way before the slot is looked at)
+    if (slot < 0 || slot >= a.S) {
+        if (mine)
+            for (int hh = 0; hh < at.nh; ++hh)
+                for (int k0 = 0; k0 < K; k0 += 16)
+                    store_y(static_cast<T*>(a.y) + (row0 * H + at.h0 + hh) * P + at.p0, ys, k0, K, lane, sel, upper, zero4);
+        return;
+    }
     f32x4 gcr[NK], gbr[NK];  // the delta rule's B C^T and B B^T of this wave's node tile
 #pragma unroll
     for (int jt = 0; jt < NK; ++jt) gcr[jt] = gbr[jt] = zero4;
-    {
-        F8 cf[KS], bf[KS];
-        if (tiled) {
+    if (mine) fetch(at.h0);  // (behind what the products wait for)
+    if (tiled) {
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                cf[ks] = frag(Cm, a.cs, 16 * w + l16, ks);
-                bf[ks] = frag(Bm, a.bs, 16 * w + l16, ks);
-            }
+        for (int ks = 0; ks < KS; ++ks) {
+            if (CF::LCB) st8(crow + ((w * KS + ks) * 64 + lane) * 8, cf[ks]);
+            if (CF::LCB || !DELTA) st8(brow + ((w * KS + ks) * 64 + lane) * 8, bf[ks]);
         }
-        if (mine) fetch(at.h0);  // (behind what the products wait for)
-        if (tiled) {
+    }
+    __syncthreads();
+    if (tiled) {
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                if (CF::LCB) st8(crow + ((w * KS + ks) * 64 + lane) * 8, cf[ks]);
-                if (CF::LCB || !DELTA) st8(brow + ((w * KS + ks) * 64 + lane) * 8, bf[ks]);
-            }
-        }
-        __syncthreads();
-        if (tiled) {
+        for (int jt = 0; jt < NK; ++jt)
+            if (jt <= w) {
+                f32x4 c = zero4, b = zero4;
 #pragma unroll
-            for (int jt = 0; jt < NK; ++jt)
-                if (jt <= w) {
-                    f32x4 c = zero4, b = zero4;
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        const F8 bj = CF::LCB || !DELTA ? kept(brow, jt, ks) : frag(Bm, a.bs, 16 * jt + l16, ks);
-                        c = mma(c, bj, cf[ks]);
-                        if (DELTA) b = mma(b, bj, bf[ks]);
-                    }
-                    settle(c);
-                    if (DELTA) {
-                        settle(b);
-                        gcr[jt] = c;
-                        gbr[jt] = b;
-                        if (jt == w) {
-                            // |B_k|^2 on the diagonal tells whether the row is finite
-                            const float d = l16 & 2 ? (l16 & 1 ? b[3] : b[2]) : (l16 & 1 ? b[1] : b[0]);
-                            u64 who = __ballot(q == l16 >> 2 && odd_bits(d));
-                            who |= who >> 32;
-                            if (lane == 0) badb[w] = ((who | who >> 16) & 0xffff) << (16 * w);
-                        }
-                    } else {
-                        st4(gc + (w * (w + 1) / 2 + jt) * 256 + lane * 4, c);
-                    }
+                for (int ks = 0; ks < KS; ++ks) {
+                    const F8 bj = CF::LCB || !DELTA ? kept(brow, jt, ks) : frag(Bm, a.bs, 16 * jt + l16, ks);
+                    c = mma(c, bj, cf[ks]);
+                    if (DELTA) b = mma(b, bj, bf[ks]);
                 }
-        }
+                settle(c);
+                if (DELTA) {
+                    settle(b);
+                    gcr[jt] = c;
+                    gbr[jt] = b;
+                    if (jt == w) {
+                        // |B_k|^2 on the diagonal tells whether the row is finite
+                        const float d = l16 & 2 ? (l16 & 1 ? b[3] : b[2]) : (l16 & 1 ? b[1] : b[0]);
+                        u64 who = __ballot(q == l16 >> 2 && odd_bits(d));
+                        who |= who >> 32;
+                        if (lane == 0) badb[w] = ((who | who >> 16) & 0xffff) << (16 * w);
+                    }
+                } else {
+                    st4(gc + (w * (w + 1) / 2 + jt) * 256 + lane * 4, c);
+                }
+            }
     }
     // the paths, by doubling: pr[r] is the node 2^r above
     bool there = lane < K && par >= -1 && par < lane;
