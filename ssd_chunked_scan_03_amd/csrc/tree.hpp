@@ -114,22 +114,26 @@ struct TreeCfg {
     static __device__ int at(int kt) { return kt < 2 ? kt * 2048 : (kt - 1) * kTableBytes; }
 };
 
-// More nodes, in panels of 64.  kp: nodes rounded up to panels.
+// More nodes, in panels of 64.  kp: nodes rounded up to panels.  Where they fit (STG), the rows of the panel in
+// work go through LDS: x1 holds its C, then B of one earlier panel after another, then the inverses; x2 its own B.
+template <typename T, int N, bool DELTA>
+struct LongCfg {
+    static constexpr int KS = N < 32 ? 1 : N / 32;
+    static constexpr int ROWS = 4 * KS * 512 * (int)sizeof(T);
+    static constexpr bool STG = 2 * ROWS <= 65536;
+    static constexpr int M = 0, TT = 4 * kTableBytes, X1 = TT + (DELTA ? 4 * kTableBytes : 0);
+    static constexpr int X2 = X1 + (STG && ROWS > 4096 ? ROWS : 4096), MASK = X2 + (STG ? ROWS : 0);
+};
 struct LongLds {
-    int m, t, inv, mask, c, e, beta, ptr, badx, u, total;
-    __host__ __device__ LongLds(int K, int waves, bool rule_delta) {
+    int mask, c, e, beta, badx, u, total;
+    __host__ __device__ LongLds(int mask0, int K, bool rule_delta) : mask(mask0) {
         const int kp = (K + kPanel - 1) / kPanel * kPanel, panels = kp / kPanel;
-        m = 0;
-        t = m + 4 * kTableBytes;
-        inv = t + (rule_delta ? 4 * kTableBytes : 0);
-        mask = inv + (rule_delta ? 4 * 1024 : 0);      // [node][panel]
-        c = mask + kp * panels * 8;
+        c = mask + kp * panels * 8;                    // mask: [node][panel]
         e = c + kp * 8;
         beta = e + kp * 4;
-        ptr = beta + (rule_delta ? kp * 4 : 0);        // [node] while the paths are formed
-        badx = ptr + kp * 4;                           // [panel][column] nodes whose x is not finite
-        u = badx + panels * waves * 16 * 8;            // [panel][wave] u of the panels before the last
-        total = u + (rule_delta ? (panels - 1) * waves * kTableBytes : 0);
+        badx = beta + (rule_delta ? kp * 4 : 0);       // [panel][column] nodes whose x is not finite
+        u = badx + panels * 64 * 8;                    // [panel][wave] u of the panels before the last
+        total = u + (rule_delta ? (panels - 1) * 4 * kTableBytes : 0);
     }
 };
 
@@ -570,27 +574,34 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
 }
 
 // ---------------------------------------------------------------------------
-// k_tree_long: trees of 65 to 256 nodes, one head a work-group, 64 nodes at a time against every panel of 64 up to their own.
+// k_tree_long: trees of 65 to 256 nodes, one head a work-group of four waves (cols of them with columns), 64 nodes at a time against
+// every panel of 64 up to their own.
 // ---------------------------------------------------------------------------
 template <typename T, int N, bool DELTA>
 __global__ __launch_bounds__(256) void k_tree_long(Args a) {
     typedef typename V8<T>::type F8;
-    constexpr int KS = N < 32 ? 1 : N / 32;
+    typedef LongCfg<T, N, DELTA> CF;
+    constexpr int KS = CF::KS;
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    const int waves = blockDim.x >> 6, K = (int)a.T, P = a.P, H = a.H;
+    const int K = (int)a.T, P = a.P, H = a.H, cols = P < 64 ? P / 16 : 4;
     const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
-    const Place place(a, 1, waves, w);
+    const Place place(a, 1, cols, w);
     const int64_t row0 = place.bi * K, ys = (int64_t)H * P;
     const int g = place.g, h = place.h0, p0 = place.p0;
     const unsigned sel = delta::quad_sel(lane);
-    const bool upper = (lane & 2) != 0;
+    const bool upper = (lane & 2) != 0, mine = w < cols;
     const int kp = (K + kPanel - 1) / kPanel * kPanel, panels = kp / kPanel;
-    const LongLds at(K, waves, DELTA);
+    const LongLds at(CF::MASK, K, DELTA);
+    T* mt = reinterpret_cast<T*>(smem + CF::M);
+    T* tt = reinterpret_cast<T*>(smem + CF::TT);
+    T* x1 = reinterpret_cast<T*>(smem + CF::X1);
+    T* x2 = reinterpret_cast<T*>(smem + CF::X2);
+    constexpr int TAB = kTableBytes / (int)sizeof(T);
     u64* mask = reinterpret_cast<u64*>(smem + at.mask);
     double* cs = reinterpret_cast<double*>(smem + at.c);
     float* decay = reinterpret_cast<float*>(smem + at.e);
     float* betas = reinterpret_cast<float*>(smem + at.beta);
-    int* ptr = reinterpret_cast<int*>(smem + at.ptr);
+    int* ptr = reinterpret_cast<int*>(smem + CF::M);  // [node], in M's place while the paths are formed
     u64* badx = reinterpret_cast<u64*>(smem + at.badx);
     const T* x = static_cast<const T*>(a.x) + row0 * a.xs + h * P + p0;
     const T* Bm = static_cast<const T*>(a.B) + row0 * a.bs + g * N;
@@ -600,24 +611,37 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
     const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
     const int slot = a.slots[place.bi];
     if (slot < 0 || slot >= a.S) {
-        for (int k0 = 0; k0 < K; k0 += 16) store_y(y, ys, k0, K, lane, sel, upper, zero4);
+        if (mine)
+            for (int k0 = 0; k0 < K; k0 += 16) store_y(y, ys, k0, K, lane, sel, upper, zero4);
         return;
     }
     const bool has = N >= 32 || q < 2;
     const int n0 = 8 * (N >= 32 ? q : q & 1);
     f32x8 hf[KS];
-    const float* hp = a.pool + slot * a.ss + (int64_t)(h * P + p0 + l16) * N + n0;
+    {
+        const float* hp = a.pool + slot * a.ss + (int64_t)(h * P + (mine ? p0 + l16 : 0)) * N + n0;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) hf[ks] = ld8(hp + 32 * ks);
+        for (int ks = 0; ks < KS; ++ks) hf[ks] = ld8(hp + 32 * ks);
+    }
     auto frag = [&](const T* m, int64_t stride, int node, int ks) {
         const F8 v = ld8(m + (int64_t)(node < K ? node : K - 1) * stride + 32 * ks + n0);
         return N >= 32 ? v : sel8(has, v);
     };
+    auto kept = [&](const T* rows, int tile, int ks) { return ld8(rows + ((tile * KS + ks) * 64 + lane) * 8); };
+    // rows of this wave's node tile of a panel
+    auto rows_of = [&](const T* m, int64_t stride, int j0, F8 (&v)[KS]) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) v[ks] = frag(m, stride, j0 + 16 * w + l16, ks);
+    };
+    auto keep = [&](T* rows, const F8 (&v)[KS]) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) st8(rows + ((w * KS + ks) * 64 + lane) * 8, v[ks]);
+    };
     constexpr int R = N / 8;
     const double Ah = (double)a.A[h] * 1.4426950408889634;
-    for (int i = lane; i < 16 * panels; i += 64) badx[((i >> 4) * waves + w) * 16 + (i & 15)] = 0;
+    for (int i = tid; i < 64 * panels; i += 256) badx[i] = 0;
     // N / 8 lanes a node: for the delta rule its row of B as well
-    for (int k0 = 0; k0 < kp; k0 += (int)blockDim.x / R) {
+    for (int k0 = 0; k0 < kp; k0 += 256 / R) {
         const int k = k0 + tid / R;
         const bool in = k < K;
         const bool odd = DELTA && in && any_odd(ld8(Bm + (int64_t)(in ? k : 0) * a.bs + 8 * (tid % R)));
@@ -639,44 +663,28 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
         }
     }
     __syncthreads();
-    // the paths, by doubling; a node is absent below an absent one, and not computable below such a one
+    // the paths, by doubling, a thread a node; a node is absent below an absent one, and not computable below such a one
     for (int reach = 1; reach < K; reach *= 2) {
-        double c[4];
-        int up[4];
-        float d[4];
-        u64 m[4][4];
-        // (at most four nodes a thread: 256 nodes, 64 threads)
+        const int k = tid < kp ? tid : 0, p = ptr[k], from = p < 0 ? k : p;
+        const double c = p < 0 ? cs[k] : cs[k] + cs[from];
+        const int up = p < 0 ? -1 : ptr[from];
+        const float self = decay[k], theirs = decay[from];
+        u64 m[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int k = tid + i * (int)blockDim.x;
-            if (k < kp) {
-                const int p = ptr[k], from = p < 0 ? k : p;
-                c[i] = p < 0 ? cs[k] : cs[k] + cs[from];
-                up[i] = p < 0 ? -1 : ptr[from];
-                const float mine = decay[k], theirs = decay[from];
-                d[i] = mine == -1.f || theirs == -1.f ? -1.f : mine < theirs ? mine : theirs;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j < panels) m[i][j] = mask[k * panels + j] | mask[from * panels + j];
-            }
-        }
+        for (int j = 0; j < 4; ++j)
+            if (j < panels) m[j] = mask[k * panels + j] | mask[from * panels + j];
         __syncthreads();
+        if (tid < kp) {
+            cs[k] = c;
+            ptr[k] = up;
+            decay[k] = self == -1.f || theirs == -1.f ? -1.f : self < theirs ? self : theirs;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int k = tid + i * (int)blockDim.x;
-            if (k < kp) {
-                cs[k] = c[i];
-                ptr[k] = up[i];
-                decay[k] = d[i];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j < panels) mask[k * panels + j] = m[i][j];
-            }
+            for (int j = 0; j < 4; ++j)
+                if (j < panels) mask[k * panels + j] = m[j];
         }
         __syncthreads();
     }
-    for (int k = tid; k < kp; k += (int)blockDim.x)
-        if (!(decay[k] < 0.f)) decay[k] = exp2f_fast((float)cs[k]);
+    if (tid < kp && !(decay[tid] < 0.f)) decay[tid] = exp2f_fast((float)cs[tid]);
     __syncthreads();
 
     const float nan = __builtin_nanf("");
@@ -688,7 +696,7 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
         const f32x4 v = clean_x(open_x(load_x(x, a.xs, k0, K, lane), sel, upper), decay + k0 + 4 * q, odd);
         if (__ballot(odd != 0)) {
             anybad = true;
-            if (odd) atomicOr(&badx[((k0 >> 6) * waves + w) * 16 + l16], (u64)odd << ((k0 & 63) + 4 * q));
+            if (odd) atomicOr(&badx[(k0 >> 6) * 64 + 16 * w + l16], (u64)odd << ((k0 & 63) + 4 * q));
             wave_sync();
         }
         return v;
@@ -696,20 +704,30 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
     Op<T> hs[KS];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) split(N >= 32 ? hf[ks] : sel8(has, hf[ks]), hs[ks]);
+    F8 cf[KS], bf[KS], bn[KS];  // this wave's node tile: C, B; and of the next panel's B
     for (int s = 0; s < panels; ++s) {
         const int q0 = s * kPanel, nk = (K - q0 + 15) / 16 < 4 ? (K - q0 + 15) / 16 : 4;
+        rows_of(Cm, a.cs, q0, cf);
+        rows_of(Bm, a.bs, q0, bf);
+        if (CF::STG) {
+            if (s > 0) __syncthreads();  // x1 and x2 are free
+            keep(x1, cf);
+            keep(x2, bf);
+            __syncthreads();
+            if (s > 0) rows_of(Bm, a.bs, 0, bn);
+        }
         f32x4 O[4], Rt[4], xt[4];
         // ---- what the held state gives: O = diag(E) C h^T, Rt = beta (x - diag(E) B h^T) ----
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt) {
             O[kt] = Rt[kt] = xt[kt] = zero4;
-            if (kt < nk) {
+            if (kt < nk && mine) {
                 const int k0 = q0 + 16 * kt;
                 f32x4 o = zero4, v = zero4;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    o = mul(o, frag(Cm, a.cs, k0 + l16, ks), hs[ks]);
-                    if (DELTA) v = mul(v, frag(Bm, a.bs, k0 + l16, ks), hs[ks]);
+                    o = mul(o, CF::STG ? kept(x1, kt, ks) : frag(Cm, a.cs, k0 + l16, ks), hs[ks]);
+                    if (DELTA) v = mul(v, CF::STG ? kept(x2, kt, ks) : frag(Bm, a.bs, k0 + l16, ks), hs[ks]);
                 }
                 const f32x4 e4 = ld4(decay + k0 + 4 * q);
                 settle(o);
@@ -726,21 +744,19 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
         for (int sp = 0; sp <= s; ++sp) {
             const bool own = sp == s;
             const int j0 = sp * kPanel;
-            if (s > 0) __syncthreads();  // the tables are free
-            // ---- M and T of this wave's node tiles against panel sp ----
-            for (int kt = w; kt < nk; kt += waves) {
-                T* mt = reinterpret_cast<T*>(smem + at.m + kt * kTableBytes);
-                T* tt = reinterpret_cast<T*>(smem + at.t + kt * kTableBytes);
-                F8 cf[KS], bf[KS];
-                const int k = q0 + 16 * kt + l16, jn = own ? kt + 1 : 4;
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    cf[ks] = frag(Cm, a.cs, k, ks);
-                    if (DELTA) bf[ks] = frag(Bm, a.bs, k, ks);
-                }
+            // the tables are free, and so is x1 (the products with C, or the panel before, are done)
+            if (s > 0 || (CF::STG && DELTA)) __syncthreads();
+            if (CF::STG && !own && sp == 0) {
+                keep(x1, bn);
+                __syncthreads();
+            }
+            // ---- M and T of this wave's node tile against panel sp ----
+            if (w < nk) {
+                const int k = q0 + 16 * w + l16, jn = own ? w + 1 : 4;
                 const u64 on = decay[k] < 0.f ? 0 : mask[k * panels + sp];
                 const double ck = cs[k];
                 const float bk = DELTA ? betas[k] : 0.f;
+                const T* bj0 = own ? x2 : x1;
                 f32x4 diag = zero4;
                 for (int jt = 0; jt < ((jn + 1) & ~1); ++jt) {
                     f32x4 m = zero4, t = zero4;
@@ -748,7 +764,7 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
                         f32x4 c = zero4, b = zero4;
 #pragma unroll
                         for (int ks = 0; ks < KS; ++ks) {
-                            const F8 bj = frag(Bm, a.bs, j0 + 16 * jt + l16, ks);
+                            const F8 bj = CF::STG ? kept(bj0, jt, ks) : frag(Bm, a.bs, j0 + 16 * jt + l16, ks);
                             c = mma(c, bj, cf[ks]);
                             if (DELTA) b = mma(b, bj, bf[ks]);
                         }
@@ -757,21 +773,24 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
                         weigh<DELTA>((unsigned)(on >> (16 * jt + 4 * q)) & 15u, ck, cs + j0 + 16 * jt + 4 * q, bk,
                                      k - j0 - 16 * jt - 4 * q, c, b, m, t);
                     }
-                    put(mt, jt >> 1, jt & 1, lane, m);
+                    put(mt + w * TAB, jt >> 1, jt & 1, lane, m);
                     if (DELTA) {
-                        if (own && jt == kt) {
+                        if (own && jt == w) {
                             diag = t;
                             t = zero4;
                         }
-                        put(tt, jt >> 1, jt & 1, lane, t);
+                        put(tt + w * TAB, jt >> 1, jt & 1, lane, t);
                     }
                 }
                 if (DELTA && own) {
-                    T* inv = reinterpret_cast<T*>(smem + at.inv + kt * 1024);
+                    T* inv = x1 + w * 1024 / (int)sizeof(T);
                     put_inv(inv, lane, inverse16(diag, reinterpret_cast<float*>(inv), lane));
                 }
             }
+            if (CF::STG && sp + 1 < s) rows_of(Bm, a.bs, j0 + kPanel, bn);
             __syncthreads();
+            if (CF::STG && sp + 1 < s) keep(x1, bn);  // (read behind the next barrier)
+            if (!mine) continue;
             // ---- panel sp's part of Rt and O ----
             if constexpr (!DELTA) {
                 F8 xf[2];
@@ -782,14 +801,13 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
 #pragma unroll
                 for (int kt = 0; kt < 4; ++kt)
                     if (kt < nk) {
-                        const T* mt = reinterpret_cast<const T*>(smem + at.m + kt * kTableBytes);
-                        O[kt] = mul(O[kt], get(mt, 0, lane), xf[0]);
-                        if (!own || kt >= 2) O[kt] = mul(O[kt], get(mt, 1, lane), xf[1]);
+                                                O[kt] = mul(O[kt], get(mt + kt * TAB, 0, lane), xf[0]);
+                        if (!own || kt >= 2) O[kt] = mul(O[kt], get(mt + kt * TAB, 1, lane), xf[1]);
                         settle(O[kt]);
                     }
             } else {
                 Op<T> uf[2];
-                T* us = reinterpret_cast<T*>(smem + at.u + (sp * waves + w) * kTableBytes);
+                T* us = reinterpret_cast<T*>(smem + at.u + (sp * 4 + w) * kTableBytes);
                 if (own) {
                     f32x4 u[4] = {zero4, zero4, zero4, zero4};
                     split(join(zero4, zero4), uf[0]);
@@ -797,12 +815,11 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
 #pragma unroll
                     for (int kt = 0; kt < 4; ++kt)
                         if (kt < nk) {
-                            const T* tt = reinterpret_cast<const T*>(smem + at.t + kt * kTableBytes);
-                            f32x4 t = zero4;
+                                                        f32x4 t = zero4;
 #pragma unroll
                             for (int f = 0; f < 2; ++f)
-                                if (2 * f < kt) t = mul(t, get(tt, f, lane), uf[f]);
-                            u[kt] = times_inv(reinterpret_cast<const T*>(smem + at.inv + kt * 1024), lane, Rt[kt] - t);
+                                if (2 * f < kt) t = mul(t, get(tt + kt * TAB, f, lane), uf[f]);
+                            u[kt] = times_inv(x1 + kt * 1024 / (int)sizeof(T), lane, Rt[kt] - t);
                             split(join(u[kt & ~1], u[kt | 1]), uf[kt >> 1]);
                         }
                     if (s + 1 < panels) {
@@ -817,8 +834,7 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
 #pragma unroll
                     for (int kt = 0; kt < 4; ++kt)
                         if (kt < nk) {
-                            const T* tt = reinterpret_cast<const T*>(smem + at.t + kt * kTableBytes);
-                            f32x4 t = mul(mul(zero4, get(tt, 0, lane), uf[0]), get(tt, 1, lane), uf[1]);
+                                                        f32x4 t = mul(mul(zero4, get(tt + kt * TAB, 0, lane), uf[0]), get(tt + kt * TAB, 1, lane), uf[1]);
                             settle(t);
                             Rt[kt] -= t;
                         }
@@ -826,9 +842,8 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
 #pragma unroll
                 for (int kt = 0; kt < 4; ++kt)
                     if (kt < nk) {
-                        const T* mt = reinterpret_cast<const T*>(smem + at.m + kt * kTableBytes);
-                        O[kt] = mul(O[kt], get(mt, 0, lane), uf[0]);
-                        if (!own || kt >= 2) O[kt] = mul(O[kt], get(mt, 1, lane), uf[1]);
+                                                O[kt] = mul(O[kt], get(mt + kt * TAB, 0, lane), uf[0]);
+                        if (!own || kt >= 2) O[kt] = mul(O[kt], get(mt + kt * TAB, 1, lane), uf[1]);
                         settle(O[kt]);
                     }
             }
@@ -836,7 +851,7 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
         // ---- y ----
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt)
-            if (kt < nk) {
+            if (kt < nk && mine) {
                 const int k0 = q0 + 16 * kt;
                 const f32x4 e4 = ld4(decay + k0 + 4 * q);
                 f32x4 v;
@@ -849,7 +864,7 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         u64 hit = 0;  // a bad x on the node's path
-                        for (int i = 0; i <= s; ++i) hit |= mask[(k0 + 4 * q + e) * panels + i] & badx[(i * waves + w) * 16 + l16];
+                        for (int i = 0; i <= s; ++i) hit |= mask[(k0 + 4 * q + e) * panels + i] & badx[i * 64 + 16 * w + l16];
                         if (hit && !(e4[e] < 0.f)) v[e] = nan;
                     }
                 }
@@ -889,10 +904,9 @@ int run_tree_n(const Args& a) {
     if (a.T <= 32) return launch_tree<T, N, DELTA, 2>(a);
     if (a.T <= 48) return launch_tree<T, N, DELTA, 3>(a);
     if (a.T <= kPanel) return launch_tree<T, N, DELTA, 4>(a);
-    const int waves = a.P < 64 ? a.P / 16 : 4;
-    const size_t lds = (size_t)LongLds((int)a.T, waves, DELTA).total;
+    const size_t lds = (size_t)LongLds(LongCfg<T, N, DELTA>::MASK, (int)a.T, DELTA).total;
     if (!delta::lds_limit(k_tree_long<T, N, DELTA>, lds)) return 7;
-    k_tree_long<T, N, DELTA><<<(unsigned)(a.b * a.H * (a.P / (16 * waves))), 64 * waves, lds, a.stream>>>(a);
+    k_tree_long<T, N, DELTA><<<(unsigned)(a.b * a.H * (a.P > 64 ? a.P / 64 : 1)), 256, lds, a.stream>>>(a);
     return hipGetLastError() == hipSuccess ? 0 : 7;
 }
 template <typename T, bool DELTA>
