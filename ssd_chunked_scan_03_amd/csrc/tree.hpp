@@ -121,6 +121,7 @@ struct LongCfg {
     static constexpr int KS = N < 32 ? 1 : N / 32;
     static constexpr int ROWS = 4 * KS * 512 * (int)sizeof(T);
     static constexpr bool STG = 2 * ROWS <= 65536;
+    static constexpr int OCC = DELTA || ROWS > 16384 ? 1 : 2;  // work-groups on a CU at the largest trees, by LDS
     static constexpr int M = 0, TT = 4 * kTableBytes, X1 = TT + (DELTA ? 4 * kTableBytes : 0);
     static constexpr int X2 = X1 + (STG && ROWS > 4096 ? ROWS : 4096), MASK = X2 + (STG ? ROWS : 0);
 };
@@ -161,6 +162,16 @@ __device__ __forceinline__ void wave_sync() {
 // matrix instruction has written them (seen: a read one instruction later, where eight have to lie between),
 // so the wait is stated here.
 __device__ __forceinline__ void settle(f32x4& v) { asm volatile("s_nop 7\n\ts_nop 3" : "+v"(v)); }
+
+// All of v has arrived here: its reads go out together ahead of this, and not one by one between the products
+// (which cost an LDS latency each).
+template <typename F8, int KS>
+__device__ __forceinline__ void together(F8 (&v)[KS]) {
+    if constexpr (KS == 1) asm volatile("" : "+v"(v[0]));
+    else if constexpr (KS == 2) asm volatile("" : "+v"(v[0]), "+v"(v[1]));
+    else if constexpr (KS == 4) asm volatile("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]));
+    else asm volatile("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]), "+v"(v[5]), "+v"(v[6]), "+v"(v[7]));
+}
 
 // (I + t)^-1 of a strictly lower 16 x 16 tile: lane (q, k) holds t[k][4 q + e] and gets the inverse's.
 // Row by row: X_k = e_k - sum_{j < k} t_kj X_j, row j of X from its lanes to all by DPP.
@@ -387,11 +398,14 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
         for (int jt = 0; jt < NK; ++jt)
             if (jt <= w) {
                 f32x4 c = zero4, b = zero4;
+                F8 bj[KS];
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) bj[ks] = CF::LCB || !DELTA ? kept(brow, jt, ks) : frag(Bm, a.bs, 16 * jt + l16, ks);
+                together(bj);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    const F8 bj = CF::LCB || !DELTA ? kept(brow, jt, ks) : frag(Bm, a.bs, 16 * jt + l16, ks);
-                    c = mma(c, bj, cf[ks]);
-                    if (DELTA) b = mma(b, bj, bf[ks]);
+                    c = mma(c, bj[ks], cf[ks]);
+                    if (DELTA) b = mma(b, bj[ks], bf[ks]);
                 }
                 settle(c);
                 if (DELTA) {
@@ -531,10 +545,18 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
         for (int kt = 0; kt < NK; ++kt) {
             const int k0 = 16 * kt;
             f32x4 o = zero4, v = zero4;
+            F8 fc[KS], fb[KS];
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                o = mul(o, CF::LCB ? kept(crow, kt, ks) : frag(Cm, a.cs, k0 + l16, ks), hs[ks]);
-                if (DELTA) v = mul(v, CF::LCB ? kept(brow, kt, ks) : frag(Bm, a.bs, k0 + l16, ks), hs[ks]);
+                fc[ks] = CF::LCB ? kept(crow, kt, ks) : frag(Cm, a.cs, k0 + l16, ks);
+                if (DELTA) fb[ks] = CF::LCB ? kept(brow, kt, ks) : frag(Bm, a.bs, k0 + l16, ks);
+            }
+            together(fc);
+            if (DELTA) together(fb);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                o = mul(o, fc[ks], hs[ks]);
+                if (DELTA) v = mul(v, fb[ks], hs[ks]);
             }
             const f32x4 e4 = ld4(decay + hh * 64 + k0 + 4 * q);
             o *= e4;
@@ -578,7 +600,8 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
 // every panel of 64 up to their own.
 // ---------------------------------------------------------------------------
 template <typename T, int N, bool DELTA>
-__global__ __launch_bounds__(256) void k_tree_long(Args a) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(LongCfg<T, N, DELTA>::OCC, LongCfg<T, N, DELTA>::OCC)))
+void k_tree_long(Args a) {
     typedef typename V8<T>::type F8;
     typedef LongCfg<T, N, DELTA> CF;
     constexpr int KS = CF::KS;
@@ -637,32 +660,43 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) st8(rows + ((w * KS + ks) * 64 + lane) * 8, v[ks]);
     };
-    constexpr int R = N / 8;
-    const double Ah = (double)a.A[h] * 1.4426950408889634;
     for (int i = tid; i < 64 * panels; i += 256) badx[i] = 0;
-    // N / 8 lanes a node: for the delta rule its row of B as well
-    for (int k0 = 0; k0 < kp; k0 += 256 / R) {
-        const int k = k0 + tid / R;
-        const bool in = k < K;
-        const bool odd = DELTA && in && any_odd(ld8(Bm + (int64_t)(in ? k : 0) * a.bs + 8 * (tid % R)));
-        const u64 who = __ballot(odd) >> (lane / R * R);
-        if (k < kp && tid % R == 0) {
-            const double s = orders(in ? a.dt[(row0 + k) * H + h] : 0.f, Ah);
-            const int par = in ? a.parents[row0 + k] : -2;
-            const bool ok = par >= -1 && par < k;
-            bool bad = false;
-            if (DELTA) {
-                const float bt = in ? to_f(beta[(row0 + k) * H + h]) : 0.f;
-                bad = (who & ((1ull << R) - 1)) != 0 || s != s || odd_bits(bt);
-                betas[k] = bt;
-            }
-            cs[k] = s;
-            ptr[k] = ok ? par : -1;
-            decay[k] = !ok ? -1.f : bad ? -2.f : 0.f;
-            for (int i = 0; i < panels; ++i) mask[k * panels + i] = i == k >> 6 ? 1ull << (k & 63) : 0;
+    if (tid < kp) {
+        const bool in = tid < K;
+        const double c = orders(in ? a.dt[(row0 + tid) * H + h] : 0.f, (double)a.A[h] * 1.4426950408889634);
+        const int par = in ? a.parents[row0 + tid] : -2;
+        const bool ok = par >= -1 && par < tid;
+        bool bad = false;
+        if (DELTA) {
+            const float bt = in ? to_f(beta[(row0 + tid) * H + h]) : 0.f;
+            bad = c != c || odd_bits(bt);
+            betas[tid] = bt;
         }
+        cs[tid] = c;
+        ptr[tid] = ok ? par : -1;
+        decay[tid] = !ok ? -1.f : bad ? -2.f : 0.f;
+        for (int i = 0; i < panels; ++i) mask[tid * panels + i] = i == tid >> 6 ? 1ull << (tid & 63) : 0;
     }
     __syncthreads();
+    if (DELTA) {
+        // nodes whose row of B is not finite: N / 8 lanes a node, eight pieces a lane on their way at once
+        constexpr int R = N / 8, PER = 256 / R;
+        for (int k0 = 0; k0 < K; k0 += 8 * PER) {
+            F8 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int k = k0 + i * PER + tid / R;
+                v[i] = ld8(Bm + (int64_t)(k < K ? k : K - 1) * a.bs + 8 * (tid % R));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int k = k0 + i * PER + tid / R;
+                const u64 who = __ballot(any_odd(v[i])) >> (lane / R * R);
+                if (k < K && tid % R == 0 && (who & ((1ull << R) - 1)) != 0 && decay[k] != -1.f) decay[k] = -2.f;
+            }
+        }
+        __syncthreads();
+    }
     // the paths, by doubling, a thread a node; a node is absent below an absent one, and not computable below such a one
     for (int reach = 1; reach < K; reach *= 2) {
         const int k = tid < kp ? tid : 0, p = ptr[k], from = p < 0 ? k : p;
@@ -724,10 +758,18 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
             if (kt < nk && mine) {
                 const int k0 = q0 + 16 * kt;
                 f32x4 o = zero4, v = zero4;
+                F8 fc[KS], fb[KS];
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    o = mul(o, CF::STG ? kept(x1, kt, ks) : frag(Cm, a.cs, k0 + l16, ks), hs[ks]);
-                    if (DELTA) v = mul(v, CF::STG ? kept(x2, kt, ks) : frag(Bm, a.bs, k0 + l16, ks), hs[ks]);
+                    fc[ks] = CF::STG ? kept(x1, kt, ks) : frag(Cm, a.cs, k0 + l16, ks);
+                    if (DELTA) fb[ks] = CF::STG ? kept(x2, kt, ks) : frag(Bm, a.bs, k0 + l16, ks);
+                }
+                together(fc);
+                if (DELTA) together(fb);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    o = mul(o, fc[ks], hs[ks]);
+                    if (DELTA) v = mul(v, fb[ks], hs[ks]);
                 }
                 const f32x4 e4 = ld4(decay + k0 + 4 * q);
                 settle(o);
@@ -762,11 +804,14 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
                     f32x4 m = zero4, t = zero4;
                     if (jt < jn) {
                         f32x4 c = zero4, b = zero4;
+                        F8 bj[KS];
+#pragma unroll
+                        for (int ks = 0; ks < KS; ++ks) bj[ks] = CF::STG ? kept(bj0, jt, ks) : frag(Bm, a.bs, j0 + 16 * jt + l16, ks);
+                        together(bj);
 #pragma unroll
                         for (int ks = 0; ks < KS; ++ks) {
-                            const F8 bj = CF::STG ? kept(bj0, jt, ks) : frag(Bm, a.bs, j0 + 16 * jt + l16, ks);
-                            c = mma(c, bj, cf[ks]);
-                            if (DELTA) b = mma(b, bj, bf[ks]);
+                            c = mma(c, bj[ks], cf[ks]);
+                            if (DELTA) b = mma(b, bj[ks], bf[ks]);
                         }
                         settle(c);
                         if (DELTA) settle(b);
