@@ -78,16 +78,15 @@ __device__ __forceinline__ void put_inv(bf16* tab, int lane, f32x4 v) {
     st8(tab + lane * 8, join(o[0], o[1]));
 }
 __device__ __forceinline__ void put_inv(float* tab, int lane, f32x4 v) { st4(tab + lane * 4, v); }
-__device__ __forceinline__ f32x4 times_inv(const bf16* tab, int lane, f32x4 v) {
+__device__ __forceinline__ bf16x8 get_inv(const bf16* tab, int lane) { return ld8(tab + lane * 8); }
+__device__ __forceinline__ f32x4 get_inv(const float* tab, int lane) { return ld4(tab + lane * 4); }
+__device__ __forceinline__ f32x4 times_inv(bf16x8 a, f32x4 v) {
     bf16x4 o[2];
     delta::split4<2>(v, o);
-    const bf16x8 a = ld8(tab + lane * 8);
     const bf16x4 zero = {};
     return mma(mma(f32x4{0.f, 0.f, 0.f, 0.f}, a, join(o[1], zero)), a, join(o[0], o[0]));
 }
-__device__ __forceinline__ f32x4 times_inv(const float* tab, int lane, f32x4 v) {
-    return delta::mma16(f32x4{0.f, 0.f, 0.f, 0.f}, ld4(tab + lane * 4), v);
-}
+__device__ __forceinline__ f32x4 times_inv(f32x4 a, f32x4 v) { return delta::mma16(f32x4{0.f, 0.f, 0.f, 0.f}, a, v); }
 
 constexpr int kTableBytes = 4096;  // of a node tile's M (or T) against a panel
 
@@ -121,19 +120,20 @@ struct LongCfg {
     static constexpr int KS = N < 32 ? 1 : N / 32;
     static constexpr int ROWS = 4 * KS * 512 * (int)sizeof(T);
     static constexpr bool STG = 2 * ROWS <= 65536;
-    static constexpr int OCC = DELTA || ROWS > 16384 ? 1 : 2;  // work-groups on a CU at the largest trees, by LDS
+    static constexpr int NB = KS * (int)sizeof(T) <= 16 ? 2 : 1;  // tiles of B in registers at a time
     static constexpr int M = 0, TT = 4 * kTableBytes, X1 = TT + (DELTA ? 4 * kTableBytes : 0);
     static constexpr int X2 = X1 + (STG && ROWS > 4096 ? ROWS : 4096), MASK = X2 + (STG ? ROWS : 0);
 };
 struct LongLds {
-    int mask, c, e, beta, badx, u, total;
+    int mask, c, e, beta, badx, badb, u, total;
     __host__ __device__ LongLds(int mask0, int K, bool rule_delta) : mask(mask0) {
         const int kp = (K + kPanel - 1) / kPanel * kPanel, panels = kp / kPanel;
         c = mask + kp * panels * 8;                    // mask: [node][panel]
         e = c + kp * 8;
         beta = e + kp * 4;
         badx = beta + (rule_delta ? kp * 4 : 0);       // [panel][column] nodes whose x is not finite
-        u = badx + panels * 64 * 8;                    // [panel][wave] u of the panels before the last
+        badb = badx + panels * 64 * 8;                 // [tile] nodes whose row of B is not finite
+        u = badb + 64;                                 // [panel][wave] u of the panels before the last
         total = u + (rule_delta ? (panels - 1) * 4 * kTableBytes : 0);
     }
 };
@@ -172,6 +172,9 @@ __device__ __forceinline__ void together(F8 (&v)[KS]) {
     else if constexpr (KS == 4) asm volatile("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]));
     else asm volatile("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]), "+v"(v[5]), "+v"(v[6]), "+v"(v[7]));
 }
+
+__device__ __forceinline__ void together(Op<bf16>& a) { asm volatile("" : "+v"(a.t[0]), "+v"(a.t[1])); }
+__device__ __forceinline__ void together(Op<float>& a) { asm volatile("" : "+v"(a.t[0])); }
 
 // (I + t)^-1 of a strictly lower 16 x 16 tile: lane (q, k) holds t[k][4 q + e] and gets the inverse's.
 // Row by row: X_k = e_k - sum_{j < k} t_kj X_j, row j of X from its lanes to all by DPP.
@@ -256,7 +259,8 @@ __device__ __forceinline__ double orders(float dt, double A) {
 
 typedef unsigned long long u64;
 
-// Which (row, group, heads, columns) a work-group takes; cols: its waves that have columns.  Blocks k, k + 8, ... run on one XCD: each takes a
+// Which (row, group, heads, columns) a work-group takes; cols: its waves that have columns (the others get addresses of
+// theirs, so that loads need no branch: behind one the compiler waits for everything that may be on its way).  Blocks k, k + 8, ... run on one XCD: each takes a
 // contiguous range, so that a row's B, C and dt stay in its L2.
 struct Place {
     int64_t bi;
@@ -264,7 +268,7 @@ struct Place {
     __device__ Place(const Args& a, int hb, int cols, int w) {
         const unsigned hg = a.H / a.G, slabs = a.P / (16 * cols), chunks = (hg + hb - 1) / hb, nb = gridDim.x;
         unsigned id = nb % 8 == 0 ? blockIdx.x % 8 * (nb / 8) + blockIdx.x / 8 : blockIdx.x;
-        p0 = ((int)(id % slabs) * cols + w) * 16;
+        p0 = ((int)(id % slabs) * cols + w % cols) * 16;
         id /= slabs;
         const unsigned chunk = id % chunks;
         id /= chunks;
@@ -327,6 +331,7 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
     T* brow = reinterpret_cast<T*>(smem + CF::BF);
     u64* mask = reinterpret_cast<u64*>(smem + CF::MASK);
     u64* badb = reinterpret_cast<u64*>(smem + CF::BADB);
+    float* skips = reinterpret_cast<float*>(smem + CF::BADB);  // [head] the scan's D (which has no use for badb)
     double* cs = reinterpret_cast<double*>(smem + CF::C);
     float* decay = reinterpret_cast<float*>(smem + CF::C + hb * 512);
     float* betas = reinterpret_cast<float*>(smem + CF::C + hb * 768);
@@ -365,13 +370,12 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
         dtv[i] = a.dt[k];
         btv[i] = DELTA ? to_f(beta[k]) : 0.f;
     }
+    const float skip = !DELTA && a.D ? a.D[at.h0 + (lane < at.nh ? lane : 0)] : 0.f;
     F8 cf[KS], bf[KS];  // the rows of this wave's node tile
-    if (tiled) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            cf[ks] = frag(Cm, a.cs, 16 * w + l16, ks);
-            bf[ks] = frag(Bm, a.bs, 16 * w + l16, ks);
-        }
+    for (int ks = 0; ks < KS; ++ks) {
+        cf[ks] = frag(Cm, a.cs, 16 * w + l16, ks);
+        bf[ks] = frag(Bm, a.bs, 16 * w + l16, ks);
     }
     // (all of the above is on its way before the slot is looked at)
     if (slot < 0 || slot >= a.S) {
@@ -384,7 +388,7 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
     f32x4 gcr[NK], gbr[NK];  // the delta rule's B C^T and B B^T of this wave's node tile
 #pragma unroll
     for (int jt = 0; jt < NK; ++jt) gcr[jt] = gbr[jt] = zero4;
-    if (mine) fetch(at.h0);  // (behind what the products wait for)
+    fetch(at.h0);  // (behind what the products wait for)
     if (tiled) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
@@ -440,7 +444,10 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
             rounds = r + 1;
         }
     }
-    if (w == 0) mask[lane] = mk;
+    if (w == 0) {
+        mask[lane] = mk;
+        if (!DELTA && lane < 16) skips[lane] = skip;
+    }
     if (DELTA) __syncthreads();
     for (int i = 0, hh = w; hh < at.nh; ++i, hh += waves) {
         float dt = dtv[0], bt = btv[0];
@@ -530,7 +537,7 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
         for (int ks = 0; ks < KS; ++ks) split(N >= 32 ? hf[ks] : sel8(has, hf[ks]), hs[ks]);
         if (hh + 1 < at.nh) fetch(h + 1);
         T* y = static_cast<T*>(a.y) + (row0 * H + h) * P + at.p0;
-        const float D = a.D ? a.D[h] : 0.f;
+        const float D = DELTA ? 0.f : skips[hh];
         F8 xf[(NK + 1) / 2];
         Op<T> uf[(NK + 1) / 2];
         f32x4 u[NK + 1];
@@ -551,32 +558,42 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
                 fc[ks] = CF::LCB ? kept(crow, kt, ks) : frag(Cm, a.cs, k0 + l16, ks);
                 if (DELTA) fb[ks] = CF::LCB ? kept(brow, kt, ks) : frag(Bm, a.bs, k0 + l16, ks);
             }
+            const f32x4 e4 = ld4(decay + hh * 64 + k0 + 4 * q);
+            Op<T> mo[2], to[2];
+#pragma unroll
+            for (int f = 0; 2 * f <= kt; ++f) {
+                mo[f] = get(mtab + CF::at(kt) / (int)sizeof(T), f, lane);
+                if (DELTA && 2 * f < kt) to[f] = get(ttab + CF::at(kt) / (int)sizeof(T), f, lane);
+            }
             together(fc);
             if (DELTA) together(fb);
+#pragma unroll
+            for (int f = 0; 2 * f <= kt; ++f) {
+                together(mo[f]);
+                if (DELTA && 2 * f < kt) together(to[f]);
+            }
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 o = mul(o, fc[ks], hs[ks]);
                 if (DELTA) v = mul(v, fb[ks], hs[ks]);
             }
-            const f32x4 e4 = ld4(decay + hh * 64 + k0 + 4 * q);
             o *= e4;
-            const T* mt = mtab + CF::at(kt) / (int)sizeof(T);
             if constexpr (DELTA) {
-                const T* tt = ttab + CF::at(kt) / (int)sizeof(T);
                 const f32x4 b4 = ld4(betas + hh * 64 + k0 + 4 * q);
+                const auto inv = get_inv(reinterpret_cast<const T*>(smem + CF::INV + kt * 1024), lane);
                 f32x4 r;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) r[e] = e4[e] < 0.f ? 0.f : b4[e] * (xr[kt][e] - e4[e] * v[e]);
                 f32x4 t = zero4;
 #pragma unroll
-                for (int f = 0; 2 * f < kt; ++f) t = mul(t, get(tt, f, lane), uf[f]);
-                u[kt] = times_inv(reinterpret_cast<const T*>(smem + CF::INV + kt * 1024), lane, r - t);
+                for (int f = 0; 2 * f < kt; ++f) t = mul(t, to[f], uf[f]);
+                u[kt] = times_inv(inv, r - t);
                 split(join(u[kt & ~1], u[kt | 1]), uf[kt >> 1]);
             }
 #pragma unroll
             for (int f = 0; 2 * f <= kt; ++f) {
-                if constexpr (DELTA) o = mul(o, get(mt, f, lane), uf[f]);
-                else o = mul(o, get(mt, f, lane), xf[f]);
+                if constexpr (DELTA) o = mul(o, mo[f], uf[f]);
+                else o = mul(o, mo[f], xf[f]);
             }
             settle(o);
 #pragma unroll
@@ -600,8 +617,7 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
 // every panel of 64 up to their own.
 // ---------------------------------------------------------------------------
 template <typename T, int N, bool DELTA>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(LongCfg<T, N, DELTA>::OCC, LongCfg<T, N, DELTA>::OCC)))
-void k_tree_long(Args a) {
+__global__ __launch_bounds__(256) void k_tree_long(Args a) {
     typedef typename V8<T>::type F8;
     typedef LongCfg<T, N, DELTA> CF;
     constexpr int KS = CF::KS;
@@ -626,26 +642,15 @@ void k_tree_long(Args a) {
     float* betas = reinterpret_cast<float*>(smem + at.beta);
     int* ptr = reinterpret_cast<int*>(smem + CF::M);  // [node], in M's place while the paths are formed
     u64* badx = reinterpret_cast<u64*>(smem + at.badx);
+    unsigned* badb = reinterpret_cast<unsigned*>(smem + at.badb);  // [tile] nodes whose row of B is not finite
     const T* x = static_cast<const T*>(a.x) + row0 * a.xs + h * P + p0;
     const T* Bm = static_cast<const T*>(a.B) + row0 * a.bs + g * N;
     const T* Cm = static_cast<const T*>(a.C) + row0 * a.cs + g * N;
     const T* beta = static_cast<const T*>(a.beta);
     T* y = static_cast<T*>(a.y) + (row0 * H + h) * P + p0;
     const f32x4 zero4 = {0.f, 0.f, 0.f, 0.f};
-    const int slot = a.slots[place.bi];
-    if (slot < 0 || slot >= a.S) {
-        if (mine)
-            for (int k0 = 0; k0 < K; k0 += 16) store_y(y, ys, k0, K, lane, sel, upper, zero4);
-        return;
-    }
     const bool has = N >= 32 || q < 2;
     const int n0 = 8 * (N >= 32 ? q : q & 1);
-    f32x8 hf[KS];
-    {
-        const float* hp = a.pool + slot * a.ss + (int64_t)(h * P + (mine ? p0 + l16 : 0)) * N + n0;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) hf[ks] = ld8(hp + 32 * ks);
-    }
     auto frag = [&](const T* m, int64_t stride, int node, int ks) {
         const F8 v = ld8(m + (int64_t)(node < K ? node : K - 1) * stride + 32 * ks + n0);
         return N >= 32 ? v : sel8(has, v);
@@ -660,43 +665,38 @@ void k_tree_long(Args a) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) st8(rows + ((w * KS + ks) * 64 + lane) * 8, v[ks]);
     };
+    const bool in = tid < K;
+    const int64_t node = row0 + (in ? tid : K - 1);
+    const float dt = a.dt[node * H + h], bt = DELTA ? to_f(beta[node * H + h]) : 0.f;
+    const int par = a.parents[node];
+    F8 cf[KS], bf[KS], bn[KS];  // this wave's node tile: C, B; and of the next panel's B
+    typename Raw<T>::type xq[4], xn[4];
+    rows_of(Cm, a.cs, 0, cf);
+    rows_of(Bm, a.bs, 0, bf);
+    const int slot = a.slots[place.bi];
+    if (slot < 0 || slot >= a.S) {
+        if (mine)
+            for (int k0 = 0; k0 < K; k0 += 16) store_y(y, ys, k0, K, lane, sel, upper, zero4);
+        return;
+    }
+    f32x8 hf[KS];  // (behind what the panels wait for)
+    {
+        const float* hp = a.pool + slot * a.ss + (int64_t)(h * P + p0 + l16) * N + n0;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) hf[ks] = ld8(hp + 32 * ks);
+    }
     for (int i = tid; i < 64 * panels; i += 256) badx[i] = 0;
+    if (tid < 16) badb[tid] = 0;
     if (tid < kp) {
-        const bool in = tid < K;
-        const double c = orders(in ? a.dt[(row0 + tid) * H + h] : 0.f, (double)a.A[h] * 1.4426950408889634);
-        const int par = in ? a.parents[row0 + tid] : -2;
-        const bool ok = par >= -1 && par < tid;
-        bool bad = false;
-        if (DELTA) {
-            const float bt = in ? to_f(beta[(row0 + tid) * H + h]) : 0.f;
-            bad = c != c || odd_bits(bt);
-            betas[tid] = bt;
-        }
+        const double c = orders(in ? dt : 0.f, (double)a.A[h] * 1.4426950408889634);
+        const bool ok = in && par >= -1 && par < tid;
+        if (DELTA) betas[tid] = in ? bt : 0.f;
         cs[tid] = c;
         ptr[tid] = ok ? par : -1;
-        decay[tid] = !ok ? -1.f : bad ? -2.f : 0.f;
+        decay[tid] = !ok ? -1.f : DELTA && (c != c || odd_bits(bt)) ? -2.f : 0.f;
         for (int i = 0; i < panels; ++i) mask[tid * panels + i] = i == tid >> 6 ? 1ull << (tid & 63) : 0;
     }
     __syncthreads();
-    if (DELTA) {
-        // nodes whose row of B is not finite: N / 8 lanes a node, eight pieces a lane on their way at once
-        constexpr int R = N / 8, PER = 256 / R;
-        for (int k0 = 0; k0 < K; k0 += 8 * PER) {
-            F8 v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int k = k0 + i * PER + tid / R;
-                v[i] = ld8(Bm + (int64_t)(k < K ? k : K - 1) * a.bs + 8 * (tid % R));
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int k = k0 + i * PER + tid / R;
-                const u64 who = __ballot(any_odd(v[i])) >> (lane / R * R);
-                if (k < K && tid % R == 0 && (who & ((1ull << R) - 1)) != 0 && decay[k] != -1.f) decay[k] = -2.f;
-            }
-        }
-        __syncthreads();
-    }
     // the paths, by doubling, a thread a node; a node is absent below an absent one, and not computable below such a one
     for (int reach = 1; reach < K; reach *= 2) {
         const int k = tid < kp ? tid : 0, p = ptr[k], from = p < 0 ? k : p;
@@ -724,13 +724,16 @@ void k_tree_long(Args a) {
     const float nan = __builtin_nanf("");
     const float D = a.D ? a.D[h] : 0.f;
     bool anybad = false;
-    auto take_x = [&](int k0) {
-        if (k0 >= K) return zero4;
+    auto ask_x = [&](int k0, typename Raw<T>::type (&v)[4]) {
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) v[kt] = load_x(x, a.xs, k0 + 16 * kt, K, lane);
+    };
+    auto take_x = [&](typename Raw<T>::type raw, int k0) {
         unsigned odd;
-        const f32x4 v = clean_x(open_x(load_x(x, a.xs, k0, K, lane), sel, upper), decay + k0 + 4 * q, odd);
+        const f32x4 v = clean_x(open_x(raw, sel, upper), decay + k0 + 4 * q, odd);
         if (__ballot(odd != 0)) {
             anybad = true;
-            if (odd) atomicOr(&badx[(k0 >> 6) * 64 + 16 * w + l16], (u64)odd << ((k0 & 63) + 4 * q));
+            if (odd && mine) atomicOr(&badx[(k0 >> 6) * 64 + 16 * w + l16], (u64)odd << ((k0 & 63) + 4 * q));
             wave_sync();
         }
         return v;
@@ -738,43 +741,67 @@ void k_tree_long(Args a) {
     Op<T> hs[KS];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) split(N >= 32 ? hf[ks] : sel8(has, hf[ks]), hs[ks]);
-    F8 cf[KS], bf[KS], bn[KS];  // this wave's node tile: C, B; and of the next panel's B
+    ask_x(0, xq);
     for (int s = 0; s < panels; ++s) {
         const int q0 = s * kPanel, nk = (K - q0 + 15) / 16 < 4 ? (K - q0 + 15) / 16 : 4;
-        rows_of(Cm, a.cs, q0, cf);
-        rows_of(Bm, a.bs, q0, bf);
+        if (s > 0) __syncthreads();  // x1 and x2 are free
         if (CF::STG) {
-            if (s > 0) __syncthreads();  // x1 and x2 are free
             keep(x1, cf);
             keep(x2, bf);
-            __syncthreads();
-            if (s > 0) rows_of(Bm, a.bs, 0, bn);
         }
+        if (DELTA) {
+            // a node below one whose row of B is not finite cannot be computed
+            bool odd = false;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) odd |= any_odd(bf[ks]);
+            u64 who = __ballot(odd);
+            who |= who >> 32;
+            if (lane == 0) badb[4 * s + w] = (unsigned)(who | who >> 16) & 0xffffu;
+        }
+        __syncthreads();
+        if (DELTA) {
+            if (tid < kPanel) {
+                u64 hit = 0;
+                for (int i = 0; i <= s; ++i) {
+                    const u64 odd = badb[4 * i] | badb[4 * i + 1] << 16 | (u64)(badb[4 * i + 2] | badb[4 * i + 3] << 16) << 32;
+                    hit |= mask[(q0 + tid) * panels + i] & odd;
+                }
+                if (hit && decay[q0 + tid] != -1.f) decay[q0 + tid] = -2.f;
+            }
+            __syncthreads();
+        }
+        if (CF::STG && s > 0) rows_of(Bm, a.bs, 0, bn);
+        if (!DELTA && s > 0) ask_x(0, xn);
         f32x4 O[4], Rt[4], xt[4];
         // ---- what the held state gives: O = diag(E) C h^T, Rt = beta (x - diag(E) B h^T) ----
+        F8 fc[CF::NB][KS], fb[CF::NB][KS];  // the tile in work and, where registers allow, the next
+        auto ask_rows = [&](int kt, F8 (&c)[KS], F8 (&b)[KS]) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                c[ks] = CF::STG ? kept(x1, kt, ks) : frag(Cm, a.cs, q0 + 16 * kt + l16, ks);
+                if (DELTA) b[ks] = CF::STG ? kept(x2, kt, ks) : frag(Bm, a.bs, q0 + 16 * kt + l16, ks);
+            }
+        };
+        if (CF::NB == 2) ask_rows(0, fc[0], fb[0]);
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt) {
-            O[kt] = Rt[kt] = xt[kt] = zero4;
+            const int k0 = q0 + 16 * kt;
+            O[kt] = Rt[kt] = zero4;
+            xt[kt] = take_x(xq[kt], k0);  // (zero past the last node)
             if (kt < nk && mine) {
-                const int k0 = q0 + 16 * kt;
                 f32x4 o = zero4, v = zero4;
-                F8 fc[KS], fb[KS];
+                if (CF::NB == 1) ask_rows(kt, fc[0], fb[0]);
+                together(fc[kt % CF::NB]);
+                if (DELTA) together(fb[kt % CF::NB]);
+                if (CF::NB == 2 && kt + 1 < 4) ask_rows(kt + 1, fc[(kt + 1) % CF::NB], fb[(kt + 1) % CF::NB]);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    fc[ks] = CF::STG ? kept(x1, kt, ks) : frag(Cm, a.cs, k0 + l16, ks);
-                    if (DELTA) fb[ks] = CF::STG ? kept(x2, kt, ks) : frag(Bm, a.bs, k0 + l16, ks);
-                }
-                together(fc);
-                if (DELTA) together(fb);
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    o = mul(o, fc[ks], hs[ks]);
-                    if (DELTA) v = mul(v, fb[ks], hs[ks]);
+                    o = mul(o, fc[kt % CF::NB][ks], hs[ks]);
+                    if (DELTA) v = mul(v, fb[kt % CF::NB][ks], hs[ks]);
                 }
                 const f32x4 e4 = ld4(decay + k0 + 4 * q);
                 settle(o);
                 O[kt] = e4 * o;
-                xt[kt] = take_x(k0);
                 if (DELTA) {
                     const f32x4 b4 = ld4(betas + k0 + 4 * q);
                     settle(v);
@@ -794,43 +821,53 @@ void k_tree_long(Args a) {
             }
             // ---- M and T of this wave's node tile against panel sp ----
             if (w < nk) {
-                const int k = q0 + 16 * w + l16, jn = own ? w + 1 : 4;
+                const int k = q0 + 16 * w + l16;
                 const u64 on = decay[k] < 0.f ? 0 : mask[k * panels + sp];
                 const double ck = cs[k];
                 const float bk = DELTA ? betas[k] : 0.f;
                 const T* bj0 = own ? x2 : x1;
                 f32x4 diag = zero4;
-                for (int jt = 0; jt < ((jn + 1) & ~1); ++jt) {
-                    f32x4 m = zero4, t = zero4;
-                    if (jt < jn) {
-                        f32x4 c = zero4, b = zero4;
-                        F8 bj[KS];
+                F8 bj[CF::NB][KS];  // the tile in work and, where registers allow, the next
+                auto ask = [&](int jt, F8 (&v)[KS]) {
 #pragma unroll
-                        for (int ks = 0; ks < KS; ++ks) bj[ks] = CF::STG ? kept(bj0, jt, ks) : frag(Bm, a.bs, j0 + 16 * jt + l16, ks);
-                        together(bj);
+                    for (int ks = 0; ks < KS; ++ks) v[ks] = CF::STG ? kept(bj0, jt, ks) : frag(Bm, a.bs, j0 + 16 * jt + l16, ks);
+                };
+                if (CF::NB == 2) ask(0, bj[0]);
+#pragma unroll
+                for (int jt = 0; jt < 4; ++jt)
+                    if (!own || jt < ((w + 2) & ~1)) {
+                        if (CF::NB == 1) ask(jt, bj[0]);
+                        together(bj[jt % CF::NB]);
+                        if (CF::NB == 2 && jt + 1 < 4) ask(jt + 1, bj[(jt + 1) % CF::NB]);
+                        f32x4 m, t, c = zero4, b = zero4;
 #pragma unroll
                         for (int ks = 0; ks < KS; ++ks) {
-                            c = mma(c, bj[ks], cf[ks]);
-                            if (DELTA) b = mma(b, bj[ks], bf[ks]);
+                            c = mma(c, bj[jt % CF::NB][ks], cf[ks]);
+                            if (DELTA) b = mma(b, bj[jt % CF::NB][ks], bf[ks]);
                         }
                         settle(c);
                         if (DELTA) settle(b);
+                        // (no node behind its own is on its path, so the tile past the last is zero of itself)
                         weigh<DELTA>((unsigned)(on >> (16 * jt + 4 * q)) & 15u, ck, cs + j0 + 16 * jt + 4 * q, bk,
                                      k - j0 - 16 * jt - 4 * q, c, b, m, t);
-                    }
-                    put(mt + w * TAB, jt >> 1, jt & 1, lane, m);
-                    if (DELTA) {
-                        if (own && jt == w) {
-                            diag = t;
-                            t = zero4;
+                        put(mt + w * TAB, jt >> 1, jt & 1, lane, m);
+                        if (DELTA) {
+                            if (own && jt == w) {
+                                diag = t;
+                                t = zero4;
+                            }
+                            put(tt + w * TAB, jt >> 1, jt & 1, lane, t);
                         }
-                        put(tt + w * TAB, jt >> 1, jt & 1, lane, t);
                     }
-                }
                 if (DELTA && own) {
                     T* inv = x1 + w * 1024 / (int)sizeof(T);
                     put_inv(inv, lane, inverse16(diag, reinterpret_cast<float*>(inv), lane));
                 }
+            }
+            if (own) {  // the next panel's rows, behind this one's last use of them
+                rows_of(Cm, a.cs, q0 + kPanel, cf);
+                rows_of(Bm, a.bs, q0 + kPanel, bf);
+                ask_x(q0 + kPanel, xq);
             }
             if (CF::STG && sp + 1 < s) rows_of(Bm, a.bs, j0 + kPanel, bn);
             __syncthreads();
@@ -842,12 +879,16 @@ void k_tree_long(Args a) {
 #pragma unroll
                 for (int f = 0; f < 2; ++f)
                     xf[f] = own ? pair8(x, xt[2 * f], xt[2 * f + 1])
-                                : pair8(x, take_x(j0 + 32 * f), take_x(j0 + 32 * f + 16));
+                                : pair8(x, take_x(xn[2 * f], j0 + 32 * f), take_x(xn[2 * f + 1], j0 + 32 * f + 16));
+                if (sp + 1 < s) ask_x(j0 + kPanel, xn);
 #pragma unroll
                 for (int kt = 0; kt < 4; ++kt)
                     if (kt < nk) {
-                                                O[kt] = mul(O[kt], get(mt + kt * TAB, 0, lane), xf[0]);
-                        if (!own || kt >= 2) O[kt] = mul(O[kt], get(mt + kt * TAB, 1, lane), xf[1]);
+                        Op<T> m0 = get(mt + kt * TAB, 0, lane), m1 = get(mt + kt * TAB, 1, lane);
+                        together(m0);
+                        together(m1);
+                        O[kt] = mul(O[kt], m0, xf[0]);
+                        if (!own || kt >= 2) O[kt] = mul(O[kt], m1, xf[1]);
                         settle(O[kt]);
                     }
             } else {
@@ -860,11 +901,17 @@ void k_tree_long(Args a) {
 #pragma unroll
                     for (int kt = 0; kt < 4; ++kt)
                         if (kt < nk) {
-                                                        f32x4 t = zero4;
+                            const auto inv = get_inv(x1 + kt * 1024 / (int)sizeof(T), lane);
+                            f32x4 t = zero4;
+                            Op<T> to[2];
 #pragma unroll
-                            for (int f = 0; f < 2; ++f)
-                                if (2 * f < kt) t = mul(t, get(tt + kt * TAB, f, lane), uf[f]);
-                            u[kt] = times_inv(x1 + kt * 1024 / (int)sizeof(T), lane, Rt[kt] - t);
+                            for (int f = 0; 2 * f < kt; ++f) to[f] = get(tt + kt * TAB, f, lane);
+#pragma unroll
+                            for (int f = 0; 2 * f < kt; ++f) {
+                                together(to[f]);
+                                t = mul(t, to[f], uf[f]);
+                            }
+                            u[kt] = times_inv(inv, Rt[kt] - t);
                             split(join(u[kt & ~1], u[kt | 1]), uf[kt >> 1]);
                         }
                     if (s + 1 < panels) {
@@ -879,7 +926,10 @@ void k_tree_long(Args a) {
 #pragma unroll
                     for (int kt = 0; kt < 4; ++kt)
                         if (kt < nk) {
-                                                        f32x4 t = mul(mul(zero4, get(tt + kt * TAB, 0, lane), uf[0]), get(tt + kt * TAB, 1, lane), uf[1]);
+                            Op<T> t0 = get(tt + kt * TAB, 0, lane), t1 = get(tt + kt * TAB, 1, lane);
+                            together(t0);
+                            together(t1);
+                            f32x4 t = mul(mul(zero4, t0, uf[0]), t1, uf[1]);
                             settle(t);
                             Rt[kt] -= t;
                         }
@@ -887,8 +937,11 @@ void k_tree_long(Args a) {
 #pragma unroll
                 for (int kt = 0; kt < 4; ++kt)
                     if (kt < nk) {
-                                                O[kt] = mul(O[kt], get(mt + kt * TAB, 0, lane), uf[0]);
-                        if (!own || kt >= 2) O[kt] = mul(O[kt], get(mt + kt * TAB, 1, lane), uf[1]);
+                        Op<T> m0 = get(mt + kt * TAB, 0, lane), m1 = get(mt + kt * TAB, 1, lane);
+                        together(m0);
+                        together(m1);
+                        O[kt] = mul(O[kt], m0, uf[0]);
+                        if (!own || kt >= 2) O[kt] = mul(O[kt], m1, uf[1]);
                         settle(O[kt]);
                     }
             }
