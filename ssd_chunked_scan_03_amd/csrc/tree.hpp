@@ -114,27 +114,32 @@ struct TreeCfg {
 };
 
 // More nodes, in panels of 64.  kp: nodes rounded up to panels.  Where they fit (STG), the rows of the panel in
-// work go through LDS: x1 holds its C, then B of one earlier panel after another, then the inverses; x2 its own B.
+// work go through LDS: x1 holds its C, then B of one earlier panel after another; x2 its own B.
 template <typename T, int N, bool DELTA>
 struct LongCfg {
     static constexpr int KS = N < 32 ? 1 : N / 32;
     static constexpr int ROWS = 4 * KS * 512 * (int)sizeof(T);
     static constexpr bool STG = 2 * ROWS <= 65536;
-    static constexpr int NB = KS * (int)sizeof(T) <= 16 ? 2 : 1;  // tiles of B in registers at a time
-    static constexpr int M = 0, TT = 4 * kTableBytes, X1 = TT + (DELTA ? 4 * kTableBytes : 0);
-    static constexpr int X2 = X1 + (STG && ROWS > 4096 ? ROWS : 4096), MASK = X2 + (STG ? ROWS : 0);
+    static constexpr int KC = KS * (int)sizeof(T) <= 8 ? KS : 8 / (int)sizeof(T);  // fragments asked for at a time
+    static constexpr int CH = KS / KC;                                             // such chunks of a tile's rows
+    static constexpr int KH = KS > 1 ? KS / 2 : 1;               // a wave's share of an earlier panel's tile
 };
 struct LongLds {
-    int mask, c, e, beta, badx, badb, u, total;
-    __host__ __device__ LongLds(int mask0, int K, bool rule_delta) : mask(mask0) {
-        const int kp = (K + kPanel - 1) / kPanel * kPanel, panels = kp / kPanel;
-        c = mask + kp * panels * 8;                    // mask: [node][panel]
-        e = c + kp * 8;
-        beta = e + kp * 4;
-        badx = beta + (rule_delta ? kp * 4 : 0);       // [panel][column] nodes whose x is not finite
-        badb = badx + panels * 64 * 8;                 // [tile] nodes whose row of B is not finite
-        u = badb + 64;                                 // [panel][wave] u of the panels before the last
-        total = u + (rule_delta ? (panels - 1) * 4 * kTableBytes : 0);
+    int tt, inv, x1, x2, mask, c, e, beta, badx, badb, more, total;  // M at 0: [head][tile], as T
+    __host__ __device__ LongLds(int K, int heads, int cols, bool rule_delta, int rows) {
+        const int kp = (K + kPanel - 1) / kPanel * kPanel, panels = kp / kPanel, tabs = heads * 4 * kTableBytes;
+        tt = tabs;
+        inv = tt + (rule_delta ? tabs : 0);  // [head][tile] the diagonal tiles' inverses
+        x1 = inv + (rule_delta ? heads * 4096 : 0);
+        x2 = x1 + rows;
+        mask = x2 + rows;              // [panel][node]
+        c = mask + kp * panels * 8;    // [head][node], as E and beta
+        e = c + heads * kp * 8;
+        beta = e + heads * kp * 4;
+        badx = beta + (rule_delta ? heads * kp * 4 : 0);  // [panel][wave with columns][column] nodes whose x is not finite
+        badb = badx + panels * heads * cols * 16 * 8;     // [tile] nodes whose row of B is not finite
+        more = badb + 64;  // [round] whether paths go on
+        total = more + 64;
     }
 };
 
@@ -279,7 +284,17 @@ struct Place {
     }
 };
 
-// A node tile's table row from its decays: bits: which of the lane's nodes 4 q + e are on the path of node k.
+// A node tile's table row from its products and decays; bits: which of the lane's nodes 4 q + e are on the path of
+// node k; ck, cj: their orders.  A row that two waves share: one table's; or a wave's alone: M's (of c) and T's (of b).
+__device__ __forceinline__ f32x4 weigh(unsigned bits, double ck, const double* cj, float scale, f32x4 c) {
+    f32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float f = exp2f_fast((float)(ck - cj[e]));
+        v[e] = bits >> e & 1 ? scale * f * c[e] : 0.f;
+    }
+    return v;
+}
 template <bool DELTA>
 __device__ __forceinline__ void weigh(unsigned bits, double ck, const double* cj, float bk, int self, f32x4 c, f32x4 b,
                                       f32x4& m, f32x4& t) {
@@ -613,36 +628,54 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
 }
 
 // ---------------------------------------------------------------------------
-// k_tree_long: trees of 65 to 256 nodes, one head a work-group of four waves (cols of them with columns), 64 nodes at a time against
-// every panel of 64 up to their own.
+// k_tree_long: trees of 65 to 256 nodes, 64 nodes at a time against every panel of 64 up to their own.  Eight waves
+// take one head, or two of a group (16 columns a wave).  For the tables, wave w has node tile w % 4 and one operand's
+// rows: C's (waves 0 to 3, M) or B's (4 to 7, T and the inverses); a product serves both heads.  The scan has no T:
+// its waves 4 to 7 take half of M's tiles.
 // ---------------------------------------------------------------------------
 template <typename T, int N, bool DELTA>
-__global__ __launch_bounds__(256) void k_tree_long(Args a) {
+__global__ __launch_bounds__(512) void k_tree_long(Args a, int heads) {
     typedef typename V8<T>::type F8;
     typedef LongCfg<T, N, DELTA> CF;
-    constexpr int KS = CF::KS;
+    constexpr int KS = CF::KS, KH = CF::KH, KC = CF::KC, CH = CF::CH;
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    const int K = (int)a.T, P = a.P, H = a.H, cols = P < 64 ? P / 16 : 4;
-    const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
-    const Place place(a, 1, cols, w);
+    const int K = (int)a.T, P = a.P, H = a.H, cols = P / 16;
+    const int tid = threadIdx.x, w = wave_id();
+    int lane = tid & 63, l16 = lane & 15, q = lane >> 4;
+    // addresses are formed again where they are used: kept over the loops they would take the registers of operands
+    auto again = [&] {
+        asm volatile("" : "+v"(lane));
+        l16 = lane & 15;
+        q = lane >> 4;
+    };
+    const int tw = w & 3, kind = w >> 2;  // of the tables
+    const int hw = heads == 2 ? w >> 2 : 0, cw = heads == 2 ? w & 3 : w;  // of the columns
+    const Place place(a, heads, cols, cw);
+    const bool mine = hw < place.nh && cw < cols;
     const int64_t row0 = place.bi * K, ys = (int64_t)H * P;
-    const int g = place.g, h = place.h0, p0 = place.p0;
+    const int g = place.g, h = place.h0 + (mine ? hw : 0), p0 = place.p0;
     const unsigned sel = delta::quad_sel(lane);
-    const bool upper = (lane & 2) != 0, mine = w < cols;
+    const bool upper = (lane & 2) != 0;
     const int kp = (K + kPanel - 1) / kPanel * kPanel, panels = kp / kPanel;
-    const LongLds at(CF::MASK, K, DELTA);
-    T* mt = reinterpret_cast<T*>(smem + CF::M);
-    T* tt = reinterpret_cast<T*>(smem + CF::TT);
-    T* x1 = reinterpret_cast<T*>(smem + CF::X1);
-    T* x2 = reinterpret_cast<T*>(smem + CF::X2);
+    const LongLds at(K, heads, cols, DELTA, CF::STG ? CF::ROWS : 0);
+    T* mtabs = reinterpret_cast<T*>(smem);
+    T* ttabs = reinterpret_cast<T*>(smem + at.tt);
+    T* x1 = reinterpret_cast<T*>(smem + at.x1);
+    T* x2 = reinterpret_cast<T*>(smem + at.x2);
     constexpr int TAB = kTableBytes / (int)sizeof(T);
     u64* mask = reinterpret_cast<u64*>(smem + at.mask);
-    double* cs = reinterpret_cast<double*>(smem + at.c);
-    float* decay = reinterpret_cast<float*>(smem + at.e);
+    double* css = reinterpret_cast<double*>(smem + at.c);
+    float* decays = reinterpret_cast<float*>(smem + at.e);
     float* betas = reinterpret_cast<float*>(smem + at.beta);
-    int* ptr = reinterpret_cast<int*>(smem + CF::M);  // [node], in M's place while the paths are formed
-    u64* badx = reinterpret_cast<u64*>(smem + at.badx);
-    unsigned* badb = reinterpret_cast<unsigned*>(smem + at.badb);  // [tile] nodes whose row of B is not finite
+    int* ptr = reinterpret_cast<int*>(smem);  // [node], in M's place while the paths are formed
+    u64* badx = reinterpret_cast<u64*>(smem + at.badx) + (mine ? w * 16 + l16 : 0);
+    const int badp = heads * cols * 16;       // from one panel's to the next
+    unsigned* badb = reinterpret_cast<unsigned*>(smem + at.badb);
+    unsigned* more = reinterpret_cast<unsigned*>(smem + at.more);
+    // this wave's head's
+    const T* mt = mtabs + (mine ? hw : 0) * 4 * TAB;
+    const T* tt = ttabs + (mine ? hw : 0) * 4 * TAB;
+    float* decay = decays + (mine ? hw : 0) * kp;
     const T* x = static_cast<const T*>(a.x) + row0 * a.xs + h * P + p0;
     const T* Bm = static_cast<const T*>(a.B) + row0 * a.bs + g * N;
     const T* Cm = static_cast<const T*>(a.C) + row0 * a.cs + g * N;
@@ -656,23 +689,33 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
         return N >= 32 ? v : sel8(has, v);
     };
     auto kept = [&](const T* rows, int tile, int ks) { return ld8(rows + ((tile * KS + ks) * 64 + lane) * 8); };
-    // rows of this wave's node tile of a panel
-    auto rows_of = [&](const T* m, int64_t stride, int j0, F8 (&v)[KS]) {
+    // the rows that this wave stages: node tile tw of a panel's C or B; and its share of an earlier panel's B
+    const T* rows = kind ? Bm : Cm;
+    const int64_t rows_st = kind ? a.bs : a.cs;
+    F8 rs[KS];
+    auto ask_own = [&](int j0) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) v[ks] = frag(m, stride, j0 + 16 * w + l16, ks);
+        for (int ks = 0; ks < KS; ++ks) rs[ks] = frag(rows, rows_st, j0 + 16 * tw + l16, ks);
     };
-    auto keep = [&](T* rows, const F8 (&v)[KS]) {
+    const int first = KS > 1 ? kind * KH : 0;
+    auto ask_b = [&](int j0, F8 (&bn)[KH]) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) st8(rows + ((w * KS + ks) * 64 + lane) * 8, v[ks]);
+        for (int i = 0; i < KH; ++i) bn[i] = frag(Bm, a.bs, j0 + 16 * tw + l16, first + i);
     };
-    const bool in = tid < K;
-    const int64_t node = row0 + (in ? tid : K - 1);
-    const float dt = a.dt[node * H + h], bt = DELTA ? to_f(beta[node * H + h]) : 0.f;
+    auto keep_b = [&](const F8 (&bn)[KH]) {
+        if (KS > 1 || kind == 0)
+#pragma unroll
+            for (int i = 0; i < KH; ++i) st8(x1 + ((tw * KS + first + i) * 64 + lane) * 8, bn[i]);
+    };
+    // a thread a node and head
+    const int nt = tid & 255, ht = tid >> 8;
+    const bool in = nt < K;
+    const int64_t node = row0 + (in ? nt : K - 1);
+    const int hn = place.h0 + (ht < place.nh ? ht : 0);
+    const float dt = a.dt[node * H + hn], bt = DELTA ? to_f(beta[node * H + hn]) : 0.f;
     const int par = a.parents[node];
-    F8 cf[KS], bf[KS], bn[KS];  // this wave's node tile: C, B; and of the next panel's B
     typename Raw<T>::type xq[4], xn[4];
-    rows_of(Cm, a.cs, 0, cf);
-    rows_of(Bm, a.bs, 0, bf);
+    if (CF::STG) ask_own(0);
     const int slot = a.slots[place.bi];
     if (slot < 0 || slot >= a.S) {
         if (mine)
@@ -685,40 +728,49 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) hf[ks] = ld8(hp + 32 * ks);
     }
-    for (int i = tid; i < 64 * panels; i += 256) badx[i] = 0;
-    if (tid < 16) badb[tid] = 0;
-    if (tid < kp) {
-        const double c = orders(in ? dt : 0.f, (double)a.A[h] * 1.4426950408889634);
-        const bool ok = in && par >= -1 && par < tid;
-        if (DELTA) betas[tid] = in ? bt : 0.f;
-        cs[tid] = c;
-        ptr[tid] = ok ? par : -1;
-        decay[tid] = !ok ? -1.f : DELTA && (c != c || odd_bits(bt)) ? -2.f : 0.f;
-        for (int i = 0; i < panels; ++i) mask[tid * panels + i] = i == tid >> 6 ? 1ull << (tid & 63) : 0;
+    for (int i = tid; i < badp * panels; i += 512) reinterpret_cast<u64*>(smem + at.badx)[i] = 0;
+    if (tid < 16) badb[tid] = more[tid] = 0;
+    const bool sets = ht < place.nh && nt < kp;
+    const int kn = ht * kp + nt;
+    if (sets) {
+        const double c = orders(in ? dt : 0.f, (double)a.A[hn] * 1.4426950408889634);
+        const bool ok = in && par >= -1 && par < nt;
+        if (DELTA) betas[kn] = in ? bt : 0.f;
+        css[kn] = c;
+        decays[kn] = !ok ? -1.f : DELTA && (c != c || odd_bits(bt)) ? -2.f : 0.f;
+        if (ht == 0) {
+            ptr[nt] = ok ? par : -1;
+            for (int i = 0; i < panels; ++i) mask[i * kp + nt] = i == nt >> 6 ? 1ull << (nt & 63) : 0;
+        }
     }
     __syncthreads();
-    // the paths, by doubling, a thread a node; a node is absent below an absent one, and not computable below such a one
-    for (int reach = 1; reach < K; reach *= 2) {
-        const int k = tid < kp ? tid : 0, p = ptr[k], from = p < 0 ? k : p;
-        const double c = p < 0 ? cs[k] : cs[k] + cs[from];
+    // the paths, by doubling; a node is absent below an absent one, and not computable below such a one
+    for (int r = 0, reach = 1; reach < K; reach *= 2, ++r) {
+        const int k = sets ? nt : 0, of = sets ? ht * kp : 0, p = ptr[k], from = p < 0 ? k : p;
+        const double c = p < 0 ? css[of + k] : css[of + k] + css[of + from];
         const int up = p < 0 ? -1 : ptr[from];
-        const float self = decay[k], theirs = decay[from];
+        const float self = decays[of + k], theirs = decays[of + from];
         u64 m[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j < panels) m[j] = mask[k * panels + j] | mask[from * panels + j];
-        __syncthreads();
-        if (tid < kp) {
-            cs[k] = c;
-            ptr[k] = up;
-            decay[k] = self == -1.f || theirs == -1.f ? -1.f : self < theirs ? self : theirs;
+        if (ht == 0)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (j < panels) mask[k * panels + j] = m[j];
+                if (j < panels) m[j] = mask[j * kp + k] | mask[j * kp + from];
+        if (__ballot(up >= 0) && lane == 0) more[r] = 1;
+        __syncthreads();
+        if (sets) {
+            css[kn] = c;
+            decays[kn] = self == -1.f || theirs == -1.f ? -1.f : self < theirs ? self : theirs;
+            if (ht == 0) {
+                ptr[k] = up;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < panels) mask[j * kp + k] = m[j];
+            }
         }
         __syncthreads();
+        if (!more[r]) break;
     }
-    if (tid < kp && !(decay[tid] < 0.f)) decay[tid] = exp2f_fast((float)cs[tid]);
+    if (sets && !(decays[kn] < 0.f)) decays[kn] = exp2f_fast((float)css[kn]);
     __syncthreads();
 
     const float nan = __builtin_nanf("");
@@ -733,219 +785,277 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
         const f32x4 v = clean_x(open_x(raw, sel, upper), decay + k0 + 4 * q, odd);
         if (__ballot(odd != 0)) {
             anybad = true;
-            if (odd && mine) atomicOr(&badx[(k0 >> 6) * 64 + 16 * w + l16], (u64)odd << ((k0 & 63) + 4 * q));
+            if (odd && mine) atomicOr(badx + (k0 >> 6) * badp, (u64)odd << ((k0 & 63) + 4 * q));
             wave_sync();
         }
         return v;
     };
-    Op<T> hs[KS];
+    Op<T> hs[KS], u0[2], u1[2], u2[2];  // the state; u of the panels before the last
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) split(N >= 32 ? hf[ks] : sel8(has, hf[ks]), hs[ks]);
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+        split(join(zero4, zero4), u0[f]);
+        u2[f] = u1[f] = u0[f];
+    }
     ask_x(0, xq);
+#pragma unroll 1
     for (int s = 0; s < panels; ++s) {
+        again();
         const int q0 = s * kPanel, nk = (K - q0 + 15) / 16 < 4 ? (K - q0 + 15) / 16 : 4;
         if (s > 0) __syncthreads();  // x1 and x2 are free
         if (CF::STG) {
-            keep(x1, cf);
-            keep(x2, bf);
+            T* to = kind ? x2 : x1;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) st8(to + ((tw * KS + ks) * 64 + lane) * 8, rs[ks]);
         }
-        if (DELTA) {
+        if (DELTA && kind) {
             // a node below one whose row of B is not finite cannot be computed
+            if (!CF::STG) ask_own(q0);
             bool odd = false;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) odd |= any_odd(bf[ks]);
+            for (int ks = 0; ks < KS; ++ks) odd |= any_odd(rs[ks]);
             u64 who = __ballot(odd);
             who |= who >> 32;
-            if (lane == 0) badb[4 * s + w] = (unsigned)(who | who >> 16) & 0xffffu;
+            if (lane == 0) badb[4 * s + tw] = (unsigned)(who | who >> 16) & 0xffffu;
         }
         __syncthreads();
         if (DELTA) {
-            if (tid < kPanel) {
-                u64 hit = 0;
-                for (int i = 0; i <= s; ++i) {
-                    const u64 odd = badb[4 * i] | badb[4 * i + 1] << 16 | (u64)(badb[4 * i + 2] | badb[4 * i + 3] << 16) << 32;
-                    hit |= mask[(q0 + tid) * panels + i] & odd;
-                }
-                if (hit && decay[q0 + tid] != -1.f) decay[q0 + tid] = -2.f;
+            u64 odd[4];
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // (zero for panels to come)
+                odd[i] = badb[4 * i] | badb[4 * i + 1] << 16 | (u64)(badb[4 * i + 2] | badb[4 * i + 3] << 16) << 32;
+                any |= odd[i] != 0;
             }
-            __syncthreads();
+            if (any) {
+                if (ht < place.nh && nt < kPanel) {
+                    u64 hit = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i <= s) hit |= mask[i * kp + q0 + nt] & odd[i];
+                    float& e = decays[ht * kp + q0 + nt];
+                    if (hit && e != -1.f) e = -2.f;
+                }
+                __syncthreads();
+            }
         }
-        if (CF::STG && s > 0) rows_of(Bm, a.bs, 0, bn);
         if (!DELTA && s > 0) ask_x(0, xn);
         f32x4 O[4], Rt[4], xt[4];
         // ---- what the held state gives: O = diag(E) C h^T, Rt = beta (x - diag(E) B h^T) ----
-        F8 fc[CF::NB][KS], fb[CF::NB][KS];  // the tile in work and, where registers allow, the next
-        auto ask_rows = [&](int kt, F8 (&c)[KS], F8 (&b)[KS]) {
+        constexpr int MATS = DELTA ? 2 : 1, STEPS = MATS * CH;  // chunks of a tile: C's, then B's
+        F8 fr[2][KC];  // the chunk in work and the next
+        auto ask = [&](int i) {
+            const int kt = i / STEPS, mat = i / CH % MATS, c = i % CH;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                c[ks] = CF::STG ? kept(x1, kt, ks) : frag(Cm, a.cs, q0 + 16 * kt + l16, ks);
-                if (DELTA) b[ks] = CF::STG ? kept(x2, kt, ks) : frag(Bm, a.bs, q0 + 16 * kt + l16, ks);
-            }
+            for (int ks = 0; ks < KC; ++ks)
+                fr[i & 1][ks] = CF::STG ? kept(mat ? x2 : x1, kt, c * KC + ks)
+                                        : frag(mat ? Bm : Cm, mat ? a.bs : a.cs, q0 + 16 * kt + l16, c * KC + ks);
         };
-        if (CF::NB == 2) ask_rows(0, fc[0], fb[0]);
+        ask(0);
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt) {
             const int k0 = q0 + 16 * kt;
             O[kt] = Rt[kt] = zero4;
             xt[kt] = take_x(xq[kt], k0);  // (zero past the last node)
             if (kt < nk && mine) {
-                f32x4 o = zero4, v = zero4;
-                if (CF::NB == 1) ask_rows(kt, fc[0], fb[0]);
-                together(fc[kt % CF::NB]);
-                if (DELTA) together(fb[kt % CF::NB]);
-                if (CF::NB == 2 && kt + 1 < 4) ask_rows(kt + 1, fc[(kt + 1) % CF::NB], fb[(kt + 1) % CF::NB]);
+                f32x4 ov[MATS][kTwo<T>];
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    o = mul(o, fc[kt % CF::NB][ks], hs[ks]);
-                    if (DELTA) v = mul(v, fb[kt % CF::NB][ks], hs[ks]);
+                for (int j = 0; j < STEPS; ++j) {
+                    const int i = kt * STEPS + j, mat = j / CH, c = j % CH;
+                    together(fr[i & 1]);
+                    if (i + 1 < 4 * STEPS) ask(i + 1);
+#pragma unroll
+                    for (int ks = 0; ks < KC; ++ks)
+#pragma unroll
+                        for (int p = 0; p < kTwo<T>; ++p)
+                            ov[mat][p] = mma(c == 0 && ks == 0 ? zero4 : ov[mat][p], fr[i & 1][ks], hs[c * KC + ks].t[p]);
                 }
                 const f32x4 e4 = ld4(decay + k0 + 4 * q);
-                settle(o);
-                O[kt] = e4 * o;
+#pragma unroll
+                for (int p = 0; p < kTwo<T>; ++p) {
+                    settle(ov[0][p]);
+                    if (DELTA) settle(ov[MATS - 1][p]);
+                }
+                O[kt] = e4 * (kTwo<T> == 2 ? ov[0][0] + ov[0][kTwo<T> - 1] : ov[0][0]);
                 if (DELTA) {
-                    const f32x4 b4 = ld4(betas + k0 + 4 * q);
-                    settle(v);
+                    const f32x4 v = kTwo<T> == 2 ? ov[MATS - 1][0] + ov[MATS - 1][kTwo<T> - 1] : ov[MATS - 1][0];
+                    const f32x4 b4 = ld4(betas + (mine ? hw : 0) * kp + k0 + 4 * q);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) Rt[kt][e] = e4[e] < 0.f ? 0.f : b4[e] * (xt[kt][e] - e4[e] * v[e]);
                 }
             }
         }
+        if (CF::STG) {  // the table rows of this wave again, from LDS: the state's products had their registers
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) rs[ks] = kept(DELTA && kind ? x2 : x1, tw, ks);
+        }
+#pragma unroll 1
         for (int sp = 0; sp <= s; ++sp) {
             const bool own = sp == s;
             const int j0 = sp * kPanel;
+            again();
             // the tables are free, and so is x1 (the products with C, or the panel before, are done)
-            if (s > 0 || (CF::STG && DELTA)) __syncthreads();
-            if (CF::STG && !own && sp == 0) {
-                keep(x1, bn);
+            if (CF::STG && sp == 0 && !own) {
+                F8 bn[KH];
+                ask_b(0, bn);
+                __syncthreads();
+                keep_b(bn);
+                __syncthreads();
+            } else if (s > 0) {
                 __syncthreads();
             }
-            // ---- M and T of this wave's node tile against panel sp ----
-            if (w < nk) {
-                const int k = q0 + 16 * w + l16;
-                const u64 on = decay[k] < 0.f ? 0 : mask[k * panels + sp];
-                const double ck = cs[k];
-                const float bk = DELTA ? betas[k] : 0.f;
+            // ---- this wave's table rows against panel sp ----
+            if (tw < nk) {
+                const int k = q0 + 16 * tw + l16;
+                const u64 path = mask[sp * kp + k];
                 const T* bj0 = own ? x2 : x1;
-                f32x4 diag = zero4;
-                F8 bj[CF::NB][KS];  // the tile in work and, where registers allow, the next
-                auto ask = [&](int jt, F8 (&v)[KS]) {
+                T* tab = (DELTA && kind ? ttabs : mtabs) + tw * TAB;
+                F8 fr[2][KC];
+                constexpr int JT = DELTA ? 4 : 2;
+                const int jt0 = DELTA ? 0 : 2 * kind;
+                auto ask = [&](int i) {
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) v[ks] = CF::STG ? kept(bj0, jt, ks) : frag(Bm, a.bs, j0 + 16 * jt + l16, ks);
+                    for (int ks = 0; ks < KC; ++ks)
+                        fr[i & 1][ks] = CF::STG ? kept(bj0, jt0 + i / CH, i % CH * KC + ks)
+                                                : frag(Bm, a.bs, j0 + 16 * (jt0 + i / CH) + l16, i % CH * KC + ks);
                 };
-                if (CF::NB == 2) ask(0, bj[0]);
+                ask(0);
 #pragma unroll
-                for (int jt = 0; jt < 4; ++jt)
-                    if (!own || jt < ((w + 2) & ~1)) {
-                        if (CF::NB == 1) ask(jt, bj[0]);
-                        together(bj[jt % CF::NB]);
-                        if (CF::NB == 2 && jt + 1 < 4) ask(jt + 1, bj[(jt + 1) % CF::NB]);
-                        f32x4 m, t, c = zero4, b = zero4;
+                for (int j = 0; j < JT; ++j) {
+                    const int jt = jt0 + j;
+                    if (!own || jt < ((tw + 2) & ~1)) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        f32x4 c = zero4;
 #pragma unroll
-                        for (int ks = 0; ks < KS; ++ks) {
-                            c = mma(c, bj[jt % CF::NB][ks], cf[ks]);
-                            if (DELTA) b = mma(b, bj[jt % CF::NB][ks], bf[ks]);
+                        for (int i = 0; i < CH; ++i) {
+                            F8(&f)[KC] = fr[(j * CH + i) & 1];
+                            together(f);
+                            if (j * CH + i + 1 < JT * CH) ask(j * CH + i + 1);
+#pragma unroll
+                            for (int ks = 0; ks < KC; ++ks)
+                                c = mma(c, f[ks], CF::STG ? rs[i * KC + ks] : DELTA ? frag(rows, rows_st, k, i * KC + ks) : frag(Cm, a.cs, k, i * KC + ks));
                         }
                         settle(c);
-                        if (DELTA) settle(b);
-                        // (no node behind its own is on its path, so the tile past the last is zero of itself)
-                        weigh<DELTA>((unsigned)(on >> (16 * jt + 4 * q)) & 15u, ck, cs + j0 + 16 * jt + 4 * q, bk,
-                                     k - j0 - 16 * jt - 4 * q, c, b, m, t);
-                        put(mt + w * TAB, jt >> 1, jt & 1, lane, m);
-                        if (DELTA) {
-                            if (own && jt == w) {
-                                diag = t;
-                                t = zero4;
+#pragma unroll
+                        for (int hd = 0; hd < 2; ++hd)
+                            if (hd < place.nh) {
+                                // (no node behind its own is on its path, so the tile past the last is zero of itself; T's
+                                // diagonal tile is in its inverse)
+                                const float* dh = decays + hd * kp;
+                                const double* ch = css + hd * kp;
+                                f32x4 v = weigh(dh[k] < 0.f ? 0u : (unsigned)(path >> (16 * jt + 4 * q)) & 15u, ch[k],
+                                                ch + j0 + 16 * jt + 4 * q, DELTA && kind ? betas[hd * kp + k] : 1.f, c);
+                                if (DELTA && kind && own && jt == tw) v = zero4;
+                                put(tab + hd * 4 * TAB, jt >> 1, jt & 1, lane, v);
                             }
-                            put(tt + w * TAB, jt >> 1, jt & 1, lane, t);
-                        }
                     }
-                if (DELTA && own) {
-                    T* inv = x1 + w * 1024 / (int)sizeof(T);
-                    put_inv(inv, lane, inverse16(diag, reinterpret_cast<float*>(inv), lane));
+                }
+                if (DELTA && own && kind < place.nh) {  // head `kind`'s inverse
+                    f32x4 b = zero4;
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) {
+#pragma unroll
+                        for (int ks = 0; ks < KC; ++ks)
+                            fr[0][ks] = CF::STG ? kept(x2, tw, i * KC + ks) : frag(Bm, a.bs, k, i * KC + ks);
+                        together(fr[0]);
+#pragma unroll
+                        for (int ks = 0; ks < KC; ++ks) b = mma(b, fr[0][ks], fr[0][ks]);
+                    }
+                    settle(b);
+                    const int of = kind * kp;
+                    const u64 strict = decays[of + k] < 0.f ? 0 : path & ~(1ull << (16 * tw + l16));
+                    T* inv = reinterpret_cast<T*>(smem + at.inv + (kind * 4 + tw) * 1024);
+                    const f32x4 t = weigh((unsigned)(strict >> (16 * tw + 4 * q)) & 15u, css[of + k], css + of + q0 + 16 * tw + 4 * q, betas[of + k], b);
+                    put_inv(inv, lane, inverse16(t, reinterpret_cast<float*>(inv), lane));
                 }
             }
-            if (own) {  // the next panel's rows, behind this one's last use of them
-                rows_of(Cm, a.cs, q0 + kPanel, cf);
-                rows_of(Bm, a.bs, q0 + kPanel, bf);
-                ask_x(q0 + kPanel, xq);
+            if (CF::STG && sp + 1 < s) {
+                F8 bn[KH];
+                ask_b(j0 + kPanel, bn);
+                __syncthreads();
+                keep_b(bn);  // (read behind the next barrier)
+            } else {
+                __syncthreads();
             }
-            if (CF::STG && sp + 1 < s) rows_of(Bm, a.bs, j0 + kPanel, bn);
-            __syncthreads();
-            if (CF::STG && sp + 1 < s) keep(x1, bn);  // (read behind the next barrier)
-            if (!mine) continue;
+            again();
             // ---- panel sp's part of Rt and O ----
+            F8 xf[2];
+            Op<T> uf[2];
             if constexpr (!DELTA) {
-                F8 xf[2];
 #pragma unroll
                 for (int f = 0; f < 2; ++f)
                     xf[f] = own ? pair8(x, xt[2 * f], xt[2 * f + 1])
                                 : pair8(x, take_x(xn[2 * f], j0 + 32 * f), take_x(xn[2 * f + 1], j0 + 32 * f + 16));
                 if (sp + 1 < s) ask_x(j0 + kPanel, xn);
+            } else if (own) {
+                const T* inv0 = reinterpret_cast<const T*>(smem + at.inv + (mine ? hw : 0) * 4096);
+                f32x4 u[2];
+                split(join(zero4, zero4), uf[0]);
+                split(join(zero4, zero4), uf[1]);
 #pragma unroll
                 for (int kt = 0; kt < 4; ++kt)
-                    if (kt < nk) {
-                        Op<T> m0 = get(mt + kt * TAB, 0, lane), m1 = get(mt + kt * TAB, 1, lane);
-                        together(m0);
-                        together(m1);
-                        O[kt] = mul(O[kt], m0, xf[0]);
-                        if (!own || kt >= 2) O[kt] = mul(O[kt], m1, xf[1]);
-                        settle(O[kt]);
+                    if (kt < nk && mine) {
+                        const auto inv = get_inv(inv0 + kt * 1024 / (int)sizeof(T), lane);
+                        f32x4 t = zero4;
+                        Op<T> to[2];
+#pragma unroll
+                        for (int f = 0; 2 * f < kt; ++f) to[f] = get(tt + kt * TAB, f, lane);
+#pragma unroll
+                        for (int f = 0; 2 * f < kt; ++f) {
+                            together(to[f]);
+                            t = mul(t, to[f], uf[f]);
+                        }
+                        u[kt & 1] = times_inv(inv, Rt[kt] - t);
+                        split(join(u[0], kt & 1 ? u[1] : zero4), uf[kt >> 1]);
                     }
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    if (s == 0) u0[f] = uf[f];
+                    if (s == 1) u1[f] = uf[f];
+                    if (s == 2) u2[f] = uf[f];
+                }
             } else {
-                Op<T> uf[2];
-                T* us = reinterpret_cast<T*>(smem + at.u + (sp * 4 + w) * kTableBytes);
-                if (own) {
-                    f32x4 u[4] = {zero4, zero4, zero4, zero4};
-                    split(join(zero4, zero4), uf[0]);
-                    split(join(zero4, zero4), uf[1]);
 #pragma unroll
-                    for (int kt = 0; kt < 4; ++kt)
-                        if (kt < nk) {
-                            const auto inv = get_inv(x1 + kt * 1024 / (int)sizeof(T), lane);
-                            f32x4 t = zero4;
-                            Op<T> to[2];
-#pragma unroll
-                            for (int f = 0; 2 * f < kt; ++f) to[f] = get(tt + kt * TAB, f, lane);
-#pragma unroll
-                            for (int f = 0; 2 * f < kt; ++f) {
-                                together(to[f]);
-                                t = mul(t, to[f], uf[f]);
-                            }
-                            u[kt] = times_inv(inv, Rt[kt] - t);
-                            split(join(u[kt & ~1], u[kt | 1]), uf[kt >> 1]);
-                        }
-                    if (s + 1 < panels) {
-#pragma unroll
-                        for (int f = 0; f < 2; ++f)
-#pragma unroll
-                            for (int t = 0; t < kTwo<T>; ++t) st8(us + ((f * kTwo<T> + t) * 64 + lane) * 8, uf[f].t[t]);
-                    }
-                } else {
-                    uf[0] = get(us, 0, lane);
-                    uf[1] = get(us, 1, lane);
-#pragma unroll
-                    for (int kt = 0; kt < 4; ++kt)
-                        if (kt < nk) {
-                            Op<T> t0 = get(tt + kt * TAB, 0, lane), t1 = get(tt + kt * TAB, 1, lane);
-                            together(t0);
-                            together(t1);
-                            f32x4 t = mul(mul(zero4, t0, uf[0]), t1, uf[1]);
-                            settle(t);
-                            Rt[kt] -= t;
-                        }
+                for (int f = 0; f < 2; ++f) {
+                    uf[f] = u0[f];
+                    if (sp == 1) uf[f] = u1[f];
+                    if (sp == 2) uf[f] = u2[f];
                 }
 #pragma unroll
                 for (int kt = 0; kt < 4; ++kt)
-                    if (kt < nk) {
-                        Op<T> m0 = get(mt + kt * TAB, 0, lane), m1 = get(mt + kt * TAB, 1, lane);
-                        together(m0);
-                        together(m1);
-                        O[kt] = mul(O[kt], m0, uf[0]);
-                        if (!own || kt >= 2) O[kt] = mul(O[kt], m1, uf[1]);
-                        settle(O[kt]);
+                    if (kt < nk && mine) {
+                        Op<T> t0 = get(tt + kt * TAB, 0, lane), t1 = get(tt + kt * TAB, 1, lane);
+                        together(t0);
+                        together(t1);
+                        f32x4 t = mul(mul(zero4, t0, uf[0]), t1, uf[1]);
+                        settle(t);
+                        Rt[kt] -= t;
                     }
             }
+            if (own) {  // the next panel's rows
+                __builtin_amdgcn_sched_barrier(0);
+                if (CF::STG) ask_own(q0 + kPanel);
+                ask_x(q0 + kPanel, xq);
+            }
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt)
+                if (kt < nk && mine) {
+                    Op<T> m0 = get(mt + kt * TAB, 0, lane), m1 = get(mt + kt * TAB, 1, lane);
+                    together(m0);
+                    together(m1);
+                    if constexpr (DELTA) {
+                        O[kt] = mul(O[kt], m0, uf[0]);
+                        if (!own || kt >= 2) O[kt] = mul(O[kt], m1, uf[1]);
+                    } else {
+                        O[kt] = mul(O[kt], m0, xf[0]);
+                        if (!own || kt >= 2) O[kt] = mul(O[kt], m1, xf[1]);
+                    }
+                    settle(O[kt]);
+                }
         }
+        again();
         // ---- y ----
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt)
@@ -958,13 +1068,14 @@ __global__ __launch_bounds__(256) void k_tree_long(Args a) {
                     const float o = DELTA ? O[kt][e] : O[kt][e] + D * xt[kt][e];
                     v[e] = e4[e] == -1.f ? 0.f : e4[e] == -2.f ? nan : o;
                 }
-                if (anybad) {
+                if (anybad) {  // a bad x on the node's path
+                    unsigned hits = 0;
+#pragma unroll 1
+                    for (int i = 0; i < 4 * (s + 1); ++i)
+                        if (mask[(i >> 2) * kp + k0 + 4 * q + (i & 3)] & badx[(i >> 2) * badp]) hits |= 1u << (i & 3);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        u64 hit = 0;  // a bad x on the node's path
-                        for (int i = 0; i <= s; ++i) hit |= mask[(k0 + 4 * q + e) * panels + i] & badx[i * 64 + 16 * w + l16];
-                        if (hit && !(e4[e] < 0.f)) v[e] = nan;
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        if (hits >> e & 1 && !(e4[e] < 0.f)) v[e] = nan;
                 }
                 store_y(y, ys, k0, K, lane, sel, upper, v);
             }
@@ -1002,9 +1113,11 @@ int run_tree_n(const Args& a) {
     if (a.T <= 32) return launch_tree<T, N, DELTA, 2>(a);
     if (a.T <= 48) return launch_tree<T, N, DELTA, 3>(a);
     if (a.T <= kPanel) return launch_tree<T, N, DELTA, 4>(a);
-    const size_t lds = (size_t)LongLds(LongCfg<T, N, DELTA>::MASK, (int)a.T, DELTA).total;
+    typedef LongCfg<T, N, DELTA> CF;
+    const int hg = a.H / a.G, heads = a.P <= 64 && hg > 1 && a.b * a.H > 256 ? 2 : 1;
+    const size_t lds = (size_t)LongLds((int)a.T, heads, a.P / 16, DELTA, CF::STG ? CF::ROWS : 0).total;
     if (!delta::lds_limit(k_tree_long<T, N, DELTA>, lds)) return 7;
-    k_tree_long<T, N, DELTA><<<(unsigned)(a.b * a.H * (a.P > 64 ? a.P / 64 : 1)), 256, lds, a.stream>>>(a);
+    k_tree_long<T, N, DELTA><<<(unsigned)(a.b * a.G * ((hg + heads - 1) / heads)), 512, lds, a.stream>>>(a, heads);
     return hipGetLastError() == hipSuccess ? 0 : 7;
 }
 template <typename T, bool DELTA>
