@@ -708,7 +708,7 @@ __global__ __launch_bounds__(512) void k_tree_long(Args a, int heads) {
             for (int i = 0; i < KH; ++i) st8(x1 + ((tw * KS + first + i) * 64 + lane) * 8, bn[i]);
     };
     // a thread a node and head
-    const int nt = tid & 255, ht = tid >> 8;
+    const int nt = tid & 255, ht = w >> 2;
     const bool in = nt < K;
     const int64_t node = row0 + (in ? nt : K - 1);
     const int hn = place.h0 + (ht < place.nh ? ht : 0);
@@ -952,24 +952,27 @@ __global__ __launch_bounds__(512) void k_tree_long(Args a, int heads) {
                             }
                     }
                 }
-                if (DELTA && own && kind < place.nh) {  // head `kind`'s inverse
-                    f32x4 b = zero4;
+                // head `kind`'s inverses: two tiles each for the waves with the shorter table rows
+                if (DELTA && own && tw < 2 && kind < place.nh)
+#pragma unroll 1
+                    for (int it = tw; it < nk && it <= 3 - tw; it += 3 - 2 * tw) {
+                        f32x4 b = zero4;
 #pragma unroll
-                    for (int i = 0; i < CH; ++i) {
+                        for (int i = 0; i < CH; ++i) {
 #pragma unroll
-                        for (int ks = 0; ks < KC; ++ks)
-                            fr[0][ks] = CF::STG ? kept(x2, tw, i * KC + ks) : frag(Bm, a.bs, k, i * KC + ks);
-                        together(fr[0]);
+                            for (int ks = 0; ks < KC; ++ks)
+                                fr[0][ks] = CF::STG ? kept(x2, it, i * KC + ks) : frag(Bm, a.bs, q0 + 16 * it + l16, i * KC + ks);
+                            together(fr[0]);
 #pragma unroll
-                        for (int ks = 0; ks < KC; ++ks) b = mma(b, fr[0][ks], fr[0][ks]);
+                            for (int ks = 0; ks < KC; ++ks) b = mma(b, fr[0][ks], fr[0][ks]);
+                        }
+                        settle(b);
+                        const int n = kind * kp + q0 + 16 * it;
+                        const u64 strict = decays[n + l16] < 0.f ? 0 : mask[s * kp + q0 + 16 * it + l16] & ~(1ull << (16 * it + l16));
+                        T* inv = reinterpret_cast<T*>(smem + at.inv + (kind * 4 + it) * 1024);
+                        const f32x4 t = weigh((unsigned)(strict >> (16 * it + 4 * q)) & 15u, css[n + l16], css + n + 4 * q, betas[n + l16], b);
+                        put_inv(inv, lane, inverse16(t, reinterpret_cast<float*>(inv), lane));
                     }
-                    settle(b);
-                    const int of = kind * kp;
-                    const u64 strict = decays[of + k] < 0.f ? 0 : path & ~(1ull << (16 * tw + l16));
-                    T* inv = reinterpret_cast<T*>(smem + at.inv + (kind * 4 + tw) * 1024);
-                    const f32x4 t = weigh((unsigned)(strict >> (16 * tw + 4 * q)) & 15u, css[of + k], css + of + q0 + 16 * tw + 4 * q, betas[of + k], b);
-                    put_inv(inv, lane, inverse16(t, reinterpret_cast<float*>(inv), lane));
-                }
             }
             if (CF::STG && sp + 1 < s) {
                 F8 bn[KH];
