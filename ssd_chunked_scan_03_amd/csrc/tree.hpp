@@ -96,6 +96,9 @@ template <typename T, int N, bool DELTA, int NK>
 struct TreeCfg {
     static constexpr int KS = N < 32 ? 1 : N / 32;
     static constexpr int ROWS = NK * KS * 512 * (int)sizeof(T);  // bytes of C's or B's fragments
+    // Waves a SIMD at least: three where the registers suffice without spills (32 trees of 40 nodes, wide heads, the
+    // delta rule: 30.9 us, with two 35.3).
+    static constexpr int WAVES = DELTA && NK < 4 && KS * (int)sizeof(T) <= 8 && sizeof(T) == 2 ? 3 : 1;
     static constexpr bool LCB = ROWS * (DELTA ? 2 : 1) <= 65536;
     static constexpr int TAB = NK == 1 ? 2048 : NK == 2 ? 4096 : NK == 3 ? 8192 : 12288;
     static constexpr int M = 0;                                                   // [tile] M as fragments
@@ -328,13 +331,20 @@ __device__ __forceinline__ f32x4 clean_x(f32x4 v, const float* decay4, unsigned&
 // from LDS alone, while the next head's state and x are on their way: no load is waited for behind a store of y.
 // ---------------------------------------------------------------------------
 template <typename T, int N, bool DELTA, int NK>
-__global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
+__global__ __launch_bounds__(256, (TreeCfg<T, N, DELTA, NK>::WAVES)) void k_tree(Args a, int hb) {
     typedef typename V8<T>::type F8;
     typedef TreeCfg<T, N, DELTA, NK> CF;
     constexpr int KS = CF::KS;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int waves = blockDim.x >> 6, K = (int)a.T, P = a.P, H = a.H, cols = P < 64 ? P / 16 : 4;
-    const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4;
+    const int w = wave_id();
+    int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+    // addresses are formed again where they are used: kept over the loop they would take the registers of operands
+    auto again = [&] {
+        asm volatile("" : "+v"(lane));
+        l16 = lane & 15;
+        q = lane >> 4;
+    };
     const Place at(a, hb, cols, w);
     const int64_t row0 = at.bi * K, ys = (int64_t)H * P;
     const unsigned sel = delta::quad_sel(lane);
@@ -494,6 +504,7 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
 
     const float nan = __builtin_nanf("");
     for (int hh = 0; hh < at.nh; ++hh) {
+        again();
         const int h = at.h0 + hh;
         // ---- M and T of this wave's node tile ----
         if (tiled) {
@@ -534,6 +545,7 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
             if (hh + 1 < at.nh) __syncthreads();
             continue;
         }
+        again();
         // ---- this head's operands; then the next head's are asked for ----
         f32x4 xr[NK];
         u64 badx = 0;
@@ -567,30 +579,40 @@ __global__ __launch_bounds__(256) void k_tree(Args a, int hb) {
         for (int kt = 0; kt < NK; ++kt) {
             const int k0 = 16 * kt;
             f32x4 o = zero4, v = zero4;
-            F8 fc[KS], fb[KS];
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                fc[ks] = CF::LCB ? kept(crow, kt, ks) : frag(Cm, a.cs, k0 + l16, ks);
-                if (DELTA) fb[ks] = CF::LCB ? kept(brow, kt, ks) : frag(Bm, a.bs, k0 + l16, ks);
-            }
-            const f32x4 e4 = ld4(decay + hh * 64 + k0 + 4 * q);
+            F8 fr[KS];
             Op<T> mo[2], to[2];
+            auto ask_tables = [&] {
 #pragma unroll
-            for (int f = 0; 2 * f <= kt; ++f) {
-                mo[f] = get(mtab + CF::at(kt) / (int)sizeof(T), f, lane);
-                if (DELTA && 2 * f < kt) to[f] = get(ttab + CF::at(kt) / (int)sizeof(T), f, lane);
-            }
-            together(fc);
-            if (DELTA) together(fb);
+                for (int f = 0; 2 * f <= kt; ++f) {
+                    mo[f] = get(mtab + CF::at(kt) / (int)sizeof(T), f, lane);
+                    if (DELTA && 2 * f < kt) to[f] = get(ttab + CF::at(kt) / (int)sizeof(T), f, lane);
+                }
+            };
+            auto have_tables = [&] {
 #pragma unroll
-            for (int f = 0; 2 * f <= kt; ++f) {
-                together(mo[f]);
-                if (DELTA && 2 * f < kt) together(to[f]);
-            }
+                for (int f = 0; 2 * f <= kt; ++f) {
+                    together(mo[f]);
+                    if (DELTA && 2 * f < kt) together(to[f]);
+                }
+            };
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                o = mul(o, fc[ks], hs[ks]);
-                if (DELTA) v = mul(v, fb[ks], hs[ks]);
+            for (int ks = 0; ks < KS; ++ks) fr[ks] = CF::LCB ? kept(crow, kt, ks) : frag(Cm, a.cs, k0 + l16, ks);
+            const f32x4 e4 = ld4(decay + hh * 64 + k0 + 4 * q);
+            if (!DELTA) ask_tables();
+            together(fr);
+            if (!DELTA) have_tables();
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) o = mul(o, fr[ks], hs[ks]);
+            if constexpr (DELTA) {
+                // B's rows take the registers of C's, and the tables theirs: a third wave a SIMD hides the wait
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) fr[ks] = CF::LCB ? kept(brow, kt, ks) : frag(Bm, a.bs, k0 + l16, ks);
+                together(fr);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) v = mul(v, fr[ks], hs[ks]);
+                ask_tables();
+                have_tables();
             }
             o *= e4;
             if constexpr (DELTA) {
