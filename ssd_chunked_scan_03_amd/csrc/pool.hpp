@@ -37,6 +37,9 @@ struct Args {
 // state is read once and written once, and asked for first.  Tokens' operands (STAGE) come to LDS
 // kBatch tokens at a time, so that their latency is paid once for all of them; a single token's
 // go straight to registers.  Grid (b H, ceil(P N / (2048 CH))), 256 threads.
+// Bound by the state's bytes where there are many rows: one token of 128 rows, 80 heads of 64, dstate 128, 671 MB in 136 us
+// (4.9 TB/s; a large copy reaches 5.2); paths of 5 nodes of 64 such rows with the delta rule, 336 MB, 80 us, behind the
+// walk up the tree and the row sums of every token.  One row of 48 heads: 5 us, a chain of latencies.
 // ---------------------------------------------------------------------------
 constexpr int kBatch = 16;
 

@@ -9,12 +9,19 @@
 // u_t = (I + T_tt)^-1 (r_t - T_{t,<t} u_{<t}) for tiles t of 16 nodes.  The state is read once and no
 // state is formed per node.
 //
-// One work-group per (row, head, up to 64 columns of headdim), a wave per 16 columns.  The waves share
-// the forming of M and T (a node tile each, B B^T and B C^T on the matrix cores, weighted by the
-// decays) through LDS; every other product stays in its wave: the state's rows are operand fragments
-// straight from memory, and accumulators (rows 4 (l / 16) + e of a node tile, column l % 16) feed the
-// next product as operands whose k index runs 16 (e / 4) + 4 (l / 16) + e % 4.  Nodes are taken 64 at a
-// time, against panels of 64 nodes up to their own.
+// A wave has 16 columns of headdim of one head; the state's rows are operand fragments straight from
+// memory, and accumulators (rows 4 (l / 16) + e of a node tile, column l % 16) feed the next product as
+// operands whose k index runs 16 (e / 4) + 4 (l / 16) + e % 4, so u never leaves its wave.  The waves of a
+// work-group share the forming of M and T (B B^T and B C^T on the matrix cores, weighted by the decays), which
+// reach them through LDS.  Up to 64 nodes (k_tree) the heads of a group follow each other in a work-group that
+// keeps B's products; longer trees (k_tree_long) go 64 nodes at a time against panels of 64 up to their own.
+//
+// What bounds it.  A batch of trees reads each state once and each x, y once: 64 trees of 64 nodes, 80 heads of
+// 64, dstate 128 move 255 MB in 67 us, 3.8 TB/s of reads and writes mixed (a large copy: 5.2), with the
+// setup of a work-group (paths, decays, the first state: 13 to 22 thousand cycles, the last of which wait for memory)
+// overlapped with its neighbours only.  Long trees are bound inside the CU: of 84 us for 16 lines of 200 nodes, 32 heads
+// of 64, dstate 256, the delta rule, the table rows take 40% (the decays' exponentials and the splitting in two terms on
+// the vector ALU), the reads of tables and rows from LDS 30%; memory would need 17 us.
 //
 // Precision.  bfloat16 problems: float32 factors (state, M, T, inverse, right side, u) enter the matrix
 // cores as two bfloat16 terms, which leaves 2^-16 of them, far below y's own rounding; float32 problems
@@ -268,8 +275,8 @@ __device__ __forceinline__ double orders(float dt, double A) {
 typedef unsigned long long u64;
 
 // Which (row, group, heads, columns) a work-group takes; cols: its waves that have columns (the others get addresses of
-// theirs, so that loads need no branch: behind one the compiler waits for everything that may be on its way).  Blocks k, k + 8, ... run on one XCD: each takes a
-// contiguous range, so that a row's B, C and dt stay in its L2.
+// theirs, so that loads need no branch: behind one the compiler waits for everything that may be on its way).  Blocks
+// k, k + 8, ... run on one XCD: each takes a contiguous range, so that a row's B, C and dt stay in its L2.
 struct Place {
     int64_t bi;
     int g, h0, nh, p0;
@@ -326,9 +333,12 @@ __device__ __forceinline__ f32x4 clean_x(f32x4 v, const float* decay4, unsigned&
 
 // ---------------------------------------------------------------------------
 // k_tree: trees of up to 16 NK nodes.  A work-group takes hb heads of a group one after another: paths, the
-// products of B with C and itself, and the rows of C and B are formed or fetched once for them.  Wave w forms the tables of node
-// tile w (w < NK) and has 16 columns (w < cols).  Per head: tables, a barrier, then each wave's columns tile by tile
-// from LDS alone, while the next head's state and x are on their way: no load is waited for behind a store of y.
+// products of B with C and itself, and the rows of C and B are formed or fetched once for them.  Wave w forms the tables
+// of node tile w (w < NK) and has 16 columns (w < cols).  Per head: tables, a barrier, then each wave's columns tile by
+// tile from LDS alone, while the next head's state and x are on their way: no load is waited for behind a store of y.
+// Times: one tree of 8 nodes over 48 heads of 64, dstate 128 6.0 us (a chain of latencies: parents and slot, the
+// state, tables, products); 64 trees of 64 nodes, 80 heads 67 us; 32 trees of 40 nodes, 32 heads of 128, 16 groups, the
+// delta rule 31 us (k_tree_long, which has the 64 nodes in one panel, would need 113 and 52).
 // ---------------------------------------------------------------------------
 template <typename T, int N, bool DELTA, int NK>
 __global__ __launch_bounds__(256, (TreeCfg<T, N, DELTA, NK>::WAVES)) void k_tree(Args a, int hb) {
@@ -652,8 +662,11 @@ __global__ __launch_bounds__(256, (TreeCfg<T, N, DELTA, NK>::WAVES)) void k_tree
 // ---------------------------------------------------------------------------
 // k_tree_long: trees of 65 to 256 nodes, 64 nodes at a time against every panel of 64 up to their own.  Eight waves
 // take one head, or two of a group (16 columns a wave).  For the tables, wave w has node tile w % 4 and one operand's
-// rows: C's (waves 0 to 3, M) or B's (4 to 7, T and the inverses); a product serves both heads.  The scan has no T:
-// its waves 4 to 7 take half of M's tiles.
+// rows: C's (waves 0 to 3, M) or B's (4 to 7, T); a product serves both heads, and the diagonal tiles' inverses go to the
+// waves with the shorter rows of the own panel.  The scan has no T: its waves 4 to 7 take half of M's tiles.  u of
+// earlier panels stays in registers, two terms as the next product takes them; no tile goes back to memory.
+// 16 lines of 200 nodes, 32 heads of 64, 8 groups, dstate 256, the delta rule: 84 us (one head a work-group 129, rows
+// from memory for every product 298).
 // ---------------------------------------------------------------------------
 template <typename T, int N, bool DELTA>
 __global__ __launch_bounds__(512) void k_tree_long(Args a, int heads) {
@@ -690,7 +703,7 @@ __global__ __launch_bounds__(512) void k_tree_long(Args a, int heads) {
     float* decays = reinterpret_cast<float*>(smem + at.e);
     float* betas = reinterpret_cast<float*>(smem + at.beta);
     int* ptr = reinterpret_cast<int*>(smem);  // [node], in M's place while the paths are formed
-    u64* badx = reinterpret_cast<u64*>(smem + at.badx) + (mine ? w * 16 + l16 : 0);
+    u64* badx = reinterpret_cast<u64*>(smem + at.badx) + (mine ? (hw * cols + cw) * 16 + l16 : 0);
     const int badp = heads * cols * 16;       // from one panel's to the next
     unsigned* badb = reinterpret_cast<unsigned*>(smem + at.badb);
     unsigned* more = reinterpret_cast<unsigned*>(smem + at.more);
@@ -1107,8 +1120,10 @@ __global__ __launch_bounds__(512) void k_tree_long(Args a, int heads) {
     }
 }
 
-// Heads of a group that a work-group takes one after another: the fewest rounds of work-groups (as many at once as LDS lets
-// in, up to three a CU), each of which costs its heads and two more for what they share.
+// Heads of a group that a work-group takes one after another: the fewest rounds of work-groups (as many at once as LDS
+// lets in, up to three a CU), each of which costs its heads and two more for what they share.  One / the rule's / four /
+// eight heads: 64 trees of 64 nodes, 80 heads in one group 85 / 68 / 68 / 74 us, the delta rule 131 / 92 / 95 / 109; 8 of
+// them 15.7 / 15.5 / 20 / 33; one tree of 8 nodes over 48 heads 9.6 / 9.7 / 9.9 / 15.9.
 inline int tree_heads(const Args& a, int slabs, int lds0, int lds_head) {
     const int hg = a.H / a.G;
     int best = 1;
@@ -1139,6 +1154,8 @@ int run_tree_n(const Args& a) {
     if (a.T <= 48) return launch_tree<T, N, DELTA, 3>(a);
     if (a.T <= kPanel) return launch_tree<T, N, DELTA, 4>(a);
     typedef LongCfg<T, N, DELTA> CF;
+    // Two heads a work-group where one each would leave CUs a second one and the waves suffice (16 lines of 200 nodes
+    // above: one 129 us, two 84; 16 rows of 65 nodes at dstate 128: 44 and 28).
     const int hg = a.H / a.G, heads = a.P <= 64 && hg > 1 && a.b * a.H > 256 ? 2 : 1;
     const size_t lds = (size_t)LongLds((int)a.T, heads, a.P / 16, DELTA, CF::STG ? CF::ROWS : 0).total;
     if (!delta::lds_limit(k_tree_long<T, N, DELTA>, lds)) return 7;

@@ -185,6 +185,55 @@ def test_many_rows_fill_the_gpu_like_few():
         assert torch.equal(tree(one)[0], y[i]), i
 
 
+@pytest.mark.parametrize("rule", ["scan", "delta"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [16, 32, 64, 128, 256])
+def test_every_state_width(N, dtype, rule):
+    """Every dstate at each number of node tiles and of panels, over the headdims (16 and 32 leave waves
+    without columns, 128 needs a second set)."""
+    for i, K in enumerate([2, 15, 16, 31, 32, 47, 48, 64, 65, 127, 129, 193]):
+        P = [16, 32, 64, 128][(i + N // 16) % 4]
+        check_tree(ref.make(2, K, 3, P, N, 1, 700 + K, dtype, rule, ["tree", "holes"][i % 2]), (N, K, P, rule, dtype))
+
+
+# b, K, H, P, N, G, dtype, kind: enough rows and heads that a work-group of a long tree takes two heads
+LONG = [
+    (43, 70, 6, 16, 32, 2, "bf16", "holes"),  # (three heads a group: the last one alone)
+    (33, 129, 8, 32, 16, 1, "f32", "deep"),
+    (33, 65, 8, 64, 128, 4, "bf16", "ragged"),
+    (65, 200, 4, 16, 256, 2, "bf16", "line"),
+    (65, 200, 4, 64, 256, 1, "bf16", "deep"),
+    (33, 256, 8, 16, 64, 1, "f32", "tree"),
+    (65, 100, 4, 32, 256, 1, "f32", "deep"),
+    (129, 193, 2, 64, 128, 1, "f32", "star"),
+]
+
+
+@pytest.mark.parametrize("rule", ["scan", "delta"])
+@pytest.mark.parametrize("case", LONG, ids=lambda c: "b{}K{}H{}P{}N{}G{}{}{}".format(*c))
+def test_long_trees_of_many_rows(case, rule):
+    """Rows of a call that fills the GPU: the definition's, and bit for bit those of calls with one row; a
+    value that is not finite stays in its branch, head and column."""
+    b, K, H, P, N, G, dtype, kind = case
+    print(f"[tree] {case} {rule}", flush=True)
+    d = ref.make(b, K, H, P, N, G, 500 + K, dtype, rule, kind)
+    y = tree(d)
+    for i in (0, b // 2, b - 1):
+        one = {k: (v[i:i + 1].contiguous() if k in ("x", "dt", "B", "C", "beta", "parents", "slots") and v is not None else v)
+               for k, v in d.items()}
+        assert torch.equal(check_tree(one, (case, rule, i)), y[i:i + 1]), i
+    i, k = b // 2, next(n for n, p in enumerate(ref.paths(d["parents"])[b // 2]) if p is not None)
+    for name in ("x", "B", "dt", "beta"):
+        if d[name] is None:
+            continue
+        e = {n: (v.clone() if isinstance(v, torch.Tensor) else v) for n, v in d.items()}
+        e[name][(i, k, G - 1 if name == "B" else H - 1) + ((3,) if name in "xB" else ())] = float("nan")
+        hit = torch.zeros(d["x"].shape, dtype=torch.bool)
+        hit[i, below(d, i, k), slice(H - H // G if name == "B" else H - 1, H), 3 if name == "x" else slice(None)] = True
+        z = tree(e).cpu()
+        assert torch.equal(z[~hit], y.cpu()[~hit]) and not torch.isfinite(z[hit]).any(), name
+
+
 # ---- commit ----
 def commit(d, last, inplace=None):
     g = up(d)

@@ -55,6 +55,7 @@ def test_bad_calls_are_refused(name, rule):
                dict(bs=(1 << 40)), dict(S=1 << 31), dict(S=1 << 20, ss=1 << 30), dict(ss=1 << 41),
                dict(b=1 << 13, T=256 if "tree" in name else 1 << 24, xs=1 << 32)):
         assert go(name, prob(**kw), every) == UNSUPPORTED, kw
+    assert go(name, prob(H=1 << 18, P=128, G=1), every) == UNSUPPORTED  # (16 nodes of y within 2 GiB)
     if "tree" in name:
         assert go(name, prob(T=257), every) == UNSUPPORTED
     if name != "ssd_tree_commit":
