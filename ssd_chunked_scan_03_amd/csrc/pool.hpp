@@ -2,6 +2,7 @@
 // indices, one token after another or along the accepted path of a tree.
 #pragma once
 
+#include "delta.hpp"
 #include "device.hpp"
 
 namespace ssd {
@@ -38,10 +39,21 @@ struct Args {
 // kBatch tokens at a time, so that their latency is paid once for all of them; a single token's
 // go straight to registers.  Grid (b H, ceil(P N / (2048 CH))), 256 threads.
 // Bound by the state's bytes where there are many rows: one token of 128 rows, 80 heads of 64, dstate 128, 671 MB in 136 us
-// (4.9 TB/s; a large copy reaches 5.2); paths of 5 nodes of 64 such rows with the delta rule, 336 MB, 80 us, behind the
+// (4.9 TB/s; a large copy reaches 5.2); paths of 5 nodes of 64 such rows with the delta rule, 336 MB, 77 us, behind the
 // walk up the tree and the row sums of every token.  One row of 48 heads: 5 us, a chain of latencies.
 // ---------------------------------------------------------------------------
 constexpr int kBatch = 16;
+
+// The sum over R = 2 .. 32 neighbouring lanes, in each of them: inside a row of 16 in the ALU (through LDS the
+// commit of 64 rows below takes 80 us, so 77).
+__device__ __forceinline__ float lanes_sum(float v, int R) {
+    v += delta::lane_turn<0xB1>(v);            // lane ^ 1
+    if (R > 2) v += delta::lane_turn<0x4E>(v);   // lane ^ 2
+    if (R > 4) v += delta::lane_turn<0x141>(v);  // the other four of eight, mirrored
+    if (R > 8) v += delta::lane_turn<0x140>(v);  // the other eight of sixteen, mirrored
+    if (R > 16) v += __shfl_xor(v, 16, 64);
+    return v;
+}
 
 template <typename T, bool DELTA, bool PATH, bool STAGE, int CH>
 __global__ __launch_bounds__(256) void k_walk(Args a) {
@@ -115,7 +127,7 @@ __global__ __launch_bounds__(256) void k_walk(Args a) {
             if (DELTA) {
 #pragma unroll
                 for (int k = 0; k < E; ++k) s += hv[c][k] * bv[k];
-                for (int off = R >> 1; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
+                s = lanes_sum(s, R);
                 u = bt * (xp - s);
             }
 #pragma unroll
@@ -123,7 +135,7 @@ __global__ __launch_bounds__(256) void k_walk(Args a) {
             if (!PATH) {
 #pragma unroll
                 for (int k = 0; k < E; ++k) o += hv[c][k] * cv[k];
-                for (int off = R >> 1; off > 0; off >>= 1) o += __shfl_xor(o, off, 64);
+                o = lanes_sum(o, R);
                 if (active && (lane & (R - 1)) == 0) y[(row * a.H + h) * P + p + c * dp] = from_f<T>(o + Dh * xp);
             }
         }
@@ -193,7 +205,7 @@ template <typename T, bool DELTA>
 int walk_rule(const Args& a, bool path) {
     // The most state a thread that leaves every CU its eight work-groups, so that fewer work-groups read a token's
     // operands (8 / 16 / 32 elements a thread: one token of 128 rows, 80 heads of 64, dstate 128, 143 / 139 / 136 us; the
-    // delta rule's commit of 64 such rows, paths of 5 nodes, 83 / 78 / 81 us).
+    // delta rule's commit of 64 such rows, paths of 5 nodes, 83 / 78 / 81 us with the row sums through LDS).
     const int64_t pn = (int64_t)a.P * a.N, all = a.b * a.H;
     int ch = path ? 2 : 4;
     while (ch > 1 && (pn % (2048 * ch) != 0 || all * (pn / (2048 * ch)) < 2048)) ch >>= 1;
