@@ -463,8 +463,9 @@ int ssd_bc_norm_bwd(const ssd_norm* p, const void* B, const void* C, const float
  *   y  [batch, seqlen, nheads, headdim] contiguous, problem dtype
  *
  * headdim in {16, 32, 64, 128}, dstate in {16, 32, 64, 128, 256}, both dtypes, flags 0; batch * nheads
- * under 2^24, nheads * headdim at most 2^24, strides to 2^32, batch * seqlen times any of them under 2^40.  Alignment: x, B, C, y and
- * pool 16 bytes, the slot stride a multiple of 4 elements, the rest one element.  No workspace.
+ * under 2^24, nheads * headdim at most 2^24, strides to 2^32, batch * seqlen times any of them under
+ * 2^40.  Alignment: x, B, C, y and pool 16 bytes, the slot stride a multiple of 4 elements, the rest
+ * one element.  No workspace.
  * Sums, decays and states are float32 (each decay's exponent float64); y is rounded once.
  * Outputs (y, the pool where it is written) overlap no input and each other nowhere.
  * Ownership, ordering, capture and errors as for ssd_scan_fwd.
@@ -504,8 +505,9 @@ int ssd_pool_step(const ssd_pool_problem* p, const void* x, const float* dt, con
  * A node whose parent lies outside [-1, k - 1] is absent, and so is every node below it: its y is zero
  * and none of its values (which may be anything) reaches another node.  Rows of fewer nodes are padded
  * with such nodes (-2).  A NaN or infinity in a node's x, dt, B or beta makes the y of that node and
- * those below it NaN or infinite where the formulas need it, in no other branch; for the delta rule one in dt, B or beta
- * reaches every column of the heads that read it.
+ * those below it NaN or infinite where the formulas need it, in no other branch; for the delta rule
+ * one in dt, B or beta reaches every column of the heads that read it.  Where finite values of the delta
+ * rule add up past float32's range, other nodes of that row, head and column may be NaN too.
  *
  * seqlen (the nodes) at most SSD_TREE_NODES. */
 #define SSD_TREE_NODES 256
@@ -515,8 +517,8 @@ int ssd_tree_step(const ssd_pool_problem* p, const void* x, const float* dt, con
 
 /* Accept a path of such a tree: the state of slots[i] becomes, in out_slots[i] (NULL = slots), the state
  * behind node last[i] (int32 [batch]).  last = -1 accepts none (the state goes to the out slot as it is);
- * any other value that names no present node leaves the row idle.  C and D play no part (cstride is not read).  In float32, like
- * ssd_pool_step over the path's tokens. */
+ * any other value that names no present node leaves the row idle.  C and D play no part (cstride is
+ * not read).  In float32, like ssd_pool_step over the path's tokens. */
 int ssd_tree_commit(const ssd_pool_problem* p, const void* x, const float* dt, const float* A, const void* B,
                     const void* beta, const int32_t* parents, const int32_t* last, float* pool,
                     const int32_t* slots, const int32_t* out_slots, void* stream);
@@ -524,7 +526,8 @@ int ssd_tree_commit(const ssd_pool_problem* p, const void* x, const float* dt, c
 /* The pool's pages: a table (device int32 [rows]) names the slot of every row, entries outside
  * [0, slots) mean none.  A pool holds the same slots in every layer: element (layer, slot, i) lies at
  * layer * layer_stride + slot * slot_stride + i, i under slot_elems (a multiple of 4, as the strides are;
- * slots and layers do not overlap).  pool is 16-byte aligned; slots at most 16384, layers at most 65536, rows at most 65536. */
+ * slots and layers do not overlap).  pool is 16-byte aligned; slots at most 16384, layers and rows at
+ * most 65536. */
 typedef struct {
     int64_t rows, layers, slots, slot_elems, layer_stride, slot_stride;
 } ssd_pages;
