@@ -205,7 +205,7 @@ template <typename T, bool DELTA>
 int walk_rule(const Args& a, bool path) {
     // The most state a thread that leaves every CU its eight work-groups, so that fewer work-groups read a token's
     // operands (8 / 16 / 32 elements a thread: one token of 128 rows, 80 heads of 64, dstate 128, 143 / 139 / 136 us; the
-    // delta rule's commit of 64 such rows, paths of 5 nodes, 83 / 78 / 81 us with the row sums through LDS).
+    // delta rule's commit of 64 such rows, paths of 5 nodes, 82 / 79 / 80 us).
     const int64_t pn = (int64_t)a.P * a.N, all = a.b * a.H;
     int ch = path ? 2 : 4;
     while (ch > 1 && (pn % (2048 * ch) != 0 || all * (pn / (2048 * ch)) < 2048)) ch >>= 1;
