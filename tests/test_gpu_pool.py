@@ -309,6 +309,41 @@ def test_graphs_follow_their_tensors(rule):
             assert torch.equal(got, w), seed
 
 
+@pytest.mark.parametrize("rule", ["scan", "delta"])
+def test_long_trees_captured_and_as_views(rule):
+    """Trees of several panels, two heads a work-group: x, B and C out of wider rows and a layer of a slot-major
+    pool are the contiguous call's bits, and so is every replay of a captured call on other values."""
+    b, K, H, P, N, G, S = 33, 150, 8, 32, 64, 2, 36
+    d = ref.make(b, K, H, P, N, G, 61, "bf16", rule, "holes", spare=S - b)
+    g = up(d)
+    y = torch.empty_like(g["x"])
+    prob = ssd.PoolProblem(b, K, H, P, N, G, H * P, G * N, G * N, S, H * P * N, ssd.SSD_BF16, 0)
+
+    def run():
+        ssd.tree_step_into(prob, g["x"], g["dt"], g["A"], g["B"], g["C"], g["D"], g["beta"], g["parents"], g["pool"], g["slots"], y)
+
+    run()
+    inner = torch.full((S, 3, H, P, N), float("nan"), device="cuda")
+    inner[:, 1] = g["pool"]
+    got = ssd.tree_step(wide(d["x"], 24), g["dt"], g["A"], wide(d["B"], 8, 16), wide(d["C"], 40, 8), g["parents"], inner[:, 1],
+                        g["slots"], D=g["D"], beta=g["beta"])
+    assert torch.equal(got, y)
+    graph = graph_of(run)
+    for seed in (62, 63, 64):
+        n = up(ref.make(b, K, H, P, N, G, seed, "bf16", rule, ["deep", "ragged", "tree"][seed - 62], spare=S - b))
+        for k in ("x", "dt", "B", "C", "D", "beta", "parents", "pool", "slots", "A"):
+            if n[k] is not None:
+                g[k].copy_(n[k])
+        run()
+        torch.cuda.synchronize()
+        want = y.clone()
+        y.fill_(float("nan"))
+        float((torch.randn(1 << 20, device="cuda") ** 2).sum())
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), seed
+
+
 def test_calls_on_another_stream():
     """Work goes to the current stream, in order with what it follows there."""
     d = ref.make(4, 20, 4, 64, 128, 2, 45, "bf16", "delta", "tree", out=True)
