@@ -123,8 +123,9 @@ struct TreeCfg {
     static __device__ int at(int kt) { return kt < 2 ? kt * 2048 : (kt - 1) * kTableBytes; }
 };
 
-// More nodes, in panels of 64.  kp: nodes rounded up to panels.  Where they fit (STG), the rows of the panel in
-// work go through LDS: x1 holds its C, then B of one earlier panel after another; x2 its own B.
+// More nodes, in panels of 64.  kp: nodes rounded up to panels.  Where they fit (STG; not float32 at dstate 256), the rows
+// of the panel in work go through LDS: x1 holds its C, then B of one earlier panel after another; x2 its own B (with
+// one head and four waves a work-group: staged 226 us, every product's rows from memory 298).
 template <typename T, int N, bool DELTA>
 struct LongCfg {
     static constexpr int KS = N < 32 ? 1 : N / 32;
@@ -665,8 +666,7 @@ __global__ __launch_bounds__(256, (TreeCfg<T, N, DELTA, NK>::WAVES)) void k_tree
 // rows: C's (waves 0 to 3, M) or B's (4 to 7, T); a product serves both heads, and the diagonal tiles' inverses go to the
 // waves with the shorter rows of the own panel.  The scan has no T: its waves 4 to 7 take half of M's tiles.  u of
 // earlier panels stays in registers, two terms as the next product takes them; no tile goes back to memory.
-// 16 lines of 200 nodes, 32 heads of 64, 8 groups, dstate 256, the delta rule: 84 us (one head a work-group 129, rows
-// from memory for every product 298).
+// 16 lines of 200 nodes, 32 heads of 64, 8 groups, dstate 256, the delta rule: 84 us (one head a work-group 129).
 // ---------------------------------------------------------------------------
 template <typename T, int N, bool DELTA>
 __global__ __launch_bounds__(512) void k_tree_long(Args a, int heads) {
