@@ -39,13 +39,13 @@ struct Args {
 // kBatch tokens at a time, so that their latency is paid once for all of them; a single token's
 // go straight to registers.  Grid (b H, ceil(P N / (2048 CH))), 256 threads.
 // Bound by the state's bytes where there are many rows: one token of 128 rows, 80 heads of 64, dstate 128, 671 MB in 136 us
-// (4.9 TB/s; a large copy reaches 5.2); paths of 5 nodes of 64 such rows with the delta rule, 336 MB, 77 us, behind the
+// (4.9 TB/s; a large copy reaches 5.2); paths of 5 nodes of 64 such rows with the delta rule, 336 MB, 78 us, behind the
 // walk up the tree and the row sums of every token.  One row of 48 heads: 5 us, a chain of latencies.
 // ---------------------------------------------------------------------------
 constexpr int kBatch = 16;
 
 // The sum over R = 2 .. 32 neighbouring lanes, in each of them: inside a row of 16 in the ALU (through LDS the
-// commit of 64 rows below takes 80 us, so 77).
+// commit of 64 rows below takes 81 us, so 78).
 __device__ __forceinline__ float lanes_sum(float v, int R) {
     v += delta::lane_turn<0xB1>(v);            // lane ^ 1
     if (R > 2) v += delta::lane_turn<0x4E>(v);   // lane ^ 2
