@@ -23,6 +23,8 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
+constexpr int64_t kMaxThreads = 0xffffffffLL;  // of one launch, along a dimension of its grid
+
 template <typename T> struct V8;
 template <> struct V8<bf16> { typedef bf16x8 type; };
 template <> struct V8<float> { typedef f32x8 type; };

@@ -1137,15 +1137,35 @@ inline int tree_heads(const Args& a, int slabs, int lds0, int lds_head) {
     return best;
 }
 
+// `groups` work-groups a row.  Past 2^32 - 1 threads a launch covers only their remainder and reports nothing, so rows
+// go in as many launches as that takes (a row has under 2^29 threads: nheads * headdim is at most 2^24).
+template <typename T, typename K>
+int launch_rows(K* kernel, const Args& a, int heads, int64_t groups, int threads, size_t lds) {
+    if (!delta::lds_limit(kernel, lds)) return 7;
+    const int64_t most = kMaxThreads / (groups * threads);
+    for (int64_t row = 0; row < a.b; row += most) {
+        const int64_t tok = row * a.T;
+        Args p = a;
+        p.b = a.b - row < most ? a.b - row : most;
+        p.x = static_cast<const T*>(a.x) + tok * a.xs;
+        p.dt = a.dt + tok * a.H;
+        p.B = static_cast<const T*>(a.B) + tok * a.bs;
+        p.C = static_cast<const T*>(a.C) + tok * a.cs;
+        if (a.beta) p.beta = static_cast<const T*>(a.beta) + tok * a.H;
+        p.parents = a.parents + tok;
+        p.slots = a.slots + row;
+        p.y = static_cast<T*>(a.y) + tok * a.H * a.P;
+        kernel<<<(unsigned)(p.b * groups), threads, lds, a.stream>>>(p, heads);
+    }
+    return hipGetLastError() == hipSuccess ? 0 : 7;
+}
+
 template <typename T, int N, bool DELTA, int NK>
 int launch_tree(const Args& a) {
     typedef TreeCfg<T, N, DELTA, NK> CF;
     const int cols = a.P < 64 ? a.P / 16 : 4, waves = cols > NK ? cols : NK;
     const int slabs = a.P / (16 * cols), hg = a.H / a.G, hb = tree_heads(a, slabs, CF::C, CF::HEAD);
-    const size_t lds = CF::total(hb);
-    if (!delta::lds_limit(k_tree<T, N, DELTA, NK>, lds)) return 7;
-    k_tree<T, N, DELTA, NK><<<(unsigned)(a.b * a.G * ((hg + hb - 1) / hb) * slabs), 64 * waves, lds, a.stream>>>(a, hb);
-    return hipGetLastError() == hipSuccess ? 0 : 7;
+    return launch_rows<T>(k_tree<T, N, DELTA, NK>, a, hb, (int64_t)a.G * ((hg + hb - 1) / hb) * slabs, 64 * waves, CF::total(hb));
 }
 template <typename T, int N, bool DELTA>
 int run_tree_n(const Args& a) {
@@ -1158,9 +1178,7 @@ int run_tree_n(const Args& a) {
     // above: one 129 us, two 84; 16 rows of 65 nodes at dstate 128: 44 and 28).
     const int hg = a.H / a.G, heads = a.P <= 64 && hg > 1 && a.b * a.H > 256 ? 2 : 1;
     const size_t lds = (size_t)LongLds((int)a.T, heads, a.P / 16, DELTA, CF::STG ? CF::ROWS : 0).total;
-    if (!delta::lds_limit(k_tree_long<T, N, DELTA>, lds)) return 7;
-    k_tree_long<T, N, DELTA><<<(unsigned)(a.b * a.G * ((hg + heads - 1) / heads)), 512, lds, a.stream>>>(a, heads);
-    return hipGetLastError() == hipSuccess ? 0 : 7;
+    return launch_rows<T>(k_tree_long<T, N, DELTA>, a, heads, (int64_t)a.G * ((hg + heads - 1) / heads), 512, lds);
 }
 template <typename T, bool DELTA>
 int run_tree_rule(const Args& a) {

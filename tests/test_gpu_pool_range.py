@@ -1,0 +1,38 @@
+"""The operators on a pool of states at the far ends of their ranges."""
+import pytest
+import torch
+
+import ssd_chunked_scan_03_amd as ssd
+
+pytestmark = pytest.mark.gpu
+
+
+# b, K, H, P, N, G, rule: 4 295 032 832 threads each in one launch
+@pytest.mark.parametrize("case", [(65537, 1, 128, 128, 16, 128, "scan"), (65537, 1, 128, 128, 16, 128, "delta"),
+                                  (65537, 65, 128, 16, 16, 128, "scan")], ids=lambda c: "b{}K{}H{}P{}N{}G{}{}".format(*c))
+def test_trees_of_more_threads_than_a_launch(case):
+    """Every row is written, and rows at the ends and around the launches' border are a small call's bits."""
+    b, K, H, P, N, G, rule = case
+    print(f"[far] {case}", flush=True)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(91)
+    x, B, C = (torch.empty(b, K, n, m, **bf).normal_(generator=g) for n, m in ((H, P), (G, N), (G, N)))
+    B, C = B.mul_(0.25), C.mul_(0.25)
+    dt = 0.1 * torch.rand(b, K, H, generator=g, device="cuda")
+    A = -1 - 15 * torch.rand(H, generator=g, device="cuda")
+    beta = torch.rand(b, K, H, generator=g, device="cuda").bfloat16() if rule == "delta" else None
+    D = torch.randn(H, generator=g, device="cuda") if rule == "scan" else None
+    pool = torch.randn(5, H, P, N, generator=g, device="cuda")
+    slots = torch.randint(0, 5, (b,), generator=g, device="cuda", dtype=torch.int32)
+    parents = (torch.rand(b, K, generator=g, device="cuda") * torch.arange(K, device="cuda")).int() - 1
+    y = torch.full((b, K, H, P), float("nan"), **bf)
+    prob = ssd.PoolProblem(b, K, H, P, N, G, H * P, G * N, G * N, 5, H * P * N, ssd.SSD_BF16, 0)
+    ssd.tree_step_into(prob, x, dt, A, B, C, D, beta, parents, pool, slots, y)
+    torch.cuda.synchronize()
+    for lo in range(0, b, 4096):
+        assert torch.isfinite(y[lo:lo + 4096]).all(), lo
+    most = 0xffffffff // (H * max(1, P // 64 if K <= 64 else 1) * (256 if K <= 64 else 512))
+    for lo in (0, most - 2, most, b - 3):
+        s = slice(lo, min(b, lo + 3))
+        one = ssd.tree_step(x[s], dt[s], A, B[s], C[s], parents[s], pool, slots[s], D=D, beta=None if beta is None else beta[s])
+        assert torch.equal(one, y[s]), lo
