@@ -448,9 +448,11 @@ __global__ __launch_bounds__(kThreads) void k_bwd_x(const T* __restrict__ x, con
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (k < rpw)
+                if (k < rpw) {
 #pragma unroll
                     for (int pt = 0; pt < PT; ++pt) acc[k][pt] = mma(acc[k][pt], hf[pt], cf[k]);
+                    if (sizeof(T) == 2 && n0 + 32 >= N) settle(acc[k]);
+                }
         }
     };
 

@@ -182,4 +182,18 @@ __device__ __forceinline__ f32x4 mma(f32x4 c, f32x8 a, f32x8 b) {
     return c;
 }
 
+// Accumulators that a branch ends on.  The hardware does not hold a read back until a matrix instruction has written
+// its result: 8 wait states have to lie between (bfloat16, 4 passes; 10 for float32).  The compiler states them within a
+// block, but behind a branch it may leave some out (seen: a read one instruction later, with wrong values in a few
+// tiles).  So the wait is stated here: right behind the products, in their block (the array form: of all its
+// accumulators' products).
+__device__ __forceinline__ void settle(f32x4& v) { asm volatile("s_nop 7\n\ts_nop 3" : "+v"(v)); }
+template <int M>
+__device__ __forceinline__ void settle(f32x4 (&v)[M]) {
+    __builtin_amdgcn_sched_barrier(0);
+    settle(v[0]);
+#pragma unroll
+    for (int i = 1; i < M; ++i) asm volatile("" : "+v"(v[i]));  // (volatile: behind the wait)
+}
+
 }  // namespace ssd

@@ -1274,6 +1274,7 @@ __global__ __launch_bounds__(kThreads, (out_min_blocks<T, P>())) void k_out(cons
                                 }
                                 gt[s2] = mma(gt[s2], a, b);
                             }
+                            settle(gt[s2]);
                         } else {
                             // direct sums for this lane's 4 entries (i, j = sI + 4q + r)
 #pragma unroll
@@ -1569,6 +1570,7 @@ __global__ __launch_bounds__(kThreads) void k_gtab(const T* __restrict__ Bm, con
                 }
                 gt = mma(gt, a, b);
             }
+            settle(gt);
         } else {
             // direct sums for this lane's 4 entries (i, j = J 64 + 16 J16 + 4q + r)
 #pragma unroll

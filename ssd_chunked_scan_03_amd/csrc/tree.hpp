@@ -174,11 +174,6 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// Accumulators that a branch ends on: the compiler may let the code behind the branch read them before the
-// matrix instruction has written them (seen: a read one instruction later, where eight have to lie between),
-// so the wait is stated here.
-__device__ __forceinline__ void settle(f32x4& v) { asm volatile("s_nop 7\n\ts_nop 3" : "+v"(v)); }
-
 // All of v has arrived here: its reads go out together ahead of this, and not one by one between the products
 // (which cost an LDS latency each).
 template <typename F8, int KS>
