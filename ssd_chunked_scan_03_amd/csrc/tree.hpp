@@ -155,18 +155,15 @@ struct LongLds {
 };
 
 __device__ __forceinline__ bool odd_bits(float v) { return (__builtin_bit_cast(unsigned, v) & 0x7f800000u) == 0x7f800000u; }
-__device__ __forceinline__ bool any_odd(bf16x8 v) {
-    const u32x4v w = __builtin_bit_cast(u32x4v, v);
-    bool o = false;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
-    return o;
+// Whether an element of v is not finite, its exponent's bits all ones: one more carries into the sign's place.
+__device__ __forceinline__ unsigned odd_carry(bf16x8 v) {
+    const u32x4v w = (__builtin_bit_cast(u32x4v, v) & 0x7f807f80u) + 0x00800080u;
+    return (w[0] | w[1] | w[2] | w[3]) & 0x80008000u;
 }
-__device__ __forceinline__ bool any_odd(f32x8 v) {
-    bool o = false;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o |= odd_bits(v[e]);
-    return o;
+__device__ __forceinline__ unsigned odd_carry(f32x8 v) {
+    typedef unsigned u32x8v __attribute__((ext_vector_type(8)));
+    const u32x8v w = (__builtin_bit_cast(u32x8v, v) & 0x7f800000u) + 0x00800000u;
+    return (w[0] | w[1] | w[2] | w[3] | w[4] | w[5] | w[6] | w[7]) & 0x80000000u;
 }
 // orders LDS traffic of one wave's lanes (LDS serves a wave in order; this keeps the compiler to it)
 __device__ __forceinline__ void wave_sync() {
@@ -448,11 +445,21 @@ __global__ __launch_bounds__(256, (TreeCfg<T, N, DELTA, NK>::WAVES)) void k_tree
                     gcr[jt] = c;
                     gbr[jt] = b;
                     if (jt == w) {
-                        // |B_k|^2 on the diagonal tells whether the row is finite
+                        // |B_k|^2 on the diagonal is finite where the row is, unless the square leaves float32: then its
+                        // elements tell (looked at always they spill at three waves a SIMD: tree of 40 nodes above 34.0 us, so 30.7)
                         const float d = l16 & 2 ? (l16 & 1 ? b[3] : b[2]) : (l16 & 1 ? b[1] : b[0]);
                         u64 who = __ballot(q == l16 >> 2 && odd_bits(d));
                         who |= who >> 32;
-                        if (lane == 0) badb[w] = ((who | who >> 16) & 0xffff) << (16 * w);
+                        who = (who | who >> 16) & 0xffff;
+                        if (who) {
+                            unsigned odd = 0;
+#pragma unroll 1
+                            for (int ks = 0; ks < KS; ++ks) odd |= odd_carry(CF::LCB ? kept(brow, w, ks) : frag(Bm, a.bs, 16 * w + l16, ks));
+                            who = __ballot(odd != 0);
+                            who |= who >> 32;
+                            who = (who | who >> 16) & 0xffff;
+                        }
+                        if (lane == 0) badb[w] = who << (16 * w);
                     }
                 } else {
                     st4(gc + (w * (w + 1) / 2 + jt) * 256 + lane * 4, c);
@@ -842,10 +849,10 @@ __global__ __launch_bounds__(512) void k_tree_long(Args a, int heads) {
         if (DELTA && kind) {
             // a node below one whose row of B is not finite cannot be computed
             if (!CF::STG) ask_own(q0);
-            bool odd = false;
+            unsigned odd = 0;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) odd |= any_odd(rs[ks]);
-            u64 who = __ballot(odd);
+            for (int ks = 0; ks < KS; ++ks) odd |= odd_carry(rs[ks]);
+            u64 who = __ballot(odd != 0);
             who |= who >> 32;
             if (lane == 0) badb[4 * s + tw] = (unsigned)(who | who >> 16) & 0xffffu;
         }

@@ -2,7 +2,9 @@
 import pytest
 import torch
 
+import pool_ref as ref
 import ssd_chunked_scan_03_amd as ssd
+from test_gpu_tree import check_tree, tree
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +38,21 @@ def test_trees_of_more_threads_than_a_launch(case):
         s = slice(lo, min(b, lo + 3))
         one = ssd.tree_step(x[s], dt[s], A, B[s], C[s], parents[s], pool, slots[s], D=D, beta=None if beta is None else beta[s])
         assert torch.equal(one, y[s]), lo
+
+
+# K: every number of node tiles, and panels
+@pytest.mark.parametrize("K", [1, 16, 17, 48, 64, 65, 200])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_row_of_b_whose_square_leaves_float32(K, dtype):
+    """The delta rule at a leaf with a finite B of norm 8e19: |B|^2 is in none of its formulas, so its y is the
+    definition's, and every other node keeps its bits."""
+    d = ref.make(2, K, 4, 32, 64, 2, 95, dtype, "delta", "tree")
+    clean = tree(d)
+    sign = 1 - 2 * (torch.arange(64) % 3 == 1).float()
+    d["B"][1, K - 1, 1] = (1e19 * sign).to(d["B"].dtype)
+    d["C"][1, K - 1, 1] *= 1e-19
+    assert (d["B"][1, K - 1, 1].double() ** 2).sum() > torch.finfo(torch.float32).max
+    y = check_tree(d, (K, dtype))
+    hit = torch.zeros(y.shape, dtype=torch.bool)
+    hit[1, K - 1, 2:] = True
+    assert torch.equal(y.cpu()[~hit], clean.cpu()[~hit])
