@@ -4,7 +4,7 @@ import torch
 
 import pool_ref as ref
 import ssd_chunked_scan_03_amd as ssd
-from test_gpu_tree import check_tree, tree
+from test_gpu_tree import check_state, check_tree, commit, tree, up
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +56,46 @@ def test_a_row_of_b_whose_square_leaves_float32(K, dtype):
     hit = torch.zeros(y.shape, dtype=torch.bool)
     hit[1, K - 1, 2:] = True
     assert torch.equal(y.cpu()[~hit], clean.cpu()[~hit])
+
+
+# b, K, H, P, N, G, dtype, kind
+SAME = [(32, 40, 32, 128, 128, 16, "bf16", "tree"), (16, 200, 32, 64, 256, 8, "bf16", "line"), (64, 64, 16, 64, 128, 1, "bf16", "tree"),
+        (33, 129, 8, 32, 64, 2, "f32", "deep"), (20, 27, 6, 32, 64, 3, "f32", "ragged")]
+
+
+@pytest.mark.parametrize("rule", ["scan", "delta"])
+@pytest.mark.parametrize("case", SAME, ids=lambda c: "b{}K{}H{}P{}N{}G{}{}{}".format(*c))
+def test_the_same_tree_is_the_same_bits(case, rule):
+    """Calls on the same inputs, back to back and beside other work on another stream."""
+    b, K, H, P, N, G, dtype, kind = case
+    d = up(ref.make(b, K, H, P, N, G, 93, dtype, rule, kind))
+    call = lambda: ssd.tree_step(d["x"], d["dt"], d["A"], d["B"], d["C"], d["parents"], d["pool"], d["slots"], D=d["D"], beta=d["beta"])  # noqa: E731
+    y = call()
+    assert all(torch.equal(call(), y) for _ in range(20))
+    side, big = torch.cuda.Stream(), torch.randn(4096, 4096, device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(10):
+            big = big @ big * 1e-3
+    again = [call() for _ in range(20)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(v, y) for v in again)
+
+
+@pytest.mark.parametrize("rule", ["scan", "delta"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [20, 80])
+def test_an_infinite_step_forgets(K, dtype, rule):
+    """dt = inf decays by exp(-inf) = 0, a value like any other: at and below such nodes y and the committed
+    states are the definition's, and elsewhere the bits of the call without them."""
+    d = ref.make(2, K, 4, 32, 64, 2, 97, dtype, rule, "deep")
+    clean = tree(d)
+    d["dt"][1, K // 3, 2] = d["dt"][1, K - 2, 0] = float("inf")
+    y = check_tree(d, (K, dtype, rule))
+    hit = torch.zeros(y.shape, dtype=torch.bool)
+    for k, h in ((K // 3, 2), (K - 2, 0)):
+        hit[1, [n for n, path in enumerate(ref.paths(d["parents"])[1]) if k in path], h] = True
+    assert hit.any() and torch.equal(y.cpu()[~hit], clean.cpu()[~hit]) and not torch.equal(y.cpu(), clean.cpu())
+    last = [K - 1, K // 3]
+    deep = max(len(path) for row in ref.paths(d["parents"]) for path in row)
+    check_state(commit(d, last), ref.commit(d, last), d["pool"], deep, (K, dtype, rule))
