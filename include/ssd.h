@@ -77,7 +77,11 @@ typedef enum {
  * dstate in {16, 32, 64, 128, 256}; any seqlen >= 0 (a ragged last chunk is allowed);
  * batch >= 0; nheads >= 1; ngroups >= 1 dividing nheads; launch-grid limits: batch and
  * batch * ngroups at most 65535, ceil(nheads / 16) + 28 * ngroups at most 65535, nheads
- * at most 2^20, batch * nheads * nchunks under 2^31 (else SSD_ERR_UNSUPPORTED). */
+ * at most 2^20, batch * nheads * nchunks under 2^31, and every launch under 2^32 threads:
+ * batch * nchunks and batch * nheads under 2^24; outside the fused schedule and the packed
+ * form also batch * nheads * nchunks, and batch * nheads * headdim * dstate / 1024 (a backward
+ * in bfloat16 with headdim 64, dstate 64 or 128 and batch * nheads >= 512 not that one); for a
+ * scalar backward batch * nchunks * ngroups * chunk / 64 under 2^22 (else SSD_ERR_UNSUPPORTED). */
 typedef struct {
     int64_t batch, seqlen, nheads, headdim, dstate, ngroups, chunk;
     int32_t dtype;  /* ssd_dtype */
@@ -252,8 +256,8 @@ int ssd_scan_fwd_varlen(const ssd_problem* p, const int32_t* cu_seqlens, const v
  *                          in place: the state before the first token on entry, the
  *                          state after the last on return.
  * `chunk` is ignored; `flags` must be 0.  No workspace.  headdim in {16,32,64,128},
- * dstate in {16,32,64,128,256}.  batch = 0 or seqlen = 0 leaves h untouched.
- * Errors as for ssd_scan_fwd: NULL pointers, h not 16-byte aligned, B/C not aligned to
+ * dstate in {16,32,64,128,256}; batch * nheads under 2^24.  batch = 0 or seqlen = 0 leaves h
+ * untouched.  Errors as for ssd_scan_fwd: NULL pointers, h not 16-byte aligned, B/C not aligned to
  * 4 elements, y or h overlapping an input or each other, unsupported sizes -- all
  * reported before any HIP call. */
 int ssd_step(const ssd_problem* p, const void* x, const float* dt, const float* A,

@@ -225,7 +225,7 @@ int check_varlen(const ssd_problem* p) {
     const int64_t lim = (int64_t)1 << 31, kcap = (T + Q - 1) / Q + p->batch;
     if (T * H * 64 * 2 >= lim || T * G * N * 2 >= lim || kcap * H * Q >= lim) return SSD_ERR_UNSUPPORTED;
     if (kcap * G * Q * Q * 2 >= lim || kcap * G * N * Q * 2 >= lim) return SSD_ERR_UNSUPPORTED;
-    if (p->batch * H >= lim) return SSD_ERR_UNSUPPORTED;
+    if (!grid_ok(p->batch * H, 256)) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
 
@@ -308,7 +308,7 @@ int step(const ssd_problem* p, int diag, const void* x, const float* dt, const f
     if (p->dtype != SSD_F32 && p->dtype != SSD_BF16) return SSD_ERR_UNSUPPORTED;
     if (!pn_supported(p->headdim, p->dstate) || p->flags != 0) return SSD_ERR_UNSUPPORTED;
     const int64_t b = p->batch, T = p->seqlen, H = p->nheads, P = p->headdim, N = p->dstate, G = p->ngroups;
-    if (b * H > 0x7fffffffLL || b * T * H * P > ((int64_t)1 << 40)) return SSD_ERR_UNSUPPORTED;
+    if (!grid_ok(b * H, 256) || b * T * H * P > ((int64_t)1 << 40)) return SSD_ERR_UNSUPPORTED;
     if (b == 0 || T == 0) return SSD_OK;  // nothing to do: h is left as it is
     if (!x || !dt || !A || !B || !C || !h || !y) return SSD_ERR_NULL;
     const size_t es = esize(p->dtype);
@@ -410,7 +410,7 @@ int check_bwd(const ssd_problem* p, int diag) {
         // reductions (4 elements per thread)
         const int64_t walks = p->batch * p->nheads * nc * ssd::diag_bwd_slices(p->headdim, p->dstate);
         const int64_t elems = p->batch * p->seqlen * p->nheads * (p->headdim > p->dstate ? p->headdim : p->dstate);
-        if ((walks + 3) / 4 > 0x7fffffffLL || elems / 4 / 256 + 1 > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;
+        if (!grid_ok((walks + 3) / 4, 256) || !grid_ok(elems / 4 / 256 + 1, 256)) return SSD_ERR_UNSUPPORTED;
         return SSD_OK;
     }
     // k_bwd_bc's grid: (batch, chunk, group, 64-token slab, n range)

@@ -6,9 +6,13 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "device.hpp"
 #include "ssd.h"
 
 namespace {
+
+using ssd::grid_ok;
+using ssd::kMaxThreads;
 
 // hT = h0 (or 0) for an empty sequence: a fill kernel, not a memset, so that the
 // call stays safe under stream capture.

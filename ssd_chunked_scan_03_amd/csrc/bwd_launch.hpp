@@ -114,6 +114,17 @@ int run_bwd(const BwdArgs& a) {
     rows.H = H;
     rows.kcap = (int)(a.b * a.nc);
     const unsigned kc = (unsigned)rows.kcap;
+    const int per_head = (int)((a.P * a.N / 4 + kThreads - 1) / kThreads);
+    // the double-buffered gradients of B and C: buffer offsets of a batch row within 32 bits
+    const int64_t lim = (int64_t)1 << 31;
+    const bool bcs = std::is_same<T, bf16>::value && P == 64 && (N == 64 || N == 128) && a.T * H * P * 2 < lim &&
+                     H * a.nc * P * N * 2 < lim && H * a.nc * Q * 4 < lim;
+    // every launch's work-groups, before the first
+    const int64_t bcg = a.b * nc * G * (Q / 64);
+    if (!grid_ok(rows.kcap, kThreads) || !grid_ok(a.b * H * nc, kThreads) ||
+        !grid_ok(a.b * H * (walk_applies<T, P, N>(a) ? 1 : per_head), kThreads) ||
+        !(bcs ? grid_ok(bcg, kBcsThreads) : grid_ok(bcg * (N / NB), kBcThreads)))
+        return 3;
 
     // the forward's tables (cdt, C B^T in both orientations, B^T and C^T per chunk; with
     // a.bcp / a.ccp also B and C per chunk by token) in one launch, then the entering states
@@ -128,7 +139,6 @@ int run_bwd(const BwdArgs& a) {
         default: return 3;
     }
     const dim3 g3((unsigned)(a.b * H * nc));
-    const int per_head = (int)((a.P * a.N / 4 + kThreads - 1) / kThreads);
     int nvalid = (int)(a.P * a.N / 4 / 64);  // partials of <R_c, H_{c+1}> per chunk
     bool walked = false;
     if constexpr (std::is_same<T, bf16>::value && P == 64 && (N == 64 || N == 128)) {
@@ -191,10 +201,8 @@ int run_bwd(const BwdArgs& a) {
     }
     bool bc_done = false;
     if constexpr (std::is_same<T, bf16>::value && P == 64 && (N == 64 || N == 128)) {
-        // the double-buffered variant: buffer offsets of a batch row within 32 bits
-        const int64_t lim = (int64_t)1 << 31;
-        if (a.T * H * P * 2 < lim && H * a.nc * P * N * 2 < lim && H * a.nc * Q * 4 < lim) {
-            const dim3 g7((unsigned)(a.b * nc * G * (Q / 64)));
+        if (bcs) {
+            const dim3 g7((unsigned)bcg);
             const bf16* xb = x;
             switch (Q) {
                 case 64: k_bwd_bcs<64, N, N><<<g7, kBcsThreads, 0, s>>>(xb, dy, bt, ct, hin, rin, a.A, a.cdt,
@@ -214,7 +222,7 @@ int run_bwd(const BwdArgs& a) {
     if (!bc_done) {
         (void)hipFuncSetAttribute((const void*)k_bwd_bc<T, P, N, NB>, hipFuncAttributeMaxDynamicSharedMemorySize,
                                   (int)sbc);
-        const dim3 g7((unsigned)(a.b * nc * G * (Q / 64) * (N / NB)));
+        const dim3 g7((unsigned)(bcg * (N / NB)));
         k_bwd_bc<T, P, N, NB><<<g7, kBcThreads, sbc, s>>>(x, dy, bt, ct, hin, rin, a.A, a.cdt, static_cast<T*>(a.dB),
                                                         static_cast<T*>(a.dC), a.T, H, G, Q, nc);
     }
@@ -248,6 +256,10 @@ int run_bwd_diag(const BwdArgs& a) {
     rows.H = H;
     rows.kcap = (int)(a.b * a.nc);
     const dim3 g1((unsigned)rows.kcap, 1, (H + 15) / 16);
+    const int PN = (int)(a.P * a.N);
+    const int per_head = (PN / 4 + kThreads - 1) / kThreads;
+    // every launch's work-groups, before the first (the walks' and the reductions' are the caller's to check)
+    if (!grid_ok(rows.kcap, kThreads) || !grid_ok(a.b * H * (nc > per_head ? nc : per_head), kThreads)) return 3;
     switch (Q) {
         case 64: k_cumsum<64><<<g1, kThreads, 0, s>>>(a.dt, a.cdt, rows); break;
         case 128: k_cumsum<128><<<g1, kThreads, 0, s>>>(a.dt, a.cdt, rows); break;
@@ -255,8 +267,6 @@ int run_bwd_diag(const BwdArgs& a) {
         default: return 3;
     }
     const dim3 g3((unsigned)(a.b * H * nc));
-    const int PN = (int)(a.P * a.N);
-    const int per_head = (PN / 4 + kThreads - 1) / kThreads;
     const dim3 g4((unsigned)(a.b * H * per_head));
     const int64_t BHPN = a.b * H * a.P * a.N;
     // entering states H_c and the final state

@@ -13,8 +13,6 @@ namespace {
 using ssd::delta::kTab;
 using ssd::delta::kVec;
 
-bool grid_ok(int64_t groups, int64_t threads) { return groups <= 0x7fffffffLL && groups * threads <= ssd::kMaxThreads; }
-
 constexpr int64_t kReach = 0x7fff0000;  // bytes that a kernel addresses from one base
 
 int check_delta(const ssd_problem* p, bool packed) {
@@ -281,7 +279,7 @@ int check_norm(const ssd_norm* p) {
     if (!(p->eps > 0.f) || isinf(p->eps)) return SSD_ERR_UNSUPPORTED;
     if (p->bheads > 1 << 16 || p->cheads > 1 << 16 || p->batch > (int64_t)1 << 31 || p->seqlen > (int64_t)1 << 31)
         return SSD_ERR_UNSUPPORTED;
-    if (p->batch * p->seqlen > ssd::kMaxThreads / 256) return SSD_ERR_UNSUPPORTED;
+    if (p->batch * p->seqlen > kMaxThreads / 256) return SSD_ERR_UNSUPPORTED;
     if (p->batch > 0 && p->seqlen > 0) {
         if (p->bstride < p->bheads * p->dstate || p->cstride < p->cheads * p->dstate) return SSD_ERR_SHAPE;
         if (p->bstride > (int64_t)1 << 32 || p->cstride > (int64_t)1 << 32) return SSD_ERR_UNSUPPORTED;

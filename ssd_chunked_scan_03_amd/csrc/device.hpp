@@ -23,7 +23,9 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
-constexpr int64_t kMaxThreads = 0xffffffffLL;  // of one launch, along a dimension of its grid
+// Threads of one launch along a dimension of its grid: past them it covers their remainder and reports nothing.
+constexpr int64_t kMaxThreads = 0xffffffffLL;
+inline bool grid_ok(int64_t groups, int64_t threads) { return groups <= 0x7fffffffLL && groups * threads <= kMaxThreads; }
 
 template <typename T> struct V8;
 template <> struct V8<bf16> { typedef bf16x8 type; };

@@ -162,6 +162,11 @@ int run(const RunArgs& a) {
     // the whole preparation of a forward (cumsum, C B^T, and B^T for the fused schedule)
     // in one launch; a stage mask that asks for part of it runs the separate kernels
     const int prep_bits = fused ? (1 | 2 | 32) : (1 | 2);
+    const int per_head = (P * N / 4 + kThreads - 1) / kThreads;
+    // every launch's work-groups, before the first
+    const int64_t bt_groups = (st & prep_bits) == prep_bits || !(st & 32) ? 1 : Q / 64;
+    if (!grid_ok(rows.kcap * bt_groups, kThreads) || !grid_ok(a.b * H * (fused ? 1 : nc > per_head ? nc : per_head), kThreads))
+        return 3;
     if (!a.diag && (st & prep_bits) == prep_bits) {
         const int nb = Q / 64;
         const dim3 gp(kc, (unsigned)((H + 15) / 16 + prep_cb_tasks<T, N>(nb) * G + (fused ? nb * G : 0)));
@@ -200,7 +205,6 @@ int run(const RunArgs& a) {
     else
         k_state<T, P, N, false, false, T><<<g3, kThreads, 0, s>>>(x, Bm, a.A, a.cdt, Sc, a.T, H, G, Q, nc);
 
-    const int per_head = (P * N / 4 + kThreads - 1) / kThreads;
     const int L = (int)scan_segment_len(a.b, H, P, N, nc);
     const int nseg = (nc + L - 1) / L;
     const int64_t BHPN = a.b * H * P * N;

@@ -1139,8 +1139,8 @@ inline int tree_heads(const Args& a, int slabs, int lds0, int lds_head) {
     return best;
 }
 
-// `groups` work-groups a row.  Past 2^32 - 1 threads a launch covers only their remainder and reports nothing, so rows
-// go in as many launches as that takes (a row has under 2^29 threads: nheads * headdim is at most 2^24).
+// `groups` work-groups a row.  Rows go in as many launches as a launch's threads take (a row has at most 2^29: nheads *
+// headdim is at most 2^24).
 template <typename T, typename K>
 int launch_rows(K* kernel, const Args& a, int heads, int64_t groups, int threads, size_t lds) {
     if (!delta::lds_limit(kernel, lds)) return 7;
