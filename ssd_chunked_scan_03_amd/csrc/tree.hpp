@@ -1176,8 +1176,9 @@ int run_tree_n(const Args& a) {
     if (a.T <= 48) return launch_tree<T, N, DELTA, 3>(a);
     if (a.T <= kPanel) return launch_tree<T, N, DELTA, 4>(a);
     typedef LongCfg<T, N, DELTA> CF;
-    // Two heads a work-group where one each would leave CUs a second one and the waves suffice (16 lines of 200 nodes
-    // above: one 129 us, two 84; 16 rows of 65 nodes at dstate 128: 44 and 28).
+    // Two heads a work-group where one each would leave CUs a second one and the waves suffice (one / two: 16 lines of
+    // 200 nodes above 127 / 85 us, the scan 99 / 61, in float32 628 / 379 and 377 / 213; 16 rows of 65 nodes at dstate 128
+    // 44 / 28, the scan 35 / 22; 9 rows of 200 at dstate 256 120 / 79, the scan 93 / 57).
     const int hg = a.H / a.G, heads = a.P <= 64 && hg > 1 && a.b * a.H > 256 ? 2 : 1;
     const size_t lds = (size_t)LongLds((int)a.T, heads, a.P / 16, DELTA, CF::STG ? CF::ROWS : 0).total;
     return launch_rows<T>(k_tree_long<T, N, DELTA>, a, heads, (int64_t)a.G * ((hg + heads - 1) / heads), 512, lds);
