@@ -10,23 +10,22 @@ import launch_record as lr
 import ssd_chunked_scan_03_amd as ssd
 
 UNSUPPORTED = 3
-lib = ssd._load()
-# entry point: its operands, its workspace
+# entry point: its operands, its workspace's query and what that takes beside the problem
 SCAN = {
-    "ssd_scan_fwd": (9, lambda p: lib.ssd_workspace_bytes(p, 0)), "ssd_diag_scan_fwd": (9, lambda p: lib.ssd_workspace_bytes(p, 1)),
-    "ssd_scan_fwd_varlen": (10, lib.ssd_varlen_workspace_bytes), "ssd_step": (8, None), "ssd_diag_step": (8, None),
-    "ssd_scan_bwd": (16, lib.ssd_bwd_workspace_bytes), "ssd_diag_scan_bwd": (16, lib.ssd_diag_bwd_workspace_bytes),
-    "ssd_delta_fwd": (9, lib.ssd_delta_workspace_bytes), "ssd_delta_fwd_varlen": (10, lib.ssd_delta_varlen_workspace_bytes),
-    "ssd_delta_step": (8, None), "ssd_delta_bwd": (16, lib.ssd_delta_bwd_workspace_bytes),
+    "ssd_scan_fwd": (9, "ssd_workspace_bytes", 0), "ssd_diag_scan_fwd": (9, "ssd_workspace_bytes", 1),
+    "ssd_scan_fwd_varlen": (10, "ssd_varlen_workspace_bytes"), "ssd_step": (8, None), "ssd_diag_step": (8, None),
+    "ssd_scan_bwd": (16, "ssd_bwd_workspace_bytes"), "ssd_diag_scan_bwd": (16, "ssd_diag_bwd_workspace_bytes"),
+    "ssd_delta_fwd": (9, "ssd_delta_workspace_bytes"), "ssd_delta_fwd_varlen": (10, "ssd_delta_varlen_workspace_bytes"),
+    "ssd_delta_step": (8, None), "ssd_delta_bwd": (16, "ssd_delta_bwd_workspace_bytes"),
 }
 
 
 def scan_call(name, b, T, H, P, N, G, Q, dtype):
     """None where an operand would be wider than the operands' distance."""
-    n, workspace = SCAN[name]
+    n, workspace, *more = SCAN[name]
     p = ssd.make_problem(b, T, H, P, N, G, Q, dtype)
     es = 2 if dtype == ssd.SSD_BF16 else 4
-    ws = [] if workspace is None else [lr.FAKE + 30 * lr.FAR, int(workspace(ctypes.byref(p)))]
+    ws = [] if workspace is None else [lr.FAKE + 30 * lr.FAR, int(getattr(ssd._load(), workspace)(ctypes.byref(p), *more))]
     if max([b * T * H * P * es, b * T * G * N * es, b * H * P * N * 4] + ws[1:]) >= lr.FAR:
         return None
     return name, p, [lr.FAKE + i * lr.FAR for i in range(n)] + ws + [0]
@@ -93,7 +92,7 @@ def test_norm_and_pool(tmp_path):
             if b * T * H * N * es >= lr.FAR:
                 continue
             calls.append(("ssd_bc_norm", p, at[:8] + [0]))
-            ws = int(lib.ssd_bc_norm_bwd_workspace_bytes(ctypes.byref(p)))
+            ws = int(ssd._load().ssd_bc_norm_bwd_workspace_bytes(ctypes.byref(p)))
             calls.append(("ssd_bc_norm_bwd", p, at[:12] + [lr.FAKE + 30 * lr.FAR, ws, 0]))
             continue
         p = ssd.PoolProblem(b, T, H, P, N, G, H * P, G * N, G * N, 4, H * P * N, dtype, 0)
